@@ -583,6 +583,235 @@ int mxfp4_dequantize_nvfp4(const uint8_t* codes, const uint8_t* scales,
                            const float* global_scale, int64_t M, int64_t K, void* y,
                            void* stream);
 
+/* ---------------------------------------------- products and the 4-bit cache
+ * What a decode step does with the quantized tensors: products with 4-bit
+ * weights (dense and per expert), keys and values quantized into a paged
+ * cache and read back, and the attention of one query token per sequence over
+ * that cache.  No counterpart exists in the method's sources; the formats,
+ * the scale rules and the tiled layout are those of the calls above.
+ *
+ * mxfp4_matvec — y[t, n] = sum_k x[t, k] * W[n, k] for a few tokens t, with W
+ * as MXFP4: W[n, k] = e2m1(code) * 2^(s-127) (s = 255: NaN).  The weights are
+ * decoded on the way to the tensor cores; sums are float32, rounded once to
+ * the output type.
+ *
+ * x           BF16 [num_tokens, K], row stride ldx elements (ldx >= K,
+ *             ldx % 8 == 0), 16-byte aligned; num_tokens may be any size, the
+ *             call is made for few (weights are read once per 32 tokens).
+ *             Inside a 32-element block of x, a value more than 2^39 below the
+ *             block's largest is rounded to a multiple of 2^-40 of it.
+ * codes       [N, K/2] packed E2M1 codes as mxfp4_quantize writes them,
+ *             16-byte aligned; K % 32 == 0.
+ * scales      mxfp4_scale_bytes(N, K) bytes, tiled layout, 16-byte aligned.
+ * y           [num_tokens, N], row stride ldy >= N elements, of x's type, or
+ *             float32 with y_f32 == 1; aligned to its element.  K == 0 writes
+ *             zeros.
+ * The _f16 form takes IEEE binary16 x (and writes binary16 y).
+ *
+ * mxfp4_matvec_nvfp4 — the same with NVFP4 weights (K % 16 == 0):
+ * W[n, k] = e2m1(code) * e4m3(scale byte) / g, global_scale = g a DEVICE
+ * float32; scales hold mxfp4_nvfp4_scale_bytes(N, K) bytes. */
+int mxfp4_matvec(const void* x, int64_t num_tokens, int64_t K, int64_t ldx, const uint8_t* codes,
+                 const uint8_t* scales, int64_t N, void* y, int64_t ldy, int32_t y_f32,
+                 void* stream);
+int mxfp4_matvec_f16(const void* x, int64_t num_tokens, int64_t K, int64_t ldx,
+                     const uint8_t* codes, const uint8_t* scales, int64_t N, void* y, int64_t ldy,
+                     int32_t y_f32, void* stream);
+int mxfp4_matvec_nvfp4(const void* x, int64_t num_tokens, int64_t K, int64_t ldx,
+                       const uint8_t* codes, const uint8_t* scales, const float* global_scale,
+                       int64_t N, void* y, int64_t ldy, int32_t y_f32, void* stream);
+int mxfp4_matvec_nvfp4_f16(const void* x, int64_t num_tokens, int64_t K, int64_t ldx,
+                           const uint8_t* codes, const uint8_t* scales, const float* global_scale,
+                           int64_t N, void* y, int64_t ldy, int32_t y_f32, void* stream);
+
+/* mxfp4_moe_matvec — the experts' products: row r of segment e of the routed
+ * batch (expert_offsets[e] <= r < expert_offsets[e+1], as mxfp4_moe_route
+ * writes them) times expert e's weights:
+ *   y[r, n] = sum_k x[row_index ? row_index[r] : r, k] * W[e][n, k].
+ * Only the weights of experts that have rows are read.
+ *
+ * x               [num_src_rows, K], as in mxfp4_matvec.
+ * row_index       DEVICE int32 [total_rows] or NULL (then num_src_rows >=
+ *                 total_rows): the token of every row.
+ * total_rows      the rows y has room for; expert_offsets must satisfy
+ *                 0 = o[0] <= o[1] <= ... <= o[E] <= total_rows (checked on
+ *                 the device).  Rows from o[E] on are not written: the routes
+ *                 a router drops need no rows.  E <= MXFP4_ROUTE_MAX_EXPERTS.
+ * codes, scales   E consecutive weights [N, K/2] and tiled scale buffers of
+ *                 mxfp4_scale_bytes(N, K) (NVFP4: mxfp4_nvfp4_scale_bytes)
+ *                 bytes each.
+ * global_scales   (NVFP4) DEVICE float32 [E].
+ * y               [total_rows, N], row stride ldy, as in mxfp4_matvec.
+ * status          DEVICE int32 or NULL, out: MXFP4_OK, MXFP4_EOFFSETS (y is
+ *                 then not written), or MXFP4_EINDEX when a used row_index is
+ *                 outside [0, num_src_rows) (that row of y becomes zeros). */
+int mxfp4_moe_matvec(const void* x, int64_t num_src_rows, int64_t K, int64_t ldx,
+                     const int32_t* row_index, int64_t total_rows, const int32_t* expert_offsets,
+                     int32_t E, const uint8_t* codes, const uint8_t* scales, int64_t N, void* y,
+                     int64_t ldy, int32_t y_f32, int32_t* status, void* stream);
+int mxfp4_moe_matvec_f16(const void* x, int64_t num_src_rows, int64_t K, int64_t ldx,
+                         const int32_t* row_index, int64_t total_rows,
+                         const int32_t* expert_offsets, int32_t E, const uint8_t* codes,
+                         const uint8_t* scales, int64_t N, void* y, int64_t ldy, int32_t y_f32,
+                         int32_t* status, void* stream);
+int mxfp4_moe_matvec_nvfp4(const void* x, int64_t num_src_rows, int64_t K, int64_t ldx,
+                           const int32_t* row_index, int64_t total_rows,
+                           const int32_t* expert_offsets, int32_t E, const uint8_t* codes,
+                           const uint8_t* scales, const float* global_scales, int64_t N, void* y,
+                           int64_t ldy, int32_t y_f32, int32_t* status, void* stream);
+int mxfp4_moe_matvec_nvfp4_f16(const void* x, int64_t num_src_rows, int64_t K, int64_t ldx,
+                               const int32_t* row_index, int64_t total_rows,
+                               const int32_t* expert_offsets, int32_t E, const uint8_t* codes,
+                               const uint8_t* scales, const float* global_scales, int64_t N,
+                               void* y, int64_t ldy, int32_t y_f32, int32_t* status,
+                               void* stream);
+
+/* The paged cache.  Keys and values are two pairs of tensors:
+ *   codes   uint8 [num_pages, num_heads, page_size, head_dim/2]
+ *   scales  uint8 [num_pages, num_heads, page_size, head_dim/32]  (MXFP4: E8M0)
+ *                 [num_pages, num_heads, page_size, head_dim/16]  (NVFP4: E4M3)
+ * row-major, 16-byte aligned; head_dim % 32 == 0.  Slot s is position
+ * s % page_size of page s / page_size.  Each (token, head) row is quantized
+ * on its own by the rules of mxfp4_quantize / mxfp4_quantize_nvfp4.
+ *
+ * mxfp4_cache_write — token t's keys and values into slot slots[t].
+ * k, v            BF16 (_f16: binary16): element d of head h of token t at
+ *                 t*token_stride + h*head_stride + d; strides % 8 == 0,
+ *                 >= 0, pointers 16-byte aligned (slices of a fused
+ *                 projection's output need no copy).
+ * slots           DEVICE int32 [num_tokens]; -1: the token is not written.
+ *                 No two tokens may have the same slot (its bytes would be
+ *                 unspecified).  num_pages * page_size <= INT32_MAX.
+ * k_global, v_global  (NVFP4) DEVICE float32: the global scales of mxfp4_quantize_nvfp4.
+ * status          DEVICE int32 or NULL, out: MXFP4_OK, or MXFP4_EINDEX when a
+ *                 slot is outside [-1, num_pages*page_size) (skipped).
+ *
+ * mxfp4_cache_read — the inverse: k_out, v_out [num_tokens, num_heads,
+ * head_dim], BF16 (_f16: binary16), contiguous, from the slots; rounded as
+ * mxfp4_dequantize / mxfp4_dequantize_nvfp4 do.  Slot -1 (and a slot out of
+ * range, with MXFP4_EINDEX) gives zeros. */
+int mxfp4_cache_write(const void* k, const void* v, int64_t num_tokens, int32_t num_heads,
+                      int32_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
+                      int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
+                      int64_t num_pages, int32_t page_size, uint8_t* k_codes, uint8_t* k_scales,
+                      uint8_t* v_codes, uint8_t* v_scales, int32_t* status, void* stream);
+int mxfp4_cache_write_f16(const void* k, const void* v, int64_t num_tokens, int32_t num_heads,
+                          int32_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
+                          int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
+                          int64_t num_pages, int32_t page_size, uint8_t* k_codes,
+                          uint8_t* k_scales, uint8_t* v_codes, uint8_t* v_scales, int32_t* status,
+                          void* stream);
+int mxfp4_cache_write_nvfp4(const void* k, const void* v, int64_t num_tokens, int32_t num_heads,
+                            int32_t head_dim, int64_t k_token_stride, int64_t k_head_stride,
+                            int64_t v_token_stride, int64_t v_head_stride, const int32_t* slots,
+                            int64_t num_pages, int32_t page_size, const float* k_global,
+                            const float* v_global, uint8_t* k_codes, uint8_t* k_scales,
+                            uint8_t* v_codes, uint8_t* v_scales, int32_t* status, void* stream);
+int mxfp4_cache_write_nvfp4_f16(const void* k, const void* v, int64_t num_tokens,
+                                int32_t num_heads, int32_t head_dim, int64_t k_token_stride,
+                                int64_t k_head_stride, int64_t v_token_stride,
+                                int64_t v_head_stride, const int32_t* slots, int64_t num_pages,
+                                int32_t page_size, const float* k_global, const float* v_global,
+                                uint8_t* k_codes, uint8_t* k_scales, uint8_t* v_codes,
+                                uint8_t* v_scales, int32_t* status, void* stream);
+int mxfp4_cache_read(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                     const uint8_t* v_scales, int64_t num_pages, int32_t page_size,
+                     int32_t num_heads, int32_t head_dim, const int32_t* slots,
+                     int64_t num_tokens, void* k_out, void* v_out, int32_t* status, void* stream);
+int mxfp4_cache_read_f16(const uint8_t* k_codes, const uint8_t* k_scales, const uint8_t* v_codes,
+                         const uint8_t* v_scales, int64_t num_pages, int32_t page_size,
+                         int32_t num_heads, int32_t head_dim, const int32_t* slots,
+                         int64_t num_tokens, void* k_out, void* v_out, int32_t* status,
+                         void* stream);
+int mxfp4_cache_read_nvfp4(const uint8_t* k_codes, const uint8_t* k_scales,
+                           const uint8_t* v_codes, const uint8_t* v_scales, const float* k_global,
+                           const float* v_global, int64_t num_pages, int32_t page_size,
+                           int32_t num_heads, int32_t head_dim, const int32_t* slots,
+                           int64_t num_tokens, void* k_out, void* v_out, int32_t* status,
+                           void* stream);
+int mxfp4_cache_read_nvfp4_f16(const uint8_t* k_codes, const uint8_t* k_scales,
+                               const uint8_t* v_codes, const uint8_t* v_scales,
+                               const float* k_global, const float* v_global, int64_t num_pages,
+                               int32_t page_size, int32_t num_heads, int32_t head_dim,
+                               const int32_t* slots, int64_t num_tokens, void* k_out, void* v_out,
+                               int32_t* status, void* stream);
+
+/* mxfp4_cache_attention — attention of one query token per sequence over the
+ * paged cache, the keys and values decoded on the way to the tensor cores:
+ *   o[b, h] = sum_j p_j v_j,  p = softmax_j(softmax_scale * q[b, h] . k_j)
+ * over the positions j in [max(0, n_b - window), n_b) (window == 0: from 0),
+ * n_b = seq_lens[b]; position j of sequence b is position j % page_size of
+ * page page_table[b][j / page_size], head h reads kv head h / (num_q_heads /
+ * num_kv_heads).
+ *
+ * q               BF16 (_f16: binary16): element d of head h of sequence b at
+ *                 b*q_seq_stride + h*q_head_stride + d; strides % 8 == 0,
+ *                 >= 0, 16-byte aligned.
+ * head_dim        % 32 == 0, <= MXFP4_ATTENTION_MAX_HEAD_DIM.
+ * num_q_heads     a multiple of num_kv_heads.
+ * page_table      DEVICE int32, row b at b*table_stride, max_pages entries
+ *                 (those past a sequence's length are not read).
+ * seq_lens        DEVICE int32 [num_seqs], 0 <= n_b <= max_pages*page_size
+ *                 <= INT32_MAX.
+ * softmax_scale   finite.  window >= 0.
+ * workspace       DEVICE, 16-byte aligned, at least
+ *                 mxfp4_cache_attention_workspace_bytes(...) bytes (partial
+ *                 results of long sequences split over CTAs; NULL allowed when
+ *                 that is 0); contents on entry irrelevant.  Two calls in
+ *                 flight at once need two workspaces.
+ * out             [num_seqs, num_q_heads, head_dim], q's type, contiguous.
+ *                 A sequence with no positions gives zeros.
+ * lse             DEVICE float32 [num_seqs, num_q_heads] or NULL, out: the
+ *                 natural logarithm of the softmax's denominator,
+ *                 log sum_j exp(softmax_scale * q . k_j) (-inf without positions).
+ * status          DEVICE int32 or NULL, out: MXFP4_OK, or MXFP4_EINDEX when a
+ *                 length is out of range (the sequence is then empty) or a
+ *                 needed page is outside [0, num_pages) (its positions are
+ *                 left out).
+ * Positions outside the range never matter, whatever bytes they hold. */
+#define MXFP4_ATTENTION_MAX_HEAD_DIM 256
+size_t mxfp4_cache_attention_workspace_bytes(int64_t num_seqs, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_dim,
+                                             int32_t page_size, int64_t max_pages);
+int mxfp4_cache_attention(const void* q, int64_t num_seqs, int32_t num_q_heads, int32_t head_dim,
+                          int64_t q_seq_stride, int64_t q_head_stride, const uint8_t* k_codes,
+                          const uint8_t* k_scales, const uint8_t* v_codes,
+                          const uint8_t* v_scales, int64_t num_pages, int32_t page_size,
+                          int32_t num_kv_heads, const int32_t* page_table, int64_t table_stride,
+                          int64_t max_pages, const int32_t* seq_lens, float softmax_scale,
+                          int32_t window, void* workspace, size_t workspace_bytes, void* out,
+                          float* lse, int32_t* status, void* stream);
+int mxfp4_cache_attention_f16(const void* q, int64_t num_seqs, int32_t num_q_heads,
+                              int32_t head_dim, int64_t q_seq_stride, int64_t q_head_stride,
+                              const uint8_t* k_codes, const uint8_t* k_scales,
+                              const uint8_t* v_codes, const uint8_t* v_scales, int64_t num_pages,
+                              int32_t page_size, int32_t num_kv_heads, const int32_t* page_table,
+                              int64_t table_stride, int64_t max_pages, const int32_t* seq_lens,
+                              float softmax_scale, int32_t window, void* workspace,
+                              size_t workspace_bytes, void* out, float* lse, int32_t* status,
+                              void* stream);
+int mxfp4_cache_attention_nvfp4(const void* q, int64_t num_seqs, int32_t num_q_heads,
+                                int32_t head_dim, int64_t q_seq_stride, int64_t q_head_stride,
+                                const uint8_t* k_codes, const uint8_t* k_scales,
+                                const uint8_t* v_codes, const uint8_t* v_scales,
+                                const float* k_global, const float* v_global, int64_t num_pages,
+                                int32_t page_size, int32_t num_kv_heads,
+                                const int32_t* page_table, int64_t table_stride,
+                                int64_t max_pages, const int32_t* seq_lens, float softmax_scale,
+                                int32_t window, void* workspace, size_t workspace_bytes,
+                                void* out, float* lse, int32_t* status, void* stream);
+int mxfp4_cache_attention_nvfp4_f16(const void* q, int64_t num_seqs, int32_t num_q_heads,
+                                    int32_t head_dim, int64_t q_seq_stride,
+                                    int64_t q_head_stride, const uint8_t* k_codes,
+                                    const uint8_t* k_scales, const uint8_t* v_codes,
+                                    const uint8_t* v_scales, const float* k_global,
+                                    const float* v_global, int64_t num_pages, int32_t page_size,
+                                    int32_t num_kv_heads, const int32_t* page_table,
+                                    int64_t table_stride, int64_t max_pages,
+                                    const int32_t* seq_lens, float softmax_scale, int32_t window,
+                                    void* workspace, size_t workspace_bytes, void* out,
+                                    float* lse, int32_t* status, void* stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* mxfp4_status_string(int status);
 

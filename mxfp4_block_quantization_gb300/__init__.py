@@ -7,6 +7,9 @@ current CUDA stream); every step of the computation runs in the library's
 CUDA kernels.  ``quantize``, ``quantize_grouped``, ``dequantize`` and
 ``swap_w13`` are conveniences that allocate the outputs with torch and call
 the matching entry point.  PyTorch supplies device memory and streams only.
+A decode step's calls (``matvec``, ``moe_matvec``, ``cache_write``,
+``cache_read``, ``cache_attention``) pick the BF16 or FP16 entry point by
+their tensors' type.
 
 There is no CPU path: importing this package fails when the library has not
 been built (``python mxfp4_block_quantization_gb300/_build.py``), and every
@@ -23,6 +26,7 @@ import contextlib
 import ctypes
 import functools
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -47,6 +51,11 @@ __all__ = [
     "quantize_nvfp4_grouped_scatter", "mxfp4_nvfp4_scatter_workspace_bytes",
     "mxfp4_quantize_nvfp4_grouped_scatter_ws", "mxfp4_quantize_nvfp4_grouped_scatter_ws_f16",
     "MXFP4_ROUTE_MAX_EXPERTS", "mxfp4_route_workspace_bytes", "mxfp4_moe_route", "moe_route",
+    "MXFP4_ATTENTION_MAX_HEAD_DIM", "mxfp4_matvec", "mxfp4_matvec_nvfp4", "mxfp4_moe_matvec",
+    "mxfp4_moe_matvec_nvfp4", "matvec", "matvec_nvfp4", "moe_matvec", "moe_matvec_nvfp4",
+    "KVCache", "cache_alloc", "mxfp4_cache_write", "mxfp4_cache_read", "cache_write",
+    "cache_read", "mxfp4_cache_attention_workspace_bytes", "mxfp4_cache_attention",
+    "cache_attention",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxfp4_gb300.so")
@@ -57,6 +66,7 @@ DEBUG_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmx
 MXFP4_SCATTER_MAX_TOP_K = 32
 MXFP4_ROUTE_MAX_EXPERTS = 8192
 MXFP4_NOALLOC_SCRATCH_BYTES = 4 << 20
+MXFP4_ATTENTION_MAX_HEAD_DIM = 256
 MXFP4_OK = 0
 MXFP4_EINVAL = -1
 MXFP4_EALIGN = -2
@@ -154,6 +164,26 @@ def _load(path=LIB_PATH):
     L.mxfp4_route_workspace_bytes.argtypes = [i64, i32, i32]
     L.mxfp4_moe_route.restype = ctypes.c_int
     L.mxfp4_moe_route.argtypes = [vp, i64, i32, i32, vp, ctypes.c_size_t, vp, vp, vp, vp, vp]
+    f32, size = ctypes.c_float, ctypes.c_size_t
+    for nv in (False, True):
+        for f16 in (False, True):
+            tail = ("_nvfp4" if nv else "") + ("_f16" if f16 else "")
+            g1, g2 = ([vp], [vp, vp]) if nv else ([], [])
+            for name, args in (
+                    ("matvec", [vp, i64, i64, i64, vp, vp] + g1 + [i64, vp, i64, i32, vp]),
+                    ("moe_matvec", [vp, i64, i64, i64, vp, i64, vp, i32, vp, vp] + g1 +
+                     [i64, vp, i64, i32, vp, vp]),
+                    ("cache_write", [vp, vp, i64, i32, i32, i64, i64, i64, i64, vp, i64, i32] +
+                     g2 + [vp, vp, vp, vp, vp, vp]),
+                    ("cache_read", [vp, vp, vp, vp] + g2 + [i64, i32, i32, i32, vp, i64, vp, vp,
+                                                            vp, vp]),
+                    ("cache_attention", [vp, i64, i32, i32, i64, i64, vp, vp, vp, vp] + g2 +
+                     [i64, i32, i32, vp, i64, i64, vp, f32, i32, vp, size, vp, vp, vp, vp])):
+                fn = getattr(L, "mxfp4_" + name + tail)
+                fn.restype = ctypes.c_int
+                fn.argtypes = args
+    L.mxfp4_cache_attention_workspace_bytes.restype = size
+    L.mxfp4_cache_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i64]
     L.mxfp4_status_string.restype = ctypes.c_char_p
     L.mxfp4_status_string.argtypes = [ctypes.c_int]
     L.mxfp4_version.restype = ctypes.c_int
@@ -776,6 +806,260 @@ def mxfp4_dequantize_nvfp4(codes, scales, global_scale, M: int, K: int, y, strea
                "mxfp4_dequantize_nvfp4")
 
 
+# ------------------------------------------- products with 4-bit weights
+def _half_type(name, t):
+    """Whether ``t`` is FP16 (True) or BF16 (False)."""
+    if t.dtype == torch.float16:
+        return True
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    return False
+
+
+def _need_product(x, codes, scales, global_scales, y, rows, E, N, nvfp4):
+    """The tensors of a product of ``rows`` rows with E weights [N, K/2]."""
+    K = x.shape[1]
+    if codes.shape[-1] * 2 != K:
+        raise ValueError(f"codes hold {codes.shape[-1] * 2} elements per row, x has {K}")
+    if y.dim() != 2 or y.shape[0] != rows or y.shape[1] != N or (N > 1 and y.stride(1) != 1):
+        raise ValueError(f"y must be [{rows}, {N}] with unit column stride")
+    if y.dtype != x.dtype and y.dtype != torch.float32:
+        raise ValueError(f"y must be {x.dtype} or torch.float32, got {y.dtype}")
+    _need_bytes("codes", codes, E * N * (K // 2))
+    _need_bytes("scales", scales,
+                E * (mxfp4_nvfp4_scale_bytes(N, K) if nvfp4 else mxfp4_scale_bytes(N, K)))
+    if nvfp4:
+        _need_bytes("global_scales", global_scales, 4 * E)
+
+
+def _row_stride(t):
+    """The row stride of a 2-D tensor (a single row may report any)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _strides2(t):
+    """The two outer strides of a 3-D tensor (0 for a dimension of one, which
+    may report any)."""
+    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _matvec(x, codes, scales, global_scale, y, stream, nvfp4):
+    _need_cuda("x", x)
+    _need_cuda("codes", codes, torch.uint8)
+    _need_cuda("scales", scales, torch.uint8)
+    _need_cuda("global_scale", global_scale, torch.float32)
+    _need_cuda("y", y)
+    if x.dim() != 2 or x.stride(1) != 1 or codes.dim() != 2:
+        raise ValueError("x must be 2-D with unit column stride, codes [N, K/2]")
+    T, K = x.shape
+    N = codes.shape[0]
+    _need_product(x, codes, scales, global_scale, y, T, 1, N, nvfp4)
+    name = ("mxfp4_matvec" + ("_nvfp4" if nvfp4 else "") +
+            ("_f16" if _half_type("x", x) else ""))
+    g = (_ptr(global_scale),) if nvfp4 else ()
+    with _switch(_device_of(x, codes, scales, global_scale, y)):
+        _check(getattr(_lib, name)(_ptr(x), T, K, _row_stride(x), _ptr(codes), _ptr(scales), *g,
+                                   N, _ptr(y), _row_stride(y), int(y.dtype == torch.float32),
+                                   _stream(stream, x.device)), name)
+
+
+def mxfp4_matvec(x, codes, scales, y, stream=None) -> None:
+    """``y`` [T, N] = ``x`` [T, K] (BF16 or FP16) times the transpose of the
+    MXFP4 weights ``codes`` [N, K/2] with tiled ``scales``; ``y`` of x's type
+    or float32.  Made for few tokens."""
+    _matvec(x, codes, scales, None, y, stream, False)
+
+
+def mxfp4_matvec_nvfp4(x, codes, scales, global_scale, y, stream=None) -> None:
+    """mxfp4_matvec with NVFP4 weights (float32 device ``global_scale``)."""
+    _matvec(x, codes, scales, global_scale, y, stream, True)
+
+
+def _moe_matvec(x, row_index, expert_offsets, codes, scales, global_scales, y, status, stream,
+                nvfp4):
+    _need_cuda("x", x)
+    _need_cuda("row_index", row_index, torch.int32)
+    _need_cuda("expert_offsets", expert_offsets, torch.int32)
+    _need_cuda("codes", codes, torch.uint8)
+    _need_cuda("scales", scales, torch.uint8)
+    _need_cuda("global_scales", global_scales, torch.float32)
+    _need_cuda("y", y)
+    _need_cuda("status", status, torch.int32)
+    if x.dim() != 2 or x.stride(1) != 1 or codes.dim() != 3 or y.dim() != 2:
+        raise ValueError("x and y must be 2-D with unit column stride, codes [E, N, K/2]")
+    src, K = x.shape
+    E, N = codes.shape[:2]
+    rows = y.shape[0]
+    _need_product(x, codes, scales, global_scales, y, rows, E, N, nvfp4)
+    _need_bytes("expert_offsets", expert_offsets, 4 * (E + 1))
+    _need_bytes("status", status, 4)
+    if row_index is not None:
+        _need_bytes("row_index", row_index, 4 * rows)
+    elif src < rows:
+        raise ValueError(f"x holds {src} rows; without row_index this call needs {rows}")
+    name = ("mxfp4_moe_matvec" + ("_nvfp4" if nvfp4 else "") +
+            ("_f16" if _half_type("x", x) else ""))
+    g = (_ptr(global_scales),) if nvfp4 else ()
+    with _switch(_device_of(x, row_index, expert_offsets, codes, scales, global_scales, y,
+                            status)):
+        _check(getattr(_lib, name)(_ptr(x), src, K, _row_stride(x), _ptr(row_index), rows,
+                                   _ptr(expert_offsets), E, _ptr(codes), _ptr(scales), *g, N,
+                                   _ptr(y), _row_stride(y), int(y.dtype == torch.float32),
+                                   _ptr(status), _stream(stream, x.device)), name)
+
+
+def mxfp4_moe_matvec(x, row_index, expert_offsets, codes, scales, y, status=None,
+                     stream=None) -> None:
+    """The experts' products: row r of segment e (``expert_offsets`` int32
+    [E+1]) of the routed batch is ``x[row_index[r]]`` (or ``x[r]`` without
+    ``row_index``) times the transpose of expert e's MXFP4 weights ``codes``
+    [E, N, K/2].  Rows of ``y`` from expert_offsets[E] on are not written."""
+    _moe_matvec(x, row_index, expert_offsets, codes, scales, None, y, status, stream, False)
+
+
+def mxfp4_moe_matvec_nvfp4(x, row_index, expert_offsets, codes, scales, global_scales, y,
+                           status=None, stream=None) -> None:
+    """mxfp4_moe_matvec with NVFP4 weights (float32 ``global_scales`` [E])."""
+    _moe_matvec(x, row_index, expert_offsets, codes, scales, global_scales, y, status, stream,
+                True)
+
+
+# ------------------------------------------------------ the paged 4-bit cache
+class KVCache(NamedTuple):
+    """A paged cache of keys and values: uint8 codes [pages, heads, page_size,
+    head_dim/2] and scales [pages, heads, page_size, head_dim/32 (MXFP4) or
+    head_dim/16 (NVFP4)].  An NVFP4 cache has the float32 device scalars
+    ``k_global`` and ``v_global``; an MXFP4 cache has None there."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+    k_global: Optional[torch.Tensor] = None
+    v_global: Optional[torch.Tensor] = None
+
+
+def _need_cache(c):
+    """(pages, heads, page_size, head_dim, nvfp4) of a cache whose tensors fit
+    together."""
+    nvfp4 = c.k_global is not None
+    if nvfp4 != (c.v_global is not None):
+        raise ValueError("an NVFP4 cache has both k_global and v_global, an MXFP4 cache neither")
+    for name, t in (("k_codes", c.k_codes), ("k_scales", c.k_scales), ("v_codes", c.v_codes),
+                    ("v_scales", c.v_scales)):
+        _need_cuda(name, t, torch.uint8)
+        if t.dim() != 4 or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [pages, heads, page_size, ...] tensor")
+    pages, heads, page_size, half = c.k_codes.shape
+    want = (pages, heads, page_size, half // (8 if nvfp4 else 16))
+    if c.v_codes.shape != c.k_codes.shape or c.k_scales.shape != want or c.v_scales.shape != want:
+        raise ValueError(f"k_codes and v_codes must agree and the scales be {want}")
+    if nvfp4:
+        for name, t in (("k_global", c.k_global), ("v_global", c.v_global)):
+            _need_cuda(name, t, torch.float32)
+            _need_bytes(name, t, 4)
+    return pages, heads, page_size, 2 * half, nvfp4
+
+
+def _cache_globals(c, nvfp4):
+    return (_ptr(c.k_global), _ptr(c.v_global)) if nvfp4 else ()
+
+
+def mxfp4_cache_write(k, v, slots, cache, status=None, stream=None) -> None:
+    """Quantize ``k`` and ``v`` [T, heads, head_dim] (BF16 or FP16, any token
+    and head stride that is a multiple of 8) into the slots ``slots`` (int32
+    [T], -1: not written) of ``cache``."""
+    pages, heads, page_size, D, nvfp4 = _need_cache(cache)
+    _need_cuda("k", k)
+    _need_cuda("v", v, k.dtype)
+    _need_cuda("slots", slots, torch.int32)
+    _need_cuda("status", status, torch.int32)
+    T = slots.numel()
+    for name, t in (("k", k), ("v", v)):
+        if t.dim() != 3 or t.shape != (T, heads, D) or (D > 1 and t.stride(2) != 1):
+            raise ValueError(f"{name} must be [{T}, {heads}, {D}] with unit element stride")
+    _need_bytes("slots", slots, 4 * T)
+    _need_bytes("status", status, 4)
+    name = ("mxfp4_cache_write" + ("_nvfp4" if nvfp4 else "") +
+            ("_f16" if _half_type("k", k) else ""))
+    with _switch(_device_of(k, v, slots, *cache, status)):
+        _check(getattr(_lib, name)(
+            _ptr(k), _ptr(v), T, heads, D, *_strides2(k), *_strides2(v),
+            _ptr(slots), pages, page_size, *_cache_globals(cache, nvfp4), _ptr(cache.k_codes),
+            _ptr(cache.k_scales), _ptr(cache.v_codes), _ptr(cache.v_scales), _ptr(status),
+            _stream(stream, k.device)), name)
+
+
+def mxfp4_cache_read(cache, slots, k_out, v_out, status=None, stream=None) -> None:
+    """Dequantize the slots ``slots`` (int32 [T], -1: zeros) of ``cache`` into
+    contiguous ``k_out`` and ``v_out`` [T, heads, head_dim] (BF16 or FP16)."""
+    pages, heads, page_size, D, nvfp4 = _need_cache(cache)
+    _need_cuda("slots", slots, torch.int32)
+    _need_cuda("k_out", k_out)
+    _need_cuda("v_out", v_out, k_out.dtype)
+    _need_cuda("status", status, torch.int32)
+    T = slots.numel()
+    _need_bytes("slots", slots, 4 * T)
+    _need_bytes("k_out", k_out, 2 * T * heads * D)
+    _need_bytes("v_out", v_out, 2 * T * heads * D)
+    _need_bytes("status", status, 4)
+    name = ("mxfp4_cache_read" + ("_nvfp4" if nvfp4 else "") +
+            ("_f16" if _half_type("k_out", k_out) else ""))
+    with _switch(_device_of(slots, k_out, v_out, *cache, status)):
+        _check(getattr(_lib, name)(
+            _ptr(cache.k_codes), _ptr(cache.k_scales), _ptr(cache.v_codes), _ptr(cache.v_scales),
+            *_cache_globals(cache, nvfp4), pages, page_size, heads, D, _ptr(slots), T,
+            _ptr(k_out), _ptr(v_out), _ptr(status), _stream(stream, slots.device)), name)
+
+
+@functools.lru_cache(maxsize=1024)
+def mxfp4_cache_attention_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int,
+                                          head_dim: int, page_size: int, max_pages: int) -> int:
+    return int(_lib.mxfp4_cache_attention_workspace_bytes(
+        int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size),
+        int(max_pages)))
+
+
+def mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, out, window=0,
+                          workspace=None, lse=None, status=None, stream=None) -> None:
+    """Attention of one query token per sequence, ``q`` [B, q_heads, head_dim]
+    (BF16 or FP16), over ``cache``: sequence b's position j is in page
+    ``page_table[b, j // page_size]`` (int32 [B, max_pages]), its length
+    ``seq_lens[b]`` (int32).  ``window`` > 0 keeps the last ``window``
+    positions.  ``workspace``: >= mxfp4_cache_attention_workspace_bytes bytes;
+    ``lse``: float32 [B, q_heads]."""
+    pages, heads, page_size, D, nvfp4 = _need_cache(cache)
+    _need_cuda("q", q)
+    _need_cuda("out", out, q.dtype)
+    _need_cuda("page_table", page_table, torch.int32)
+    _need_cuda("seq_lens", seq_lens, torch.int32)
+    _need_cuda("workspace", workspace)
+    _need_cuda("lse", lse, torch.float32)
+    _need_cuda("status", status, torch.int32)
+    if q.dim() != 3 or q.shape[2] != D or (D > 1 and q.stride(2) != 1):
+        raise ValueError(f"q must be [sequences, heads, {D}] with unit element stride")
+    B, Hq = q.shape[:2]
+    if (page_table.dim() != 2 or page_table.shape[0] != B or
+            (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError(f"page_table must be [{B}, max_pages] with unit column stride")
+    max_pages = page_table.shape[1]
+    _need_bytes("seq_lens", seq_lens, 4 * B)
+    _need_bytes("out", out, 2 * B * Hq * D)
+    _need_bytes("lse", lse, 4 * B * Hq)
+    _need_bytes("workspace", workspace, 0)
+    _need_bytes("status", status, 4)
+    name = ("mxfp4_cache_attention" + ("_nvfp4" if nvfp4 else "") +
+            ("_f16" if _half_type("q", q) else ""))
+    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _switch(_device_of(q, out, page_table, seq_lens, *cache, workspace, lse, status)):
+        _check(getattr(_lib, name)(
+            _ptr(q), B, Hq, D, *_strides2(q), _ptr(cache.k_codes),
+            _ptr(cache.k_scales), _ptr(cache.v_codes), _ptr(cache.v_scales),
+            *_cache_globals(cache, nvfp4), pages, page_size, heads, _ptr(page_table),
+            _row_stride(page_table), max_pages, _ptr(seq_lens), float(softmax_scale),
+            int(window), _ptr(workspace), ws, _ptr(out), _ptr(lse), _ptr(status),
+            _stream(stream, q.device)), name)
+
+
 # --------------------------------------------------- allocating wrappers
 def quantize(x, stream=None):
     """BF16 or FP16 ``x`` [M, K] -> (codes uint8 [M, K/2], scales uint8 [scale_bytes])."""
@@ -948,3 +1232,100 @@ def dequantize_nvfp4(codes, scales, global_scale, M: int, K: int, stream=None):
     y = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
     mxfp4_dequantize_nvfp4(codes, scales, global_scale, M, K, y, stream)
     return y
+
+
+def _product_out(x, rows, N, out, out_dtype):
+    return out if out is not None else torch.empty((rows, N), dtype=out_dtype or x.dtype,
+                                                   device=x.device)
+
+
+def matvec(x, codes, scales, out=None, out_dtype=None, stream=None):
+    """``x`` [T, K] (BF16 or FP16) times the transpose of the MXFP4 weights
+    ``codes`` [N, K/2], ``scales`` (tiled): [T, N] of x's type, of
+    ``out_dtype`` (torch.float32) or into ``out``."""
+    out = _product_out(x, x.shape[0], codes.shape[0], out, out_dtype)
+    _matvec(x, codes, scales, None, out, stream, False)
+    return out
+
+
+def matvec_nvfp4(x, codes, scales, global_scale, out=None, out_dtype=None, stream=None):
+    """matvec with NVFP4 weights and their float32 ``global_scale``."""
+    out = _product_out(x, x.shape[0], codes.shape[0], out, out_dtype)
+    _matvec(x, codes, scales, global_scale, out, stream, True)
+    return out
+
+
+def _moe_outputs(x, row_index, codes, out, out_dtype, status):
+    rows = x.shape[0] if row_index is None else row_index.numel()
+    if status is None:
+        status = torch.empty(1, dtype=torch.int32, device=x.device)
+    return _product_out(x, rows, codes.shape[1], out, out_dtype), status
+
+
+def moe_matvec(x, row_index, expert_offsets, codes, scales, out=None, out_dtype=None, status=None,
+               stream=None):
+    """Returns (y, status): y [rows, N], row r of segment e = x[row_index[r]]
+    (x[r] if row_index is None) times the transpose of expert e's MXFP4
+    weights ``codes`` [E, N, K/2].  Rows from expert_offsets[E] on are not
+    written."""
+    out, status = _moe_outputs(x, row_index, codes, out, out_dtype, status)
+    _moe_matvec(x, row_index, expert_offsets, codes, scales, None, out, status, stream, False)
+    return out, status
+
+
+def moe_matvec_nvfp4(x, row_index, expert_offsets, codes, scales, global_scales, out=None,
+                     out_dtype=None, status=None, stream=None):
+    """moe_matvec with NVFP4 weights and float32 ``global_scales`` [E]."""
+    out, status = _moe_outputs(x, row_index, codes, out, out_dtype, status)
+    _moe_matvec(x, row_index, expert_offsets, codes, scales, global_scales, out, status, stream,
+                True)
+    return out, status
+
+
+def cache_alloc(num_pages: int, page_size: int, num_heads: int, head_dim: int, k_global=None,
+                v_global=None, device="cuda"):
+    """A zeroed KVCache; NVFP4 when the float32 global scales are given."""
+    per = 32 if k_global is None else 16
+    shape = (num_pages, num_heads, page_size)
+    parts = [torch.zeros(*shape, n, dtype=torch.uint8, device=device)
+             for n in (head_dim // 2, head_dim // per) * 2]
+    return KVCache(*parts, k_global, v_global)
+
+
+def cache_write(k, v, slots, cache, status=None, stream=None):
+    """mxfp4_cache_write with a status word allocated here; returns it."""
+    if status is None:
+        status = torch.empty(1, dtype=torch.int32, device=k.device)
+    mxfp4_cache_write(k, v, slots, cache, status, stream)
+    return status
+
+
+def cache_read(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16, status=None,
+               stream=None):
+    """Returns (k, v, status): the slots' keys and values [T, heads, head_dim]."""
+    shape = (slots.numel(), cache.k_codes.shape[1], cache.k_codes.shape[3] * 2)
+    k_out, v_out = (t if t is not None else torch.empty(shape, dtype=dtype, device=slots.device)
+                    for t in (k_out, v_out))
+    if status is None:
+        status = torch.empty(1, dtype=torch.int32, device=slots.device)
+    mxfp4_cache_read(cache, slots, k_out, v_out, status, stream)
+    return k_out, v_out, status
+
+
+def cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, window=0, out=None,
+                    lse=None, status=None, stream=None):
+    """Returns (out [B, q_heads, head_dim], lse float32 [B, q_heads], status),
+    with the workspace allocated here."""
+    B, Hq, D = q.shape
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if status is None:
+        status = torch.empty(1, dtype=torch.int32, device=q.device)
+    nbytes = mxfp4_cache_attention_workspace_bytes(B, Hq, cache.k_codes.shape[1], D,
+                                                   cache.k_codes.shape[2], page_table.shape[1])
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale, out, window, ws, lse,
+                          status, stream)
+    return out, lse, status

@@ -9,6 +9,7 @@
 
 #include <cuda_runtime.h>
 
+#include "mxfp4_checks.h"
 #include "mxfp4_internal.h"
 #include "../../include/mxfp4.h"
 #ifdef MXFP4_DEBUG_BOUNDS
@@ -95,44 +96,7 @@ int32_t* noalloc_scratch() {
 
 }  // namespace mxfp4
 
-namespace {
-
-constexpr int64_t kMaxGrid = INT_MAX / 2;  // tile counts stay far from int overflow
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void* p, int64_t bytes) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return Range{a, a + static_cast<uintptr_t>(bytes > 0 ? bytes : 0)};
-}
-
-bool overlap(Range a, Range b) {
-  if (a.lo == a.hi || b.lo == b.hi) return false;
-  return a.lo < b.hi && b.lo < a.hi;
-}
-
-int from_cuda(cudaError_t e) { return e == cudaSuccess ? MXFP4_OK : MXFP4_ECUDA; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-int64_t padded_scale_cols(int64_t K) { return ceil_div(K / 32, 4) * 4; }
-
-// Byte count of `rows` rows of `cols` scale bytes for a size query, or 0 when
-// it does not fit in int64 (no call accepts such sizes).
-size_t rows_times_cols(int64_t rows, int64_t cols) {
-  int64_t r = 0;
-  return __builtin_mul_overflow(rows, cols, &r) ? 0 : static_cast<size_t>(r);
-}
-
-// Row counts above this are rejected by every call; the size queries return
-// 0 for them instead of wrapping around.
-constexpr int64_t kMaxRows = INT64_MAX / 4;
-
-}  // namespace
+using namespace mxfp4::checks;
 
 extern "C" {
 
@@ -911,7 +875,9 @@ int64_t mxfp4_debug_bounds_violations(void) {
   return static_cast<int64_t>(mxfp4::debug_violations_quantize()) +
          mxfp4::debug_violations_dispatch() +
          mxfp4::debug_violations_dequantize() + mxfp4::debug_violations_nvfp4() +
-         mxfp4::debug_violations_swap() + mxfp4::debug_violations_route();
+         mxfp4::debug_violations_swap() + mxfp4::debug_violations_route() +
+         mxfp4::debug_violations_matvec() + mxfp4::debug_violations_cache() +
+         mxfp4::debug_violations_attention();
 }
 #endif
 

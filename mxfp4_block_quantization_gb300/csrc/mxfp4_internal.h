@@ -139,6 +139,71 @@ cudaError_t launch_moe_route(const int32_t* ids, int64_t num_tokens, int32_t top
                              int32_t* workspace, int32_t* offsets, int32_t* dest,
                              int32_t* row_index, int32_t* status, cudaStream_t stream);
 
+// Products with 4-bit weights: dense (offsets == NULL: rows = tokens, one
+// weight) or per expert segment (offsets [E+1] on the device).
+struct MatvecArgs {
+  const void* x;
+  int64_t src_rows;
+  int64_t K;
+  int64_t ldx;
+  const int32_t* row_index;  // NULL: row r reads x row r
+  int64_t rows;
+  const int32_t* offsets;
+  int32_t E;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* global_scales;  // NVFP4 only
+  int64_t N;
+  void* y;
+  int64_t ldy;
+  bool y_f32;
+  bool f16;
+  bool nvfp4;
+  int32_t* status;
+};
+cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream);
+
+// The paged cache: [num_pages, num_heads, page_size, head_dim/2] codes and
+// their scales, for keys and values.
+struct CacheArgs {
+  uint8_t* codes[2];   // keys, values
+  uint8_t* scales[2];
+  const float* global_scales[2];  // NVFP4 only
+  int64_t num_pages;
+  int32_t page_size;
+  int32_t num_heads;
+  int32_t head_dim;
+  bool f16;
+  bool nvfp4;
+};
+cudaError_t launch_cache_write(const CacheArgs& c, const void* const x[2], int64_t num_tokens,
+                               const int64_t token_stride[2], const int64_t head_stride[2],
+                               const int32_t* slots, int32_t* status, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheArgs& c, const int32_t* slots, int64_t num_tokens,
+                              void* const out[2], int32_t* status, cudaStream_t stream);
+
+struct AttentionArgs {
+  CacheArgs cache;
+  const void* q;
+  int64_t num_seqs;
+  int32_t num_q_heads;
+  int64_t q_seq_stride;
+  int64_t q_head_stride;
+  const int32_t* page_table;
+  int64_t table_stride;
+  int64_t max_pages;
+  const int32_t* seq_lens;
+  float softmax_scale;
+  int32_t window;
+  float* workspace;
+  void* out;
+  float* lse;
+  int32_t* status;
+};
+int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int64_t max_len);
+cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
@@ -151,6 +216,9 @@ unsigned int debug_violations_dequantize();
 unsigned int debug_violations_nvfp4();
 unsigned int debug_violations_swap();
 unsigned int debug_violations_route();
+unsigned int debug_violations_matvec();
+unsigned int debug_violations_cache();
+unsigned int debug_violations_attention();
 #endif
 
 // Launch with programmatic dependent launch allowed: the grid may be
