@@ -5,6 +5,31 @@
 //   MXFP4: W = e2m1(code) * 2^(s-127), one scale byte per 32 elements of K
 //   NVFP4: W = e2m1(code) * e4m3(s) / g, one scale byte per 16 elements
 // Sums are float32; the result is rounded once to the output's type.
+//
+// What bounds it: every weight byte is read once and used for T tokens, so
+// for few tokens HBM does.  At 6.8 TB/s an SM has to decode and multiply
+// about 45 weights a clock, which leaves no room for scalar multiply-adds on
+// each token; the tensor cores' m16n8k16 form takes 16 weight rows by 8
+// tokens, and a weight costs one conversion (two codes to two halves) for any
+// number of tokens up to 8.
+//
+// A warp owns 16 rows of W and a range of K, and streams its codes through
+// its own ring of shared-memory stages (16-byte asynchronous copies, 128
+// elements of K by 16 rows each), so warps never wait on one another inside a
+// product.  The 16 rows are {4j..4j+3} + {0, 32, 64, 96} of a 128-row tile:
+// their scale bytes are 64 consecutive bytes of the tiled layout.
+//
+// x is staged once per CTA as halves: the order of k inside a 32-element
+// block is free as long as both operands agree, so a lane's 4-byte word of
+// codes (8 elements) meets the 16 bytes of x at the same place.  BF16 has
+// more exponents than a half: each 32-element block of a token is scaled by
+// the power of two that puts its largest element in [2^15, 2^16) (11 bits hold
+// BF16's 8 exactly down to 2^-29 of that; below, to 2^-40), and the power is
+// multiplied back in float32.
+// The MXFP4 scale is a power of two of any size, so it is applied in float32
+// to the 32-element partial sums; the E4M3 scale times an E2M1 value has at
+// most 6 bits and fits a half, so NVFP4 weights are scaled before the product.
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -15,6 +40,14 @@
 
 namespace mxfp4 {
 namespace {
+
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16;                      // weight rows of a warp's tile
+constexpr int kChunk = 128;                    // elements of K per stage
+constexpr int kStageCodes = kTile * kChunk / 2;  // 1024 bytes
+constexpr int kAhead = 4;                      // stages in flight per warp
+constexpr int kStages = kAhead + 1;
 
 struct MatvecParams {
   const uint8_t* __restrict__ x;
@@ -28,14 +61,22 @@ struct MatvecParams {
   int64_t src_rows;
   int64_t ldx;
   int64_t ldy;
-  int64_t rows;
-  int64_t N;
   int64_t expert_codes;   // bytes of one expert's codes
   int64_t expert_scales;  // bytes of one expert's tiled scales
+  int32_t rows;
+  int32_t N;
   int32_t K;
   int32_t E;
-  int32_t nKT;  // 4-column scale chunks of a row
+  int32_t nKT;        // 4-column scale chunks of a row
+  int32_t tiles;      // 16-row tiles of N (8 per 128 rows)
+  int32_t groups;     // tile groups (16 / kw tiles) per unit
+  int32_t kw;         // warps that share a tile, each with its range of K
+  int32_t chunks;     // 128-element chunks of K
+  int32_t panel;      // chunks of x staged at a time
+  int32_t x_rows;     // token rows that x's shared memory holds
+  int32_t x_pitch;    // bytes between them
   int32_t y_f32;
+  int32_t half_rows;  // rows of codes start at 8-byte (not 16-byte) boundaries
 #ifdef MXFP4_DEBUG_BOUNDS
   DebugRanges dbg;
 #endif
@@ -43,95 +84,507 @@ struct MatvecParams {
 
 enum : int { kDbgX = 0, kDbgCodes, kDbgScales, kDbgGlobal, kDbgY, kDbgIndex, kDbgOffsets };
 
-template <bool kNv>
-__device__ __forceinline__ float scale_value(uint32_t s) {
-  if constexpr (kNv) {
-    return e4m3_to_f32(s);
-  } else {
-    return s == 255u ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(s);
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool take) {
+  const int n = take ? kBytes : 0;  // 0: the destination is filled with zeros
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds64f(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+
+// D += A (16x16 halves, row) * B (16x8 halves, col), float32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// One word of eight E2M1 codes -> four half pairs, in element order.
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t"
+      ".reg .b8 q0, q1, q2, q3;\n\t"
+      "mov.b32 {q0, q1, q2, q3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, q0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, q1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, q2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, q3;\n\t"
+      "}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Two E8M0 bytes (low 16 bits) -> two BF16 values 2^(s-127) (255: NaN).
+__device__ __forceinline__ uint32_t e8m0x2_to_bf16x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+  return r;
+}
+
+// An E4M3 byte -> that value in both halves of a pair (exact).
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t byte) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(byte * 0x0101u)));
+  return r;
+}
+
+// The rows of one unit of work: up to 8*NT consecutive rows of one segment.
+struct UnitRows {
+  int e, row0, n;
+};
+
+struct Shared {
+  int32_t prefix[kThreads];  // units up to and with each thread's experts
+  int32_t warp_sum[kWarps];
+};
+
+// Expert and rows of unit u, from the prefix sums (same result in all lanes).
+template <int NT>
+__device__ __forceinline__ UnitRows find_unit(const MatvecParams& p, const Shared& s, int u) {
+  constexpr int R = 8 * NT;
+  UnitRows r;
+  if (p.offsets == nullptr) {
+    r.e = 0;
+    r.row0 = u * R;
+    r.n = min(R, p.rows - r.row0);
+    return r;
+  }
+  int lo = 0, hi = kThreads - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (s.prefix[mid] > u) hi = mid; else lo = mid + 1;
+  }
+  int base = lo > 0 ? s.prefix[lo - 1] : 0;
+  const int per = (p.E + kThreads - 1) / kThreads;
+  int e = lo * per;
+  for (;; ++e) {
+    const int a = __ldg(p.offsets + e), n = __ldg(p.offsets + e + 1) - a;
+    const int c = (n + R - 1) / R;
+    if (base + c > u || e + 1 >= p.E) {
+      r.e = e;
+      r.row0 = a + (u - base) * R;
+      r.n = min(R, a + n - r.row0);
+      return r;
+    }
+    base += c;
   }
 }
 
-template <bool kF16>
-__device__ __forceinline__ float value16(uint16_t v) {
-  return kF16 ? __uint_as_float(f16_bits_to_f32_bits(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
-}
+// Where a warp stands in its stream of (item, panel, chunk) stages.
+struct Cursor {
+  int item, panel, chunk, end;  // chunk: next of [.., end) in this panel
+  const uint8_t* codes;         // the tile's first row, chunk 0
+  const uint8_t* scales;        // the tile's 64 bytes of scale chunk 0
+  int rows_ok;                  // rows of the tile's four 32-row quarters inside N
+  int unit, e;
+};
 
-// Whether the expert offsets are 0 = o[0] <= ... <= o[E] <= rows, by the whole
-// CTA.
-__device__ __forceinline__ bool offsets_ok(const MatvecParams& p) {
-  int bad = 0;
-  for (int e = threadIdx.x; e <= p.E; e += blockDim.x) {
-    const int32_t o = __ldg(p.offsets + e);
-    if (e == 0 ? o != 0 : o < __ldg(p.offsets + e - 1)) bad = 1;
-    if (o < 0 || o > p.rows) bad = 1;
-  }
-  return __syncthreads_or(bad) == 0;
-}
+template <bool kNv, bool kF16, int NT>
+__global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams p) {
+  constexpr int R = 8 * NT;
+  constexpr int kScaleBytes = kNv ? 128 : 64;
+  constexpr int kStage = kStageCodes + kScaleBytes;
+  constexpr int kUnroll = NT == 4 ? 1 : 4;  // registers: 32 tokens hold 16 sums and 16 words of x
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Shared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  // shared memory: rings | x halves | x block scales | partial sums (two sets)
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  uint8_t* const x_s = smem + kWarps * kStages * kStage;
+  float* const xs_s = reinterpret_cast<float*>(x_s + p.x_rows * p.x_pitch);
+  float* const part_s = xs_s + (kF16 ? 0 : p.panel * 4 * R);
 
-template <bool kNv, bool kF16>
-__global__ void __launch_bounds__(256) matvec_kernel(const MatvecParams p) {
-  constexpr int kBlk = kNv ? 16 : 32;
   pdl_wait();
   pdl_release();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (p.offsets != nullptr) {
-    const bool ok = offsets_ok(p);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && p.status != nullptr) {
-      int bad = 0;
-      if (ok && p.row_index != nullptr)
-        for (int r = threadIdx.x; r < __ldg(p.offsets + p.E); r += blockDim.x) {
+
+  // units of work: token chunks of the experts that have rows
+  int units;
+  if (p.offsets == nullptr) {
+    units = (p.rows + R - 1) / R;
+  } else {
+    const int per = (p.E + kThreads - 1) / kThreads;
+    int sum = 0, bad = 0;
+    for (int i = 0; i < per; ++i) {
+      const int e = threadIdx.x * per + i;
+      if (e >= p.E) break;
+      const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+      if (a < 0 || b < a || b > p.rows || (e == 0 && a != 0)) bad = 1;
+      else sum += (b - a + R - 1) / R;
+    }
+    if (p.E == 0 && threadIdx.x == 0 && __ldg(p.offsets) != 0) bad = 1;
+    bad = __syncthreads_or(bad);
+    int scan = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) sh.warp_sum[warp] = scan;
+    __syncthreads();
+    int before = 0;
+    units = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sh.warp_sum[w];
+      units += sh.warp_sum[w];
+    }
+    sh.prefix[threadIdx.x] = before + scan;
+    if (blockIdx.x == 0 && p.status != nullptr) {
+      int wrong = 0;
+      if (!bad && p.row_index != nullptr) {
+        const int used = p.E > 0 ? __ldg(p.offsets + p.E) : 0;
+        for (int r = threadIdx.x; r < used; r += kThreads) {
           const int32_t i = __ldg(p.row_index + r);
-          if (i < 0 || i >= p.src_rows) bad = 1;
+          if (i < 0 || i >= p.src_rows) wrong = 1;
         }
-      bad = __syncthreads_or(bad);
-      if (threadIdx.x == 0) *p.status = !ok ? -6 : bad ? -7 : 0;
-    }
-    if (!ok) return;
-  }
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * 8 + warp;
-  if (n >= p.N) return;
-  for (int64_t r = blockIdx.y; r < p.rows; r += gridDim.y) {
-    int e = 0;
-    int64_t src = r;
-    if (p.offsets != nullptr) {
-      if (r >= __ldg(p.offsets + p.E)) return;
-      e = find_segment(p.offsets, p.E, static_cast<int>(r), __ldg(p.offsets + p.E));
-      if (p.row_index != nullptr) src = __ldg(p.row_index + r);
-    }
-    const bool live = src >= 0 && src < p.src_rows;
-    const uint8_t* codes = p.codes + e * p.expert_codes + n * (p.K / 2);
-    const uint8_t* scales = p.scales + e * p.expert_scales + (n / 128) * p.nKT * kChunkBytes +
-                            (n % 32) * 16 + (n % 128) / 32 * 4;
-    float acc = 0.0f;
-    if (live) {
-      const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x) + src * p.ldx;
-      for (int k = lane * 2; k < p.K; k += 64) {
-        const int c = k / kBlk;
-        const uint8_t* sp = scales + static_cast<int64_t>(c >> 2) * kChunkBytes + (c & 3);
-        if (!MXFP4_IN_BOUNDS(p, kDbgX, x + k, 4) || !MXFP4_IN_BOUNDS(p, kDbgCodes, codes + k / 2, 1) ||
-            !MXFP4_IN_BOUNDS(p, kDbgScales, sp, 1))
-          continue;
-        const uint32_t h = cvt_e2m1x2_to_f16x2(__ldg(codes + k / 2));
-        const float s = scale_value<kNv>(__ldg(sp));
-        acc = fmaf(value16<kF16>(x[k]) * half_lo_to_f32(h), s, acc);
-        acc = fmaf(value16<kF16>(x[k + 1]) * half_hi_to_f32(h), s, acc);
       }
+      wrong = __syncthreads_or(wrong);
+      if (threadIdx.x == 0) *p.status = bad ? -6 : wrong ? -7 : 0;
     }
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
-    if (kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + e, 4))
-      acc /= __ldg(p.global_scales + e);
-    if (lane == 0) {
-      if (p.y_f32) {
-        float* y = reinterpret_cast<float*>(p.y) + r * p.ldy + n;
-        if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = acc;
+    if (bad) return;
+    __syncthreads();
+  }
+
+  // this CTA's items: consecutive (unit, tile group) pairs
+  const int64_t items = static_cast<int64_t>(units) * p.groups;
+  const int first = static_cast<int>(items * blockIdx.x / gridDim.x);
+  const int last = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+  if (first >= last) return;
+  const int kw = p.kw;
+  const int my_k = warp % kw, my_tile = warp / kw, tiles_per_item = kWarps / kw;
+  const int n_panels = p.chunks > 0 ? (p.chunks + p.panel - 1) / p.panel : 0;
+
+  // row i of a tile is tile_base + 32 * (i / 4) + i % 4
+  auto open_item = [&](Cursor& u) {
+    const int unit = u.item / p.groups, group = u.item - unit * p.groups;
+    const int tile = group * tiles_per_item + my_tile;
+    if (unit != u.unit) {
+      u.unit = unit;
+      u.e = p.offsets == nullptr ? 0 : find_unit<NT>(p, sh, unit).e;
+    }
+    const int row = (tile >> 3) * 128 + (tile & 7) * 4;
+    u.rows_ok = tile < p.tiles ? p.N - row : 0;
+    u.codes = p.codes + u.e * p.expert_codes + static_cast<int64_t>(row) * (p.K >> 1);
+    u.scales = p.scales + u.e * p.expert_scales +
+               static_cast<int64_t>(tile >> 3) * p.nKT * kChunkBytes + (tile & 7) * 64;
+  };
+  auto open_panel = [&](Cursor& u) {
+    const int lo = u.panel * p.panel, n = min(p.panel, p.chunks - lo);
+    u.chunk = lo + n * my_k / kw;
+    u.end = u.rows_ok > 0 ? lo + n * (my_k + 1) / kw : u.chunk;
+  };
+  // to the next stage that has work; false at the end
+  auto settle = [&](Cursor& u) {
+    while (u.chunk >= u.end) {
+      if (++u.panel >= n_panels) {
+        if (++u.item >= last) return false;
+        u.panel = 0;
+        open_item(u);
+      }
+      open_panel(u);
+    }
+    return true;
+  };
+
+  Cursor in;
+  in.item = first;
+  in.unit = -1;
+  in.e = 0;
+  in.panel = 0;
+  open_item(in);
+  in.chunk = in.end = 0;
+  bool more = n_panels > 0;
+  if (more) {
+    open_panel(in);
+    more = settle(in);
+  }
+  int in_stage = 0;
+  auto issue = [&]() {
+    if (more) {
+      const uint32_t dst = ring + in_stage * kStage;
+      const int k0 = in.chunk * kChunk;
+      if (!p.half_rows) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = (lane >> 2) + 8 * i, ch = lane & 3;
+          const int row = 32 * (r >> 2) + (r & 3), k = k0 + ch * 32;
+          const uint8_t* src = in.codes + static_cast<int64_t>(row) * (p.K >> 1) + (k >> 1);
+          const bool take = row < in.rows_ok && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 16);
+          cp_async<16>(dst + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4), take ? src : p.codes, take);
+        }
       } else {
-        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + r * p.ldy + n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = (lane >> 3) + 4 * i, ch = (lane >> 1) & 3, hf = lane & 1;
+          const int row = 32 * (r >> 2) + (r & 3), k = k0 + ch * 32 + hf * 16;
+          const uint8_t* src = in.codes + static_cast<int64_t>(row) * (p.K >> 1) + (k >> 1);
+          const bool take = row < in.rows_ok && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 8);
+          cp_async<8>(dst + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) + hf * 8, take ? src : p.codes, take);
+        }
+      }
+      if (lane < kScaleBytes / 16) {
+        const int kt = in.chunk * (kNv ? 2 : 1) + (lane >> 2);
+        const uint8_t* src = in.scales + static_cast<int64_t>(kt) * kChunkBytes + (lane & 3) * 16;
+        const bool take = kt < p.nKT && MXFP4_IN_BOUNDS(p, kDbgScales, src, 16);
+        cp_async<16>(dst + kStageCodes + lane * 16, take ? src : p.scales, take);
+      }
+      if (++in_stage == kStages) in_stage = 0;
+      ++in.chunk;
+      more = settle(in);
+    }
+    cp_commit();  // an empty group at the end keeps the count of groups
+  };
+
+  for (int i = 0; i < kAhead; ++i) issue();
+
+  int out_stage = 0, staged_unit = -1, parity = 0;
+  UnitRows ur{0, 0, 0};
+  for (int item = first; item < last; ++item) {
+    const int unit = item / p.groups, group = item - unit * p.groups;
+    const int tile = group * tiles_per_item + my_tile;
+    const bool live = tile < p.tiles;
+    float acc[NT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+    if (unit != staged_unit) ur = find_unit<NT>(p, sh, unit);
+    for (int panel = 0; panel < n_panels; ++panel) {
+      const int lo = panel * p.panel, n = min(p.panel, p.chunks - lo);
+      if (unit != staged_unit || n_panels > 1) {
+        // stage x: 4 lanes to a 32-element block of a token
+        __syncthreads();
+        const int blocks = n * 4;
+        for (int w = threadIdx.x >> 2; w < blocks * ur.n; w += kThreads / 4) {
+          const int t = w / blocks, b = w - t * blocks;
+          const int k = (lo * 4 + b) * 32 + c * 8;
+          int64_t src_row = ur.row0 + t;
+          if (p.row_index != nullptr) src_row = __ldg(p.row_index + src_row);
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          const uint8_t* src = p.x + (src_row * p.ldx + k) * 2;
+          if (src_row >= 0 && src_row < p.src_rows && k < p.K && MXFP4_IN_BOUNDS(p, kDbgX, src, 16))
+            v = __ldg(reinterpret_cast<const uint4*>(src));
+          if constexpr (!kF16) {
+            uint32_t m = 0u;
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a = q[i] & 0x7FFFu, h = (q[i] >> 16) & 0x7FFFu;
+              m = max(m, max(a < 0x7F80u ? a : 0u, h < 0x7F80u ? h : 0u));
+            }
+            m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 1));
+            m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 2));
+            const uint32_t e = max(m >> 7, 15u);
+            const float f = __uint_as_float((269u - e) << 23);       // 2^(15 - (e - 127))
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = __uint_as_float(q[i] << 16) * f;
+              const float h = __uint_as_float(q[i] & 0xFFFF0000u) * f;
+              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(h), "f"(a));
+            }
+            v = make_uint4(o[0], o[1], o[2], o[3]);
+            if (c == 0) xs_s[b * R + t] = __uint_as_float(e > 15u ? (e - 15u) << 23 : 0x00400000u);
+          }
+          *reinterpret_cast<uint4*>(x_s + t * p.x_pitch + b * 64 + c * 16) = v;
+        }
+        __syncthreads();
+      }
+      const int c0 = lo + n * my_k / kw, c1 = live ? lo + n * (my_k + 1) / kw : c0;
+      for (int ch = c0; ch < c1; ++ch) {
+        cp_wait<kAhead - 1>();
+        __syncwarp();  // the copies of all lanes are in; the stage read last is free
+        issue();
+        const uint32_t st = ring + out_stage * kStage;
+        if (++out_stage == kStages) out_stage = 0;
+        // scale words of rows g and g + 8
+        const uint32_t sa = st + kStageCodes + (g & 3) * 16 + (g >> 2) * 4;
+        uint32_t sw[kNv ? 2 : 1][2];
+#pragma unroll
+        for (int i = 0; i < (kNv ? 2 : 1); ++i) {
+          sw[i][0] = lds32(sa + i * 64);
+          sw[i][1] = lds32(sa + i * 64 + 8);
+        }
+        float run[NT][4];  // FP16 x with NVFP4: sums of the whole stage
+        if constexpr (kNv && kF16) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) run[t][i] = 0.0f;
+        }
+        const uint32_t xa = smem_u32(x_s) + g * p.x_pitch + (ch - lo) * (kChunk * 2) + c * 16;
+        const uint32_t sx = smem_u32(xs_s) + ((ch - lo) * 4 * R + 2 * c) * 4;
+#pragma unroll kUnroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t at = ((b ^ ((g >> 1) & 3)) << 4) + c * 4;
+          uint32_t a0[4], a1[4];
+          decode_word(lds32(st + g * 64 + at), a0);
+          decode_word(lds32(st + (g + 8) * 64 + at), a1);
+          float ws0 = 1.0f, ws1 = 1.0f;
+          if constexpr (!kNv) {
+            ws0 = __uint_as_float(e8m0x2_to_bf16x2((sw[0][0] >> (8 * b)) & 0xFFu) << 16);
+            ws1 = __uint_as_float(e8m0x2_to_bf16x2((sw[0][1] >> (8 * b)) & 0xFFu) << 16);
+          } else {
+            // lanes 0, 1 hold the block's first 16 elements, lanes 2, 3 the rest
+            const int sh8 = ((b & 1) * 2 + (c >> 1)) * 8;
+            const uint32_t f0 = e4m3_to_f16x2(((b < 2 ? sw[0][0] : sw[kNv][0]) >> sh8) & 0xFFu);
+            const uint32_t f1 = e4m3_to_f16x2(((b < 2 ? sw[0][1] : sw[kNv][1]) >> sh8) & 0xFFu);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              a0[i] = hmul2(a0[i], f0);
+              a1[i] = hmul2(a1[i], f1);
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            uint4 xb = make_uint4(0u, 0u, 0u, 0u);
+            if (t * 8 + g < ur.n) xb = lds128(xa + t * 8 * p.x_pitch + b * 64);
+            if constexpr (kNv && kF16) {
+              mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+              mma16816(run[t], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
+            } else {
+              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              mma16816(d, a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+              mma16816(d, a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
+              float2 xs = make_float2(1.0f, 1.0f);
+              if constexpr (!kF16) xs = lds64f(sx + (b * R + t * 8) * 4);
+              if constexpr (kNv) {
+                acc[t][0] = fmaf(d[0], xs.x, acc[t][0]);
+                acc[t][1] = fmaf(d[1], xs.y, acc[t][1]);
+                acc[t][2] = fmaf(d[2], xs.x, acc[t][2]);
+                acc[t][3] = fmaf(d[3], xs.y, acc[t][3]);
+              } else {
+                acc[t][0] = fmaf(d[0], ws0 * xs.x, acc[t][0]);
+                acc[t][1] = fmaf(d[1], ws0 * xs.y, acc[t][1]);
+                acc[t][2] = fmaf(d[2], ws1 * xs.x, acc[t][2]);
+                acc[t][3] = fmaf(d[3], ws1 * xs.y, acc[t][3]);
+              }
+            }
+          }
+        }
+        if constexpr (kNv && kF16) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[t][i] += run[t][i];
+        }
+      }
+    }
+    staged_unit = unit;
+
+    // partial sums to shared memory, [warp][row][token]; then every output is
+    // summed over the warps of its tile in their order
+    float* const part = part_s + parity * (kWarps * kTile * R);
+    parity ^= 1;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float* q = part + (warp * kTile + g) * R + t * 8 + 2 * c;
+      *reinterpret_cast<float2*>(q) = make_float2(acc[t][0], acc[t][1]);
+      *reinterpret_cast<float2*>(q + 8 * R) = make_float2(acc[t][2], acc[t][3]);
+    }
+    __syncthreads();
+    const float gs = kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + ur.e, 4)
+                         ? __ldg(p.global_scales + ur.e)
+                         : 1.0f;
+    for (int i = threadIdx.x; i < tiles_per_item * kTile * ur.n; i += kThreads) {
+      const int r = i % kTile, rest = i / kTile;
+      const int tl = rest % tiles_per_item, t = rest / tiles_per_item;
+      const int tl_g = group * tiles_per_item + tl;
+      const int64_t n = (tl_g >> 3) * 128 + (tl_g & 7) * 4 + 32 * (r >> 2) + (r & 3);
+      if (tl_g >= p.tiles || n >= p.N) continue;
+      const float* q = part + (tl * kw * kTile + r) * R + t;
+      float v = 0.0f;
+      for (int w = 0; w < kw; ++w) v += q[w * kTile * R];
+      if constexpr (kNv) v /= gs;
+      const int64_t at = (static_cast<int64_t>(ur.row0) + t) * p.ldy + n;
+      if (p.y_f32) {
+        float* y = reinterpret_cast<float*>(p.y) + at;
+        if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = v;
+      } else {
+        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + at;
         if (MXFP4_IN_BOUNDS(p, kDbgY, y, 2))
-          *y = kF16 ? __half_as_ushort(__float2half_rn(acc)) : static_cast<uint16_t>(cvt_bf16x2(acc, 0.0f));
+          *y = kF16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
       }
     }
   }
+}
+
+constexpr int kMaxSmem = 227 * 1024 - 3 * 1024;  // dynamic; the rest is the static part
+
+template <bool kNv, bool kF16>
+cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStream_t stream) {
+  const auto kernel = nt == 1   ? matvec_kernel<kNv, kF16, 1>
+                      : nt == 2 ? matvec_kernel<kNv, kF16, 2>
+                                : matvec_kernel<kNv, kF16, 4>;
+  const int R = 8 * nt;
+  const int kStage = kStageCodes + (kNv ? 128 : 64);
+  const int sms = sm_count();
+  p.x_rows = p.rows < R ? (p.rows > 0 ? p.rows : 1) : R;
+  // chunks of x at a time: what the shared memory left by the rings and the
+  // partial sums holds
+  const int fixed = kWarps * kStages * kStage + 2 * kWarps * kTile * R * 4;
+  const int budget = kMaxSmem - fixed;
+  const int per_chunk = p.x_rows * kChunk * 2 + (kF16 ? 0 : 4 * R * 4);
+  int panel = (budget - p.x_rows * 128) / per_chunk;
+  if (panel > p.chunks) panel = p.chunks;
+  if (p.chunks > 0) {
+    const int n = (p.chunks + panel - 1) / panel;
+    panel = (p.chunks + n - 1) / n;
+  }
+  p.panel = panel;
+  p.x_pitch = panel * kChunk * 2 + 64;
+  const int smem = fixed + p.x_rows * p.x_pitch + (kF16 ? 0 : panel * 4 * R * 4);
+  // warps per tile: the fewest chunk times over all rounds of items
+  int64_t best = -1;
+  for (int kw = 1; kw <= kWarps; kw *= 2) {
+    const int64_t groups = (p.tiles + kWarps / kw - 1) / (kWarps / kw);
+    const int64_t rounds = (expected_units * groups + sms - 1) / sms;
+    const int64_t cost = rounds * (((p.chunks + kw - 1) / kw) * 4 + 3);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.kw = kw;
+      p.groups = static_cast<int32_t>(groups);
+    }
+  }
+  static std::atomic<uint64_t> ready[3];  // devices on which each kernel may use kMaxSmem
+  if (const cudaError_t e = allow_smem(kernel, kMaxSmem, ready[nt >> 1]); e != cudaSuccess) return e;
+  // a CTA per SM, each with its share of the items (the experts that have
+  // rows are known on the device alone: rows bound their number)
+  const int64_t most = (p.offsets ? p.rows : expected_units) * p.groups;
+  const int64_t grid = most < sms ? (most > 0 ? most : 1) : sms;
+  return launch_pdl(kernel, static_cast<unsigned>(grid), kThreads, smem, stream, p);
 }
 
 }  // namespace
@@ -149,14 +602,17 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
   p.src_rows = a.src_rows;
   p.ldx = a.ldx;
   p.ldy = a.ldy;
-  p.rows = a.rows;
-  p.N = a.N;
+  p.rows = static_cast<int32_t>(a.rows);
+  p.N = static_cast<int32_t>(a.N);
   p.K = static_cast<int32_t>(a.K);
   p.E = a.E;
   p.nKT = static_cast<int32_t>((a.K / (a.nvfp4 ? 16 : 32) + 3) / 4);
+  p.tiles = static_cast<int32_t>((a.N + 127) / 128) * 8;
+  p.chunks = static_cast<int32_t>((a.K + kChunk - 1) / kChunk);
   p.expert_codes = a.N * (a.K / 2);
   p.expert_scales = (a.N + 127) / 128 * p.nKT * kChunkBytes;
   p.y_f32 = a.y_f32;
+  p.half_rows = a.K % 32 != 0;
 #ifdef MXFP4_DEBUG_BOUNDS
   debug_range(p.dbg, kDbgX, a.x, a.src_rows > 0 ? ((a.src_rows - 1) * a.ldx + a.K) * 2 : 0);
   debug_range(p.dbg, kDbgCodes, a.codes, a.E * p.expert_codes);
@@ -164,20 +620,16 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
   debug_range(p.dbg, kDbgGlobal, a.global_scales, a.nvfp4 ? a.E * 4 : 0);
   debug_range(p.dbg, kDbgY, a.y, a.rows > 0 ? ((a.rows - 1) * a.ldy + a.N) * (a.y_f32 ? 4 : 2) : 0);
 #endif
-  cudaLaunchConfig_t cfg = {};
-  const int64_t tiles = (a.N + 7) / 8;
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles > 0 ? tiles : 1),
-                     static_cast<unsigned>(a.rows > 32768 ? 32768 : a.rows > 0 ? a.rows : 1));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const auto kernel = a.nvfp4 ? (a.f16 ? matvec_kernel<true, true> : matvec_kernel<true, false>)
-                              : (a.f16 ? matvec_kernel<false, true> : matvec_kernel<false, false>);
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  // tokens per unit: 8, 16 or 32 columns of the tensor-core product
+  const int64_t avg = a.offsets ? (a.rows + a.E - 1) / (a.E > 0 ? a.E : 1) : a.rows;
+  const int nt = avg <= (a.offsets ? 6 : 8) ? 1 : avg <= (a.offsets ? 12 : 16) ? 2 : 4;
+  const int64_t used = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;  // segments with rows, about
+  const int64_t units = a.offsets ? used : (a.rows + 8 * nt - 1) / (8 * nt);
+  if (a.nvfp4)
+    return a.f16 ? launch_typed<true, true>(p, units, nt, stream)
+                 : launch_typed<true, false>(p, units, nt, stream);
+  return a.f16 ? launch_typed<false, true>(p, units, nt, stream)
+               : launch_typed<false, false>(p, units, nt, stream);
 }
 
 #ifdef MXFP4_DEBUG_BOUNDS

@@ -41,6 +41,8 @@ int matvec_checked(mxfp4::MatvecArgs a, int32_t y_f32, bool moe, void* stream) {
   if (a.K > INT32_MAX / 2 || a.N > kMaxGrid || a.rows > kMaxGrid) return MXFP4_ESHAPE;
   if (a.src_rows > 0 && a.ldx > (INT64_MAX / 4) / a.src_rows) return MXFP4_ESHAPE;
   if (a.rows > 0 && a.ldy > (INT64_MAX / 8) / a.rows) return MXFP4_ESHAPE;
+  // units of 8 or more rows by 16-row tiles of the weights, counted in int32
+  if ((a.rows / 8 + a.E + 1) > INT32_MAX / (a.N / 16 + 8)) return MXFP4_ESHAPE;
   if (reads && a.N * (a.K / 2) > (INT64_MAX / 4) / a.E) return MXFP4_ESHAPE;
   if (!aligned16(a.x) || (reads && a.src_rows > 1 && a.ldx % 8 != 0) || !aligned16(a.codes) ||
       !aligned16(a.scales) || !aligned_to(a.y, static_cast<uintptr_t>(size)) ||

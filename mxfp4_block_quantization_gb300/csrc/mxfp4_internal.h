@@ -3,6 +3,7 @@
 // caller; each launcher only enqueues work and returns the launch status.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <utility>
 
@@ -239,6 +240,20 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), unsigned grid, unsigned threads
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device,
+// asked of the runtime once per device (`ready`: one bit per device).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, int bytes, std::atomic<uint64_t>& ready) {
+  int dev = 0;
+  if (const cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (ready.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace mxfp4
