@@ -88,8 +88,7 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool take) {
-  const int n = take ? kBytes : 0;  // 0: the destination is filled with zeros
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {  // n < kBytes: zeros behind
   if constexpr (kBytes == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else
@@ -201,13 +200,14 @@ __device__ __forceinline__ UnitRows find_unit(const MatvecParams& p, const Share
   }
 }
 
-// Where a warp stands in its stream of (item, panel, chunk) stages.
+// Where a warp stands in its stream of (item, panel, chunk) stages, and what
+// its lanes copy next: pieces of two rows of codes, and of the scales.
 struct Cursor {
-  int item, panel, chunk, end;  // chunk: next of [.., end) in this panel
-  const uint8_t* codes;         // the tile's first row, chunk 0
-  const uint8_t* scales;        // the tile's 64 bytes of scale chunk 0
-  int rows_ok;                  // rows of the tile's four 32-row quarters inside N
+  int item, panel, chunk, end;  // the stage, and the end of this panel's
   int unit, e;
+  const uint8_t* row[2];
+  const uint8_t* scale;
+  int take[2];  // bytes to copy of each row's piece: 0 outside N
 };
 
 template <bool kNv, bool kF16, int NT>
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   constexpr int R = 8 * NT;
   constexpr int kScaleBytes = kNv ? 128 : 64;
   constexpr int kStage = kStageCodes + kScaleBytes;
-  constexpr int kUnroll = NT == 4 ? 1 : 4;  // registers: 32 tokens hold 16 sums and 16 words of x
+  constexpr int kUnroll = NT == 4 ? 1 : NT == 2 ? 2 : 4;  // more tokens, more registers
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -286,36 +286,33 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   const int my_k = warp % kw, my_tile = warp / kw, tiles_per_item = kWarps / kw;
   const int n_panels = p.chunks > 0 ? (p.chunks + p.panel - 1) / p.panel : 0;
 
-  // row i of a tile is tile_base + 32 * (i / 4) + i % 4
-  auto open_item = [&](Cursor& u) {
+  // Row i of a tile is row tile_base + 32 * (i / 4) + i % 4 of the weights.  In
+  // a copy, four lanes take a row's 64 bytes (or eight of its 8-byte pieces).
+  const int tail = p.K % kChunk != 0 ? p.chunks - 1 : -1;  // the chunk that ends before its stage
+  const int pieces = p.half_rows ? 3 : 2;                   // log2 of a row's pieces
+  const int copy_row = lane >> pieces, copy_at = (lane & ((1 << pieces) - 1)) * (64 >> pieces);
+  auto open = [&](Cursor& u) {
     const int unit = u.item / p.groups, group = u.item - unit * p.groups;
-    const int tile = group * tiles_per_item + my_tile;
     if (unit != u.unit) {
       u.unit = unit;
       u.e = p.offsets == nullptr ? 0 : find_unit<NT>(p, sh, unit).e;
     }
-    const int row = (tile >> 3) * 128 + (tile & 7) * 4;
-    u.rows_ok = tile < p.tiles ? p.N - row : 0;
-    u.codes = p.codes + u.e * p.expert_codes + static_cast<int64_t>(row) * (p.K >> 1);
-    u.scales = p.scales + u.e * p.expert_scales +
-               static_cast<int64_t>(tile >> 3) * p.nKT * kChunkBytes + (tile & 7) * 64;
-  };
-  auto open_panel = [&](Cursor& u) {
+    const int tile = group * tiles_per_item + my_tile;
     const int lo = u.panel * p.panel, n = min(p.panel, p.chunks - lo);
     u.chunk = lo + n * my_k / kw;
-    u.end = u.rows_ok > 0 ? lo + n * (my_k + 1) / kw : u.chunk;
-  };
-  // to the next stage that has work; false at the end
-  auto settle = [&](Cursor& u) {
-    while (u.chunk >= u.end) {
-      if (++u.panel >= n_panels) {
-        if (++u.item >= last) return false;
-        u.panel = 0;
-        open_item(u);
-      }
-      open_panel(u);
+    u.end = tile < p.tiles ? lo + n * (my_k + 1) / kw : u.chunk;
+    const int base = (tile >> 3) * 128 + (tile & 7) * 4;
+    const int row = base + 32 * (copy_row >> 2) + (copy_row & 3);
+    const uint8_t* codes = p.codes + u.e * p.expert_codes + u.chunk * (kChunk / 2) + copy_at;
+    const int64_t ld = p.K >> 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u.take[i] = row + 64 * i < p.N ? 16 : 0;
+      u.row[i] = codes + (u.take[i] ? row + 64 * i : 0) * ld;
     }
-    return true;
+    u.scale = p.scales + u.e * p.expert_scales + (tile < p.tiles ? tile & 7 : 0) * 64 +
+              (static_cast<int64_t>(tile < p.tiles ? tile >> 3 : 0) * p.nKT +
+               u.chunk * (kNv ? 2 : 1) + (lane >> 2)) * kChunkBytes + (lane & 3) * 16;
   };
 
   Cursor in;
@@ -323,50 +320,74 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   in.unit = -1;
   in.e = 0;
   in.panel = 0;
-  open_item(in);
   in.chunk = in.end = 0;
   bool more = n_panels > 0;
+  // to the next stage that has work
+  auto settle = [&]() {
+    while (in.chunk >= in.end) {
+      if (++in.panel >= n_panels) {
+        in.panel = 0;
+        if (++in.item >= last) {
+          more = false;
+          return;
+        }
+      }
+      open(in);
+    }
+  };
   if (more) {
-    open_panel(in);
-    more = settle(in);
+    open(in);
+    settle();
   }
   int in_stage = 0;
+  const uint32_t copy_dst = ring + copy_row * 64 + (((copy_at >> 4) ^ ((copy_row >> 1) & 3)) << 4) + (copy_at & 15);
+  const uint32_t scale_dst = ring + kStageCodes + lane * 16;
   auto issue = [&]() {
     if (more) {
-      const uint32_t dst = ring + in_stage * kStage;
-      const int k0 = in.chunk * kChunk;
-      if (!p.half_rows) {
+      const uint32_t at = in_stage * kStage;
+      if (!p.half_rows && in.chunk != tail) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int r = (lane >> 2) + 8 * i, ch = lane & 3;
-          const int row = 32 * (r >> 2) + (r & 3), k = k0 + ch * 32;
-          const uint8_t* src = in.codes + static_cast<int64_t>(row) * (p.K >> 1) + (k >> 1);
-          const bool take = row < in.rows_ok && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 16);
-          cp_async<16>(dst + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4), take ? src : p.codes, take);
+          const bool ok = MXFP4_IN_BOUNDS(p, kDbgCodes, in.row[i], in.take[i]);
+          cp_async<16>(copy_dst + at + i * 512, in.row[i], ok ? in.take[i] : 0);
         }
+        if (lane < kScaleBytes / 16)
+          cp_async<16>(scale_dst + at, in.scale, MXFP4_IN_BOUNDS(p, kDbgScales, in.scale, 16) ? 16 : 0);
       } else {
+        // the last, partial chunk, and rows that start at 8-byte boundaries
+        const int k = in.chunk * kChunk + copy_at * 2;
+        if (!p.half_rows) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = (lane >> 3) + 4 * i, ch = (lane >> 1) & 3, hf = lane & 1;
-          const int row = 32 * (r >> 2) + (r & 3), k = k0 + ch * 32 + hf * 16;
-          const uint8_t* src = in.codes + static_cast<int64_t>(row) * (p.K >> 1) + (k >> 1);
-          const bool take = row < in.rows_ok && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 8);
-          cp_async<8>(dst + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4) + hf * 8, take ? src : p.codes, take);
+          for (int i = 0; i < 2; ++i) {
+            const bool ok = in.take[i] != 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, in.row[i], 16);
+            cp_async<16>(copy_dst + at + i * 512, ok ? in.row[i] : p.codes, ok ? 16 : 0);
+          }
+        } else {
+          // a copy takes the four rows of one 32-row quarter
+          const int tile = (in.item % p.groups) * tiles_per_item + my_tile;
+          const int first_row = (tile >> 3) * 128 + (tile & 7) * 4 + copy_row;
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t* src = in.row[i >> 1] + (i & 1) * 32 * static_cast<int64_t>(p.K >> 1);
+            const bool ok = first_row + 32 * i < p.N && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 8);
+            const int r = copy_row + 4 * i;
+            cp_async<8>(ring + at + r * 64 + (((copy_at >> 4) ^ ((r >> 1) & 3)) << 4) + (copy_at & 15),
+                        ok ? src : p.codes, ok ? 8 : 0);
+          }
         }
-      }
-      if (lane < kScaleBytes / 16) {
-        const int kt = in.chunk * (kNv ? 2 : 1) + (lane >> 2);
-        const uint8_t* src = in.scales + static_cast<int64_t>(kt) * kChunkBytes + (lane & 3) * 16;
-        const bool take = kt < p.nKT && MXFP4_IN_BOUNDS(p, kDbgScales, src, 16);
-        cp_async<16>(dst + kStageCodes + lane * 16, take ? src : p.scales, take);
+        if (lane < kScaleBytes / 16) {
+          const bool ok = in.chunk * (kNv ? 2 : 1) + (lane >> 2) < p.nKT &&
+                          MXFP4_IN_BOUNDS(p, kDbgScales, in.scale, 16);
+          cp_async<16>(scale_dst + at, ok ? in.scale : p.scales, ok ? 16 : 0);
+        }
       }
       if (++in_stage == kStages) in_stage = 0;
-      ++in.chunk;
-      more = settle(in);
+      in.row[0] += kChunk / 2;
+      in.row[1] += kChunk / 2;
+      in.scale += (kNv ? 2 : 1) * kChunkBytes;
+      if (++in.chunk >= in.end) settle();
     }
     cp_commit();  // an empty group at the end keeps the count of groups
   };
-
   for (int i = 0; i < kAhead; ++i) issue();
 
   int out_stage = 0, staged_unit = -1, parity = 0;
@@ -437,6 +458,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           sw[i][0] = lds32(sa + i * 64);
           sw[i][1] = lds32(sa + i * 64 + 8);
         }
+        uint32_t wp[2][2];  // MXFP4: the four scales of a row as BF16 pairs
+        if constexpr (!kNv) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            wp[i][0] = e8m0x2_to_bf16x2(sw[0][i]);
+            wp[i][1] = e8m0x2_to_bf16x2(sw[0][i] >> 16);
+          }
+        }
         float run[NT][4];  // FP16 x with NVFP4: sums of the whole stage
         if constexpr (kNv && kF16) {
 #pragma unroll
@@ -454,8 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           decode_word(lds32(st + (g + 8) * 64 + at), a1);
           float ws0 = 1.0f, ws1 = 1.0f;
           if constexpr (!kNv) {
-            ws0 = __uint_as_float(e8m0x2_to_bf16x2((sw[0][0] >> (8 * b)) & 0xFFu) << 16);
-            ws1 = __uint_as_float(e8m0x2_to_bf16x2((sw[0][1] >> (8 * b)) & 0xFFu) << 16);
+            const uint32_t w0 = b < 2 ? wp[0][0] : wp[0][1], w1 = b < 2 ? wp[1][0] : wp[1][1];
+            ws0 = __uint_as_float(b & 1 ? w0 & 0xFFFF0000u : w0 << 16);
+            ws1 = __uint_as_float(b & 1 ? w1 & 0xFFFF0000u : w1 << 16);
           } else {
             // lanes 0, 1 hold the block's first 16 elements, lanes 2, 3 the rest
             const int sh8 = ((b & 1) * 2 + (c >> 1)) * 8;
@@ -566,12 +596,13 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
   p.panel = panel;
   p.x_pitch = panel * kChunk * 2 + 64;
   const int smem = fixed + p.x_rows * p.x_pitch + (kF16 ? 0 : panel * 4 * R * 4);
-  // warps per tile: the fewest chunk times over all rounds of items
+  // warps per tile: the fewest quarter-chunk times over all rounds of items
+  const int64_t restage = panel < p.chunks ? static_cast<int64_t>(p.x_rows) * p.chunks / 28 : 0;
   int64_t best = -1;
   for (int kw = 1; kw <= kWarps; kw *= 2) {
     const int64_t groups = (p.tiles + kWarps / kw - 1) / (kWarps / kw);
     const int64_t rounds = (expected_units * groups + sms - 1) / sms;
-    const int64_t cost = rounds * (((p.chunks + kw - 1) / kw) * 4 + 3);
+    const int64_t cost = rounds * (((p.chunks + kw - 1) / kw) * 4 + 3 + restage);
     if (best < 0 || cost < best) {
       best = cost;
       p.kw = kw;
