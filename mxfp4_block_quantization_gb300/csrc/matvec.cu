@@ -45,9 +45,12 @@ constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                      // weight rows of a warp's tile
 constexpr int kChunk = 128;                    // elements of K per stage
-constexpr int kStageCodes = kTile * kChunk / 2;  // 1024 bytes
-constexpr int kAhead = 4;                      // stages in flight per warp
-constexpr int kStages = kAhead + 1;
+// A row's 64 bytes of codes in a stage, 80 bytes apart: the eight rows that a
+// fragment's words come from then lie in different banks.
+constexpr int kRowPitch = 80;
+constexpr int kStageCodes = kTile * kRowPitch;
+constexpr int kStages = 4;                     // ring of a warp
+constexpr int kAhead = kStages - 1;            // stages in flight
 
 struct MatvecParams {
   const uint8_t* __restrict__ x;
@@ -69,10 +72,9 @@ struct MatvecParams {
   int32_t E;
   int32_t nKT;        // 4-column scale chunks of a row
   int32_t tiles;      // 16-row tiles of N (8 per 128 rows)
-  int32_t groups;     // tile groups (16 / kw tiles) per unit
-  int32_t kw;         // warps that share a tile, each with its range of K
   int32_t chunks;     // 128-element chunks of K
   int32_t panel;      // chunks of x staged at a time
+  int32_t batch;      // tiles that the CTA's warps take together
   int32_t x_rows;     // token rows that x's shared memory holds
   int32_t x_pitch;    // bytes between them
   int32_t y_f32;
@@ -93,6 +95,13 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// The same for whole pieces where `take`, without a branch around it.
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool take) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<int>(take))
+      : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kPending>
@@ -166,6 +175,7 @@ struct UnitRows {
 struct Shared {
   int32_t prefix[kThreads];  // units up to and with each thread's experts
   int32_t warp_sum[kWarps];
+  int64_t x_row[32];         // x's rows of the unit's tokens (-1: none)
 };
 
 // Expert and rows of unit u, from the prefix sums (same result in all lanes).
@@ -200,14 +210,19 @@ __device__ __forceinline__ UnitRows find_unit(const MatvecParams& p, const Share
   }
 }
 
-// Where a warp stands in its stream of (item, panel, chunk) stages, and what
-// its lanes copy next: pieces of two rows of codes, and of the scales.
+// The warp w whose share [total * w / kWarps, total * (w + 1) / kWarps) holds f.
+__device__ __forceinline__ int share_of(int f, int total) { return ((f + 1) * kWarps - 1) / total; }
+
+// Where a warp's copies stand: the batch of tiles, the panel of x, the chunks
+// left in the warp's share of them, and what its lanes copy next.
 struct Cursor {
-  int item, panel, chunk, end;  // the stage, and the end of this panel's
+  int64_t at;                // first tile of the batch, over all units
+  int panel, left;           // stages left in this batch and panel
+  int tile, chunk, end;      // the tile in its unit, the chunk, and the panel's end
   int unit, e;
-  const uint8_t* row[2];
+  const uint8_t* row[2];     // this lane's pieces of two rows of codes
   const uint8_t* scale;
-  int take[2];  // bytes to copy of each row's piece: 0 outside N
+  int take[2];               // bytes to copy of each: 0 outside N
 };
 
 template <bool kNv, bool kF16, int NT>
@@ -220,11 +235,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  // shared memory: rings | x halves | x block scales | partial sums (two sets)
+  // shared memory: rings | x halves | x block scales | parts of sums | sums of panels
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   uint8_t* const x_s = smem + kWarps * kStages * kStage;
   float* const xs_s = reinterpret_cast<float*>(x_s + p.x_rows * p.x_pitch);
   float* const part_s = xs_s + (kF16 ? 0 : p.panel * 4 * R);
+  float* const sum_s = part_s + (p.batch + kWarps) * kTile * R;
 
   pdl_wait();
   pdl_release();
@@ -277,31 +293,26 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     __syncthreads();
   }
 
-  // this CTA's items: consecutive (unit, tile group) pairs
-  const int64_t items = static_cast<int64_t>(units) * p.groups;
-  const int first = static_cast<int>(items * blockIdx.x / gridDim.x);
-  const int last = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+  // This CTA's tiles, consecutive over the units.  They are taken in batches
+  // of one unit's tiles; a batch's tiles times chunks are one sequence of
+  // stages, of which each warp has an even share: a tile's sum is then split
+  // over one warp or several, whatever the sizes.
+  const int64_t all = static_cast<int64_t>(units) * p.tiles;
+  const int64_t first = all * blockIdx.x / gridDim.x, last = all * (blockIdx.x + 1) / gridDim.x;
   if (first >= last) return;
-  const int kw = p.kw;
-  const int my_k = warp % kw, my_tile = warp / kw, tiles_per_item = kWarps / kw;
   const int n_panels = p.chunks > 0 ? (p.chunks + p.panel - 1) / p.panel : 0;
+  auto batch_tiles = [&](int64_t at) {  // of the batch that starts at tile `at`
+    const int left = p.tiles - static_cast<int>(at % p.tiles);
+    return static_cast<int>(min(static_cast<int64_t>(min(left, p.batch)), last - at));
+  };
 
   // Row i of a tile is row tile_base + 32 * (i / 4) + i % 4 of the weights.  In
   // a copy, four lanes take a row's 64 bytes (or eight of its 8-byte pieces).
   const int tail = p.K % kChunk != 0 ? p.chunks - 1 : -1;  // the chunk that ends before its stage
   const int pieces = p.half_rows ? 3 : 2;                   // log2 of a row's pieces
   const int copy_row = lane >> pieces, copy_at = (lane & ((1 << pieces) - 1)) * (64 >> pieces);
-  auto open = [&](Cursor& u) {
-    const int unit = u.item / p.groups, group = u.item - unit * p.groups;
-    if (unit != u.unit) {
-      u.unit = unit;
-      u.e = p.offsets == nullptr ? 0 : find_unit<NT>(p, sh, unit).e;
-    }
-    const int tile = group * tiles_per_item + my_tile;
-    const int lo = u.panel * p.panel, n = min(p.panel, p.chunks - lo);
-    u.chunk = lo + n * my_k / kw;
-    u.end = tile < p.tiles ? lo + n * (my_k + 1) / kw : u.chunk;
-    const int base = (tile >> 3) * 128 + (tile & 7) * 4;
+  auto open_tile = [&](Cursor& u) {
+    const int base = (u.tile >> 3) * 128 + (u.tile & 7) * 4;
     const int row = base + 32 * (copy_row >> 2) + (copy_row & 3);
     const uint8_t* codes = p.codes + u.e * p.expert_codes + u.chunk * (kChunk / 2) + copy_at;
     const int64_t ld = p.K >> 1;
@@ -310,49 +321,65 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       u.take[i] = row + 64 * i < p.N ? 16 : 0;
       u.row[i] = codes + (u.take[i] ? row + 64 * i : 0) * ld;
     }
-    u.scale = p.scales + u.e * p.expert_scales + (tile < p.tiles ? tile & 7 : 0) * 64 +
-              (static_cast<int64_t>(tile < p.tiles ? tile >> 3 : 0) * p.nKT +
-               u.chunk * (kNv ? 2 : 1) + (lane >> 2)) * kChunkBytes + (lane & 3) * 16;
+    u.scale = p.scales + u.e * p.expert_scales + (u.tile & 7) * 64 +
+              (static_cast<int64_t>(u.tile >> 3) * p.nKT + u.chunk * (kNv ? 2 : 1) + (lane >> 2)) *
+                  kChunkBytes + (lane & 3) * 16;
+  };
+  auto open_panel = [&](Cursor& u) {
+    const int unit = static_cast<int>(u.at / p.tiles);
+    if (unit != u.unit) {
+      u.unit = unit;
+      u.e = p.offsets == nullptr ? 0 : find_unit<NT>(p, sh, unit).e;
+    }
+    const int lo = u.panel * p.panel, n = min(p.panel, p.chunks - lo);
+    const int total = batch_tiles(u.at) * n;
+    const int f0 = total * warp / kWarps;
+    u.left = total * (warp + 1) / kWarps - f0;
+    u.tile = static_cast<int>(u.at % p.tiles) + f0 / n;
+    u.chunk = lo + f0 % n;
+    u.end = lo + n;
+    if (u.left > 0) open_tile(u);
   };
 
   Cursor in;
-  in.item = first;
+  in.at = first;
   in.unit = -1;
   in.e = 0;
   in.panel = 0;
-  in.chunk = in.end = 0;
+  in.left = 0;
   bool more = n_panels > 0;
-  // to the next stage that has work
+  // to the next panel or batch that has a stage for this warp
   auto settle = [&]() {
-    while (in.chunk >= in.end) {
+    while (in.left == 0) {
       if (++in.panel >= n_panels) {
         in.panel = 0;
-        if (++in.item >= last) {
+        in.at += batch_tiles(in.at);
+        if (in.at >= last) {
           more = false;
           return;
         }
       }
-      open(in);
+      open_panel(in);
     }
   };
   if (more) {
-    open(in);
+    open_panel(in);
     settle();
   }
-  int in_stage = 0;
-  const uint32_t copy_dst = ring + copy_row * 64 + (((copy_at >> 4) ^ ((copy_row >> 1) & 3)) << 4) + (copy_at & 15);
+  uint32_t in_at = 0;  // byte offset of the stage to fill
+  const uint32_t copy_dst = ring + copy_row * kRowPitch + copy_at;
   const uint32_t scale_dst = ring + kStageCodes + lane * 16;
   auto issue = [&]() {
     if (more) {
-      const uint32_t at = in_stage * kStage;
+      const uint32_t at = in_at;
       if (!p.half_rows && in.chunk != tail) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const bool ok = MXFP4_IN_BOUNDS(p, kDbgCodes, in.row[i], in.take[i]);
-          cp_async<16>(copy_dst + at + i * 512, in.row[i], ok ? in.take[i] : 0);
+          cp_async<16>(copy_dst + at + i * 8 * kRowPitch, in.row[i], ok ? in.take[i] : 0);
         }
-        if (lane < kScaleBytes / 16)
-          cp_async<16>(scale_dst + at, in.scale, MXFP4_IN_BOUNDS(p, kDbgScales, in.scale, 16) ? 16 : 0);
+        cp_async16_if(scale_dst + at, in.scale,
+                      lane < kScaleBytes / 16 && MXFP4_IN_BOUNDS(p, kDbgScales, in.scale, 16));
       } else {
         // the last, partial chunk, and rows that start at 8-byte boundaries
         const int k = in.chunk * kChunk + copy_at * 2;
@@ -360,18 +387,15 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const bool ok = in.take[i] != 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, in.row[i], 16);
-            cp_async<16>(copy_dst + at + i * 512, ok ? in.row[i] : p.codes, ok ? 16 : 0);
+            cp_async<16>(copy_dst + at + i * 8 * kRowPitch, ok ? in.row[i] : p.codes, ok ? 16 : 0);
           }
         } else {
           // a copy takes the four rows of one 32-row quarter
-          const int tile = (in.item % p.groups) * tiles_per_item + my_tile;
-          const int first_row = (tile >> 3) * 128 + (tile & 7) * 4 + copy_row;
+          const int first_row = (in.tile >> 3) * 128 + (in.tile & 7) * 4 + copy_row;
           for (int i = 0; i < 4; ++i) {
             const uint8_t* src = in.row[i >> 1] + (i & 1) * 32 * static_cast<int64_t>(p.K >> 1);
             const bool ok = first_row + 32 * i < p.N && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 8);
-            const int r = copy_row + 4 * i;
-            cp_async<8>(ring + at + r * 64 + (((copy_at >> 4) ^ ((r >> 1) & 3)) << 4) + (copy_at & 15),
-                        ok ? src : p.codes, ok ? 8 : 0);
+            cp_async<8>(copy_dst + at + i * 4 * kRowPitch, ok ? src : p.codes, ok ? 8 : 0);
           }
         }
         if (lane < kScaleBytes / 16) {
@@ -380,76 +404,132 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           cp_async<16>(scale_dst + at, ok ? in.scale : p.scales, ok ? 16 : 0);
         }
       }
-      if (++in_stage == kStages) in_stage = 0;
+      in_at = in_at == kAhead * kStage ? 0 : in_at + kStage;
       in.row[0] += kChunk / 2;
       in.row[1] += kChunk / 2;
       in.scale += (kNv ? 2 : 1) * kChunkBytes;
-      if (++in.chunk >= in.end) settle();
+      ++in.chunk;
+      if (--in.left == 0) {
+        settle();
+      } else if (in.chunk == in.end) {
+        in.chunk = in.panel * p.panel;
+        ++in.tile;
+        open_tile(in);
+      }
     }
     cp_commit();  // an empty group at the end keeps the count of groups
   };
   for (int i = 0; i < kAhead; ++i) issue();
 
-  int out_stage = 0, staged_unit = -1, parity = 0;
+  uint32_t out_at = 0;  // byte offset of the stage to read
+  int staged_unit = -1;
   UnitRows ur{0, 0, 0};
-  for (int item = first; item < last; ++item) {
-    const int unit = item / p.groups, group = item - unit * p.groups;
-    const int tile = group * tiles_per_item + my_tile;
-    const bool live = tile < p.tiles;
-    float acc[NT][4];
+  for (int64_t at = first; at < last;) {
+    const int unit = static_cast<int>(at / p.tiles), tile0 = static_cast<int>(at % p.tiles);
+    const int n_tiles = batch_tiles(at);
+    at += n_tiles;
+    if (unit != staged_unit) ur = find_unit<NT>(p, sh, unit);
+    // A token past the unit's last reads the last one's x: its column of the
+    // product is not stored.
+    uint32_t xa[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
-    if (unit != staged_unit) ur = find_unit<NT>(p, sh, unit);
-    for (int panel = 0; panel < n_panels; ++panel) {
+      xa[t] = smem_u32(x_s) + min(t * 8 + g, ur.n - 1) * p.x_pitch + c * 16;
+    for (int panel = 0; panel < max(n_panels, 1); ++panel) {
       const int lo = panel * p.panel, n = min(p.panel, p.chunks - lo);
+      // the sums of the batch before are read, and its x
+      __syncthreads();
       if (unit != staged_unit || n_panels > 1) {
-        // stage x: 4 lanes to a 32-element block of a token
-        __syncthreads();
-        const int blocks = n * 4;
-        for (int w = threadIdx.x >> 2; w < blocks * ur.n; w += kThreads / 4) {
-          const int t = w / blocks, b = w - t * blocks;
-          const int k = (lo * 4 + b) * 32 + c * 8;
-          int64_t src_row = ur.row0 + t;
-          if (p.row_index != nullptr) src_row = __ldg(p.row_index + src_row);
-          uint4 v = make_uint4(0u, 0u, 0u, 0u);
-          const uint8_t* src = p.x + (src_row * p.ldx + k) * 2;
-          if (src_row >= 0 && src_row < p.src_rows && k < p.K && MXFP4_IN_BOUNDS(p, kDbgX, src, 16))
-            v = __ldg(reinterpret_cast<const uint4*>(src));
-          if constexpr (!kF16) {
-            uint32_t m = 0u;
-            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t a = q[i] & 0x7FFFu, h = (q[i] >> 16) & 0x7FFFu;
-              m = max(m, max(a < 0x7F80u ? a : 0u, h < 0x7F80u ? h : 0u));
-            }
-            m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 1));
-            m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 2));
-            const uint32_t e = max(m >> 7, 15u);
-            const float f = __uint_as_float((269u - e) << 23);       // 2^(15 - (e - 127))
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = __uint_as_float(q[i] << 16) * f;
-              const float h = __uint_as_float(q[i] & 0xFFFF0000u) * f;
-              asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(h), "f"(a));
-            }
-            v = make_uint4(o[0], o[1], o[2], o[3]);
-            if (c == 0) xs_s[b * R + t] = __uint_as_float(e > 15u ? (e - 15u) << 23 : 0x00400000u);
+        // stage x: 4 lanes to a 32-element block of a token, four blocks'
+        // loads in flight per lane
+        if (unit != staged_unit) {
+          if (threadIdx.x < ur.n) {
+            int64_t src = ur.row0 + threadIdx.x;
+            if (p.row_index != nullptr) src = __ldg(p.row_index + src);
+            sh.x_row[threadIdx.x] = src >= 0 && src < p.src_rows ? src : -1;
           }
-          *reinterpret_cast<uint4*>(x_s + t * p.x_pitch + b * 64 + c * 16) = v;
+          __syncthreads();
+        }
+        constexpr int kGroups = kThreads / 4, kLoads = 4;
+        const int blocks = n * 4;
+        for (int w0 = threadIdx.x >> 2; w0 < blocks * ur.n; w0 += kLoads * kGroups) {
+          uint4 v[kLoads];
+          int tok[kLoads], blk[kLoads];
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) {
+            const int w = w0 + j * kGroups;
+            tok[j] = w / blocks;
+            blk[j] = w - tok[j] * blocks;
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (w >= blocks * ur.n) {
+              tok[j] = -1;
+              continue;
+            }
+            const int k = (lo * 4 + blk[j]) * 32 + c * 8;
+            const int64_t src_row = sh.x_row[tok[j]];
+            const uint8_t* src = p.x + (src_row * p.ldx + k) * 2;
+            if (src_row >= 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgX, src, 16))
+              v[j] = __ldg(reinterpret_cast<const uint4*>(src));
+          }
+#pragma unroll
+          for (int j = 0; j < kLoads; ++j) {
+            uint4 o = v[j];
+            if constexpr (!kF16) {
+              uint32_t m = 0u;
+              const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t a = q[i] & 0x7FFFu, h = (q[i] >> 16) & 0x7FFFu;
+                m = max(m, max(a < 0x7F80u ? a : 0u, h < 0x7F80u ? h : 0u));
+              }
+              m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 1));
+              m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 2));
+              const uint32_t e = max(m >> 7, 15u);
+              const float f = __uint_as_float((269u - e) << 23);  // 2^(15 - (e - 127))
+              uint32_t r[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float a = __uint_as_float(q[i] << 16) * f;
+                const float h = __uint_as_float(q[i] & 0xFFFF0000u) * f;
+                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(h), "f"(a));
+              }
+              o = make_uint4(r[0], r[1], r[2], r[3]);
+              if (c == 0 && tok[j] >= 0)
+                xs_s[blk[j] * R + tok[j]] = __uint_as_float(e > 15u ? (e - 15u) << 23 : 0x00400000u);
+            }
+            if (tok[j] >= 0) *reinterpret_cast<uint4*>(x_s + tok[j] * p.x_pitch + blk[j] * 64 + c * 16) = o;
+          }
         }
         __syncthreads();
       }
-      const int c0 = lo + n * my_k / kw, c1 = live ? lo + n * (my_k + 1) / kw : c0;
-      for (int ch = c0; ch < c1; ++ch) {
+      staged_unit = unit;
+
+      float acc[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+      const int total = n_tiles * n;
+      const int f0 = total * warp / kWarps, f1 = total * (warp + 1) / kWarps;
+      int tile = n > 0 ? f0 / n : 0, ch = n > 0 ? f0 % n : 0;
+      // A warp's part of a tile's sums has slot tile + warp: the shares are
+      // consecutive, so no two parts have the same slot.
+      auto flush = [&]() {
+        float* q = part_s + ((tile + warp) * kTile + g) * R + 2 * c;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          *reinterpret_cast<float2*>(q + t * 8) = make_float2(acc[t][0], acc[t][1]);
+          *reinterpret_cast<float2*>(q + 8 * R + t * 8) = make_float2(acc[t][2], acc[t][3]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+        }
+      };
+      for (int f = f0; f < f1; ++f) {
         cp_wait<kAhead - 1>();
         __syncwarp();  // the copies of all lanes are in; the stage read last is free
         issue();
-        const uint32_t st = ring + out_stage * kStage;
-        if (++out_stage == kStages) out_stage = 0;
+        const uint32_t st = ring + out_at;
+        out_at = out_at == kAhead * kStage ? 0 : out_at + kStage;
         // scale words of rows g and g + 8
         const uint32_t sa = st + kStageCodes + (g & 3) * 16 + (g >> 2) * 4;
         uint32_t sw[kNv ? 2 : 1][2];
@@ -473,14 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
 #pragma unroll
             for (int i = 0; i < 4; ++i) run[t][i] = 0.0f;
         }
-        const uint32_t xa = smem_u32(x_s) + g * p.x_pitch + (ch - lo) * (kChunk * 2) + c * 16;
-        const uint32_t sx = smem_u32(xs_s) + ((ch - lo) * 4 * R + 2 * c) * 4;
+        const uint32_t wa = st + g * kRowPitch + c * 4;
+        const uint32_t xc = ch * (kChunk * 2);
+        const uint32_t sx = smem_u32(xs_s) + (ch * 4 * R + 2 * c) * 4;
 #pragma unroll kUnroll
         for (int b = 0; b < 4; ++b) {
-          const uint32_t at = ((b ^ ((g >> 1) & 3)) << 4) + c * 4;
           uint32_t a0[4], a1[4];
-          decode_word(lds32(st + g * 64 + at), a0);
-          decode_word(lds32(st + (g + 8) * 64 + at), a1);
+          decode_word(lds32(wa + b * 16), a0);
+          decode_word(lds32(wa + 8 * kRowPitch + b * 16), a1);
           float ws0 = 1.0f, ws1 = 1.0f;
           if constexpr (!kNv) {
             const uint32_t w0 = b < 2 ? wp[0][0] : wp[0][1], w1 = b < 2 ? wp[1][0] : wp[1][1];
@@ -499,8 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           }
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            uint4 xb = make_uint4(0u, 0u, 0u, 0u);
-            if (t * 8 + g < ur.n) xb = lds128(xa + t * 8 * p.x_pitch + b * 64);
+            const uint4 xb = lds128(xa[t] + xc + b * 64);
             if constexpr (kNv && kF16) {
               mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
               mma16816(run[t], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
@@ -530,42 +609,51 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
 #pragma unroll
             for (int i = 0; i < 4; ++i) acc[t][i] += run[t][i];
         }
+        if (++ch == n) {
+          flush();
+          ch = 0;
+          ++tile;
+        }
       }
-    }
-    staged_unit = unit;
+      if (ch != 0 && f1 > f0) flush();
+      __syncthreads();
 
-    // partial sums to shared memory, [warp][row][token]; then every output is
-    // summed over the warps of its tile in their order
-    float* const part = part_s + parity * (kWarps * kTile * R);
-    parity ^= 1;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float* q = part + (warp * kTile + g) * R + t * 8 + 2 * c;
-      *reinterpret_cast<float2*>(q) = make_float2(acc[t][0], acc[t][1]);
-      *reinterpret_cast<float2*>(q + 8 * R) = make_float2(acc[t][2], acc[t][3]);
-    }
-    __syncthreads();
-    const float gs = kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + ur.e, 4)
-                         ? __ldg(p.global_scales + ur.e)
-                         : 1.0f;
-    for (int i = threadIdx.x; i < tiles_per_item * kTile * ur.n; i += kThreads) {
-      const int r = i % kTile, rest = i / kTile;
-      const int tl = rest % tiles_per_item, t = rest / tiles_per_item;
-      const int tl_g = group * tiles_per_item + tl;
-      const int64_t n = (tl_g >> 3) * 128 + (tl_g & 7) * 4 + 32 * (r >> 2) + (r & 3);
-      if (tl_g >= p.tiles || n >= p.N) continue;
-      const float* q = part + (tl * kw * kTile + r) * R + t;
-      float v = 0.0f;
-      for (int w = 0; w < kw; ++w) v += q[w * kTile * R];
-      if constexpr (kNv) v /= gs;
-      const int64_t at = (static_cast<int64_t>(ur.row0) + t) * p.ldy + n;
-      if (p.y_f32) {
-        float* y = reinterpret_cast<float*>(p.y) + at;
-        if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = v;
-      } else {
-        uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + at;
-        if (MXFP4_IN_BOUNDS(p, kDbgY, y, 2))
-          *y = kF16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
+      // every output: the parts of its tile in the warps' order, after those
+      // of the panels before
+      const bool done = panel + 1 >= n_panels;
+      const float gs = kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + ur.e, 4)
+                           ? __ldg(p.global_scales + ur.e)
+                           : 1.0f;
+      for (int i = threadIdx.x; i < n_tiles * kTile * ur.n; i += kThreads) {
+        const int r = i % kTile, rest = i / kTile;
+        const int tl = rest % n_tiles, t = rest / n_tiles;
+        float v = 0.0f;
+        if (total > 0) {
+          // the warps whose shares [total * w / 16, total * (w + 1) / 16) meet this tile's stages
+          const int w0 = share_of(tl * n, total), w1 = share_of(tl * n + n - 1, total);
+          for (int w = w0; w <= w1; ++w)
+            if (total * w / kWarps < total * (w + 1) / kWarps)
+              v += part_s[((tl + w) * kTile + r) * R + t];
+        }
+        float* before = sum_s + (tl * kTile + r) * R + t;
+        if (panel > 0) v += *before;
+        if (!done) {
+          *before = v;
+          continue;
+        }
+        const int64_t row = static_cast<int64_t>((tile0 + tl) >> 3) * 128 + ((tile0 + tl) & 7) * 4 +
+                            32 * (r >> 2) + (r & 3);
+        if (row >= p.N) continue;
+        if constexpr (kNv) v /= gs;
+        const int64_t to = (static_cast<int64_t>(ur.row0) + t) * p.ldy + row;
+        if (p.y_f32) {
+          float* y = reinterpret_cast<float*>(p.y) + to;
+          if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = v;
+        } else {
+          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + to;
+          if (MXFP4_IN_BOUNDS(p, kDbgY, y, 2))
+            *y = kF16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
+        }
       }
     }
   }
@@ -582,38 +670,36 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
   const int kStage = kStageCodes + (kNv ? 128 : 64);
   const int sms = sm_count();
   p.x_rows = p.rows < R ? (p.rows > 0 ? p.rows : 1) : R;
-  // chunks of x at a time: what the shared memory left by the rings and the
-  // partial sums holds
-  const int fixed = kWarps * kStages * kStage + 2 * kWarps * kTile * R * 4;
-  const int budget = kMaxSmem - fixed;
+  // Tiles of a CTA, about, and how many of them its warps take together: more
+  // make their shares of the stages more even and stage x less often, but
+  // their sums' parts need room that x's panels need too.
+  const int64_t per_cta = (expected_units * p.tiles + sms - 1) / sms;
+  const int rings = kWarps * kStages * kStage;
   const int per_chunk = p.x_rows * kChunk * 2 + (kF16 ? 0 : 4 * R * 4);
-  int panel = (budget - p.x_rows * 128) / per_chunk;
-  if (panel > p.chunks) panel = p.chunks;
-  if (p.chunks > 0) {
-    const int n = (p.chunks + panel - 1) / panel;
-    panel = (p.chunks + n - 1) / n;
+  const auto parts = [&](int batch) { return (batch + kWarps) * kTile * R * 4; };
+  const auto fits = [&](int room) { return (kMaxSmem - rings - room - p.x_rows * 64) / per_chunk; };
+  int batch = nt == 1 ? 32 : 16;
+  if (batch > per_cta) batch = static_cast<int>(per_cta < 1 ? 1 : per_cta);
+  const int fewest = batch < 8 ? batch : 8;
+  int panel = p.chunks, n_panels = 1, sums = 0;
+  if (p.chunks > fits(parts(fewest))) {  // x does not fit whole
+    sums = batch * kTile * R * 4;
+    panel = fits(parts(batch) + sums);
+    n_panels = (p.chunks + panel - 1) / panel;
+    panel = (p.chunks + n_panels - 1) / n_panels;
+  } else {
+    while (p.chunks > fits(parts(batch))) --batch;
   }
+  p.batch = batch;
   p.panel = panel;
   p.x_pitch = panel * kChunk * 2 + 64;
-  const int smem = fixed + p.x_rows * p.x_pitch + (kF16 ? 0 : panel * 4 * R * 4);
-  // warps per tile: the fewest quarter-chunk times over all rounds of items
-  const int64_t restage = panel < p.chunks ? static_cast<int64_t>(p.x_rows) * p.chunks / 28 : 0;
-  int64_t best = -1;
-  for (int kw = 1; kw <= kWarps; kw *= 2) {
-    const int64_t groups = (p.tiles + kWarps / kw - 1) / (kWarps / kw);
-    const int64_t rounds = (expected_units * groups + sms - 1) / sms;
-    const int64_t cost = rounds * (((p.chunks + kw - 1) / kw) * 4 + 3 + restage);
-    if (best < 0 || cost < best) {
-      best = cost;
-      p.kw = kw;
-      p.groups = static_cast<int32_t>(groups);
-    }
-  }
+  const int smem = rings + p.x_rows * p.x_pitch + (kF16 ? 0 : panel * 4 * R * 4) +
+                   parts(batch) + sums;
   static std::atomic<uint64_t> ready[3];  // devices on which each kernel may use kMaxSmem
   if (const cudaError_t e = allow_smem(kernel, kMaxSmem, ready[nt >> 1]); e != cudaSuccess) return e;
-  // a CTA per SM, each with its share of the items (the experts that have
+  // a CTA per SM, each with its share of the tiles (the experts that have
   // rows are known on the device alone: rows bound their number)
-  const int64_t most = (p.offsets ? p.rows : expected_units) * p.groups;
+  const int64_t most = (p.offsets ? p.rows : expected_units) * static_cast<int64_t>(p.tiles);
   const int64_t grid = most < sms ? (most > 0 ? most : 1) : sms;
   return launch_pdl(kernel, static_cast<unsigned>(grid), kThreads, smem, stream, p);
 }
@@ -653,7 +739,8 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
 #endif
   // tokens per unit: 8, 16 or 32 columns of the tensor-core product
   const int64_t avg = a.offsets ? (a.rows + a.E - 1) / (a.E > 0 ? a.E : 1) : a.rows;
-  const int nt = avg <= (a.offsets ? 6 : 8) ? 1 : avg <= (a.offsets ? 12 : 16) ? 2 : 4;
+  int nt = avg <= (a.offsets ? 6 : 8) ? 1 : avg <= (a.offsets ? 12 : 16) ? 2 : 4;
+  if (nt == 4 && a.K > 1024) nt = 2;
   const int64_t used = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;  // segments with rows, about
   const int64_t units = a.offsets ? used : (a.rows + 8 * nt - 1) / (8 * nt);
   if (a.nvfp4)
