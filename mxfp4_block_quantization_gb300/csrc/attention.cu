@@ -4,23 +4,57 @@
 //   o = sum_j softmax_j(scale * q . k_j) v_j over the positions j in
 //   [max(0, n - window), n) of each sequence, with k and v decoded from
 //   MXFP4 (e2m1 * 2^(s-127)) or NVFP4 (e2m1 * e4m3(s) / g).
-// One pass over the cache with a running maximum and sum per head, all in
-// float32.  A CTA per (sequence, query head); a warp per position, a lane
-// per head_dim/32 elements.
+// One pass over the cache with a running maximum and sum per head in
+// float32.
+//
+// What bounds it: the cache is read once for the query heads that share a kv
+// head, so HBM does, if the SMs keep up with decoding about 45 values a
+// clock.  Both products run on the tensor cores with the cache as the 16-row
+// operand, so up to 8 query heads cost what one does:
+//   scores  S^T [16 positions x 8 heads] = K [16 x D] Q^T, a position's codes
+//           as they lie (a lane's word of 8 codes meets the same 8 elements
+//           of q);
+//   output  O^T [16 values of D x 8 heads] = V^T [16 x 16 positions] P^T:
+//           ldmatrix transposes V's 16-bit groups of four codes, so a
+//           register holds four codes of each of two positions.
+// The sums keep the heads in the same columns in both, so the softmax's
+// rescaling needs no exchange.
+//
+// A CTA is four warps on one (sequence, kv head, 8 query heads, split of the
+// positions); a warp takes every fourth step of 32 positions with its own
+// ring of copies, maximum, sum and output, so the warps meet once, at the
+// end.  Long sequences are split over CTAs whose partial results a second
+// kernel joins.
+//
+// Scales.  K, MXFP4: a power of two of any size, applied in float32 to the
+// 32-element partial scores; NVFP4: e2m1 * e4m3 has at most 6 bits and is
+// formed in halves, exactly.  V: a position's scales vary along the sum, so
+// they go into the operands: NVFP4 into V; MXFP4 into P, relative to the
+// largest scale that the warp has met in that 32-value block (an integer
+// maximum, with the output rescaled when it grows).  P is rounded to a half (11
+// bits), as the scale times P would be in any 16-bit operand; at 2^15 times
+// its size the product keeps P down to 2^-29.
 #include <cstdint>
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "fragments.cuh"
 #include "mxfp4_device.cuh"
 #include "mxfp4_internal.h"
 
 namespace mxfp4 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kMaxDim = 256;
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 32;   // positions of a warp's step
+constexpr int kStages = 3;
+constexpr int kAhead = kStages - 1;
+constexpr int kHeads = 8;   // query heads of a CTA: the columns of the products
+constexpr int kMinSplit = 256;  // positions below which a split does not pay
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct AttentionParams {
   const uint8_t* __restrict__ q;
@@ -31,6 +65,8 @@ struct AttentionParams {
   const int32_t* __restrict__ seq_lens;
   uint8_t* __restrict__ out;
   float* __restrict__ lse;
+  float* __restrict__ part_o;   // [sequence, head, split, head_dim]
+  float* __restrict__ part_ml;  // [sequence, head, split, 2]: maximum (log2), sum
   int32_t* __restrict__ status;
   int64_t q_seq_stride;
   int64_t q_head_stride;
@@ -39,17 +75,21 @@ struct AttentionParams {
   int32_t num_seqs;
   int32_t num_q_heads;
   int32_t num_kv_heads;
+  int32_t group;     // query heads of a kv head
+  int32_t chunks;    // CTAs of 8 query heads per kv head
+  int32_t splits;
   int32_t num_pages;
   int32_t page_size;
   int32_t head_dim;
   int32_t window;
+  int32_t f16;
   float softmax_scale;
 #ifdef MXFP4_DEBUG_BOUNDS
   DebugRanges dbg;
 #endif
 };
 
-enum : int { kDbgQ = 0, kDbgCodes0, kDbgCodes1, kDbgScales0, kDbgScales1, kDbgTable, kDbgOut };
+enum : int { kDbgQ = 0, kDbgCodes0, kDbgCodes1, kDbgScales0, kDbgScales1, kDbgTable, kDbgOut, kDbgPart };
 
 // The positions [lo, hi) of sequence b; a length out of range gives none.
 __device__ __forceinline__ bool positions(const AttentionParams& p, int b, int& lo, int& hi) {
@@ -59,124 +99,550 @@ __device__ __forceinline__ bool positions(const AttentionParams& p, int b, int& 
   lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
   return ok;
 }
-
-template <bool kNv>
-__device__ __forceinline__ float scale_value(uint32_t s) {
-  if constexpr (kNv) return e4m3_to_f32(s);
-  return s == 255u ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(s);
+// Over how many CTAs a sequence of n positions is split.
+__device__ __forceinline__ int splits_of(const AttentionParams& p, int n) {
+  return max(1, min(p.splits, (n + kMinSplit - 1) / kMinSplit));
 }
 
-template <bool kNv, bool kF16>
-__global__ void __launch_bounds__(kThreads) attention_kernel(const AttentionParams p) {
-  __shared__ float s_o[kWarps][kMaxDim];
-  __shared__ float s_m[kWarps], s_l[kWarps];
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// kBytes consecutive bytes as words, by the widest loads their alignment (a
+// multiple of kBytes) allows.
+template <int kBytes>
+__device__ __forceinline__ void load_bytes(uint32_t (&w)[(kBytes + 3) / 4], const uint8_t* p) {
+  if constexpr (kBytes % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < kBytes / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < (kBytes + 3) / 4; ++i) w[i] = 0u;
+    if constexpr (kBytes % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 2; ++i)
+        w[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i % 2));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBytes; ++i) w[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
+    }
+  }
+}
+
+// Status word: every length and every page that a sequence needs.
+__device__ __forceinline__ void write_status(const AttentionParams& p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int bad = 0;
+  for (int b = warp; b < p.num_seqs; b += kWarps) {
+    int lo, hi;
+    if (!positions(p, b, lo, hi)) bad = 1;
+    const int last = hi > lo ? (hi - 1) / p.page_size : -1;
+    for (int i = lo / p.page_size + lane; i <= last; i += 32) {
+      const int32_t* entry = p.page_table + b * p.table_stride + i;
+      const int32_t page = MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
+      if (page < 0 || page >= p.num_pages) bad = 1;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *p.status = bad ? -7 : 0;
+}
+
+// Shared memory of a stage, for head_dim = 32 * DB.
+template <bool kNv, int DB>
+struct Stage {
+  static constexpr int kScale = kNv ? 2 * DB : DB;         // scale bytes of a position
+  static constexpr int kWords = (kScale + 3) / 4;
+  // Positions an odd number of 16-byte pieces apart: eight rows of a fragment
+  // then lie in different banks.
+  static constexpr int kPitch = (DB | 1) * 16;
+  static constexpr int kK = 0;
+  static constexpr int kV = kStep * kPitch;
+  static constexpr int kScaleK = 2 * kStep * kPitch;             // [position][words]
+  static constexpr int kScaleV = kScaleK + kStep * kWords * 4;   // MXFP4 the same; NVFP4 [block][position]
+  static constexpr int kValid = kScaleV + kStep * kWords * 4;    // a bit per position
+  static constexpr int kBytes = kValid + 16;
+};
+
+// One value of the output: acc / sum (zero without positions), NVFP4 with V's
+// global scale divided out; and, with the first value, the head's lse.
+template <bool kNv>
+__device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head, int d, int D, float acc,
+                                          float sum, float top) {
+  float v = sum == 0.0f ? 0.0f : acc / sum;
+  if constexpr (kNv) v /= __ldg(p.global_scales[1]);
+  uint16_t* y = reinterpret_cast<uint16_t*>(p.out) + head * D + d;
+  if (MXFP4_IN_BOUNDS(p, kDbgOut, y, 2))
+    *y = p.f16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
+  if (d == 0 && p.lse != nullptr) p.lse[head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+}
+
+template <bool kNv, int DB>
+__global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionParams p) {
+  using S = Stage<kNv, DB>;
+  constexpr int D = 32 * DB;
+  extern __shared__ __align__(128) uint8_t smem[];
   pdl_wait();
   pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (blockIdx.x == static_cast<unsigned>(p.num_seqs * p.num_q_heads)) {  // the status word
-    int bad = 0;
-    for (int b = warp; b < p.num_seqs; b += kWarps) {
-      int lo, hi;
-      if (!positions(p, b, lo, hi)) bad = 1;
-      const int last = hi > lo ? (hi - 1) / p.page_size : -1;
-      for (int i = lo / p.page_size + lane; i <= last; i += 32) {
-        const int32_t page = __ldg(p.page_table + b * p.table_stride + i);
-        if (page < 0 || page >= p.num_pages) bad = 1;
-      }
-    }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *p.status = bad ? -7 : 0;
+  const int g = lane >> 2, c = lane & 3;
+
+  // CTA -> (sequence, kv head, 8 query heads, split); one more for the status
+  const int per_seq = p.num_kv_heads * p.chunks * p.splits;
+  const int b = blockIdx.x / per_seq;
+  if (b >= p.num_seqs) {
+    write_status(p);
     return;
   }
-  const int b = blockIdx.x / p.num_q_heads, h = blockIdx.x % p.num_q_heads;
-  const int kvh = h / (p.num_q_heads / p.num_kv_heads);
-  const int D = p.head_dim;
-  const int per = kNv ? 16 : 32;
+  int rest = blockIdx.x - b * per_seq;
+  const int kvh = rest % p.num_kv_heads;
+  rest /= p.num_kv_heads;
+  const int chunk = rest % p.chunks, split = rest / p.chunks;
   int lo, hi;
   positions(p, b, lo, hi);
-  // a lane's elements: pairs 2 * (lane + 32 i)
-  float q[8], o[8];
-  const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.q) + b * p.q_seq_stride + h * p.q_head_stride;
+  const int splits = splits_of(p, hi - lo);
+  if (split >= splits) return;
+  // this CTA's positions: whole steps, as even as they come
+  const int steps = (hi - lo + kStep - 1) / kStep;
+  const int first = lo + static_cast<int>(static_cast<int64_t>(steps) * split / splits) * kStep;
+  const int last = min(hi, lo + static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / splits) * kStep);
+  const int head0 = kvh * p.group + chunk * kHeads;
+  const int heads = min(kHeads, p.group - chunk * kHeads);
+
+  // ---- copies
+  const uint32_t ring = smem_u32(smem) + warp * kStages * S::kBytes;
+  const int32_t* table = p.page_table + b * p.table_stride;
+  auto page_of = [&](int t) {
+    if (t >= last) return -1;
+    const int32_t* entry = table + t / p.page_size;
+    return MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
+  };
+  int next = first + warp * kStep + lane;  // this lane's position in the step to copy
+  int next_page = page_of(next);
+  uint32_t fill = 0, pending = 0;          // stage to fill; stage whose scales are in registers
+  uint32_t sk[S::kWords], sv[S::kWords];
+  bool have = false;
+  auto store_scales = [&]() {
+    if (!have) return;
+    const uint32_t st = ring + pending;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int d = (i >> 1) * 64 + lane * 2 + (i & 1);
-    o[i] = 0.0f;
-    q[i] = 0.0f;
-    if (d < D && MXFP4_IN_BOUNDS(p, kDbgQ, qp + d, 2))
-      q[i] = kF16 ? __uint_as_float(f16_bits_to_f32_bits(qp[d])) : __uint_as_float(static_cast<uint32_t>(qp[d]) << 16);
-  }
-  const float kg = kNv ? 1.0f / __ldg(p.global_scales[0]) : 1.0f;
-  const float vg = kNv ? 1.0f / __ldg(p.global_scales[1]) : 1.0f;
-  float m = -INFINITY, l = 0.0f;
-  for (int j = lo + warp; j < hi; j += kWarps) {
-    const int32_t page = __ldg(p.page_table + b * p.table_stride + j / p.page_size);
-    if (page < 0 || page >= p.num_pages) continue;
-    const int64_t row = (static_cast<int64_t>(page) * p.num_kv_heads + kvh) * p.page_size + j % p.page_size;
-    float dot = 0.0f;
-    float v[8];
+    for (int i = 0; i < S::kWords; ++i) {
+      sts32(st + S::kScaleK + (lane * S::kWords + i) * 4, sk[i]);
+      if constexpr (!kNv) sts32(st + S::kScaleV + (lane * S::kWords + i) * 4, sv[i]);
+    }
+    if constexpr (kNv) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int d = i * 64 + lane * 2;
-      v[2 * i] = v[2 * i + 1] = 0.0f;
-      if (d >= D) continue;
-      uint32_t h2[2];
-      float s[2];
+      for (int i = 0; i < S::kScale; ++i) sts8(st + S::kScaleV + i * kStep + lane, sv[i / 4] >> (8 * (i % 4)));
+    }
+  };
+  auto issue = [&]() {
+    store_scales();
+    have = next - lane < last;
+    if (have) {
+      const bool ok = next_page >= 0 && next_page < p.num_pages;
+      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
+      const int64_t row =
+          ok ? (static_cast<int64_t>(next_page) * p.num_kv_heads + kvh) * p.page_size + next % p.page_size : 0;
+      const uint32_t st = ring + fill;
 #pragma unroll
-      for (int part = 0; part < 2; ++part) {
-        const uint8_t* cp = p.codes[part] + row * (D / 2) + d / 2;
-        const uint8_t* sp = p.scales[part] + row * (D / per) + d / per;
-        h2[part] = 0u;
-        s[part] = 0.0f;
-        if (MXFP4_IN_BOUNDS(p, kDbgCodes0 + part, cp, 1) && MXFP4_IN_BOUNDS(p, kDbgScales0 + part, sp, 1)) {
-          h2[part] = cvt_e2m1x2_to_f16x2(__ldg(cp));
-          s[part] = scale_value<kNv>(__ldg(sp));
+      for (int i = 0; i < DB; ++i) {
+        const int piece = i * 32 + lane, at = piece / DB, ch = piece - at * DB;
+        const int64_t off = __shfl_sync(0xFFFFFFFFu, row, at) * (D / 2) + ch * 16;
+        const bool take = (valid >> at) & 1u;
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          const uint8_t* src = p.codes[part] + off;
+          const bool in = take && MXFP4_IN_BOUNDS(p, kDbgCodes0 + part, src, 16);
+          cp_async<16>(st + (part ? S::kV : S::kK) + at * S::kPitch + ch * 16, src, in ? 16 : 0);
         }
       }
-      dot = fmaf(q[2 * i], half_lo_to_f32(h2[0]) * s[0], dot);
-      dot = fmaf(q[2 * i + 1], half_hi_to_f32(h2[0]) * s[0], dot);
-      v[2 * i] = half_lo_to_f32(h2[1]) * s[1];
-      v[2 * i + 1] = half_hi_to_f32(h2[1]) * s[1];
+#pragma unroll
+      for (int i = 0; i < S::kWords; ++i) sk[i] = sv[i] = 0u;
+      if (ok) {
+        const uint8_t* ks = p.scales[0] + row * S::kScale;
+        const uint8_t* vs = p.scales[1] + row * S::kScale;
+        if (MXFP4_IN_BOUNDS(p, kDbgScales0, ks, S::kScale)) load_bytes<S::kScale>(sk, ks);
+        if (MXFP4_IN_BOUNDS(p, kDbgScales1, vs, S::kScale)) load_bytes<S::kScale>(sv, vs);
+      }
+      if (lane == 0) sts32(st + S::kValid, valid);
+      pending = fill;
+      fill = fill == kAhead * S::kBytes ? 0 : fill + S::kBytes;
+      next += kWarps * kStep;
+      next_page = page_of(next);
     }
-    for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
-    const float a = dot * kg * p.softmax_scale;
-    const float top = fmaxf(m, a);
-    const float keep = m == -INFINITY ? 0.0f : expf(m - top);
-    const float w = top == -INFINITY ? 0.0f : expf(a - top);
-    l = l * keep + w;
-    m = top;
+    cp_commit();  // an empty group at the end keeps the count of groups
+  };
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * keep + w * v[i];
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
+  for (int i = 0; i < kAhead; ++i) issue();
+
+  // ---- q: a lane holds elements 8c..8c+7 of each 32-element block of head g,
+  // as halves; BF16 scaled by the head's power of two (see matvec.cu)
+  uint4 q[DB];
+  float qs0, qs1;  // what undoes it, with the softmax's scale, for heads 2c and 2c + 1
+  {
+    const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.q) + b * p.q_seq_stride +
+                         static_cast<int64_t>(head0 + g) * p.q_head_stride + c * 8;
+    uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int d = (i >> 1) * 64 + lane * 2 + (i & 1);
-    if (d < D) s_o[warp][d] = o[i];
+    for (int i = 0; i < DB; ++i) {
+      q[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (g < heads && MXFP4_IN_BOUNDS(p, kDbgQ, qp + i * 32, 16))
+        q[i] = __ldg(reinterpret_cast<const uint4*>(qp + i * 32));
+      m = max_finite_bf16x2(max_finite_bf16x2(m, q[i].x), q[i].y);
+      m = max_finite_bf16x2(max_finite_bf16x2(m, q[i].z), q[i].w);
+    }
+    float inverse = 1.0f;
+    if (!p.f16) {
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      const float f = half_scale(m, inverse);
+      auto scaled = [&](uint32_t v) {
+        return pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
+      };
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+        q[i] = make_uint4(scaled(q[i].x), scaled(q[i].y), scaled(q[i].z), scaled(q[i].w));
+    }
+    const float more = p.softmax_scale * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
+    qs0 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c);
+    qs1 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4);
+    qs0 *= more;
+    qs1 *= more;
+  }
+
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // of heads 2c and 2c + 1, log2
+  float o[DB][2][4];
+#pragma unroll
+  for (int i = 0; i < DB; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] = 0.0f;
+  int vref[DB];  // MXFP4: the largest scale byte of V so far, per block (same in all lanes)
+#pragma unroll
+  for (int i = 0; i < DB; ++i) vref[i] = 0;
+
+  uint32_t read = 0;
+  for (int t0 = first + warp * kStep; t0 < last; t0 += kWarps * kStep) {
+    cp_wait<kAhead - 1>();
+    __syncwarp();  // all lanes' copies and scales are in; the stage read last is free
+    issue();
+    const uint32_t st = ring + read;
+    read = read == kAhead * S::kBytes ? 0 : read + S::kBytes;
+    const uint32_t valid = lds32(st + S::kValid);
+
+    // ---- scores of 2 x 16 positions by 8 heads
+    float s[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
+      uint32_t w0[S::kWords], w1[S::kWords];  // scales of positions g and g + 8
+#pragma unroll
+      for (int i = 0; i < S::kWords; ++i) {
+        w0[i] = lds32(st + S::kScaleK + ((t * 16 + g) * S::kWords + i) * 4);
+        w1[i] = lds32(st + S::kScaleK + ((t * 16 + g + 8) * S::kWords + i) * 4);
+      }
+      const uint32_t ka = st + S::kK + (t * 16 + g) * S::kPitch + c * 4;
+#pragma unroll
+      for (int i = 0; i < DB; ++i) {
+        uint32_t a0[4], a1[4];
+        decode_word(lds32(ka + i * 16), a0);
+        decode_word(lds32(ka + 8 * S::kPitch + i * 16), a1);
+        if constexpr (kNv) {
+          const uint32_t pick = ((i & 1) * 2 + (c >> 1)) * 0x11u;  // the block's byte, twice
+          const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(w0[i / 2], 0u, pick));
+          const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(w1[i / 2], 0u, pick));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            a0[k] = hmul2(a0[k], f0);
+            a1[k] = hmul2(a1[k], f1);
+          }
+          mma16816(s[t], a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
+          mma16816(s[t], a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
+        } else {
+          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma16816(d, a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
+          mma16816(d, a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
+          const uint32_t p0 = e8m0x2_to_bf16x2(w0[i / 4] >> (16 * (i / 2 % 2)));
+          const uint32_t p1 = e8m0x2_to_bf16x2(w1[i / 4] >> (16 * (i / 2 % 2)));
+          const float f0 = __uint_as_float(i & 1 ? p0 & 0xFFFF0000u : p0 << 16);
+          const float f1 = __uint_as_float(i & 1 ? p1 & 0xFFFF0000u : p1 << 16);
+          s[t][0] = fmaf(d[0], f0, s[t][0]);
+          s[t][1] = fmaf(d[1], f0, s[t][1]);
+          s[t][2] = fmaf(d[2], f1, s[t][2]);
+          s[t][3] = fmaf(d[3], f1, s[t][3]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const bool seen = (valid >> (t * 16 + g + 8 * r)) & 1u;
+        s[t][2 * r] = seen ? s[t][2 * r] * qs0 : -INFINITY;
+        s[t][2 * r + 1] = seen ? s[t][2 * r + 1] * qs1 : -INFINITY;
+      }
+    }
+
+    // ---- running maximum and sum
+    float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+    float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+    if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
+#pragma unroll
+      for (int k = 4; k < 32; k *= 2) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, k));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, k));
+      }
+      x0 = fmaxf(x0, m0);
+      x1 = fmaxf(x1, m1);
+      const float k0 = exp2_approx(m0 - (x0 == -INFINITY ? 0.0f : x0));
+      const float k1 = exp2_approx(m1 - (x1 == -INFINITY ? 0.0f : x1));
+      m0 = x0;
+      m1 = x1;
+      l0 *= k0;
+      l1 *= k1;
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= j & 1 ? k1 : k0;
+    }
+    const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+    uint32_t pk[2][2];  // P of positions g and g + 8 of each half, heads 2c and 2c + 1
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float e0 = exp2_approx(s[t][2 * r] - z0), e1 = exp2_approx(s[t][2 * r + 1] - z1);
+        l0 += e0;
+        l1 += e1;
+        pk[t][r] = pack_f16x2(e0, e1);
+      }
+
+    // ---- output
+    uint32_t vw[2][2][S::kWords];  // MXFP4: V's scales of the lane's four positions
+    if constexpr (!kNv) {
+      bool grow = false;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int i = 0; i < S::kWords; ++i)
+            vw[t][r][i] = lds32(st + S::kScaleV + ((t * 16 + g + 8 * r) * S::kWords + i) * 4);
+      int top[DB];
+#pragma unroll
+      for (int i = 0; i < DB; ++i) {
+        top[i] = vref[i];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) top[i] = max(top[i], static_cast<int>((vw[t][r][i / 4] >> (8 * (i % 4))) & 0xFFu));
+        grow |= top[i] > vref[i];
+      }
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          const int now = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(top[i])));
+          const float f = __uint_as_float(static_cast<uint32_t>(max(127 + vref[i] - now, 0)) << 23);
+          vref[i] = now;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= f;
+        }
+      }
+    }
+    uint32_t pb[2][2];  // P^T: columns of heads, pairs of positions
+    if constexpr (kNv) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) pb[t][r] = movmatrix_trans(pk[t][r]);
+    }
+    const uint32_t va = st + S::kV + lane * S::kPitch;
+#pragma unroll
+    for (int i = 0; i < DB; ++i) {
+      if constexpr (!kNv) {
+        const int up = 30 - vref[i];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int byte = static_cast<int>((vw[t][r][i / 4] >> (8 * (i % 4))) & 0xFFu);
+            // 2^(15 + byte - vref) in both halves
+            const uint32_t f = static_cast<uint32_t>(max(byte + up, 0)) * 0x04000400u;
+            pb[t][r] = movmatrix_trans(hmul2(pk[t][r], f));
+          }
+      }
+      uint32_t v[4];
+      ldmatrix4_trans(v, va + i * 16);
+      uint32_t h[4][4];  // [8 positions][code]: that code of positions 2c and 2c + 1
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t e[4];
+        decode_word(v[k], e);  // codes 0, 1 | 2, 3 of position 2c, then of 2c + 1
+        h[k][0] = __byte_perm(e[0], e[2], 0x5410);
+        h[k][1] = __byte_perm(e[0], e[2], 0x7632);
+        h[k][2] = __byte_perm(e[1], e[3], 0x5410);
+        h[k][3] = __byte_perm(e[1], e[3], 0x7632);
+        if constexpr (kNv) {
+          const uint32_t f =
+              e4m3x2_to_f16x2(lds16(st + S::kScaleV + (2 * i + (g >> 2)) * kStep + 8 * k + 2 * c));
+#pragma unroll
+          for (int n = 0; n < 4; ++n) h[k][n] = hmul2(h[k][n], f);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        mma16816(o[i][0], h[2 * t][0], h[2 * t][1], h[2 * t + 1][0], h[2 * t + 1][1], pb[t][0], pb[t][1]);
+        mma16816(o[i][1], h[2 * t][2], h[2 * t][3], h[2 * t + 1][2], h[2 * t + 1][3], pb[t][0], pb[t][1]);
+      }
+    }
+  }
+  cp_wait<0>();
+
+  // ---- the four warps' results
+#pragma unroll
+  for (int k = 4; k < 32; k *= 2) {
+    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, k);
+    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, k);
+  }
+  __syncthreads();  // the rings are free
+  float* const so = reinterpret_cast<float*>(smem);             // [warp][head][D]
+  float* const sm = so + kWarps * kHeads * D;                   // [warp][head][2]
+#pragma unroll
+  for (int i = 0; i < DB; ++i) {
+    // MXFP4: 2^(vref - 127 - 15); a block that met the NaN scale is NaN
+    float f = 1.0f;
+    if constexpr (!kNv)
+      f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-15f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      so[(warp * kHeads + 2 * c + (j & 1)) * D + i * 32 + 4 * g + 2 * (j >> 2) + ((j >> 1) & 1)] =
+          o[i][j >> 2][j & 3] * f;
+  }
+  if (g == 0) {
+    float* q2 = sm + (warp * kHeads + 2 * c) * 2;
+    q2[0] = m0;
+    q2[1] = l0;
+    q2[2] = m1;
+    q2[3] = l1;
   }
   __syncthreads();
-  float top = -INFINITY, sum = 0.0f;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  for (int w = 0; w < kWarps; ++w)
-    if (s_m[w] != -INFINITY) sum += s_l[w] * expf(s_m[w] - top);
-  const int64_t head = static_cast<int64_t>(b) * p.num_q_heads + h;
-  for (int d = threadIdx.x; d < D; d += kThreads) {
-    float acc = 0.0f;
-    for (int w = 0; w < kWarps; ++w)
-      if (s_m[w] != -INFINITY) acc += s_o[w][d] * expf(s_m[w] - top);
-    acc = sum > 0.0f || sum != sum ? acc * vg / sum : 0.0f;
-    uint16_t* y = reinterpret_cast<uint16_t*>(p.out) + head * D + d;
-    if (MXFP4_IN_BOUNDS(p, kDbgOut, y, 2))
-      *y = kF16 ? __half_as_ushort(__float2half_rn(acc)) : static_cast<uint16_t>(cvt_bf16x2(acc, 0.0f));
+  const int64_t head_at = static_cast<int64_t>(b) * p.num_q_heads + head0;
+  for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+    const int h = i / D, d = i - h * D;
+    float top = -INFINITY, sum = 0.0f, acc = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[(w * kHeads + h) * 2]);
+    const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2_approx(sm[(w * kHeads + h) * 2] - z);
+      sum += sm[(w * kHeads + h) * 2 + 1] * f;
+      acc += so[(w * kHeads + h) * D + d] * f;
+    }
+    if (splits > 1) {
+      const int64_t at = (head_at + h) * p.splits + split;
+      if (MXFP4_IN_BOUNDS(p, kDbgPart, p.part_o + at * D + d, 4)) p.part_o[at * D + d] = acc;
+      if (d < 2 && MXFP4_IN_BOUNDS(p, kDbgPart, p.part_ml + at * 2 + d, 4)) p.part_ml[at * 2 + d] = d == 0 ? top : sum;
+    } else {
+      store_out<kNv>(p, head_at + h, d, D, acc, sum, top);
+    }
   }
-  if (threadIdx.x == 0 && p.lse != nullptr) p.lse[head] = sum == 0.0f ? -INFINITY : top + logf(sum);
+}
+
+__global__ void __launch_bounds__(kThreads) attention_status_kernel(const AttentionParams p) {
+  pdl_wait();
+  pdl_release();
+  write_status(p);
+}
+
+// Joins the splits of each head: a warp per (sequence, head).
+template <bool kNv>
+__global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttentionParams p) {
+  pdl_wait();
+  pdl_release();
+  const int64_t head = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (head >= static_cast<int64_t>(p.num_seqs) * p.num_q_heads) return;
+  int lo, hi;
+  positions(p, static_cast<int>(head / p.num_q_heads), lo, hi);
+  const int splits = splits_of(p, hi - lo);
+  if (splits == 1) return;  // written by the CTA itself
+  const float* ml = p.part_ml + head * p.splits * 2;
+  const float* po = p.part_o + head * p.splits * p.head_dim;
+  float top = -INFINITY;
+  for (int s = lane; s < splits; s += 32) top = fmaxf(top, ml[2 * s]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+  const float z = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f, acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float f = exp2_approx(ml[2 * s] - z);
+    sum += ml[2 * s + 1] * f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i * 32 < p.head_dim) acc[i] += po[static_cast<int64_t>(s) * p.head_dim + i * 32 + lane] * f;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i * 32 < p.head_dim) store_out<kNv>(p, head, i * 32 + lane, p.head_dim, acc[i], sum, top);
+}
+
+template <bool kNv, int DB>
+cudaError_t launch_dim(const AttentionParams& p, unsigned grid, cudaStream_t stream) {
+  using S = Stage<kNv, DB>;
+  constexpr int kRings = kWarps * kStages * S::kBytes;
+  constexpr int kJoin = kWarps * kHeads * (32 * DB + 2) * 4;
+  constexpr int kSmem = kRings > kJoin ? kRings : kJoin;
+  static std::atomic<uint64_t> ready{0};
+  if (const cudaError_t e = allow_smem(attention_kernel<kNv, DB>, kSmem, ready); e != cudaSuccess)
+    return e;
+  return launch_pdl(attention_kernel<kNv, DB>, grid, kThreads, kSmem, stream, p);
+}
+
+template <bool kNv>
+cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t stream) {
+  cudaError_t e = cudaSuccess;
+  switch (p.head_dim / 32) {
+    case 1: e = launch_dim<kNv, 1>(p, grid, stream); break;
+    case 2: e = launch_dim<kNv, 2>(p, grid, stream); break;
+    case 3: e = launch_dim<kNv, 3>(p, grid, stream); break;
+    case 4: e = launch_dim<kNv, 4>(p, grid, stream); break;
+    case 5: e = launch_dim<kNv, 5>(p, grid, stream); break;
+    case 6: e = launch_dim<kNv, 6>(p, grid, stream); break;
+    case 7: e = launch_dim<kNv, 7>(p, grid, stream); break;
+    default: e = launch_dim<kNv, 8>(p, grid, stream); break;
+  }
+  if (e != cudaSuccess || p.splits == 1) return e;
+  const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
+  return launch_pdl(attention_join_kernel<kNv>, static_cast<unsigned>((heads + kWarps - 1) / kWarps), kThreads,
+                    0, stream, p);
+}
+
+// CTAs that the positions of a sequence are split over, at most: enough for
+// every SM to have some, in pieces of at least kMinSplit positions.
+int max_splits(int64_t num_seqs, int32_t num_kv_heads, int32_t chunks, int64_t max_len) {
+  constexpr int kResident = 152 * 3;  // CTAs that the GPU holds at once, about
+  const int64_t base = num_seqs * num_kv_heads * chunks;
+  if (base <= 0) return 1;
+  const int64_t want = num_seqs == 1 ? kResident / base : (4 * kResident + base - 1) / base;
+  const int64_t most = (max_len + kMinSplit - 1) / kMinSplit;
+  const int64_t n = want < most ? want : most;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+
+int chunks_of(int32_t num_q_heads, int32_t num_kv_heads) {
+  return (num_q_heads / num_kv_heads + kHeads - 1) / kHeads;
 }
 
 }  // namespace
 
-int64_t attention_workspace_floats(int64_t, int32_t, int32_t, int32_t, int64_t) { return 0; }
+int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+                                   int32_t head_dim, int64_t max_len) {
+  if (num_seqs == 0 || num_q_heads == 0 || head_dim == 0) return 0;
+  const int splits = max_splits(num_seqs, num_kv_heads, chunks_of(num_q_heads, num_kv_heads), max_len);
+  return splits > 1 ? num_seqs * num_q_heads * splits * (head_dim + 2) : 0;
+}
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) {
   const CacheArgs& c = a.cache;
@@ -195,30 +661,46 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   p.q_seq_stride = a.q_seq_stride;
   p.q_head_stride = a.q_head_stride;
   p.table_stride = a.table_stride;
-  p.max_len = a.max_pages * c.page_size;
+  // without pages every position is out of range
+  p.max_len = c.num_pages > 0 ? a.max_pages * c.page_size : 0;
   p.num_seqs = static_cast<int32_t>(a.num_seqs);
-  p.num_q_heads = c.head_dim > 0 ? a.num_q_heads : 0;
+  p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = c.num_heads;
   p.num_pages = static_cast<int32_t>(c.num_pages);
   p.page_size = c.page_size;
   p.head_dim = c.head_dim;
   p.window = a.window;
+  p.f16 = c.f16;
   p.softmax_scale = a.softmax_scale;
+  if (a.num_q_heads == 0 || c.head_dim == 0) {  // the status word alone
+    p.num_kv_heads = p.chunks = p.splits = 1;
+    p.head_dim = 32;
+    if (a.status == nullptr) return cudaSuccess;
+    return launch_pdl(attention_status_kernel, 1, kThreads, 0, stream, p);
+  }
+  p.group = a.num_q_heads / c.num_heads;
+  p.chunks = chunks_of(a.num_q_heads, c.num_heads);
+  const int64_t n_heads = a.num_seqs * a.num_q_heads;
+  p.splits = max_splits(a.num_seqs, c.num_heads, p.chunks, p.max_len);
+  p.part_o = a.workspace;
+  p.part_ml = a.workspace + n_heads * p.splits * c.head_dim;
 #ifdef MXFP4_DEBUG_BOUNDS
   const int64_t rows = c.num_pages * c.page_size * c.num_heads;
-  debug_range(p.dbg, kDbgQ, a.q, a.num_seqs > 0 && a.num_q_heads > 0
+  debug_range(p.dbg, kDbgQ, a.q, a.num_seqs > 0
       ? ((a.num_seqs - 1) * a.q_seq_stride + (a.num_q_heads - 1) * a.q_head_stride + c.head_dim) * 2 : 0);
   for (int i = 0; i < 2; ++i) {
     debug_range(p.dbg, kDbgCodes0 + i, c.codes[i], rows * (c.head_dim / 2));
     debug_range(p.dbg, kDbgScales0 + i, c.scales[i], rows * (c.head_dim / (c.nvfp4 ? 16 : 32)));
   }
-  debug_range(p.dbg, kDbgOut, a.out, a.num_seqs * a.num_q_heads * c.head_dim * 2);
+  debug_range(p.dbg, kDbgTable, a.page_table,
+              a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
+  debug_range(p.dbg, kDbgOut, a.out, n_heads * c.head_dim * 2);
+  debug_range(p.dbg, kDbgPart, a.workspace, p.splits > 1 ? n_heads * p.splits * (c.head_dim + 2) * 4 : 0);
 #endif
-  const unsigned grid = static_cast<unsigned>(p.num_seqs) * p.num_q_heads + (a.status ? 1 : 0);
+  const int64_t grid = a.num_seqs * c.num_heads * p.chunks * p.splits + (a.status ? 1 : 0);
   if (grid == 0) return cudaSuccess;
-  const auto kernel = c.nvfp4 ? (c.f16 ? attention_kernel<true, true> : attention_kernel<true, false>)
-                              : (c.f16 ? attention_kernel<false, true> : attention_kernel<false, false>);
-  return launch_pdl(kernel, grid, kThreads, 0, stream, p);
+  return c.nvfp4 ? launch_format<true>(p, static_cast<unsigned>(grid), stream)
+                 : launch_format<false>(p, static_cast<unsigned>(grid), stream);
 }
 
 #ifdef MXFP4_DEBUG_BOUNDS

@@ -1,0 +1,144 @@
+// fragments.cuh — tensor-core fragments of 4-bit operands, and the
+// asynchronous copies that feed them, shared by the product and attention
+// kernels (matvec.cu, attention.cu).
+//
+// Both use m16n8k16 products of halves with float32 sums.  A thread of a warp
+// is (g, c) = (lane / 4, lane % 4): it holds rows g and g + 8 of A (16 x 16),
+// column g of B (16 x 8), and rows g and g + 8, columns 2c and 2c + 1 of the
+// sums.
+#pragma once
+
+#include <cstdint>
+
+namespace mxfp4 {
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// Asynchronous copy of n <= kBytes bytes to shared memory, zeros behind them.
+template <int kBytes>
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// The same for whole pieces where `take`, without a branch around it.
+__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool take) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<int>(take))
+      : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ float2 lds64f(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts8(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
+// Four 8x8 matrices of 16-bit elements, transposed: thread (g, c) gets
+// elements (2c, g) and (2c + 1, g) of each; lane l names row l % 8 of matrix l / 8.
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a));
+}
+// An 8x8 matrix of halves held as rows (thread (g, c): row g, columns 2c and
+// 2c + 1), transposed in registers.
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// D += A (16x16 halves, row) * B (16x8 halves, col), float32 sums.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// One word of eight E2M1 codes -> four half pairs, in element order.
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t"
+      ".reg .b8 q0, q1, q2, q3;\n\t"
+      "mov.b32 {q0, q1, q2, q3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, q0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, q1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, q2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, q3;\n\t"
+      "}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two float32 -> halves, `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two E8M0 bytes (low 16 bits) -> two BF16 values 2^(s-127) (255: NaN).
+__device__ __forceinline__ uint32_t e8m0x2_to_bf16x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+  return r;
+}
+// Two E4M3 bytes (low 16 bits) -> two halves (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
+  return r;
+}
+
+// The power of two that puts the largest of values with float32 bits of at
+// most `m` << 16 (BF16 magnitudes; infinities and NaN left out) into [2^15,
+// 2^16), and its inverse: what a block of BF16 is scaled by to become halves.
+__device__ __forceinline__ float half_scale(uint32_t m, float& inverse) {
+  const uint32_t e = max(m >> 7, 15u);
+  inverse = __uint_as_float(e > 15u ? (e - 15u) << 23 : 0x00400000u);  // 2^(e - 142)
+  return __uint_as_float((269u - e) << 23);                            // 2^(142 - e)
+}
+// The larger finite magnitude of m and a BF16 pair's two.
+__device__ __forceinline__ uint32_t max_finite_bf16x2(uint32_t m, uint32_t pair) {
+  const uint32_t a = pair & 0x7FFFu, h = (pair >> 16) & 0x7FFFu;
+  return max(m, max(a < 0x7F80u ? a : 0u, h < 0x7F80u ? h : 0u));
+}
+
+}  // namespace mxfp4

@@ -35,6 +35,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "fragments.cuh"
 #include "mxfp4_device.cuh"
 #include "mxfp4_internal.h"
 
@@ -85,87 +86,6 @@ struct MatvecParams {
 };
 
 enum : int { kDbgX = 0, kDbgCodes, kDbgScales, kDbgGlobal, kDbgY, kDbgIndex, kDbgOffsets };
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-template <int kBytes>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {  // n < kBytes: zeros behind
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-// The same for whole pieces where `take`, without a branch around it.
-__device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool take) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<int>(take))
-      : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float2 lds64f(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
-  return v;
-}
-
-// D += A (16x16 halves, row) * B (16x8 halves, col), float32 sums.
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// One word of eight E2M1 codes -> four half pairs, in element order.
-__device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t"
-      ".reg .b8 q0, q1, q2, q3;\n\t"
-      "mov.b32 {q0, q1, q2, q3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, q0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, q1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, q2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, q3;\n\t"
-      "}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Two E8M0 bytes (low 16 bits) -> two BF16 values 2^(s-127) (255: NaN).
-__device__ __forceinline__ uint32_t e8m0x2_to_bf16x2(uint32_t v) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(v)));
-  return r;
-}
-
-// An E4M3 byte -> that value in both halves of a pair (exact).
-__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(byte * 0x0101u)));
-  return r;
-}
 
 // The rows of one unit of work: up to 8*NT consecutive rows of one segment.
 struct UnitRows {
@@ -475,27 +395,21 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           for (int j = 0; j < kLoads; ++j) {
             uint4 o = v[j];
             if constexpr (!kF16) {
-              uint32_t m = 0u;
               const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+              uint32_t m = 0u, r[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t a = q[i] & 0x7FFFu, h = (q[i] >> 16) & 0x7FFFu;
-                m = max(m, max(a < 0x7F80u ? a : 0u, h < 0x7F80u ? h : 0u));
-              }
+              for (int i = 0; i < 4; ++i) m = max_finite_bf16x2(m, q[i]);
               m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 1));
               m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 2));
-              const uint32_t e = max(m >> 7, 15u);
-              const float f = __uint_as_float((269u - e) << 23);  // 2^(15 - (e - 127))
-              uint32_t r[4];
+              float inverse;
+              const float f = half_scale(m, inverse);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float a = __uint_as_float(q[i] << 16) * f;
-                const float h = __uint_as_float(q[i] & 0xFFFF0000u) * f;
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r[i]) : "f"(h), "f"(a));
-              }
+              for (int i = 0; i < 4; ++i)
+                r[i] = pack_f16x2(__uint_as_float(q[i] << 16) * f,
+                                  __uint_as_float(q[i] & 0xFFFF0000u) * f);
               o = make_uint4(r[0], r[1], r[2], r[3]);
               if (c == 0 && tok[j] >= 0)
-                xs_s[blk[j] * R + tok[j]] = __uint_as_float(e > 15u ? (e - 15u) << 23 : 0x00400000u);
+                xs_s[blk[j] * R + tok[j]] = inverse;
             }
             if (tok[j] >= 0) *reinterpret_cast<uint4*>(x_s + tok[j] * p.x_pitch + blk[j] * 64 + c * 16) = o;
           }
@@ -568,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
             ws1 = __uint_as_float(b & 1 ? w1 & 0xFFFF0000u : w1 << 16);
           } else {
             // lanes 0, 1 hold the block's first 16 elements, lanes 2, 3 the rest
-            const int sh8 = ((b & 1) * 2 + (c >> 1)) * 8;
-            const uint32_t f0 = e4m3_to_f16x2(((b < 2 ? sw[0][0] : sw[kNv][0]) >> sh8) & 0xFFu);
-            const uint32_t f1 = e4m3_to_f16x2(((b < 2 ? sw[0][1] : sw[kNv][1]) >> sh8) & 0xFFu);
+            const uint32_t pick = ((b & 1) * 2 + (c >> 1)) * 0x11u;  // that byte twice
+            const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(b < 2 ? sw[0][0] : sw[kNv][0], 0u, pick));
+            const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(b < 2 ? sw[0][1] : sw[kNv][1], 0u, pick));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               a0[i] = hmul2(a0[i], f0);
