@@ -165,6 +165,7 @@ def _load(path=LIB_PATH):
     L.mxfp4_moe_route.restype = ctypes.c_int
     L.mxfp4_moe_route.argtypes = [vp, i64, i32, i32, vp, ctypes.c_size_t, vp, vp, vp, vp, vp]
     f32, size = ctypes.c_float, ctypes.c_size_t
+    decode = L.decode = {}  # (call, NVFP4, FP16) -> entry point and its name
     for nv in (False, True):
         for f16 in (False, True):
             tail = ("_nvfp4" if nv else "") + ("_f16" if f16 else "")
@@ -182,6 +183,7 @@ def _load(path=LIB_PATH):
                 fn = getattr(L, "mxfp4_" + name + tail)
                 fn.restype = ctypes.c_int
                 fn.argtypes = args
+                decode[name, nv, f16] = fn, "mxfp4_" + name + tail
     L.mxfp4_cache_attention_workspace_bytes.restype = size
     L.mxfp4_cache_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i64]
     L.mxfp4_status_string.restype = ctypes.c_char_p
@@ -807,60 +809,109 @@ def mxfp4_dequantize_nvfp4(codes, scales, global_scale, M: int, K: int, y, strea
 
 
 # ------------------------------------------- products with 4-bit weights
+# These calls are made once a layer and token, so their checks read each
+# tensor property once (a few us of host time per call).
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _decode_call(key, device, stream, args):
+    """Launch an entry point on ``device`` (an index): args, then the stream."""
+    fn, name = _lib.decode[key]
+    if stream is not None:
+        stream = stream.cuda_stream
+    elif _raw_current_stream is not None:
+        stream = _raw_current_stream(device)
+    else:
+        stream = torch.cuda.current_stream(device).cuda_stream
+    if device == _get_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if rc:
+        raise MXFP4Error(rc, name)
+
+
 def _half_type(name, t):
     """Whether ``t`` is FP16 (True) or BF16 (False)."""
-    if t.dtype == torch.float16:
+    d = t.dtype
+    if d is torch.float16:
         return True
-    if t.dtype != torch.bfloat16:
-        raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    if d is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float16, got {d}")
     return False
 
 
-def _need_product(x, codes, scales, global_scales, y, rows, E, N, nvfp4):
-    """The tensors of a product of ``rows`` rows with E weights [N, K/2]."""
-    K = x.shape[1]
+def _device_index(name, t):
+    """The index of the CUDA device of the tensor ``t``."""
+    device = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    return device
+
+
+def _address(name, t, device, dtype, nbytes):
+    """The address of ``t`` (None: no address), a contiguous ``dtype`` tensor
+    on ``device`` that holds at least ``nbytes``."""
+    if t is None:
+        return None
+    if _device_index(name, t) != device:
+        raise ValueError(f"all tensors must be on the same CUDA device, {name} is on {t.device}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    have = t.numel() * t.element_size()
+    if have < nbytes:
+        raise ValueError(f"{name} holds {have} bytes; this call needs {nbytes}")
+    return t.data_ptr()
+
+
+def _matrix(name, t, device, dtypes):
+    """(address, rows, columns, row stride) of a 2-D tensor with unit column
+    stride, of one of ``dtypes``."""
+    if _device_index(name, t) != device:
+        raise ValueError(f"all tensors must be on the same CUDA device, {name} is on {t.device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    (rows, cols), (row_stride, col_stride) = t.shape, t.stride()
+    if col_stride != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), rows, cols, row_stride if rows > 1 else cols
+
+
+def _product(x, codes, scales, global_scales, y, E, nvfp4):
+    """The checked arguments that the dense and the experts' products share:
+    (FP16, device, x's, y's, the weights' [, global scales'], N)."""
+    f16 = _half_type("x", x) if isinstance(x, torch.Tensor) else False
+    device = _device_index("x", x)
+    xa = _matrix("x", x, device, (x.dtype,))
+    ya = _matrix("y", y, device, (x.dtype, torch.float32))
+    K, N = xa[2], codes.shape[-2]
     if codes.shape[-1] * 2 != K:
         raise ValueError(f"codes hold {codes.shape[-1] * 2} elements per row, x has {K}")
-    if y.dim() != 2 or y.shape[0] != rows or y.shape[1] != N or (N > 1 and y.stride(1) != 1):
-        raise ValueError(f"y must be [{rows}, {N}] with unit column stride")
-    if y.dtype != x.dtype and y.dtype != torch.float32:
-        raise ValueError(f"y must be {x.dtype} or torch.float32, got {y.dtype}")
-    _need_bytes("codes", codes, E * N * (K // 2))
-    _need_bytes("scales", scales,
-                E * (mxfp4_nvfp4_scale_bytes(N, K) if nvfp4 else mxfp4_scale_bytes(N, K)))
+    if ya[2] != N:
+        raise ValueError(f"y must have {N} columns, got {ya[2]}")
+    per = mxfp4_nvfp4_scale_bytes(N, K) if nvfp4 else mxfp4_scale_bytes(N, K)
+    w = [_address("codes", codes, device, torch.uint8, E * N * (K // 2)),
+         _address("scales", scales, device, torch.uint8, E * per)]
     if nvfp4:
-        _need_bytes("global_scales", global_scales, 4 * E)
-
-
-def _row_stride(t):
-    """The row stride of a 2-D tensor (a single row may report any)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
-
-
-def _strides2(t):
-    """The two outer strides of a 3-D tensor (0 for a dimension of one, which
-    may report any)."""
-    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+        if global_scales is None:
+            raise ValueError("NVFP4 weights have a global scale")
+        w.append(_address("global_scales", global_scales, device, torch.float32, 4 * E))
+    return f16, device, xa, ya, w, N
 
 
 def _matvec(x, codes, scales, global_scale, y, stream, nvfp4):
-    _need_cuda("x", x)
-    _need_cuda("codes", codes, torch.uint8)
-    _need_cuda("scales", scales, torch.uint8)
-    _need_cuda("global_scale", global_scale, torch.float32)
-    _need_cuda("y", y)
-    if x.dim() != 2 or x.stride(1) != 1 or codes.dim() != 2:
-        raise ValueError("x must be 2-D with unit column stride, codes [N, K/2]")
-    T, K = x.shape
-    N = codes.shape[0]
-    _need_product(x, codes, scales, global_scale, y, T, 1, N, nvfp4)
-    name = ("mxfp4_matvec" + ("_nvfp4" if nvfp4 else "") +
-            ("_f16" if _half_type("x", x) else ""))
-    g = (_ptr(global_scale),) if nvfp4 else ()
-    with _switch(_device_of(x, codes, scales, global_scale, y)):
-        _check(getattr(_lib, name)(_ptr(x), T, K, _row_stride(x), _ptr(codes), _ptr(scales), *g,
-                                   N, _ptr(y), _row_stride(y), int(y.dtype == torch.float32),
-                                   _stream(stream, x.device)), name)
+    if codes.dim() != 2:
+        raise ValueError("codes must be [N, K/2]")
+    f16, device, xa, ya, w, N = _product(x, codes, scales, global_scale, y, 1, nvfp4)
+    if ya[1] != xa[1]:
+        raise ValueError(f"y must have {xa[1]} rows, got {ya[1]}")
+    _decode_call(("matvec", nvfp4, f16), device, stream,
+                 (*xa, *w, N, ya[0], ya[3], y.dtype is torch.float32))
 
 
 def mxfp4_matvec(x, codes, scales, y, stream=None) -> None:
@@ -877,35 +928,18 @@ def mxfp4_matvec_nvfp4(x, codes, scales, global_scale, y, stream=None) -> None:
 
 def _moe_matvec(x, row_index, expert_offsets, codes, scales, global_scales, y, status, stream,
                 nvfp4):
-    _need_cuda("x", x)
-    _need_cuda("row_index", row_index, torch.int32)
-    _need_cuda("expert_offsets", expert_offsets, torch.int32)
-    _need_cuda("codes", codes, torch.uint8)
-    _need_cuda("scales", scales, torch.uint8)
-    _need_cuda("global_scales", global_scales, torch.float32)
-    _need_cuda("y", y)
-    _need_cuda("status", status, torch.int32)
-    if x.dim() != 2 or x.stride(1) != 1 or codes.dim() != 3 or y.dim() != 2:
-        raise ValueError("x and y must be 2-D with unit column stride, codes [E, N, K/2]")
-    src, K = x.shape
-    E, N = codes.shape[:2]
-    rows = y.shape[0]
-    _need_product(x, codes, scales, global_scales, y, rows, E, N, nvfp4)
-    _need_bytes("expert_offsets", expert_offsets, 4 * (E + 1))
-    _need_bytes("status", status, 4)
-    if row_index is not None:
-        _need_bytes("row_index", row_index, 4 * rows)
-    elif src < rows:
-        raise ValueError(f"x holds {src} rows; without row_index this call needs {rows}")
-    name = ("mxfp4_moe_matvec" + ("_nvfp4" if nvfp4 else "") +
-            ("_f16" if _half_type("x", x) else ""))
-    g = (_ptr(global_scales),) if nvfp4 else ()
-    with _switch(_device_of(x, row_index, expert_offsets, codes, scales, global_scales, y,
-                            status)):
-        _check(getattr(_lib, name)(_ptr(x), src, K, _row_stride(x), _ptr(row_index), rows,
-                                   _ptr(expert_offsets), E, _ptr(codes), _ptr(scales), *g, N,
-                                   _ptr(y), _row_stride(y), int(y.dtype == torch.float32),
-                                   _ptr(status), _stream(stream, x.device)), name)
+    if codes.dim() != 3:
+        raise ValueError("codes must be [E, N, K/2]")
+    E = codes.shape[0]
+    f16, device, xa, ya, w, N = _product(x, codes, scales, global_scales, y, E, nvfp4)
+    rows = ya[1]
+    offsets = _address("expert_offsets", expert_offsets, device, torch.int32, 4 * (E + 1))
+    index = _address("row_index", row_index, device, torch.int32, 4 * rows)
+    if index is None and xa[1] < rows:
+        raise ValueError(f"x holds {xa[1]} rows; without row_index this call needs {rows}")
+    _decode_call(("moe_matvec", nvfp4, f16), device, stream,
+                 (*xa, index, rows, offsets, E, *w, N, ya[0], ya[3], y.dtype is torch.float32,
+                  _address("status", status, device, torch.int32, 4)))
 
 
 def mxfp4_moe_matvec(x, row_index, expert_offsets, codes, scales, y, status=None,
@@ -938,77 +972,78 @@ class KVCache(NamedTuple):
     v_global: Optional[torch.Tensor] = None
 
 
-def _need_cache(c):
-    """(pages, heads, page_size, head_dim, nvfp4) of a cache whose tensors fit
-    together."""
-    nvfp4 = c.k_global is not None
-    if nvfp4 != (c.v_global is not None):
+def _cache(c, device):
+    """(shape, addresses of codes and scales, of the global scales) of a cache
+    whose tensors fit together."""
+    k_codes, k_scales, v_codes, v_scales, k_global, v_global = c
+    nvfp4 = k_global is not None
+    if nvfp4 != (v_global is not None):
         raise ValueError("an NVFP4 cache has both k_global and v_global, an MXFP4 cache neither")
-    for name, t in (("k_codes", c.k_codes), ("k_scales", c.k_scales), ("v_codes", c.v_codes),
-                    ("v_scales", c.v_scales)):
-        _need_cuda(name, t, torch.uint8)
-        if t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous [pages, heads, page_size, ...] tensor")
-    pages, heads, page_size, half = c.k_codes.shape
-    want = (pages, heads, page_size, half // (8 if nvfp4 else 16))
-    if c.v_codes.shape != c.k_codes.shape or c.k_scales.shape != want or c.v_scales.shape != want:
-        raise ValueError(f"k_codes and v_codes must agree and the scales be {want}")
-    if nvfp4:
-        for name, t in (("k_global", c.k_global), ("v_global", c.v_global)):
-            _need_cuda(name, t, torch.float32)
-            _need_bytes(name, t, 4)
-    return pages, heads, page_size, 2 * half, nvfp4
+    if k_codes.dim() != 4:
+        raise ValueError("k_codes must be [pages, heads, page_size, head_dim/2]")
+    shape = pages, heads, page_size, half = k_codes.shape
+    per = 8 if nvfp4 else 16
+    if v_codes.shape != shape:
+        raise ValueError(f"v_codes must be {tuple(shape)}, got {tuple(v_codes.shape)}")
+    want = (pages, heads, page_size, half // per)
+    if k_scales.shape != want or v_scales.shape != want:
+        raise ValueError(f"k_scales and v_scales must be {want}")
+    u8 = torch.uint8
+    tensors = (_address("k_codes", k_codes, device, u8, 0),
+               _address("k_scales", k_scales, device, u8, 0),
+               _address("v_codes", v_codes, device, u8, 0),
+               _address("v_scales", v_scales, device, u8, 0))
+    scalars = (_address("k_global", k_global, device, torch.float32, 4),
+               _address("v_global", v_global, device, torch.float32, 4)) if nvfp4 else ()
+    return pages, heads, page_size, 2 * half, tensors, scalars
 
 
-def _cache_globals(c, nvfp4):
-    return (_ptr(c.k_global), _ptr(c.v_global)) if nvfp4 else ()
+def _strided(name, t, device, dtype, shape):
+    """(address, outer strides) of a 3-D tensor with unit element stride; a
+    dimension of one, which may report any stride, has 0."""
+    if _device_index(name, t) != device:
+        raise ValueError(f"all tensors must be on the same CUDA device, {name} is on {t.device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    a, b, c = t.stride()
+    if c != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must have unit element stride")
+    return t.data_ptr(), (a if shape[0] > 1 else 0, b if shape[1] > 1 else 0)
 
 
 def mxfp4_cache_write(k, v, slots, cache, status=None, stream=None) -> None:
     """Quantize ``k`` and ``v`` [T, heads, head_dim] (BF16 or FP16, any token
     and head stride that is a multiple of 8) into the slots ``slots`` (int32
     [T], -1: not written) of ``cache``."""
-    pages, heads, page_size, D, nvfp4 = _need_cache(cache)
-    _need_cuda("k", k)
-    _need_cuda("v", v, k.dtype)
-    _need_cuda("slots", slots, torch.int32)
-    _need_cuda("status", status, torch.int32)
+    device = _device_index("k", k)
+    f16 = _half_type("k", k)
+    pages, heads, page_size, D, tensors, scalars = _cache(cache, device)
     T = slots.numel()
-    for name, t in (("k", k), ("v", v)):
-        if t.dim() != 3 or t.shape != (T, heads, D) or (D > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name} must be [{T}, {heads}, {D}] with unit element stride")
-    _need_bytes("slots", slots, 4 * T)
-    _need_bytes("status", status, 4)
-    name = ("mxfp4_cache_write" + ("_nvfp4" if nvfp4 else "") +
-            ("_f16" if _half_type("k", k) else ""))
-    with _switch(_device_of(k, v, slots, *cache, status)):
-        _check(getattr(_lib, name)(
-            _ptr(k), _ptr(v), T, heads, D, *_strides2(k), *_strides2(v),
-            _ptr(slots), pages, page_size, *_cache_globals(cache, nvfp4), _ptr(cache.k_codes),
-            _ptr(cache.k_scales), _ptr(cache.v_codes), _ptr(cache.v_scales), _ptr(status),
-            _stream(stream, k.device)), name)
+    shape = (T, heads, D)
+    ka, ks = _strided("k", k, device, k.dtype, shape)
+    va, vs = _strided("v", v, device, k.dtype, shape)
+    _decode_call(("cache_write", len(scalars) > 0, f16), device, stream,
+                 (ka, va, T, heads, D, *ks, *vs, _address("slots", slots, device, torch.int32, 0),
+                  pages, page_size, *scalars, *tensors,
+                  _address("status", status, device, torch.int32, 4)))
 
 
 def mxfp4_cache_read(cache, slots, k_out, v_out, status=None, stream=None) -> None:
     """Dequantize the slots ``slots`` (int32 [T], -1: zeros) of ``cache`` into
     contiguous ``k_out`` and ``v_out`` [T, heads, head_dim] (BF16 or FP16)."""
-    pages, heads, page_size, D, nvfp4 = _need_cache(cache)
-    _need_cuda("slots", slots, torch.int32)
-    _need_cuda("k_out", k_out)
-    _need_cuda("v_out", v_out, k_out.dtype)
-    _need_cuda("status", status, torch.int32)
+    device = _device_index("k_out", k_out)
+    f16 = _half_type("k_out", k_out)
+    pages, heads, page_size, D, tensors, scalars = _cache(cache, device)
     T = slots.numel()
-    _need_bytes("slots", slots, 4 * T)
-    _need_bytes("k_out", k_out, 2 * T * heads * D)
-    _need_bytes("v_out", v_out, 2 * T * heads * D)
-    _need_bytes("status", status, 4)
-    name = ("mxfp4_cache_read" + ("_nvfp4" if nvfp4 else "") +
-            ("_f16" if _half_type("k_out", k_out) else ""))
-    with _switch(_device_of(slots, k_out, v_out, *cache, status)):
-        _check(getattr(_lib, name)(
-            _ptr(cache.k_codes), _ptr(cache.k_scales), _ptr(cache.v_codes), _ptr(cache.v_scales),
-            *_cache_globals(cache, nvfp4), pages, page_size, heads, D, _ptr(slots), T,
-            _ptr(k_out), _ptr(v_out), _ptr(status), _stream(stream, slots.device)), name)
+    nbytes = 2 * T * heads * D
+    _decode_call(("cache_read", len(scalars) > 0, f16), device, stream,
+                 (*tensors, *scalars, pages, page_size, heads, D,
+                  _address("slots", slots, device, torch.int32, 0), T,
+                  _address("k_out", k_out, device, k_out.dtype, nbytes),
+                  _address("v_out", v_out, device, k_out.dtype, nbytes),
+                  _address("status", status, device, torch.int32, 4)))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -1027,37 +1062,25 @@ def mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, 
     ``seq_lens[b]`` (int32).  ``window`` > 0 keeps the last ``window``
     positions.  ``workspace``: >= mxfp4_cache_attention_workspace_bytes bytes;
     ``lse``: float32 [B, q_heads]."""
-    pages, heads, page_size, D, nvfp4 = _need_cache(cache)
-    _need_cuda("q", q)
-    _need_cuda("out", out, q.dtype)
-    _need_cuda("page_table", page_table, torch.int32)
-    _need_cuda("seq_lens", seq_lens, torch.int32)
-    _need_cuda("workspace", workspace)
-    _need_cuda("lse", lse, torch.float32)
-    _need_cuda("status", status, torch.int32)
-    if q.dim() != 3 or q.shape[2] != D or (D > 1 and q.stride(2) != 1):
-        raise ValueError(f"q must be [sequences, heads, {D}] with unit element stride")
-    B, Hq = q.shape[:2]
-    if (page_table.dim() != 2 or page_table.shape[0] != B or
-            (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-        raise ValueError(f"page_table must be [{B}, max_pages] with unit column stride")
-    max_pages = page_table.shape[1]
-    _need_bytes("seq_lens", seq_lens, 4 * B)
-    _need_bytes("out", out, 2 * B * Hq * D)
-    _need_bytes("lse", lse, 4 * B * Hq)
-    _need_bytes("workspace", workspace, 0)
-    _need_bytes("status", status, 4)
-    name = ("mxfp4_cache_attention" + ("_nvfp4" if nvfp4 else "") +
-            ("_f16" if _half_type("q", q) else ""))
-    ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _switch(_device_of(q, out, page_table, seq_lens, *cache, workspace, lse, status)):
-        _check(getattr(_lib, name)(
-            _ptr(q), B, Hq, D, *_strides2(q), _ptr(cache.k_codes),
-            _ptr(cache.k_scales), _ptr(cache.v_codes), _ptr(cache.v_scales),
-            *_cache_globals(cache, nvfp4), pages, page_size, heads, _ptr(page_table),
-            _row_stride(page_table), max_pages, _ptr(seq_lens), float(softmax_scale),
-            int(window), _ptr(workspace), ws, _ptr(out), _ptr(lse), _ptr(status),
-            _stream(stream, q.device)), name)
+    device = _device_index("q", q)
+    f16 = _half_type("q", q)
+    pages, heads, page_size, D, tensors, scalars = _cache(cache, device)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [sequences, heads, {D}]")
+    B, Hq, _ = q.shape
+    qa, qs = _strided("q", q, device, q.dtype, (B, Hq, D))
+    table = _matrix("page_table", page_table, device, (torch.int32,))
+    if table[1] != B:
+        raise ValueError(f"page_table must have {B} rows, got {table[1]}")
+    ws = _address("workspace", workspace, device, None, 0)
+    _decode_call(("cache_attention", len(scalars) > 0, f16), device, stream,
+                 (qa, B, Hq, D, *qs, *tensors, *scalars, pages, page_size, heads, table[0],
+                  table[3], table[2], _address("seq_lens", seq_lens, device, torch.int32, 4 * B),
+                  softmax_scale, window, ws,
+                  0 if ws is None else workspace.numel() * workspace.element_size(),
+                  _address("out", out, device, q.dtype, 2 * B * Hq * D),
+                  _address("lse", lse, device, torch.float32, 4 * B * Hq),
+                  _address("status", status, device, torch.int32, 4)))
 
 
 # --------------------------------------------------- allocating wrappers
