@@ -131,6 +131,31 @@ __device__ __forceinline__ void load_bytes(uint32_t (&w)[(kBytes + 3) / 4], cons
   }
 }
 
+// kN consecutive float32 of shared memory, kN * 4-byte aligned.
+template <int kN>
+__device__ __forceinline__ void lds_floats(float (&f)[kN], uint32_t a) {
+  if constexpr (kN % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < kN / 4; ++i) {
+      const uint4 v = lds128(a + 16 * i);
+      f[4 * i] = __uint_as_float(v.x);
+      f[4 * i + 1] = __uint_as_float(v.y);
+      f[4 * i + 2] = __uint_as_float(v.z);
+      f[4 * i + 3] = __uint_as_float(v.w);
+    }
+  } else if constexpr (kN % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) {
+      const float2 v = lds64f(a + 8 * i);
+      f[2 * i] = v.x;
+      f[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) f[i] = __uint_as_float(lds32(a + 4 * i));
+  }
+}
+
 // Status word: every length and every page that a sequence needs.
 __device__ __forceinline__ void write_status(const AttentionParams& p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -159,9 +184,12 @@ struct Stage {
   static constexpr int kPitch = (DB | 1) * 16;
   static constexpr int kK = 0;
   static constexpr int kV = kStep * kPitch;
-  static constexpr int kScaleK = 2 * kStep * kPitch;             // [position][words]
-  static constexpr int kScaleV = kScaleK + kStep * kWords * 4;   // MXFP4 the same; NVFP4 [block][position]
-  static constexpr int kValid = kScaleV + kStep * kWords * 4;    // a bit per position
+  static constexpr int kScaleK = 2 * kStep * kPitch;
+  // MXFP4: K's scales as float32 [position][block], V's as halves relative to
+  // the running largest, [block][c][8 positions each][2] (a B fragment's
+  // pairs); NVFP4: the bytes, [position][words] and [block][position].
+  static constexpr int kScaleV = kScaleK + kStep * (kNv ? kWords * 4 : DB * 4);
+  static constexpr int kValid = kScaleV + kStep * (kNv ? kWords * 4 : DB * 2);  // a bit per position
   static constexpr int kBytes = kValid + 16;
 };
 
@@ -179,7 +207,7 @@ __device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head
 }
 
 template <bool kNv, int DB>
-__global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionParams p) {
+__global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) attention_kernel(const AttentionParams p) {
   using S = Stage<kNv, DB>;
   constexpr int D = 32 * DB;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -213,27 +241,51 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
   // ---- copies
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kBytes;
   const int32_t* table = p.page_table + b * p.table_stride;
-  auto page_of = [&](int t) {
-    if (t >= last) return -1;
-    const int32_t* entry = table + t / p.page_size;
-    return MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
-  };
   int next = first + warp * kStep + lane;  // this lane's position in the step to copy
-  int next_page = page_of(next);
+  int page_at = next / p.page_size, in_page = next - page_at * p.page_size;
+  const int page_step = kWarps * kStep / p.page_size;
+  const int in_step = kWarps * kStep - page_step * p.page_size;
+  auto load_page = [&]() {
+    const int32_t* entry = table + page_at;
+    return next < last && MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
+  };
+  int next_page = load_page();
   uint32_t fill = 0, pending = 0;          // stage to fill; stage whose scales are in registers
   uint32_t sk[S::kWords], sv[S::kWords];
-  bool have = false;
+  bool have = false, grown = false;
+  int vrun[DB];  // MXFP4: the largest scale byte of V stored so far, per block (same in all lanes)
+#pragma unroll
+  for (int i = 0; i < DB; ++i) vrun[i] = 0;
+  // a lane has the scales of its position: what all lanes need of them, once
   auto store_scales = [&]() {
     if (!have) return;
     const uint32_t st = ring + pending;
-#pragma unroll
-    for (int i = 0; i < S::kWords; ++i) {
-      sts32(st + S::kScaleK + (lane * S::kWords + i) * 4, sk[i]);
-      if constexpr (!kNv) sts32(st + S::kScaleV + (lane * S::kWords + i) * 4, sv[i]);
-    }
     if constexpr (kNv) {
 #pragma unroll
+      for (int i = 0; i < S::kWords; ++i) sts32(st + S::kScaleK + (lane * S::kWords + i) * 4, sk[i]);
+#pragma unroll
       for (int i = 0; i < S::kScale; ++i) sts8(st + S::kScaleV + i * kStep + lane, sv[i / 4] >> (8 * (i % 4)));
+    } else {
+      int byte[DB];
+      bool more = false;
+#pragma unroll
+      for (int i = 0; i < DB; ++i) {
+        const uint32_t pair = e8m0x2_to_bf16x2(sk[i / 4] >> (16 * (i / 2 % 2)));
+        sts32(st + S::kScaleK + (lane * DB + i) * 4, i & 1 ? pair & 0xFFFF0000u : pair << 16);
+        byte[i] = static_cast<int>((sv[i / 4] >> (8 * (i % 4))) & 0xFFu);
+        more |= byte[i] > vrun[i];
+      }
+      if (__any_sync(0xFFFFFFFFu, more)) {
+        grown = true;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+          vrun[i] = static_cast<int>(
+              __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(max(byte[i], vrun[i]))));
+      }
+      const uint32_t at = st + S::kScaleV + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
+#pragma unroll
+      for (int i = 0; i < DB; ++i)  // 2^(15 + byte - vrun)
+        sts16(at + i * 64, static_cast<uint32_t>(max(byte[i] + 30 - vrun[i], 0)) << 10);
     }
   };
   auto issue = [&]() {
@@ -242,26 +294,25 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
     if (have) {
       const bool ok = next_page >= 0 && next_page < p.num_pages;
       const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
-      const int64_t row =
-          ok ? (static_cast<int64_t>(next_page) * p.num_kv_heads + kvh) * p.page_size + next % p.page_size : 0;
+      const uint32_t row = ok ? (static_cast<uint32_t>(next_page) * p.num_kv_heads + kvh) * p.page_size + in_page : 0u;
       const uint32_t st = ring + fill;
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
         const int piece = i * 32 + lane, at = piece / DB, ch = piece - at * DB;
-        const int64_t off = __shfl_sync(0xFFFFFFFFu, row, at) * (D / 2) + ch * 16;
-        const bool take = (valid >> at) & 1u;
+        const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, row, at)) * (D / 2) + ch * 16;
+        const int take = (valid >> at) & 1u ? 16 : 0;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           const uint8_t* src = p.codes[part] + off;
-          const bool in = take && MXFP4_IN_BOUNDS(p, kDbgCodes0 + part, src, 16);
-          cp_async<16>(st + (part ? S::kV : S::kK) + at * S::kPitch + ch * 16, src, in ? 16 : 0);
+          cp_async<16>(st + (part ? S::kV : S::kK) + at * S::kPitch + ch * 16, src,
+                       MXFP4_IN_BOUNDS(p, kDbgCodes0 + part, src, take) ? take : 0);
         }
       }
 #pragma unroll
       for (int i = 0; i < S::kWords; ++i) sk[i] = sv[i] = 0u;
       if (ok) {
-        const uint8_t* ks = p.scales[0] + row * S::kScale;
-        const uint8_t* vs = p.scales[1] + row * S::kScale;
+        const uint8_t* ks = p.scales[0] + static_cast<uint64_t>(row) * S::kScale;
+        const uint8_t* vs = p.scales[1] + static_cast<uint64_t>(row) * S::kScale;
         if (MXFP4_IN_BOUNDS(p, kDbgScales0, ks, S::kScale)) load_bytes<S::kScale>(sk, ks);
         if (MXFP4_IN_BOUNDS(p, kDbgScales1, vs, S::kScale)) load_bytes<S::kScale>(sv, vs);
       }
@@ -269,7 +320,13 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
       pending = fill;
       fill = fill == kAhead * S::kBytes ? 0 : fill + S::kBytes;
       next += kWarps * kStep;
-      next_page = page_of(next);
+      page_at += page_step;
+      in_page += in_step;
+      if (in_page >= p.page_size) {
+        in_page -= p.page_size;
+        ++page_at;
+      }
+      next_page = load_page();
     }
     cp_commit();  // an empty group at the end keeps the count of groups
   };
@@ -317,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
   for (int i = 0; i < DB; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] = 0.0f;
-  int vref[DB];  // MXFP4: the largest scale byte of V so far, per block (same in all lanes)
+  int vref[DB];  // MXFP4: what the output is relative to: vrun when its scales were stored
 #pragma unroll
   for (int i = 0; i < DB; ++i) vref[i] = 0;
 
@@ -325,6 +382,18 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
   for (int t0 = first + warp * kStep; t0 < last; t0 += kWarps * kStep) {
     cp_wait<kAhead - 1>();
     __syncwarp();  // all lanes' copies and scales are in; the stage read last is free
+    if constexpr (!kNv) {
+      if (grown) {  // by this step's scales, which are the last that were stored
+        grown = false;
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          const float f = __uint_as_float(static_cast<uint32_t>(max(127 + vref[i] - vrun[i], 0)) << 23);
+          vref[i] = vrun[i];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= f;
+        }
+      }
+    }
     issue();
     const uint32_t st = ring + read;
     read = read == kAhead * S::kBytes ? 0 : read + S::kBytes;
@@ -337,10 +406,16 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
 #pragma unroll
       for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
       uint32_t w0[S::kWords], w1[S::kWords];  // scales of positions g and g + 8
+      float f0[DB], f1[DB];
+      if constexpr (kNv) {
 #pragma unroll
-      for (int i = 0; i < S::kWords; ++i) {
-        w0[i] = lds32(st + S::kScaleK + ((t * 16 + g) * S::kWords + i) * 4);
-        w1[i] = lds32(st + S::kScaleK + ((t * 16 + g + 8) * S::kWords + i) * 4);
+        for (int i = 0; i < S::kWords; ++i) {
+          w0[i] = lds32(st + S::kScaleK + ((t * 16 + g) * S::kWords + i) * 4);
+          w1[i] = lds32(st + S::kScaleK + ((t * 16 + g + 8) * S::kWords + i) * 4);
+        }
+      } else {
+        lds_floats<DB>(f0, st + S::kScaleK + (t * 16 + g) * DB * 4);
+        lds_floats<DB>(f1, st + S::kScaleK + (t * 16 + g + 8) * DB * 4);
       }
       const uint32_t ka = st + S::kK + (t * 16 + g) * S::kPitch + c * 4;
 #pragma unroll
@@ -350,12 +425,12 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
         decode_word(lds32(ka + 8 * S::kPitch + i * 16), a1);
         if constexpr (kNv) {
           const uint32_t pick = ((i & 1) * 2 + (c >> 1)) * 0x11u;  // the block's byte, twice
-          const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(w0[i / 2], 0u, pick));
-          const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(w1[i / 2], 0u, pick));
+          const uint32_t e0 = e4m3x2_to_f16x2(__byte_perm(w0[i / 2], 0u, pick));
+          const uint32_t e1 = e4m3x2_to_f16x2(__byte_perm(w1[i / 2], 0u, pick));
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            a0[k] = hmul2(a0[k], f0);
-            a1[k] = hmul2(a1[k], f1);
+            a0[k] = hmul2(a0[k], e0);
+            a1[k] = hmul2(a1[k], e1);
           }
           mma16816(s[t], a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
           mma16816(s[t], a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
@@ -363,22 +438,24 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
           float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           mma16816(d, a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
           mma16816(d, a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
-          const uint32_t p0 = e8m0x2_to_bf16x2(w0[i / 4] >> (16 * (i / 2 % 2)));
-          const uint32_t p1 = e8m0x2_to_bf16x2(w1[i / 4] >> (16 * (i / 2 % 2)));
-          const float f0 = __uint_as_float(i & 1 ? p0 & 0xFFFF0000u : p0 << 16);
-          const float f1 = __uint_as_float(i & 1 ? p1 & 0xFFFF0000u : p1 << 16);
-          s[t][0] = fmaf(d[0], f0, s[t][0]);
-          s[t][1] = fmaf(d[1], f0, s[t][1]);
-          s[t][2] = fmaf(d[2], f1, s[t][2]);
-          s[t][3] = fmaf(d[3], f1, s[t][3]);
+          s[t][0] = fmaf(d[0], f0[i], s[t][0]);
+          s[t][1] = fmaf(d[1], f0[i], s[t][1]);
+          s[t][2] = fmaf(d[2], f1[i], s[t][2]);
+          s[t][3] = fmaf(d[3], f1[i], s[t][3]);
         }
       }
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const bool seen = (valid >> (t * 16 + g + 8 * r)) & 1u;
-        s[t][2 * r] = seen ? s[t][2 * r] * qs0 : -INFINITY;
-        s[t][2 * r + 1] = seen ? s[t][2 * r + 1] * qs1 : -INFINITY;
+        s[t][2 * r] *= qs0;
+        s[t][2 * r + 1] *= qs1;
       }
+    }
+    if (valid != 0xFFFFFFFFu) {  // the last step, or a page that is not there
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (((valid >> (t * 16 + g + 8 * r)) & 1u) == 0u) s[t][2 * r] = s[t][2 * r + 1] = -INFINITY;
     }
 
     // ---- running maximum and sum
@@ -416,58 +493,24 @@ __global__ void __launch_bounds__(kThreads, 2) attention_kernel(const AttentionP
       }
 
     // ---- output
-    uint32_t vw[2][2][S::kWords];  // MXFP4: V's scales of the lane's four positions
-    if constexpr (!kNv) {
-      bool grow = false;
+    uint32_t pt[2][2];  // P^T: columns of heads, pairs of positions
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int i = 0; i < S::kWords; ++i)
-            vw[t][r][i] = lds32(st + S::kScaleV + ((t * 16 + g + 8 * r) * S::kWords + i) * 4);
-      int top[DB];
-#pragma unroll
-      for (int i = 0; i < DB; ++i) {
-        top[i] = vref[i];
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) top[i] = max(top[i], static_cast<int>((vw[t][r][i / 4] >> (8 * (i % 4))) & 0xFFu));
-        grow |= top[i] > vref[i];
-      }
-      if (__any_sync(0xFFFFFFFFu, grow)) {
-#pragma unroll
-        for (int i = 0; i < DB; ++i) {
-          const int now = static_cast<int>(__reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(top[i])));
-          const float f = __uint_as_float(static_cast<uint32_t>(max(127 + vref[i] - now, 0)) << 23);
-          vref[i] = now;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= f;
-        }
-      }
-    }
-    uint32_t pb[2][2];  // P^T: columns of heads, pairs of positions
-    if constexpr (kNv) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) pb[t][r] = movmatrix_trans(pk[t][r]);
-    }
+      for (int r = 0; r < 2; ++r) pt[t][r] = movmatrix_trans(pk[t][r]);
     const uint32_t va = st + S::kV + lane * S::kPitch;
 #pragma unroll
     for (int i = 0; i < DB; ++i) {
-      if constexpr (!kNv) {
-        const int up = 30 - vref[i];
+      uint32_t pb[2][2];
+      if constexpr (kNv) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int byte = static_cast<int>((vw[t][r][i / 4] >> (8 * (i % 4))) & 0xFFu);
-            // 2^(15 + byte - vref) in both halves
-            const uint32_t f = static_cast<uint32_t>(max(byte + up, 0)) * 0x04000400u;
-            pb[t][r] = movmatrix_trans(hmul2(pk[t][r], f));
-          }
+        for (int k = 0; k < 4; ++k) pb[k >> 1][k & 1] = pt[k >> 1][k & 1];
+      } else {
+        const uint4 f = lds128(st + S::kScaleV + i * 64 + c * 16);
+        pb[0][0] = hmul2(pt[0][0], f.x);
+        pb[0][1] = hmul2(pt[0][1], f.y);
+        pb[1][0] = hmul2(pt[1][0], f.z);
+        pb[1][1] = hmul2(pt[1][1], f.w);
       }
       uint32_t v[4];
       ldmatrix4_trans(v, va + i * 16);

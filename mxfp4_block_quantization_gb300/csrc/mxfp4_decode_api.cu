@@ -240,6 +240,9 @@ int attention_checked(const mxfp4::AttentionArgs& a, size_t workspace_bytes, voi
   if (c.head_dim > MXFP4_ATTENTION_MAX_HEAD_DIM || a.max_pages > INT32_MAX / c.page_size ||
       a.table_stride < a.max_pages)
     return MXFP4_ESHAPE;
+  // rows of the cache are counted in uint32
+  if (c.num_heads > 0 && c.num_pages * c.page_size > static_cast<int64_t>(UINT32_MAX) / c.num_heads)
+    return MXFP4_ESHAPE;
   if (a.num_q_heads > 0 && (c.num_heads == 0 || a.num_q_heads % c.num_heads != 0))
     return MXFP4_ESHAPE;
   if (work && (!a.q || !a.out || !a.seq_lens || (a.max_pages > 0 && !a.page_table)))
