@@ -20,11 +20,11 @@
 // The sums keep the heads in the same columns in both, so the softmax's
 // rescaling needs no exchange.
 //
-// A CTA is four warps on one (sequence, kv head, 8 query heads, split of the
-// positions); a warp takes every fourth step of 32 positions with its own
+// A CTA is four warps on one unit (sequence, kv head, 8 query heads); a warp takes every fourth step of 32 positions with its own
 // ring of copies, maximum, sum and output, so the warps meet once, at the
-// end.  Long sequences are split over CTAs whose partial results a second
-// kernel joins.
+// end of a unit.  The steps of all units are one sequence of which every CTA has
+// an even share (as many CTAs as the GPU holds at once), so ragged lengths
+// leave none idle; a unit that spans CTAs is joined by a second kernel.
 //
 // Scales.  K, MXFP4: a power of two of any size, applied in float32 to the
 // 32-element partial scores; NVFP4: e2m1 * e4m3 has at most 6 bits and is
@@ -52,7 +52,7 @@ constexpr int kStep = 32;   // positions of a warp's step
 constexpr int kStages = 3;
 constexpr int kAhead = kStages - 1;
 constexpr int kHeads = 8;   // query heads of a CTA: the columns of the products
-constexpr int kMinSplit = 256;  // positions below which a split does not pay
+constexpr int kMinSteps = 4;  // steps of a CTA, at least: one per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -65,8 +65,9 @@ struct AttentionParams {
   const int32_t* __restrict__ seq_lens;
   uint8_t* __restrict__ out;
   float* __restrict__ lse;
-  float* __restrict__ part_o;   // [sequence, head, split, head_dim]
-  float* __restrict__ part_ml;  // [sequence, head, split, 2]: maximum (log2), sum
+  float* __restrict__ part_o;   // [slot, 8 heads, head_dim]
+  float* __restrict__ part_ml;  // [slot, 8 heads, 2]: maximum (log2), sum
+  int32_t* __restrict__ parts;  // [unit, 2]: first CTA, number of CTAs
   int32_t* __restrict__ status;
   int64_t q_seq_stride;
   int64_t q_head_stride;
@@ -77,7 +78,7 @@ struct AttentionParams {
   int32_t num_kv_heads;
   int32_t group;     // query heads of a kv head
   int32_t chunks;    // CTAs of 8 query heads per kv head
-  int32_t splits;
+  int32_t ctas;      // that share the positions; 0: a CTA per unit
   int32_t num_pages;
   int32_t page_size;
   int32_t head_dim;
@@ -99,9 +100,74 @@ __device__ __forceinline__ bool positions(const AttentionParams& p, int b, int& 
   lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
   return ok;
 }
-// Over how many CTAs a sequence of n positions is split.
-__device__ __forceinline__ int splits_of(const AttentionParams& p, int n) {
-  return max(1, min(p.splits, (n + kMinSplit - 1) / kMinSplit));
+__device__ __forceinline__ int steps_of(const AttentionParams& p, int b) {
+  int lo, hi;
+  positions(p, b, lo, hi);
+  return (hi - lo + kStep - 1) / kStep;
+}
+__device__ __forceinline__ bool one_sequence(const AttentionParams& p) {
+  return p.num_seqs == 1 && p.ctas >= p.num_kv_heads * p.chunks;
+}
+// A single sequence's units are padded to whole shares, so that no CTA has
+// parts of two; with several sequences of any lengths a share may end anywhere.
+__device__ __forceinline__ int64_t padded_steps(const AttentionParams& p, int steps, int64_t share) {
+  return one_sequence(p) ? (steps + share - 1) / share * share : steps;
+}
+// Steps of one CTA, from the steps of all units.
+__device__ __forceinline__ int64_t share_of(const AttentionParams& p, int64_t& total, int units) {
+  if (one_sequence(p)) {
+    const int64_t steps = total / units, per_unit = p.ctas / units;
+    const int64_t share = max((steps + per_unit - 1) / per_unit, static_cast<int64_t>(kMinSteps));
+    total = padded_steps(p, static_cast<int>(steps), share) * units;
+    return share;
+  }
+  return max((total + p.ctas - 1) / p.ctas, static_cast<int64_t>(kMinSteps));
+}
+// The steps of all units, and their prefix sums by thread.
+__device__ __forceinline__ int64_t scan_steps(const AttentionParams& p, int units, int64_t* prefix) {
+  __shared__ int64_t warp_sum[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.num_seqs + kThreads - 1) / kThreads;
+  int64_t sum = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = threadIdx.x * per + i;
+    if (b < p.num_seqs) sum += static_cast<int64_t>(steps_of(p, b)) * units;
+  }
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, k);
+    if (lane >= k) sum += v;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) sum += warp_sum[w];
+    total += warp_sum[w];
+  }
+  prefix[threadIdx.x] = sum;
+  __syncthreads();
+  return total;
+}
+// The sequence that step `at` belongs to, and its first step.
+__device__ __forceinline__ int find_sequence(const AttentionParams& p, const int64_t* prefix, int units,
+                                             int64_t at, int64_t& first) {
+  first = 0;
+  if (p.num_seqs == 1) return 0;
+  int lo = 0, hi = kThreads - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] > at) hi = mid; else lo = mid + 1;
+  }
+  if (lo > 0) first = prefix[lo - 1];
+  const int per = (p.num_seqs + kThreads - 1) / kThreads;
+  int b = lo * per;
+  for (;; ++b) {
+    const int64_t n = static_cast<int64_t>(steps_of(p, b)) * units;
+    if (at < first + n || b + 1 >= p.num_seqs) return b;
+    first += n;
+  }
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -216,377 +282,409 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
 
-  // CTA -> (sequence, kv head, 8 query heads, split); one more for the status
-  const int per_seq = p.num_kv_heads * p.chunks * p.splits;
-  const int b = blockIdx.x / per_seq;
-  if (b >= p.num_seqs) {
+  if (blockIdx.x == gridDim.x - 1 && p.status != nullptr) {
     write_status(p);
     return;
   }
-  int rest = blockIdx.x - b * per_seq;
-  const int kvh = rest % p.num_kv_heads;
-  rest /= p.num_kv_heads;
-  const int chunk = rest % p.chunks, split = rest / p.chunks;
-  int lo, hi;
-  positions(p, b, lo, hi);
-  const int splits = splits_of(p, hi - lo);
-  if (split >= splits) return;
-  // this CTA's positions: whole steps, as even as they come
-  const int steps = (hi - lo + kStep - 1) / kStep;
-  const int first = lo + static_cast<int>(static_cast<int64_t>(steps) * split / splits) * kStep;
-  const int last = min(hi, lo + static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / splits) * kStep);
-  const int head0 = kvh * p.group + chunk * kHeads;
-  const int heads = min(kHeads, p.group - chunk * kHeads);
-
-  // ---- copies
-  const uint32_t ring = smem_u32(smem) + warp * kStages * S::kBytes;
-  const int32_t* table = p.page_table + b * p.table_stride;
-  int next = first + warp * kStep + lane;  // this lane's position in the step to copy
-  int page_at = next / p.page_size, in_page = next - page_at * p.page_size;
-  const int page_step = kWarps * kStep / p.page_size;
-  const int in_step = kWarps * kStep - page_step * p.page_size;
-  auto load_page = [&]() {
-    const int32_t* entry = table + page_at;
-    return next < last && MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
-  };
-  int next_page = load_page();
-  uint32_t fill = 0, pending = 0;          // stage to fill; stage whose scales are in registers
-  uint32_t sk[S::kWords], sv[S::kWords];
-  bool have = false, grown = false;
-  int vrun[DB];  // MXFP4: the largest scale byte of V stored so far, per block (same in all lanes)
-#pragma unroll
-  for (int i = 0; i < DB; ++i) vrun[i] = 0;
-  // a lane has the scales of its position: what all lanes need of them, once
-  auto store_scales = [&]() {
-    if (!have) return;
-    const uint32_t st = ring + pending;
-    if constexpr (kNv) {
-#pragma unroll
-      for (int i = 0; i < S::kWords; ++i) sts32(st + S::kScaleK + (lane * S::kWords + i) * 4, sk[i]);
-#pragma unroll
-      for (int i = 0; i < S::kScale; ++i) sts8(st + S::kScaleV + i * kStep + lane, sv[i / 4] >> (8 * (i % 4)));
-    } else {
-      int byte[DB];
-      bool more = false;
-#pragma unroll
-      for (int i = 0; i < DB; ++i) {
-        const uint32_t pair = e8m0x2_to_bf16x2(sk[i / 4] >> (16 * (i / 2 % 2)));
-        sts32(st + S::kScaleK + (lane * DB + i) * 4, i & 1 ? pair & 0xFFFF0000u : pair << 16);
-        byte[i] = static_cast<int>((sv[i / 4] >> (8 * (i % 4))) & 0xFFu);
-        more |= byte[i] > vrun[i];
-      }
-      if (__any_sync(0xFFFFFFFFu, more)) {
-        grown = true;
-#pragma unroll
-        for (int i = 0; i < DB; ++i)
-          vrun[i] = static_cast<int>(
-              __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(max(byte[i], vrun[i]))));
-      }
-      const uint32_t at = st + S::kScaleV + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
-#pragma unroll
-      for (int i = 0; i < DB; ++i)  // 2^(15 + byte - vrun)
-        sts16(at + i * 64, static_cast<uint32_t>(max(byte[i] + 30 - vrun[i], 0)) << 10);
-    }
-  };
-  auto issue = [&]() {
-    store_scales();
-    have = next - lane < last;
-    if (have) {
-      const bool ok = next_page >= 0 && next_page < p.num_pages;
-      const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
-      const uint32_t row = ok ? (static_cast<uint32_t>(next_page) * p.num_kv_heads + kvh) * p.page_size + in_page : 0u;
-      const uint32_t st = ring + fill;
-#pragma unroll
-      for (int i = 0; i < DB; ++i) {
-        const int piece = i * 32 + lane, at = piece / DB, ch = piece - at * DB;
-        const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, row, at)) * (D / 2) + ch * 16;
-        const int take = (valid >> at) & 1u ? 16 : 0;
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          const uint8_t* src = p.codes[part] + off;
-          cp_async<16>(st + (part ? S::kV : S::kK) + at * S::kPitch + ch * 16, src,
-                       MXFP4_IN_BOUNDS(p, kDbgCodes0 + part, src, take) ? take : 0);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < S::kWords; ++i) sk[i] = sv[i] = 0u;
-      if (ok) {
-        const uint8_t* ks = p.scales[0] + static_cast<uint64_t>(row) * S::kScale;
-        const uint8_t* vs = p.scales[1] + static_cast<uint64_t>(row) * S::kScale;
-        if (MXFP4_IN_BOUNDS(p, kDbgScales0, ks, S::kScale)) load_bytes<S::kScale>(sk, ks);
-        if (MXFP4_IN_BOUNDS(p, kDbgScales1, vs, S::kScale)) load_bytes<S::kScale>(sv, vs);
-      }
-      if (lane == 0) sts32(st + S::kValid, valid);
-      pending = fill;
-      fill = fill == kAhead * S::kBytes ? 0 : fill + S::kBytes;
-      next += kWarps * kStep;
-      page_at += page_step;
-      in_page += in_step;
-      if (in_page >= p.page_size) {
-        in_page -= p.page_size;
-        ++page_at;
-      }
-      next_page = load_page();
-    }
-    cp_commit();  // an empty group at the end keeps the count of groups
-  };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) issue();
-
-  // ---- q: a lane holds elements 8c..8c+7 of each 32-element block of head g,
-  // as halves; BF16 scaled by the head's power of two (see matvec.cu)
-  uint4 q[DB];
-  float qs0, qs1;  // what undoes it, with the softmax's scale, for heads 2c and 2c + 1
-  {
-    const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.q) + b * p.q_seq_stride +
-                         static_cast<int64_t>(head0 + g) * p.q_head_stride + c * 8;
-    uint32_t m = 0u;
-#pragma unroll
-    for (int i = 0; i < DB; ++i) {
-      q[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (g < heads && MXFP4_IN_BOUNDS(p, kDbgQ, qp + i * 32, 16))
-        q[i] = __ldg(reinterpret_cast<const uint4*>(qp + i * 32));
-      m = max_finite_bf16x2(max_finite_bf16x2(m, q[i].x), q[i].y);
-      m = max_finite_bf16x2(max_finite_bf16x2(m, q[i].z), q[i].w);
-    }
-    float inverse = 1.0f;
-    if (!p.f16) {
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-      const float f = half_scale(m, inverse);
-      auto scaled = [&](uint32_t v) {
-        return pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
-      };
-#pragma unroll
-      for (int i = 0; i < DB; ++i)
-        q[i] = make_uint4(scaled(q[i].x), scaled(q[i].y), scaled(q[i].z), scaled(q[i].w));
-    }
-    const float more = p.softmax_scale * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
-    qs0 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c);
-    qs1 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4);
-    qs0 *= more;
-    qs1 *= more;
+  // A unit of work is the positions of one sequence for one kv head and 8 of
+  // its query heads, in steps of 32.
+  const int units_per_seq = p.num_kv_heads * p.chunks;
+  __shared__ int64_t prefix[kThreads];  // steps up to and with each thread's sequences
+  int64_t at = 0, end = 1, share = 1;   // this CTA's steps, over all units
+  if (p.ctas > 0) {
+    int64_t total = scan_steps(p, units_per_seq, prefix);
+    share = share_of(p, total, units_per_seq);
+    at = share * blockIdx.x;
+    end = min(total, at + share);
   }
-
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // of heads 2c and 2c + 1, log2
-  float o[DB][2][4];
-#pragma unroll
-  for (int i = 0; i < DB; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] = 0.0f;
-  int vref[DB];  // MXFP4: what the output is relative to: vrun when its scales were stored
-#pragma unroll
-  for (int i = 0; i < DB; ++i) vref[i] = 0;
-
-  uint32_t read = 0;
-  for (int t0 = first + warp * kStep; t0 < last; t0 += kWarps * kStep) {
-    cp_wait<kAhead - 1>();
-    __syncwarp();  // all lanes' copies and scales are in; the stage read last is free
-    if constexpr (!kNv) {
-      if (grown) {  // by this step's scales, which are the last that were stored
-        grown = false;
-#pragma unroll
-        for (int i = 0; i < DB; ++i) {
-          const float f = __uint_as_float(static_cast<uint32_t>(max(127 + vref[i] - vrun[i], 0)) << 23);
-          vref[i] = vrun[i];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= f;
-        }
-      }
+  while (at < end) {
+    // the unit that step `at` is in, and this CTA's part of its steps
+    int b, unit, s0 = 0, s1;
+    int64_t unit_at = 0;
+    if (p.ctas > 0) {
+      b = find_sequence(p, prefix, units_per_seq, at, unit_at);
+      const int64_t padded = padded_steps(p, steps_of(p, b), share);
+      unit = static_cast<int>((at - unit_at) / padded);
+      unit_at += unit * padded;
+      s0 = static_cast<int>(at - unit_at);
+      s1 = static_cast<int>(min(padded, s0 + (end - at)));
+      at += s1 - s0;
+    } else {
+      b = blockIdx.x / units_per_seq;
+      unit = blockIdx.x - b * units_per_seq;
+      s1 = steps_of(p, b);
+      at = end;
     }
-    issue();
-    const uint32_t st = ring + read;
-    read = read == kAhead * S::kBytes ? 0 : read + S::kBytes;
-    const uint32_t valid = lds32(st + S::kValid);
+    const int kvh = unit % p.num_kv_heads, chunk = unit / p.num_kv_heads;
+    int lo, hi;
+    positions(p, b, lo, hi);
+    const int first = lo + s0 * kStep, last = min(hi, lo + s1 * kStep);
+    const int head0 = kvh * p.group + chunk * kHeads;
+    const int heads = min(kHeads, p.group - chunk * kHeads);
+    // the CTAs that have a part of this unit
+    const int64_t unit_index = static_cast<int64_t>(b) * units_per_seq + unit;
+    const int steps = steps_of(p, b);
+    const int first_cta = p.ctas > 0 ? static_cast<int>(unit_at / share) : 0;
+    const int n_ctas = p.ctas > 0 ? static_cast<int>((unit_at + steps - 1) / share) - first_cta + 1 : 1;
+    if (p.ctas > 0 && s0 == 0 && threadIdx.x == 0 && MXFP4_IN_BOUNDS(p, kDbgPart, p.parts + 2 * unit_index, 8)) {
+      p.parts[2 * unit_index] = first_cta;
+      p.parts[2 * unit_index + 1] = n_ctas;
+    }
+    if (s0 >= steps && p.ctas > 0) continue;  // padding
 
-    // ---- scores of 2 x 16 positions by 8 heads
-    float s[2][4];
+    // ---- copies
+    const uint32_t ring = smem_u32(smem) + warp * kStages * S::kBytes;
+    const int32_t* table = p.page_table + b * p.table_stride;
+    int next = first + warp * kStep + lane;  // this lane's position in the step to copy
+    int page_at = next / p.page_size, in_page = next - page_at * p.page_size;
+    const int page_step = kWarps * kStep / p.page_size;
+    const int in_step = kWarps * kStep - page_step * p.page_size;
+    auto load_page = [&]() {
+      const int32_t* entry = table + page_at;
+      return next < last && MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
+    };
+    int next_page = load_page();
+    uint32_t fill = 0, pending = 0;          // stage to fill; stage whose scales are in registers
+    uint32_t sk[S::kWords], sv[S::kWords];
+    bool have = false, grown = false;
+    int vrun[DB];  // MXFP4: the largest scale byte of V stored so far, per block (same in all lanes)
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
-      uint32_t w0[S::kWords], w1[S::kWords];  // scales of positions g and g + 8
-      float f0[DB], f1[DB];
+    for (int i = 0; i < DB; ++i) vrun[i] = 0;
+    // a lane has the scales of its position: what all lanes need of them, once
+    auto store_scales = [&]() {
+      if (!have) return;
+      const uint32_t st = ring + pending;
       if constexpr (kNv) {
 #pragma unroll
-        for (int i = 0; i < S::kWords; ++i) {
-          w0[i] = lds32(st + S::kScaleK + ((t * 16 + g) * S::kWords + i) * 4);
-          w1[i] = lds32(st + S::kScaleK + ((t * 16 + g + 8) * S::kWords + i) * 4);
-        }
+        for (int i = 0; i < S::kWords; ++i) sts32(st + S::kScaleK + (lane * S::kWords + i) * 4, sk[i]);
+#pragma unroll
+        for (int i = 0; i < S::kScale; ++i) sts8(st + S::kScaleV + i * kStep + lane, sv[i / 4] >> (8 * (i % 4)));
       } else {
-        lds_floats<DB>(f0, st + S::kScaleK + (t * 16 + g) * DB * 4);
-        lds_floats<DB>(f1, st + S::kScaleK + (t * 16 + g + 8) * DB * 4);
+        int byte[DB];
+        bool more = false;
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          const uint32_t pair = e8m0x2_to_bf16x2(sk[i / 4] >> (16 * (i / 2 % 2)));
+          sts32(st + S::kScaleK + (lane * DB + i) * 4, i & 1 ? pair & 0xFFFF0000u : pair << 16);
+          byte[i] = static_cast<int>((sv[i / 4] >> (8 * (i % 4))) & 0xFFu);
+          more |= byte[i] > vrun[i];
+        }
+        if (__any_sync(0xFFFFFFFFu, more)) {
+          grown = true;
+#pragma unroll
+          for (int i = 0; i < DB; ++i)
+            vrun[i] = static_cast<int>(
+                __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(max(byte[i], vrun[i]))));
+        }
+        const uint32_t at = st + S::kScaleV + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)  // 2^(15 + byte - vrun)
+          sts16(at + i * 64, static_cast<uint32_t>(max(byte[i] + 30 - vrun[i], 0)) << 10);
       }
-      const uint32_t ka = st + S::kK + (t * 16 + g) * S::kPitch + c * 4;
+    };
+    auto issue = [&]() {
+      store_scales();
+      have = next - lane < last;
+      if (have) {
+        const bool ok = next_page >= 0 && next_page < p.num_pages;
+        const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
+        const uint32_t row = ok ? (static_cast<uint32_t>(next_page) * p.num_kv_heads + kvh) * p.page_size + in_page : 0u;
+        const uint32_t st = ring + fill;
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          const int piece = i * 32 + lane, at = piece / DB, ch = piece - at * DB;
+          const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, row, at)) * (D / 2) + ch * 16;
+          const int take = (valid >> at) & 1u ? 16 : 0;
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint8_t* src = p.codes[part] + off;
+            cp_async<16>(st + (part ? S::kV : S::kK) + at * S::kPitch + ch * 16, src,
+                         MXFP4_IN_BOUNDS(p, kDbgCodes0 + part, src, take) ? take : 0);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < S::kWords; ++i) sk[i] = sv[i] = 0u;
+        if (ok) {
+          const uint8_t* ks = p.scales[0] + static_cast<uint64_t>(row) * S::kScale;
+          const uint8_t* vs = p.scales[1] + static_cast<uint64_t>(row) * S::kScale;
+          if (MXFP4_IN_BOUNDS(p, kDbgScales0, ks, S::kScale)) load_bytes<S::kScale>(sk, ks);
+          if (MXFP4_IN_BOUNDS(p, kDbgScales1, vs, S::kScale)) load_bytes<S::kScale>(sv, vs);
+        }
+        if (lane == 0) sts32(st + S::kValid, valid);
+        pending = fill;
+        fill = fill == kAhead * S::kBytes ? 0 : fill + S::kBytes;
+        next += kWarps * kStep;
+        page_at += page_step;
+        in_page += in_step;
+        if (in_page >= p.page_size) {
+          in_page -= p.page_size;
+          ++page_at;
+        }
+        next_page = load_page();
+      }
+      cp_commit();  // an empty group at the end keeps the count of groups
+    };
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) issue();
+
+    // ---- q: a lane holds elements 8c..8c+7 of each 32-element block of head g,
+    // as halves; BF16 scaled by the head's power of two (see matvec.cu)
+    uint4 q[DB];
+    float qs0, qs1;  // what undoes it, with the softmax's scale, for heads 2c and 2c + 1
+    {
+      const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.q) + b * p.q_seq_stride +
+                           static_cast<int64_t>(head0 + g) * p.q_head_stride + c * 8;
+      uint32_t m = 0u;
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        uint32_t a0[4], a1[4];
-        decode_word(lds32(ka + i * 16), a0);
-        decode_word(lds32(ka + 8 * S::kPitch + i * 16), a1);
-        if constexpr (kNv) {
-          const uint32_t pick = ((i & 1) * 2 + (c >> 1)) * 0x11u;  // the block's byte, twice
-          const uint32_t e0 = e4m3x2_to_f16x2(__byte_perm(w0[i / 2], 0u, pick));
-          const uint32_t e1 = e4m3x2_to_f16x2(__byte_perm(w1[i / 2], 0u, pick));
+        q[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (g < heads && MXFP4_IN_BOUNDS(p, kDbgQ, qp + i * 32, 16))
+          q[i] = __ldg(reinterpret_cast<const uint4*>(qp + i * 32));
+        m = max_finite_bf16x2(max_finite_bf16x2(m, q[i].x), q[i].y);
+        m = max_finite_bf16x2(max_finite_bf16x2(m, q[i].z), q[i].w);
+      }
+      float inverse = 1.0f;
+      if (!p.f16) {
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+        const float f = half_scale(m, inverse);
+        auto scaled = [&](uint32_t v) {
+          return pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
+        };
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            a0[k] = hmul2(a0[k], e0);
-            a1[k] = hmul2(a1[k], e1);
+        for (int i = 0; i < DB; ++i)
+          q[i] = make_uint4(scaled(q[i].x), scaled(q[i].y), scaled(q[i].z), scaled(q[i].w));
+      }
+      const float more = p.softmax_scale * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
+      qs0 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c);
+      qs1 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4);
+      qs0 *= more;
+      qs1 *= more;
+    }
+
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // of heads 2c and 2c + 1, log2
+    float o[DB][2][4];
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] = 0.0f;
+    int vref[DB];  // MXFP4: what the output is relative to: vrun when its scales were stored
+#pragma unroll
+    for (int i = 0; i < DB; ++i) vref[i] = 0;
+
+    uint32_t read = 0;
+    for (int t0 = first + warp * kStep; t0 < last; t0 += kWarps * kStep) {
+      cp_wait<kAhead - 1>();
+      __syncwarp();  // all lanes' copies and scales are in; the stage read last is free
+      if constexpr (!kNv) {
+        if (grown) {  // by this step's scales, which are the last that were stored
+          grown = false;
+#pragma unroll
+          for (int i = 0; i < DB; ++i) {
+            const float f = __uint_as_float(static_cast<uint32_t>(max(127 + vref[i] - vrun[i], 0)) << 23);
+            vref[i] = vrun[i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= f;
           }
-          mma16816(s[t], a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
-          mma16816(s[t], a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
-        } else {
-          float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          mma16816(d, a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
-          mma16816(d, a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
-          s[t][0] = fmaf(d[0], f0[i], s[t][0]);
-          s[t][1] = fmaf(d[1], f0[i], s[t][1]);
-          s[t][2] = fmaf(d[2], f1[i], s[t][2]);
-          s[t][3] = fmaf(d[3], f1[i], s[t][3]);
         }
       }
+      issue();
+      const uint32_t st = ring + read;
+      read = read == kAhead * S::kBytes ? 0 : read + S::kBytes;
+      const uint32_t valid = lds32(st + S::kValid);
+
+      // ---- scores of 2 x 16 positions by 8 heads
+      float s[2][4];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        s[t][2 * r] *= qs0;
-        s[t][2 * r + 1] *= qs1;
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
+        uint32_t w0[S::kWords], w1[S::kWords];  // scales of positions g and g + 8
+        float f0[DB], f1[DB];
+        if constexpr (kNv) {
+#pragma unroll
+          for (int i = 0; i < S::kWords; ++i) {
+            w0[i] = lds32(st + S::kScaleK + ((t * 16 + g) * S::kWords + i) * 4);
+            w1[i] = lds32(st + S::kScaleK + ((t * 16 + g + 8) * S::kWords + i) * 4);
+          }
+        } else {
+          lds_floats<DB>(f0, st + S::kScaleK + (t * 16 + g) * DB * 4);
+          lds_floats<DB>(f1, st + S::kScaleK + (t * 16 + g + 8) * DB * 4);
+        }
+        const uint32_t ka = st + S::kK + (t * 16 + g) * S::kPitch + c * 4;
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          uint32_t a0[4], a1[4];
+          decode_word(lds32(ka + i * 16), a0);
+          decode_word(lds32(ka + 8 * S::kPitch + i * 16), a1);
+          if constexpr (kNv) {
+            const uint32_t pick = ((i & 1) * 2 + (c >> 1)) * 0x11u;  // the block's byte, twice
+            const uint32_t e0 = e4m3x2_to_f16x2(__byte_perm(w0[i / 2], 0u, pick));
+            const uint32_t e1 = e4m3x2_to_f16x2(__byte_perm(w1[i / 2], 0u, pick));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              a0[k] = hmul2(a0[k], e0);
+              a1[k] = hmul2(a1[k], e1);
+            }
+            mma16816(s[t], a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
+            mma16816(s[t], a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
+          } else {
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            mma16816(d, a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
+            mma16816(d, a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
+            s[t][0] = fmaf(d[0], f0[i], s[t][0]);
+            s[t][1] = fmaf(d[1], f0[i], s[t][1]);
+            s[t][2] = fmaf(d[2], f1[i], s[t][2]);
+            s[t][3] = fmaf(d[3], f1[i], s[t][3]);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          s[t][2 * r] *= qs0;
+          s[t][2 * r + 1] *= qs1;
+        }
       }
-    }
-    if (valid != 0xFFFFFFFFu) {  // the last step, or a page that is not there
+      if (valid != 0xFFFFFFFFu) {  // the last step, or a page that is not there
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            if (((valid >> (t * 16 + g + 8 * r)) & 1u) == 0u) s[t][2 * r] = s[t][2 * r + 1] = -INFINITY;
+      }
+
+      // ---- running maximum and sum
+      float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+      float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+      if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
+#pragma unroll
+        for (int k = 4; k < 32; k *= 2) {
+          x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, k));
+          x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, k));
+        }
+        x0 = fmaxf(x0, m0);
+        x1 = fmaxf(x1, m1);
+        const float k0 = exp2_approx(m0 - (x0 == -INFINITY ? 0.0f : x0));
+        const float k1 = exp2_approx(m1 - (x1 == -INFINITY ? 0.0f : x1));
+        m0 = x0;
+        m1 = x1;
+        l0 *= k0;
+        l1 *= k1;
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= j & 1 ? k1 : k0;
+      }
+      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
+      uint32_t pk[2][2];  // P of positions g and g + 8 of each half, heads 2c and 2c + 1
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          if (((valid >> (t * 16 + g + 8 * r)) & 1u) == 0u) s[t][2 * r] = s[t][2 * r + 1] = -INFINITY;
-    }
+        for (int r = 0; r < 2; ++r) {
+          const float e0 = exp2_approx(s[t][2 * r] - z0), e1 = exp2_approx(s[t][2 * r + 1] - z1);
+          l0 += e0;
+          l1 += e1;
+          pk[t][r] = pack_f16x2(e0, e1);
+        }
 
-    // ---- running maximum and sum
-    float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
-    float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-    if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
+      // ---- output
+      uint32_t pt[2][2];  // P^T: columns of heads, pairs of positions
 #pragma unroll
-      for (int k = 4; k < 32; k *= 2) {
-        x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, k));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, k));
-      }
-      x0 = fmaxf(x0, m0);
-      x1 = fmaxf(x1, m1);
-      const float k0 = exp2_approx(m0 - (x0 == -INFINITY ? 0.0f : x0));
-      const float k1 = exp2_approx(m1 - (x1 == -INFINITY ? 0.0f : x1));
-      m0 = x0;
-      m1 = x1;
-      l0 *= k0;
-      l1 *= k1;
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < DB; ++i)
+        for (int r = 0; r < 2; ++r) pt[t][r] = movmatrix_trans(pk[t][r]);
+      const uint32_t va = st + S::kV + lane * S::kPitch;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= j & 1 ? k1 : k0;
-    }
-    const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
-    uint32_t pk[2][2];  // P of positions g and g + 8 of each half, heads 2c and 2c + 1
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float e0 = exp2_approx(s[t][2 * r] - z0), e1 = exp2_approx(s[t][2 * r + 1] - z1);
-        l0 += e0;
-        l1 += e1;
-        pk[t][r] = pack_f16x2(e0, e1);
-      }
-
-    // ---- output
-    uint32_t pt[2][2];  // P^T: columns of heads, pairs of positions
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) pt[t][r] = movmatrix_trans(pk[t][r]);
-    const uint32_t va = st + S::kV + lane * S::kPitch;
-#pragma unroll
-    for (int i = 0; i < DB; ++i) {
-      uint32_t pb[2][2];
-      if constexpr (kNv) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) pb[k >> 1][k & 1] = pt[k >> 1][k & 1];
-      } else {
-        const uint4 f = lds128(st + S::kScaleV + i * 64 + c * 16);
-        pb[0][0] = hmul2(pt[0][0], f.x);
-        pb[0][1] = hmul2(pt[0][1], f.y);
-        pb[1][0] = hmul2(pt[1][0], f.z);
-        pb[1][1] = hmul2(pt[1][1], f.w);
-      }
-      uint32_t v[4];
-      ldmatrix4_trans(v, va + i * 16);
-      uint32_t h[4][4];  // [8 positions][code]: that code of positions 2c and 2c + 1
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t e[4];
-        decode_word(v[k], e);  // codes 0, 1 | 2, 3 of position 2c, then of 2c + 1
-        h[k][0] = __byte_perm(e[0], e[2], 0x5410);
-        h[k][1] = __byte_perm(e[0], e[2], 0x7632);
-        h[k][2] = __byte_perm(e[1], e[3], 0x5410);
-        h[k][3] = __byte_perm(e[1], e[3], 0x7632);
+      for (int i = 0; i < DB; ++i) {
+        uint32_t pb[2][2];
         if constexpr (kNv) {
-          const uint32_t f =
-              e4m3x2_to_f16x2(lds16(st + S::kScaleV + (2 * i + (g >> 2)) * kStep + 8 * k + 2 * c));
 #pragma unroll
-          for (int n = 0; n < 4; ++n) h[k][n] = hmul2(h[k][n], f);
+          for (int k = 0; k < 4; ++k) pb[k >> 1][k & 1] = pt[k >> 1][k & 1];
+        } else {
+          const uint4 f = lds128(st + S::kScaleV + i * 64 + c * 16);
+          pb[0][0] = hmul2(pt[0][0], f.x);
+          pb[0][1] = hmul2(pt[0][1], f.y);
+          pb[1][0] = hmul2(pt[1][0], f.z);
+          pb[1][1] = hmul2(pt[1][1], f.w);
+        }
+        uint32_t v[4];
+        ldmatrix4_trans(v, va + i * 16);
+        uint32_t h[4][4];  // [8 positions][code]: that code of positions 2c and 2c + 1
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t e[4];
+          decode_word(v[k], e);  // codes 0, 1 | 2, 3 of position 2c, then of 2c + 1
+          h[k][0] = __byte_perm(e[0], e[2], 0x5410);
+          h[k][1] = __byte_perm(e[0], e[2], 0x7632);
+          h[k][2] = __byte_perm(e[1], e[3], 0x5410);
+          h[k][3] = __byte_perm(e[1], e[3], 0x7632);
+          if constexpr (kNv) {
+            const uint32_t f =
+                e4m3x2_to_f16x2(lds16(st + S::kScaleV + (2 * i + (g >> 2)) * kStep + 8 * k + 2 * c));
+#pragma unroll
+            for (int n = 0; n < 4; ++n) h[k][n] = hmul2(h[k][n], f);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          mma16816(o[i][0], h[2 * t][0], h[2 * t][1], h[2 * t + 1][0], h[2 * t + 1][1], pb[t][0], pb[t][1]);
+          mma16816(o[i][1], h[2 * t][2], h[2 * t][3], h[2 * t + 1][2], h[2 * t + 1][3], pb[t][0], pb[t][1]);
         }
       }
+    }
+    cp_wait<0>();
+
+    // ---- the four warps' results
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        mma16816(o[i][0], h[2 * t][0], h[2 * t][1], h[2 * t + 1][0], h[2 * t + 1][1], pb[t][0], pb[t][1]);
-        mma16816(o[i][1], h[2 * t][2], h[2 * t][3], h[2 * t + 1][2], h[2 * t + 1][3], pb[t][0], pb[t][1]);
+    for (int k = 4; k < 32; k *= 2) {
+      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, k);
+      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, k);
+    }
+    __syncthreads();  // the rings are free
+    float* const so = reinterpret_cast<float*>(smem);             // [warp][head][D]
+    float* const sm = so + kWarps * kHeads * D;                   // [warp][head][2]
+#pragma unroll
+    for (int i = 0; i < DB; ++i) {
+      // MXFP4: 2^(vref - 127 - 15); a block that met the NaN scale is NaN
+      float f = 1.0f;
+      if constexpr (!kNv)
+        f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-15f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        so[(warp * kHeads + 2 * c + (j & 1)) * D + i * 32 + 4 * g + 2 * (j >> 2) + ((j >> 1) & 1)] =
+            o[i][j >> 2][j & 3] * f;
+    }
+    if (g == 0) {
+      float* q2 = sm + (warp * kHeads + 2 * c) * 2;
+      q2[0] = m0;
+      q2[1] = l0;
+      q2[2] = m1;
+      q2[3] = l1;
+    }
+    __syncthreads();
+    const int64_t head_at = static_cast<int64_t>(b) * p.num_q_heads + head0;
+    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
+      const int h = i / D, d = i - h * D;
+      float top = -INFINITY, sum = 0.0f, acc = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[(w * kHeads + h) * 2]);
+      const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_approx(sm[(w * kHeads + h) * 2] - z);
+        sum += sm[(w * kHeads + h) * 2 + 1] * f;
+        acc += so[(w * kHeads + h) * D + d] * f;
+      }
+      if (n_ctas > 1) {
+        // slot unit + CTA: the CTAs' shares are consecutive, so no two parts have the same
+        const int64_t slot = (unit_index + blockIdx.x) * kHeads + h;
+        if (MXFP4_IN_BOUNDS(p, kDbgPart, p.part_o + slot * D + d, 4)) p.part_o[slot * D + d] = acc;
+        if (d < 2 && MXFP4_IN_BOUNDS(p, kDbgPart, p.part_ml + slot * 2 + d, 4))
+          p.part_ml[slot * 2 + d] = d == 0 ? top : sum;
+      } else {
+        store_out<kNv>(p, head_at + h, d, D, acc, sum, top);
       }
     }
-  }
-  cp_wait<0>();
-
-  // ---- the four warps' results
-#pragma unroll
-  for (int k = 4; k < 32; k *= 2) {
-    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, k);
-    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, k);
-  }
-  __syncthreads();  // the rings are free
-  float* const so = reinterpret_cast<float*>(smem);             // [warp][head][D]
-  float* const sm = so + kWarps * kHeads * D;                   // [warp][head][2]
-#pragma unroll
-  for (int i = 0; i < DB; ++i) {
-    // MXFP4: 2^(vref - 127 - 15); a block that met the NaN scale is NaN
-    float f = 1.0f;
-    if constexpr (!kNv)
-      f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-15f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      so[(warp * kHeads + 2 * c + (j & 1)) * D + i * 32 + 4 * g + 2 * (j >> 2) + ((j >> 1) & 1)] =
-          o[i][j >> 2][j & 3] * f;
-  }
-  if (g == 0) {
-    float* q2 = sm + (warp * kHeads + 2 * c) * 2;
-    q2[0] = m0;
-    q2[1] = l0;
-    q2[2] = m1;
-    q2[3] = l1;
-  }
-  __syncthreads();
-  const int64_t head_at = static_cast<int64_t>(b) * p.num_q_heads + head0;
-  for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-    const int h = i / D, d = i - h * D;
-    float top = -INFINITY, sum = 0.0f, acc = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[(w * kHeads + h) * 2]);
-    const float z = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2_approx(sm[(w * kHeads + h) * 2] - z);
-      sum += sm[(w * kHeads + h) * 2 + 1] * f;
-      acc += so[(w * kHeads + h) * D + d] * f;
-    }
-    if (splits > 1) {
-      const int64_t at = (head_at + h) * p.splits + split;
-      if (MXFP4_IN_BOUNDS(p, kDbgPart, p.part_o + at * D + d, 4)) p.part_o[at * D + d] = acc;
-      if (d < 2 && MXFP4_IN_BOUNDS(p, kDbgPart, p.part_ml + at * 2 + d, 4)) p.part_ml[at * 2 + d] = d == 0 ? top : sum;
-    } else {
-      store_out<kNv>(p, head_at + h, d, D, acc, sum, top);
-    }
+    __syncthreads();  // the next unit's copies take the same memory
   }
 }
 
@@ -596,7 +694,8 @@ __global__ void __launch_bounds__(kThreads) attention_status_kernel(const Attent
   write_status(p);
 }
 
-// Joins the splits of each head: a warp per (sequence, head).
+// Joins the parts of each head, and writes what an empty sequence gives: a
+// warp per (sequence, head).
 template <bool kNv>
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttentionParams p) {
   pdl_wait();
@@ -604,27 +703,30 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const Attentio
   const int64_t head = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (head >= static_cast<int64_t>(p.num_seqs) * p.num_q_heads) return;
-  int lo, hi;
-  positions(p, static_cast<int>(head / p.num_q_heads), lo, hi);
-  const int splits = splits_of(p, hi - lo);
-  if (splits == 1) return;  // written by the CTA itself
-  const float* ml = p.part_ml + head * p.splits * 2;
-  const float* po = p.part_o + head * p.splits * p.head_dim;
-  float top = -INFINITY;
-  for (int s = lane; s < splits; s += 32) top = fmaxf(top, ml[2 * s]);
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-  const float z = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f, acc[8];
+  const int b = static_cast<int>(head / p.num_q_heads), h = static_cast<int>(head - static_cast<int64_t>(b) * p.num_q_heads);
+  const int kvh = h / p.group, in_group = h - kvh * p.group;
+  const int64_t unit = (static_cast<int64_t>(b) * p.chunks + in_group / kHeads) * p.num_kv_heads + kvh;
+  float top = -INFINITY, sum = 0.0f, acc[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float f = exp2_approx(ml[2 * s] - z);
-    sum += ml[2 * s + 1] * f;
+  if (steps_of(p, b) > 0) {
+    const int first = p.parts[2 * unit], n = p.parts[2 * unit + 1];
+    if (n == 1) return;  // written by the CTA itself
+    const int64_t slot = (unit + first) * kHeads + in_group % kHeads;
+    const float* ml = p.part_ml + slot * 2;
+    const float* po = p.part_o + slot * p.head_dim;
+    for (int s = lane; s < n; s += 32) top = fmaxf(top, ml[s * kHeads * 2]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i * 32 < p.head_dim) acc[i] += po[static_cast<int64_t>(s) * p.head_dim + i * 32 + lane] * f;
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+    const float z = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float f = exp2_approx(ml[s * kHeads * 2] - z);
+      sum += ml[s * kHeads * 2 + 1] * f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i * 32 < p.head_dim) acc[i] += po[static_cast<int64_t>(s) * kHeads * p.head_dim + i * 32 + lane] * f;
+    }
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
@@ -656,22 +758,20 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
     case 7: e = launch_dim<kNv, 7>(p, grid, stream); break;
     default: e = launch_dim<kNv, 8>(p, grid, stream); break;
   }
-  if (e != cudaSuccess || p.splits == 1) return e;
+  if (e != cudaSuccess || p.ctas == 0) return e;
   const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
   return launch_pdl(attention_join_kernel<kNv>, static_cast<unsigned>((heads + kWarps - 1) / kWarps), kThreads,
                     0, stream, p);
 }
 
-// CTAs that the positions of a sequence are split over, at most: enough for
-// every SM to have some, in pieces of at least kMinSplit positions.
-int max_splits(int64_t num_seqs, int32_t num_kv_heads, int32_t chunks, int64_t max_len) {
-  constexpr int kResident = 152 * 3;  // CTAs that the GPU holds at once, about
-  const int64_t base = num_seqs * num_kv_heads * chunks;
-  if (base <= 0) return 1;
-  const int64_t want = num_seqs == 1 ? kResident / base : (4 * kResident + base - 1) / base;
-  const int64_t most = (max_len + kMinSplit - 1) / kMinSplit;
-  const int64_t n = want < most ? want : most;
-  return static_cast<int>(n < 1 ? 1 : n);
+// CTAs that share the positions of all sequences: as many as the GPU holds at
+// once, so that all end together; 0 for contexts so short that a CTA takes a
+// unit whole.
+int shared_ctas(int64_t units, int32_t head_dim, int64_t max_len) {
+  if (max_len <= 2 * kMinSteps * kStep) return 0;
+  const int64_t resident = 152 * (head_dim <= 64 ? 4 : head_dim <= 128 ? 3 : 2);
+  const int64_t most = units * ((max_len + kMinSteps * kStep - 1) / (kMinSteps * kStep));
+  return static_cast<int>(most < resident ? most : resident);
 }
 
 int chunks_of(int32_t num_q_heads, int32_t num_kv_heads) {
@@ -683,8 +783,9 @@ int chunks_of(int32_t num_q_heads, int32_t num_kv_heads) {
 int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                    int32_t head_dim, int64_t max_len) {
   if (num_seqs == 0 || num_q_heads == 0 || head_dim == 0) return 0;
-  const int splits = max_splits(num_seqs, num_kv_heads, chunks_of(num_q_heads, num_kv_heads), max_len);
-  return splits > 1 ? num_seqs * num_q_heads * splits * (head_dim + 2) : 0;
+  const int64_t units = num_seqs * num_kv_heads * chunks_of(num_q_heads, num_kv_heads);
+  const int ctas = shared_ctas(units, head_dim, max_len);
+  return ctas > 0 ? (units + ctas) * kHeads * (head_dim + 2) + 2 * units : 0;
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) {
@@ -716,17 +817,16 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   p.f16 = c.f16;
   p.softmax_scale = a.softmax_scale;
   if (a.num_q_heads == 0 || c.head_dim == 0) {  // the status word alone
-    p.num_kv_heads = p.chunks = p.splits = 1;
-    p.head_dim = 32;
     if (a.status == nullptr) return cudaSuccess;
     return launch_pdl(attention_status_kernel, 1, kThreads, 0, stream, p);
   }
   p.group = a.num_q_heads / c.num_heads;
   p.chunks = chunks_of(a.num_q_heads, c.num_heads);
-  const int64_t n_heads = a.num_seqs * a.num_q_heads;
-  p.splits = max_splits(a.num_seqs, c.num_heads, p.chunks, p.max_len);
+  const int64_t units = a.num_seqs * c.num_heads * p.chunks;
+  p.ctas = shared_ctas(units, c.head_dim, a.max_pages * c.page_size);
   p.part_o = a.workspace;
-  p.part_ml = a.workspace + n_heads * p.splits * c.head_dim;
+  p.part_ml = p.part_o + (units + p.ctas) * kHeads * c.head_dim;
+  p.parts = reinterpret_cast<int32_t*>(p.part_ml + (units + p.ctas) * kHeads * 2);
 #ifdef MXFP4_DEBUG_BOUNDS
   const int64_t rows = c.num_pages * c.page_size * c.num_heads;
   debug_range(p.dbg, kDbgQ, a.q, a.num_seqs > 0
@@ -737,10 +837,11 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   }
   debug_range(p.dbg, kDbgTable, a.page_table,
               a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
-  debug_range(p.dbg, kDbgOut, a.out, n_heads * c.head_dim * 2);
-  debug_range(p.dbg, kDbgPart, a.workspace, p.splits > 1 ? n_heads * p.splits * (c.head_dim + 2) * 4 : 0);
+  debug_range(p.dbg, kDbgOut, a.out, a.num_seqs * a.num_q_heads * c.head_dim * 2);
+  debug_range(p.dbg, kDbgPart, a.workspace,
+              p.ctas > 0 ? ((units + p.ctas) * kHeads * (c.head_dim + 2) + 2 * units) * 4 : 0);
 #endif
-  const int64_t grid = a.num_seqs * c.num_heads * p.chunks * p.splits + (a.status ? 1 : 0);
+  const int64_t grid = (p.ctas > 0 ? p.ctas : units) + (a.status ? 1 : 0);
   if (grid == 0) return cudaSuccess;
   return c.nvfp4 ? launch_format<true>(p, static_cast<unsigned>(grid), stream)
                  : launch_format<false>(p, static_cast<unsigned>(grid), stream);
