@@ -529,8 +529,8 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
             mma16816(s[t], a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
             mma16816(s[t], a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
           } else {
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            mma16816(d, a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
+            float d[4];
+            mma16816_first(d, a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
             mma16816(d, a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
             s[t][0] = fmaf(d[0], f0[i], s[t][0]);
             s[t][1] = fmaf(d[1], f0[i], s[t][1]);
@@ -695,14 +695,14 @@ __global__ void __launch_bounds__(kThreads) attention_status_kernel(const Attent
 }
 
 // Joins the parts of each head, and writes what an empty sequence gives: a
-// warp per (sequence, head).
+// CTA per (sequence, head), the parts shared by its warps.
 template <bool kNv>
 __global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttentionParams p) {
+  __shared__ float s_acc[kWarps][256], s_sum[kWarps];
   pdl_wait();
   pdl_release();
-  const int64_t head = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (head >= static_cast<int64_t>(p.num_seqs) * p.num_q_heads) return;
+  const int64_t head = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = static_cast<int>(head / p.num_q_heads), h = static_cast<int>(head - static_cast<int64_t>(b) * p.num_q_heads);
   const int kvh = h / p.group, in_group = h - kvh * p.group;
   const int64_t unit = (static_cast<int64_t>(b) * p.chunks + in_group / kHeads) * p.num_kv_heads + kvh;
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const Attentio
     for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
     const float z = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
-    for (int s = 0; s < n; ++s) {
+    for (int s = warp; s < n; s += kWarps) {
       const float f = exp2_approx(ml[s * kHeads * 2] - z);
       sum += ml[s * kHeads * 2 + 1] * f;
 #pragma unroll
@@ -729,8 +729,18 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const Attentio
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i * 32 < p.head_dim) store_out<kNv>(p, head, i * 32 + lane, p.head_dim, acc[i], sum, top);
+  for (int i = 0; i < 8; ++i) s_acc[warp][i * 32 + lane] = acc[i];
+  if (lane == 0) s_sum[warp] = sum;
+  __syncthreads();
+  for (int d = threadIdx.x; d < p.head_dim; d += kThreads) {
+    float a = 0.0f, l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      a += s_acc[w][d];
+      l += s_sum[w];
+    }
+    store_out<kNv>(p, head, d, p.head_dim, a, l, top);
+  }
 }
 
 template <bool kNv, int DB>
@@ -760,8 +770,7 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
   }
   if (e != cudaSuccess || p.ctas == 0) return e;
   const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
-  return launch_pdl(attention_join_kernel<kNv>, static_cast<unsigned>((heads + kWarps - 1) / kWarps), kThreads,
-                    0, stream, p);
+  return launch_pdl(attention_join_kernel<kNv>, static_cast<unsigned>(heads), kThreads, 0, stream, p);
 }
 
 // CTAs that share the positions of all sequences: as many as the GPU holds at

@@ -498,8 +498,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
               mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
               mma16816(run[t], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
             } else {
-              float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              mma16816(d, a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+              float d[4];
+              mma16816_first(d, a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
               mma16816(d, a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
               float2 xs = make_float2(1.0f, 1.0f);
               if constexpr (!kF16) xs = lds64f(sx + (b * R + t * 8) * 4);
