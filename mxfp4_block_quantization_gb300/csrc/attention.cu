@@ -73,6 +73,7 @@ struct AttentionParams {
   int64_t q_head_stride;
   int64_t table_stride;
   int64_t max_len;
+  uint64_t scale_bytes;  // of keys, and of values
   int32_t num_seqs;
   int32_t num_q_heads;
   int32_t num_kv_heads;
@@ -176,27 +177,6 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// kBytes consecutive bytes as words, by the widest loads their alignment (a
-// multiple of kBytes) allows.
-template <int kBytes>
-__device__ __forceinline__ void load_bytes(uint32_t (&w)[(kBytes + 3) / 4], const uint8_t* p) {
-  if constexpr (kBytes % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < kBytes / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t*>(p) + i);
-  } else {
-#pragma unroll
-    for (int i = 0; i < (kBytes + 3) / 4; ++i) w[i] = 0u;
-    if constexpr (kBytes % 2 == 0) {
-#pragma unroll
-      for (int i = 0; i < kBytes / 2; ++i)
-        w[i / 2] |= static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t*>(p) + i)) << (16 * (i % 2));
-    } else {
-#pragma unroll
-      for (int i = 0; i < kBytes; ++i) w[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
-    }
-  }
-}
-
 // kN consecutive float32 of shared memory, kN * 4-byte aligned.
 template <int kN>
 __device__ __forceinline__ void lds_floats(float (&f)[kN], uint32_t a) {
@@ -256,7 +236,15 @@ struct Stage {
   // pairs); NVFP4: the bytes, [position][words] and [block][position].
   static constexpr int kScaleV = kScaleK + kStep * (kNv ? kWords * 4 : DB * 4);
   static constexpr int kValid = kScaleV + kStep * (kNv ? kWords * 4 : DB * 2);  // a bit per position
-  static constexpr int kBytes = kValid + 16;
+  // As they are copied: the 4-byte words that hold a position's scale bytes, of
+  // K and of V, with the bytes before them in the first (when they can start
+  // inside a word), and the page of the position two steps on.
+  static constexpr int kRaw = kScale % 4 == 0 ? kWords : (kScale + (kScale % 2 == 0 ? 2 : 3) + 3) / 4;
+  static constexpr int kRawK = kValid + 16;
+  static constexpr int kRawV = kRawK + kStep * kRaw * 4;
+  static constexpr int kSkip = kRawV + kStep * kRaw * 4;
+  static constexpr int kPage = kSkip + (kScale % 4 == 0 ? 0 : kStep * 4);
+  static constexpr int kBytes = kPage + kStep * 4;
 };
 
 // One value of the output: acc / sum (zero without positions), NVFP4 with V's
@@ -270,6 +258,25 @@ __device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head
   if (MXFP4_IN_BOUNDS(p, kDbgOut, y, 2))
     *y = p.f16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
   if (d == 0 && p.lse != nullptr) p.lse[head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+}
+
+// The scale bytes of this lane's position, as words that start with the first.
+template <typename S>
+__device__ __forceinline__ void own_scales(uint32_t (&k)[S::kWords], uint32_t (&v)[S::kWords], uint32_t st,
+                                           int lane) {
+  uint32_t a[S::kRaw + 1], b[S::kRaw + 1];
+#pragma unroll
+  for (int i = 0; i < S::kRaw; ++i) {
+    a[i] = lds32(st + S::kRawK + (lane * S::kRaw + i) * 4);
+    b[i] = lds32(st + S::kRawV + (lane * S::kRaw + i) * 4);
+  }
+  a[S::kRaw] = b[S::kRaw] = 0u;
+  const uint32_t skip = S::kScale % 4 == 0 ? 0u : 8u * lds32(st + S::kSkip + lane * 4);
+#pragma unroll
+  for (int i = 0; i < S::kWords; ++i) {
+    k[i] = S::kScale % 4 == 0 ? a[i] : __funnelshift_r(a[i], a[i + 1], skip);
+    v[i] = S::kScale % 4 == 0 ? b[i] : __funnelshift_r(b[i], b[i + 1], skip);
+  }
 }
 
 template <bool kNv, int DB>
@@ -336,96 +343,81 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
     const uint32_t ring = smem_u32(smem) + warp * kStages * S::kBytes;
     const int32_t* table = p.page_table + b * p.table_stride;
     int next = first + warp * kStep + lane;  // this lane's position in the step to copy
-    int page_at = next / p.page_size, in_page = next - page_at * p.page_size;
+    int in_page = next % p.page_size;
     const int page_step = kWarps * kStep / p.page_size;
     const int in_step = kWarps * kStep - page_step * p.page_size;
-    auto load_page = [&]() {
-      const int32_t* entry = table + page_at;
-      return next < last && MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
+    // where the position kAhead steps on has its page
+    int ahead = next + kAhead * kWarps * kStep;
+    int ahead_at = ahead / p.page_size, ahead_in = ahead - ahead_at * p.page_size;
+    auto load_page = [&](int position) {
+      const int32_t* entry = table + position / p.page_size;
+      return position < last && MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
     };
-    int next_page = load_page();
-    uint32_t fill = 0, pending = 0;          // stage to fill; stage whose scales are in registers
-    uint32_t sk[S::kWords], sv[S::kWords];
-    bool have = false, grown = false;
-    int vrun[DB];  // MXFP4: the largest scale byte of V stored so far, per block (same in all lanes)
-#pragma unroll
-    for (int i = 0; i < DB; ++i) vrun[i] = 0;
-    // a lane has the scales of its position: what all lanes need of them, once
-    auto store_scales = [&]() {
-      if (!have) return;
-      const uint32_t st = ring + pending;
-      if constexpr (kNv) {
-#pragma unroll
-        for (int i = 0; i < S::kWords; ++i) sts32(st + S::kScaleK + (lane * S::kWords + i) * 4, sk[i]);
-#pragma unroll
-        for (int i = 0; i < S::kScale; ++i) sts8(st + S::kScaleV + i * kStep + lane, sv[i / 4] >> (8 * (i % 4)));
-      } else {
-        int byte[DB];
-        bool more = false;
-#pragma unroll
-        for (int i = 0; i < DB; ++i) {
-          const uint32_t pair = e8m0x2_to_bf16x2(sk[i / 4] >> (16 * (i / 2 % 2)));
-          sts32(st + S::kScaleK + (lane * DB + i) * 4, i & 1 ? pair & 0xFFFF0000u : pair << 16);
-          byte[i] = static_cast<int>((sv[i / 4] >> (8 * (i % 4))) & 0xFFu);
-          more |= byte[i] > vrun[i];
-        }
-        if (__any_sync(0xFFFFFFFFu, more)) {
-          grown = true;
-#pragma unroll
-          for (int i = 0; i < DB; ++i)
-            vrun[i] = static_cast<int>(
-                __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(max(byte[i], vrun[i]))));
-        }
-        const uint32_t at = st + S::kScaleV + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
-#pragma unroll
-        for (int i = 0; i < DB; ++i)  // 2^(15 + byte - vrun)
-          sts16(at + i * 64, static_cast<uint32_t>(max(byte[i] + 30 - vrun[i], 0)) << 10);
-      }
-    };
-    auto issue = [&]() {
-      store_scales();
-      have = next - lane < last;
-      if (have) {
-        const bool ok = next_page >= 0 && next_page < p.num_pages;
+    uint32_t fill = 0;  // stage to fill
+    auto issue = [&](int page) {
+      if (next - lane < last) {
+        const bool ok = next < last && page >= 0 && page < p.num_pages;
         const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
-        const uint32_t row = ok ? (static_cast<uint32_t>(next_page) * p.num_kv_heads + kvh) * p.page_size + in_page : 0u;
+        const uint32_t row = ok ? (static_cast<uint32_t>(page) * p.num_kv_heads + kvh) * p.page_size + in_page : 0u;
         const uint32_t st = ring + fill;
 #pragma unroll
         for (int i = 0; i < DB; ++i) {
-          const int piece = i * 32 + lane, at = piece / DB, ch = piece - at * DB;
-          const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, row, at)) * (D / 2) + ch * 16;
-          const int take = (valid >> at) & 1u ? 16 : 0;
+          const int piece = i * 32 + lane, to = piece / DB, ch = piece - to * DB;
+          const uint64_t off = static_cast<uint64_t>(__shfl_sync(0xFFFFFFFFu, row, to)) * (D / 2) + ch * 16;
+          const int take = (valid >> to) & 1u ? 16 : 0;
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
             const uint8_t* src = p.codes[part] + off;
-            cp_async<16>(st + (part ? S::kV : S::kK) + at * S::kPitch + ch * 16, src,
+            cp_async<16>(st + (part ? S::kV : S::kK) + to * S::kPitch + ch * 16, src,
                          MXFP4_IN_BOUNDS(p, kDbgCodes0 + part, src, take) ? take : 0);
           }
         }
+        // a position that is not there has zero scales: nothing of V, and its
+        // scores are masked
+        const uint64_t soff = static_cast<uint64_t>(row) * S::kScale;
+        const int skip = S::kScale % 4 == 0 ? 0 : static_cast<int>(soff & 3);
 #pragma unroll
-        for (int i = 0; i < S::kWords; ++i) sk[i] = sv[i] = 0u;
-        if (ok) {
-          const uint8_t* ks = p.scales[0] + static_cast<uint64_t>(row) * S::kScale;
-          const uint8_t* vs = p.scales[1] + static_cast<uint64_t>(row) * S::kScale;
-          if (MXFP4_IN_BOUNDS(p, kDbgScales0, ks, S::kScale)) load_bytes<S::kScale>(sk, ks);
-          if (MXFP4_IN_BOUNDS(p, kDbgScales1, vs, S::kScale)) load_bytes<S::kScale>(sv, vs);
+        for (int i = 0; i < S::kRaw; ++i) {
+          const uint64_t w = soff - skip + 4 * i;
+          const int64_t left = static_cast<int64_t>(p.scale_bytes - w);
+          const int take = !ok || (S::kScale % 4 != 0 && left <= 0) ? 0
+                           : S::kScale % 4 != 0 && left < 4         ? static_cast<int>(left)
+                                                                    : 4;
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const uint8_t* src = p.scales[part] + (take ? w : 0);
+            cp_async4(st + (part ? S::kRawV : S::kRawK) + (lane * S::kRaw + i) * 4, src,
+                      MXFP4_IN_BOUNDS(p, kDbgScales0 + part, src, take) ? take : 0);
+          }
+        }
+        if constexpr (S::kScale % 4 != 0) sts32(st + S::kSkip + lane * 4, skip);
+        {
+          const int32_t* entry = table + (ahead < last ? ahead_at : 0);
+          cp_async4(st + S::kPage + lane * 4, entry,
+                    ahead < last && MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? 4 : 0);
         }
         if (lane == 0) sts32(st + S::kValid, valid);
-        pending = fill;
         fill = fill == kAhead * S::kBytes ? 0 : fill + S::kBytes;
         next += kWarps * kStep;
-        page_at += page_step;
         in_page += in_step;
-        if (in_page >= p.page_size) {
-          in_page -= p.page_size;
-          ++page_at;
+        if (in_page >= p.page_size) in_page -= p.page_size;
+        ahead += kWarps * kStep;
+        ahead_at += page_step;
+        ahead_in += in_step;
+        if (ahead_in >= p.page_size) {
+          ahead_in -= p.page_size;
+          ++ahead_at;
         }
-        next_page = load_page();
       }
       cp_commit();  // an empty group at the end keeps the count of groups
     };
+    {
+      int page[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) issue();
+      for (int i = 0; i < kAhead; ++i) page[i] = load_page(next + i * kWarps * kStep);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) issue(page[i]);
+    }
 
     // ---- q: a lane holds elements 8c..8c+7 of each 32-element block of head g,
     // as halves; BF16 scaled by the head's power of two (see matvec.cu)
@@ -468,29 +460,55 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
     for (int i = 0; i < DB; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] = 0.0f;
-    int vref[DB];  // MXFP4: what the output is relative to: vrun when its scales were stored
+    int vref[DB];  // MXFP4: the largest scale byte of V so far, per block (same in all lanes)
 #pragma unroll
     for (int i = 0; i < DB; ++i) vref[i] = 0;
 
     uint32_t read = 0;
     for (int t0 = first + warp * kStep; t0 < last; t0 += kWarps * kStep) {
       cp_wait<kAhead - 1>();
-      __syncwarp();  // all lanes' copies and scales are in; the stage read last is free
-      if constexpr (!kNv) {
-        if (grown) {  // by this step's scales, which are the last that were stored
-          grown = false;
-#pragma unroll
-          for (int i = 0; i < DB; ++i) {
-            const float f = __uint_as_float(static_cast<uint32_t>(max(127 + vref[i] - vrun[i], 0)) << 23);
-            vref[i] = vrun[i];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= f;
-          }
-        }
-      }
-      issue();
       const uint32_t st = ring + read;
       read = read == kAhead * S::kBytes ? 0 : read + S::kBytes;
+      // a lane has copied its position's scales: what all lanes need of them, once
+      {
+        uint32_t sk[S::kWords], sv[S::kWords];
+        own_scales<S>(sk, sv, st, lane);
+        if constexpr (kNv) {
+#pragma unroll
+          for (int i = 0; i < S::kWords; ++i) sts32(st + S::kScaleK + (lane * S::kWords + i) * 4, sk[i]);
+#pragma unroll
+          for (int i = 0; i < S::kScale; ++i)
+            sts8(st + S::kScaleV + i * kStep + lane, sv[i / 4] >> (8 * (i % 4)));
+        } else {
+          int byte[DB];
+          bool more = false;
+#pragma unroll
+          for (int i = 0; i < DB; ++i) {
+            const uint32_t pair = e8m0x2_to_bf16x2(sk[i / 4] >> (16 * (i / 2 % 2)));
+            sts32(st + S::kScaleK + (lane * DB + i) * 4, i & 1 ? pair & 0xFFFF0000u : pair << 16);
+            byte[i] = static_cast<int>((sv[i / 4] >> (8 * (i % 4))) & 0xFFu);
+            more |= byte[i] > vref[i];
+          }
+          if (__any_sync(0xFFFFFFFFu, more)) {
+#pragma unroll
+            for (int i = 0; i < DB; ++i) {
+              const int now = static_cast<int>(
+                  __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(max(byte[i], vref[i]))));
+              const float f = __uint_as_float(static_cast<uint32_t>(max(127 + vref[i] - now, 0)) << 23);
+              vref[i] = now;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= f;
+            }
+          }
+          const uint32_t to = st + S::kScaleV + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
+#pragma unroll
+          for (int i = 0; i < DB; ++i)  // 2^(15 + byte - vref)
+            sts16(to + i * 64, static_cast<uint32_t>(max(byte[i] + 30 - vref[i], 0)) << 10);
+        }
+      }
+      const int next_page = static_cast<int>(lds32(st + S::kPage + lane * 4));
+      __syncwarp();  // all lanes' copies and scales are in; the stage read last is free
+      issue(next_page);
       const uint32_t valid = lds32(st + S::kValid);
 
       // ---- scores of 2 x 16 positions by 8 heads
@@ -823,6 +841,7 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   p.page_size = c.page_size;
   p.head_dim = c.head_dim;
   p.window = a.window;
+  p.scale_bytes = static_cast<uint64_t>(c.num_pages) * c.page_size * c.num_heads * (c.head_dim / (c.nvfp4 ? 16 : 32));
   p.f16 = c.f16;
   p.softmax_scale = a.softmax_scale;
   if (a.num_q_heads == 0 || c.head_dim == 0) {  // the status word alone

@@ -24,6 +24,9 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
 // The same for whole pieces where `take`, without a branch around it.
 __device__ __forceinline__ void cp_async16_if(uint32_t dst, const void* src, bool take) {
   asm volatile(
