@@ -20,11 +20,10 @@
 // The sums keep the heads in the same columns in both, so the softmax's
 // rescaling needs no exchange.
 //
-// A CTA is four warps on one unit (sequence, kv head, 8 query heads); a warp takes every fourth step of 32 positions with its own
-// ring of copies, maximum, sum and output, so the warps meet once, at the
-// end of a unit.  The steps of all units are one sequence of which every CTA has
-// an even share (as many CTAs as the GPU holds at once), so ragged lengths
-// leave none idle; a unit that spans CTAs is joined by a second kernel.
+// A warp works alone: the steps (32 positions) of all units (a sequence, a kv
+// head, 8 query heads) are one sequence of which every warp that the GPU holds
+// has an even share, whatever the lengths, with its own ring of copies.  A unit
+// that spans warps is joined by a second kernel.
 //
 // Scales.  K, MXFP4: a power of two of any size, applied in float32 to the
 // 32-element partial scores; NVFP4: e2m1 * e4m3 has at most 6 bits and is
@@ -52,7 +51,6 @@ constexpr int kStep = 32;   // positions of a warp's step
 constexpr int kStages = 3;
 constexpr int kAhead = kStages - 1;
 constexpr int kHeads = 8;   // query heads of a CTA: the columns of the products
-constexpr int kMinSteps = 4;  // steps of a CTA, at least: one per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -67,7 +65,7 @@ struct AttentionParams {
   float* __restrict__ lse;
   float* __restrict__ part_o;   // [slot, 8 heads, head_dim]
   float* __restrict__ part_ml;  // [slot, 8 heads, 2]: maximum (log2), sum
-  int32_t* __restrict__ parts;  // [unit, 2]: first CTA, number of CTAs
+  int32_t* __restrict__ parts;  // [unit, 2]: first warp, number of warps
   int32_t* __restrict__ status;
   int64_t q_seq_stride;
   int64_t q_head_stride;
@@ -79,7 +77,7 @@ struct AttentionParams {
   int32_t num_kv_heads;
   int32_t group;     // query heads of a kv head
   int32_t chunks;    // CTAs of 8 query heads per kv head
-  int32_t ctas;      // that share the positions; 0: a CTA per unit
+  int32_t workers;   // warps that share the positions; 0: a warp per unit
   int32_t num_pages;
   int32_t page_size;
   int32_t head_dim;
@@ -107,22 +105,22 @@ __device__ __forceinline__ int steps_of(const AttentionParams& p, int b) {
   return (hi - lo + kStep - 1) / kStep;
 }
 __device__ __forceinline__ bool one_sequence(const AttentionParams& p) {
-  return p.num_seqs == 1 && p.ctas >= p.num_kv_heads * p.chunks;
+  return p.num_seqs == 1 && p.workers >= p.num_kv_heads * p.chunks;
 }
-// A single sequence's units are padded to whole shares, so that no CTA has
+// A single sequence's units are padded to whole shares, so that no warp has
 // parts of two; with several sequences of any lengths a share may end anywhere.
 __device__ __forceinline__ int64_t padded_steps(const AttentionParams& p, int steps, int64_t share) {
   return one_sequence(p) ? (steps + share - 1) / share * share : steps;
 }
-// Steps of one CTA, from the steps of all units.
+// Steps of one warp, from the steps of all units.
 __device__ __forceinline__ int64_t share_of(const AttentionParams& p, int64_t& total, int units) {
   if (one_sequence(p)) {
-    const int64_t steps = total / units, per_unit = p.ctas / units;
-    const int64_t share = max((steps + per_unit - 1) / per_unit, static_cast<int64_t>(kMinSteps));
+    const int64_t steps = total / units, per_unit = p.workers / units;
+    const int64_t share = max((steps + per_unit - 1) / per_unit, static_cast<int64_t>(1));
     total = padded_steps(p, static_cast<int>(steps), share) * units;
     return share;
   }
-  return max((total + p.ctas - 1) / p.ctas, static_cast<int64_t>(kMinSteps));
+  return max((total + p.workers - 1) / p.workers, static_cast<int64_t>(1));
 }
 // The steps of all units, and their prefix sums by thread.
 __device__ __forceinline__ int64_t scan_steps(const AttentionParams& p, int units, int64_t* prefix) {
@@ -247,17 +245,26 @@ struct Stage {
   static constexpr int kBytes = kPage + kStep * 4;
 };
 
-// One value of the output: acc / sum (zero without positions), NVFP4 with V's
-// global scale divided out; and, with the first value, the head's lse.
+// Four values of the output: acc / sum (zero without positions), NVFP4 with
+// V's global scale divided out.
 template <bool kNv>
-__device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head, int d, int D, float acc,
-                                          float sum, float top) {
-  float v = sum == 0.0f ? 0.0f : acc / sum;
-  if constexpr (kNv) v /= __ldg(p.global_scales[1]);
-  uint16_t* y = reinterpret_cast<uint16_t*>(p.out) + head * D + d;
-  if (MXFP4_IN_BOUNDS(p, kDbgOut, y, 2))
-    *y = p.f16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
-  if (d == 0 && p.lse != nullptr) p.lse[head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+__device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head, int d, int D, float4 acc,
+                                          float sum) {
+  const float by = kNv ? sum * __ldg(p.global_scales[1]) : sum;
+  auto one = [&](float v) { return sum == 0.0f ? 0.0f : v / by; };
+  uint2 y;
+  if (p.f16) {
+    y.x = pack_f16x2(one(acc.x), one(acc.y));
+    y.y = pack_f16x2(one(acc.z), one(acc.w));
+  } else {
+    y.x = cvt_bf16x2(one(acc.x), one(acc.y));
+    y.y = cvt_bf16x2(one(acc.z), one(acc.w));
+  }
+  uint8_t* to = p.out + (head * D + d) * 2;
+  if (MXFP4_IN_BOUNDS(p, kDbgOut, to, 8)) *reinterpret_cast<uint2*>(to) = y;
+}
+__device__ __forceinline__ void store_lse(const AttentionParams& p, int64_t head, float sum, float top) {
+  if (p.lse != nullptr) p.lse[head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
 // The scale bytes of this lane's position, as words that start with the first.
@@ -296,29 +303,43 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
   // A unit of work is the positions of one sequence for one kv head and 8 of
   // its query heads, in steps of 32.
   const int units_per_seq = p.num_kv_heads * p.chunks;
+  const int worker = blockIdx.x * kWarps + warp;
   __shared__ int64_t prefix[kThreads];  // steps up to and with each thread's sequences
-  int64_t at = 0, end = 1, share = 1;   // this CTA's steps, over all units
-  if (p.ctas > 0) {
+  int64_t at = 0, end = 0, share = 1;   // this warp's steps, over all units
+  if (p.workers > 0) {
     int64_t total = scan_steps(p, units_per_seq, prefix);
     share = share_of(p, total, units_per_seq);
-    at = share * blockIdx.x;
+    at = share * worker;
     end = min(total, at + share);
+  } else if (worker < static_cast<int64_t>(p.num_seqs) * units_per_seq) {
+    end = 1;
   }
+  const uint32_t ring = smem_u32(smem) + warp * kStages * S::kBytes;
   while (at < end) {
-    // the unit that step `at` is in, and this CTA's part of its steps
-    int b, unit, s0 = 0, s1;
-    int64_t unit_at = 0;
-    if (p.ctas > 0) {
+    // the unit that step `at` is in, and this warp's part of its steps
+    int b, unit, s0 = 0, s1, n_parts = 1;
+    if (p.workers > 0) {
+      int64_t unit_at;
       b = find_sequence(p, prefix, units_per_seq, at, unit_at);
-      const int64_t padded = padded_steps(p, steps_of(p, b), share);
+      const int steps = steps_of(p, b);
+      const int64_t padded = padded_steps(p, steps, share);
       unit = static_cast<int>((at - unit_at) / padded);
       unit_at += unit * padded;
       s0 = static_cast<int>(at - unit_at);
       s1 = static_cast<int>(min(padded, s0 + (end - at)));
       at += s1 - s0;
+      // the warps that have a part of the unit
+      const int first_part = static_cast<int>(unit_at / share);
+      n_parts = static_cast<int>((unit_at + steps - 1) / share) - first_part + 1;
+      int32_t* parts = p.parts + 2 * (static_cast<int64_t>(b) * units_per_seq + unit);
+      if (s0 == 0 && lane == 0 && MXFP4_IN_BOUNDS(p, kDbgPart, parts, 8)) {
+        parts[0] = first_part;
+        parts[1] = n_parts;
+      }
+      if (s0 >= steps) continue;  // padding
     } else {
-      b = blockIdx.x / units_per_seq;
-      unit = blockIdx.x - b * units_per_seq;
+      b = worker / units_per_seq;
+      unit = worker - b * units_per_seq;
       s1 = steps_of(p, b);
       at = end;
     }
@@ -328,26 +349,16 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
     const int first = lo + s0 * kStep, last = min(hi, lo + s1 * kStep);
     const int head0 = kvh * p.group + chunk * kHeads;
     const int heads = min(kHeads, p.group - chunk * kHeads);
-    // the CTAs that have a part of this unit
-    const int64_t unit_index = static_cast<int64_t>(b) * units_per_seq + unit;
-    const int steps = steps_of(p, b);
-    const int first_cta = p.ctas > 0 ? static_cast<int>(unit_at / share) : 0;
-    const int n_ctas = p.ctas > 0 ? static_cast<int>((unit_at + steps - 1) / share) - first_cta + 1 : 1;
-    if (p.ctas > 0 && s0 == 0 && threadIdx.x == 0 && MXFP4_IN_BOUNDS(p, kDbgPart, p.parts + 2 * unit_index, 8)) {
-      p.parts[2 * unit_index] = first_cta;
-      p.parts[2 * unit_index + 1] = n_ctas;
-    }
-    if (s0 >= steps && p.ctas > 0) continue;  // padding
+    __syncwarp();  // the unit before is done with the ring
 
     // ---- copies
-    const uint32_t ring = smem_u32(smem) + warp * kStages * S::kBytes;
     const int32_t* table = p.page_table + b * p.table_stride;
-    int next = first + warp * kStep + lane;  // this lane's position in the step to copy
+    int next = first + lane;  // this lane's position in the step to copy
     int in_page = next % p.page_size;
-    const int page_step = kWarps * kStep / p.page_size;
-    const int in_step = kWarps * kStep - page_step * p.page_size;
+    const int page_step = kStep / p.page_size;
+    const int in_step = kStep - page_step * p.page_size;
     // where the position kAhead steps on has its page
-    int ahead = next + kAhead * kWarps * kStep;
+    int ahead = next + kAhead * kStep;
     int ahead_at = ahead / p.page_size, ahead_in = ahead - ahead_at * p.page_size;
     auto load_page = [&](int position) {
       const int32_t* entry = table + position / p.page_size;
@@ -398,10 +409,10 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
         }
         if (lane == 0) sts32(st + S::kValid, valid);
         fill = fill == kAhead * S::kBytes ? 0 : fill + S::kBytes;
-        next += kWarps * kStep;
+        next += kStep;
         in_page += in_step;
         if (in_page >= p.page_size) in_page -= p.page_size;
-        ahead += kWarps * kStep;
+        ahead += kStep;
         ahead_at += page_step;
         ahead_in += in_step;
         if (ahead_in >= p.page_size) {
@@ -414,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
     {
       int page[kAhead];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) page[i] = load_page(next + i * kWarps * kStep);
+      for (int i = 0; i < kAhead; ++i) page[i] = load_page(next + i * kStep);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) issue(page[i]);
     }
@@ -465,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
     for (int i = 0; i < DB; ++i) vref[i] = 0;
 
     uint32_t read = 0;
-    for (int t0 = first + warp * kStep; t0 < last; t0 += kWarps * kStep) {
+    for (int t0 = first; t0 < last; t0 += kStep) {
       cp_wait<kAhead - 1>();
       const uint32_t st = ring + read;
       read = read == kAhead * S::kBytes ? 0 : read + S::kBytes;
@@ -651,58 +662,44 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
     }
     cp_wait<0>();
 
-    // ---- the four warps' results
+    // ---- the result, or this part of it
 #pragma unroll
     for (int k = 4; k < 32; k *= 2) {
       l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, k);
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, k);
     }
-    __syncthreads();  // the rings are free
-    float* const so = reinterpret_cast<float*>(smem);             // [warp][head][D]
-    float* const sm = so + kWarps * kHeads * D;                   // [warp][head][2]
-#pragma unroll
-    for (int i = 0; i < DB; ++i) {
-      // MXFP4: 2^(vref - 127 - 15); a block that met the NaN scale is NaN
-      float f = 1.0f;
-      if constexpr (!kNv)
-        f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-15f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        so[(warp * kHeads + 2 * c + (j & 1)) * D + i * 32 + 4 * g + 2 * (j >> 2) + ((j >> 1) & 1)] =
-            o[i][j >> 2][j & 3] * f;
-    }
-    if (g == 0) {
-      float* q2 = sm + (warp * kHeads + 2 * c) * 2;
-      q2[0] = m0;
-      q2[1] = l0;
-      q2[2] = m1;
-      q2[3] = l1;
-    }
-    __syncthreads();
+    const int64_t slot = (static_cast<int64_t>(b) * units_per_seq + unit + worker) * kHeads;
     const int64_t head_at = static_cast<int64_t>(b) * p.num_q_heads + head0;
-    for (int i = threadIdx.x; i < heads * D; i += kThreads) {
-      const int h = i / D, d = i - h * D;
-      float top = -INFINITY, sum = 0.0f, acc = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[(w * kHeads + h) * 2]);
-      const float z = top == -INFINITY ? 0.0f : top;
+    for (int e = 0; e < 2; ++e) {  // heads 2c and 2c + 1; four values of each block in a lane
+      const int h = 2 * c + e;
+      const float top = e ? m1 : m0, sum = e ? l1 : l0;
+      if (h >= heads) continue;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_approx(sm[(w * kHeads + h) * 2] - z);
-        sum += sm[(w * kHeads + h) * 2 + 1] * f;
-        acc += so[(w * kHeads + h) * D + d] * f;
+      for (int i = 0; i < DB; ++i) {
+        // MXFP4: 2^(vref - 127 - 15); a block that met the NaN scale is NaN
+        float f = 1.0f;
+        if constexpr (!kNv)
+          f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-15f;
+        const float4 v = make_float4(o[i][0][e] * f, o[i][0][2 + e] * f, o[i][1][e] * f, o[i][1][2 + e] * f);
+        const int d = i * 32 + 4 * g;
+        if (n_parts > 1) {
+          // slot unit + warp: the shares are consecutive, so no two parts have the same
+          float* to = p.part_o + (slot + h) * D + d;
+          if (MXFP4_IN_BOUNDS(p, kDbgPart, to, 16)) *reinterpret_cast<float4*>(to) = v;
+        } else {
+          store_out<kNv>(p, head_at + h, d, D, v, sum);
+        }
       }
-      if (n_ctas > 1) {
-        // slot unit + CTA: the CTAs' shares are consecutive, so no two parts have the same
-        const int64_t slot = (unit_index + blockIdx.x) * kHeads + h;
-        if (MXFP4_IN_BOUNDS(p, kDbgPart, p.part_o + slot * D + d, 4)) p.part_o[slot * D + d] = acc;
-        if (d < 2 && MXFP4_IN_BOUNDS(p, kDbgPart, p.part_ml + slot * 2 + d, 4))
-          p.part_ml[slot * 2 + d] = d == 0 ? top : sum;
-      } else {
-        store_out<kNv>(p, head_at + h, d, D, acc, sum, top);
+      if (g == 0) {
+        if (n_parts > 1) {
+          float* to = p.part_ml + (slot + h) * 2;
+          if (MXFP4_IN_BOUNDS(p, kDbgPart, to, 8)) *reinterpret_cast<float2*>(to) = make_float2(top, sum);
+        } else {
+          store_lse(p, head_at + h, sum, top);
+        }
       }
     }
-    __syncthreads();  // the next unit's copies take the same memory
   }
 }
 
@@ -713,60 +710,74 @@ __global__ void __launch_bounds__(kThreads) attention_status_kernel(const Attent
 }
 
 // Joins the parts of each head, and writes what an empty sequence gives: a
-// CTA per (sequence, head), the parts shared by its warps.
+// CTA per (sequence, head), the parts shared by its warps, four values of the
+// output to a lane.
+constexpr int kJoinWarps = 16;
 template <bool kNv>
-__global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttentionParams p) {
-  __shared__ float s_acc[kWarps][256], s_sum[kWarps];
+__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttentionParams p) {
+  __shared__ float4 s_acc[kJoinWarps][64];
+  __shared__ float s_sum[kJoinWarps];
   pdl_wait();
   pdl_release();
+  const int warps = blockDim.x >> 5;
   const int64_t head = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = static_cast<int>(head / p.num_q_heads), h = static_cast<int>(head - static_cast<int64_t>(b) * p.num_q_heads);
   const int kvh = h / p.group, in_group = h - kvh * p.group;
   const int64_t unit = (static_cast<int64_t>(b) * p.chunks + in_group / kHeads) * p.num_kv_heads + kvh;
-  float top = -INFINITY, sum = 0.0f, acc[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
+  const int quads = p.head_dim / 4;
+  float top = -INFINITY, sum = 0.0f;
+  float4 acc[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (steps_of(p, b) > 0) {
     const int first = p.parts[2 * unit], n = p.parts[2 * unit + 1];
-    if (n == 1) return;  // written by the CTA itself
+    if (n == 1) return;  // written by the warp itself
     const int64_t slot = (unit + first) * kHeads + in_group % kHeads;
-    const float* ml = p.part_ml + slot * 2;
-    const float* po = p.part_o + slot * p.head_dim;
-    for (int s = lane; s < n; s += 32) top = fmaxf(top, ml[s * kHeads * 2]);
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml + slot * 2);
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + slot * p.head_dim);
+    for (int s = lane; s < n; s += 32) top = fmaxf(top, ml[s * kHeads].x);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
     const float z = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
-    for (int s = warp; s < n; s += kWarps) {
-      const float f = exp2_approx(ml[s * kHeads * 2] - z);
-      sum += ml[s * kHeads * 2 + 1] * f;
+    for (int s = warp; s < n; s += warps) {
+      const float2 part = ml[s * kHeads];
+      const float f = exp2_approx(part.x - z);
+      sum += part.y * f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i * 32 < p.head_dim) acc[i] += po[static_cast<int64_t>(s) * kHeads * p.head_dim + i * 32 + lane] * f;
+      for (int i = 0; i < 2; ++i)
+        if (i * 32 + lane < quads) {
+          const float4 v = po[static_cast<int64_t>(s) * kHeads * quads + i * 32 + lane];
+          acc[i].x += v.x * f;
+          acc[i].y += v.y * f;
+          acc[i].z += v.z * f;
+          acc[i].w += v.w * f;
+        }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_acc[warp][i * 32 + lane] = acc[i];
+  for (int i = 0; i < 2; ++i) s_acc[warp][i * 32 + lane] = acc[i];
   if (lane == 0) s_sum[warp] = sum;
   __syncthreads();
-  for (int d = threadIdx.x; d < p.head_dim; d += kThreads) {
-    float a = 0.0f, l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      a += s_acc[w][d];
+  if (threadIdx.x < quads) {
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+    for (int w = 0; w < warps; ++w) {
+      const float4 v = s_acc[w][threadIdx.x];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
       l += s_sum[w];
     }
-    store_out<kNv>(p, head, d, p.head_dim, a, l, top);
+    store_out<kNv>(p, head, 4 * threadIdx.x, p.head_dim, a, l);
+    if (threadIdx.x == 0) store_lse(p, head, l, top);
   }
 }
 
 template <bool kNv, int DB>
 cudaError_t launch_dim(const AttentionParams& p, unsigned grid, cudaStream_t stream) {
   using S = Stage<kNv, DB>;
-  constexpr int kRings = kWarps * kStages * S::kBytes;
-  constexpr int kJoin = kWarps * kHeads * (32 * DB + 2) * 4;
-  constexpr int kSmem = kRings > kJoin ? kRings : kJoin;
+  constexpr int kSmem = kWarps * kStages * S::kBytes;
   static std::atomic<uint64_t> ready{0};
   if (const cudaError_t e = allow_smem(attention_kernel<kNv, DB>, kSmem, ready); e != cudaSuccess)
     return e;
@@ -786,18 +797,20 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
     case 7: e = launch_dim<kNv, 7>(p, grid, stream); break;
     default: e = launch_dim<kNv, 8>(p, grid, stream); break;
   }
-  if (e != cudaSuccess || p.ctas == 0) return e;
+  if (e != cudaSuccess || p.workers == 0) return e;
   const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
-  return launch_pdl(attention_join_kernel<kNv>, static_cast<unsigned>(heads), kThreads, 0, stream, p);
+  const int64_t units = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * p.chunks;
+  return launch_pdl(attention_join_kernel<kNv>, static_cast<unsigned>(heads),
+                    32 * (p.workers >= 16 * units ? kJoinWarps : 4), 0, stream, p);
 }
 
-// CTAs that share the positions of all sequences: as many as the GPU holds at
-// once, so that all end together; 0 for contexts so short that a CTA takes a
+// Warps that share the positions of all sequences: as many as the GPU holds at
+// once, so that all end together; 0 for contexts so short that a warp takes a
 // unit whole.
-int shared_ctas(int64_t units, int32_t head_dim, int64_t max_len) {
-  if (max_len <= 2 * kMinSteps * kStep) return 0;
-  const int64_t resident = 152 * (head_dim <= 64 ? 4 : head_dim <= 128 ? 3 : 2);
-  const int64_t most = units * ((max_len + kMinSteps * kStep - 1) / (kMinSteps * kStep));
+int shared_workers(int64_t units, int32_t head_dim, int64_t max_len) {
+  if (max_len <= kAhead * kStep) return 0;
+  const int64_t resident = 152 * kWarps * (head_dim <= 64 ? 4 : head_dim <= 128 ? 3 : 2);
+  const int64_t most = (units * ((max_len + kStep - 1) / kStep) + kWarps - 1) / kWarps * kWarps;
   return static_cast<int>(most < resident ? most : resident);
 }
 
@@ -811,8 +824,8 @@ int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_
                                    int32_t head_dim, int64_t max_len) {
   if (num_seqs == 0 || num_q_heads == 0 || head_dim == 0) return 0;
   const int64_t units = num_seqs * num_kv_heads * chunks_of(num_q_heads, num_kv_heads);
-  const int ctas = shared_ctas(units, head_dim, max_len);
-  return ctas > 0 ? (units + ctas) * kHeads * (head_dim + 2) + 2 * units : 0;
+  const int workers = shared_workers(units, head_dim, max_len);
+  return workers > 0 ? (units + workers) * kHeads * (head_dim + 2) + 2 * units : 0;
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) {
@@ -851,10 +864,10 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   p.group = a.num_q_heads / c.num_heads;
   p.chunks = chunks_of(a.num_q_heads, c.num_heads);
   const int64_t units = a.num_seqs * c.num_heads * p.chunks;
-  p.ctas = shared_ctas(units, c.head_dim, a.max_pages * c.page_size);
+  p.workers = shared_workers(units, c.head_dim, a.max_pages * c.page_size);
   p.part_o = a.workspace;
-  p.part_ml = p.part_o + (units + p.ctas) * kHeads * c.head_dim;
-  p.parts = reinterpret_cast<int32_t*>(p.part_ml + (units + p.ctas) * kHeads * 2);
+  p.part_ml = p.part_o + (units + p.workers) * kHeads * c.head_dim;
+  p.parts = reinterpret_cast<int32_t*>(p.part_ml + (units + p.workers) * kHeads * 2);
 #ifdef MXFP4_DEBUG_BOUNDS
   const int64_t rows = c.num_pages * c.page_size * c.num_heads;
   debug_range(p.dbg, kDbgQ, a.q, a.num_seqs > 0
@@ -867,9 +880,9 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
               a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
   debug_range(p.dbg, kDbgOut, a.out, a.num_seqs * a.num_q_heads * c.head_dim * 2);
   debug_range(p.dbg, kDbgPart, a.workspace,
-              p.ctas > 0 ? ((units + p.ctas) * kHeads * (c.head_dim + 2) + 2 * units) * 4 : 0);
+              p.workers > 0 ? ((units + p.workers) * kHeads * (c.head_dim + 2) + 2 * units) * 4 : 0);
 #endif
-  const int64_t grid = (p.ctas > 0 ? p.ctas : units) + (a.status ? 1 : 0);
+  const int64_t grid = ((p.workers > 0 ? p.workers : units) + kWarps - 1) / kWarps + (a.status ? 1 : 0);
   if (grid == 0) return cudaSuccess;
   return c.nvfp4 ? launch_format<true>(p, static_cast<unsigned>(grid), stream)
                  : launch_format<false>(p, static_cast<unsigned>(grid), stream);
