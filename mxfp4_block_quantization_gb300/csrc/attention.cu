@@ -292,7 +292,6 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
   constexpr int D = 32 * DB;
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_wait();
-  pdl_release();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
 
@@ -701,6 +700,7 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
       }
     }
   }
+  pdl_release();
 }
 
 __global__ void __launch_bounds__(kThreads) attention_status_kernel(const AttentionParams p) {
@@ -709,19 +709,16 @@ __global__ void __launch_bounds__(kThreads) attention_status_kernel(const Attent
   write_status(p);
 }
 
-// Joins the parts of each head, and writes what an empty sequence gives: a
-// CTA per (sequence, head), the parts shared by its warps, four values of the
-// output to a lane.
-constexpr int kJoinWarps = 16;
-template <bool kNv>
-__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const AttentionParams p) {
-  __shared__ float4 s_acc[kJoinWarps][64];
-  __shared__ float s_sum[kJoinWarps];
+// Joins the parts of each head, and writes what an empty sequence gives.  Four
+// values of the output to a lane; with few parts to a head a warp takes them
+// all (kPerHead 1), with many a CTA of 16 warps shares them.
+template <bool kNv, int kPerHead>
+__global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
+    attention_join_kernel(const AttentionParams p) {
   pdl_wait();
-  pdl_release();
-  const int warps = blockDim.x >> 5;
-  const int64_t head = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t head = kPerHead == 1 ? static_cast<int64_t>(blockIdx.x) * kWarps + warp : blockIdx.x;
+  if (head >= static_cast<int64_t>(p.num_seqs) * p.num_q_heads) return;
   const int b = static_cast<int>(head / p.num_q_heads), h = static_cast<int>(head - static_cast<int64_t>(b) * p.num_q_heads);
   const int kvh = h / p.group, in_group = h - kvh * p.group;
   const int64_t unit = (static_cast<int64_t>(b) * p.chunks + in_group / kHeads) * p.num_kv_heads + kvh;
@@ -739,7 +736,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
     for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
     const float z = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
-    for (int s = warp; s < n; s += warps) {
+    for (int s = kPerHead == 1 ? 0 : warp; s < n; s += kPerHead) {
       const float2 part = ml[s * kHeads];
       const float f = exp2_approx(part.x - z);
       sum += part.y * f;
@@ -754,24 +751,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const A
         }
     }
   }
+  if constexpr (kPerHead == 1) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) s_acc[warp][i * 32 + lane] = acc[i];
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  if (threadIdx.x < quads) {
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-    for (int w = 0; w < warps; ++w) {
-      const float4 v = s_acc[w][threadIdx.x];
-      a.x += v.x;
-      a.y += v.y;
-      a.z += v.z;
-      a.w += v.w;
-      l += s_sum[w];
+    for (int i = 0; i < 2; ++i)
+      if (i * 32 + lane < quads) store_out<kNv>(p, head, 4 * (i * 32 + lane), p.head_dim, acc[i], sum);
+    if (lane == 0) store_lse(p, head, sum, top);
+  } else {
+    __shared__ float4 s_acc[kPerHead][64];
+    __shared__ float s_sum[kPerHead];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s_acc[warp][i * 32 + lane] = acc[i];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x < quads) {
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float l = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kPerHead; ++w) {
+        const float4 v = s_acc[w][threadIdx.x];
+        a.x += v.x;
+        a.y += v.y;
+        a.z += v.z;
+        a.w += v.w;
+        l += s_sum[w];
+      }
+      store_out<kNv>(p, head, 4 * threadIdx.x, p.head_dim, a, l);
+      if (threadIdx.x == 0) store_lse(p, head, l, top);
     }
-    store_out<kNv>(p, head, 4 * threadIdx.x, p.head_dim, a, l);
-    if (threadIdx.x == 0) store_lse(p, head, l, top);
   }
+  // Not before the end: the next call's warps have even shares, so its CTAs
+  // should find the SMs free of this kernel's.
+  pdl_release();
 }
 
 template <bool kNv, int DB>
@@ -800,8 +810,10 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
   if (e != cudaSuccess || p.workers == 0) return e;
   const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
   const int64_t units = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * p.chunks;
-  return launch_pdl(attention_join_kernel<kNv>, static_cast<unsigned>(heads),
-                    32 * (p.workers >= 16 * units ? kJoinWarps : 4), 0, stream, p);
+  if (p.workers >= 16 * units)
+    return launch_pdl(attention_join_kernel<kNv, 16>, static_cast<unsigned>(heads), 32 * 16, 0, stream, p);
+  return launch_pdl(attention_join_kernel<kNv, 1>, static_cast<unsigned>((heads + kWarps - 1) / kWarps), kThreads,
+                    0, stream, p);
 }
 
 // Warps that share the positions of all sequences: as many as the GPU holds at
