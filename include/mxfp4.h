@@ -748,7 +748,9 @@ int mxfp4_cache_read_nvfp4_f16(const uint8_t* k_codes, const uint8_t* k_scales,
  *                 b*q_seq_stride + h*q_head_stride + d; strides % 8 == 0,
  *                 >= 0, 16-byte aligned.
  * head_dim        % 32 == 0, <= MXFP4_ATTENTION_MAX_HEAD_DIM.  The cache has
- *                 fewer than 2^32 rows (pages * page_size * kv heads).
+ *                 fewer than 2^32 rows (pages * page_size * kv heads), and
+ *                 num_seqs * ceil(num_q_heads / num_kv_heads / 8) *
+ *                 num_kv_heads * max_pages * page_size / 32 < 2^30.
  * num_q_heads     a multiple of num_kv_heads.
  * page_table      DEVICE int32, row b at b*table_stride, max_pages entries
  *                 (those past a sequence's length are not read).

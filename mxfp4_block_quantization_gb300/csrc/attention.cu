@@ -31,8 +31,8 @@
 // they go into the operands: NVFP4 into V; MXFP4 into P, relative to the
 // largest scale that the warp has met in that 32-value block (an integer
 // maximum, with the output rescaled when it grows).  P is rounded to a half (11
-// bits), as the scale times P would be in any 16-bit operand; at 2^15 times
-// its size the product keeps P down to 2^-29.
+// bits), as the scale times P would be in any 16-bit operand; at 2^12 times
+// its size the product keeps P down to 2^-26.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -48,9 +48,10 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;   // positions of a warp's step
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kAhead = kStages - 1;
 constexpr int kHeads = 8;   // query heads of a CTA: the columns of the products
+constexpr float kLag = 3.0f;  // log2: how far a warp's reference may lag behind its maximum
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -109,37 +110,37 @@ __device__ __forceinline__ bool one_sequence(const AttentionParams& p) {
 }
 // A single sequence's units are padded to whole shares, so that no warp has
 // parts of two; with several sequences of any lengths a share may end anywhere.
-__device__ __forceinline__ int64_t padded_steps(const AttentionParams& p, int steps, int64_t share) {
+__device__ __forceinline__ int padded_steps(const AttentionParams& p, int steps, int share) {
   return one_sequence(p) ? (steps + share - 1) / share * share : steps;
 }
 // Steps of one warp, from the steps of all units.
-__device__ __forceinline__ int64_t share_of(const AttentionParams& p, int64_t& total, int units) {
+__device__ __forceinline__ int share_of(const AttentionParams& p, int& total, int units) {
   if (one_sequence(p)) {
-    const int64_t steps = total / units, per_unit = p.workers / units;
-    const int64_t share = max((steps + per_unit - 1) / per_unit, static_cast<int64_t>(1));
-    total = padded_steps(p, static_cast<int>(steps), share) * units;
+    const int steps = total / units, per_unit = p.workers / units;
+    const int share = max((steps + per_unit - 1) / per_unit, 1);
+    total = padded_steps(p, steps, share) * units;
     return share;
   }
-  return max((total + p.workers - 1) / p.workers, static_cast<int64_t>(1));
+  return max((total + p.workers - 1) / p.workers, 1);
 }
 // The steps of all units, and their prefix sums by thread.
-__device__ __forceinline__ int64_t scan_steps(const AttentionParams& p, int units, int64_t* prefix) {
-  __shared__ int64_t warp_sum[kWarps];
+__device__ __forceinline__ int scan_steps(const AttentionParams& p, int units, int* prefix) {
+  __shared__ int warp_sum[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (p.num_seqs + kThreads - 1) / kThreads;
-  int64_t sum = 0;
+  int sum = 0;
   for (int i = 0; i < per; ++i) {
     const int b = threadIdx.x * per + i;
-    if (b < p.num_seqs) sum += static_cast<int64_t>(steps_of(p, b)) * units;
+    if (b < p.num_seqs) sum += steps_of(p, b) * units;
   }
 #pragma unroll
   for (int k = 1; k < 32; k *= 2) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, k);
+    const int v = __shfl_up_sync(0xFFFFFFFFu, sum, k);
     if (lane >= k) sum += v;
   }
   if (lane == 31) warp_sum[warp] = sum;
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) sum += warp_sum[w];
@@ -150,8 +151,8 @@ __device__ __forceinline__ int64_t scan_steps(const AttentionParams& p, int unit
   return total;
 }
 // The sequence that step `at` belongs to, and its first step.
-__device__ __forceinline__ int find_sequence(const AttentionParams& p, const int64_t* prefix, int units,
-                                             int64_t at, int64_t& first) {
+__device__ __forceinline__ int find_sequence(const AttentionParams& p, const int* prefix, int units,
+                                             int at, int& first) {
   first = 0;
   if (p.num_seqs == 1) return 0;
   int lo = 0, hi = kThreads - 1;
@@ -163,7 +164,7 @@ __device__ __forceinline__ int find_sequence(const AttentionParams& p, const int
   const int per = (p.num_seqs + kThreads - 1) / kThreads;
   int b = lo * per;
   for (;; ++b) {
-    const int64_t n = static_cast<int64_t>(steps_of(p, b)) * units;
+    const int n = steps_of(p, b) * units;
     if (at < first + n || b + 1 >= p.num_seqs) return b;
     first += n;
   }
@@ -287,7 +288,7 @@ __device__ __forceinline__ void own_scales(uint32_t (&k)[S::kWords], uint32_t (&
 }
 
 template <bool kNv, int DB>
-__global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) attention_kernel(const AttentionParams p) {
+__global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) attention_kernel(const AttentionParams p) {
   using S = Stage<kNv, DB>;
   constexpr int D = 32 * DB;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -303,13 +304,13 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
   // its query heads, in steps of 32.
   const int units_per_seq = p.num_kv_heads * p.chunks;
   const int worker = blockIdx.x * kWarps + warp;
-  __shared__ int64_t prefix[kThreads];  // steps up to and with each thread's sequences
-  int64_t at = 0, end = 0, share = 1;   // this warp's steps, over all units
+  __shared__ int prefix[kThreads];  // steps up to and with each thread's sequences
+  int at = 0, end = 0, share = 1;   // this warp's steps, over all units
   if (p.workers > 0) {
-    int64_t total = scan_steps(p, units_per_seq, prefix);
+    int total = scan_steps(p, units_per_seq, prefix);
     share = share_of(p, total, units_per_seq);
-    at = share * worker;
-    end = min(total, at + share);
+    at = static_cast<int>(min(static_cast<int64_t>(share) * worker, static_cast<int64_t>(total)));
+    end = min(total - at, share) + at;
   } else if (worker < static_cast<int64_t>(p.num_seqs) * units_per_seq) {
     end = 1;
   }
@@ -318,18 +319,18 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
     // the unit that step `at` is in, and this warp's part of its steps
     int b, unit, s0 = 0, s1, n_parts = 1;
     if (p.workers > 0) {
-      int64_t unit_at;
+      int unit_at;
       b = find_sequence(p, prefix, units_per_seq, at, unit_at);
       const int steps = steps_of(p, b);
-      const int64_t padded = padded_steps(p, steps, share);
-      unit = static_cast<int>((at - unit_at) / padded);
+      const int padded = padded_steps(p, steps, share);
+      unit = (at - unit_at) / padded;
       unit_at += unit * padded;
-      s0 = static_cast<int>(at - unit_at);
-      s1 = static_cast<int>(min(padded, s0 + (end - at)));
+      s0 = at - unit_at;
+      s1 = min(padded, s0 + (end - at));
       at += s1 - s0;
       // the warps that have a part of the unit
-      const int first_part = static_cast<int>(unit_at / share);
-      n_parts = static_cast<int>((unit_at + steps - 1) / share) - first_part + 1;
+      const int first_part = unit_at / share;
+      n_parts = (unit_at + steps - 1) / share - first_part + 1;
       int32_t* parts = p.parts + 2 * (static_cast<int64_t>(b) * units_per_seq + unit);
       if (s0 == 0 && lane == 0 && MXFP4_IN_BOUNDS(p, kDbgPart, parts, 8)) {
         parts[0] = first_part;
@@ -512,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
           }
           const uint32_t to = st + S::kScaleV + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
 #pragma unroll
-          for (int i = 0; i < DB; ++i)  // 2^(15 + byte - vref)
-            sts16(to + i * 64, static_cast<uint32_t>(max(byte[i] + 30 - vref[i], 0)) << 10);
+          for (int i = 0; i < DB; ++i)  // 2^(12 + byte - vref)
+            sts16(to + i * 64, static_cast<uint32_t>(max(byte[i] + 27 - vref[i], 0)) << 10);
         }
       }
       const int next_page = static_cast<int>(lds32(st + S::kPage + lane * 4));
@@ -580,10 +581,12 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
             if (((valid >> (t * 16 + g + 8 * r)) & 1u) == 0u) s[t][2 * r] = s[t][2 * r + 1] = -INFINITY;
       }
 
-      // ---- running maximum and sum
+      // ---- running maximum and sum.  The reference m may lag behind the
+      // maximum by kLag (P then grows to 2^kLag at most, far inside a half), so
+      // that the output is rescaled a few times at all, not at every new maximum.
       float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
       float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-      if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
+      if (__any_sync(0xFFFFFFFFu, x0 > m0 + kLag || x1 > m1 + kLag)) {
 #pragma unroll
         for (int k = 4; k < 32; k *= 2) {
           x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, k));
@@ -676,10 +679,10 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 4 : DB <= 4 ? 3 : 2) atten
       if (h >= heads) continue;
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        // MXFP4: 2^(vref - 127 - 15); a block that met the NaN scale is NaN
+        // MXFP4: 2^(vref - 127 - 12); a block that met the NaN scale is NaN
         float f = 1.0f;
         if constexpr (!kNv)
-          f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-15f;
+          f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-12f;
         const float4 v = make_float4(o[i][0][e] * f, o[i][0][2 + e] * f, o[i][1][e] * f, o[i][1][2 + e] * f);
         const int d = i * 32 + 4 * g;
         if (n_parts > 1) {
@@ -731,24 +734,41 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
     const int64_t slot = (unit + first) * kHeads + in_group % kHeads;
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml + slot * 2);
     const float4* po = reinterpret_cast<const float4*>(p.part_o + slot * p.head_dim);
-    for (int s = lane; s < n; s += 32) top = fmaxf(top, ml[s * kHeads].x);
+    // one pass, kBatch parts' loads in flight
+    constexpr int kBatch = 6;
+    for (int s0 = kPerHead == 1 ? 0 : warp; s0 < n; s0 += kBatch * kPerHead) {
+      float2 part[kBatch];
+      float4 v[kBatch][2];
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-    const float z = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-    for (int s = kPerHead == 1 ? 0 : warp; s < n; s += kPerHead) {
-      const float2 part = ml[s * kHeads];
-      const float f = exp2_approx(part.x - z);
-      sum += part.y * f;
+      for (int k = 0; k < kBatch; ++k) {
+        const int s = s0 + k * kPerHead;
+        part[k] = s < n ? ml[s * kHeads] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (i * 32 + lane < quads) {
-          const float4 v = po[static_cast<int64_t>(s) * kHeads * quads + i * 32 + lane];
-          acc[i].x += v.x * f;
-          acc[i].y += v.y * f;
-          acc[i].z += v.z * f;
-          acc[i].w += v.w * f;
+        for (int i = 0; i < 2; ++i)
+          v[k][i] = s < n && i * 32 + lane < quads ? po[static_cast<int64_t>(s) * kHeads * quads + i * 32 + lane]
+                                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+      float x = top;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) x = fmaxf(x, part[k].x);
+      const float z = x == -INFINITY ? 0.0f : x;
+      const float keep = exp2_approx(top - z);
+      top = x;
+      sum *= keep;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) acc[i] = make_float4(acc[i].x * keep, acc[i].y * keep, acc[i].z * keep, acc[i].w * keep);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float f = exp2_approx(part[k].x - z);
+        sum += part[k].y * f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          acc[i].x += v[k][i].x * f;
+          acc[i].y += v[k][i].y * f;
+          acc[i].z += v[k][i].z * f;
+          acc[i].w += v[k][i].w * f;
         }
+      }
     }
   }
   if constexpr (kPerHead == 1) {
@@ -758,25 +778,32 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
     if (lane == 0) store_lse(p, head, sum, top);
   } else {
     __shared__ float4 s_acc[kPerHead][64];
-    __shared__ float s_sum[kPerHead];
+    __shared__ float s_sum[kPerHead], s_top[kPerHead];
 #pragma unroll
     for (int i = 0; i < 2; ++i) s_acc[warp][i * 32 + lane] = acc[i];
-    if (lane == 0) s_sum[warp] = sum;
+    if (lane == 0) {
+      s_sum[warp] = sum;
+      s_top[warp] = top;
+    }
     __syncthreads();
     if (threadIdx.x < quads) {
       float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float l = 0.0f;
+      float l = 0.0f, x = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kPerHead; ++w) x = fmaxf(x, s_top[w]);
+      const float z = x == -INFINITY ? 0.0f : x;
 #pragma unroll
       for (int w = 0; w < kPerHead; ++w) {
         const float4 v = s_acc[w][threadIdx.x];
-        a.x += v.x;
-        a.y += v.y;
-        a.z += v.z;
-        a.w += v.w;
-        l += s_sum[w];
+        const float f = exp2_approx(s_top[w] - z);
+        a.x += v.x * f;
+        a.y += v.y * f;
+        a.z += v.z * f;
+        a.w += v.w * f;
+        l += s_sum[w] * f;
       }
       store_out<kNv>(p, head, 4 * threadIdx.x, p.head_dim, a, l);
-      if (threadIdx.x == 0) store_lse(p, head, l, top);
+      if (threadIdx.x == 0) store_lse(p, head, l, x);
     }
   }
   // Not before the end: the next call's warps have even shares, so its CTAs
@@ -810,8 +837,10 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
   if (e != cudaSuccess || p.workers == 0) return e;
   const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
   const int64_t units = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * p.chunks;
-  if (p.workers >= 16 * units)
+  if (p.workers >= 32 * units)
     return launch_pdl(attention_join_kernel<kNv, 16>, static_cast<unsigned>(heads), 32 * 16, 0, stream, p);
+  if (p.workers >= 6 * units)
+    return launch_pdl(attention_join_kernel<kNv, 4>, static_cast<unsigned>(heads), 32 * 4, 0, stream, p);
   return launch_pdl(attention_join_kernel<kNv, 1>, static_cast<unsigned>((heads + kWarps - 1) / kWarps), kThreads,
                     0, stream, p);
 }
@@ -821,7 +850,7 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
 // unit whole.
 int shared_workers(int64_t units, int32_t head_dim, int64_t max_len) {
   if (max_len <= kAhead * kStep) return 0;
-  const int64_t resident = 152 * kWarps * (head_dim <= 64 ? 4 : head_dim <= 128 ? 3 : 2);
+  const int64_t resident = 152 * kWarps * (head_dim <= 64 ? 5 : head_dim <= 128 ? 4 : 2);
   const int64_t most = (units * ((max_len + kStep - 1) / kStep) + kWarps - 1) / kWarps * kWarps;
   return static_cast<int>(most < resident ? most : resident);
 }

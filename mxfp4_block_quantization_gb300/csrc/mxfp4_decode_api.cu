@@ -240,7 +240,12 @@ int attention_checked(const mxfp4::AttentionArgs& a, size_t workspace_bytes, voi
   if (c.head_dim > MXFP4_ATTENTION_MAX_HEAD_DIM || a.max_pages > INT32_MAX / c.page_size ||
       a.table_stride < a.max_pages)
     return MXFP4_ESHAPE;
-  // rows of the cache are counted in uint32
+  // the steps of all (sequence, kv head, 8 query heads) are counted in int32,
+  // padded by at most a share of each; rows of the cache in uint32
+  if (work && c.num_heads > 0) {
+    const int64_t units = a.num_seqs * c.num_heads * ceil_div(a.num_q_heads / c.num_heads, 8);
+    if (units > INT32_MAX / 2 / (a.max_pages * c.page_size / 32 + 1)) return MXFP4_ESHAPE;
+  }
   if (c.num_heads > 0 && c.num_pages * c.page_size > static_cast<int64_t>(UINT32_MAX) / c.num_heads)
     return MXFP4_ESHAPE;
   if (a.num_q_heads > 0 && (c.num_heads == 0 || a.num_q_heads % c.num_heads != 0))
