@@ -140,7 +140,7 @@ struct Cursor {
   int panel, left;           // stages left in this batch and panel
   int tile, chunk, end;      // the tile in its unit, the chunk, and the panel's end
   int unit, e;
-  const uint8_t* row[2];     // this lane's pieces of two rows of codes
+  const uint8_t* row[2];     // this lane's pieces of two rows of codes, chunk 0
   const uint8_t* scale;
   int take[2];               // bytes to copy of each: 0 outside N
 };
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   auto open_tile = [&](Cursor& u) {
     const int base = (u.tile >> 3) * 128 + (u.tile & 7) * 4;
     const int row = base + 32 * (copy_row >> 2) + (copy_row & 3);
-    const uint8_t* codes = p.codes + u.e * p.expert_codes + u.chunk * (kChunk / 2) + copy_at;
+    const uint8_t* codes = p.codes + u.e * p.expert_codes + copy_at;
     const int64_t ld = p.K >> 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -242,8 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       u.row[i] = codes + (u.take[i] ? row + 64 * i : 0) * ld;
     }
     u.scale = p.scales + u.e * p.expert_scales + (u.tile & 7) * 64 +
-              (static_cast<int64_t>(u.tile >> 3) * p.nKT + u.chunk * (kNv ? 2 : 1) + (lane >> 2)) *
-                  kChunkBytes + (lane & 3) * 16;
+              (static_cast<int64_t>(u.tile >> 3) * p.nKT + (lane >> 2)) * kChunkBytes + (lane & 3) * 16;
   };
   auto open_panel = [&](Cursor& u) {
     const int unit = static_cast<int>(u.at / p.tiles);
@@ -291,43 +290,43 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   const uint32_t scale_dst = ring + kStageCodes + lane * 16;
   auto issue = [&]() {
     if (more) {
-      const uint32_t at = in_at;
+      const uint32_t at = in_at, chunk = in.chunk;
+      const uint8_t* const row[2] = {in.row[0] + static_cast<uint64_t>(chunk) * (kChunk / 2),
+                                     in.row[1] + static_cast<uint64_t>(chunk) * (kChunk / 2)};
+      const uint8_t* const scale = in.scale + static_cast<uint64_t>(chunk) * ((kNv ? 2 : 1) * kChunkBytes);
       if (!p.half_rows && in.chunk != tail) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const bool ok = MXFP4_IN_BOUNDS(p, kDbgCodes, in.row[i], in.take[i]);
-          cp_async<16>(copy_dst + at + i * 8 * kRowPitch, in.row[i], ok ? in.take[i] : 0);
+          const bool ok = MXFP4_IN_BOUNDS(p, kDbgCodes, row[i], in.take[i]);
+          cp_async<16>(copy_dst + at + i * 8 * kRowPitch, row[i], ok ? in.take[i] : 0);
         }
-        cp_async16_if(scale_dst + at, in.scale,
-                      lane < kScaleBytes / 16 && MXFP4_IN_BOUNDS(p, kDbgScales, in.scale, 16));
+        cp_async16_if(scale_dst + at, scale,
+                      lane < kScaleBytes / 16 && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16));
       } else {
         // the last, partial chunk, and rows that start at 8-byte boundaries
         const int k = in.chunk * kChunk + copy_at * 2;
         if (!p.half_rows) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const bool ok = in.take[i] != 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, in.row[i], 16);
-            cp_async<16>(copy_dst + at + i * 8 * kRowPitch, ok ? in.row[i] : p.codes, ok ? 16 : 0);
+            const bool ok = in.take[i] != 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, row[i], 16);
+            cp_async<16>(copy_dst + at + i * 8 * kRowPitch, ok ? row[i] : p.codes, ok ? 16 : 0);
           }
         } else {
           // a copy takes the four rows of one 32-row quarter
           const int first_row = (in.tile >> 3) * 128 + (in.tile & 7) * 4 + copy_row;
           for (int i = 0; i < 4; ++i) {
-            const uint8_t* src = in.row[i >> 1] + (i & 1) * 32 * static_cast<int64_t>(p.K >> 1);
+            const uint8_t* src = row[i >> 1] + (i & 1) * 32 * static_cast<int64_t>(p.K >> 1);
             const bool ok = first_row + 32 * i < p.N && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 8);
             cp_async<8>(copy_dst + at + i * 4 * kRowPitch, ok ? src : p.codes, ok ? 8 : 0);
           }
         }
         if (lane < kScaleBytes / 16) {
           const bool ok = in.chunk * (kNv ? 2 : 1) + (lane >> 2) < p.nKT &&
-                          MXFP4_IN_BOUNDS(p, kDbgScales, in.scale, 16);
-          cp_async<16>(scale_dst + at, ok ? in.scale : p.scales, ok ? 16 : 0);
+                          MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16);
+          cp_async<16>(scale_dst + at, ok ? scale : p.scales, ok ? 16 : 0);
         }
       }
       in_at = in_at == kAhead * kStage ? 0 : in_at + kStage;
-      in.row[0] += kChunk / 2;
-      in.row[1] += kChunk / 2;
-      in.scale += (kNv ? 2 : 1) * kChunkBytes;
       ++in.chunk;
       if (--in.left == 0) {
         settle();
@@ -360,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       // the sums of the batch before are read, and its x
       __syncthreads();
       if (unit != staged_unit || n_panels > 1) {
-        // stage x: 4 lanes to a 32-element block of a token, four blocks'
-        // loads in flight per lane
+        // stage x: 4 lanes to a 32-element block of a token, copied, then
+        // scaled to halves in place
         if (unit != staged_unit) {
           if (threadIdx.x < ur.n) {
             int64_t src = ur.row0 + threadIdx.x;
@@ -370,48 +369,36 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           }
           __syncthreads();
         }
-        constexpr int kGroups = kThreads / 4, kLoads = 4;
-        const int blocks = n * 4;
-        for (int w0 = threadIdx.x >> 2; w0 < blocks * ur.n; w0 += kLoads * kGroups) {
-          uint4 v[kLoads];
-          int tok[kLoads], blk[kLoads];
+        const int blocks = n * 4, total_x = blocks * ur.n;
+        for (int w = threadIdx.x >> 2; w < total_x; w += kThreads / 4) {
+          const int tok = w / blocks, blk = w - tok * blocks;
+          const int k = (lo * 4 + blk) * 32 + c * 8;
+          const int64_t row = sh.x_row[tok];
+          const uint8_t* src = p.x + (row * p.ldx + k) * 2;
+          const bool take = row >= 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgX, src, 16);
+          cp_async<16>(smem_u32(x_s + tok * p.x_pitch + blk * 64 + c * 16), take ? src : p.x, take ? 16 : 0);
+        }
+        cp_commit();
+        cp_wait<0>();
+        if constexpr (!kF16) {
+          // each lane has copied what it converts
+          for (int w = threadIdx.x >> 2; w < total_x; w += kThreads / 4) {
+            const int tok = w / blocks, blk = w - tok * blocks;
+            uint4* at = reinterpret_cast<uint4*>(x_s + tok * p.x_pitch + blk * 64 + c * 16);
+            const uint4 v = *at;
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+            uint32_t m = 0u, r[4];
 #pragma unroll
-          for (int j = 0; j < kLoads; ++j) {
-            const int w = w0 + j * kGroups;
-            tok[j] = w / blocks;
-            blk[j] = w - tok[j] * blocks;
-            v[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (w >= blocks * ur.n) {
-              tok[j] = -1;
-              continue;
-            }
-            const int k = (lo * 4 + blk[j]) * 32 + c * 8;
-            const int64_t src_row = sh.x_row[tok[j]];
-            const uint8_t* src = p.x + (src_row * p.ldx + k) * 2;
-            if (src_row >= 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgX, src, 16))
-              v[j] = __ldg(reinterpret_cast<const uint4*>(src));
-          }
+            for (int i = 0; i < 4; ++i) m = max_finite_bf16x2(m, q[i]);
+            m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 1));
+            m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 2));
+            float inverse;
+            const float f = half_scale(m, inverse);
 #pragma unroll
-          for (int j = 0; j < kLoads; ++j) {
-            uint4 o = v[j];
-            if constexpr (!kF16) {
-              const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-              uint32_t m = 0u, r[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) m = max_finite_bf16x2(m, q[i]);
-              m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 1));
-              m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 2));
-              float inverse;
-              const float f = half_scale(m, inverse);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                r[i] = pack_f16x2(__uint_as_float(q[i] << 16) * f,
-                                  __uint_as_float(q[i] & 0xFFFF0000u) * f);
-              o = make_uint4(r[0], r[1], r[2], r[3]);
-              if (c == 0 && tok[j] >= 0)
-                xs_s[blk[j] * R + tok[j]] = inverse;
-            }
-            if (tok[j] >= 0) *reinterpret_cast<uint4*>(x_s + tok[j] * p.x_pitch + blk[j] * 64 + c * 16) = o;
+            for (int i = 0; i < 4; ++i)
+              r[i] = pack_f16x2(__uint_as_float(q[i] << 16) * f, __uint_as_float(q[i] & 0xFFFF0000u) * f);
+            *at = make_uint4(r[0], r[1], r[2], r[3]);
+            if (c == 0) xs_s[blk * R + tok] = inverse;
           }
         }
         __syncthreads();
@@ -592,18 +579,26 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
   const int per_chunk = p.x_rows * kChunk * 2 + (kF16 ? 0 : 4 * R * 4);
   const auto parts = [&](int batch) { return (batch + kWarps) * kTile * R * 4; };
   const auto fits = [&](int room) { return (kMaxSmem - rings - room - p.x_rows * 64) / per_chunk; };
-  int batch = nt == 1 ? 32 : 16;
-  if (batch > per_cta) batch = static_cast<int>(per_cta < 1 ? 1 : per_cta);
-  const int fewest = batch < 8 ? batch : 8;
-  int panel = p.chunks, n_panels = 1, sums = 0;
-  if (p.chunks > fits(parts(fewest))) {  // x does not fit whole
-    sums = batch * kTile * R * 4;
-    panel = fits(parts(batch) + sums);
-    n_panels = (p.chunks + panel - 1) / panel;
-    panel = (p.chunks + n_panels - 1) / n_panels;
-  } else {
-    while (p.chunks > fits(parts(batch))) --batch;
+  // All of a CTA's tiles in one batch and x whole if they fit; else the split
+  // with the fewest batches times panels.
+  int batch = 1, panel = 1, n_panels = 1;
+  int64_t fewest = -1;
+  for (int64_t n_batches = 1; n_batches <= (per_cta > 1 ? per_cta : 1); ++n_batches) {
+    const int64_t tiles = ((per_cta > 1 ? per_cta : 1) + n_batches - 1) / n_batches;
+    if (tiles > 96) continue;
+    const int bt = static_cast<int>(tiles), sum_bytes = bt * kTile * R * 4;
+    int pn = fits(parts(bt)) >= p.chunks ? p.chunks : fits(parts(bt) + sum_bytes);
+    if (pn < 1) continue;
+    const int panels = p.chunks > 0 ? (p.chunks + pn - 1) / pn : 1;
+    if (fewest < 0 || n_batches * panels < fewest) {
+      fewest = n_batches * panels;
+      batch = bt;
+      n_panels = panels;
+      panel = p.chunks > 0 ? (p.chunks + panels - 1) / panels : 0;
+    }
+    if (panels == 1 || n_batches > 64) break;
   }
+  const int sums = n_panels > 1 ? batch * kTile * R * 4 : 0;
   p.batch = batch;
   p.panel = panel;
   p.x_pitch = panel * kChunk * 2 + 64;
