@@ -14,7 +14,7 @@
 // number of tokens up to 8.
 //
 // A warp owns 16 rows of W and a range of K, and streams its codes through
-// its own ring of shared-memory stages (16-byte asynchronous copies, 128
+// its own ring of shared-memory stages (16-byte asynchronous copies, 256
 // elements of K by 16 rows each), so warps never wait on one another inside a
 // product.  The 16 rows are {4j..4j+3} + {0, 32, 64, 96} of a 128-row tile:
 // their scale bytes are 64 consecutive bytes of the tiled layout.
@@ -45,13 +45,12 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                      // weight rows of a warp's tile
-constexpr int kChunk = 128;                    // elements of K per stage
-// A row's 64 bytes of codes in a stage, 80 bytes apart: the eight rows that a
+constexpr int kChunk = 256;                    // elements of K per stage
+constexpr int kBlocks = kChunk / 32;
+// A row's 128 bytes of codes in a stage, 144 bytes apart: the eight rows that a
 // fragment's words come from then lie in different banks.
-constexpr int kRowPitch = 80;
+constexpr int kRowPitch = 144;
 constexpr int kStageCodes = kTile * kRowPitch;
-constexpr int kStages = 4;                     // ring of a warp
-constexpr int kAhead = kStages - 1;            // stages in flight
 
 struct MatvecParams {
   const uint8_t* __restrict__ x;
@@ -73,11 +72,12 @@ struct MatvecParams {
   int32_t E;
   int32_t nKT;        // 4-column scale chunks of a row
   int32_t tiles;      // 16-row tiles of N (8 per 128 rows)
-  int32_t chunks;     // 128-element chunks of K
+  int32_t chunks;     // 256-element chunks of K
   int32_t panel;      // chunks of x staged at a time
   int32_t batch;      // tiles that the CTA's warps take together
   int32_t x_rows;     // token rows that x's shared memory holds
   int32_t x_pitch;    // bytes between them
+  int32_t stages;     // of a warp's ring, 2 or 3
   int32_t y_f32;
   int32_t half_rows;  // rows of codes start at 8-byte (not 16-byte) boundaries
 #ifdef MXFP4_DEBUG_BOUNDS
@@ -136,30 +136,33 @@ __device__ __forceinline__ int share_of(int f, int total) { return ((f + 1) * kW
 // Where a warp's copies stand: the batch of tiles, the panel of x, the chunks
 // left in the warp's share of them, and what its lanes copy next.
 struct Cursor {
-  int64_t at;                // first tile of the batch, over all units
+  int at;                    // first tile of the batch, over all units
   int panel, left;           // stages left in this batch and panel
   int tile, chunk, end;      // the tile in its unit, the chunk, and the panel's end
   int unit, e;
-  const uint8_t* row[2];     // this lane's pieces of two rows of codes, chunk 0
+  int quarters;              // of the tile's four 32-row quarters, those in which this lane's row is in N
+  const uint8_t* row;        // this lane's piece of its row of the first quarter, chunk 0
   const uint8_t* scale;
-  int take[2];               // bytes to copy of each: 0 outside N
 };
 
 template <bool kNv, bool kF16, int NT>
 __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams p) {
   constexpr int R = 8 * NT;
-  constexpr int kScaleBytes = kNv ? 128 : 64;
+  constexpr int kScaleBytes = kNv ? 256 : 128;
+  constexpr int kChunkKt = kChunk / (kNv ? 64 : 128);  // 4-column scale chunks of a stage
   constexpr int kStage = kStageCodes + kScaleBytes;
-  constexpr int kUnroll = NT == 4 ? 1 : NT == 2 ? 2 : 4;  // more tokens, more registers
+  // more tokens, more registers: fewer blocks at once
+  constexpr int kUnroll = NT == 4 ? 1 : 4, kUnrollKt = NT == 1 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   // shared memory: rings | x halves | x block scales | parts of sums | sums of panels
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
-  uint8_t* const x_s = smem + kWarps * kStages * kStage;
+  const int ring_bytes = p.stages * kStage;
+  const uint32_t ring = smem_u32(smem) + warp * ring_bytes;
+  uint8_t* const x_s = smem + kWarps * ring_bytes;
   float* const xs_s = reinterpret_cast<float*>(x_s + p.x_rows * p.x_pitch);
-  float* const part_s = xs_s + (kF16 ? 0 : p.panel * 4 * R);
+  float* const part_s = xs_s + (kF16 ? 0 : p.panel * kBlocks * R);
   float* const sum_s = part_s + (p.batch + kWarps) * kTile * R;
 
   pdl_wait();
@@ -218,34 +221,28 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   // stages, of which each warp has an even share: a tile's sum is then split
   // over one warp or several, whatever the sizes.
   const int64_t all = static_cast<int64_t>(units) * p.tiles;
-  const int64_t first = all * blockIdx.x / gridDim.x, last = all * (blockIdx.x + 1) / gridDim.x;
+  const int first = static_cast<int>(all * blockIdx.x / gridDim.x);
+  const int last = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
   if (first >= last) return;
   const int n_panels = p.chunks > 0 ? (p.chunks + p.panel - 1) / p.panel : 0;
-  auto batch_tiles = [&](int64_t at) {  // of the batch that starts at tile `at`
-    const int left = p.tiles - static_cast<int>(at % p.tiles);
-    return static_cast<int>(min(static_cast<int64_t>(min(left, p.batch)), last - at));
+  auto batch_tiles = [&](int at) {  // of the batch that starts at tile `at`
+    return min(min(p.tiles - at % p.tiles, p.batch), last - at);
   };
 
-  // Row i of a tile is row tile_base + 32 * (i / 4) + i % 4 of the weights.  In
-  // a copy, four lanes take a row's 64 bytes (or eight of its 8-byte pieces).
+  // Row i of a tile is row tile_base + 32 * (i / 4) + i % 4 of the weights.  A
+  // copy takes the four rows of a quarter, eight lanes to a row's 128 bytes.
   const int tail = p.K % kChunk != 0 ? p.chunks - 1 : -1;  // the chunk that ends before its stage
-  const int pieces = p.half_rows ? 3 : 2;                   // log2 of a row's pieces
-  const int copy_row = lane >> pieces, copy_at = (lane & ((1 << pieces) - 1)) * (64 >> pieces);
+  const int copy_row = lane >> 3, copy_at = (lane & 7) * 16;
+  const int64_t quarter = 32 * static_cast<int64_t>(p.K >> 1);  // bytes of 32 rows
   auto open_tile = [&](Cursor& u) {
-    const int base = (u.tile >> 3) * 128 + (u.tile & 7) * 4;
-    const int row = base + 32 * (copy_row >> 2) + (copy_row & 3);
-    const uint8_t* codes = p.codes + u.e * p.expert_codes + copy_at;
-    const int64_t ld = p.K >> 1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      u.take[i] = row + 64 * i < p.N ? 16 : 0;
-      u.row[i] = codes + (u.take[i] ? row + 64 * i : 0) * ld;
-    }
+    const int base = (u.tile >> 3) * 128 + (u.tile & 7) * 4 + copy_row;
+    u.quarters = base < p.N ? min(4, (p.N - base + 31) >> 5) : 0;
+    u.row = p.codes + u.e * p.expert_codes + (u.quarters ? base : 0) * static_cast<int64_t>(p.K >> 1) + copy_at;
     u.scale = p.scales + u.e * p.expert_scales + (u.tile & 7) * 64 +
               (static_cast<int64_t>(u.tile >> 3) * p.nKT + (lane >> 2)) * kChunkBytes + (lane & 3) * 16;
   };
   auto open_panel = [&](Cursor& u) {
-    const int unit = static_cast<int>(u.at / p.tiles);
+    const int unit = u.at / p.tiles;
     if (unit != u.unit) {
       u.unit = unit;
       u.e = p.offsets == nullptr ? 0 : find_unit<NT>(p, sh, unit).e;
@@ -254,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     const int total = batch_tiles(u.at) * n;
     const int f0 = total * warp / kWarps;
     u.left = total * (warp + 1) / kWarps - f0;
-    u.tile = static_cast<int>(u.at % p.tiles) + f0 / n;
+    u.tile = u.at - unit * p.tiles + f0 / n;
     u.chunk = lo + f0 % n;
     u.end = lo + n;
     if (u.left > 0) open_tile(u);
@@ -285,48 +282,48 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     open_panel(in);
     settle();
   }
-  uint32_t in_at = 0;  // byte offset of the stage to fill
-  const uint32_t copy_dst = ring + copy_row * kRowPitch + copy_at;
-  const uint32_t scale_dst = ring + kStageCodes + lane * 16;
+  uint32_t in_at = ring;  // the stage to fill
+  const uint32_t copy_to = copy_row * kRowPitch + copy_at, ring_end = ring + ring_bytes;
   auto issue = [&]() {
     if (more) {
-      const uint32_t at = in_at, chunk = in.chunk;
-      const uint8_t* const row[2] = {in.row[0] + static_cast<uint64_t>(chunk) * (kChunk / 2),
-                                     in.row[1] + static_cast<uint64_t>(chunk) * (kChunk / 2)};
-      const uint8_t* const scale = in.scale + static_cast<uint64_t>(chunk) * ((kNv ? 2 : 1) * kChunkBytes);
+      const uint32_t to = in_at + copy_to, scale_to = in_at + kStageCodes + lane * 16;
+      const uint8_t* row = in.row + static_cast<uint32_t>(in.chunk) * static_cast<uint64_t>(kChunk / 2);
+      const uint8_t* const scale =
+          in.scale + static_cast<uint32_t>(in.chunk) * static_cast<uint64_t>(kChunkKt * kChunkBytes);
       if (!p.half_rows && in.chunk != tail) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bool ok = MXFP4_IN_BOUNDS(p, kDbgCodes, row[i], in.take[i]);
-          cp_async<16>(copy_dst + at + i * 8 * kRowPitch, row[i], ok ? in.take[i] : 0);
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* src = i < in.quarters ? row : p.codes;
+          cp_async<16>(to + i * 4 * kRowPitch, src,
+                       i < in.quarters && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 16) ? 16 : 0);
+          row += quarter;
         }
-        cp_async16_if(scale_dst + at, scale,
+        cp_async16_if(scale_to, scale,
                       lane < kScaleBytes / 16 && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16));
       } else {
         // the last, partial chunk, and rows that start at 8-byte boundaries
         const int k = in.chunk * kChunk + copy_at * 2;
-        if (!p.half_rows) {
+        for (int i = 0; i < 4; ++i) {
+          if (!p.half_rows) {
+            const bool ok = i < in.quarters && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, row, 16);
+            cp_async<16>(to + i * 4 * kRowPitch, ok ? row : p.codes, ok ? 16 : 0);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const bool ok = in.take[i] != 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, row[i], 16);
-            cp_async<16>(copy_dst + at + i * 8 * kRowPitch, ok ? row[i] : p.codes, ok ? 16 : 0);
+            for (int h = 0; h < 2; ++h) {
+              const bool ok =
+                  i < in.quarters && k + 16 * h < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, row + 8 * h, 8);
+              cp_async<8>(to + i * 4 * kRowPitch + 8 * h, ok ? row + 8 * h : p.codes, ok ? 8 : 0);
+            }
           }
-        } else {
-          // a copy takes the four rows of one 32-row quarter
-          const int first_row = (in.tile >> 3) * 128 + (in.tile & 7) * 4 + copy_row;
-          for (int i = 0; i < 4; ++i) {
-            const uint8_t* src = row[i >> 1] + (i & 1) * 32 * static_cast<int64_t>(p.K >> 1);
-            const bool ok = first_row + 32 * i < p.N && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 8);
-            cp_async<8>(copy_dst + at + i * 4 * kRowPitch, ok ? src : p.codes, ok ? 8 : 0);
-          }
+          row += quarter;
         }
         if (lane < kScaleBytes / 16) {
-          const bool ok = in.chunk * (kNv ? 2 : 1) + (lane >> 2) < p.nKT &&
-                          MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16);
-          cp_async<16>(scale_dst + at, ok ? scale : p.scales, ok ? 16 : 0);
+          const bool ok = in.chunk * kChunkKt + (lane >> 2) < p.nKT && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16);
+          cp_async<16>(scale_to, ok ? scale : p.scales, ok ? 16 : 0);
         }
       }
-      in_at = in_at == kAhead * kStage ? 0 : in_at + kStage;
+      in_at += kStage;
+      if (in_at == ring_end) in_at = ring;
       ++in.chunk;
       if (--in.left == 0) {
         settle();
@@ -338,13 +335,13 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     }
     cp_commit();  // an empty group at the end keeps the count of groups
   };
-  for (int i = 0; i < kAhead; ++i) issue();
+  for (int i = 1; i < p.stages; ++i) issue();
 
-  uint32_t out_at = 0;  // byte offset of the stage to read
+  uint32_t out_at = ring;  // the stage to read
   int staged_unit = -1;
   UnitRows ur{0, 0, 0};
-  for (int64_t at = first; at < last;) {
-    const int unit = static_cast<int>(at / p.tiles), tile0 = static_cast<int>(at % p.tiles);
+  for (int at = first; at < last;) {
+    const int unit = at / p.tiles, tile0 = at - unit * p.tiles;
     const int n_tiles = batch_tiles(at);
     at += n_tiles;
     if (unit != staged_unit) ur = find_unit<NT>(p, sh, unit);
@@ -369,10 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           }
           __syncthreads();
         }
-        const int blocks = n * 4, total_x = blocks * ur.n;
+        const int blocks = n * kBlocks, total_x = blocks * ur.n;
         for (int w = threadIdx.x >> 2; w < total_x; w += kThreads / 4) {
           const int tok = w / blocks, blk = w - tok * blocks;
-          const int k = (lo * 4 + blk) * 32 + c * 8;
+          const int k = (lo * kBlocks + blk) * 32 + c * 8;
           const int64_t row = sh.x_row[tok];
           const uint8_t* src = p.x + (row * p.ldx + k) * 2;
           const bool take = row >= 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgX, src, 16);
@@ -426,27 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
         }
       };
       for (int f = f0; f < f1; ++f) {
-        cp_wait<kAhead - 1>();
+        if (p.stages == 3) cp_wait<1>(); else cp_wait<0>();
         __syncwarp();  // the copies of all lanes are in; the stage read last is free
         issue();
-        const uint32_t st = ring + out_at;
-        out_at = out_at == kAhead * kStage ? 0 : out_at + kStage;
+        const uint32_t st = out_at;
+        out_at += kStage;
+        if (out_at == ring_end) out_at = ring;
         // scale words of rows g and g + 8
         const uint32_t sa = st + kStageCodes + (g & 3) * 16 + (g >> 2) * 4;
-        uint32_t sw[kNv ? 2 : 1][2];
-#pragma unroll
-        for (int i = 0; i < (kNv ? 2 : 1); ++i) {
-          sw[i][0] = lds32(sa + i * 64);
-          sw[i][1] = lds32(sa + i * 64 + 8);
-        }
-        uint32_t wp[2][2];  // MXFP4: the four scales of a row as BF16 pairs
-        if constexpr (!kNv) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            wp[i][0] = e8m0x2_to_bf16x2(sw[0][i]);
-            wp[i][1] = e8m0x2_to_bf16x2(sw[0][i] >> 16);
-          }
-        }
         float run[NT][4];  // FP16 x with NVFP4: sums of the whole stage
         if constexpr (kNv && kF16) {
 #pragma unroll
@@ -456,50 +440,56 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
         }
         const uint32_t wa = st + g * kRowPitch + c * 4;
         const uint32_t xc = ch * (kChunk * 2);
-        const uint32_t sx = smem_u32(xs_s) + (ch * 4 * R + 2 * c) * 4;
+        const uint32_t sx = smem_u32(xs_s) + (ch * kBlocks * R + 2 * c) * 4;
+#pragma unroll kUnrollKt
+        for (int kt = 0; kt < kChunkKt; ++kt) {
+          const uint32_t sw0 = lds32(sa + kt * 64), sw1 = lds32(sa + kt * 64 + 8);
 #pragma unroll kUnroll
-        for (int b = 0; b < 4; ++b) {
-          uint32_t a0[4], a1[4];
-          decode_word(lds32(wa + b * 16), a0);
-          decode_word(lds32(wa + 8 * kRowPitch + b * 16), a1);
-          float ws0 = 1.0f, ws1 = 1.0f;
-          if constexpr (!kNv) {
-            const uint32_t w0 = b < 2 ? wp[0][0] : wp[0][1], w1 = b < 2 ? wp[1][0] : wp[1][1];
-            ws0 = __uint_as_float(b & 1 ? w0 & 0xFFFF0000u : w0 << 16);
-            ws1 = __uint_as_float(b & 1 ? w1 & 0xFFFF0000u : w1 << 16);
-          } else {
-            // lanes 0, 1 hold the block's first 16 elements, lanes 2, 3 the rest
-            const uint32_t pick = ((b & 1) * 2 + (c >> 1)) * 0x11u;  // that byte twice
-            const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(b < 2 ? sw[0][0] : sw[kNv][0], 0u, pick));
-            const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(b < 2 ? sw[0][1] : sw[kNv][1], 0u, pick));
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              a0[i] = hmul2(a0[i], f0);
-              a1[i] = hmul2(a1[i], f1);
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const uint4 xb = lds128(xa[t] + xc + b * 64);
-            if constexpr (kNv && kF16) {
-              mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
-              mma16816(run[t], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
+          for (int b4 = 0; b4 < kBlocks / kChunkKt; ++b4) {
+            const int b = kt * (kBlocks / kChunkKt) + b4;
+            uint32_t a0[4], a1[4];
+            decode_word(lds32(wa + b * 16), a0);
+            decode_word(lds32(wa + 8 * kRowPitch + b * 16), a1);
+            float ws0 = 1.0f, ws1 = 1.0f;
+            if constexpr (!kNv) {
+              const uint32_t w0 = e8m0x2_to_bf16x2(sw0 >> (16 * (b4 / 2)));
+              const uint32_t w1 = e8m0x2_to_bf16x2(sw1 >> (16 * (b4 / 2)));
+              ws0 = __uint_as_float(b4 & 1 ? w0 & 0xFFFF0000u : w0 << 16);
+              ws1 = __uint_as_float(b4 & 1 ? w1 & 0xFFFF0000u : w1 << 16);
             } else {
-              float d[4];
-              mma16816_first(d, a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
-              mma16816(d, a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
-              float2 xs = make_float2(1.0f, 1.0f);
-              if constexpr (!kF16) xs = lds64f(sx + (b * R + t * 8) * 4);
-              if constexpr (kNv) {
-                acc[t][0] = fmaf(d[0], xs.x, acc[t][0]);
-                acc[t][1] = fmaf(d[1], xs.y, acc[t][1]);
-                acc[t][2] = fmaf(d[2], xs.x, acc[t][2]);
-                acc[t][3] = fmaf(d[3], xs.y, acc[t][3]);
+              // lanes 0, 1 hold the block's first 16 elements, lanes 2, 3 the rest
+              const uint32_t pick = (b4 * 2 + (c >> 1)) * 0x11u;  // that byte twice
+              const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(sw0, 0u, pick));
+              const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(sw1, 0u, pick));
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                a0[i] = hmul2(a0[i], f0);
+                a1[i] = hmul2(a1[i], f1);
+              }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const uint4 xb = lds128(xa[t] + xc + b * 64);
+              if constexpr (kNv && kF16) {
+                mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+                mma16816(run[t], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
               } else {
-                acc[t][0] = fmaf(d[0], ws0 * xs.x, acc[t][0]);
-                acc[t][1] = fmaf(d[1], ws0 * xs.y, acc[t][1]);
-                acc[t][2] = fmaf(d[2], ws1 * xs.x, acc[t][2]);
-                acc[t][3] = fmaf(d[3], ws1 * xs.y, acc[t][3]);
+                float d[4];
+                mma16816_first(d, a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+                mma16816(d, a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
+                float2 xs = make_float2(1.0f, 1.0f);
+                if constexpr (!kF16) xs = lds64f(sx + (b * R + t * 8) * 4);
+                if constexpr (kNv) {
+                  acc[t][0] = fmaf(d[0], xs.x, acc[t][0]);
+                  acc[t][1] = fmaf(d[1], xs.y, acc[t][1]);
+                  acc[t][2] = fmaf(d[2], xs.x, acc[t][2]);
+                  acc[t][3] = fmaf(d[3], xs.y, acc[t][3]);
+                } else {
+                  acc[t][0] = fmaf(d[0], ws0 * xs.x, acc[t][0]);
+                  acc[t][1] = fmaf(d[1], ws0 * xs.y, acc[t][1]);
+                  acc[t][2] = fmaf(d[2], ws1 * xs.x, acc[t][2]);
+                  acc[t][3] = fmaf(d[3], ws1 * xs.y, acc[t][3]);
+                }
               }
             }
           }
@@ -525,35 +515,47 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       const float gs = kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + ur.e, 4)
                            ? __ldg(p.global_scales + ur.e)
                            : 1.0f;
-      for (int i = threadIdx.x; i < n_tiles * kTile * ur.n; i += kThreads) {
+      const int quads = (ur.n + 3) >> 2;  // of tokens
+      for (int i = threadIdx.x; i < n_tiles * kTile * quads; i += kThreads) {
         const int r = i % kTile, rest = i / kTile;
-        const int tl = rest % n_tiles, t = rest / n_tiles;
-        float v = 0.0f;
+        const int tl = rest / quads, t = (rest - tl * quads) * 4;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        auto add = [&](const float* q) {
+          const float4 u = *reinterpret_cast<const float4*>(q);
+          v.x += u.x;
+          v.y += u.y;
+          v.z += u.z;
+          v.w += u.w;
+        };
         if (total > 0) {
           // the warps whose shares [total * w / 16, total * (w + 1) / 16) meet this tile's stages
           const int w0 = share_of(tl * n, total), w1 = share_of(tl * n + n - 1, total);
           for (int w = w0; w <= w1; ++w)
-            if (total * w / kWarps < total * (w + 1) / kWarps)
-              v += part_s[((tl + w) * kTile + r) * R + t];
+            if (total * w / kWarps < total * (w + 1) / kWarps) add(part_s + ((tl + w) * kTile + r) * R + t);
         }
         float* before = sum_s + (tl * kTile + r) * R + t;
-        if (panel > 0) v += *before;
+        if (panel > 0) add(before);
         if (!done) {
-          *before = v;
+          *reinterpret_cast<float4*>(before) = v;
           continue;
         }
         const int64_t row = static_cast<int64_t>((tile0 + tl) >> 3) * 128 + ((tile0 + tl) & 7) * 4 +
                             32 * (r >> 2) + (r & 3);
         if (row >= p.N) continue;
-        if constexpr (kNv) v /= gs;
-        const int64_t to = (static_cast<int64_t>(ur.row0) + t) * p.ldy + row;
-        if (p.y_f32) {
-          float* y = reinterpret_cast<float*>(p.y) + to;
-          if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = v;
-        } else {
-          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + to;
-          if (MXFP4_IN_BOUNDS(p, kDbgY, y, 2))
-            *y = kF16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
+        const float out[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (t + j >= ur.n) break;
+          const float o = kNv ? out[j] / gs : out[j];
+          const int64_t to = (static_cast<int64_t>(ur.row0) + t + j) * p.ldy + row;
+          if (p.y_f32) {
+            float* y = reinterpret_cast<float*>(p.y) + to;
+            if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = o;
+          } else {
+            uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + to;
+            if (MXFP4_IN_BOUNDS(p, kDbgY, y, 2))
+              *y = kF16 ? __half_as_ushort(__float2half_rn(o)) : static_cast<uint16_t>(cvt_bf16x2(o, 0.0f));
+          }
         }
       }
     }
@@ -568,41 +570,46 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
                       : nt == 2 ? matvec_kernel<kNv, kF16, 2>
                                 : matvec_kernel<kNv, kF16, 4>;
   const int R = 8 * nt;
-  const int kStage = kStageCodes + (kNv ? 128 : 64);
+  const int kStage = kStageCodes + (kNv ? 256 : 128);
   const int sms = sm_count();
   p.x_rows = p.rows < R ? (p.rows > 0 ? p.rows : 1) : R;
   // Tiles of a CTA, about, and how many of them its warps take together: more
   // make their shares of the stages more even and stage x less often, but
   // their sums' parts need room that x's panels need too.
   const int64_t per_cta = (expected_units * p.tiles + sms - 1) / sms;
-  const int rings = kWarps * kStages * kStage;
-  const int per_chunk = p.x_rows * kChunk * 2 + (kF16 ? 0 : 4 * R * 4);
+  const int per_chunk = p.x_rows * kChunk * 2 + (kF16 ? 0 : kBlocks * R * 4);
   const auto parts = [&](int batch) { return (batch + kWarps) * kTile * R * 4; };
-  const auto fits = [&](int room) { return (kMaxSmem - rings - room - p.x_rows * 64) / per_chunk; };
-  // All of a CTA's tiles in one batch and x whole if they fit; else the split
-  // with the fewest batches times panels.
+  // All of a CTA's tiles in one batch, x whole and three stages if they fit;
+  // else the split with the fewest batches times panels.
   int batch = 1, panel = 1, n_panels = 1;
   int64_t fewest = -1;
-  for (int64_t n_batches = 1; n_batches <= (per_cta > 1 ? per_cta : 1); ++n_batches) {
-    const int64_t tiles = ((per_cta > 1 ? per_cta : 1) + n_batches - 1) / n_batches;
-    if (tiles > 96) continue;
-    const int bt = static_cast<int>(tiles), sum_bytes = bt * kTile * R * 4;
-    int pn = fits(parts(bt)) >= p.chunks ? p.chunks : fits(parts(bt) + sum_bytes);
-    if (pn < 1) continue;
-    const int panels = p.chunks > 0 ? (p.chunks + pn - 1) / pn : 1;
-    if (fewest < 0 || n_batches * panels < fewest) {
-      fewest = n_batches * panels;
-      batch = bt;
-      n_panels = panels;
-      panel = p.chunks > 0 ? (p.chunks + panels - 1) / panels : 0;
+  for (int stages = 3; stages >= 2; --stages) {
+    const auto fits = [&](int room) {
+      return (kMaxSmem - kWarps * stages * kStage - room - p.x_rows * 64) / per_chunk;
+    };
+    for (int64_t n_batches = 1; n_batches <= (per_cta > 1 ? per_cta : 1) && n_batches <= 64; ++n_batches) {
+      const int64_t tiles = ((per_cta > 1 ? per_cta : 1) + n_batches - 1) / n_batches;
+      if (tiles > 96) continue;
+      const int bt = static_cast<int>(tiles), sum_bytes = bt * kTile * R * 4;
+      const int pn = fits(parts(bt)) >= p.chunks ? p.chunks : fits(parts(bt) + sum_bytes);
+      if (pn < 1 && p.chunks > 0) continue;
+      const int panels = p.chunks > 0 ? (p.chunks + pn - 1) / pn : 1;
+      if (fewest < 0 || n_batches * panels < fewest) {
+        fewest = n_batches * panels;
+        p.stages = stages;
+        batch = bt;
+        n_panels = panels;
+        panel = p.chunks > 0 ? (p.chunks + panels - 1) / panels : 0;
+      }
+      if (panels == 1) break;
     }
-    if (panels == 1 || n_batches > 64) break;
   }
+  const int rings = kWarps * p.stages * kStage;
   const int sums = n_panels > 1 ? batch * kTile * R * 4 : 0;
   p.batch = batch;
   p.panel = panel;
   p.x_pitch = panel * kChunk * 2 + 64;
-  const int smem = rings + p.x_rows * p.x_pitch + (kF16 ? 0 : panel * 4 * R * 4) +
+  const int smem = rings + p.x_rows * p.x_pitch + (kF16 ? 0 : panel * kBlocks * R * 4) +
                    parts(batch) + sums;
   static std::atomic<uint64_t> ready[3];  // devices on which each kernel may use kMaxSmem
   if (const cudaError_t e = allow_smem(kernel, kMaxSmem, ready[nt >> 1]); e != cudaSuccess) return e;
