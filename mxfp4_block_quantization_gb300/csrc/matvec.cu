@@ -24,13 +24,15 @@
 // codes (8 elements) meets the 16 bytes of x at the same place.  BF16 has
 // more exponents than a half: each 32-element block of a token is scaled by
 // the power of two that puts its largest element in [2^15, 2^16) (11 bits hold
-// BF16's 8 exactly down to 2^-29 of that; below, to 2^-40), and the power is
-// multiplied back in float32.
+// BF16's 8 exactly down to 2^-32 of that; below, to 2^-40), and the power is
+// multiplied back in float32.  Where a token's whole x lies within 2^32, one
+// power serves all of it and is multiplied back at the end.
 // The MXFP4 scale is a power of two of any size, so it is applied in float32
 // to the 32-element partial sums; the E4M3 scale times an E2M1 value has at
 // most 6 bits and fits a half, so NVFP4 weights are scaled before the product.
 #include <atomic>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -96,6 +98,11 @@ struct Shared {
   int32_t prefix[kThreads];  // units up to and with each thread's experts
   int32_t warp_sum[kWarps];
   int64_t x_row[32];         // x's rows of the unit's tokens (-1: none)
+  uint32_t x_max[32];        // BF16: largest finite and smallest nonzero magnitude of a token
+  uint32_t x_min[32];
+  float x_scale[32];         // what undoes a token's scaling (MXFP4: beyond `common`)
+  float common;              // MXFP4: what undoes the largest token's scaling
+  int by_token;              // whether a token's whole x has one power of two
 };
 
 // Expert and rows of unit u, from the prefix sums (same result in all lanes).
@@ -151,8 +158,6 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   constexpr int kScaleBytes = kNv ? 256 : 128;
   constexpr int kChunkKt = kChunk / (kNv ? 64 : 128);  // 4-column scale chunks of a stage
   constexpr int kStage = kStageCodes + kScaleBytes;
-  // more tokens, more registers: fewer blocks at once
-  constexpr int kUnroll = NT == 4 ? 1 : 4, kUnrollKt = NT == 1 ? 2 : 1;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -340,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   uint32_t out_at = ring;  // the stage to read
   int staged_unit = -1;
   UnitRows ur{0, 0, 0};
+  bool by_token = true;  // BF16: x scaled by token, not by block
   for (int at = first; at < last;) {
     const int unit = at / p.tiles, tile0 = at - unit * p.tiles;
     const int n_tiles = batch_tiles(at);
@@ -356,46 +362,104 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       // the sums of the batch before are read, and its x
       __syncthreads();
       if (unit != staged_unit || n_panels > 1) {
-        // stage x: 4 lanes to a 32-element block of a token, copied, then
-        // scaled to halves in place
-        if (unit != staged_unit) {
-          if (threadIdx.x < ur.n) {
-            int64_t src = ur.row0 + threadIdx.x;
-            if (p.row_index != nullptr) src = __ldg(p.row_index + src);
-            sh.x_row[threadIdx.x] = src >= 0 && src < p.src_rows ? src : -1;
-          }
-          __syncthreads();
+        // stage x: copied in 16-byte pieces, four to a 32-element block, then
+        // scaled to halves in place.  With fewer tokens than warps, several
+        // warps share a token.
+        if (threadIdx.x < ur.n) {
+          int64_t src = ur.row0 + threadIdx.x;
+          if (p.row_index != nullptr) src = __ldg(p.row_index + src);
+          sh.x_row[threadIdx.x] = src >= 0 && src < p.src_rows ? src : -1;
+          sh.x_max[threadIdx.x] = 0u;
+          sh.x_min[threadIdx.x] = 0xFFFFu;
         }
-        const int blocks = n * kBlocks, total_x = blocks * ur.n;
-        for (int w = threadIdx.x >> 2; w < total_x; w += kThreads / 4) {
-          const int tok = w / blocks, blk = w - tok * blocks;
-          const int k = (lo * kBlocks + blk) * 32 + c * 8;
+        __syncthreads();
+        const int pieces = n * kBlocks * 4;
+        const int sharing = max(kWarps / ur.n, 1), tokens_at_once = kWarps / sharing;
+        const int my_token = warp / sharing < tokens_at_once ? warp / sharing : ur.n;
+        const int my_piece = (warp % sharing) * 32 + lane;
+        for (int tok = my_token; tok < ur.n; tok += tokens_at_once) {
           const int64_t row = sh.x_row[tok];
-          const uint8_t* src = p.x + (row * p.ldx + k) * 2;
-          const bool take = row >= 0 && k < p.K && MXFP4_IN_BOUNDS(p, kDbgX, src, 16);
-          cp_async<16>(smem_u32(x_s + tok * p.x_pitch + blk * 64 + c * 16), take ? src : p.x, take ? 16 : 0);
+          const uint8_t* const src = p.x + ((row < 0 ? 0 : row) * p.ldx + lo * kChunk) * 2;
+          const int there = row < 0 ? 0 : (p.K - lo * kChunk) / 8;  // pieces that x has
+          const uint32_t to = smem_u32(x_s + tok * p.x_pitch);
+          for (int i = my_piece; i < pieces; i += sharing * 32) {
+            const bool take = i < there && MXFP4_IN_BOUNDS(p, kDbgX, src + i * 16, 16);
+            cp_async<16>(to + i * 16, take ? src + i * 16 : p.x, take ? 16 : 0);
+          }
         }
         cp_commit();
         cp_wait<0>();
         if constexpr (!kF16) {
-          // each lane has copied what it converts
-          for (int w = threadIdx.x >> 2; w < total_x; w += kThreads / 4) {
-            const int tok = w / blocks, blk = w - tok * blocks;
-            uint4* at = reinterpret_cast<uint4*>(x_s + tok * p.x_pitch + blk * 64 + c * 16);
-            const uint4 v = *at;
-            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-            uint32_t m = 0u, r[4];
+          // A lane converts what it copied.  With the sign bits set, the order of
+          // the patterns is that of the magnitudes; one less, zero is the largest.
+          for (int tok = my_token; tok < ur.n; tok += tokens_at_once) {
+            uint32_t most = 0x80008000u, least = 0xFFFFFFFFu;
+            for (int i = my_piece; i < pieces; i += sharing * 32) {
+              const uint4 v = *reinterpret_cast<const uint4*>(x_s + tok * p.x_pitch + i * 16);
+              const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m = max_finite_bf16x2(m, q[i]);
-            m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 1));
-            m = max(m, __shfl_xor_sync(0xFu << (lane & 28), m, 2));
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t m = q[k] | 0x80008000u;
+                most = __vmaxu2(most, m);
+                least = __vminu2(least, (m - 0x00010001u) ^ 0x80008000u);
+              }
+            }
+            most = max(most & 0x7FFFu, (most >> 16) & 0x7FFFu);
+            least = min(least & 0xFFFFu, least >> 16);
+            most = __reduce_max_sync(0xFFFFFFFFu, most);
+            least = __reduce_min_sync(0xFFFFFFFFu, least);
+            if (lane == 0) {
+              atomicMax(&sh.x_max[tok], most);
+              atomicMin(&sh.x_min[tok], least);
+            }
+          }
+          __syncthreads();
+          // One power of two for a token's whole (panel of) x if that loses
+          // nothing: all of it within 2^32; else one for each 32 elements.  For
+          // MXFP4, whose weights may be of any size, the largest token's goes
+          // into the weights' scales (so that the sums are of the result's size)
+          // and the tokens are within 2^8 of it.
+          if (warp == 0) {
+            const uint32_t most = sh.x_max[lane], least = sh.x_min[lane] + 1u;
+            const bool there = lane < ur.n && most != 0u;  // a token of zeros takes any scale
+            const uint32_t e_max = __reduce_max_sync(0xFFFFFFFFu, there ? max(most >> 7, 15u) : 15u);
+            const uint32_t e = there ? max(most >> 7, 15u) : e_max;
+            const bool near = most < 0x7F80u && max(least >> 7, 1u) + 32 >= most >> 7 && (kNv || e + 8 >= e_max);
             float inverse;
-            const float f = half_scale(m, inverse);
+            half_scale(kNv ? most : e_max << 7, inverse);
+            sh.x_scale[lane] = kNv ? inverse : __uint_as_float((127u + e - e_max) << 23);
+            const bool all = __all_sync(0xFFFFFFFFu, !there || near);
+            if (lane == 0) {
+              sh.by_token = all;
+              sh.common = inverse;
+            }
+          }
+          __syncthreads();
+          by_token = sh.by_token;
+          for (int tok = my_token; tok < ur.n; tok += tokens_at_once) {
+            float inverse_whole;
+            const float f_whole = half_scale(sh.x_max[tok], inverse_whole);
+            for (int base = my_piece - lane; base < pieces; base += sharing * 32) {  // pieces % 32 == 0
+              uint4* at = reinterpret_cast<uint4*>(x_s + tok * p.x_pitch + (base + lane) * 16);
+              const uint4 v = *at;
+              const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+              float f = f_whole;
+              if (!by_token) {
+                uint32_t m = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              r[i] = pack_f16x2(__uint_as_float(q[i] << 16) * f, __uint_as_float(q[i] & 0xFFFF0000u) * f);
-            *at = make_uint4(r[0], r[1], r[2], r[3]);
-            if (c == 0) xs_s[blk * R + tok] = inverse;
+                for (int k = 0; k < 4; ++k) m = max_finite_bf16x2(m, q[k]);
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+                float inverse;
+                f = half_scale(m, inverse);
+                if (c == 0) xs_s[((base + lane) >> 2) * R + tok] = inverse;
+              }
+              uint32_t r[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                r[k] = pack_f16x2(__uint_as_float(q[k] << 16) * f, __uint_as_float(q[k] & 0xFFFF0000u) * f);
+              *at = make_uint4(r[0], r[1], r[2], r[3]);
+            }
           }
         }
         __syncthreads();
@@ -416,95 +480,113 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
         float* q = part_s + ((tile + warp) * kTile + g) * R + 2 * c;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          *reinterpret_cast<float2*>(q + t * 8) = make_float2(acc[t][0], acc[t][1]);
-          *reinterpret_cast<float2*>(q + 8 * R + t * 8) = make_float2(acc[t][2], acc[t][3]);
+          float2 xs = make_float2(1.0f, 1.0f);
+          if (!kF16 && by_token) xs = *reinterpret_cast<const float2*>(&sh.x_scale[t * 8 + 2 * c]);
+          *reinterpret_cast<float2*>(q + t * 8) = make_float2(acc[t][0] * xs.x, acc[t][1] * xs.y);
+          *reinterpret_cast<float2*>(q + 8 * R + t * 8) = make_float2(acc[t][2] * xs.x, acc[t][3] * xs.y);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
         }
       };
-      for (int f = f0; f < f1; ++f) {
-        if (p.stages == 3) cp_wait<1>(); else cp_wait<0>();
-        __syncwarp();  // the copies of all lanes are in; the stage read last is free
-        issue();
-        const uint32_t st = out_at;
-        out_at += kStage;
-        if (out_at == ring_end) out_at = ring;
-        // scale words of rows g and g + 8
-        const uint32_t sa = st + kStageCodes + (g & 3) * 16 + (g >> 2) * 4;
-        float run[NT][4];  // FP16 x with NVFP4: sums of the whole stage
-        if constexpr (kNv && kF16) {
+      // the warp's share of the stages; x scaled by block needs a factor for each
+      auto multiply = [&](auto by_block) {
+        constexpr bool kByBlock = decltype(by_block)::value;
+        // more tokens, more registers: fewer 32-element blocks at once
+        constexpr int kUnroll = NT == 4 || kByBlock ? 1 : 4, kUnrollKt = NT == 1 && !kByBlock ? 2 : 1;
+        [[maybe_unused]] const float common = kF16 || kNv ? 1.0f : sh.common;
+        for (int f = f0; f < f1; ++f) {
+          if (p.stages == 3) cp_wait<1>(); else cp_wait<0>();
+          __syncwarp();  // the copies of all lanes are in; the stage read last is free
+          issue();
+          const uint32_t st = out_at;
+          out_at += kStage;
+          if (out_at == ring_end) out_at = ring;
+          // scale words of rows g and g + 8
+          const uint32_t sa = st + kStageCodes + (g & 3) * 16 + (g >> 2) * 4;
+          float run[NT][4];  // NVFP4: sums of the whole stage
+          if constexpr (kNv && !kByBlock) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) run[t][i] = 0.0f;
-        }
-        const uint32_t wa = st + g * kRowPitch + c * 4;
-        const uint32_t xc = ch * (kChunk * 2);
-        const uint32_t sx = smem_u32(xs_s) + (ch * kBlocks * R + 2 * c) * 4;
+              for (int i = 0; i < 4; ++i) run[t][i] = 0.0f;
+          }
+          const uint32_t wa = st + g * kRowPitch + c * 4;
+          const uint32_t xc = ch * (kChunk * 2);
+          const uint32_t sx = smem_u32(xs_s) + (ch * kBlocks * R + 2 * c) * 4;
 #pragma unroll kUnrollKt
-        for (int kt = 0; kt < kChunkKt; ++kt) {
-          const uint32_t sw0 = lds32(sa + kt * 64), sw1 = lds32(sa + kt * 64 + 8);
+          for (int kt = 0; kt < kChunkKt; ++kt) {
+            const uint32_t sw0 = lds32(sa + kt * 64), sw1 = lds32(sa + kt * 64 + 8);
 #pragma unroll kUnroll
-          for (int b4 = 0; b4 < kBlocks / kChunkKt; ++b4) {
-            const int b = kt * (kBlocks / kChunkKt) + b4;
-            uint32_t a0[4], a1[4];
-            decode_word(lds32(wa + b * 16), a0);
-            decode_word(lds32(wa + 8 * kRowPitch + b * 16), a1);
-            float ws0 = 1.0f, ws1 = 1.0f;
-            if constexpr (!kNv) {
-              const uint32_t w0 = e8m0x2_to_bf16x2(sw0 >> (16 * (b4 / 2)));
-              const uint32_t w1 = e8m0x2_to_bf16x2(sw1 >> (16 * (b4 / 2)));
-              ws0 = __uint_as_float(b4 & 1 ? w0 & 0xFFFF0000u : w0 << 16);
-              ws1 = __uint_as_float(b4 & 1 ? w1 & 0xFFFF0000u : w1 << 16);
-            } else {
-              // lanes 0, 1 hold the block's first 16 elements, lanes 2, 3 the rest
-              const uint32_t pick = (b4 * 2 + (c >> 1)) * 0x11u;  // that byte twice
-              const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(sw0, 0u, pick));
-              const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(sw1, 0u, pick));
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a0[i] = hmul2(a0[i], f0);
-                a1[i] = hmul2(a1[i], f1);
-              }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const uint4 xb = lds128(xa[t] + xc + b * 64);
-              if constexpr (kNv && kF16) {
-                mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
-                mma16816(run[t], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
+            for (int b4 = 0; b4 < kBlocks / kChunkKt; ++b4) {
+              const int b = kt * (kBlocks / kChunkKt) + b4;
+              uint32_t a0[4], a1[4];
+              decode_word(lds32(wa + b * 16), a0);
+              decode_word(lds32(wa + 8 * kRowPitch + b * 16), a1);
+              [[maybe_unused]] float ws0 = 1.0f, ws1 = 1.0f;
+              if constexpr (!kNv) {
+                const uint32_t w0 = e8m0x2_to_bf16x2(sw0 >> (16 * (b4 / 2)));
+                const uint32_t w1 = e8m0x2_to_bf16x2(sw1 >> (16 * (b4 / 2)));
+                ws0 = __uint_as_float(b4 & 1 ? w0 & 0xFFFF0000u : w0 << 16);
+                ws1 = __uint_as_float(b4 & 1 ? w1 & 0xFFFF0000u : w1 << 16);
+                if constexpr (!kF16 && !kByBlock) {
+                  ws0 *= common;
+                  ws1 *= common;
+                }
               } else {
-                float d[4];
-                mma16816_first(d, a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
-                mma16816(d, a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
-                float2 xs = make_float2(1.0f, 1.0f);
-                if constexpr (!kF16) xs = lds64f(sx + (b * R + t * 8) * 4);
-                if constexpr (kNv) {
-                  acc[t][0] = fmaf(d[0], xs.x, acc[t][0]);
-                  acc[t][1] = fmaf(d[1], xs.y, acc[t][1]);
-                  acc[t][2] = fmaf(d[2], xs.x, acc[t][2]);
-                  acc[t][3] = fmaf(d[3], xs.y, acc[t][3]);
+                // lanes 0, 1 hold the block's first 16 elements, lanes 2, 3 the rest
+                const uint32_t pick = (b4 * 2 + (c >> 1)) * 0x11u;  // that byte twice
+                const uint32_t f0 = e4m3x2_to_f16x2(__byte_perm(sw0, 0u, pick));
+                const uint32_t f1 = e4m3x2_to_f16x2(__byte_perm(sw1, 0u, pick));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  a0[i] = hmul2(a0[i], f0);
+                  a1[i] = hmul2(a1[i], f1);
+                }
+              }
+#pragma unroll
+              for (int t = 0; t < NT; ++t) {
+                const uint4 xb = lds128(xa[t] + xc + b * 64);
+                if constexpr (kNv && !kByBlock) {
+                  mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+                  mma16816(run[t], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
                 } else {
-                  acc[t][0] = fmaf(d[0], ws0 * xs.x, acc[t][0]);
-                  acc[t][1] = fmaf(d[1], ws0 * xs.y, acc[t][1]);
-                  acc[t][2] = fmaf(d[2], ws1 * xs.x, acc[t][2]);
-                  acc[t][3] = fmaf(d[3], ws1 * xs.y, acc[t][3]);
+                  float d[4];
+                  mma16816_first(d, a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
+                  mma16816(d, a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
+                  float2 xs = make_float2(1.0f, 1.0f);
+                  if constexpr (kByBlock) xs = lds64f(sx + (b * R + t * 8) * 4);
+                  if constexpr (kNv) {
+                    acc[t][0] = fmaf(d[0], xs.x, acc[t][0]);
+                    acc[t][1] = fmaf(d[1], xs.y, acc[t][1]);
+                    acc[t][2] = fmaf(d[2], xs.x, acc[t][2]);
+                    acc[t][3] = fmaf(d[3], xs.y, acc[t][3]);
+                  } else {
+                    acc[t][0] = fmaf(d[0], ws0 * xs.x, acc[t][0]);
+                    acc[t][1] = fmaf(d[1], ws0 * xs.y, acc[t][1]);
+                    acc[t][2] = fmaf(d[2], ws1 * xs.x, acc[t][2]);
+                    acc[t][3] = fmaf(d[3], ws1 * xs.y, acc[t][3]);
+                  }
                 }
               }
             }
           }
-        }
-        if constexpr (kNv && kF16) {
+          if constexpr (kNv && !kByBlock) {
 #pragma unroll
-          for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] += run[t][i];
+              for (int i = 0; i < 4; ++i) acc[t][i] += run[t][i];
+          }
+          if (++ch == n) {
+            flush();
+            ch = 0;
+            ++tile;
+          }
         }
-        if (++ch == n) {
-          flush();
-          ch = 0;
-          ++tile;
-        }
+      };
+      if (kF16 || by_token) {
+        multiply(std::false_type{});
+      } else {
+        multiply(std::true_type{});
       }
       if (ch != 0 && f1 > f0) flush();
       __syncthreads();
