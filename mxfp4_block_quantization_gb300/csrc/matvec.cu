@@ -80,6 +80,7 @@ struct MatvecParams {
   int32_t x_rows;     // token rows that x's shared memory holds
   int32_t x_pitch;    // bytes between them
   int32_t stages;     // of a warp's ring, 2 or 3
+  int32_t few;        // four stages to a warp at most: x is scaled by block at once
   int32_t y_f32;
   int32_t half_rows;  // rows of codes start at 8-byte (not 16-byte) boundaries
 #ifdef MXFP4_DEBUG_BOUNDS
@@ -340,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     }
     cp_commit();  // an empty group at the end keeps the count of groups
   };
-  for (int i = 1; i < p.stages; ++i) issue();
+  for (int i = 0; i < p.stages; ++i) issue();
 
   uint32_t out_at = ring;  // the stage to read
   int staged_unit = -1;
@@ -392,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
         if constexpr (!kF16) {
           // A lane converts what it copied.  With the sign bits set, the order of
           // the patterns is that of the magnitudes; one less, zero is the largest.
-          for (int tok = my_token; tok < ur.n; tok += tokens_at_once) {
+          by_token = !p.few;
+          for (int tok = p.few ? ur.n : my_token; tok < ur.n; tok += tokens_at_once) {
             uint32_t most = 0x80008000u, least = 0xFFFFFFFFu;
             for (int i = my_piece; i < pieces; i += sharing * 32) {
               const uint4 v = *reinterpret_cast<const uint4*>(x_s + tok * p.x_pitch + i * 16);
@@ -413,29 +415,31 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
               atomicMin(&sh.x_min[tok], least);
             }
           }
-          __syncthreads();
-          // One power of two for a token's whole (panel of) x if that loses
-          // nothing: all of it within 2^32; else one for each 32 elements.  For
-          // MXFP4, whose weights may be of any size, the largest token's goes
-          // into the weights' scales (so that the sums are of the result's size)
-          // and the tokens are within 2^8 of it.
-          if (warp == 0) {
-            const uint32_t most = sh.x_max[lane], least = sh.x_min[lane] + 1u;
-            const bool there = lane < ur.n && most != 0u;  // a token of zeros takes any scale
-            const uint32_t e_max = __reduce_max_sync(0xFFFFFFFFu, there ? max(most >> 7, 15u) : 15u);
-            const uint32_t e = there ? max(most >> 7, 15u) : e_max;
-            const bool near = most < 0x7F80u && max(least >> 7, 1u) + 32 >= most >> 7 && (kNv || e + 8 >= e_max);
-            float inverse;
-            half_scale(kNv ? most : e_max << 7, inverse);
-            sh.x_scale[lane] = kNv ? inverse : __uint_as_float((127u + e - e_max) << 23);
-            const bool all = __all_sync(0xFFFFFFFFu, !there || near);
-            if (lane == 0) {
-              sh.by_token = all;
-              sh.common = inverse;
+          if (!p.few) {
+            __syncthreads();
+            // One power of two for a token's whole (panel of) x if that loses
+            // nothing: all of it within 2^32; else one for each 32 elements.  For
+            // MXFP4, whose weights may be of any size, the largest token's goes
+            // into the weights' scales (so that the sums are of the result's size)
+            // and the tokens are within 2^8 of it.
+            if (warp == 0) {
+              const uint32_t most = sh.x_max[lane], least = sh.x_min[lane] + 1u;
+              const bool there = lane < ur.n && most != 0u;  // a token of zeros takes any scale
+              const uint32_t e_max = __reduce_max_sync(0xFFFFFFFFu, there ? max(most >> 7, 15u) : 15u);
+              const uint32_t e = there ? max(most >> 7, 15u) : e_max;
+              const bool near = most < 0x7F80u && max(least >> 7, 1u) + 32 >= most >> 7 && (kNv || e + 8 >= e_max);
+              float inverse;
+              half_scale(kNv ? most : e_max << 7, inverse);
+              sh.x_scale[lane] = kNv ? inverse : __uint_as_float((127u + e - e_max) << 23);
+              const bool all = __all_sync(0xFFFFFFFFu, !there || near);
+              if (lane == 0) {
+                sh.by_token = all;
+                sh.common = inverse;
+              }
             }
+            __syncthreads();
+            by_token = sh.by_token;
           }
-          __syncthreads();
-          by_token = sh.by_token;
           for (int tok = my_token; tok < ur.n; tok += tokens_at_once) {
             float inverse_whole;
             const float f_whole = half_scale(sh.x_max[tok], inverse_whole);
@@ -491,18 +495,23 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       // the warp's share of the stages; x scaled by block needs a factor for each
       auto multiply = [&](auto by_block) {
         constexpr bool kByBlock = decltype(by_block)::value;
-        // more tokens, more registers: fewer 32-element blocks at once
-        constexpr int kUnroll = NT == 4 || kByBlock ? 1 : 4, kUnrollKt = NT == 1 && !kByBlock ? 2 : 1;
+        // The last kHold of a stage's scale chunks, with their codes, are taken
+        // to registers at once, so that the next copy into the stage runs beside
+        // their products: as many as the tokens' registers leave room for.
+        constexpr int kHold = NT == 4 || kByBlock ? 0 : NT == 2 && !kNv ? 1 : kChunkKt;
+        constexpr int kPerKt = kBlocks / kChunkKt;  // 32-element blocks of a scale chunk
+        constexpr int kUnroll = kHold > 0 ? kPerKt : 1, kUnrollKt = kHold > 0 ? kChunkKt : 1;
         [[maybe_unused]] const float common = kF16 || kNv ? 1.0f : sh.common;
         for (int f = f0; f < f1; ++f) {
-          if (p.stages == 3) cp_wait<1>(); else cp_wait<0>();
-          __syncwarp();  // the copies of all lanes are in; the stage read last is free
-          issue();
+          if (p.stages == 3) cp_wait<2>(); else cp_wait<1>();
+          __syncwarp();  // the copies of all lanes are in
           const uint32_t st = out_at;
           out_at += kStage;
           if (out_at == ring_end) out_at = ring;
+          const uint32_t wa = st + g * kRowPitch + c * 4;
           // scale words of rows g and g + 8
           const uint32_t sa = st + kStageCodes + (g & 3) * 16 + (g >> 2) * 4;
+          [[maybe_unused]] uint32_t words[2][kHold * kPerKt + 1], scale_words[2][kHold + 1];
           float run[NT][4];  // NVFP4: sums of the whole stage
           if constexpr (kNv && !kByBlock) {
 #pragma unroll
@@ -510,18 +519,32 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
 #pragma unroll
               for (int i = 0; i < 4; ++i) run[t][i] = 0.0f;
           }
-          const uint32_t wa = st + g * kRowPitch + c * 4;
           const uint32_t xc = ch * (kChunk * 2);
           const uint32_t sx = smem_u32(xs_s) + (ch * kBlocks * R + 2 * c) * 4;
 #pragma unroll kUnrollKt
           for (int kt = 0; kt < kChunkKt; ++kt) {
-            const uint32_t sw0 = lds32(sa + kt * 64), sw1 = lds32(sa + kt * 64 + 8);
+            constexpr int kFree = kChunkKt - kHold;
+            if (kHold > 0 && kt == kFree) {
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int k = 0; k < kHold * kPerKt; ++k)
+                  words[r][k] = lds32(wa + r * 8 * kRowPitch + (kFree * kPerKt + k) * 16);
+#pragma unroll
+                for (int k = 0; k < kHold; ++k) scale_words[r][k] = lds32(sa + r * 8 + (kFree + k) * 64);
+              }
+              __syncwarp();  // the stage is read
+              issue();
+            }
+            const bool held = kHold > 0 && kt >= kFree;
+            const uint32_t sw0 = held ? scale_words[0][kt - kFree] : lds32(sa + kt * 64);
+            const uint32_t sw1 = held ? scale_words[1][kt - kFree] : lds32(sa + kt * 64 + 8);
 #pragma unroll kUnroll
-            for (int b4 = 0; b4 < kBlocks / kChunkKt; ++b4) {
-              const int b = kt * (kBlocks / kChunkKt) + b4;
+            for (int b4 = 0; b4 < kPerKt; ++b4) {
+              const int b = kt * kPerKt + b4;
               uint32_t a0[4], a1[4];
-              decode_word(lds32(wa + b * 16), a0);
-              decode_word(lds32(wa + 8 * kRowPitch + b * 16), a1);
+              decode_word(held ? words[0][b - kFree * kPerKt] : lds32(wa + b * 16), a0);
+              decode_word(held ? words[1][b - kFree * kPerKt] : lds32(wa + 8 * kRowPitch + b * 16), a1);
               [[maybe_unused]] float ws0 = 1.0f, ws1 = 1.0f;
               if constexpr (!kNv) {
                 const uint32_t w0 = e8m0x2_to_bf16x2(sw0 >> (16 * (b4 / 2)));
@@ -575,6 +598,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
             for (int t = 0; t < NT; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i) acc[t][i] += run[t][i];
+          }
+          if constexpr (kHold == 0) {
+            __syncwarp();  // the stage is read
+            issue();
           }
           if (++ch == n) {
             flush();
@@ -686,6 +713,7 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
       if (panels == 1) break;
     }
   }
+  p.few = per_cta * p.chunks <= 4 * kWarps;
   const int rings = kWarps * p.stages * kStage;
   const int sums = n_panels > 1 ? batch * kTile * R * 4 : 0;
   p.batch = batch;
