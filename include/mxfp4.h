@@ -597,7 +597,7 @@ int mxfp4_dequantize_nvfp4(const uint8_t* codes, const uint8_t* scales,
  *
  * x           BF16 [num_tokens, K], row stride ldx elements (ldx >= K,
  *             ldx % 8 == 0), 16-byte aligned; num_tokens may be any size, the
- *             call is made for few (weights are read once per 32 tokens).
+ *             call is made for few (weights are read once per 16 tokens).
  *             Inside a 32-element block of x, a value more than 2^39 below the
  *             block's largest is rounded to a multiple of 2^-40 of it.
  * codes       [N, K/2] packed E2M1 codes as mxfp4_quantize writes them,

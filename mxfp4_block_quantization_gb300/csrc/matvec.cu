@@ -53,6 +53,12 @@ constexpr int kBlocks = kChunk / 32;
 // fragment's words come from then lie in different banks.
 constexpr int kRowPitch = 144;
 constexpr int kStageCodes = kTile * kRowPitch;
+// A part of a tile's sums: [token][16 rows], the quads of rows (one 16-byte
+// load) exchanged by token, so that a fragment's stores meet fewer banks twice.
+__device__ __forceinline__ int part_at(int token, int quad) {
+  return token * kTile + ((quad ^ (token >> 1 & 3)) << 2);
+}
+constexpr int kMaxBatch = 96;  // tiles of a batch
 
 struct MatvecParams {
   const uint8_t* __restrict__ x;
@@ -82,6 +88,7 @@ struct MatvecParams {
   int32_t stages;     // of a warp's ring, 2 or 3
   int32_t few;        // four stages to a warp at most: x is scaled by block at once
   int32_t y_f32;
+  int32_t y_quads;    // four elements of y, from a multiple of four, are aligned together
   int32_t half_rows;  // rows of codes start at 8-byte (not 16-byte) boundaries
 #ifdef MXFP4_DEBUG_BOUNDS
   DebugRanges dbg;
@@ -98,11 +105,12 @@ struct UnitRows {
 struct Shared {
   int32_t prefix[kThreads];  // units up to and with each thread's experts
   int32_t warp_sum[kWarps];
-  int64_t x_row[32];         // x's rows of the unit's tokens (-1: none)
-  uint32_t x_max[32];        // BF16: largest finite and smallest nonzero magnitude of a token
-  uint32_t x_min[32];
-  float x_scale[32];         // what undoes a token's scaling (MXFP4: beyond `common`)
+  int64_t x_row[16];         // x's rows of the unit's tokens (-1: none)
+  uint32_t x_max[16];        // BF16: largest finite and smallest nonzero magnitude of a token
+  uint32_t x_min[16];
+  float x_scale[16];         // what undoes a token's scaling (MXFP4: beyond `common`)
   float common;              // MXFP4: what undoes the largest token's scaling
+  uint8_t tile_warps[kMaxBatch][2];  // the first and last warp with a part of each tile
   int by_token;              // whether a token's whole x has one power of two
 };
 
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   uint8_t* const x_s = smem + kWarps * ring_bytes;
   float* const xs_s = reinterpret_cast<float*>(x_s + p.x_rows * p.x_pitch);
   float* const part_s = xs_s + (kF16 ? 0 : p.panel * kBlocks * R);
-  float* const sum_s = part_s + (p.batch + kWarps) * kTile * R;
+  float* const sum_s = part_s + (p.batch + kWarps) * R * kTile;
 
   pdl_wait();
   pdl_release();
@@ -423,14 +431,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
             // into the weights' scales (so that the sums are of the result's size)
             // and the tokens are within 2^8 of it.
             if (warp == 0) {
-              const uint32_t most = sh.x_max[lane], least = sh.x_min[lane] + 1u;
+              const uint32_t most = sh.x_max[lane & 15], least = sh.x_min[lane & 15] + 1u;
               const bool there = lane < ur.n && most != 0u;  // a token of zeros takes any scale
               const uint32_t e_max = __reduce_max_sync(0xFFFFFFFFu, there ? max(most >> 7, 15u) : 15u);
               const uint32_t e = there ? max(most >> 7, 15u) : e_max;
               const bool near = most < 0x7F80u && max(least >> 7, 1u) + 32 >= most >> 7 && (kNv || e + 8 >= e_max);
               float inverse;
               half_scale(kNv ? most : e_max << 7, inverse);
-              sh.x_scale[lane] = kNv ? inverse : __uint_as_float((127u + e - e_max) << 23);
+              if (lane < 16) sh.x_scale[lane] = kNv ? inverse : __uint_as_float((127u + e - e_max) << 23);
               const bool all = __all_sync(0xFFFFFFFFu, !there || near);
               if (lane == 0) {
                 sh.by_token = all;
@@ -481,26 +489,31 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       // A warp's part of a tile's sums has slot tile + warp: the shares are
       // consecutive, so no two parts have the same slot.
       auto flush = [&]() {
-        float* q = part_s + ((tile + warp) * kTile + g) * R + 2 * c;
+        float* const q = part_s + (tile + warp) * R * kTile + (g & 3);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
+          if (t > 0 && t * 8 >= ur.n) break;
           float2 xs = make_float2(1.0f, 1.0f);
           if (!kF16 && by_token) xs = *reinterpret_cast<const float2*>(&sh.x_scale[t * 8 + 2 * c]);
-          *reinterpret_cast<float2*>(q + t * 8) = make_float2(acc[t][0] * xs.x, acc[t][1] * xs.y);
-          *reinterpret_cast<float2*>(q + 8 * R + t * 8) = make_float2(acc[t][2] * xs.x, acc[t][3] * xs.y);
+          const int lo = part_at(t * 8 + 2 * c, g >> 2), hi = part_at(t * 8 + 2 * c, 2 + (g >> 2));
+          q[lo] = acc[t][0] * xs.x;
+          q[lo + kTile] = acc[t][1] * xs.y;
+          q[hi] = acc[t][2] * xs.x;
+          q[hi + kTile] = acc[t][3] * xs.y;
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
         }
       };
       // the warp's share of the stages; x scaled by block needs a factor for each
-      auto multiply = [&](auto by_block) {
+      auto multiply = [&](auto by_block, auto columns) {
         constexpr bool kByBlock = decltype(by_block)::value;
+        constexpr int kCols = decltype(columns)::value;  // blocks of 8 tokens
         // The last kHold of a stage's scale chunks, with their codes, are taken
         // to registers at once, so that the next copy into the stage runs beside
         // their products: as many as the tokens' registers leave room for.
-        constexpr int kHold = NT == 4 || kByBlock ? 0 : NT == 2 && !kNv ? 1 : kChunkKt;
+        constexpr int kHold = kByBlock ? 0 : kCols == 2 && !kNv ? (kF16 ? 1 : 0) : kChunkKt;
         constexpr int kPerKt = kBlocks / kChunkKt;  // 32-element blocks of a scale chunk
-        constexpr int kUnroll = kHold > 0 ? kPerKt : 1, kUnrollKt = kHold > 0 ? kChunkKt : 1;
+        constexpr int kUnroll = kByBlock ? 1 : kPerKt, kUnrollKt = kHold > 0 ? kChunkKt : 1;
         [[maybe_unused]] const float common = kF16 || kNv ? 1.0f : sh.common;
         for (int f = f0; f < f1; ++f) {
           if (p.stages == 3) cp_wait<2>(); else cp_wait<1>();
@@ -512,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           // scale words of rows g and g + 8
           const uint32_t sa = st + kStageCodes + (g & 3) * 16 + (g >> 2) * 4;
           [[maybe_unused]] uint32_t words[2][kHold * kPerKt + 1], scale_words[2][kHold + 1];
-          float run[NT][4];  // NVFP4: sums of the whole stage
+          float run[kCols][4];  // NVFP4: sums of the whole stage
           if constexpr (kNv && !kByBlock) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < kCols; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i) run[t][i] = 0.0f;
           }
@@ -567,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
                 }
               }
 #pragma unroll
-              for (int t = 0; t < NT; ++t) {
+              for (int t = 0; t < kCols; ++t) {
                 const uint4 xb = lds128(xa[t] + xc + b * 64);
                 if constexpr (kNv && !kByBlock) {
                   mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
@@ -595,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           }
           if constexpr (kNv && !kByBlock) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < kCols; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i) acc[t][i] += run[t][i];
           }
@@ -610,24 +623,30 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           }
         }
       };
-      if (kF16 || by_token) {
-        multiply(std::false_type{});
+      if (!kF16 && !by_token) {
+        multiply(std::true_type{}, std::integral_constant<int, NT>{});
+      } else if (NT == 2 && ur.n <= 8) {  // one block of columns is enough
+        multiply(std::false_type{}, std::integral_constant<int, 1>{});
       } else {
-        multiply(std::true_type{});
+        multiply(std::false_type{}, std::integral_constant<int, NT>{});
       }
       if (ch != 0 && f1 > f0) flush();
+      // the warps whose shares [total * w / 16, total * (w + 1) / 16) meet each tile's stages
+      if (threadIdx.x < n_tiles && total > 0) {
+        sh.tile_warps[threadIdx.x][0] = share_of(threadIdx.x * n, total);
+        sh.tile_warps[threadIdx.x][1] = share_of(threadIdx.x * n + n - 1, total);
+      }
       __syncthreads();
 
       // every output: the parts of its tile in the warps' order, after those
-      // of the panels before
+      // of the panels before; a thread has four rows (consecutive in y) of a token
       const bool done = panel + 1 >= n_panels;
       const float gs = kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + ur.e, 4)
                            ? __ldg(p.global_scales + ur.e)
                            : 1.0f;
-      const int quads = (ur.n + 3) >> 2;  // of tokens
-      for (int i = threadIdx.x; i < n_tiles * kTile * quads; i += kThreads) {
-        const int r = i % kTile, rest = i / kTile;
-        const int tl = rest / quads, t = (rest - tl * quads) * 4;
+      for (int i = threadIdx.x; i < n_tiles * 4 * ur.n; i += kThreads) {
+        const int rest = i / n_tiles, tl = i - rest * n_tiles, quad = rest & 3, t = rest >> 2;
+        const int at_row = part_at(t, quad);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         auto add = [&](const float* q) {
           const float4 u = *reinterpret_cast<const float4*>(q);
@@ -637,33 +656,41 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           v.w += u.w;
         };
         if (total > 0) {
-          // the warps whose shares [total * w / 16, total * (w + 1) / 16) meet this tile's stages
-          const int w0 = share_of(tl * n, total), w1 = share_of(tl * n + n - 1, total);
-          for (int w = w0; w <= w1; ++w)
-            if (total * w / kWarps < total * (w + 1) / kWarps) add(part_s + ((tl + w) * kTile + r) * R + t);
+          const int w1 = sh.tile_warps[tl][1];
+          for (int w = sh.tile_warps[tl][0]; w <= w1; ++w)
+            if (total >= kWarps || total * w / kWarps < total * (w + 1) / kWarps)
+              add(part_s + (tl + w) * R * kTile + at_row);
         }
-        float* before = sum_s + (tl * kTile + r) * R + t;
+        float* before = sum_s + tl * R * kTile + at_row;
         if (panel > 0) add(before);
         if (!done) {
           *reinterpret_cast<float4*>(before) = v;
           continue;
         }
-        const int64_t row = static_cast<int64_t>((tile0 + tl) >> 3) * 128 + ((tile0 + tl) & 7) * 4 +
-                            32 * (r >> 2) + (r & 3);
-        if (row >= p.N) continue;
+        const int row = ((tile0 + tl) >> 3) * 128 + ((tile0 + tl) & 7) * 4 + 32 * quad;
+        const int left = p.N - row;
+        if (left <= 0) continue;
+        if constexpr (kNv) v = make_float4(v.x / gs, v.y / gs, v.z / gs, v.w / gs);
+        const int64_t to = (static_cast<int64_t>(ur.row0) + t) * p.ldy + row;
         const float out[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (t + j >= ur.n) break;
-          const float o = kNv ? out[j] / gs : out[j];
-          const int64_t to = (static_cast<int64_t>(ur.row0) + t + j) * p.ldy + row;
-          if (p.y_f32) {
-            float* y = reinterpret_cast<float*>(p.y) + to;
-            if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = o;
+        if (p.y_f32) {
+          float* y = reinterpret_cast<float*>(p.y) + to;
+          if (p.y_quads && left >= 4 && MXFP4_IN_BOUNDS(p, kDbgY, y, 16)) {
+            *reinterpret_cast<float4*>(y) = v;
           } else {
-            uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + to;
-            if (MXFP4_IN_BOUNDS(p, kDbgY, y, 2))
-              *y = kF16 ? __half_as_ushort(__float2half_rn(o)) : static_cast<uint16_t>(cvt_bf16x2(o, 0.0f));
+            for (int j = 0; j < 4 && j < left; ++j)
+              if (MXFP4_IN_BOUNDS(p, kDbgY, y + j, 4)) y[j] = out[j];
+          }
+        } else {
+          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + to;
+          const uint2 h = kF16 ? make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w))
+                               : make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
+          if (p.y_quads && left >= 4 && MXFP4_IN_BOUNDS(p, kDbgY, y, 8)) {
+            *reinterpret_cast<uint2*>(y) = h;
+          } else {
+            for (int j = 0; j < 4 && j < left; ++j)
+              if (MXFP4_IN_BOUNDS(p, kDbgY, y + j, 2))
+                y[j] = static_cast<uint16_t>((j < 2 ? h.x : h.y) >> (16 * (j & 1)));
           }
         }
       }
@@ -675,9 +702,7 @@ constexpr int kMaxSmem = 227 * 1024 - 3 * 1024;  // dynamic; the rest is the sta
 
 template <bool kNv, bool kF16>
 cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStream_t stream) {
-  const auto kernel = nt == 1   ? matvec_kernel<kNv, kF16, 1>
-                      : nt == 2 ? matvec_kernel<kNv, kF16, 2>
-                                : matvec_kernel<kNv, kF16, 4>;
+  const auto kernel = nt == 1 ? matvec_kernel<kNv, kF16, 1> : matvec_kernel<kNv, kF16, 2>;
   const int R = 8 * nt;
   const int kStage = kStageCodes + (kNv ? 256 : 128);
   const int sms = sm_count();
@@ -687,7 +712,7 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
   // their sums' parts need room that x's panels need too.
   const int64_t per_cta = (expected_units * p.tiles + sms - 1) / sms;
   const int per_chunk = p.x_rows * kChunk * 2 + (kF16 ? 0 : kBlocks * R * 4);
-  const auto parts = [&](int batch) { return (batch + kWarps) * kTile * R * 4; };
+  const auto parts = [&](int batch) { return (batch + kWarps) * R * kTile * 4; };
   // All of a CTA's tiles in one batch, x whole and three stages if they fit;
   // else the split with the fewest batches times panels.
   int batch = 1, panel = 1, n_panels = 1;
@@ -698,8 +723,8 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
     };
     for (int64_t n_batches = 1; n_batches <= (per_cta > 1 ? per_cta : 1) && n_batches <= 64; ++n_batches) {
       const int64_t tiles = ((per_cta > 1 ? per_cta : 1) + n_batches - 1) / n_batches;
-      if (tiles > 96) continue;
-      const int bt = static_cast<int>(tiles), sum_bytes = bt * kTile * R * 4;
+      if (tiles > kMaxBatch) continue;
+      const int bt = static_cast<int>(tiles), sum_bytes = bt * R * kTile * 4;
       const int pn = fits(parts(bt)) >= p.chunks ? p.chunks : fits(parts(bt) + sum_bytes);
       if (pn < 1 && p.chunks > 0) continue;
       const int panels = p.chunks > 0 ? (p.chunks + pn - 1) / pn : 1;
@@ -715,14 +740,14 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
   }
   p.few = per_cta * p.chunks <= 4 * kWarps;
   const int rings = kWarps * p.stages * kStage;
-  const int sums = n_panels > 1 ? batch * kTile * R * 4 : 0;
+  const int sums = n_panels > 1 ? batch * R * kTile * 4 : 0;
   p.batch = batch;
   p.panel = panel;
   p.x_pitch = panel * kChunk * 2 + 64;
   const int smem = rings + p.x_rows * p.x_pitch + (kF16 ? 0 : panel * kBlocks * R * 4) +
                    parts(batch) + sums;
-  static std::atomic<uint64_t> ready[3];  // devices on which each kernel may use kMaxSmem
-  if (const cudaError_t e = allow_smem(kernel, kMaxSmem, ready[nt >> 1]); e != cudaSuccess) return e;
+  static std::atomic<uint64_t> ready[2];  // devices on which each kernel may use kMaxSmem
+  if (const cudaError_t e = allow_smem(kernel, kMaxSmem, ready[nt - 1]); e != cudaSuccess) return e;
   // a CTA per SM, each with its share of the tiles (the experts that have
   // rows are known on the device alone: rows bound their number)
   const int64_t most = (p.offsets ? p.rows : expected_units) * static_cast<int64_t>(p.tiles);
@@ -755,6 +780,8 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
   p.expert_codes = a.N * (a.K / 2);
   p.expert_scales = (a.N + 127) / 128 * p.nKT * kChunkBytes;
   p.y_f32 = a.y_f32;
+  const int64_t quad = a.y_f32 ? 16 : 8;  // bytes of four elements of y
+  p.y_quads = reinterpret_cast<uintptr_t>(a.y) % quad == 0 && a.ldy % 4 == 0;
   p.half_rows = a.K % 32 != 0;
 #ifdef MXFP4_DEBUG_BOUNDS
   debug_range(p.dbg, kDbgX, a.x, a.src_rows > 0 ? ((a.src_rows - 1) * a.ldx + a.K) * 2 : 0);
@@ -763,10 +790,10 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
   debug_range(p.dbg, kDbgGlobal, a.global_scales, a.nvfp4 ? a.E * 4 : 0);
   debug_range(p.dbg, kDbgY, a.y, a.rows > 0 ? ((a.rows - 1) * a.ldy + a.N) * (a.y_f32 ? 4 : 2) : 0);
 #endif
-  // tokens per unit: 8, 16 or 32 columns of the tensor-core product
+  // Tokens per unit: 8 or 16 columns of the tensor-core product (more would
+  // leave x no room); segments whose average is near 8 have some longer.
   const int64_t avg = a.offsets ? (a.rows + a.E - 1) / (a.E > 0 ? a.E : 1) : a.rows;
-  int nt = avg <= (a.offsets ? 6 : 8) ? 1 : avg <= (a.offsets ? 12 : 16) ? 2 : 4;
-  if (nt == 4 && a.K > 1024) nt = 2;
+  const int nt = avg <= (a.offsets ? 6 : 8) ? 1 : 2;
   const int64_t used = a.offsets ? (a.rows < a.E ? a.rows : a.E) : 1;  // segments with rows, about
   const int64_t units = a.offsets ? used : (a.rows + 8 * nt - 1) / (8 * nt);
   if (a.nvfp4)
