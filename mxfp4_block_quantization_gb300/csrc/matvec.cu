@@ -53,12 +53,8 @@ constexpr int kBlocks = kChunk / 32;
 // fragment's words come from then lie in different banks.
 constexpr int kRowPitch = 144;
 constexpr int kStageCodes = kTile * kRowPitch;
-// A part of a tile's sums: [token][16 rows], the quads of rows (one 16-byte
-// load) exchanged by token, so that a fragment's stores meet fewer banks twice.
-__device__ __forceinline__ int part_at(int token, int quad) {
-  return token * kTile + ((quad ^ (token >> 1 & 3)) << 2);
-}
-constexpr int kMaxBatch = 96;  // tiles of a batch
+constexpr int kMaxUnits = 16;  // of a phase
+constexpr int kMaxRows = 64;   // of x, of a phase
 
 struct MatvecParams {
   const uint8_t* __restrict__ x;
@@ -82,13 +78,13 @@ struct MatvecParams {
   int32_t tiles;      // 16-row tiles of N (8 per 128 rows)
   int32_t chunks;     // 256-element chunks of K
   int32_t panel;      // chunks of x staged at a time
-  int32_t batch;      // tiles that the CTA's warps take together
+  int32_t panels;
+  int32_t batch;      // tiles of a phase at most, with several panels
   int32_t x_rows;     // token rows that x's shared memory holds
   int32_t x_pitch;    // bytes between them
   int32_t stages;     // of a warp's ring, 2 or 3
   int32_t few;        // four stages to a warp at most: x is scaled by block at once
   int32_t y_f32;
-  int32_t y_quads;    // four elements of y, from a multiple of four, are aligned together
   int32_t half_rows;  // rows of codes start at 8-byte (not 16-byte) boundaries
 #ifdef MXFP4_DEBUG_BOUNDS
   DebugRanges dbg;
@@ -97,21 +93,25 @@ struct MatvecParams {
 
 enum : int { kDbgX = 0, kDbgCodes, kDbgScales, kDbgGlobal, kDbgY, kDbgIndex, kDbgOffsets };
 
-// The rows of one unit of work: up to 8*NT consecutive rows of one segment.
+// The rows of one unit of work: up to 8*NT consecutive rows of one segment;
+// `x`: the first of its rows of x's shared memory.
 struct UnitRows {
-  int e, row0, n;
+  int e, row0, n, x;
 };
 
 struct Shared {
   int32_t prefix[kThreads];  // units up to and with each thread's experts
   int32_t warp_sum[kWarps];
-  int64_t x_row[16];         // x's rows of the unit's tokens (-1: none)
-  uint32_t x_max[16];        // BF16: largest finite and smallest nonzero magnitude of a token
-  uint32_t x_min[16];
-  float x_scale[16];         // what undoes a token's scaling (MXFP4: beyond `common`)
-  float common;              // MXFP4: what undoes the largest token's scaling
-  uint8_t tile_warps[kMaxBatch][2];  // the first and last warp with a part of each tile
-  int by_token;              // whether a token's whole x has one power of two
+  UnitRows unit[kMaxUnits];  // of the phase
+  int32_t n_units, n_rows;
+  int64_t x_row[kMaxRows];   // x's row of each staged row (-1: none)
+  int32_t x_unit[kMaxRows];  // and its unit (-1: padding)
+  uint32_t x_max[kMaxRows];  // BF16: largest magnitude of a row, and smallest but zero, less one
+  uint32_t x_min[kMaxRows];
+  uint32_t unit_max[kMaxUnits];  // MXFP4: largest exponent of a unit's rows
+  float x_scale[kMaxRows];   // what undoes a row's scaling (MXFP4: beyond the unit's)
+  float unit_scale[kMaxUnits];
+  int32_t far;               // BF16: some row needs a power of two for each block
 };
 
 // Expert and rows of unit u, from the prefix sums (same result in all lanes).
@@ -119,6 +119,7 @@ template <int NT>
 __device__ __forceinline__ UnitRows find_unit(const MatvecParams& p, const Shared& s, int u) {
   constexpr int R = 8 * NT;
   UnitRows r;
+  r.x = 0;
   if (p.offsets == nullptr) {
     r.e = 0;
     r.row0 = u * R;
@@ -149,13 +150,10 @@ __device__ __forceinline__ UnitRows find_unit(const MatvecParams& p, const Share
 // The warp w whose share [total * w / kWarps, total * (w + 1) / kWarps) holds f.
 __device__ __forceinline__ int share_of(int f, int total) { return ((f + 1) * kWarps - 1) / total; }
 
-// Where a warp's copies stand: the batch of tiles, the panel of x, the chunks
-// left in the warp's share of them, and what its lanes copy next.
+// Where a warp's copies stand in its share of a phase, and what its lanes copy next.
 struct Cursor {
-  int at;                    // first tile of the batch, over all units
-  int panel, left;           // stages left in this batch and panel
-  int tile, chunk, end;      // the tile in its unit, the chunk, and the panel's end
-  int unit, e;
+  int panel, f;              // the panel of x; where the run after this one starts
+  int chunk, left;           // the next chunk, and the chunks left of this run (one tile's)
   int quarters;              // of the tile's four 32-row quarters, those in which this lane's row is in N
   const uint8_t* row;        // this lane's piece of its row of the first quarter, chunk 0
   const uint8_t* scale;
@@ -171,13 +169,13 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   __shared__ Shared sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  // shared memory: rings | x halves | x block scales | parts of sums | sums of panels
+  // shared memory: rings | x halves | x block scales | parts of sums
   const int ring_bytes = p.stages * kStage;
   const uint32_t ring = smem_u32(smem) + warp * ring_bytes;
   uint8_t* const x_s = smem + kWarps * ring_bytes;
+  static_assert(sizeof(Shared) <= 5 * 1024, "kMaxSmem leaves this much");
   float* const xs_s = reinterpret_cast<float*>(x_s + p.x_rows * p.x_pitch);
-  float* const part_s = xs_s + (kF16 ? 0 : p.panel * kBlocks * R);
-  float* const sum_s = part_s + (p.batch + kWarps) * R * kTile;
+  float4* const part_s = reinterpret_cast<float4*>(xs_s + (kF16 ? 0 : p.panel * kBlocks * p.x_rows));
 
   pdl_wait();
   pdl_release();
@@ -230,182 +228,209 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     __syncthreads();
   }
 
-  // This CTA's tiles, consecutive over the units.  They are taken in batches
-  // of one unit's tiles; a batch's tiles times chunks are one sequence of
-  // stages, of which each warp has an even share: a tile's sum is then split
-  // over one warp or several, whatever the sizes.
+  // This CTA's tiles, consecutive over the units, in phases: as many units as x
+  // has room for (one, with x in panels).  A phase's tiles times chunks are one
+  // sequence of stages of which each warp has an even share, whatever the
+  // sizes; a tile whose stages are shared is summed over its warps at the end.
   const int64_t all = static_cast<int64_t>(units) * p.tiles;
-  const int first = static_cast<int>(all * blockIdx.x / gridDim.x);
+  int at = static_cast<int>(all * blockIdx.x / gridDim.x);
   const int last = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x);
-  if (first >= last) return;
-  const int n_panels = p.chunks > 0 ? (p.chunks + p.panel - 1) / p.panel : 0;
-  auto batch_tiles = [&](int at) {  // of the batch that starts at tile `at`
-    return min(min(p.tiles - at % p.tiles, p.batch), last - at);
-  };
-
-  // Row i of a tile is row tile_base + 32 * (i / 4) + i % 4 of the weights.  A
-  // copy takes the four rows of a quarter, eight lanes to a row's 128 bytes.
+  const int n = p.panel;  // chunks of a tile in a panel
   const int tail = p.K % kChunk != 0 ? p.chunks - 1 : -1;  // the chunk that ends before its stage
-  const int copy_row = lane >> 3, copy_at = (lane & 7) * 16;
-  const int64_t quarter = 32 * static_cast<int64_t>(p.K >> 1);  // bytes of 32 rows
-  auto open_tile = [&](Cursor& u) {
-    const int base = (u.tile >> 3) * 128 + (u.tile & 7) * 4 + copy_row;
-    u.quarters = base < p.N ? min(4, (p.N - base + 31) >> 5) : 0;
-    u.row = p.codes + u.e * p.expert_codes + (u.quarters ? base : 0) * static_cast<int64_t>(p.K >> 1) + copy_at;
-    u.scale = p.scales + u.e * p.expert_scales + (u.tile & 7) * 64 +
-              (static_cast<int64_t>(u.tile >> 3) * p.nKT + (lane >> 2)) * kChunkBytes + (lane & 3) * 16;
-  };
-  auto open_panel = [&](Cursor& u) {
-    const int unit = u.at / p.tiles;
-    if (unit != u.unit) {
-      u.unit = unit;
-      u.e = p.offsets == nullptr ? 0 : find_unit<NT>(p, sh, unit).e;
-    }
-    const int lo = u.panel * p.panel, n = min(p.panel, p.chunks - lo);
-    const int total = batch_tiles(u.at) * n;
-    const int f0 = total * warp / kWarps;
-    u.left = total * (warp + 1) / kWarps - f0;
-    u.tile = u.at - unit * p.tiles + f0 / n;
-    u.chunk = lo + f0 % n;
-    u.end = lo + n;
-    if (u.left > 0) open_tile(u);
-  };
 
-  Cursor in;
-  in.at = first;
-  in.unit = -1;
-  in.e = 0;
-  in.panel = 0;
-  in.left = 0;
-  bool more = n_panels > 0;
-  // to the next panel or batch that has a stage for this warp
-  auto settle = [&]() {
-    while (in.left == 0) {
-      if (++in.panel >= n_panels) {
-        in.panel = 0;
-        in.at += batch_tiles(in.at);
-        if (in.at >= last) {
-          more = false;
-          return;
-        }
+  while (at < last) {
+    // ---- the phase's units, and their rows of x
+    const int u0 = at / p.tiles, tile0 = at - u0 * p.tiles;
+    __syncthreads();  // the phase before is done with the tables and the sums
+    if (warp == 0) {
+      UnitRows u{0, 0, 0, 0};
+      const int most = p.panels > 1 ? 1 : kMaxUnits;
+      const bool there = lane < most && static_cast<int64_t>(u0 + lane) * p.tiles < last;
+      if (there) u = find_unit<NT>(p, sh, u0 + lane);
+      int x = (u.n + 1) & ~1, sum = x;  // an even number of rows: pairs of factors stay together
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
       }
-      open_panel(in);
+      u.x = sum - x;
+      const bool fits = there && sum <= p.x_rows;
+      const int count = __popc(__ballot_sync(0xFFFFFFFFu, fits));
+      if (fits) sh.unit[lane] = u;
+      if (lane == count - 1) {
+        sh.n_units = count;
+        sh.n_rows = sum;
+      }
+      if (lane < kMaxUnits) sh.unit_max[lane] = 15u;
+      if (lane == 0) sh.far = 0;
     }
-  };
-  if (more) {
-    open_panel(in);
-    settle();
-  }
-  uint32_t in_at = ring;  // the stage to fill
-  const uint32_t copy_to = copy_row * kRowPitch + copy_at, ring_end = ring + ring_bytes;
-  auto issue = [&]() {
-    if (more) {
-      const uint32_t to = in_at + copy_to, scale_to = in_at + kStageCodes + lane * 16;
-      const uint8_t* row = in.row + static_cast<uint32_t>(in.chunk) * static_cast<uint64_t>(kChunk / 2);
-      const uint8_t* const scale =
-          in.scale + static_cast<uint32_t>(in.chunk) * static_cast<uint64_t>(kChunkKt * kChunkBytes);
-      if (!p.half_rows && in.chunk != tail) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint8_t* src = i < in.quarters ? row : p.codes;
-          cp_async<16>(to + i * 4 * kRowPitch, src,
-                       i < in.quarters && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 16) ? 16 : 0);
-          row += quarter;
+    __syncthreads();
+    const int n_rows = sh.n_rows;
+    int end = static_cast<int>(min(static_cast<int64_t>(last), static_cast<int64_t>(u0 + sh.n_units) * p.tiles));
+    if (p.panels > 1) end = min(end, at + p.batch);
+    const int n_tiles = end - at, total = n_tiles * n;
+    const int f0 = total * warp / kWarps, f1 = total * (warp + 1) / kWarps;
+    if (threadIdx.x < n_rows) {
+      int i = 0;
+      while (i + 1 < sh.n_units && sh.unit[i + 1].x <= static_cast<int>(threadIdx.x)) ++i;
+      const int r = threadIdx.x - sh.unit[i].x;
+      int64_t src = -1;
+      if (r < sh.unit[i].n) {
+        src = sh.unit[i].row0 + r;
+        if (p.row_index != nullptr) src = __ldg(p.row_index + src);
+      }
+      sh.x_row[threadIdx.x] = src >= 0 && src < p.src_rows ? src : -1;
+      sh.x_unit[threadIdx.x] = r < sh.unit[i].n ? i : -1;
+    }
+
+    // ---- copies.  Row i of a tile is row tile_base + 32 * (i / 4) + i % 4 of the
+    // weights; a copy takes the four rows of a quarter, eight lanes to a row's
+    // 128 bytes.
+    const int copy_row = lane >> 3, copy_at = (lane & 7) * 16;
+    const int64_t quarter = 32 * static_cast<int64_t>(p.K >> 1);  // bytes of 32 rows
+    Cursor in;
+    in.panel = 0;
+    in.f = f0;
+    bool more = true;
+    auto open_run = [&]() {  // the next run of chunks that is not empty
+      for (;;) {
+        if (in.f >= f1) {
+          if (++in.panel >= p.panels) {
+            more = false;
+            return;
+          }
+          in.f = f0;
+          continue;
         }
-        cp_async16_if(scale_to, scale,
-                      lane < kScaleBytes / 16 && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16));
-      } else {
-        // the last, partial chunk, and rows that start at 8-byte boundaries
-        const int k = in.chunk * kChunk + copy_at * 2;
-        for (int i = 0; i < 4; ++i) {
-          if (!p.half_rows) {
-            const bool ok = i < in.quarters && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, row, 16);
-            cp_async<16>(to + i * 4 * kRowPitch, ok ? row : p.codes, ok ? 16 : 0);
-          } else {
+        const int t = in.f / n, first = in.f - t * n, len = min(f1 - in.f, n - first);
+        in.f += len;
+        in.chunk = in.panel * n + first;
+        in.left = min(len, p.chunks - in.chunk);  // the last panel may be shorter
+        if (in.left <= 0) continue;
+        const int all_tile = tile0 + t, i = all_tile / p.tiles, tile = all_tile - i * p.tiles;
+        const int e = sh.unit[i].e;
+        const int base = (tile >> 3) * 128 + (tile & 7) * 4 + copy_row;
+        in.quarters = base < p.N ? min(4, (p.N - base + 31) >> 5) : 0;
+        in.row = p.codes + e * p.expert_codes + (in.quarters ? base : 0) * static_cast<int64_t>(p.K >> 1) + copy_at;
+        in.scale = p.scales + e * p.expert_scales + (tile & 7) * 64 +
+                   (static_cast<int64_t>(tile >> 3) * p.nKT + (lane >> 2)) * kChunkBytes + (lane & 3) * 16;
+        return;
+      }
+    };
+    open_run();
+    uint32_t in_at = ring;  // the stage to fill
+    const uint32_t copy_to = copy_row * kRowPitch + copy_at, ring_end = ring + ring_bytes;
+    auto issue = [&]() {
+      if (more) {
+        const uint32_t to = in_at + copy_to, scale_to = in_at + kStageCodes + lane * 16;
+        const uint8_t* row = in.row + static_cast<uint32_t>(in.chunk) * static_cast<uint64_t>(kChunk / 2);
+        const uint8_t* const scale =
+            in.scale + static_cast<uint32_t>(in.chunk) * static_cast<uint64_t>(kChunkKt * kChunkBytes);
+        if (!p.half_rows && in.chunk != tail) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const bool ok =
-                  i < in.quarters && k + 16 * h < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, row + 8 * h, 8);
-              cp_async<8>(to + i * 4 * kRowPitch + 8 * h, ok ? row + 8 * h : p.codes, ok ? 8 : 0);
+          for (int i = 0; i < 4; ++i) {
+            const uint8_t* src = i < in.quarters ? row : p.codes;
+            cp_async<16>(to + i * 4 * kRowPitch, src,
+                         i < in.quarters && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 16) ? 16 : 0);
+            row += quarter;
+          }
+          cp_async16_if(scale_to, scale,
+                        lane < kScaleBytes / 16 && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16));
+        } else {
+          // the last, partial chunk, and rows that start at 8-byte boundaries
+          const int k = in.chunk * kChunk + copy_at * 2;
+          for (int i = 0; i < 4; ++i) {
+            if (!p.half_rows) {
+              const bool ok = i < in.quarters && k < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, row, 16);
+              cp_async<16>(to + i * 4 * kRowPitch, ok ? row : p.codes, ok ? 16 : 0);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const bool ok =
+                    i < in.quarters && k + 16 * h < p.K && MXFP4_IN_BOUNDS(p, kDbgCodes, row + 8 * h, 8);
+                cp_async<8>(to + i * 4 * kRowPitch + 8 * h, ok ? row + 8 * h : p.codes, ok ? 8 : 0);
+              }
             }
+            row += quarter;
           }
-          row += quarter;
+          if (lane < kScaleBytes / 16) {
+            const bool ok = in.chunk * kChunkKt + (lane >> 2) < p.nKT && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16);
+            cp_async<16>(scale_to, ok ? scale : p.scales, ok ? 16 : 0);
+          }
         }
-        if (lane < kScaleBytes / 16) {
-          const bool ok = in.chunk * kChunkKt + (lane >> 2) < p.nKT && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16);
-          cp_async<16>(scale_to, ok ? scale : p.scales, ok ? 16 : 0);
-        }
+        in_at += kStage;
+        if (in_at == ring_end) in_at = ring;
+        ++in.chunk;
+        if (--in.left == 0) open_run();
       }
-      in_at += kStage;
-      if (in_at == ring_end) in_at = ring;
-      ++in.chunk;
-      if (--in.left == 0) {
-        settle();
-      } else if (in.chunk == in.end) {
-        in.chunk = in.panel * p.panel;
-        ++in.tile;
-        open_tile(in);
-      }
-    }
-    cp_commit();  // an empty group at the end keeps the count of groups
-  };
-  for (int i = 0; i < p.stages; ++i) issue();
+      cp_commit();  // an empty group at the end keeps the count of groups
+    };
+    for (int i = 0; i < p.stages; ++i) issue();
 
-  uint32_t out_at = ring;  // the stage to read
-  int staged_unit = -1;
-  UnitRows ur{0, 0, 0};
-  bool by_token = true;  // BF16: x scaled by token, not by block
-  for (int at = first; at < last;) {
-    const int unit = at / p.tiles, tile0 = at - unit * p.tiles;
-    const int n_tiles = batch_tiles(at);
-    at += n_tiles;
-    if (unit != staged_unit) ur = find_unit<NT>(p, sh, unit);
-    // A token past the unit's last reads the last one's x: its column of the
-    // product is not stored.
-    uint32_t xa[NT];
+    // a tile's sums of this lane (rows g and g + 8, columns 2c and 2c + 1 of
+    // each block of 8) to y
+    auto store = [&](int all_tile, const float (&acc)[NT][4]) {
+      const int i = all_tile / p.tiles, tile = all_tile - i * p.tiles;
+      const UnitRows u = sh.unit[i];
+      const int row0 = (tile >> 3) * 128 + (tile & 7) * 4 + 32 * (g >> 2) + (g & 3);
+      const float gs = kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + u.e, 4)
+                           ? __ldg(p.global_scales + u.e)
+                           : 1.0f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      xa[t] = smem_u32(x_s) + min(t * 8 + g, ur.n - 1) * p.x_pitch + c * 16;
-    for (int panel = 0; panel < max(n_panels, 1); ++panel) {
-      const int lo = panel * p.panel, n = min(p.panel, p.chunks - lo);
-      // the sums of the batch before are read, and its x
+      for (int j = 0; j < NT * 4; ++j) {
+        const int tok = (j >> 2) * 8 + 2 * c + (j & 1), row = row0 + ((j >> 1) & 1) * 64;
+        if (tok >= u.n || row >= p.N) continue;
+        const float v = kNv ? acc[j >> 2][j & 3] / gs : acc[j >> 2][j & 3];
+        const int64_t to = (static_cast<int64_t>(u.row0) + tok) * p.ldy + row;
+        if (p.y_f32) {
+          float* y = reinterpret_cast<float*>(p.y) + to;
+          if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = v;
+        } else {
+          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + to;
+          if (MXFP4_IN_BOUNDS(p, kDbgY, y, 2))
+            *y = kF16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
+        }
+      }
+    };
+    // sums of this lane in a slot of shared memory
+    auto slot_at = [&](int slot) { return part_s + slot * (NT * 32) + lane; };
+
+    uint32_t out_at = ring;  // the stage to read
+    for (int panel = 0; panel < max(p.panels, 1); ++panel) {
+      const int lo = panel * n, n_here = min(n, p.chunks - lo);  // this panel's chunks
+      // ---- x: copied in 16-byte pieces, four to a 32-element block, then scaled
+      // to halves in place.  With fewer rows than warps, several warps share one.
+      if (threadIdx.x < n_rows) {
+        sh.x_max[threadIdx.x] = 0u;
+        sh.x_min[threadIdx.x] = 0xFFFFu;
+      }
       __syncthreads();
-      if (unit != staged_unit || n_panels > 1) {
-        // stage x: copied in 16-byte pieces, four to a 32-element block, then
-        // scaled to halves in place.  With fewer tokens than warps, several
-        // warps share a token.
-        if (threadIdx.x < ur.n) {
-          int64_t src = ur.row0 + threadIdx.x;
-          if (p.row_index != nullptr) src = __ldg(p.row_index + src);
-          sh.x_row[threadIdx.x] = src >= 0 && src < p.src_rows ? src : -1;
-          sh.x_max[threadIdx.x] = 0u;
-          sh.x_min[threadIdx.x] = 0xFFFFu;
+      const int pieces = n_here * kBlocks * 4;
+      const int sharing = max(kWarps / n_rows, 1), rows_at_once = kWarps / sharing;
+      const int my_row = warp / sharing < rows_at_once ? warp / sharing : n_rows;
+      const int my_piece = (warp % sharing) * 32 + lane;
+      for (int r = my_row; r < n_rows; r += rows_at_once) {
+        const int64_t row = sh.x_row[r];
+        const uint8_t* const src = p.x + ((row < 0 ? 0 : row) * p.ldx + lo * kChunk) * 2;
+        const int there = row < 0 ? 0 : (p.K - lo * kChunk) / 8;  // pieces that x has
+        const uint32_t to = smem_u32(x_s + r * p.x_pitch);
+        for (int i = my_piece; i < pieces; i += sharing * 32) {
+          const bool take = i < there && MXFP4_IN_BOUNDS(p, kDbgX, src + i * 16, 16);
+          cp_async<16>(to + i * 16, take ? src + i * 16 : p.x, take ? 16 : 0);
         }
-        __syncthreads();
-        const int pieces = n * kBlocks * 4;
-        const int sharing = max(kWarps / ur.n, 1), tokens_at_once = kWarps / sharing;
-        const int my_token = warp / sharing < tokens_at_once ? warp / sharing : ur.n;
-        const int my_piece = (warp % sharing) * 32 + lane;
-        for (int tok = my_token; tok < ur.n; tok += tokens_at_once) {
-          const int64_t row = sh.x_row[tok];
-          const uint8_t* const src = p.x + ((row < 0 ? 0 : row) * p.ldx + lo * kChunk) * 2;
-          const int there = row < 0 ? 0 : (p.K - lo * kChunk) / 8;  // pieces that x has
-          const uint32_t to = smem_u32(x_s + tok * p.x_pitch);
-          for (int i = my_piece; i < pieces; i += sharing * 32) {
-            const bool take = i < there && MXFP4_IN_BOUNDS(p, kDbgX, src + i * 16, 16);
-            cp_async<16>(to + i * 16, take ? src + i * 16 : p.x, take ? 16 : 0);
-          }
-        }
-        cp_commit();
-        cp_wait<0>();
-        if constexpr (!kF16) {
-          // A lane converts what it copied.  With the sign bits set, the order of
-          // the patterns is that of the magnitudes; one less, zero is the largest.
-          by_token = !p.few;
-          for (int tok = p.few ? ur.n : my_token; tok < ur.n; tok += tokens_at_once) {
+      }
+      cp_commit();
+      cp_wait<0>();
+      bool by_row = true;  // one power of two for a row's whole panel of x
+      if constexpr (!kF16) {
+        by_row = !p.few;
+        if (!p.few) {
+          // A lane reads what it copied.  With the sign bits set, the order of the
+          // patterns is that of the magnitudes; one less, zero is the largest.
+          for (int r = my_row; r < n_rows; r += rows_at_once) {
             uint32_t most = 0x80008000u, least = 0xFFFFFFFFu;
             for (int i = my_piece; i < pieces; i += sharing * 32) {
-              const uint4 v = *reinterpret_cast<const uint4*>(x_s + tok * p.x_pitch + i * 16);
+              const uint4 v = *reinterpret_cast<const uint4*>(x_s + r * p.x_pitch + i * 16);
               const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -419,93 +444,67 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
             most = __reduce_max_sync(0xFFFFFFFFu, most);
             least = __reduce_min_sync(0xFFFFFFFFu, least);
             if (lane == 0) {
-              atomicMax(&sh.x_max[tok], most);
-              atomicMin(&sh.x_min[tok], least);
+              atomicMax(&sh.x_max[r], most);
+              atomicMin(&sh.x_min[r], least);
+              if (!kNv && sh.x_unit[r] >= 0) atomicMax(&sh.unit_max[sh.x_unit[r]], most >> 7);
             }
           }
-          if (!p.few) {
-            __syncthreads();
-            // One power of two for a token's whole (panel of) x if that loses
-            // nothing: all of it within 2^32; else one for each 32 elements.  For
-            // MXFP4, whose weights may be of any size, the largest token's goes
-            // into the weights' scales (so that the sums are of the result's size)
-            // and the tokens are within 2^8 of it.
-            if (warp == 0) {
-              const uint32_t most = sh.x_max[lane & 15], least = sh.x_min[lane & 15] + 1u;
-              const bool there = lane < ur.n && most != 0u;  // a token of zeros takes any scale
-              const uint32_t e_max = __reduce_max_sync(0xFFFFFFFFu, there ? max(most >> 7, 15u) : 15u);
-              const uint32_t e = there ? max(most >> 7, 15u) : e_max;
-              const bool near = most < 0x7F80u && max(least >> 7, 1u) + 32 >= most >> 7 && (kNv || e + 8 >= e_max);
+          __syncthreads();
+          // One power of two for a row's whole (panel of) x if that loses nothing:
+          // all of it within 2^32; else one for each 32 elements.  For MXFP4, whose
+          // weights may be of any size, the unit's largest goes into the weights'
+          // scales (so that the sums are of the result's size) and its other rows
+          // are within 2^8 of it.
+          if (threadIdx.x < n_rows) {
+            const uint32_t most = sh.x_max[threadIdx.x], least = sh.x_min[threadIdx.x] + 1u;
+            const int unit = max(sh.x_unit[threadIdx.x], 0);
+            const uint32_t e_max = sh.unit_max[unit];
+            const uint32_t e = most != 0u ? max(most >> 7, 15u) : e_max;  // a row of zeros takes any scale
+            const bool near =
+                most == 0u || (most < 0x7F80u && max(least >> 7, 1u) + 32 >= most >> 7 && (kNv || e + 8 >= e_max));
+            float inverse;
+            half_scale(kNv ? most : e_max << 7, inverse);
+            sh.x_scale[threadIdx.x] = kNv ? inverse : near ? __uint_as_float((127u + e - e_max) << 23) : 1.0f;
+            if (!kNv) sh.unit_scale[unit] = inverse;
+            if (!near) sh.far = 1;
+          }
+          __syncthreads();
+          by_row = sh.far == 0;
+        }
+        for (int r = my_row; r < n_rows; r += rows_at_once) {
+          float inverse_whole;
+          const float f_whole = half_scale(sh.x_max[r], inverse_whole);
+          for (int base = my_piece - lane; base < pieces; base += sharing * 32) {  // pieces % 32 == 0
+            uint4* to = reinterpret_cast<uint4*>(x_s + r * p.x_pitch + (base + lane) * 16);
+            const uint4 v = *to;
+            const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+            float f = f_whole;
+            if (!by_row) {
+              uint32_t m = 0u;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m = max_finite_bf16x2(m, q[k]);
+              m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+              m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
               float inverse;
-              half_scale(kNv ? most : e_max << 7, inverse);
-              if (lane < 16) sh.x_scale[lane] = kNv ? inverse : __uint_as_float((127u + e - e_max) << 23);
-              const bool all = __all_sync(0xFFFFFFFFu, !there || near);
-              if (lane == 0) {
-                sh.by_token = all;
-                sh.common = inverse;
-              }
+              f = half_scale(m, inverse);
+              if (c == 0) xs_s[((base + lane) >> 2) * p.x_rows + r] = inverse;
             }
-            __syncthreads();
-            by_token = sh.by_token;
-          }
-          for (int tok = my_token; tok < ur.n; tok += tokens_at_once) {
-            float inverse_whole;
-            const float f_whole = half_scale(sh.x_max[tok], inverse_whole);
-            for (int base = my_piece - lane; base < pieces; base += sharing * 32) {  // pieces % 32 == 0
-              uint4* at = reinterpret_cast<uint4*>(x_s + tok * p.x_pitch + (base + lane) * 16);
-              const uint4 v = *at;
-              const uint32_t q[4] = {v.x, v.y, v.z, v.w};
-              float f = f_whole;
-              if (!by_token) {
-                uint32_t m = 0u;
+            uint32_t h[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) m = max_finite_bf16x2(m, q[k]);
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-                float inverse;
-                f = half_scale(m, inverse);
-                if (c == 0) xs_s[((base + lane) >> 2) * R + tok] = inverse;
-              }
-              uint32_t r[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                r[k] = pack_f16x2(__uint_as_float(q[k] << 16) * f, __uint_as_float(q[k] & 0xFFFF0000u) * f);
-              *at = make_uint4(r[0], r[1], r[2], r[3]);
-            }
+            for (int k = 0; k < 4; ++k)
+              h[k] = pack_f16x2(__uint_as_float(q[k] << 16) * f, __uint_as_float(q[k] & 0xFFFF0000u) * f);
+            *to = make_uint4(h[0], h[1], h[2], h[3]);
           }
         }
-        __syncthreads();
       }
-      staged_unit = unit;
+      __syncthreads();
 
+      // ---- the warp's share, a tile's run of chunks at a time
       float acc[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
-      const int total = n_tiles * n;
-      const int f0 = total * warp / kWarps, f1 = total * (warp + 1) / kWarps;
-      int tile = n > 0 ? f0 / n : 0, ch = n > 0 ? f0 % n : 0;
-      // A warp's part of a tile's sums has slot tile + warp: the shares are
-      // consecutive, so no two parts have the same slot.
-      auto flush = [&]() {
-        float* const q = part_s + (tile + warp) * R * kTile + (g & 3);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (t > 0 && t * 8 >= ur.n) break;
-          float2 xs = make_float2(1.0f, 1.0f);
-          if (!kF16 && by_token) xs = *reinterpret_cast<const float2*>(&sh.x_scale[t * 8 + 2 * c]);
-          const int lo = part_at(t * 8 + 2 * c, g >> 2), hi = part_at(t * 8 + 2 * c, 2 + (g >> 2));
-          q[lo] = acc[t][0] * xs.x;
-          q[lo + kTile] = acc[t][1] * xs.y;
-          q[hi] = acc[t][2] * xs.x;
-          q[hi + kTile] = acc[t][3] * xs.y;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
-        }
-      };
-      // the warp's share of the stages; x scaled by block needs a factor for each
-      auto multiply = [&](auto by_block, auto columns) {
+      // Sums of `len` stages from chunk `ch` of the panel; x scaled by block needs
+      // a factor for each, and few tokens one block of columns.
+      auto multiply = [&](int ch, int len, const UnitRows& u, [[maybe_unused]] float common, auto by_block,
+                          auto columns) {
         constexpr bool kByBlock = decltype(by_block)::value;
         constexpr int kCols = decltype(columns)::value;  // blocks of 8 tokens
         // The last kHold of a stage's scale chunks, with their codes, are taken
@@ -514,8 +513,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
         constexpr int kHold = kByBlock ? 0 : kCols == 2 && !kNv ? (kF16 ? 1 : 0) : kChunkKt;
         constexpr int kPerKt = kBlocks / kChunkKt;  // 32-element blocks of a scale chunk
         constexpr int kUnroll = kByBlock ? 1 : kPerKt, kUnrollKt = kHold > 0 ? kChunkKt : 1;
-        [[maybe_unused]] const float common = kF16 || kNv ? 1.0f : sh.common;
-        for (int f = f0; f < f1; ++f) {
+        // A token past the unit's last reads the last one's x: its column of the
+        // product is not stored.
+        uint32_t xa[kCols];
+#pragma unroll
+        for (int t = 0; t < kCols; ++t)
+          xa[t] = smem_u32(x_s) + (u.x + min(t * 8 + g, u.n - 1)) * p.x_pitch + c * 16 + ch * (kChunk * 2);
+        [[maybe_unused]] uint32_t sx = smem_u32(xs_s) + (ch * kBlocks * p.x_rows + u.x + 2 * c) * 4;
+        for (int f = 0; f < len; ++f) {
           if (p.stages == 3) cp_wait<2>(); else cp_wait<1>();
           __syncwarp();  // the copies of all lanes are in
           const uint32_t st = out_at;
@@ -525,15 +530,13 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           // scale words of rows g and g + 8
           const uint32_t sa = st + kStageCodes + (g & 3) * 16 + (g >> 2) * 4;
           [[maybe_unused]] uint32_t words[2][kHold * kPerKt + 1], scale_words[2][kHold + 1];
-          float run[kCols][4];  // NVFP4: sums of the whole stage
+          [[maybe_unused]] float run[kCols][4];  // NVFP4: sums of the whole stage
           if constexpr (kNv && !kByBlock) {
 #pragma unroll
             for (int t = 0; t < kCols; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i) run[t][i] = 0.0f;
           }
-          const uint32_t xc = ch * (kChunk * 2);
-          const uint32_t sx = smem_u32(xs_s) + (ch * kBlocks * R + 2 * c) * 4;
 #pragma unroll kUnrollKt
           for (int kt = 0; kt < kChunkKt; ++kt) {
             constexpr int kFree = kChunkKt - kHold;
@@ -581,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
               }
 #pragma unroll
               for (int t = 0; t < kCols; ++t) {
-                const uint4 xb = lds128(xa[t] + xc + b * 64);
+                const uint4 xb = lds128(xa[t] + b * 64);
                 if constexpr (kNv && !kByBlock) {
                   mma16816(run[t], a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
                   mma16816(run[t], a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
@@ -590,7 +593,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
                   mma16816_first(d, a0[0], a1[0], a0[1], a1[1], xb.x, xb.y);
                   mma16816(d, a0[2], a1[2], a0[3], a1[3], xb.z, xb.w);
                   float2 xs = make_float2(1.0f, 1.0f);
-                  if constexpr (kByBlock) xs = lds64f(sx + (b * R + t * 8) * 4);
+                  if constexpr (kByBlock) {
+                    // columns past the unit's last read factors of other rows, inside x_rows
+                    if (t * 8 + 2 * c < u.n) xs = lds64f(sx + (b * p.x_rows + t * 8) * 4);
+                  }
                   if constexpr (kNv) {
                     acc[t][0] = fmaf(d[0], xs.x, acc[t][0]);
                     acc[t][1] = fmaf(d[1], xs.y, acc[t][1]);
@@ -616,89 +622,109 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
             __syncwarp();  // the stage is read
             issue();
           }
-          if (++ch == n) {
-            flush();
-            ch = 0;
-            ++tile;
-          }
+#pragma unroll
+          for (int t = 0; t < kCols; ++t) xa[t] += kChunk * 2;
+          if constexpr (kByBlock) sx += kBlocks * p.x_rows * 4;
         }
       };
-      if (!kF16 && !by_token) {
-        multiply(std::true_type{}, std::integral_constant<int, NT>{});
-      } else if (NT == 2 && ur.n <= 8) {  // one block of columns is enough
-        multiply(std::false_type{}, std::integral_constant<int, 1>{});
-      } else {
-        multiply(std::false_type{}, std::integral_constant<int, NT>{});
-      }
-      if (ch != 0 && f1 > f0) flush();
-      // the warps whose shares [total * w / 16, total * (w + 1) / 16) meet each tile's stages
-      if (threadIdx.x < n_tiles && total > 0) {
-        sh.tile_warps[threadIdx.x][0] = share_of(threadIdx.x * n, total);
-        sh.tile_warps[threadIdx.x][1] = share_of(threadIdx.x * n + n - 1, total);
-      }
-      __syncthreads();
-
-      // every output: the parts of its tile in the warps' order, after those
-      // of the panels before; a thread has four rows (consecutive in y) of a token
-      const bool done = panel + 1 >= n_panels;
-      const float gs = kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + ur.e, 4)
-                           ? __ldg(p.global_scales + ur.e)
-                           : 1.0f;
-      for (int i = threadIdx.x; i < n_tiles * 4 * ur.n; i += kThreads) {
-        const int rest = i / n_tiles, tl = i - rest * n_tiles, quad = rest & 3, t = rest >> 2;
-        const int at_row = part_at(t, quad);
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        auto add = [&](const float* q) {
-          const float4 u = *reinterpret_cast<const float4*>(q);
-          v.x += u.x;
-          v.y += u.y;
-          v.z += u.z;
-          v.w += u.w;
-        };
-        if (total > 0) {
-          const int w1 = sh.tile_warps[tl][1];
-          for (int w = sh.tile_warps[tl][0]; w <= w1; ++w)
-            if (total >= kWarps || total * w / kWarps < total * (w + 1) / kWarps)
-              add(part_s + (tl + w) * R * kTile + at_row);
-        }
-        float* before = sum_s + tl * R * kTile + at_row;
-        if (panel > 0) add(before);
-        if (!done) {
-          *reinterpret_cast<float4*>(before) = v;
-          continue;
-        }
-        const int row = ((tile0 + tl) >> 3) * 128 + ((tile0 + tl) & 7) * 4 + 32 * quad;
-        const int left = p.N - row;
-        if (left <= 0) continue;
-        if constexpr (kNv) v = make_float4(v.x / gs, v.y / gs, v.z / gs, v.w / gs);
-        const int64_t to = (static_cast<int64_t>(ur.row0) + t) * p.ldy + row;
-        const float out[4] = {v.x, v.y, v.z, v.w};
-        if (p.y_f32) {
-          float* y = reinterpret_cast<float*>(p.y) + to;
-          if (p.y_quads && left >= 4 && MXFP4_IN_BOUNDS(p, kDbgY, y, 16)) {
-            *reinterpret_cast<float4*>(y) = v;
+      for (int f = f0; f < f1;) {
+        const int t = f / n, first = f - t * n, whole = min(f1 - f, n - first);
+        f += whole;
+        const int i = (tile0 + t) / p.tiles;
+        const UnitRows u = sh.unit[i];
+#pragma unroll
+        for (int k = 0; k < NT * 4; ++k) acc[k >> 2][k & 3] = 0.0f;
+        const int len = min(whole, n_here - first);
+        if (len > 0) {
+          const float common = kF16 || kNv ? 1.0f : sh.unit_scale[i];
+          if (!kF16 && !by_row) {
+            multiply(first, len, u, 1.0f, std::true_type{}, std::integral_constant<int, NT>{});
+          } else if (NT == 2 && u.n <= 8) {
+            multiply(first, len, u, common, std::false_type{}, std::integral_constant<int, 1>{});
           } else {
-            for (int j = 0; j < 4 && j < left; ++j)
-              if (MXFP4_IN_BOUNDS(p, kDbgY, y + j, 4)) y[j] = out[j];
+            multiply(first, len, u, common, std::false_type{}, std::integral_constant<int, NT>{});
           }
+          if (!kF16 && by_row) {
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+              if (k * 8 + 2 * c >= u.n) break;
+              const float2 xs = *reinterpret_cast<const float2*>(&sh.x_scale[u.x + k * 8 + 2 * c]);
+              acc[k][0] *= xs.x;
+              acc[k][1] *= xs.y;
+              acc[k][2] *= xs.x;
+              acc[k][3] *= xs.y;
+            }
+          }
+        }
+        if (p.panels > 1) {
+          // slot tile + warp: the shares are consecutive, so no two parts have the
+          // same; a lane adds up the panels of its own
+          float4* q = slot_at(t + warp);
+#pragma unroll
+          for (int k = 0; k < NT; ++k) {
+            const float4 v = panel > 0 ? q[k * 32] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            q[k * 32] = make_float4(v.x + acc[k][0], v.y + acc[k][1], v.z + acc[k][2], v.w + acc[k][3]);
+          }
+        } else if (whole == n) {
+          store(tile0 + t, acc);  // the tile is this warp's alone
         } else {
-          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + to;
-          const uint2 h = kF16 ? make_uint2(pack_f16x2(v.x, v.y), pack_f16x2(v.z, v.w))
-                               : make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
-          if (p.y_quads && left >= 4 && MXFP4_IN_BOUNDS(p, kDbgY, y, 8)) {
-            *reinterpret_cast<uint2*>(y) = h;
-          } else {
-            for (int j = 0; j < 4 && j < left; ++j)
-              if (MXFP4_IN_BOUNDS(p, kDbgY, y + j, 2))
-                y[j] = static_cast<uint16_t>((j < 2 ? h.x : h.y) >> (16 * (j & 1)));
-          }
+          // the first run of a share that starts inside a tile, or its last
+          float4* q = slot_at(2 * warp + (first == 0));
+#pragma unroll
+          for (int k = 0; k < NT; ++k) q[k * 32] = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
         }
       }
+      if (p.panels > 1) __syncthreads();  // x is read
     }
+    __syncthreads();
+
+    // ---- the tiles that are summed over warps, in the warps' order
+    if (p.panels > 1) {
+      for (int t = warp; t < n_tiles; t += kWarps) {
+        float acc[NT][4] = {};
+        const int w1 = share_of(t * n + n - 1, total);
+        for (int w = share_of(t * n, total); w <= w1; ++w) {
+          if (total * w / kWarps >= total * (w + 1) / kWarps) continue;
+          const float4* q = slot_at(t + w);
+#pragma unroll
+          for (int k = 0; k < NT; ++k) {
+            acc[k][0] += q[k * 32].x;
+            acc[k][1] += q[k * 32].y;
+            acc[k][2] += q[k * 32].z;
+            acc[k][3] += q[k * 32].w;
+          }
+        }
+        store(tile0 + t, acc);
+      }
+    } else if (n == 0) {
+      // no elements to sum
+      for (int t = warp; t < n_tiles; t += kWarps) {
+        float acc[NT][4] = {};
+        store(tile0 + t, acc);
+      }
+    } else if (f0 < f1 && f0 % n != 0 && f1 >= (f0 / n + 1) * n) {
+      // this warp has the last part of a tile that others begin
+      const int t = f0 / n;
+      float acc[NT][4] = {};
+      for (int w = share_of(t * n, total); w <= warp; ++w) {
+        const int start = total * w / kWarps;
+        if (start >= total * (w + 1) / kWarps) continue;
+        const float4* q = slot_at(2 * w + (start <= t * n));
+#pragma unroll
+        for (int k = 0; k < NT; ++k) {
+          acc[k][0] += q[k * 32].x;
+          acc[k][1] += q[k * 32].y;
+          acc[k][2] += q[k * 32].z;
+          acc[k][3] += q[k * 32].w;
+        }
+      }
+      store(tile0 + t, acc);
+    }
+    at = end;
   }
 }
 
-constexpr int kMaxSmem = 227 * 1024 - 3 * 1024;  // dynamic; the rest is the static part
+constexpr int kMaxSmem = 227 * 1024 - 5 * 1024;  // dynamic; the rest holds Shared
 
 template <bool kNv, bool kF16>
 cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStream_t stream) {
@@ -706,46 +732,54 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
   const int R = 8 * nt;
   const int kStage = kStageCodes + (kNv ? 256 : 128);
   const int sms = sm_count();
-  p.x_rows = p.rows < R ? (p.rows > 0 ? p.rows : 1) : R;
-  // Tiles of a CTA, about, and how many of them its warps take together: more
-  // make their shares of the stages more even and stage x less often, but
-  // their sums' parts need room that x's panels need too.
+  // Tiles of a CTA, about.  Its phases are few if x of all their units fits; x
+  // too long to fit whole goes in panels, with sums for all tiles of a phase.
   const int64_t per_cta = (expected_units * p.tiles + sms - 1) / sms;
-  const int per_chunk = p.x_rows * kChunk * 2 + (kF16 ? 0 : kBlocks * R * 4);
-  const auto parts = [&](int batch) { return (batch + kWarps) * R * kTile * 4; };
-  // All of a CTA's tiles in one batch, x whole and three stages if they fit;
-  // else the split with the fewest batches times panels.
-  int batch = 1, panel = 1, n_panels = 1;
+  const int unit_rows = static_cast<int>(p.rows < R ? (p.rows > 0 ? p.rows + (p.rows & 1) : 2) : R);
+  const int slot_bytes = nt * 32 * 16;  // a tile's sums, 16 bytes to a lane and column block
+  const int pitch_of_chunk = kChunk * 2, xs_of_chunk = kF16 ? 0 : kBlocks * 4;
+  int64_t spanned = per_cta / (p.tiles > 0 ? p.tiles : 1) + 2;  // units that a CTA's tiles meet
+  if (p.offsets == nullptr && spanned > expected_units) spanned = expected_units;
   int64_t fewest = -1;
   for (int stages = 3; stages >= 2; --stages) {
-    const auto fits = [&](int room) {
-      return (kMaxSmem - kWarps * stages * kStage - room - p.x_rows * 64) / per_chunk;
-    };
+    const int free_bytes = kMaxSmem - kWarps * stages * kStage;
+    // whole: two slots per warp, and as many rows as there is room and use for
+    const int row_bytes = p.chunks * (pitch_of_chunk + xs_of_chunk) + 64;
+    const int64_t fit = (free_bytes - 2 * kWarps * slot_bytes) / row_bytes & ~1;
+    const int64_t use = spanned * unit_rows < kMaxRows ? spanned * unit_rows : kMaxRows;
+    if (fit >= unit_rows) {
+      const int64_t phases = (use + fit - 1) / fit;
+      if (fewest < 0 || phases < fewest) {
+        fewest = phases;
+        p.stages = stages;
+        p.panels = p.chunks > 0 ? 1 : 0;
+        p.panel = p.chunks;
+        p.batch = 0;
+        p.x_rows = static_cast<int32_t>(fit < use ? fit : use);
+      }
+      continue;
+    }
     for (int64_t n_batches = 1; n_batches <= (per_cta > 1 ? per_cta : 1) && n_batches <= 64; ++n_batches) {
       const int64_t tiles = ((per_cta > 1 ? per_cta : 1) + n_batches - 1) / n_batches;
-      if (tiles > kMaxBatch) continue;
-      const int bt = static_cast<int>(tiles), sum_bytes = bt * R * kTile * 4;
-      const int pn = fits(parts(bt)) >= p.chunks ? p.chunks : fits(parts(bt) + sum_bytes);
-      if (pn < 1 && p.chunks > 0) continue;
-      const int panels = p.chunks > 0 ? (p.chunks + pn - 1) / pn : 1;
+      const int64_t room = free_bytes - (tiles + kWarps) * slot_bytes - unit_rows * 64;
+      const int64_t chunks = room / (unit_rows * (pitch_of_chunk + xs_of_chunk));
+      if (chunks < 1) continue;
+      int64_t panels = (p.chunks + chunks - 1) / chunks;
+      if (panels < 2) panels = 2;  // there is room for the chunks, not for a whole x's slots
       if (fewest < 0 || n_batches * panels < fewest) {
         fewest = n_batches * panels;
         p.stages = stages;
-        batch = bt;
-        n_panels = panels;
-        panel = p.chunks > 0 ? (p.chunks + panels - 1) / panels : 0;
+        p.panels = static_cast<int32_t>(panels);
+        p.panel = static_cast<int32_t>((p.chunks + panels - 1) / panels);
+        p.batch = static_cast<int32_t>(tiles);
+        p.x_rows = unit_rows;
       }
-      if (panels == 1) break;
     }
   }
   p.few = per_cta * p.chunks <= 4 * kWarps;
-  const int rings = kWarps * p.stages * kStage;
-  const int sums = n_panels > 1 ? batch * R * kTile * 4 : 0;
-  p.batch = batch;
-  p.panel = panel;
-  p.x_pitch = panel * kChunk * 2 + 64;
-  const int smem = rings + p.x_rows * p.x_pitch + (kF16 ? 0 : panel * kBlocks * R * 4) +
-                   parts(batch) + sums;
+  p.x_pitch = p.panel * pitch_of_chunk + 64;
+  const int smem = kWarps * p.stages * kStage + p.x_rows * (p.x_pitch + p.panel * xs_of_chunk) +
+                   (p.panels > 1 ? p.batch + kWarps : 2 * kWarps) * slot_bytes;
   static std::atomic<uint64_t> ready[2];  // devices on which each kernel may use kMaxSmem
   if (const cudaError_t e = allow_smem(kernel, kMaxSmem, ready[nt - 1]); e != cudaSuccess) return e;
   // a CTA per SM, each with its share of the tiles (the experts that have
@@ -780,8 +814,6 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
   p.expert_codes = a.N * (a.K / 2);
   p.expert_scales = (a.N + 127) / 128 * p.nKT * kChunkBytes;
   p.y_f32 = a.y_f32;
-  const int64_t quad = a.y_f32 ? 16 : 8;  // bytes of four elements of y
-  p.y_quads = reinterpret_cast<uintptr_t>(a.y) % quad == 0 && a.ldy % 4 == 0;
   p.half_rows = a.K % 32 != 0;
 #ifdef MXFP4_DEBUG_BOUNDS
   debug_range(p.dbg, kDbgX, a.x, a.src_rows > 0 ? ((a.src_rows - 1) * a.ldx + a.K) * 2 : 0);
