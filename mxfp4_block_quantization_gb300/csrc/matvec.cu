@@ -111,6 +111,7 @@ struct Shared {
   uint32_t unit_max[kMaxUnits];  // MXFP4: largest exponent of a unit's rows
   float x_scale[kMaxRows];   // what undoes a row's scaling (MXFP4: beyond the unit's)
   float unit_scale[kMaxUnits];
+  float unit_inverse[kMaxUnits];  // NVFP4: 1 / global scale
   int32_t far;               // BF16: some row needs a power of two for each block
 };
 
@@ -256,7 +257,11 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       u.x = sum - x;
       const bool fits = there && sum <= p.x_rows;
       const int count = __popc(__ballot_sync(0xFFFFFFFFu, fits));
-      if (fits) sh.unit[lane] = u;
+      if (fits) {
+        sh.unit[lane] = u;
+        if (kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + u.e, 4))
+          sh.unit_inverse[lane] = 1.0f / __ldg(p.global_scales + u.e);
+      }
       if (lane == count - 1) {
         sh.n_units = count;
         sh.n_rows = sum;
@@ -373,24 +378,30 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       const int i = all_tile / p.tiles, tile = all_tile - i * p.tiles;
       const UnitRows u = sh.unit[i];
       const int row0 = (tile >> 3) * 128 + (tile & 7) * 4 + 32 * (g >> 2) + (g & 3);
-      const float gs = kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + u.e, 4)
-                           ? __ldg(p.global_scales + u.e)
-                           : 1.0f;
+      const float by = kNv ? sh.unit_inverse[i] : 1.0f;
+      const int64_t size = p.y_f32 ? 4 : 2, ld = p.ldy * size;
+      uint8_t* const to = p.y + (static_cast<int64_t>(u.row0) + 2 * c) * ld + row0 * size;
+      const bool in_n[2] = {row0 < p.N, row0 + 64 < p.N};
 #pragma unroll
-      for (int j = 0; j < NT * 4; ++j) {
-        const int tok = (j >> 2) * 8 + 2 * c + (j & 1), row = row0 + ((j >> 1) & 1) * 64;
-        if (tok >= u.n || row >= p.N) continue;
-        const float v = kNv ? acc[j >> 2][j & 3] / gs : acc[j >> 2][j & 3];
-        const int64_t to = (static_cast<int64_t>(u.row0) + tok) * p.ldy + row;
-        if (p.y_f32) {
-          float* y = reinterpret_cast<float*>(p.y) + to;
-          if (MXFP4_IN_BOUNDS(p, kDbgY, y, 4)) *y = v;
-        } else {
-          uint16_t* y = reinterpret_cast<uint16_t*>(p.y) + to;
-          if (MXFP4_IN_BOUNDS(p, kDbgY, y, 2))
-            *y = kF16 ? __half_as_ushort(__float2half_rn(v)) : static_cast<uint16_t>(cvt_bf16x2(v, 0.0f));
+      for (int k = 0; k < NT; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (k * 8 + 2 * c + e >= u.n) continue;
+          uint8_t* const y = to + (k * 8 + e) * ld;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!in_n[h]) continue;
+            const float v = kNv ? acc[k][2 * h + e] * by : acc[k][2 * h + e];
+            if (p.y_f32) {
+              float* q = reinterpret_cast<float*>(y) + 64 * h;
+              if (MXFP4_IN_BOUNDS(p, kDbgY, q, 4)) *q = v;
+            } else {
+              uint16_t* q = reinterpret_cast<uint16_t*>(y) + 64 * h;
+              if (MXFP4_IN_BOUNDS(p, kDbgY, q, 2))
+                *q = static_cast<uint16_t>(kF16 ? pack_f16x2(v, 0.0f) : cvt_bf16x2(v, 0.0f));
+            }
+          }
         }
-      }
     };
     // sums of this lane in a slot of shared memory
     auto slot_at = [&](int slot) { return part_s + slot * (NT * 32) + lane; };
