@@ -989,10 +989,11 @@ def _cache(c, device):
     if k_scales.shape != want or v_scales.shape != want:
         raise ValueError(f"k_scales and v_scales must be {want}")
     u8 = torch.uint8
-    tensors = (_address("k_codes", k_codes, device, u8, 0),
-               _address("k_scales", k_scales, device, u8, 0),
-               _address("v_codes", v_codes, device, u8, 0),
-               _address("v_scales", v_scales, device, u8, 0))
+    for t in (k_codes, k_scales, v_codes, v_scales):
+        if t.get_device() != device or t.dtype is not u8 or not t.is_contiguous():
+            for name in KVCache._fields[:4]:  # says which and why
+                _address(name, getattr(c, name), device, u8, 0)
+    tensors = (k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(), v_scales.data_ptr())
     scalars = (_address("k_global", k_global, device, torch.float32, 4),
                _address("v_global", v_global, device, torch.float32, 4)) if nvfp4 else ()
     return pages, heads, page_size, 2 * half, tensors, scalars
