@@ -759,7 +759,7 @@ int mxfp4_cache_read_nvfp4_f16(const uint8_t* k_codes, const uint8_t* k_scales,
  * softmax_scale   finite.  window >= 0.
  * workspace       DEVICE, 16-byte aligned, at least
  *                 mxfp4_cache_attention_workspace_bytes(...) bytes (partial
- *                 results of long sequences split over CTAs; NULL allowed when
+ *                 results of long sequences split over warps; NULL allowed when
  *                 that is 0); contents on entry irrelevant.  Two calls in
  *                 flight at once need two workspaces.
  * out             [num_seqs, num_q_heads, head_dim], q's type, contiguous.

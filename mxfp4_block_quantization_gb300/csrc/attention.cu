@@ -20,10 +20,11 @@
 // The sums keep the heads in the same columns in both, so the softmax's
 // rescaling needs no exchange.
 //
-// A warp works alone: the steps (32 positions) of all units (a sequence, a kv
-// head, 8 query heads) are one sequence of which every warp that the GPU holds
-// has an even share, whatever the lengths, with its own ring of copies.  A unit
-// that spans warps is joined by a second kernel.
+// A warp works alone, with its own ring of copies: the steps (32 positions) of
+// all units (a sequence, a kv head, 8 query heads) are one sequence of which
+// every warp that the GPU holds has an even share, whatever the lengths.  A unit
+// that spans warps is joined by a second kernel.  Short contexts have a cluster
+// of CTAs to each unit instead, whose parts are joined in shared memory.
 //
 // Scales.  K, MXFP4: a power of two of any size, applied in float32 to the
 // 32-element partial scores; NVFP4: e2m1 * e4m3 has at most 6 bits and is
@@ -67,6 +68,7 @@ struct AttentionParams {
   float* __restrict__ part_o;   // [slot, 8 heads, head_dim]
   float* __restrict__ part_ml;  // [slot, 8 heads, 2]: maximum (log2), sum
   int32_t* __restrict__ parts;  // [unit, 2]: first warp, number of warps
+  int32_t* __restrict__ bad;    // [warp]: met a page out of range
   int32_t* __restrict__ status;
   int64_t q_seq_stride;
   int64_t q_head_stride;
@@ -78,7 +80,8 @@ struct AttentionParams {
   int32_t num_kv_heads;
   int32_t group;     // query heads of a kv head
   int32_t chunks;    // CTAs of 8 query heads per kv head
-  int32_t workers;   // warps that share the positions; 0: a warp per unit
+  int32_t workers;   // warps that share the positions; 0: a warp, or a cluster, per unit
+  int32_t ctas;      // of a unit's cluster, or 0
   int32_t num_pages;
   int32_t page_size;
   int32_t head_dim;
@@ -201,18 +204,48 @@ __device__ __forceinline__ void lds_floats(float (&f)[kN], uint32_t a) {
   }
 }
 
-// Status word: every length and every page that a sequence needs.
+// Status word of a call without shared steps: every length and every page that a
+// sequence needs.  `per` threads to a sequence; four entries of four sequences in
+// flight in each.
 __device__ __forceinline__ void write_status(const AttentionParams& p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kSeqs = 4, kEntries = 4;
+  int per = 1;
+  while (per < kThreads && static_cast<int64_t>(kEntries * per) * p.page_size < p.max_len) per *= 2;
+  const int lane = threadIdx.x % per, stride = kThreads / per;
   int bad = 0;
-  for (int b = warp; b < p.num_seqs; b += kWarps) {
-    int lo, hi;
-    if (!positions(p, b, lo, hi)) bad = 1;
-    const int last = hi > lo ? (hi - 1) / p.page_size : -1;
-    for (int i = lo / p.page_size + lane; i <= last; i += 32) {
-      const int32_t* entry = p.page_table + b * p.table_stride + i;
-      const int32_t page = MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
-      if (page < 0 || page >= p.num_pages) bad = 1;
+  for (int64_t b0 = threadIdx.x / per; b0 < p.num_seqs; b0 += kSeqs * stride) {
+    int i[kSeqs], last[kSeqs];
+    int32_t page[kSeqs][kEntries];
+#pragma unroll
+    for (int k = 0; k < kSeqs; ++k) {
+      const int64_t b = b0 + k * stride;
+      i[k] = 0;
+      last[k] = -1;
+      if (b >= p.num_seqs) continue;
+      int lo, hi;
+      if (!positions(p, static_cast<int>(b), lo, hi)) bad = 1;
+      i[k] = lo / p.page_size + lane;
+      last[k] = hi > lo ? (hi - 1) / p.page_size : -1;
+    }
+    bool more = true;
+    while (more) {
+      more = false;
+#pragma unroll
+      for (int k = 0; k < kSeqs; ++k)
+#pragma unroll
+        for (int j = 0; j < kEntries; ++j) {
+          const int at = i[k] + j * per;
+          const int32_t* entry = p.page_table + (b0 + k * stride) * p.table_stride + at;
+          page[k][j] = at > last[k] ? 0 : MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
+        }
+#pragma unroll
+      for (int k = 0; k < kSeqs; ++k) {
+#pragma unroll
+        for (int j = 0; j < kEntries; ++j)
+          if (i[k] + j * per <= last[k] && (page[k][j] < 0 || page[k][j] >= p.num_pages)) bad = 1;
+        i[k] += kEntries * per;
+        more |= i[k] <= last[k];
+      }
     }
   }
   bad = __syncthreads_or(bad);
@@ -287,7 +320,58 @@ __device__ __forceinline__ void own_scales(uint32_t (&k)[S::kWords], uint32_t (&
   }
 }
 
+// The parts of a unit that the warps of a cluster hold in their rings, joined:
+// each thread four values of a head, the parts read from the CTAs' shared
+// memory kBatch at a time.
 template <bool kNv, int DB>
+__device__ __forceinline__ void join_cluster(const AttentionParams& p, uint32_t rings, int ctas, int64_t head_at,
+                                             int heads) {
+  constexpr int D = 32 * DB, kQuads = D / 4, kBatch = 8;
+  constexpr uint32_t kRing = kStages * Stage<kNv, DB>::kBytes;
+  static_assert(kRing >= kHeads * (D + 2) * 4, "a part fits in a warp's ring");
+  const int parts = ctas * kWarps;
+  for (int u = cluster_rank() * kThreads + threadIdx.x; u < heads * kQuads; u += ctas * kThreads) {
+    const int h = u / kQuads, quad = u - h * kQuads;
+    float top = -INFINITY, sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int s0 = 0; s0 < parts; s0 += kBatch) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int s = s0 + k;
+        ml[k] = make_float2(-INFINITY, 0.0f);
+        v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (s < parts) {
+          const uint32_t from = cluster_address(rings + (s % kWarps) * kRing, s / kWarps);
+          ml[k] = ld_cluster_f2(from + (kHeads * D + h * 2) * 4);
+          v[k] = ld_cluster_f4(from + (h * D + quad * 4) * 4);
+        }
+      }
+      float x = top;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) x = fmaxf(x, ml[k].x);
+      const float z = x == -INFINITY ? 0.0f : x;
+      const float keep = exp2_approx(top - z);
+      top = x;
+      sum *= keep;
+      acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float f = exp2_approx(ml[k].x - z);
+        sum += ml[k].y * f;
+        acc.x += v[k].x * f;
+        acc.y += v[k].y * f;
+        acc.z += v[k].z * f;
+        acc.w += v[k].w * f;
+      }
+    }
+    store_out<kNv>(p, head_at + h, 4 * quad, D, acc, sum);
+    if (quad == 0) store_lse(p, head_at + h, sum, top);
+  }
+}
+
+template <bool kNv, int DB, bool kCluster>
 __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) attention_kernel(const AttentionParams p) {
   using S = Stage<kNv, DB>;
   constexpr int D = 32 * DB;
@@ -296,17 +380,20 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
 
-  if (blockIdx.x == gridDim.x - 1 && p.status != nullptr) {
-    write_status(p);
+  const int ctas = kCluster ? p.ctas : 1;  // of a unit
+  if (p.workers == 0 && blockIdx.x >= gridDim.x - ctas && p.status != nullptr) {
+    if (blockIdx.x == gridDim.x - 1) write_status(p);
     return;
   }
   // A unit of work is the positions of one sequence for one kv head and 8 of
   // its query heads, in steps of 32.
   const int units_per_seq = p.num_kv_heads * p.chunks;
-  const int worker = blockIdx.x * kWarps + warp;
+  const int worker = kCluster ? cluster_rank() * kWarps + warp : blockIdx.x * kWarps + warp;
   __shared__ int prefix[kThreads];  // steps up to and with each thread's sequences
   int at = 0, end = 0, share = 1;   // this warp's steps, over all units
-  if (p.workers > 0) {
+  if (kCluster) {
+    end = 1;
+  } else if (p.workers > 0) {
     int total = scan_steps(p, units_per_seq, prefix);
     share = share_of(p, total, units_per_seq);
     at = static_cast<int>(min(static_cast<int64_t>(share) * worker, static_cast<int64_t>(total)));
@@ -315,10 +402,19 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
     end = 1;
   }
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kBytes;
+  bool bad = false;  // shared steps: a page was out of range
   while (at < end) {
     // the unit that step `at` is in, and this warp's part of its steps
     int b, unit, s0 = 0, s1, n_parts = 1;
-    if (p.workers > 0) {
+    if constexpr (kCluster) {
+      const int which = blockIdx.x / ctas;
+      b = which / units_per_seq;
+      unit = which - b * units_per_seq;
+      const int steps = steps_of(p, b), part = (steps + ctas * kWarps - 1) / (ctas * kWarps);
+      s0 = min(steps, worker * part);
+      s1 = min(steps, s0 + part);
+      at = end;
+    } else if (p.workers > 0) {
       int unit_at;
       b = find_sequence(p, prefix, units_per_seq, at, unit_at);
       const int steps = steps_of(p, b);
@@ -574,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
         }
       }
       if (valid != 0xFFFFFFFFu) {  // the last step, or a page that is not there
+        bad |= valid != (last - t0 < kStep ? (1u << (last - t0)) - 1u : 0xFFFFFFFFu);
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -663,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
       }
     }
     cp_wait<0>();
+    if constexpr (kCluster) __syncwarp();  // the ring takes the part
 
     // ---- the result, or this part of it
 #pragma unroll
@@ -685,7 +783,10 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
           f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-12f;
         const float4 v = make_float4(o[i][0][e] * f, o[i][0][2 + e] * f, o[i][1][e] * f, o[i][1][2 + e] * f);
         const int d = i * 32 + 4 * g;
-        if (n_parts > 1) {
+        if constexpr (kCluster) {
+          sts128(ring + (h * D + d) * 4, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                 __float_as_uint(v.w));
+        } else if (n_parts > 1) {
           // slot unit + warp: the shares are consecutive, so no two parts have the same
           float* to = p.part_o + (slot + h) * D + d;
           if (MXFP4_IN_BOUNDS(p, kDbgPart, to, 16)) *reinterpret_cast<float4*>(to) = v;
@@ -694,7 +795,9 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
         }
       }
       if (g == 0) {
-        if (n_parts > 1) {
+        if constexpr (kCluster) {
+          sts64(ring + (kHeads * D + h * 2) * 4, __float_as_uint(top), __float_as_uint(sum));
+        } else if (n_parts > 1) {
           float* to = p.part_ml + (slot + h) * 2;
           if (MXFP4_IN_BOUNDS(p, kDbgPart, to, 8)) *reinterpret_cast<float2*>(to) = make_float2(top, sum);
         } else {
@@ -702,7 +805,15 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
         }
       }
     }
+    if constexpr (kCluster) {
+      __syncwarp();
+      cluster_sync();
+      join_cluster<kNv, DB>(p, smem_u32(smem), ctas, head_at, heads);
+      __syncwarp();
+      cluster_sync();  // no CTA leaves while its parts are read
+    }
   }
+  if (!kCluster && p.workers > 0 && lane == 0) p.bad[worker] = bad;
   pdl_release();
 }
 
@@ -720,7 +831,18 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
     attention_join_kernel(const AttentionParams p) {
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t head = kPerHead == 1 ? static_cast<int64_t>(blockIdx.x) * kWarps + warp : blockIdx.x;
+  const int word = p.status != nullptr;
+  if (word && blockIdx.x == 0) {
+    // status word: what the warps met, and every length
+    int bad = 0, lo, hi;
+#pragma unroll 8
+    for (int w = threadIdx.x; w < p.workers; w += blockDim.x) bad |= p.bad[w];
+    for (int64_t b = threadIdx.x; b < p.num_seqs; b += blockDim.x) bad |= !positions(p, static_cast<int>(b), lo, hi);
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *p.status = bad ? -7 : 0;
+    return;
+  }
+  const int64_t head = kPerHead == 1 ? static_cast<int64_t>(blockIdx.x - word) * kWarps + warp : blockIdx.x - word;
   if (head >= static_cast<int64_t>(p.num_seqs) * p.num_q_heads) return;
   const int b = static_cast<int>(head / p.num_q_heads), h = static_cast<int>(head - static_cast<int64_t>(b) * p.num_q_heads);
   const int kvh = h / p.group, in_group = h - kvh * p.group;
@@ -815,10 +937,10 @@ template <bool kNv, int DB>
 cudaError_t launch_dim(const AttentionParams& p, unsigned grid, cudaStream_t stream) {
   using S = Stage<kNv, DB>;
   constexpr int kSmem = kWarps * kStages * S::kBytes;
-  static std::atomic<uint64_t> ready{0};
-  if (const cudaError_t e = allow_smem(attention_kernel<kNv, DB>, kSmem, ready); e != cudaSuccess)
-    return e;
-  return launch_pdl(attention_kernel<kNv, DB>, grid, kThreads, kSmem, stream, p);
+  static std::atomic<uint64_t> ready[2] = {};
+  const auto kernel = p.ctas > 0 ? attention_kernel<kNv, DB, true> : attention_kernel<kNv, DB, false>;
+  if (const cudaError_t e = allow_smem(kernel, kSmem, ready[p.ctas > 0]); e != cudaSuccess) return e;
+  return launch_pdl_cluster(kernel, grid, kThreads, kSmem, stream, p.ctas, p);
 }
 
 template <bool kNv>
@@ -837,20 +959,40 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
   if (e != cudaSuccess || p.workers == 0) return e;
   const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
   const int64_t units = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads * p.chunks;
+  const unsigned word = p.status != nullptr;
   if (p.workers >= 32 * units)
-    return launch_pdl(attention_join_kernel<kNv, 16>, static_cast<unsigned>(heads), 32 * 16, 0, stream, p);
+    return launch_pdl(attention_join_kernel<kNv, 16>, static_cast<unsigned>(heads) + word, 32 * 16, 0, stream, p);
   if (p.workers >= 6 * units)
-    return launch_pdl(attention_join_kernel<kNv, 4>, static_cast<unsigned>(heads), 32 * 4, 0, stream, p);
-  return launch_pdl(attention_join_kernel<kNv, 1>, static_cast<unsigned>((heads + kWarps - 1) / kWarps), kThreads,
-                    0, stream, p);
+    return launch_pdl(attention_join_kernel<kNv, 4>, static_cast<unsigned>(heads) + word, 32 * 4, 0, stream, p);
+  return launch_pdl(attention_join_kernel<kNv, 1>, static_cast<unsigned>((heads + kWarps - 1) / kWarps) + word,
+                    kThreads, 0, stream, p);
+}
+
+int64_t resident_warps(int32_t head_dim) {
+  return 152 * kWarps * (head_dim <= 64 ? 5 : head_dim <= 128 ? 4 : 2);
+}
+// CTAs of the cluster that takes a unit, as many as have a step for each warp and
+// are resident together, where that leaves a warp kFewSteps steps at most; else 0.
+// Without the second kernel and the workspace, but with the SMs idle that the
+// clusters leave: 8.5 -> 6.5 us for one sequence of 700 positions (64 heads on 8,
+// head_dim 128), 26.9 -> 21.8 for 64 of up to 1024 (8 steps); at 12 steps, one
+// of 12000, 14.3 -> 15.8.
+int cluster_ctas(int64_t units, int32_t head_dim, int64_t max_len) {
+  constexpr int64_t kFewSteps = 8;
+  constexpr int kMost = 8;  // the portable size
+  if (max_len <= kAhead * kStep) return 0;
+  const int64_t steps = (max_len + kStep - 1) / kStep, most = resident_warps(head_dim) / kWarps;
+  int ctas = 1;
+  while (ctas < kMost && steps > ctas * kWarps && units * ctas * 2 <= most) ctas *= 2;
+  return units * ctas <= most && steps <= kFewSteps * ctas * kWarps ? ctas : 0;
 }
 
 // Warps that share the positions of all sequences: as many as the GPU holds at
-// once, so that all end together; 0 for contexts so short that a warp takes a
-// unit whole.
+// once, so that all end together; 0 for contexts so short that a warp or a
+// cluster takes a unit whole.
 int shared_workers(int64_t units, int32_t head_dim, int64_t max_len) {
-  if (max_len <= kAhead * kStep) return 0;
-  const int64_t resident = 152 * kWarps * (head_dim <= 64 ? 5 : head_dim <= 128 ? 4 : 2);
+  if (max_len <= kAhead * kStep || cluster_ctas(units, head_dim, max_len) > 0) return 0;
+  const int64_t resident = resident_warps(head_dim);
   const int64_t most = (units * ((max_len + kStep - 1) / kStep) + kWarps - 1) / kWarps * kWarps;
   return static_cast<int>(most < resident ? most : resident);
 }
@@ -866,7 +1008,7 @@ int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_
   if (num_seqs == 0 || num_q_heads == 0 || head_dim == 0) return 0;
   const int64_t units = num_seqs * num_kv_heads * chunks_of(num_q_heads, num_kv_heads);
   const int workers = shared_workers(units, head_dim, max_len);
-  return workers > 0 ? (units + workers) * kHeads * (head_dim + 2) + 2 * units : 0;
+  return workers > 0 ? (units + workers) * kHeads * (head_dim + 2) + 2 * units + workers : 0;
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) {
@@ -906,9 +1048,11 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   p.chunks = chunks_of(a.num_q_heads, c.num_heads);
   const int64_t units = a.num_seqs * c.num_heads * p.chunks;
   p.workers = shared_workers(units, c.head_dim, a.max_pages * c.page_size);
+  p.ctas = cluster_ctas(units, c.head_dim, a.max_pages * c.page_size);
   p.part_o = a.workspace;
   p.part_ml = p.part_o + (units + p.workers) * kHeads * c.head_dim;
   p.parts = reinterpret_cast<int32_t*>(p.part_ml + (units + p.workers) * kHeads * 2);
+  p.bad = p.parts + 2 * units;
 #ifdef MXFP4_DEBUG_BOUNDS
   const int64_t rows = c.num_pages * c.page_size * c.num_heads;
   debug_range(p.dbg, kDbgQ, a.q, a.num_seqs > 0
@@ -921,9 +1065,12 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
               a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
   debug_range(p.dbg, kDbgOut, a.out, a.num_seqs * a.num_q_heads * c.head_dim * 2);
   debug_range(p.dbg, kDbgPart, a.workspace,
-              p.workers > 0 ? ((units + p.workers) * kHeads * (c.head_dim + 2) + 2 * units) * 4 : 0);
+              p.workers > 0 ? ((units + p.workers) * kHeads * (c.head_dim + 2) + 2 * units + p.workers) * 4 : 0);
 #endif
-  const int64_t grid = ((p.workers > 0 ? p.workers : units) + kWarps - 1) / kWarps + (a.status ? 1 : 0);
+  const int64_t word = a.status != nullptr;
+  const int64_t grid = p.workers > 0 ? p.workers / kWarps
+                       : p.ctas > 0  ? (units + word) * p.ctas
+                                     : (units + kWarps - 1) / kWarps + word;
   if (grid == 0) return cudaSuccess;
   return c.nvfp4 ? launch_format<true>(p, static_cast<unsigned>(grid), stream)
                  : launch_format<false>(p, static_cast<unsigned>(grid), stream);

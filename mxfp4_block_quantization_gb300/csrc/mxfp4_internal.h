@@ -225,21 +225,29 @@ unsigned int debug_violations_attention();
 // Launch with programmatic dependent launch allowed: the grid may be
 // scheduled while the previous kernel of the stream drains; every kernel of
 // this library executes griddepcontrol.wait before touching global memory,
-// so it still observes all writes of the preceding work.
+// so it still observes all writes of the preceding work.  In clusters of `ctas`
+// CTAs (0: none), of which the grid is a multiple.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem,
-                       cudaStream_t stream, Args&&... args) {
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem,
+                               cudaStream_t stream, int ctas, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(ctas), 1u, 1u};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = ctas > 0 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, unsigned threads, size_t smem,
+                       cudaStream_t stream, Args&&... args) {
+  return launch_pdl_cluster(kernel, grid, threads, smem, stream, 0, std::forward<Args>(args)...);
 }
 
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device,
