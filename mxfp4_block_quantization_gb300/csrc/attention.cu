@@ -49,8 +49,11 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kStep = 32;   // positions of a warp's step
-constexpr int kStages = 2;
-constexpr int kAhead = kStages - 1;
+// Stages of a warp's ring, and CTAs of an SM that it is made for.
+__host__ __device__ constexpr int stages_of(int blocks, bool cluster) { return cluster || blocks > 4 ? 2 : 3; }
+__host__ __device__ constexpr int ctas_of(int blocks, bool cluster) {
+  return (blocks <= 2 ? 5 : blocks <= 4 ? 4 : 2) - (cluster || blocks > 4 ? 0 : 1);
+}
 constexpr int kHeads = 8;   // query heads of a CTA: the columns of the products
 constexpr float kLag = 3.0f;  // log2: how far a warp's reference may lag behind its maximum
 constexpr float kLog2e = 1.4426950408889634f;
@@ -67,7 +70,7 @@ struct AttentionParams {
   float* __restrict__ lse;
   float* __restrict__ part_o;   // [slot, 8 heads, head_dim]
   float* __restrict__ part_ml;  // [slot, 8 heads, 2]: maximum (log2), sum
-  int32_t* __restrict__ parts;  // [unit, 2]: first warp, number of warps
+  int4* __restrict__ parts;     // [unit]: see Parts
   int32_t* __restrict__ bad;    // [warp]: met a page out of range
   int32_t* __restrict__ status;
   int64_t q_seq_stride;
@@ -171,6 +174,28 @@ __device__ __forceinline__ int find_sequence(const AttentionParams& p, const int
     if (at < first + n || b + 1 >= p.num_seqs) return b;
     first += n;
   }
+}
+
+// Who holds the parts of a unit: the warps first..last, but of CTAs cta0..cta1 - 1,
+// which have no other unit, the first warp for all.
+struct Parts {
+  int first, last, cta0, cta1;
+  __device__ __forceinline__ int count() const {
+    return last - first + 1 - max(cta1 - cta0, 0) * (kWarps - 1);
+  }
+  __device__ __forceinline__ int warp(int k) const {
+    const int before = kWarps * cta0 - first, whole = max(cta1 - cta0, 0);
+    if (whole == 0 || k < before) return first + k;
+    return k < before + whole ? kWarps * (cta0 + k - before) : first + k + whole * (kWarps - 1);
+  }
+};
+__device__ __forceinline__ Parts parts_of(int unit_at, int steps, int share) {
+  Parts r;
+  r.first = unit_at / share;
+  r.last = (unit_at + steps - 1) / share;
+  r.cta0 = (r.first * share == unit_at ? r.first + kWarps - 1 : r.first + kWarps) / kWarps;
+  r.cta1 = ((r.last + 1) * share == unit_at + steps ? r.last + 1 : r.last) / kWarps;
+  return r;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -320,17 +345,14 @@ __device__ __forceinline__ void own_scales(uint32_t (&k)[S::kWords], uint32_t (&
   }
 }
 
-// The parts of a unit that the warps of a cluster hold in their rings, joined:
-// each thread four values of a head, the parts read from the CTAs' shared
-// memory kBatch at a time.
-template <bool kNv, int DB>
-__device__ __forceinline__ void join_cluster(const AttentionParams& p, uint32_t rings, int ctas, int64_t head_at,
-                                             int heads) {
-  constexpr int D = 32 * DB, kQuads = D / 4, kBatch = 8;
-  constexpr uint32_t kRing = kStages * Stage<kNv, DB>::kBytes;
-  static_assert(kRing >= kHeads * (D + 2) * 4, "a part fits in a warp's ring");
+// The parts of a unit that the warps of a cluster, or of a CTA, hold in their
+// rings, joined: each thread four values of a head, the parts read from the CTAs'
+// shared memory kBatch at a time.  `store(head, quad, acc, sum, top)`.
+template <int DB, bool kCluster, typename Store>
+__device__ __forceinline__ void join_rings(uint32_t rings, uint32_t ring_bytes, int ctas, int heads, Store store) {
+  constexpr int D = 32 * DB, kQuads = D / 4, kBatch = kCluster ? 8 : kWarps;
   const int parts = ctas * kWarps;
-  for (int u = cluster_rank() * kThreads + threadIdx.x; u < heads * kQuads; u += ctas * kThreads) {
+  for (int u = (kCluster ? cluster_rank() : 0) * kThreads + threadIdx.x; u < heads * kQuads; u += ctas * kThreads) {
     const int h = u / kQuads, quad = u - h * kQuads;
     float top = -INFINITY, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -343,7 +365,8 @@ __device__ __forceinline__ void join_cluster(const AttentionParams& p, uint32_t 
         ml[k] = make_float2(-INFINITY, 0.0f);
         v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (s < parts) {
-          const uint32_t from = cluster_address(rings + (s % kWarps) * kRing, s / kWarps);
+          uint32_t from = rings + (s % kWarps) * ring_bytes;
+          if constexpr (kCluster) from = cluster_address(from, s / kWarps);
           ml[k] = ld_cluster_f2(from + (kHeads * D + h * 2) * 4);
           v[k] = ld_cluster_f4(from + (h * D + quad * 4) * 4);
         }
@@ -366,15 +389,16 @@ __device__ __forceinline__ void join_cluster(const AttentionParams& p, uint32_t 
         acc.w += v[k].w * f;
       }
     }
-    store_out<kNv>(p, head_at + h, 4 * quad, D, acc, sum);
-    if (quad == 0) store_lse(p, head_at + h, sum, top);
+    store(h, quad, acc, sum, top);
   }
 }
 
 template <bool kNv, int DB, bool kCluster>
-__global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) attention_kernel(const AttentionParams p) {
+__global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_kernel(const AttentionParams p) {
+  constexpr int kStages = stages_of(DB, kCluster), kAhead = kStages - 1;
   using S = Stage<kNv, DB>;
   constexpr int D = 32 * DB;
+  static_assert(kStages * S::kBytes >= kHeads * (D + 2) * 4, "a part fits in a warp's ring");
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -405,7 +429,9 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
   bool bad = false;  // shared steps: a page was out of range
   while (at < end) {
     // the unit that step `at` is in, and this warp's part of its steps
-    int b, unit, s0 = 0, s1, n_parts = 1;
+    int b, unit, s0 = 0, s1;
+    bool whole = true;    // this warp has the whole unit
+    bool joined = false;  // the CTA's warps have this unit alone, and join their parts
     if constexpr (kCluster) {
       const int which = blockIdx.x / ctas;
       b = which / units_per_seq;
@@ -424,14 +450,13 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
       s0 = at - unit_at;
       s1 = min(padded, s0 + (end - at));
       at += s1 - s0;
-      // the warps that have a part of the unit
-      const int first_part = unit_at / share;
-      n_parts = (unit_at + steps - 1) / share - first_part + 1;
-      int32_t* parts = p.parts + 2 * (static_cast<int64_t>(b) * units_per_seq + unit);
-      if (s0 == 0 && lane == 0 && MXFP4_IN_BOUNDS(p, kDbgPart, parts, 8)) {
-        parts[0] = first_part;
-        parts[1] = n_parts;
-      }
+      const Parts parts = parts_of(unit_at, steps, share);
+      const int cta = blockIdx.x;
+      whole = parts.count() == 1;
+      joined = cta >= parts.cta0 && cta < parts.cta1;
+      int4* to = p.parts + static_cast<int64_t>(b) * units_per_seq + unit;
+      if (s0 == 0 && lane == 0 && MXFP4_IN_BOUNDS(p, kDbgPart, to, 16))
+        *to = make_int4(parts.first, parts.last, parts.cta0, parts.cta1);
       if (s0 >= steps) continue;  // padding
     } else {
       b = worker / units_per_seq;
@@ -554,7 +579,13 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
         for (int i = 0; i < DB; ++i)
           q[i] = make_uint4(scaled(q[i].x), scaled(q[i].y), scaled(q[i].z), scaled(q[i].w));
       }
-      const float more = p.softmax_scale * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
+      if (p.softmax_scale < 0.0f) {  // its sign goes into q: a larger product is a larger score
+#pragma unroll
+        for (int i = 0; i < DB; ++i)
+          q[i] = make_uint4(q[i].x ^ 0x80008000u, q[i].y ^ 0x80008000u, q[i].z ^ 0x80008000u, q[i].w ^ 0x80008000u);
+      }
+      // (not zero: a masked score is -infinity, and stays that)
+      const float more = fmaxf(fabsf(p.softmax_scale), 0x1p-126f) * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
       qs0 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c);
       qs1 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4);
       qs0 *= more;
@@ -663,11 +694,6 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
             s[t][3] = fmaf(d[3], f1[i], s[t][3]);
           }
         }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          s[t][2 * r] *= qs0;
-          s[t][2 * r + 1] *= qs1;
-        }
       }
       if (valid != 0xFFFFFFFFu) {  // the last step, or a page that is not there
         bad |= valid != (last - t0 < kStep ? (1u << (last - t0)) - 1u : 0xFFFFFFFFu);
@@ -681,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
       // ---- running maximum and sum.  The reference m may lag behind the
       // maximum by kLag (P then grows to 2^kLag at most, far inside a half), so
       // that the output is rescaled a few times at all, not at every new maximum.
-      float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
-      float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+      float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])) * qs0;
+      float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3])) * qs1;
       if (__any_sync(0xFFFFFFFFu, x0 > m0 + kLag || x1 > m1 + kLag)) {
 #pragma unroll
         for (int k = 4; k < 32; k *= 2) {
@@ -708,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float e0 = exp2_approx(s[t][2 * r] - z0), e1 = exp2_approx(s[t][2 * r + 1] - z1);
+          const float e0 = exp2_approx(fmaf(s[t][2 * r], qs0, -z0)), e1 = exp2_approx(fmaf(s[t][2 * r + 1], qs1, -z1));
           l0 += e0;
           l1 += e1;
           pk[t][r] = pack_f16x2(e0, e1);
@@ -760,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
       }
     }
     cp_wait<0>();
-    if constexpr (kCluster) __syncwarp();  // the ring takes the part
+    const bool in_ring = kCluster || joined;
+    if (in_ring) __syncwarp();  // the ring takes the part
 
     // ---- the result, or this part of it
 #pragma unroll
@@ -768,7 +795,16 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
       l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, k);
       l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, k);
     }
-    const int64_t slot = (static_cast<int64_t>(b) * units_per_seq + unit + worker) * kHeads;
+    // slot unit + warp: the shares are consecutive, so no two parts have the same
+    const int64_t unit_slot = static_cast<int64_t>(b) * units_per_seq + unit;
+    auto store_part = [&](int holder, int h, int quad, float4 v) {
+      float* to = p.part_o + ((unit_slot + holder) * kHeads + h) * D + quad * 4;
+      if (MXFP4_IN_BOUNDS(p, kDbgPart, to, 16)) *reinterpret_cast<float4*>(to) = v;
+    };
+    auto store_part_sum = [&](int holder, int h, float top, float sum) {
+      float* to = p.part_ml + ((unit_slot + holder) * kHeads + h) * 2;
+      if (MXFP4_IN_BOUNDS(p, kDbgPart, to, 8)) *reinterpret_cast<float2*>(to) = make_float2(top, sum);
+    };
     const int64_t head_at = static_cast<int64_t>(b) * p.num_q_heads + head0;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {  // heads 2c and 2c + 1; four values of each block in a lane
@@ -783,23 +819,20 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
           f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-12f;
         const float4 v = make_float4(o[i][0][e] * f, o[i][0][2 + e] * f, o[i][1][e] * f, o[i][1][2 + e] * f);
         const int d = i * 32 + 4 * g;
-        if constexpr (kCluster) {
+        if (in_ring) {
           sts128(ring + (h * D + d) * 4, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
                  __float_as_uint(v.w));
-        } else if (n_parts > 1) {
-          // slot unit + warp: the shares are consecutive, so no two parts have the same
-          float* to = p.part_o + (slot + h) * D + d;
-          if (MXFP4_IN_BOUNDS(p, kDbgPart, to, 16)) *reinterpret_cast<float4*>(to) = v;
+        } else if (!whole) {
+          store_part(worker, h, i * 8 + g, v);
         } else {
           store_out<kNv>(p, head_at + h, d, D, v, sum);
         }
       }
       if (g == 0) {
-        if constexpr (kCluster) {
+        if (in_ring) {
           sts64(ring + (kHeads * D + h * 2) * 4, __float_as_uint(top), __float_as_uint(sum));
-        } else if (n_parts > 1) {
-          float* to = p.part_ml + (slot + h) * 2;
-          if (MXFP4_IN_BOUNDS(p, kDbgPart, to, 8)) *reinterpret_cast<float2*>(to) = make_float2(top, sum);
+        } else if (!whole) {
+          store_part_sum(worker, h, top, sum);
         } else {
           store_lse(p, head_at + h, sum, top);
         }
@@ -808,9 +841,25 @@ __global__ void __launch_bounds__(kThreads, DB <= 2 ? 5 : DB <= 4 ? 4 : 2) atten
     if constexpr (kCluster) {
       __syncwarp();
       cluster_sync();
-      join_cluster<kNv, DB>(p, smem_u32(smem), ctas, head_at, heads);
+      join_rings<DB, true>(smem_u32(smem), kStages * S::kBytes, ctas, heads,
+                           [&](int h, int quad, float4 v, float sum, float top) {
+                             store_out<kNv>(p, head_at + h, 4 * quad, D, v, sum);
+                             if (quad == 0) store_lse(p, head_at + h, sum, top);
+                           });
       __syncwarp();
       cluster_sync();  // no CTA leaves while its parts are read
+    } else if (joined) {  // this warp's last unit: the barrier is the CTA's
+      __syncthreads();
+      join_rings<DB, false>(smem_u32(smem), kStages * S::kBytes, 1, heads,
+                            [&](int h, int quad, float4 v, float sum, float top) {
+                              if (whole) {
+                                store_out<kNv>(p, head_at + h, 4 * quad, D, v, sum);
+                                if (quad == 0) store_lse(p, head_at + h, sum, top);
+                              } else {
+                                store_part(worker - warp, h, quad, v);
+                                if (quad == 0) store_part_sum(worker - warp, h, top, sum);
+                              }
+                            });
     }
   }
   if (!kCluster && p.workers > 0 && lane == 0) p.bad[worker] = bad;
@@ -851,11 +900,12 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
   float top = -INFINITY, sum = 0.0f;
   float4 acc[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (steps_of(p, b) > 0) {
-    const int first = p.parts[2 * unit], n = p.parts[2 * unit + 1];
-    if (n == 1) return;  // written by the warp itself
-    const int64_t slot = (unit + first) * kHeads + in_group % kHeads;
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml + slot * 2);
-    const float4* po = reinterpret_cast<const float4*>(p.part_o + slot * p.head_dim);
+    const int4 who = p.parts[unit];
+    const Parts parts{who.x, who.y, who.z, who.w};
+    const int n = parts.count();
+    if (n == 1) return;  // written already
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + in_group % kHeads;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o) + in_group % kHeads * quads;
     // one pass, kBatch parts' loads in flight
     constexpr int kBatch = 6;
     for (int s0 = kPerHead == 1 ? 0 : warp; s0 < n; s0 += kBatch * kPerHead) {
@@ -864,10 +914,11 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int s = s0 + k * kPerHead;
-        part[k] = s < n ? ml[s * kHeads] : make_float2(-INFINITY, 0.0f);
+        const int64_t slot = (unit + parts.warp(s)) * kHeads;
+        part[k] = s < n ? ml[slot] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          v[k][i] = s < n && i * 32 + lane < quads ? po[static_cast<int64_t>(s) * kHeads * quads + i * 32 + lane]
+          v[k][i] = s < n && i * 32 + lane < quads ? po[slot * quads + i * 32 + lane]
                                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
       float x = top;
@@ -936,11 +987,12 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
 template <bool kNv, int DB>
 cudaError_t launch_dim(const AttentionParams& p, unsigned grid, cudaStream_t stream) {
   using S = Stage<kNv, DB>;
-  constexpr int kSmem = kWarps * kStages * S::kBytes;
   static std::atomic<uint64_t> ready[2] = {};
-  const auto kernel = p.ctas > 0 ? attention_kernel<kNv, DB, true> : attention_kernel<kNv, DB, false>;
-  if (const cudaError_t e = allow_smem(kernel, kSmem, ready[p.ctas > 0]); e != cudaSuccess) return e;
-  return launch_pdl_cluster(kernel, grid, kThreads, kSmem, stream, p.ctas, p);
+  const bool cluster = p.ctas > 0;
+  const auto kernel = cluster ? attention_kernel<kNv, DB, true> : attention_kernel<kNv, DB, false>;
+  const int smem = kWarps * stages_of(DB, cluster) * S::kBytes;
+  if (const cudaError_t e = allow_smem(kernel, smem, ready[cluster]); e != cudaSuccess) return e;
+  return launch_pdl_cluster(kernel, grid, kThreads, smem, stream, p.ctas, p);
 }
 
 template <bool kNv>
@@ -968,9 +1020,9 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
                     kThreads, 0, stream, p);
 }
 
-int64_t resident_warps(int32_t head_dim) {
-  return 152 * kWarps * (head_dim <= 64 ? 5 : head_dim <= 128 ? 4 : 2);
-}
+int64_t resident_ctas(int32_t head_dim, bool cluster) { return 152 * ctas_of(head_dim / 32, cluster); }
+// Contexts that one warp takes whole: a step.
+bool one_step(int64_t max_len) { return max_len <= kStep; }
 // CTAs of the cluster that takes a unit, as many as have a step for each warp and
 // are resident together, where that leaves a warp kFewSteps steps at most; else 0.
 // Without the second kernel and the workspace, but with the SMs idle that the
@@ -980,8 +1032,8 @@ int64_t resident_warps(int32_t head_dim) {
 int cluster_ctas(int64_t units, int32_t head_dim, int64_t max_len) {
   constexpr int64_t kFewSteps = 8;
   constexpr int kMost = 8;  // the portable size
-  if (max_len <= kAhead * kStep) return 0;
-  const int64_t steps = (max_len + kStep - 1) / kStep, most = resident_warps(head_dim) / kWarps;
+  if (one_step(max_len)) return 0;
+  const int64_t steps = (max_len + kStep - 1) / kStep, most = resident_ctas(head_dim, true);
   int ctas = 1;
   while (ctas < kMost && steps > ctas * kWarps && units * ctas * 2 <= most) ctas *= 2;
   return units * ctas <= most && steps <= kFewSteps * ctas * kWarps ? ctas : 0;
@@ -991,8 +1043,8 @@ int cluster_ctas(int64_t units, int32_t head_dim, int64_t max_len) {
 // once, so that all end together; 0 for contexts so short that a warp or a
 // cluster takes a unit whole.
 int shared_workers(int64_t units, int32_t head_dim, int64_t max_len) {
-  if (max_len <= kAhead * kStep || cluster_ctas(units, head_dim, max_len) > 0) return 0;
-  const int64_t resident = resident_warps(head_dim);
+  if (one_step(max_len) || cluster_ctas(units, head_dim, max_len) > 0) return 0;
+  const int64_t resident = resident_ctas(head_dim, false) * kWarps;
   const int64_t most = (units * ((max_len + kStep - 1) / kStep) + kWarps - 1) / kWarps * kWarps;
   return static_cast<int>(most < resident ? most : resident);
 }
@@ -1008,7 +1060,7 @@ int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_
   if (num_seqs == 0 || num_q_heads == 0 || head_dim == 0) return 0;
   const int64_t units = num_seqs * num_kv_heads * chunks_of(num_q_heads, num_kv_heads);
   const int workers = shared_workers(units, head_dim, max_len);
-  return workers > 0 ? (units + workers) * kHeads * (head_dim + 2) + 2 * units + workers : 0;
+  return workers > 0 ? (units + workers) * kHeads * (head_dim + 2) + 4 * units + workers : 0;
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) {
@@ -1051,8 +1103,8 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   p.ctas = cluster_ctas(units, c.head_dim, a.max_pages * c.page_size);
   p.part_o = a.workspace;
   p.part_ml = p.part_o + (units + p.workers) * kHeads * c.head_dim;
-  p.parts = reinterpret_cast<int32_t*>(p.part_ml + (units + p.workers) * kHeads * 2);
-  p.bad = p.parts + 2 * units;
+  p.parts = reinterpret_cast<int4*>(p.part_ml + (units + p.workers) * kHeads * 2);
+  p.bad = reinterpret_cast<int32_t*>(p.parts + units);
 #ifdef MXFP4_DEBUG_BOUNDS
   const int64_t rows = c.num_pages * c.page_size * c.num_heads;
   debug_range(p.dbg, kDbgQ, a.q, a.num_seqs > 0
@@ -1065,7 +1117,7 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
               a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
   debug_range(p.dbg, kDbgOut, a.out, a.num_seqs * a.num_q_heads * c.head_dim * 2);
   debug_range(p.dbg, kDbgPart, a.workspace,
-              p.workers > 0 ? ((units + p.workers) * kHeads * (c.head_dim + 2) + 2 * units + p.workers) * 4 : 0);
+              p.workers > 0 ? ((units + p.workers) * kHeads * (c.head_dim + 2) + 4 * units + p.workers) * 4 : 0);
 #endif
   const int64_t word = a.status != nullptr;
   const int64_t grid = p.workers > 0 ? p.workers / kWarps
