@@ -24,6 +24,11 @@ __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int n) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
+// The same for 16 bytes of a row of which the next stage takes the bytes that
+// follow: 256 at a time from HBM to L2.
+__device__ __forceinline__ void cp_async16_ahead(uint32_t dst, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int n) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }

@@ -83,7 +83,7 @@ struct MatvecParams {
   int32_t x_rows;     // token rows that x's shared memory holds
   int32_t x_pitch;    // bytes between them
   int32_t stages;     // of a warp's ring, 2 or 3
-  int32_t few;        // four stages to a warp at most: x is scaled by block at once
+  int32_t few;        // a stage to a warp at most: x is scaled by block at once
   int32_t y_f32;
   int32_t half_rows;  // rows of codes start at 8-byte (not 16-byte) boundaries
 #ifdef MXFP4_DEBUG_BOUNDS
@@ -293,9 +293,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     // ---- x: copied in 16-byte pieces, four to a 32-element block, and scaled to
     // halves in place below.  With fewer rows than warps, several warps share one.
     // It goes before the weights, so that its scaling runs beside their first
-    // copies (7168 x 7168 by 4 tokens: 14.4 -> 13.3 us), but with few stages to a
-    // warp after them: they are all under way then while the indexes of x are
-    // fetched (experts' 1536 x 2048 by 1 token: 11.1 -> 10.7 us).
+    // copies (7168 x 7168 by 4 tokens: 14.4 -> 13.3 us), but after them where a
+    // warp has one stage at most; x is then scaled by block, without the pass for
+    // the rows' largest (2048 x 768 by 1 token: 5.6 -> 5.4 us; with the 3 stages of
+    // experts' 1536 x 2048 by 1 token it took 10.0 -> 10.8).
     const int sharing = max(kWarps / n_rows, 1), rows_at_once = kWarps / sharing;
     const int my_row = warp / sharing < rows_at_once ? warp / sharing : n_rows;
     const int my_piece = (warp % sharing) * 32 + lane;
@@ -364,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint8_t* src = i < in.quarters ? row : p.codes;
-            cp_async<16>(to + i * 4 * kRowPitch, src,
-                         i < in.quarters && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 16) ? 16 : 0);
+            cp_async16_ahead(to + i * 4 * kRowPitch, src,
+                             i < in.quarters && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 16) ? 16 : 0);
             row += quarter;
           }
           cp_async16_if(scale_to, scale,
@@ -807,7 +808,7 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
       }
     }
   }
-  p.few = per_cta * p.chunks <= 4 * kWarps;
+  p.few = per_cta * p.chunks <= kWarps;
   p.x_pitch = p.panel * pitch_of_chunk + 64;
   const int smem = kWarps * p.stages * kStage + p.x_rows * (p.x_pitch + p.panel * xs_of_chunk) +
                    (p.panels > 1 ? p.batch + kWarps : 2 * kWarps) * slot_bytes;
