@@ -12,7 +12,14 @@
 // long calls and the launch the short ones.  A thread keeps one place of a
 // token's rows (keys or values, head, 16 consecutive elements: 32 bytes in, 8
 // out, or the reverse) and walks over tokens with kAtOnce of them in flight, so
-// that what depends on the place alone is worked out once.
+// that what depends on the place alone is worked out once (a place and a token to
+// each thread, found by divisions: 16 tokens 10.2 us, here 6.1, events around one
+// call).
+// Measured, BF16 to or from MXFP4, 8 heads of 128, slots in any order: 32768
+// tokens (170 MB) written in 30.1 us (5.6 TB/s) and read in 32.3 us (5.3 TB/s), 16
+// tokens in 1.9 and 1.8 us of device time.  The long calls issue on 65 % of the
+// cycles; reading in random order takes 32-byte sectors for 4 bytes of scales (56 MB
+// from HBM where the cache's are 36).
 #include <algorithm>
 #include <cstdint>
 
