@@ -34,7 +34,7 @@
 // Measured (device time, weights not in L2): 64000 x 7168 MXFP4 by 1 BF16 token
 // 45.5 us, 5.4 TB/s of 244 MB; the copies alone take most of that, the products
 // alone 35 us.  By 16 tokens 70 us (FP16 61): 61 % of the cycles issue, with x in
-// panels and two stages.  7168 x 7168 by 1 token 11.6 us, the 128 experts'
+// panels.  7168 x 7168 by 1 token 11.6 us, the 128 experts'
 // 1536 x 2048 NVFP4 by 64 tokens of 8 experts each 47.6 us (4.6 TB/s), 2048 x 768
 // by 1 token 5.4 us.
 #include <atomic>
@@ -60,6 +60,7 @@ constexpr int kBlocks = kChunk / 32;
 // fragment's words come from then lie in different banks.
 constexpr int kRowPitch = 144;
 constexpr int kStageCodes = kTile * kRowPitch;
+constexpr int kStages = 2;     // of a warp's ring (three: no faster, and less room for x)
 constexpr int kMaxUnits = 16;  // of a phase
 constexpr int kMaxRows = 64;   // of x, of a phase
 
@@ -89,7 +90,6 @@ struct MatvecParams {
   int32_t batch;      // tiles of a phase at most, with several panels
   int32_t x_rows;     // token rows that x's shared memory holds
   int32_t x_pitch;    // bytes between them
-  int32_t stages;     // of a warp's ring, 2 or 3
   int32_t few;        // a stage to a warp at most: x is scaled by block at once
   int32_t y_f32;
   int32_t half_rows;  // rows of codes start at 8-byte (not 16-byte) boundaries
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   // shared memory: rings | x halves | x block scales | parts of sums
-  const int ring_bytes = p.stages * kStage;
+  constexpr int ring_bytes = kStages * kStage;
   const uint32_t ring = smem_u32(smem) + warp * ring_bytes;
   uint8_t* const x_s = smem + kWarps * ring_bytes;
   static_assert(sizeof(Shared) <= 5 * 1024, "kMaxSmem leaves this much");
@@ -407,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       }
       cp_commit();  // an empty group at the end keeps the count of groups
     };
-    for (int i = 0; i < p.stages; ++i) issue();
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) issue();
 
     // a tile's sums of this lane (rows g and g + 8, columns 2c and 2c + 1 of
     // each block of 8) to y
@@ -455,10 +456,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
         __syncthreads();
         copy_x(lo, pieces);
         cp_wait<0>();
-      } else if (p.stages == 3) {
-        cp_wait<3>();  // all but the ring
       } else {
-        cp_wait<2>();
+        cp_wait<kStages>();  // all but the ring
       }
       bool by_row = true;  // one power of two for a row's whole panel of x
       if constexpr (!kF16) {
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           xa[t] = smem_u32(x_s) + (u.x + min(t * 8 + g, u.n - 1)) * p.x_pitch + c * 16 + ch * (kChunk * 2);
         [[maybe_unused]] uint32_t sx = smem_u32(xs_s) + (ch * kBlocks * p.x_rows + u.x + 2 * c) * 4;
         for (int f = 0; f < len; ++f) {
-          if (p.stages == 3) cp_wait<2>(); else cp_wait<1>();
+          cp_wait<kStages - 1>();
           __syncwarp();  // the copies of all lanes are in
           const uint32_t st = out_at;
           out_at += kStage;
@@ -781,26 +780,20 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
   const int pitch_of_chunk = kChunk * 2, xs_of_chunk = kF16 ? 0 : kBlocks * 4;
   int64_t spanned = per_cta / (p.tiles > 0 ? p.tiles : 1) + 2;  // units that a CTA's tiles meet
   if (p.offsets == nullptr && spanned > expected_units) spanned = expected_units;
-  int64_t fewest = -1;
-  for (int stages = 3; stages >= 2; --stages) {
-    const int free_bytes = kMaxSmem - kWarps * stages * kStage;
-    // whole: two slots per warp, and as many rows as there is room and use for
-    const int row_bytes = p.chunks * (pitch_of_chunk + xs_of_chunk) + 64;
-    const int64_t fit = (free_bytes - 2 * kWarps * slot_bytes) / row_bytes & ~1;
+  const int free_bytes = kMaxSmem - kWarps * kStages * kStage;
+  // whole: two slots per warp, and as many rows as there is room and use for
+  const int row_bytes = p.chunks * (pitch_of_chunk + xs_of_chunk) + 64;
+  const int64_t fit = (free_bytes - 2 * kWarps * slot_bytes) / row_bytes & ~1;
+  if (fit >= unit_rows) {
     const int64_t use = spanned * unit_rows < kMaxRows ? spanned * unit_rows : kMaxRows;
-    if (fit >= unit_rows) {
-      const int64_t phases = (use + fit - 1) / fit;
-      if (fewest < 0 || phases < fewest) {
-        fewest = phases;
-        p.stages = stages;
-        p.panels = p.chunks > 0 ? 1 : 0;
-        p.panel = p.chunks;
-        p.batch = 0;
-        p.x_rows = static_cast<int32_t>(fit < use ? fit : use);
-      }
-      continue;
-    }
-    for (int64_t n_batches = 1; n_batches <= (per_cta > 1 ? per_cta : 1) && n_batches <= 64; ++n_batches) {
+    p.panels = p.chunks > 0 ? 1 : 0;
+    p.panel = p.chunks;
+    p.batch = 0;
+    p.x_rows = static_cast<int32_t>(fit < use ? fit : use);
+  } else {
+    int64_t fewest = -1;
+    for (int64_t n_batches = 1; n_batches <= (per_cta > 1 ? per_cta : 1) && (n_batches <= 64 || fewest < 0);
+         ++n_batches) {
       const int64_t tiles = ((per_cta > 1 ? per_cta : 1) + n_batches - 1) / n_batches;
       const int64_t room = free_bytes - (tiles + kWarps) * slot_bytes - unit_rows * 64;
       const int64_t chunks = room / (unit_rows * (pitch_of_chunk + xs_of_chunk));
@@ -809,7 +802,6 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
       if (panels < 2) panels = 2;  // there is room for the chunks, not for a whole x's slots
       if (fewest < 0 || n_batches * panels < fewest) {
         fewest = n_batches * panels;
-        p.stages = stages;
         p.panels = static_cast<int32_t>(panels);
         p.panel = static_cast<int32_t>((p.chunks + panels - 1) / panels);
         p.batch = static_cast<int32_t>(tiles);
@@ -819,7 +811,7 @@ cudaError_t launch_typed(MatvecParams p, int64_t expected_units, int nt, cudaStr
   }
   p.few = per_cta * p.chunks <= kWarps;
   p.x_pitch = p.panel * pitch_of_chunk + 64;
-  const int smem = kWarps * p.stages * kStage + p.x_rows * (p.x_pitch + p.panel * xs_of_chunk) +
+  const int smem = kWarps * kStages * kStage + p.x_rows * (p.x_pitch + p.panel * xs_of_chunk) +
                    (p.panels > 1 ? p.batch + kWarps : 2 * kWarps) * slot_bytes;
   static std::atomic<uint64_t> ready[2];  // devices on which each kernel may use kMaxSmem
   if (const cudaError_t e = allow_smem(kernel, kMaxSmem, ready[nt - 1]); e != cudaSuccess) return e;
