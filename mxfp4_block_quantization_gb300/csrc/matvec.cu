@@ -163,7 +163,8 @@ struct Cursor {
   int panel, f;              // the panel of x; where the run after this one starts
   int chunk, left;           // the next chunk, and the chunks left of this run (one tile's)
   int quarters;              // of the tile's four 32-row quarters, those in which this lane's row is in N
-  const uint8_t* row;        // this lane's piece of its row of the first quarter, chunk 0
+  bool whole;                // all lanes' rows are in N, and start at 16-byte boundaries
+  const uint8_t* row;        // this lane's piece of its row of the first quarter, of the next chunk
   const uint8_t* scale;
 };
 
@@ -353,9 +354,12 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
         const int e = sh.unit[i].e;
         const int base = (tile >> 3) * 128 + (tile & 7) * 4 + copy_row;
         in.quarters = base < p.N ? min(4, (p.N - base + 31) >> 5) : 0;
-        in.row = p.codes + e * p.expert_codes + (in.quarters ? base : 0) * static_cast<int64_t>(p.K >> 1) + copy_at;
+        in.whole = !p.half_rows && __all_sync(0xFFFFFFFFu, in.quarters == 4);
+        in.row = p.codes + e * p.expert_codes + (in.quarters ? base : 0) * static_cast<int64_t>(p.K >> 1) + copy_at +
+                 in.chunk * (kChunk / 2);
         in.scale = p.scales + e * p.expert_scales + (tile & 7) * 64 +
-                   (static_cast<int64_t>(tile >> 3) * p.nKT + (lane >> 2)) * kChunkBytes + (lane & 3) * 16;
+                   (static_cast<int64_t>(tile >> 3) * p.nKT + in.chunk * kChunkKt + (lane >> 2)) * kChunkBytes +
+                   (lane & 3) * 16;
         return;
       }
     };
@@ -365,21 +369,21 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     auto issue = [&]() {
       if (more) {
         const uint32_t to = in_at + copy_to, scale_to = in_at + kStageCodes + lane * 16;
-        const uint8_t* row = in.row + static_cast<uint32_t>(in.chunk) * static_cast<uint64_t>(kChunk / 2);
-        const uint8_t* const scale =
-            in.scale + static_cast<uint32_t>(in.chunk) * static_cast<uint64_t>(kChunkKt * kChunkBytes);
-        if (!p.half_rows && in.chunk != tail) {
+        const uint8_t* row = in.row;
+        const uint8_t* const scale = in.scale;
+        in.row += kChunk / 2;
+        in.scale += kChunkKt * kChunkBytes;
+        if (in.whole && in.chunk != tail) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint8_t* src = i < in.quarters ? row : p.codes;
-            cp_async16_ahead(to + i * 4 * kRowPitch, src,
-                             i < in.quarters && MXFP4_IN_BOUNDS(p, kDbgCodes, src, 16) ? 16 : 0);
+            cp_async16_ahead(to + i * 4 * kRowPitch, row, MXFP4_IN_BOUNDS(p, kDbgCodes, row, 16) ? 16 : 0);
             row += quarter;
           }
           cp_async16_if(scale_to, scale,
                         lane < kScaleBytes / 16 && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16));
         } else {
-          // the last, partial chunk, and rows that start at 8-byte boundaries
+          // rows past N, the last, partial chunk, and rows that start at 8-byte
+          // boundaries
           const int k = in.chunk * kChunk + copy_at * 2;
           for (int i = 0; i < 4; ++i) {
             if (!p.half_rows) {
