@@ -17,6 +17,7 @@
 //   output  O^T [16 values of D x 8 heads] = V^T [16 x 16 positions] P^T:
 //           ldmatrix transposes V's 16-bit groups of four codes, so a
 //           register holds four codes of each of two positions.
+// With more heads to a kv head a unit may have two such column blocks.
 // The sums keep the heads in the same columns in both, so the softmax's
 // rescaling needs no exchange.
 //
@@ -64,10 +65,11 @@ constexpr int kStep = 32;   // positions of a warp's step
 // 128, 40.8 -> 42.6), but not with a cluster to each unit, whose few steps want the
 // warps (64 of 1024 positions: 21.7 us, with three stages 26.6).
 __host__ __device__ constexpr int stages_of(int blocks, bool cluster) { return cluster || blocks > 4 ? 2 : 3; }
-__host__ __device__ constexpr int ctas_of(int blocks, bool cluster) {
+__host__ __device__ constexpr int ctas_of(int blocks, bool cluster, int column_blocks) {
+  if (column_blocks > 1) return blocks <= 2 ? 3 : 2;
   return (blocks <= 2 ? 5 : blocks <= 4 ? 4 : 2) - (cluster || blocks > 4 ? 0 : 1);
 }
-constexpr int kHeads = 8;   // query heads of a CTA: the columns of the products
+constexpr int kColumns = 8;  // query heads of a column block of the products
 constexpr float kLag = 3.0f;  // log2: how far a warp's reference may lag behind its maximum
                               // (0: 64 sequences of 8192 99.1 -> 100.2 us)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -96,7 +98,8 @@ struct AttentionParams {
   int32_t num_q_heads;
   int32_t num_kv_heads;
   int32_t group;     // query heads of a kv head
-  int32_t chunks;    // CTAs of 8 query heads per kv head
+  int32_t columns;   // query heads of a unit, 8 or 16
+  int32_t chunks;    // units of a kv head
   int32_t workers;   // warps that share the positions; 0: a warp, or a cluster, per unit
   int32_t ctas;      // of a unit's cluster, or 0
   int32_t num_pages;
@@ -364,7 +367,7 @@ __device__ __forceinline__ void own_scales(uint32_t (&k)[S::kWords], uint32_t (&
 // rings, joined: each thread four values of a head, the parts read from the CTAs'
 // shared memory kBatch at a time.  `store(head, quad, acc, sum, top)`.  (Each warp's
 // part to the workspace instead: one sequence of 131072, head_dim 64, 28.3 -> 31.1 us.)
-template <int DB, bool kCluster, typename Store>
+template <int DB, bool kCluster, int kHeads, typename Store>
 __device__ __forceinline__ void join_rings(uint32_t rings, uint32_t ring_bytes, int ctas, int heads, Store store) {
   constexpr int D = 32 * DB, kQuads = D / 4, kBatch = kCluster ? 8 : kWarps;
   const int parts = ctas * kWarps;
@@ -409,8 +412,9 @@ __device__ __forceinline__ void join_rings(uint32_t rings, uint32_t ring_bytes, 
   }
 }
 
-template <bool kNv, int DB, bool kCluster>
-__global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_kernel(const AttentionParams p) {
+template <bool kNv, int DB, bool kCluster, int NB>
+__global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention_kernel(const AttentionParams p) {
+  constexpr int kHeads = NB * kColumns;
   constexpr int kStages = stages_of(DB, kCluster), kAhead = kStages - 1;
   using S = Stage<kNv, DB>;
   constexpr int D = 32 * DB;
@@ -569,19 +573,22 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
 
     // ---- q: a lane holds elements 8c..8c+7 of each 32-element block of head g,
     // as halves; BF16 scaled by the head's power of two (see matvec.cu)
-    uint4 q[DB];
-    float qs0, qs1;  // what undoes it, with the softmax's scale, for heads 2c and 2c + 1
-    {
+    uint4 q[NB][DB];
+    float qs[NB][2];  // what undoes it, with the softmax's scale, for heads 2c and 2c + 1 of a block
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      const int h = n * kColumns + g;
       const uint16_t* qp = reinterpret_cast<const uint16_t*>(p.q) + b * p.q_seq_stride +
-                           static_cast<int64_t>(head0 + g) * p.q_head_stride + c * 8;
+                           static_cast<int64_t>(head0 + h) * p.q_head_stride + c * 8;
       uint32_t m = 0u;
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        q[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (g < heads && MXFP4_IN_BOUNDS(p, kDbgQ, qp + i * 32, 16))
-          q[i] = __ldg(reinterpret_cast<const uint4*>(qp + i * 32));
-        m = max_finite_bf16x2(max_finite_bf16x2(m, q[i].x), q[i].y);
-        m = max_finite_bf16x2(max_finite_bf16x2(m, q[i].z), q[i].w);
+        uint4& v = q[n][i];
+        v = make_uint4(0u, 0u, 0u, 0u);
+        if (h < heads && MXFP4_IN_BOUNDS(p, kDbgQ, qp + i * 32, 16))
+          v = __ldg(reinterpret_cast<const uint4*>(qp + i * 32));
+        m = max_finite_bf16x2(max_finite_bf16x2(m, v.x), v.y);
+        m = max_finite_bf16x2(max_finite_bf16x2(m, v.z), v.w);
       }
       float inverse = 1.0f;
       if (!p.f16) {
@@ -593,27 +600,29 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
         };
 #pragma unroll
         for (int i = 0; i < DB; ++i)
-          q[i] = make_uint4(scaled(q[i].x), scaled(q[i].y), scaled(q[i].z), scaled(q[i].w));
+          q[n][i] = make_uint4(scaled(q[n][i].x), scaled(q[n][i].y), scaled(q[n][i].z), scaled(q[n][i].w));
       }
-      if (p.softmax_scale < 0.0f) {  // its sign goes into q: a larger product is a larger score
+      const uint32_t sign = p.softmax_scale < 0.0f ? 0x80008000u : 0u;  // a larger product is a larger score
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
-          q[i] = make_uint4(q[i].x ^ 0x80008000u, q[i].y ^ 0x80008000u, q[i].z ^ 0x80008000u, q[i].w ^ 0x80008000u);
-      }
+      for (int i = 0; i < DB; ++i)
+        q[n][i] = make_uint4(q[n][i].x ^ sign, q[n][i].y ^ sign, q[n][i].z ^ sign, q[n][i].w ^ sign);
       // (not zero: a masked score is -infinity, and stays that)
       const float more = fmaxf(fabsf(p.softmax_scale), 0x1p-126f) * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
-      qs0 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c);
-      qs1 = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4);
-      qs0 *= more;
-      qs1 *= more;
+      qs[n][0] = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c) * more;
+      qs[n][1] = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4) * more;
     }
 
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;  // of heads 2c and 2c + 1, log2
-    float o[DB][2][4];
+    float m[NB][2], l[NB][2];  // of heads 2c and 2c + 1 of a block, log2
+    float o[NB][DB][2][4];
 #pragma unroll
-    for (int i = 0; i < DB; ++i)
+    for (int n = 0; n < NB; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] = 0.0f;
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[n][i][j >> 2][j & 3] = 0.0f;
+    }
     int vref[DB];  // MXFP4: the largest scale byte of V so far, per block (same in all lanes)
 #pragma unroll
     for (int i = 0; i < DB; ++i) vref[i] = 0;
@@ -651,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
               const float f = __uint_as_float(static_cast<uint32_t>(max(127 + vref[i] - now, 0)) << 23);
               vref[i] = now;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= f;
+              for (int j = 0; j < 8 * NB; ++j) o[j >> 3][i][(j >> 2) & 1][j & 3] *= f;
             }
           }
           const uint32_t to = st + S::kScaleV + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
@@ -665,12 +674,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
       issue(next_page);
       const uint32_t valid = lds32(st + S::kValid);
 
-      // ---- scores of 2 x 16 positions by 8 heads
-      float s[2][4];
+      // ---- scores of 2 x 16 positions by 8 heads of each block
+      float s[NB][2][4];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] = 0.0f;
+        for (int i = 0; i < 4 * NB; ++i) s[i >> 2][t][i & 3] = 0.0f;
         uint32_t w0[S::kWords], w1[S::kWords];  // scales of positions g and g + 8
         float f0[DB], f1[DB];
         if constexpr (kNv) {
@@ -698,16 +707,22 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
               a0[k] = hmul2(a0[k], e0);
               a1[k] = hmul2(a1[k], e1);
             }
-            mma16816(s[t], a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
-            mma16816(s[t], a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              mma16816(s[n][t], a0[0], a1[0], a0[1], a1[1], q[n][i].x, q[n][i].y);
+              mma16816(s[n][t], a0[2], a1[2], a0[3], a1[3], q[n][i].z, q[n][i].w);
+            }
           } else {
-            float d[4];
-            mma16816_first(d, a0[0], a1[0], a0[1], a1[1], q[i].x, q[i].y);
-            mma16816(d, a0[2], a1[2], a0[3], a1[3], q[i].z, q[i].w);
-            s[t][0] = fmaf(d[0], f0[i], s[t][0]);
-            s[t][1] = fmaf(d[1], f0[i], s[t][1]);
-            s[t][2] = fmaf(d[2], f1[i], s[t][2]);
-            s[t][3] = fmaf(d[3], f1[i], s[t][3]);
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+              float d[4];
+              mma16816_first(d, a0[0], a1[0], a0[1], a1[1], q[n][i].x, q[n][i].y);
+              mma16816(d, a0[2], a1[2], a0[3], a1[3], q[n][i].z, q[n][i].w);
+              s[n][t][0] = fmaf(d[0], f0[i], s[n][t][0]);
+              s[n][t][1] = fmaf(d[1], f0[i], s[n][t][1]);
+              s[n][t][2] = fmaf(d[2], f1[i], s[n][t][2]);
+              s[n][t][3] = fmaf(d[3], f1[i], s[n][t][3]);
+            }
           }
         }
       }
@@ -717,64 +732,76 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            if (((valid >> (t * 16 + g + 8 * r)) & 1u) == 0u) s[t][2 * r] = s[t][2 * r + 1] = -INFINITY;
+            if (((valid >> (t * 16 + g + 8 * r)) & 1u) == 0u) {
+#pragma unroll
+              for (int n = 0; n < NB; ++n) s[n][t][2 * r] = s[n][t][2 * r + 1] = -INFINITY;
+            }
       }
 
       // ---- running maximum and sum.  The reference m may lag behind the
       // maximum by kLag (P then grows to 2^kLag at most, far inside a half), so
       // that the output is rescaled a few times at all, not at every new maximum.
-      float x0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])) * qs0;
-      float x1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3])) * qs1;
-      if (__any_sync(0xFFFFFFFFu, x0 > m0 + kLag || x1 > m1 + kLag)) {
+      float x[NB][2];
+      bool far = false;
 #pragma unroll
-        for (int k = 4; k < 32; k *= 2) {
-          x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, k));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, k));
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[n][e] = fmaxf(fmaxf(s[n][0][e], s[n][0][2 + e]), fmaxf(s[n][1][e], s[n][1][2 + e])) * qs[n][e];
+          far |= x[n][e] > m[n][e] + kLag;
         }
-        x0 = fmaxf(x0, m0);
-        x1 = fmaxf(x1, m1);
-        const float k0 = exp2_approx(m0 - (x0 == -INFINITY ? 0.0f : x0));
-        const float k1 = exp2_approx(m1 - (x1 == -INFINITY ? 0.0f : x1));
-        m0 = x0;
-        m1 = x1;
-        l0 *= k0;
-        l1 *= k1;
+      if (__any_sync(0xFFFFFFFFu, far)) {
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[i][j >> 2][j & 3] *= j & 1 ? k1 : k0;
+          for (int e = 0; e < 2; ++e) {
+            float y = x[n][e];
+#pragma unroll
+            for (int k = 4; k < 32; k *= 2) y = fmaxf(y, __shfl_xor_sync(0xFFFFFFFFu, y, k));
+            y = fmaxf(y, m[n][e]);
+            const float keep = exp2_approx(m[n][e] - (y == -INFINITY ? 0.0f : y));
+            m[n][e] = y;
+            l[n][e] *= keep;
+#pragma unroll
+            for (int i = 0; i < DB; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) o[n][i][j >> 1][(j & 1) * 2 + e] *= keep;
+          }
       }
-      const float z0 = m0 == -INFINITY ? 0.0f : m0, z1 = m1 == -INFINITY ? 0.0f : m1;
-      uint32_t pk[2][2];  // P of positions g and g + 8 of each half, heads 2c and 2c + 1
+      uint32_t pt[NB][2][2];  // P^T of each block: columns of heads, pairs of positions
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int n = 0; n < NB; ++n) {
+        const float z0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], z1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+        uint32_t pk[2][2];  // P of positions g and g + 8 of each half, heads 2c and 2c + 1
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float e0 = exp2_approx(fmaf(s[t][2 * r], qs0, -z0)), e1 = exp2_approx(fmaf(s[t][2 * r + 1], qs1, -z1));
-          l0 += e0;
-          l1 += e1;
-          pk[t][r] = pack_f16x2(e0, e1);
-        }
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float e0 = exp2_approx(fmaf(s[n][t][2 * r], qs[n][0], -z0));
+            const float e1 = exp2_approx(fmaf(s[n][t][2 * r + 1], qs[n][1], -z1));
+            l[n][0] += e0;
+            l[n][1] += e1;
+            pk[t][r] = pack_f16x2(e0, e1);
+          }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) pt[n][t][r] = movmatrix_trans(pk[t][r]);
+      }
 
       // ---- output
-      uint32_t pt[2][2];  // P^T: columns of heads, pairs of positions
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) pt[t][r] = movmatrix_trans(pk[t][r]);
       const uint32_t va = st + S::kV + lane * S::kPitch;
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        uint32_t pb[2][2];
-        if constexpr (kNv) {
+        uint32_t pb[NB][2][2];
+        uint4 f = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (!kNv) f = lds128(st + S::kScaleV + i * 64 + c * 16);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) pb[k >> 1][k & 1] = pt[k >> 1][k & 1];
-        } else {
-          const uint4 f = lds128(st + S::kScaleV + i * 64 + c * 16);
-          pb[0][0] = hmul2(pt[0][0], f.x);
-          pb[0][1] = hmul2(pt[0][1], f.y);
-          pb[1][0] = hmul2(pt[1][0], f.z);
-          pb[1][1] = hmul2(pt[1][1], f.w);
+        for (int n = 0; n < NB; ++n) {
+          pb[n][0][0] = kNv ? pt[n][0][0] : hmul2(pt[n][0][0], f.x);
+          pb[n][0][1] = kNv ? pt[n][0][1] : hmul2(pt[n][0][1], f.y);
+          pb[n][1][0] = kNv ? pt[n][1][0] : hmul2(pt[n][1][0], f.z);
+          pb[n][1][1] = kNv ? pt[n][1][1] : hmul2(pt[n][1][1], f.w);
         }
         uint32_t v[4];
         ldmatrix4_trans(v, va + i * 16);
@@ -795,10 +822,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
           }
         }
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          mma16816(o[i][0], h[2 * t][0], h[2 * t][1], h[2 * t + 1][0], h[2 * t + 1][1], pb[t][0], pb[t][1]);
-          mma16816(o[i][1], h[2 * t][2], h[2 * t][3], h[2 * t + 1][2], h[2 * t + 1][3], pb[t][0], pb[t][1]);
-        }
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            mma16816(o[n][i][0], h[2 * t][0], h[2 * t][1], h[2 * t + 1][0], h[2 * t + 1][1], pb[n][t][0], pb[n][t][1]);
+            mma16816(o[n][i][1], h[2 * t][2], h[2 * t][3], h[2 * t + 1][2], h[2 * t + 1][3], pb[n][t][0], pb[n][t][1]);
+          }
       }
     }
     cp_wait<0>();
@@ -807,10 +836,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
 
     // ---- the result, or this part of it
 #pragma unroll
-    for (int k = 4; k < 32; k *= 2) {
-      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, k);
-      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, k);
-    }
+    for (int k = 4; k < 32; k *= 2)
+#pragma unroll
+      for (int j = 0; j < 2 * NB; ++j) l[j >> 1][j & 1] += __shfl_xor_sync(0xFFFFFFFFu, l[j >> 1][j & 1], k);
     // slot unit + warp: the shares are consecutive, so no two parts have the same
     const int64_t unit_slot = static_cast<int64_t>(b) * units_per_seq + unit;
     auto store_part = [&](int holder, int h, int quad, float4 v) {
@@ -823,9 +851,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
     };
     const int64_t head_at = static_cast<int64_t>(b) * p.num_q_heads + head0;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {  // heads 2c and 2c + 1; four values of each block in a lane
-      const int h = 2 * c + e;
-      const float top = e ? m1 : m0, sum = e ? l1 : l0;
+    for (int j = 0; j < 2 * NB; ++j) {  // heads 2c and 2c + 1; four values of each 32 in a lane
+      const int n = j >> 1, e = j & 1, h = n * kColumns + 2 * c + e;
+      const float top = m[n][e], sum = l[n][e];
       if (h >= heads) continue;
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
@@ -833,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
         float f = 1.0f;
         if constexpr (!kNv)
           f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-12f;
-        const float4 v = make_float4(o[i][0][e] * f, o[i][0][2 + e] * f, o[i][1][e] * f, o[i][1][2 + e] * f);
+        const float4 v = make_float4(o[n][i][0][e] * f, o[n][i][0][2 + e] * f, o[n][i][1][e] * f, o[n][i][1][2 + e] * f);
         const int d = i * 32 + 4 * g;
         if (in_ring) {
           sts128(ring + (h * D + d) * 4, __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
@@ -857,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
     if constexpr (kCluster) {
       __syncwarp();
       cluster_sync();
-      join_rings<DB, true>(smem_u32(smem), kStages * S::kBytes, ctas, heads,
+      join_rings<DB, true, kHeads>(smem_u32(smem), kStages * S::kBytes, ctas, heads,
                            [&](int h, int quad, float4 v, float sum, float top) {
                              store_out<kNv>(p, head_at + h, 4 * quad, D, v, sum);
                              if (quad == 0) store_lse(p, head_at + h, sum, top);
@@ -866,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster)) attention_ker
       cluster_sync();  // no CTA leaves while its parts are read
     } else if (joined) {  // this warp's last unit: the barrier is the CTA's
       __syncthreads();
-      join_rings<DB, false>(smem_u32(smem), kStages * S::kBytes, 1, heads,
+      join_rings<DB, false, kHeads>(smem_u32(smem), kStages * S::kBytes, 1, heads,
                             [&](int h, int quad, float4 v, float sum, float top) {
                               if (whole) {
                                 store_out<kNv>(p, head_at + h, 4 * quad, D, v, sum);
@@ -911,7 +939,7 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
   if (head >= static_cast<int64_t>(p.num_seqs) * p.num_q_heads) return;
   const int b = static_cast<int>(head / p.num_q_heads), h = static_cast<int>(head - static_cast<int64_t>(b) * p.num_q_heads);
   const int kvh = h / p.group, in_group = h - kvh * p.group;
-  const int64_t unit = (static_cast<int64_t>(b) * p.chunks + in_group / kHeads) * p.num_kv_heads + kvh;
+  const int64_t unit = (static_cast<int64_t>(b) * p.chunks + in_group / p.columns) * p.num_kv_heads + kvh;
   const int quads = p.head_dim / 4;
   float top = -INFINITY, sum = 0.0f;
   float4 acc[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
@@ -920,8 +948,8 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
     const Parts parts{who.x, who.y, who.z, who.w};
     const int n = parts.count();
     if (n == 1) return;  // written already
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + in_group % kHeads;
-    const float4* po = reinterpret_cast<const float4*>(p.part_o) + in_group % kHeads * quads;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + in_group % p.columns;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o) + in_group % p.columns * quads;
     // one pass, kBatch parts' loads in flight
     constexpr int kBatch = 6;
     for (int s0 = kPerHead == 1 ? 0 : warp; s0 < n; s0 += kBatch * kPerHead) {
@@ -930,7 +958,7 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         const int s = s0 + k * kPerHead;
-        const int64_t slot = (unit + parts.warp(s)) * kHeads;
+        const int64_t slot = (unit + parts.warp(s)) * p.columns;
         part[k] = s < n ? ml[slot] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -1000,29 +1028,33 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
   pdl_release();
 }
 
-template <bool kNv, int DB>
+template <bool kNv, int DB, int NB>
 cudaError_t launch_dim(const AttentionParams& p, unsigned grid, cudaStream_t stream) {
   using S = Stage<kNv, DB>;
   static std::atomic<uint64_t> ready[2] = {};
   const bool cluster = p.ctas > 0;
-  const auto kernel = cluster ? attention_kernel<kNv, DB, true> : attention_kernel<kNv, DB, false>;
+  const auto kernel = cluster ? attention_kernel<kNv, DB, true, NB> : attention_kernel<kNv, DB, false, NB>;
   const int smem = kWarps * stages_of(DB, cluster) * S::kBytes;
   if (const cudaError_t e = allow_smem(kernel, smem, ready[cluster]); e != cudaSuccess) return e;
   return launch_pdl_cluster(kernel, grid, kThreads, smem, stream, p.ctas, p);
+}
+template <bool kNv, int DB>
+cudaError_t launch_columns(const AttentionParams& p, unsigned grid, cudaStream_t stream) {
+  return p.columns == kColumns ? launch_dim<kNv, DB, 1>(p, grid, stream) : launch_dim<kNv, DB, 2>(p, grid, stream);
 }
 
 template <bool kNv>
 cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   switch (p.head_dim / 32) {
-    case 1: e = launch_dim<kNv, 1>(p, grid, stream); break;
-    case 2: e = launch_dim<kNv, 2>(p, grid, stream); break;
-    case 3: e = launch_dim<kNv, 3>(p, grid, stream); break;
-    case 4: e = launch_dim<kNv, 4>(p, grid, stream); break;
-    case 5: e = launch_dim<kNv, 5>(p, grid, stream); break;
-    case 6: e = launch_dim<kNv, 6>(p, grid, stream); break;
-    case 7: e = launch_dim<kNv, 7>(p, grid, stream); break;
-    default: e = launch_dim<kNv, 8>(p, grid, stream); break;
+    case 1: e = launch_columns<kNv, 1>(p, grid, stream); break;
+    case 2: e = launch_columns<kNv, 2>(p, grid, stream); break;
+    case 3: e = launch_columns<kNv, 3>(p, grid, stream); break;
+    case 4: e = launch_columns<kNv, 4>(p, grid, stream); break;
+    case 5: e = launch_dim<kNv, 5, 1>(p, grid, stream); break;
+    case 6: e = launch_dim<kNv, 6, 1>(p, grid, stream); break;
+    case 7: e = launch_dim<kNv, 7, 1>(p, grid, stream); break;
+    default: e = launch_dim<kNv, 8, 1>(p, grid, stream); break;
   }
   if (e != cudaSuccess || p.workers == 0) return e;
   const int64_t heads = static_cast<int64_t>(p.num_seqs) * p.num_q_heads;
@@ -1039,7 +1071,9 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
                     kThreads, 0, stream, p);
 }
 
-int64_t resident_ctas(int32_t head_dim, bool cluster) { return 152 * ctas_of(head_dim / 32, cluster); }
+int64_t resident_ctas(int32_t head_dim, bool cluster, int columns) {
+  return 152 * ctas_of(head_dim / 32, cluster, columns / kColumns);
+}
 // Contexts that one warp takes whole: a step.
 bool one_step(int64_t max_len) { return max_len <= kStep; }
 // CTAs of the cluster that takes a unit, as many as have a step for each warp and
@@ -1048,11 +1082,11 @@ bool one_step(int64_t max_len) { return max_len <= kStep; }
 // clusters leave: 8.5 -> 6.5 us for one sequence of 700 positions (64 heads on 8,
 // head_dim 128), 26.9 -> 21.8 for 64 of up to 1024 (8 steps); at 12 steps, one
 // of 12000, 14.3 -> 15.8.
-int cluster_ctas(int64_t units, int32_t head_dim, int64_t max_len) {
+int cluster_ctas(int64_t units, int32_t head_dim, int columns, int64_t max_len) {
   constexpr int64_t kFewSteps = 8;
   constexpr int kMost = 8;  // the portable size
   if (one_step(max_len)) return 0;
-  const int64_t steps = (max_len + kStep - 1) / kStep, most = resident_ctas(head_dim, true);
+  const int64_t steps = (max_len + kStep - 1) / kStep, most = resident_ctas(head_dim, true, columns);
   int ctas = 1;
   while (ctas < kMost && steps > ctas * kWarps && units * ctas * 2 <= most) ctas *= 2;
   return units * ctas <= most && steps <= kFewSteps * ctas * kWarps ? ctas : 0;
@@ -1061,15 +1095,25 @@ int cluster_ctas(int64_t units, int32_t head_dim, int64_t max_len) {
 // Warps that share the positions of all sequences: as many as the GPU holds at
 // once, so that all end together; 0 for contexts so short that a warp or a
 // cluster takes a unit whole.
-int shared_workers(int64_t units, int32_t head_dim, int64_t max_len) {
-  if (one_step(max_len) || cluster_ctas(units, head_dim, max_len) > 0) return 0;
-  const int64_t resident = resident_ctas(head_dim, false) * kWarps;
+int shared_workers(int64_t units, int32_t head_dim, int columns, int64_t max_len) {
+  if (one_step(max_len) || cluster_ctas(units, head_dim, columns, max_len) > 0) return 0;
+  const int64_t resident = resident_ctas(head_dim, false, columns) * kWarps;
   const int64_t most = (units * ((max_len + kStep - 1) / kStep) + kWarps - 1) / kWarps * kWarps;
   return static_cast<int>(most < resident ? most : resident);
 }
 
-int chunks_of(int32_t num_q_heads, int32_t num_kv_heads) {
-  return (num_q_heads / num_kv_heads + kHeads - 1) / kHeads;
+// Query heads of a unit: two column blocks, for which the cache is decoded once,
+// where a kv head has more than 8, the registers hold them, and each warp has 2.5
+// steps or more with one.  128 heads on 8 of 128: 32 sequences of up to 4096 55.2 ->
+// 48.3 us; one of 700, with half as many warps to share it, 7.6 -> 8.7.  64 heads on
+// 4 of 64, 8 of 4096 (2.7 steps): 13.2 -> 10.7; 80 on 5 of 128, 16 of 1000 (2.1):
+// 11.2 -> 11.9.
+int columns_of(int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int64_t max_len) {
+  const int group = num_q_heads / num_kv_heads;
+  if (group <= kColumns || head_dim > 128) return kColumns;
+  const int64_t units = num_seqs * num_kv_heads * ((group + kColumns - 1) / kColumns);
+  const int64_t steps = units * ((max_len + kStep - 1) / kStep);
+  return 2 * steps >= 5 * kWarps * resident_ctas(head_dim, true, kColumns) ? 2 * kColumns : kColumns;
 }
 
 }  // namespace
@@ -1077,9 +1121,11 @@ int chunks_of(int32_t num_q_heads, int32_t num_kv_heads) {
 int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                    int32_t head_dim, int64_t max_len) {
   if (num_seqs == 0 || num_q_heads == 0 || head_dim == 0) return 0;
-  const int64_t units = num_seqs * num_kv_heads * chunks_of(num_q_heads, num_kv_heads);
-  const int workers = shared_workers(units, head_dim, max_len);
-  return workers > 0 ? (units + workers) * kHeads * (head_dim + 2) + 4 * units + workers : 0;
+  const int group = num_q_heads / num_kv_heads;
+  const int columns = columns_of(num_seqs, num_q_heads, num_kv_heads, head_dim, max_len);
+  const int64_t units = num_seqs * num_kv_heads * ((group + columns - 1) / columns);
+  const int workers = shared_workers(units, head_dim, columns, max_len);
+  return workers > 0 ? (units + workers) * columns * (head_dim + 2) + 4 * units + workers : 0;
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) {
@@ -1116,13 +1162,14 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
     return launch_pdl(attention_status_kernel, 1, kThreads, 0, stream, p);
   }
   p.group = a.num_q_heads / c.num_heads;
-  p.chunks = chunks_of(a.num_q_heads, c.num_heads);
+  p.columns = columns_of(a.num_seqs, a.num_q_heads, c.num_heads, c.head_dim, a.max_pages * c.page_size);
+  p.chunks = (p.group + p.columns - 1) / p.columns;
   const int64_t units = a.num_seqs * c.num_heads * p.chunks;
-  p.workers = shared_workers(units, c.head_dim, a.max_pages * c.page_size);
-  p.ctas = cluster_ctas(units, c.head_dim, a.max_pages * c.page_size);
+  p.workers = shared_workers(units, c.head_dim, p.columns, a.max_pages * c.page_size);
+  p.ctas = cluster_ctas(units, c.head_dim, p.columns, a.max_pages * c.page_size);
   p.part_o = a.workspace;
-  p.part_ml = p.part_o + (units + p.workers) * kHeads * c.head_dim;
-  p.parts = reinterpret_cast<int4*>(p.part_ml + (units + p.workers) * kHeads * 2);
+  p.part_ml = p.part_o + (units + p.workers) * p.columns * c.head_dim;
+  p.parts = reinterpret_cast<int4*>(p.part_ml + (units + p.workers) * p.columns * 2);
   p.bad = reinterpret_cast<int32_t*>(p.parts + units);
 #ifdef MXFP4_DEBUG_BOUNDS
   const int64_t rows = c.num_pages * c.page_size * c.num_heads;
@@ -1136,7 +1183,7 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
               a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
   debug_range(p.dbg, kDbgOut, a.out, a.num_seqs * a.num_q_heads * c.head_dim * 2);
   debug_range(p.dbg, kDbgPart, a.workspace,
-              p.workers > 0 ? ((units + p.workers) * kHeads * (c.head_dim + 2) + 4 * units + p.workers) * 4 : 0);
+              p.workers > 0 ? ((units + p.workers) * p.columns * (c.head_dim + 2) + 4 * units + p.workers) * 4 : 0);
 #endif
   const int64_t word = a.status != nullptr;
   const int64_t grid = p.workers > 0 ? p.workers / kWarps

@@ -33,7 +33,7 @@
 //
 // Measured (device time, weights not in L2): 64000 x 7168 MXFP4 by 1 BF16 token
 // 45 us, 5.4 TB/s of 244 MB; the copies alone take most of that, the products
-// alone 35 us.  By 16 tokens 70 us (FP16 61): 61 % of the cycles issue, with x in
+// alone 35 us.  By 16 tokens 70 us (FP16 59): 60 % of the cycles issue, with x in
 // panels.  7168 x 7168 by 1 token 11.3 us, the 128 experts'
 // 1536 x 2048 NVFP4 by 64 tokens of 8 experts each 46.9 us (4.6 TB/s), 2048 x 768
 // by 1 token 5.2 us.

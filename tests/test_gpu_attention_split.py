@@ -100,3 +100,28 @@ def test_masked_bytes_with_room(mx):  # noqa: F811
         for t in (c.k_scales, c.v_scales):
             t.transpose(1, 2)[~live] = nan
         check_attention(mx, rand((3, 16, D), 2), c, with_room(table, S), n, 0.1)
+
+
+@pytest.mark.parametrize("group", [9, 16, 17, 31, 64])
+@pytest.mark.parametrize("H,D,S", [(1, 128, 16), (2, 64, 7), (1, 32, 64), (3, 96, 16), (1, 256, 32)])
+@pytest.mark.parametrize("nvfp4,dtype", [(False, BF16), (True, F16)])
+def test_more_heads_than_a_block(mx, group, H, D, S, nvfp4, dtype):  # noqa: F811
+    lens = [700, 0, 33, 1]
+    per = -(-max(lens) // S)
+    c = filled(mx, 2 * per, S, H, D, nvfp4, group, dtype)
+    table = tables(len(lens), per, 2 * per, 3)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = rand((len(lens), group * H, D), 5, dtype)
+    check_attention(mx, q, c, table, n, D ** -0.5)
+    check_attention(mx, q, c, with_room(table, S, 70000), n, -0.7, window=300)
+
+
+@pytest.mark.parametrize("B,group,D,L,nvfp4", [(400, 16, 32, 320, False), (300, 13, 128, 352, True),
+                                               (290, 16, 128, 352, False), (150, 24, 64, 1700, False)])
+def test_more_heads_in_clusters(mx, B, group, D, L, nvfp4):  # noqa: F811
+    """Many sequences of few steps, more than 8 heads to a kv head."""
+    S, pages = 16, 400
+    c = filled(mx, pages, S, 1, D, nvfp4, 6)
+    lens = torch.randint(0, L + 1, (B,), generator=torch.Generator().manual_seed(L)).int().cuda()
+    lens[0] = L
+    check_attention(mx, rand((B, group, D), 7), c, tables(B, -(-L // S), pages, 2), lens, 0.1)
