@@ -602,14 +602,17 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
         for (int i = 0; i < DB; ++i)
           q[n][i] = make_uint4(scaled(q[n][i].x), scaled(q[n][i].y), scaled(q[n][i].z), scaled(q[n][i].w));
       }
-      const uint32_t sign = p.softmax_scale < 0.0f ? 0x80008000u : 0u;  // a larger product is a larger score
+      const float more = p.softmax_scale * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
+      const uint32_t sign = more < 0.0f ? 0x80008000u : 0u;  // a larger product is a larger score
 #pragma unroll
       for (int i = 0; i < DB; ++i)
         q[n][i] = make_uint4(q[n][i].x ^ sign, q[n][i].y ^ sign, q[n][i].z ^ sign, q[n][i].w ^ sign);
-      // (not zero: a masked score is -infinity, and stays that)
-      const float more = fmaxf(fabsf(p.softmax_scale), 0x1p-126f) * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
-      qs[n][0] = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c) * more;
-      qs[n][1] = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4) * more;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // not zero: a masked score is -infinity, and stays that
+        const float f = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4 * e) * fabsf(more);
+        qs[n][e] = f < 0x1p-126f ? 0x1p-126f : f;
+      }
     }
 
     float m[NB][2], l[NB][2];  // of heads 2c and 2c + 1 of a block, log2

@@ -106,3 +106,15 @@ def test_attention_workspace_query(lib):
     assert q(-1, 8, 1, 64, 16, 10) == q(1, 8, 3, 64, 16, 10) == q(1, 8, 1, 288, 16, 10) == 0
     assert q(1, 8, 1, 48, 16, 10) == q(1, 8, 1, 64, 0, 10) == q(1, 8, 0, 64, 16, 10) == 0
     assert q(1, 8, 1, 64, 16, 2 ** 28) == 0 and q(0, 8, 1, 64, 16, 10) == 0
+
+
+def test_attention_workspace_of_short_and_long_contexts(lib):
+    """Short contexts are joined inside the kernel; long ones need room for the
+    parts of 8 heads (16 where a kv head has more and the call is large)."""
+    q = lib.mxfp4_cache_attention_workspace_bytes
+    assert q(1, 64, 8, 128, 16, 2) == q(1, 64, 8, 128, 16, 44) == q(1, 128, 8, 128, 16, 44) == 0
+    for D in (32, 64, 96, 128, 256):
+        for heads in (8, 64, 128, 256):
+            need = q(1, heads, 8, D, 16, 8192)
+            assert need > 0 and need % 4 == 0
+            assert q(2, heads, 8, D, 16, 8192) >= need

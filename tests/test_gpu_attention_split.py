@@ -125,3 +125,23 @@ def test_more_heads_in_clusters(mx, B, group, D, L, nvfp4):  # noqa: F811
     lens = torch.randint(0, L + 1, (B,), generator=torch.Generator().manual_seed(L)).int().cuda()
     lens[0] = L
     check_attention(mx, rand((B, group, D), 7), c, tables(B, -(-L // S), pages, 2), lens, 0.1)
+
+
+@pytest.mark.parametrize("power", [-100, -60, -20, 0])
+@pytest.mark.parametrize("scale", [0.0, 1e-25, -1e-3])
+@pytest.mark.parametrize("room", [False, True])
+def test_small_queries_and_scales(mx, power, scale, room):  # noqa: F811
+    """Scores that all but vanish, beside masked positions."""
+    c = filled(mx, 8, 16, 1, 64, False, 6)
+    n = torch.tensor([100, 33, 1], dtype=torch.int32, device="cuda")
+    q = (rand((3, 4, 64), 5).float() * 2.0 ** power).to(BF16)
+    table = tables(3, 7, 8, 1)
+    check_attention(mx, q, c, with_room(table, 16) if room else table, n, scale)
+
+
+@pytest.mark.parametrize("scale", [0.2, -0.2])
+def test_negative_global_scale(mx, scale):  # noqa: F811
+    c = filled(mx, 8, 16, 2, 64, True, 6)
+    c = c._replace(k_global=-c.k_global)
+    n = torch.tensor([100, 33, 0], dtype=torch.int32, device="cuda")
+    check_attention(mx, rand((3, 8, 64), 5), c, tables(3, 7, 8, 1), n, scale)
