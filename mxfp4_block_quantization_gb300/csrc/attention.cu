@@ -32,9 +32,11 @@
 // formed in halves, exactly.  V: a position's scales vary along the sum, so
 // they go into the operands: NVFP4 into V; MXFP4 into P, relative to the
 // largest scale that the warp has met in that 32-value block (an integer
-// maximum, with the output rescaled when it grows).  P is rounded to a half (11
-// bits), as the scale times P would be in any 16-bit operand; at 2^12 times
-// its size the product keeps P down to 2^-26.
+// maximum, with the output rescaled when it grows).  P is formed at 2^12 times
+// its size and rounded to a half there, so it has 11 bits down to 2^-26 of the
+// warp's largest and is lost under 2^-37 (beside a position that dominates with
+// a small value, the others are the output); the denominator's sum keeps it in
+// float32.  2^12 is divided out of the sums at the end.
 //
 // Measured, 64 query heads on 8: 64 sequences of up to 8192 positions (head_dim
 // 128, MXFP4, 445 MB of cache) 99 us, 4.5 TB/s.  Without the products 87, without
@@ -72,6 +74,8 @@ __host__ __device__ constexpr int ctas_of(int blocks, bool cluster, int column_b
 constexpr int kColumns = 8;  // query heads of a column block of the products
 constexpr float kLag = 3.0f;  // log2: how far a warp's reference may lag behind its maximum
                               // (0: 64 sequences of 8192 99.1 -> 100.2 us)
+constexpr float kRaise = 12.0f;  // log2: what P is raised by; with kLag inside a half
+constexpr float kLower = 0x1p-12f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -668,8 +672,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
           }
           const uint32_t to = st + S::kScaleV + ((lane & 7) >> 1) * 16 + (lane >> 3) * 4 + (lane & 1) * 2;
 #pragma unroll
-          for (int i = 0; i < DB; ++i)  // 2^(12 + byte - vref)
-            sts16(to + i * 64, static_cast<uint32_t>(max(byte[i] + 27 - vref[i], 0)) << 10);
+          for (int i = 0; i < DB; ++i) {  // 2^(byte - vref), down to the smallest half
+            const float f = __uint_as_float(static_cast<uint32_t>(max(127 + byte[i] - vref[i], 0)) << 23);
+            sts16(to + i * 64, pack_f16x2(f, 0.0f));
+          }
         }
       }
       const int next_page = static_cast<int>(lds32(st + S::kPage + lane * 4));
@@ -742,8 +748,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
       }
 
       // ---- running maximum and sum.  The reference m may lag behind the
-      // maximum by kLag (P then grows to 2^kLag at most, far inside a half), so
-      // that the output is rescaled a few times at all, not at every new maximum.
+      // maximum by kLag (P then grows to 2^(kRaise + kLag) at most, inside a half),
+      // so that the output is rescaled a few times at all, not at every new maximum.
       float x[NB][2];
       bool far = false;
 #pragma unroll
@@ -774,8 +780,9 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
       uint32_t pt[NB][2][2];  // P^T of each block: columns of heads, pairs of positions
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
-        const float z0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], z1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
-        uint32_t pk[2][2];  // P of positions g and g + 8 of each half, heads 2c and 2c + 1
+        const float z0 = (m[n][0] == -INFINITY ? 0.0f : m[n][0]) - kRaise;
+        const float z1 = (m[n][1] == -INFINITY ? 0.0f : m[n][1]) - kRaise;
+        uint32_t pk[2][2];  // 2^kRaise * P of positions g and g + 8 of each half, heads 2c and 2c + 1
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -856,14 +863,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
 #pragma unroll
     for (int j = 0; j < 2 * NB; ++j) {  // heads 2c and 2c + 1; four values of each 32 in a lane
       const int n = j >> 1, e = j & 1, h = n * kColumns + 2 * c + e;
-      const float top = m[n][e], sum = l[n][e];
+      const float top = m[n][e], sum = l[n][e] * kLower;
       if (h >= heads) continue;
 #pragma unroll
       for (int i = 0; i < DB; ++i) {
-        // MXFP4: 2^(vref - 127 - 12); a block that met the NaN scale is NaN
-        float f = 1.0f;
+        // MXFP4: 2^(vref - 127); a block that met the NaN scale is NaN
+        float f = kLower;
         if constexpr (!kNv)
-          f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * 0x1p-12f;
+          f = vref[i] == 255 ? __uint_as_float(0x7FC00000u) : scale_from_e8m0(vref[i]) * kLower;
         const float4 v = make_float4(o[n][i][0][e] * f, o[n][i][0][2 + e] * f, o[n][i][1][e] * f, o[n][i][1][2 + e] * f);
         const int d = i * 32 + 4 * g;
         if (in_ring) {

@@ -1,0 +1,54 @@
+"""Attention over the paged 4-bit cache where few bits decide."""
+import math
+
+import pytest
+import torch
+
+import decode_reference as R
+from test_gpu_attention_split import with_room
+from test_gpu_cache import BF16, F16, make_cache, mx, rand  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def contents(c, pages, n):
+    """The keys and values [heads, n, head_dim] of the pages' first n positions, float64."""
+    nvfp4 = c.k_global is not None
+
+    def rows(codes, scales, g):
+        x = R.rows_of(codes[pages], scales[pages], nvfp4, 1.0 if g is None else g)
+        return x.transpose(0, 1).flatten(1, 2)[:, :n]
+
+    return rows(c.k_codes, c.k_scales, c.k_global), rows(c.v_codes, c.v_scales, c.v_global)
+
+
+@pytest.mark.parametrize("gap", [8.3, 16.4, 20.3, 22.6, 24.4])
+@pytest.mark.parametrize("n,room", [(32, False), (250, False), (250, True), (1700, False), (1700, True)])
+@pytest.mark.parametrize("nvfp4", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_tail_beside_a_dominant_position(mx, gap, n, room, nvfp4, dtype):  # noqa: F811
+    """One position's weight is 2^gap times the others' and its value is zero, as a
+    sink of attention has it: the output is the others'.
+
+    Bound: a weight is rounded to 11 bits twice (with its value's scale), and no
+    finer than 2^-36 of the largest weight, times the largest value."""
+    S, D = 16, 64
+    pages = -(-n // S)
+    c = make_cache(mx, pages, S, 1, D, nvfp4)
+    k, v = torch.zeros((n, 1, D), dtype=dtype, device="cuda"), rand((n, 1, D), n, dtype)
+    k[3, 0, 0], v[3] = 4.0, 0.0
+    mx.cache_write(k, v, torch.arange(n, dtype=torch.int32, device="cuda"), c)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
+    q = torch.zeros((1, 3, D), dtype=dtype, device="cuda")
+    q[..., 0] = torch.tensor([1.0, 0.5, 2.0])
+    scale = gap * math.log(2.0) / 4.0
+    o, lse, _ = mx.cache_attention(q, c, with_room(table, S) if room else table,
+                                   torch.tensor([n], dtype=torch.int32, device="cuda"), scale)
+    kd, vd = contents(c, table[0].long(), n)
+    a = scale * (q[0].double() @ kd[0].T)
+    p = torch.softmax(a, -1)
+    want = p @ vd[0]
+    off = (2.0 ** -10 + 2.0 ** -18) * (p @ vd[0].abs()) + n * 2.0 ** -36 * vd.abs().amax()
+    keep = [0, 1] if gap > 12 else [0, 1, 2]             # 2.0: twice the gap
+    R.close(o[0, keep], want[keep], (off + R.unit(dtype) * (want.abs() + off) + R.smallest(dtype))[keep])
+    R.close(lse[0], torch.logsumexp(a, -1), 2.0 ** -18 + 2.0 ** -22 * a.abs().amax(-1))
