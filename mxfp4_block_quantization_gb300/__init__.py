@@ -11,6 +11,10 @@ A decode step's calls (``matvec``, ``moe_matvec``, ``cache_write``,
 ``cache_read``, ``cache_attention``) pick the BF16 or FP16 entry point by
 their tensors' type.
 
+A call on ``stream`` does not wait for the current one: let it wait before its
+inputs are used, and the current one before its outputs are.  What such a call
+allocates is memory of ``stream``.
+
 There is no CPU path: importing this package fails when the library has not
 been built (``python mxfp4_block_quantization_gb300/_build.py``), and every
 call rejects tensors that are not on a CUDA device.
@@ -1258,32 +1262,46 @@ def dequantize_nvfp4(codes, scales, global_scale, M: int, K: int, stream=None):
     return y
 
 
-def _product_out(x, rows, N, out, out_dtype):
-    return out if out is not None else torch.empty((rows, N), dtype=out_dtype or x.dtype,
-                                                   device=x.device)
+def _empty(shape, dtype, device, stream):
+    """An uninitialised tensor for a call on ``stream`` (None: the current one).
+    Memory is a stream's: a block that was freed on the current stream may
+    still be in use there, and one freed here goes to the current stream's next
+    tensor, so what the call on another stream writes is that stream's memory.
+    It may be used and freed on the current stream as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
+def _product_out(x, rows, N, out, out_dtype, stream):
+    return out if out is not None else _empty((rows, N), out_dtype or x.dtype, x.device, stream)
 
 
 def matvec(x, codes, scales, out=None, out_dtype=None, stream=None):
     """``x`` [T, K] (BF16 or FP16) times the transpose of the MXFP4 weights
     ``codes`` [N, K/2], ``scales`` (tiled): [T, N] of x's type, of
     ``out_dtype`` (torch.float32) or into ``out``."""
-    out = _product_out(x, x.shape[0], codes.shape[0], out, out_dtype)
+    out = _product_out(x, x.shape[0], codes.shape[0], out, out_dtype, stream)
     _matvec(x, codes, scales, None, out, stream, False)
     return out
 
 
 def matvec_nvfp4(x, codes, scales, global_scale, out=None, out_dtype=None, stream=None):
     """matvec with NVFP4 weights and their float32 ``global_scale``."""
-    out = _product_out(x, x.shape[0], codes.shape[0], out, out_dtype)
+    out = _product_out(x, x.shape[0], codes.shape[0], out, out_dtype, stream)
     _matvec(x, codes, scales, global_scale, out, stream, True)
     return out
 
 
-def _moe_outputs(x, row_index, codes, out, out_dtype, status):
+def _moe_outputs(x, row_index, codes, out, out_dtype, status, stream):
     rows = x.shape[0] if row_index is None else row_index.numel()
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=x.device)
-    return _product_out(x, rows, codes.shape[1], out, out_dtype), status
+        status = _empty(1, torch.int32, x.device, stream)
+    return _product_out(x, rows, codes.shape[1], out, out_dtype, stream), status
 
 
 def moe_matvec(x, row_index, expert_offsets, codes, scales, out=None, out_dtype=None, status=None,
@@ -1292,7 +1310,7 @@ def moe_matvec(x, row_index, expert_offsets, codes, scales, out=None, out_dtype=
     (x[r] if row_index is None) times the transpose of expert e's MXFP4
     weights ``codes`` [E, N, K/2].  Rows from expert_offsets[E] on are not
     written."""
-    out, status = _moe_outputs(x, row_index, codes, out, out_dtype, status)
+    out, status = _moe_outputs(x, row_index, codes, out, out_dtype, status, stream)
     _moe_matvec(x, row_index, expert_offsets, codes, scales, None, out, status, stream, False)
     return out, status
 
@@ -1300,7 +1318,7 @@ def moe_matvec(x, row_index, expert_offsets, codes, scales, out=None, out_dtype=
 def moe_matvec_nvfp4(x, row_index, expert_offsets, codes, scales, global_scales, out=None,
                      out_dtype=None, status=None, stream=None):
     """moe_matvec with NVFP4 weights and float32 ``global_scales`` [E]."""
-    out, status = _moe_outputs(x, row_index, codes, out, out_dtype, status)
+    out, status = _moe_outputs(x, row_index, codes, out, out_dtype, status, stream)
     _moe_matvec(x, row_index, expert_offsets, codes, scales, global_scales, out, status, stream,
                 True)
     return out, status
@@ -1319,7 +1337,7 @@ def cache_alloc(num_pages: int, page_size: int, num_heads: int, head_dim: int, k
 def cache_write(k, v, slots, cache, status=None, stream=None):
     """mxfp4_cache_write with a status word allocated here; returns it."""
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=k.device)
+        status = _empty(1, torch.int32, k.device, stream)
     mxfp4_cache_write(k, v, slots, cache, status, stream)
     return status
 
@@ -1328,10 +1346,10 @@ def cache_read(cache, slots, k_out=None, v_out=None, dtype=torch.bfloat16, statu
                stream=None):
     """Returns (k, v, status): the slots' keys and values [T, heads, head_dim]."""
     shape = (slots.numel(), cache.k_codes.shape[1], cache.k_codes.shape[3] * 2)
-    k_out, v_out = (t if t is not None else torch.empty(shape, dtype=dtype, device=slots.device)
+    k_out, v_out = (t if t is not None else _empty(shape, dtype, slots.device, stream)
                     for t in (k_out, v_out))
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=slots.device)
+        status = _empty(1, torch.int32, slots.device, stream)
     mxfp4_cache_read(cache, slots, k_out, v_out, status, stream)
     return k_out, v_out, status
 
@@ -1342,14 +1360,14 @@ def cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, window
     with the workspace allocated here."""
     B, Hq, D = q.shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=q.dtype, device=q.device)
+        out = _empty((B, Hq, D), q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+        lse = _empty((B, Hq), torch.float32, q.device, stream)
     if status is None:
-        status = torch.empty(1, dtype=torch.int32, device=q.device)
+        status = _empty(1, torch.int32, q.device, stream)
     nbytes = mxfp4_cache_attention_workspace_bytes(B, Hq, cache.k_codes.shape[1], D,
                                                    cache.k_codes.shape[2], page_table.shape[1])
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    ws = _empty(nbytes, torch.uint8, q.device, stream) if nbytes else None
     mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale, out, window, ws, lse,
                           status, stream)
     return out, lse, status
