@@ -1089,11 +1089,27 @@ def mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, 
 
 
 # --------------------------------------------------- allocating wrappers
+def _empty(shape, dtype, device, stream, make=torch.empty):
+    """An uninitialised (``make`` torch.zeros: zeroed there) tensor for a call on
+    ``stream`` (None: the current one).  Memory is a stream's: a block that was
+    freed on the current stream may still be in use there, and one freed here
+    goes to the current stream's next tensor, so what the call on another stream
+    writes is that stream's memory.  It may be used and freed on the current
+    stream as well."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(here)
+    return t
+
+
 def quantize(x, stream=None):
     """BF16 or FP16 ``x`` [M, K] -> (codes uint8 [M, K/2], scales uint8 [scale_bytes])."""
     M, K = x.shape
-    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(mxfp4_scale_bytes(M, K), dtype=torch.uint8, device=x.device)
+    codes = _empty((M, K // 2), torch.uint8, x.device, stream)
+    scales = _empty(mxfp4_scale_bytes(M, K), torch.uint8, x.device, stream)
     if x.dtype == torch.float16:
         mxfp4_quantize_f16(x, codes, scales, stream)
     else:
@@ -1106,11 +1122,11 @@ def quantize_grouped(x, expert_offsets, stream=None):
     total, K = x.shape
     E = expert_offsets.numel() - 1
     dev = x.device
-    codes = torch.empty((total, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(max(mxfp4_grouped_scale_bytes_bound(total, E, K), 16), dtype=torch.uint8,
-                         device=dev)
-    sro = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev)
+    codes = _empty((total, K // 2), torch.uint8, dev, stream)
+    scales = _empty(max(mxfp4_grouped_scale_bytes_bound(total, E, K), 16),
+                    torch.uint8, dev, stream)
+    sro = _empty(E + 1, torch.int32, dev, stream)
+    status = _empty(1, torch.int32, dev, stream)
     _grouped(x, expert_offsets, codes, scales, sro, status, stream, x.dtype == torch.float16)
     return codes, scales, sro, status
 
@@ -1126,14 +1142,14 @@ def quantize_grouped_gather(x, row_index, expert_offsets, stream=None, via_scatt
     E = expert_offsets.numel() - 1
     dev = x.device
     f16 = x.dtype == torch.float16
-    codes = torch.empty((total, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(max(mxfp4_grouped_scale_bytes_bound(total, E, K), 16), dtype=torch.uint8,
-                         device=dev)
-    sro = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev)
+    codes = _empty((total, K // 2), torch.uint8, dev, stream)
+    scales = _empty(max(mxfp4_grouped_scale_bytes_bound(total, E, K), 16),
+                    torch.uint8, dev, stream)
+    sro = _empty(E + 1, torch.int32, dev, stream)
+    status = _empty(1, torch.int32, dev, stream)
     if via_scatter:
-        ws = torch.empty(max(mxfp4_gather_workspace_bytes(x.shape[0], total, E, K), 16),
-                         dtype=torch.uint8, device=dev)
+        ws = _empty(max(mxfp4_gather_workspace_bytes(x.shape[0], total, E, K), 16),
+                    torch.uint8, dev, stream)
         _gather_ws(x, row_index, expert_offsets, ws, codes, scales, sro, status, stream, f16)
     else:
         _gather(x, row_index, expert_offsets, codes, scales, sro, status, stream, f16)
@@ -1152,15 +1168,15 @@ def quantize_grouped_scatter(x, dest_rows, expert_offsets, total_rows=None, stre
     total = dest_rows.numel() if total_rows is None else int(total_rows)
     E = expert_offsets.numel() - 1
     dev = x.device
-    codes = torch.zeros((total, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.zeros(max(mxfp4_grouped_scale_bytes_bound(total, E, K), 16), dtype=torch.uint8,
-                         device=dev)
-    sro = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev)
+    codes = _empty((total, K // 2), torch.uint8, dev, stream, torch.zeros)
+    scales = _empty(max(mxfp4_grouped_scale_bytes_bound(total, E, K), 16),
+                    torch.uint8, dev, stream, torch.zeros)
+    sro = _empty(E + 1, torch.int32, dev, stream)
+    status = _empty(1, torch.int32, dev, stream)
     ws = None
     if staged:
-        ws = torch.empty(max(mxfp4_scatter_workspace_bytes(x.shape[0], total, E, K), 16),
-                         dtype=torch.uint8, device=dev)
+        ws = _empty(max(mxfp4_scatter_workspace_bytes(x.shape[0], total, E, K), 16),
+                    torch.uint8, dev, stream)
     _scatter(x, dest_rows, expert_offsets, total, codes, scales, sro, status, stream,
              x.dtype == torch.float16, ws)
     return codes, scales, sro, status
@@ -1173,18 +1189,18 @@ def moe_route(topk_ids, num_experts: int, stream=None):
     the rest of it is not written)."""
     dev = topk_ids.device
     T, top_k = topk_ids.shape
-    off = torch.empty(num_experts + 1, dtype=torch.int32, device=dev)
-    dest = torch.empty((T, top_k), dtype=torch.int32, device=dev)
-    rows = torch.empty(max(T * top_k, 1), dtype=torch.int32, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev)
-    ws = torch.empty(max(mxfp4_route_workspace_bytes(T, top_k, num_experts), 16),
-                     dtype=torch.uint8, device=dev)
+    off = _empty(num_experts + 1, torch.int32, dev, stream)
+    dest = _empty((T, top_k), torch.int32, dev, stream)
+    rows = _empty(max(T * top_k, 1), torch.int32, dev, stream)
+    status = _empty(1, torch.int32, dev, stream)
+    ws = _empty(max(mxfp4_route_workspace_bytes(T, top_k, num_experts), 16),
+                torch.uint8, dev, stream)
     mxfp4_moe_route(topk_ids, num_experts, ws, off, dest, rows, status, stream)
     return off, dest, rows, status
 
 
 def dequantize(codes, scales, M: int, K: int, stream=None):
-    y = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
+    y = _empty((M, K), torch.bfloat16, codes.device, stream)
     mxfp4_dequantize(codes, scales, M, K, y, stream)
     return y
 
@@ -1194,11 +1210,11 @@ def swap_w13(codes, scales, w13_bias=None, w2_bias=None, scales_tiled=True, stre
     [E, 2N, K/32].  Returns (codes, scales, w13_bias_bf16, w2_bias_bf16)."""
     E, two_n, half_k = codes.shape
     K = half_k * 2
-    codes_out = torch.empty_like(codes)
-    scales_out = torch.empty_like(scales)
-    b13 = torch.empty(w13_bias.shape, dtype=torch.bfloat16, device=codes.device) \
+    codes_out = _empty(codes.shape, codes.dtype, codes.device, stream)
+    scales_out = _empty(scales.shape, scales.dtype, scales.device, stream)
+    b13 = _empty(w13_bias.shape, torch.bfloat16, codes.device, stream) \
         if w13_bias is not None else None
-    b2 = torch.empty(w2_bias.shape, dtype=torch.bfloat16, device=codes.device) \
+    b2 = _empty(w2_bias.shape, torch.bfloat16, codes.device, stream) \
         if w2_bias is not None else None
     mxfp4_swap_w13(codes, scales, w13_bias, E, two_n, K, 1 if scales_tiled else 0, codes_out,
                    scales_out, b13, w2_bias, b2, stream)
@@ -1209,8 +1225,8 @@ def quantize_nvfp4(x, global_scale, stream=None):
     """Returns (codes uint8 [M, K/2], E4M3 scales uint8 [nvfp4_scale_bytes])
     of BF16 or FP16 ``x``."""
     M, K = x.shape
-    codes = torch.empty((M, K // 2), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(mxfp4_nvfp4_scale_bytes(M, K), dtype=torch.uint8, device=x.device)
+    codes = _empty((M, K // 2), torch.uint8, x.device, stream)
+    scales = _empty(mxfp4_nvfp4_scale_bytes(M, K), torch.uint8, x.device, stream)
     _nvfp4(x, global_scale, codes, scales, stream, x.dtype == torch.float16)
     return codes, scales
 
@@ -1221,11 +1237,11 @@ def quantize_nvfp4_grouped(x, expert_offsets, global_scales, stream=None):
     total, K = x.shape
     E = expert_offsets.numel() - 1
     dev = x.device
-    codes = torch.empty((total, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.empty(max(mxfp4_nvfp4_grouped_scale_bytes_bound(total, E, K), 16),
-                         dtype=torch.uint8, device=dev)
-    sro = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev)
+    codes = _empty((total, K // 2), torch.uint8, dev, stream)
+    scales = _empty(max(mxfp4_nvfp4_grouped_scale_bytes_bound(total, E, K), 16),
+                    torch.uint8, dev, stream)
+    sro = _empty(E + 1, torch.int32, dev, stream)
+    status = _empty(1, torch.int32, dev, stream)
     _nvfp4_grouped(x, expert_offsets, global_scales, codes, scales, sro, status, stream,
                    x.dtype == torch.float16)
     return codes, scales, sro, status
@@ -1242,39 +1258,24 @@ def quantize_nvfp4_grouped_scatter(x, dest_rows, expert_offsets, global_scales, 
     total = dest_rows.numel() if total_rows is None else int(total_rows)
     E = expert_offsets.numel() - 1
     dev = x.device
-    codes = torch.zeros((total, K // 2), dtype=torch.uint8, device=dev)
-    scales = torch.zeros(max(mxfp4_nvfp4_grouped_scale_bytes_bound(total, E, K), 16),
-                         dtype=torch.uint8, device=dev)
-    sro = torch.empty(E + 1, dtype=torch.int32, device=dev)
-    status = torch.empty(1, dtype=torch.int32, device=dev)
+    codes = _empty((total, K // 2), torch.uint8, dev, stream, torch.zeros)
+    scales = _empty(max(mxfp4_nvfp4_grouped_scale_bytes_bound(total, E, K), 16),
+                    torch.uint8, dev, stream, torch.zeros)
+    sro = _empty(E + 1, torch.int32, dev, stream)
+    status = _empty(1, torch.int32, dev, stream)
     ws = None
     if staged:
-        ws = torch.empty(max(mxfp4_nvfp4_scatter_workspace_bytes(total, E, K), 16),
-                         dtype=torch.uint8, device=dev)
+        ws = _empty(max(mxfp4_nvfp4_scatter_workspace_bytes(total, E, K), 16),
+                    torch.uint8, dev, stream)
     _nvfp4_scatter(x, dest_rows, expert_offsets, total, global_scales, codes, scales, sro, status,
                    stream, x.dtype == torch.float16, ws)
     return codes, scales, sro, status
 
 
 def dequantize_nvfp4(codes, scales, global_scale, M: int, K: int, stream=None):
-    y = torch.empty((M, K), dtype=torch.bfloat16, device=codes.device)
+    y = _empty((M, K), torch.bfloat16, codes.device, stream)
     mxfp4_dequantize_nvfp4(codes, scales, global_scale, M, K, y, stream)
     return y
-
-
-def _empty(shape, dtype, device, stream):
-    """An uninitialised tensor for a call on ``stream`` (None: the current one).
-    Memory is a stream's: a block that was freed on the current stream may
-    still be in use there, and one freed here goes to the current stream's next
-    tensor, so what the call on another stream writes is that stream's memory.
-    It may be used and freed on the current stream as well."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    here = torch.cuda.current_stream(device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(here)
-    return t
 
 
 def _product_out(x, rows, N, out, out_dtype, stream):

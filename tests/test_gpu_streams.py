@@ -96,3 +96,45 @@ def test_outputs_used_and_freed_on_the_current_stream(mx, name):  # noqa: F811
             call(1, s)
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, want))
+
+
+def quantize_calls(mx):  # noqa: F811
+    """name -> call(i, stream) of the calls with a workspace or zeroed outputs."""
+    T, k, E, K = 600, 4, 12, 512
+    x = [rand((T, K), 20 + i) for i in range(2)]
+    ids = [torch.rand((T, E), device="cuda").topk(k, 1).indices.to(torch.int32) for _ in range(2)]
+    routes = [mx.moe_route(t, E) for t in ids]
+    g = torch.linspace(100.0, 400.0, E, device="cuda")
+
+    def cut(outputs, i):
+        """Without the bytes past the last expert's scales, which no call writes."""
+        codes, scales, sro, status = outputs
+        return codes, scales[:int(routes[i][0][-1])], sro, status
+
+    return {
+        "route": lambda i, s=None: mx.moe_route(ids[i], E, stream=s),
+        "gather": lambda i, s=None: cut(mx.quantize_grouped_gather(x[i], routes[i][2], routes[i][0], stream=s), i),
+        "scatter": lambda i, s=None: mx.quantize_grouped_scatter(x[i], routes[i][1], routes[i][0], stream=s),
+        "nvfp4_scatter": lambda i, s=None: mx.quantize_nvfp4_grouped_scatter(x[i], routes[i][1], routes[i][0], g,
+                                                                             stream=s),
+        "quantize": lambda i, s=None: mx.quantize(x[i], stream=s)}
+
+
+@pytest.mark.parametrize("name", ["route", "gather", "scatter", "nvfp4_scatter", "quantize"])
+def test_quantize_calls_beside_work_on_the_current_stream(mx, name):  # noqa: F811
+    call = quantize_calls(mx)[name]
+    want = [[t.clone() for t in call(i)] for i in range(2)]
+    s, = side_streams(1)
+    sizes = [t.numel() * t.element_size() for t in want[0]] + [1 << 16, 1 << 20]
+    got, other = [], []
+    for i in range(20):
+        got.append(call(i % 2, s))
+        other += [torch.full((n,), 0xA5, dtype=torch.uint8, device="cuda") for n in sizes]
+        if i % 4 == 3:
+            del other[-2 * len(sizes):]
+    torch.cuda.synchronize()
+    for i, outputs in enumerate(got):
+        for a, b in zip(outputs, want[i % 2]):
+            assert torch.equal(a, b)
+    for t in other:
+        assert (t == 0xA5).all()
