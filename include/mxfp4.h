@@ -602,7 +602,8 @@ int mxfp4_dequantize_nvfp4(const uint8_t* codes, const uint8_t* scales,
  *             block's largest is rounded to a multiple of 2^-40 of it.
  * codes       [N, K/2] packed E2M1 codes as mxfp4_quantize writes them,
  *             16-byte aligned; K % 32 == 0.
- * scales      mxfp4_scale_bytes(N, K) bytes, tiled layout, 16-byte aligned.
+ * scales      mxfp4_scale_bytes(N, K) bytes, tiled layout, 16-byte aligned; the
+ *             bytes that pad its rows and columns may hold anything.
  * y           [num_tokens, N], row stride ldy >= N elements, of x's type, or
  *             float32 with y_f32 == 1; aligned to its element.  K == 0 writes
  *             zeros.

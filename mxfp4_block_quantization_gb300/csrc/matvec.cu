@@ -400,8 +400,17 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
             row += quarter;
           }
           if (lane < kScaleBytes / 16) {
-            const bool ok = in.chunk * kChunkKt + (lane >> 2) < p.nKT && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16);
-            cp_async<16>(scale_to, ok ? scale : p.scales, ok ? 16 : 0);
+            // A piece is four rows' words of four columns.  The layout pads the columns to
+            // a multiple of four with bytes that may be anything: zeros take their place.
+            const int kt = in.chunk * kChunkKt + (lane >> 2);
+            const bool ok = kt < p.nKT && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16);
+            const int cols = p.K / (kNv ? 16 : 32) - 4 * kt;
+            if (ok && cols < 4) {
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) cp_async4(scale_to + 4 * i, scale + 4 * i, cols);
+            } else {
+              cp_async<16>(scale_to, ok ? scale : p.scales, ok ? 16 : 0);
+            }
           }
         }
         in_at += kStage;
