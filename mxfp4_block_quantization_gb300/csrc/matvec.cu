@@ -267,8 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       const int count = __popc(__ballot_sync(0xFFFFFFFFu, fits));
       if (fits) {
         sh.unit[lane] = u;
-        if (kNv && p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + u.e, 4))
-          sh.unit_inverse[lane] = 1.0f / __ldg(p.global_scales + u.e);
+        if (kNv)  // an empty sum is zero, whatever the scale
+          sh.unit_inverse[lane] = p.K > 0 && MXFP4_IN_BOUNDS(p, kDbgGlobal, p.global_scales + u.e, 4)
+                                      ? 1.0f / __ldg(p.global_scales + u.e)
+                                      : 1.0f;
       }
       if (lane == count - 1) {
         sh.n_units = count;

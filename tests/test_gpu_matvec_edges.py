@@ -1,4 +1,5 @@
-"""Products with 4-bit weights where bytes that are no weight's lie beside the weights'."""
+"""Products with 4-bit weights where bytes that are no weight's lie beside the weights',
+and empty sums."""
 import pytest
 import torch
 
@@ -50,3 +51,24 @@ def test_unused_scale_bytes_of_experts(mx, T, k, E, N, K, nvfp4, byte):  # noqa:
     scales[pad_bytes(N, K // (16 if nvfp4 else 32)).repeat(E)] = byte
     got, _ = moe_call(mx, x, rows, off, codes, scales, g, out_dtype=F32)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T", [3, 12])
+def test_an_empty_sum_is_zero_nvfp4(mx, dtype, T):  # noqa: F811
+    """Without elements the global scale has no say either, nor one of the call before."""
+    codes, scales, _ = make_weights(mx, 5000, 64, True, 3)
+    empty = torch.empty((400, 0), dtype=torch.uint8, device="cuda")
+    none = torch.empty(0, dtype=torch.uint8, device="cuda")
+    for before in (float("nan"), float("inf"), -1.0):
+        g = torch.tensor([before], device="cuda")
+        mx.matvec_nvfp4(rand((T, 64), 1, dtype), codes, scales, g)
+        x = torch.empty((T, 0), dtype=dtype, device="cuda")
+        y = torch.full((T, 400), 5.0, dtype=F32, device="cuda")
+        mx.matvec_nvfp4(x, empty, none, g, out=y)
+        assert torch.equal(y.view(torch.int32), torch.zeros_like(y, dtype=torch.int32))
+        y = torch.full((T, 400), 5.0, dtype=F32, device="cuda")
+        off = torch.tensor([0, 1, T], dtype=torch.int32, device="cuda")
+        mx.moe_matvec_nvfp4(x, None, off, torch.empty((2, 400, 0), dtype=torch.uint8, device="cuda"), none,
+                            g.repeat(2), out=y)
+        assert torch.equal(y.view(torch.int32), torch.zeros_like(y, dtype=torch.int32))
