@@ -331,8 +331,9 @@ struct Stage {
 template <bool kNv>
 __device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head, int d, int D, float4 acc,
                                           float sum) {
-  const float by = kNv ? sum * __ldg(p.global_scales[1]) : sum;
-  auto one = [&](float v) { return sum == 0.0f ? 0.0f : v / by; };
+  // one after the other: their product may be past float32
+  const float by = kNv ? __ldg(p.global_scales[1]) : 1.0f;
+  auto one = [&](float v) { return sum == 0.0f ? 0.0f : kNv ? v / sum / by : v / sum; };
   uint2 y;
   if (p.f16) {
     y.x = pack_f16x2(one(acc.x), one(acc.y));

@@ -1,4 +1,5 @@
-"""Attention over the paged 4-bit cache where few bits decide."""
+"""Attention over the paged 4-bit cache where few bits decide, and near the ends of
+float32."""
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 import decode_reference as R
 from test_gpu_attention_split import with_room
-from test_gpu_cache import BF16, F16, make_cache, mx, rand  # noqa: F401
+from test_gpu_cache import BF16, F16, filled, make_cache, mx, rand, tables  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,20 @@ def test_tail_beside_a_dominant_position(mx, gap, n, room, nvfp4, dtype):  # noq
     keep = [0, 1] if gap > 12 else [0, 1, 2]             # 2.0: twice the gap
     R.close(o[0, keep], want[keep], (off + R.unit(dtype) * (want.abs() + off) + R.smallest(dtype))[keep])
     R.close(lse[0], torch.logsumexp(a, -1), 2.0 ** -18 + 2.0 ** -22 * a.abs().amax(-1))
+
+
+@pytest.mark.parametrize("room", [False, True])
+@pytest.mark.parametrize("v_global", [1e36, -3e38, 1e-30])
+def test_global_scale_of_values_near_the_range(mx, v_global, room):  # noqa: F811
+    """The sum of the weights times the values' global scale is past float32."""
+    n, S, D = 1000, 16, 64
+    c = filled(mx, 64, S, 1, D, True, 6)
+    c.v_scales.fill_(0x38)                                           # 1.0
+    c.v_codes.fill_(0x77)                                            # 6.0 everywhere
+    c = c._replace(v_global=torch.tensor([v_global], device="cuda"))
+    table = tables(1, 63, 64, 1)
+    q = rand((1, 4, D), 5)
+    o, _, _ = mx.cache_attention(q, c, with_room(table, S) if room else table,
+                                 torch.tensor([n], dtype=torch.int32, device="cuda"), 0.01)
+    want = torch.full((1, 4, D), 6.0 / v_global, dtype=torch.float64, device="cuda")
+    R.close(o, want, 2.0 ** -7 * want.abs() + R.smallest(BF16))
