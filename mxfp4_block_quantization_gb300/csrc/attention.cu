@@ -614,9 +614,10 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
         q[n][i] = make_uint4(q[n][i].x ^ sign, q[n][i].y ^ sign, q[n][i].z ^ sign, q[n][i].w ^ sign);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        // not zero: a masked score is -infinity, and stays that
+        // not zero: a masked score is -infinity, and stays that; the smallest float
+        // instead moves no score by more than 2^-21
         const float f = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4 * e) * fabsf(more);
-        qs[n][e] = f < 0x1p-126f ? 0x1p-126f : f;
+        qs[n][e] = f == 0.0f ? 0x1p-149f : f;
       }
     }
 

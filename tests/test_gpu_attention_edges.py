@@ -70,3 +70,29 @@ def test_global_scale_of_values_near_the_range(mx, v_global, room):  # noqa: F81
                                  torch.tensor([n], dtype=torch.int32, device="cuda"), 0.01)
     want = torch.full((1, 4, D), 6.0 / v_global, dtype=torch.float64, device="cuda")
     R.close(o, want, 2.0 ** -7 * want.abs() + R.smallest(BF16))
+
+
+def key_scales(c, low, high, seed):
+    """Random E8M0 bytes in [low, high] for the keys."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    c.k_scales.copy_(torch.randint(low, high + 1, c.k_scales.shape, device="cuda", generator=gen).to(torch.uint8))
+
+
+def check_scores(mx, q, c, n, scale, room, S=16):
+    table = tables(1, -(-n // S), c.k_codes.shape[0], 1)
+    o, lse, _ = mx.cache_attention(q, c, with_room(table, S) if room else table,
+                                   torch.tensor([n], dtype=torch.int32, device="cuda"), scale)
+    k, v = contents(c, table[0].long(), n)
+    G = q.shape[1] // k.shape[0]
+    for h in range(k.shape[0]):
+        want, bound, wl, bl = R.attention(q[0, h * G:(h + 1) * G], k[h], v[h], scale, q.dtype)
+        R.close(o[0, h * G:(h + 1) * G], want, bound)
+        R.close(lse[0, h * G:(h + 1) * G], wl, bl)
+
+
+@pytest.mark.parametrize("room", [False, True])
+@pytest.mark.parametrize("scale", [0.0, 1e-39, -3e-45, 2.0 ** -104])
+def test_vanishing_scales_beside_large_keys(mx, scale, room):  # noqa: F811
+    c = filled(mx, 20, 16, 2, 64, False, 6)
+    key_scales(c, 127 + 100, 127 + 103, 1)
+    check_scores(mx, rand((1, 8, 64), 5), c, 300, scale, room)
