@@ -577,9 +577,21 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
     }
 
     // ---- q: a lane holds elements 8c..8c+7 of each 32-element block of head g,
-    // as halves; BF16 scaled by the head's power of two (see matvec.cu)
+    // as halves; BF16 scaled by the head's power of two (see matvec.cu).  With MXFP4
+    // keys, which may be of any size, the largest of the unit's heads goes into the
+    // keys' scales, so that the scores' sums are of the size of q . k.
     uint4 q[NB][DB];
     float qs[NB][2];  // what undoes it, with the softmax's scale, for heads 2c and 2c + 1 of a block
+    float inverse[NB], common = 1.0f;
+    auto set_factor = [&](int n, float more) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // not zero: a masked score is -infinity, and stays that; the smallest float
+        // instead moves no score by more than 2^-21
+        const float f = __shfl_sync(0xFFFFFFFFu, inverse[n], 8 * c + 4 * e) * fabsf(more);
+        qs[n][e] = f == 0.0f ? 0x1p-149f : f;
+      }
+    };
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
       const int h = n * kColumns + g;
@@ -595,11 +607,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
         m = max_finite_bf16x2(max_finite_bf16x2(m, v.x), v.y);
         m = max_finite_bf16x2(max_finite_bf16x2(m, v.z), v.w);
       }
-      float inverse = 1.0f;
+      inverse[n] = 1.0f;
       if (!p.f16) {
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        const float f = half_scale(m, inverse);
+        const float f = half_scale(m, inverse[n]);
         auto scaled = [&](uint32_t v) {
           return pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
         };
@@ -612,12 +624,18 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
 #pragma unroll
       for (int i = 0; i < DB; ++i)
         q[n][i] = make_uint4(q[n][i].x ^ sign, q[n][i].y ^ sign, q[n][i].z ^ sign, q[n][i].w ^ sign);
+      if constexpr (kNv) set_factor(n, more);
+    }
+    if constexpr (!kNv) {
+      uint32_t bits = 1u << 23;  // the powers' order is that of their bits
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // not zero: a masked score is -infinity, and stays that; the smallest float
-        // instead moves no score by more than 2^-21
-        const float f = __shfl_sync(0xFFFFFFFFu, inverse, 8 * c + 4 * e) * fabsf(more);
-        qs[n][e] = f == 0.0f ? 0x1p-149f : f;
+      for (int n = 0; n < NB; ++n) bits = max(bits, __float_as_uint(inverse[n]));
+      bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+      common = __uint_as_float(bits);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        inverse[n] *= __uint_as_float((254u << 23) - bits);
+        set_factor(n, p.softmax_scale * kLog2e);
       }
     }
 
@@ -657,7 +675,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
 #pragma unroll
           for (int i = 0; i < DB; ++i) {
             const uint32_t pair = e8m0x2_to_bf16x2(sk[i / 4] >> (16 * (i / 2 % 2)));
-            sts32(st + S::kScaleK + (lane * DB + i) * 4, i & 1 ? pair & 0xFFFF0000u : pair << 16);
+            const float f = __uint_as_float(i & 1 ? pair & 0xFFFF0000u : pair << 16) * common;
+            sts32(st + S::kScaleK + (lane * DB + i) * 4, __float_as_uint(f));
             byte[i] = static_cast<int>((sv[i / 4] >> (8 * (i % 4))) & 0xFFu);
             more |= byte[i] > vref[i];
           }

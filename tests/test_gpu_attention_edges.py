@@ -96,3 +96,14 @@ def test_vanishing_scales_beside_large_keys(mx, scale, room):  # noqa: F811
     c = filled(mx, 20, 16, 2, 64, False, 6)
     key_scales(c, 127 + 100, 127 + 103, 1)
     check_scores(mx, rand((1, 8, 64), 5), c, 300, scale, room)
+
+
+@pytest.mark.parametrize("room", [False, True])
+@pytest.mark.parametrize("key,query", [(110, 0), (118, -20), (123, -100), (60, 60), (-120, 0), (-126, 20), (-60, -60)])
+def test_keys_and_queries_near_the_range(mx, key, query, room):  # noqa: F811
+    """Keys of up to 2^125 and down to 2^-127: the scores are of ordinary size
+    after the softmax's scale."""
+    c = filled(mx, 20, 16, 2, 64, False, 6)
+    key_scales(c, max(127 + key - 1, 0), 127 + key + 1, 2)
+    q = (rand((1, 8, 64), 5).float() * 2.0 ** query).to(BF16)
+    check_scores(mx, q, c, 300, 0.1 * 2.0 ** -max(min(key + query, 125), -125), room)
