@@ -598,8 +598,8 @@ int mxfp4_dequantize_nvfp4(const uint8_t* codes, const uint8_t* scales,
  * x           BF16 [num_tokens, K], row stride ldx elements (ldx >= K,
  *             ldx % 8 == 0), 16-byte aligned; num_tokens may be any size, the
  *             call is made for few (weights are read once per 16 tokens).
- *             Inside a 32-element block of x, a value more than 2^39 below the
- *             block's largest is rounded to a multiple of 2^-40 of it.
+ *             Inside a 32-element block of x, a value more than 2^32 below the
+ *             block's largest may be off by up to 2^-40 of that largest.
  * codes       [N, K/2] packed E2M1 codes as mxfp4_quantize writes them,
  *             16-byte aligned; K % 32 == 0.
  * scales      mxfp4_scale_bytes(N, K) bytes, tiled layout, 16-byte aligned; the
@@ -748,6 +748,8 @@ int mxfp4_cache_read_nvfp4_f16(const uint8_t* k_codes, const uint8_t* k_scales,
  * q               BF16 (_f16: binary16): element d of head h of sequence b at
  *                 b*q_seq_stride + h*q_head_stride + d; strides % 8 == 0,
  *                 >= 0, 16-byte aligned.
+ *                 Inside a BF16 head, a value more than 2^32 below the head's
+ *                 largest may be off by up to 2^-40 of that largest.
  * head_dim        % 32 == 0, <= MXFP4_ATTENTION_MAX_HEAD_DIM.  The cache has
  *                 fewer than 2^32 rows (pages * page_size * kv heads), and
  *                 num_seqs * ceil(num_q_heads / num_kv_heads / 8) *

@@ -577,7 +577,11 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
     }
 
     // ---- q: a lane holds elements 8c..8c+7 of each 32-element block of head g,
-    // as halves; BF16 scaled by the head's power of two (see matvec.cu).  With MXFP4
+    // as halves; BF16 scaled by the head's power of two (see matvec.cu), which keeps
+    // it exactly down to 2^-32 of its largest element and to 2^-40 of that below.  (A
+    // power for each block where a head is wider, applied to the blocks' partial
+    // scores: 64 sequences of 8192 99.4 -> 101.9 us, one of 700 6.4 -> 6.7, 32 of 4096
+    // with 128 heads on 8 49.6 -> 51.5, whether a head is or not.)  With MXFP4
     // keys, which may be of any size, the largest of the unit's heads goes into the
     // keys' scales, so that the scores' sums are of the size of q . k.
     uint4 q[NB][DB];

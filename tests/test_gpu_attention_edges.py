@@ -107,3 +107,38 @@ def test_keys_and_queries_near_the_range(mx, key, query, room):  # noqa: F811
     key_scales(c, max(127 + key - 1, 0), 127 + key + 1, 2)
     q = (rand((1, 8, 64), 5).float() * 2.0 ** query).to(BF16)
     check_scores(mx, q, c, 300, 0.1 * 2.0 ** -max(min(key + query, 125), -125), room)
+
+
+@pytest.mark.parametrize("room", [False, True])
+@pytest.mark.parametrize("D,group", [(64, 4), (128, 16), (96, 3), (256, 1), (224, 8)])
+@pytest.mark.parametrize("power", [20, 30, 36])
+def test_queries_of_a_wide_range(mx, power, D, group, room):  # noqa: F811
+    """The query's blocks are far apart and the keys' the other way round: every
+    block weighs the same in a score.  A query's value may be off by 2^-40 of its
+    head's largest where it is under 2^-32 of it."""
+    S, n = 16, 300
+    c = filled(mx, 20, S, 2, D, False, 6)
+    q = rand((1, 2 * group, D), 5).float()
+    for i in range(D // 32):
+        e = -power if i % 2 else 0
+        q[..., 32 * i:32 * i + 32] *= 2.0 ** e
+        c.k_scales[..., i] += -power - e + 10
+    q, scale = q.to(BF16), 0.02 * 2.0 ** (power - 10)
+    table = tables(1, -(-n // S), 20, 1)
+    o, lse, _ = mx.cache_attention(q, c, with_room(table, S) if room else table,
+                                   torch.tensor([n], dtype=torch.int32, device="cuda"), scale)
+    k, v = contents(c, table[0].long(), n)
+    for h in range(2):
+        qh = q[0, h * group:(h + 1) * group].double()
+        top = qh.abs().amax(-1, keepdim=True)
+        off = torch.where(qh.abs() < 2.0 ** -32 * top, 2.0 ** -40 * top, 0.0)
+        a = scale * (qh @ k[h].T)
+        d = scale * ((D + 8) * 2.0 ** -23 * (qh.abs() @ k[h].abs().T) + off @ k[h].abs().T)
+        p = torch.softmax(a, -1)
+        want = p @ v[h]
+        # a weight moves by exp of twice the scores' largest error
+        rel = 2.0 ** -10 + torch.expm1(2 * d.amax(-1, keepdim=True)) + n * 2.0 ** -22 + 2.0 ** -19
+        bound = rel * (p @ v[h].abs()) + 2.0 ** -23 * v.abs().amax()
+        bound += R.unit(BF16) * (want.abs() + bound)
+        R.close(o[0, h * group:(h + 1) * group], want, bound)
+        R.close(lse[0, h * group:(h + 1) * group], torch.logsumexp(a, -1), d.amax(-1) + n * 2.0 ** -22 + 2.0 ** -17)
