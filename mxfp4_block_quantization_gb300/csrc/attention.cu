@@ -130,7 +130,7 @@ __device__ __forceinline__ bool positions(const AttentionParams& p, int b, int& 
 __device__ __forceinline__ int steps_of(const AttentionParams& p, int b) {
   int lo, hi;
   positions(p, b, lo, hi);
-  return (hi - lo + kStep - 1) / kStep;
+  return static_cast<int>((static_cast<unsigned>(hi - lo) + kStep - 1) / kStep);
 }
 __device__ __forceinline__ bool one_sequence(const AttentionParams& p) {
   return p.num_seqs == 1 && p.workers >= p.num_kv_heads * p.chunks;
@@ -261,7 +261,7 @@ __device__ __forceinline__ void write_status(const AttentionParams& p) {
   const int lane = threadIdx.x % per, stride = kThreads / per;
   int bad = 0;
   for (int64_t b0 = threadIdx.x / per; b0 < p.num_seqs; b0 += kSeqs * stride) {
-    int i[kSeqs], last[kSeqs];
+    int64_t i[kSeqs], last[kSeqs];
     int32_t page[kSeqs][kEntries];
 #pragma unroll
     for (int k = 0; k < kSeqs; ++k) {
@@ -281,7 +281,7 @@ __device__ __forceinline__ void write_status(const AttentionParams& p) {
       for (int k = 0; k < kSeqs; ++k)
 #pragma unroll
         for (int j = 0; j < kEntries; ++j) {
-          const int at = i[k] + j * per;
+          const int64_t at = i[k] + j * per;
           const int32_t* entry = p.page_table + (b0 + k * stride) * p.table_stride + at;
           page[k][j] = at > last[k] ? 0 : MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
         }
@@ -492,22 +492,25 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
     const int kvh = unit % p.num_kv_heads, chunk = unit / p.num_kv_heads;
     int lo, hi;
     positions(p, b, lo, hi);
-    const int first = lo + s0 * kStep, last = min(hi, lo + s1 * kStep);
+    // positions past the last one, up to 2^31 + a step and a share's padding, are unsigned
+    const unsigned first = lo + static_cast<unsigned>(s0) * kStep;
+    const unsigned last = min(static_cast<unsigned>(hi), lo + static_cast<unsigned>(s1) * kStep);
+    const unsigned page_size = p.page_size;
     const int head0 = kvh * p.group + chunk * kHeads;
     const int heads = min(kHeads, p.group - chunk * kHeads);
     __syncwarp();  // the unit before is done with the ring
 
     // ---- copies
     const int32_t* table = p.page_table + b * p.table_stride;
-    int next = first + lane;  // this lane's position in the step to copy
-    int in_page = next % p.page_size;
-    const int page_step = kStep / p.page_size;
-    const int in_step = kStep - page_step * p.page_size;
+    unsigned next = first + lane;  // this lane's position in the step to copy
+    unsigned in_page = next % page_size;
+    const unsigned page_step = kStep / page_size;
+    const unsigned in_step = kStep - page_step * page_size;
     // where the position kAhead steps on has its page
-    int ahead = next + kAhead * kStep;
-    int ahead_at = ahead / p.page_size, ahead_in = ahead - ahead_at * p.page_size;
-    auto load_page = [&](int position) {
-      const int32_t* entry = table + position / p.page_size;
+    unsigned ahead = next + kAhead * kStep;
+    unsigned ahead_at = ahead / page_size, ahead_in = ahead - ahead_at * page_size;
+    auto load_page = [&](unsigned position) {
+      const int32_t* entry = table + position / page_size;
       return position < last && MXFP4_IN_BOUNDS(p, kDbgTable, entry, 4) ? __ldg(entry) : -1;
     };
     uint32_t fill = 0;  // stage to fill
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
       if (next - lane < last) {
         const bool ok = next < last && page >= 0 && page < p.num_pages;
         const uint32_t valid = __ballot_sync(0xFFFFFFFFu, ok);
-        const uint32_t row = ok ? (static_cast<uint32_t>(page) * p.num_kv_heads + kvh) * p.page_size + in_page : 0u;
+        const uint32_t row = ok ? (static_cast<uint32_t>(page) * p.num_kv_heads + kvh) * page_size + in_page : 0u;
         const uint32_t st = ring + fill;
 #pragma unroll
         for (int i = 0; i < DB; ++i) {
@@ -557,12 +560,12 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
         fill = fill == kAhead * S::kBytes ? 0 : fill + S::kBytes;
         next += kStep;
         in_page += in_step;
-        if (in_page >= p.page_size) in_page -= p.page_size;
+        if (in_page >= page_size) in_page -= page_size;
         ahead += kStep;
         ahead_at += page_step;
         ahead_in += in_step;
-        if (ahead_in >= p.page_size) {
-          ahead_in -= p.page_size;
+        if (ahead_in >= page_size) {
+          ahead_in -= page_size;
           ++ahead_at;
         }
       }
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
     for (int i = 0; i < DB; ++i) vref[i] = 0;
 
     uint32_t read = 0;
-    for (int t0 = first; t0 < last; t0 += kStep) {
+    for (unsigned t0 = first; t0 < last; t0 += kStep) {
       cp_wait<kAhead - 1>();
       const uint32_t st = ring + read;
       read = read == kAhead * S::kBytes ? 0 : read + S::kBytes;

@@ -142,3 +142,27 @@ def test_queries_of_a_wide_range(mx, power, D, group, room):  # noqa: F811
         bound += R.unit(BF16) * (want.abs() + bound)
         R.close(o[0, h * group:(h + 1) * group], want, bound)
         R.close(lse[0, h * group:(h + 1) * group], torch.logsumexp(a, -1), d.amax(-1) + n * 2.0 ** -22 + 2.0 ** -17)
+
+
+@pytest.mark.parametrize("end,window", [(0, 100), (0, 1), (17, 33), (1, 4000)])
+@pytest.mark.parametrize("nvfp4", [False, True])
+def test_positions_up_to_the_largest_length(mx, end, window, nvfp4):  # noqa: F811
+    """The last positions of a length of 2^31 - 2: what lies a few steps past them is
+    past 32 signed bits.  The table's pages are all one."""
+    S, D = 1549411, 32
+    pages = (2 ** 31 - 1) // S                        # S * pages == 2^31 - 2
+    n = S * pages - end
+    assert S * pages == 2 ** 31 - 2
+    c = filled(mx, 1, S, 1, D, nvfp4, 6)
+    table = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    q = rand((1, 4, D), 5)
+    o, lse, st = mx.cache_attention(q, c, table, torch.tensor([n], dtype=torch.int32, device="cuda"), 0.2,
+                                    window=window)
+    assert int(st.item()) == 0
+    last = (n - 1) % S + 1
+    c = c._replace(**{f: getattr(c, f)[:, :, last - window:last] for f in
+                      ("k_codes", "k_scales", "v_codes", "v_scales")})
+    k, v = contents(c, torch.tensor([0], device="cuda"), window)
+    want, bound, wl, bl = R.attention(q[0], k[0], v[0], 0.2, BF16)
+    R.close(o[0], want, bound)
+    R.close(lse[0], wl, bl)
