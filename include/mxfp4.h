@@ -764,7 +764,8 @@ int mxfp4_cache_read_nvfp4_f16(const uint8_t* k_codes, const uint8_t* k_scales,
  *                 mxfp4_cache_attention_workspace_bytes(...) bytes (partial
  *                 results of long sequences split over warps; NULL allowed when
  *                 that is 0); contents on entry irrelevant.  Two calls in
- *                 flight at once need two workspaces.
+ *                 flight at once need two workspaces.  The query is for the
+ *                 current device: the parts are as many as its SMs hold.
  * out             [num_seqs, num_q_heads, head_dim], q's type, contiguous.
  *                 A sequence with no positions gives zeros.
  * lse             DEVICE float32 [num_seqs, num_q_heads] or NULL, out: the

@@ -1052,11 +1052,19 @@ def mxfp4_cache_read(cache, slots, k_out, v_out, status=None, stream=None) -> No
 
 
 @functools.lru_cache(maxsize=1024)
+def _attention_workspace_bytes(device, *sizes) -> int:
+    """The query on ``device`` (an index; None: the one that no call has changed)."""
+    if device is None or device == _get_device():
+        return int(_lib.mxfp4_cache_attention_workspace_bytes(*map(int, sizes)))
+    with torch.cuda.device(device):
+        return int(_lib.mxfp4_cache_attention_workspace_bytes(*map(int, sizes)))
+
+
 def mxfp4_cache_attention_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int,
                                           head_dim: int, page_size: int, max_pages: int) -> int:
-    return int(_lib.mxfp4_cache_attention_workspace_bytes(
-        int(num_seqs), int(num_q_heads), int(num_kv_heads), int(head_dim), int(page_size),
-        int(max_pages)))
+    """Bytes of workspace on the current device."""
+    return _attention_workspace_bytes(_get_device() if torch.cuda.is_initialized() else None, num_seqs,
+                                      num_q_heads, num_kv_heads, head_dim, page_size, max_pages)
 
 
 def mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, out, window=0,
@@ -1366,8 +1374,8 @@ def cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, window
         lse = _empty((B, Hq), torch.float32, q.device, stream)
     if status is None:
         status = _empty(1, torch.int32, q.device, stream)
-    nbytes = mxfp4_cache_attention_workspace_bytes(B, Hq, cache.k_codes.shape[1], D,
-                                                   cache.k_codes.shape[2], page_table.shape[1])
+    nbytes = _attention_workspace_bytes(q.get_device(), B, Hq, cache.k_codes.shape[1], D,
+                                        cache.k_codes.shape[2], page_table.shape[1])
     ws = _empty(nbytes, torch.uint8, q.device, stream) if nbytes else None
     mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale, out, window, ws, lse,
                           status, stream)

@@ -1109,8 +1109,9 @@ cudaError_t launch_format(const AttentionParams& p, unsigned grid, cudaStream_t 
                     kThreads, 0, stream, p);
 }
 
-int64_t resident_ctas(int32_t head_dim, bool cluster, int columns) {
-  return 152 * ctas_of(head_dim / 32, cluster, columns / kColumns);
+// CTAs that `sms` SMs, the current device's, hold at once.
+int64_t resident_ctas(int sms, int32_t head_dim, bool cluster, int columns) {
+  return static_cast<int64_t>(sms) * ctas_of(head_dim / 32, cluster, columns / kColumns);
 }
 // Contexts that one warp takes whole: a step.
 bool one_step(int64_t max_len) { return max_len <= kStep; }
@@ -1120,11 +1121,11 @@ bool one_step(int64_t max_len) { return max_len <= kStep; }
 // clusters leave: 8.5 -> 6.5 us for one sequence of 700 positions (64 heads on 8,
 // head_dim 128), 26.9 -> 21.8 for 64 of up to 1024 (8 steps); at 12 steps, one
 // of 12000, 14.3 -> 15.8.
-int cluster_ctas(int64_t units, int32_t head_dim, int columns, int64_t max_len) {
+int cluster_ctas(int sms, int64_t units, int32_t head_dim, int columns, int64_t max_len) {
   constexpr int64_t kFewSteps = 8;
   constexpr int kMost = 8;  // the portable size
   if (one_step(max_len)) return 0;
-  const int64_t steps = (max_len + kStep - 1) / kStep, most = resident_ctas(head_dim, true, columns);
+  const int64_t steps = (max_len + kStep - 1) / kStep, most = resident_ctas(sms, head_dim, true, columns);
   int ctas = 1;
   while (ctas < kMost && steps > ctas * kWarps && units * ctas * 2 <= most) ctas *= 2;
   return units * ctas <= most && steps <= kFewSteps * ctas * kWarps ? ctas : 0;
@@ -1133,9 +1134,9 @@ int cluster_ctas(int64_t units, int32_t head_dim, int columns, int64_t max_len) 
 // Warps that share the positions of all sequences: as many as the GPU holds at
 // once, so that all end together; 0 for contexts so short that a warp or a
 // cluster takes a unit whole.
-int shared_workers(int64_t units, int32_t head_dim, int columns, int64_t max_len) {
-  if (one_step(max_len) || cluster_ctas(units, head_dim, columns, max_len) > 0) return 0;
-  const int64_t resident = resident_ctas(head_dim, false, columns) * kWarps;
+int shared_workers(int sms, int64_t units, int32_t head_dim, int columns, int64_t max_len) {
+  if (one_step(max_len) || cluster_ctas(sms, units, head_dim, columns, max_len) > 0) return 0;
+  const int64_t resident = resident_ctas(sms, head_dim, false, columns) * kWarps;
   const int64_t most = (units * ((max_len + kStep - 1) / kStep) + kWarps - 1) / kWarps * kWarps;
   return static_cast<int>(most < resident ? most : resident);
 }
@@ -1146,12 +1147,13 @@ int shared_workers(int64_t units, int32_t head_dim, int columns, int64_t max_len
 // 48.3 us; one of 700, with half as many warps to share it, 7.6 -> 8.7.  64 heads on
 // 4 of 64, 8 of 4096 (2.7 steps): 13.2 -> 10.7; 80 on 5 of 128, 16 of 1000 (2.1):
 // 11.2 -> 11.9.
-int columns_of(int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int64_t max_len) {
+int columns_of(int sms, int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+               int64_t max_len) {
   const int group = num_q_heads / num_kv_heads;
   if (group <= kColumns || head_dim > 128) return kColumns;
   const int64_t units = num_seqs * num_kv_heads * ((group + kColumns - 1) / kColumns);
   const int64_t steps = units * ((max_len + kStep - 1) / kStep);
-  return 2 * steps >= 5 * kWarps * resident_ctas(head_dim, true, kColumns) ? 2 * kColumns : kColumns;
+  return 2 * steps >= 5 * kWarps * resident_ctas(sms, head_dim, true, kColumns) ? 2 * kColumns : kColumns;
 }
 
 }  // namespace
@@ -1159,10 +1161,10 @@ int columns_of(int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int3
 int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                    int32_t head_dim, int64_t max_len) {
   if (num_seqs == 0 || num_q_heads == 0 || head_dim == 0) return 0;
-  const int group = num_q_heads / num_kv_heads;
-  const int columns = columns_of(num_seqs, num_q_heads, num_kv_heads, head_dim, max_len);
+  const int sms = sm_count(), group = num_q_heads / num_kv_heads;
+  const int columns = columns_of(sms, num_seqs, num_q_heads, num_kv_heads, head_dim, max_len);
   const int64_t units = num_seqs * num_kv_heads * ((group + columns - 1) / columns);
-  const int workers = shared_workers(units, head_dim, columns, max_len);
+  const int workers = shared_workers(sms, units, head_dim, columns, max_len);
   return workers > 0 ? (units + workers) * columns * (head_dim + 2) + 4 * units + workers : 0;
 }
 
@@ -1200,11 +1202,12 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
     return launch_pdl(attention_status_kernel, 1, kThreads, 0, stream, p);
   }
   p.group = a.num_q_heads / c.num_heads;
-  p.columns = columns_of(a.num_seqs, a.num_q_heads, c.num_heads, c.head_dim, a.max_pages * c.page_size);
+  const int sms = sm_count();
+  p.columns = columns_of(sms, a.num_seqs, a.num_q_heads, c.num_heads, c.head_dim, a.max_pages * c.page_size);
   p.chunks = (p.group + p.columns - 1) / p.columns;
   const int64_t units = a.num_seqs * c.num_heads * p.chunks;
-  p.workers = shared_workers(units, c.head_dim, p.columns, a.max_pages * c.page_size);
-  p.ctas = cluster_ctas(units, c.head_dim, p.columns, a.max_pages * c.page_size);
+  p.workers = shared_workers(sms, units, c.head_dim, p.columns, a.max_pages * c.page_size);
+  p.ctas = cluster_ctas(sms, units, c.head_dim, p.columns, a.max_pages * c.page_size);
   p.part_o = a.workspace;
   p.part_ml = p.part_o + (units + p.workers) * p.columns * c.head_dim;
   p.parts = reinterpret_cast<int4*>(p.part_ml + (units + p.workers) * p.columns * 2);

@@ -166,3 +166,12 @@ def test_positions_up_to_the_largest_length(mx, end, window, nvfp4):  # noqa: F8
     want, bound, wl, bl = R.attention(q[0], k[0], v[0], 0.2, BF16)
     R.close(o[0], want, bound)
     R.close(lse[0], wl, bl)
+
+
+def test_workspace_is_for_the_device(mx):  # noqa: F811
+    """As many warps share the steps as the device's SMs hold (head_dim 64: 4 CTAs of 4
+    warps each), whatever GPU it is: parts of 8 heads of 64 with a maximum and a sum, an
+    entry of 16 bytes per unit and a word per warp."""
+    units, warps = 8, 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    want = (units + warps) * 8 * (64 + 2) * 4 + units * 16 + warps * 4
+    assert mx.mxfp4_cache_attention_workspace_bytes(1, 8, units, 64, 16, 8192) == want
