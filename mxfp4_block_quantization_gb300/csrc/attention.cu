@@ -117,11 +117,12 @@ struct AttentionParams {
 #endif
 };
 
-enum : int { kDbgQ = 0, kDbgCodes0, kDbgCodes1, kDbgScales0, kDbgScales1, kDbgTable, kDbgOut, kDbgPart };
+enum : int { kDbgQ = 0, kDbgCodes0, kDbgCodes1, kDbgScales0, kDbgScales1, kDbgTable, kDbgOut, kDbgPart, kDbgLens, kDbgLse, kDbgStatus };
 
 // The positions [lo, hi) of sequence b; a length out of range gives none.
 __device__ __forceinline__ bool positions(const AttentionParams& p, int b, int& lo, int& hi) {
-  const int n = __ldg(p.seq_lens + b);
+  const int32_t* at = p.seq_lens + b;
+  const int n = MXFP4_IN_BOUNDS(p, kDbgLens, at, 4) ? __ldg(at) : 0;
   const bool ok = n >= 0 && n <= p.max_len;
   hi = ok ? n : 0;
   lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
@@ -296,7 +297,7 @@ __device__ __forceinline__ void write_status(const AttentionParams& p) {
     }
   }
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) *p.status = bad ? -7 : 0;
+  if (threadIdx.x == 0 && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4)) *p.status = bad ? -7 : 0;
 }
 
 // Shared memory of a stage, for head_dim = 32 * DB.
@@ -346,7 +347,8 @@ __device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head
   if (MXFP4_IN_BOUNDS(p, kDbgOut, to, 8)) *reinterpret_cast<uint2*>(to) = y;
 }
 __device__ __forceinline__ void store_lse(const AttentionParams& p, int64_t head, float sum, float top) {
-  if (p.lse != nullptr) p.lse[head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
+  if (p.lse != nullptr && MXFP4_IN_BOUNDS(p, kDbgLse, p.lse + head, 4))
+    p.lse[head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
 // The scale bytes of this lane's position, as words that start with the first.
@@ -944,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
                             });
     }
   }
-  if (!kCluster && p.workers > 0 && lane == 0) p.bad[worker] = bad;
+  if (!kCluster && p.workers > 0 && lane == 0 && MXFP4_IN_BOUNDS(p, kDbgPart, p.bad + worker, 4)) p.bad[worker] = bad;
   pdl_release();
 }
 
@@ -967,10 +969,11 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
     // status word: what the warps met, and every length
     int bad = 0, lo, hi;
 #pragma unroll 8
-    for (int w = threadIdx.x; w < p.workers; w += blockDim.x) bad |= p.bad[w];
+    for (int w = threadIdx.x; w < p.workers; w += blockDim.x)
+      if (MXFP4_IN_BOUNDS(p, kDbgPart, p.bad + w, 4)) bad |= p.bad[w];
     for (int64_t b = threadIdx.x; b < p.num_seqs; b += blockDim.x) bad |= !positions(p, static_cast<int>(b), lo, hi);
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *p.status = bad ? -7 : 0;
+    if (threadIdx.x == 0 && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4)) *p.status = bad ? -7 : 0;
     return;
   }
   const int64_t head = kPerHead == 1 ? static_cast<int64_t>(blockIdx.x - word) * kWarps + warp : blockIdx.x - word;
@@ -982,6 +985,7 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
   float top = -INFINITY, sum = 0.0f;
   float4 acc[2] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (steps_of(p, b) > 0) {
+    if (!MXFP4_IN_BOUNDS(p, kDbgPart, p.parts + unit, 16)) return;
     const int4 who = p.parts[unit];
     const Parts parts{who.x, who.y, who.z, who.w};
     const int n = parts.count();
@@ -997,11 +1001,13 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
       for (int k = 0; k < kBatch; ++k) {
         const int s = s0 + k * kPerHead;
         const int64_t slot = (unit + parts.warp(s)) * p.columns;
-        part[k] = s < n ? ml[slot] : make_float2(-INFINITY, 0.0f);
+        part[k] = s < n && MXFP4_IN_BOUNDS(p, kDbgPart, ml + slot, 8) ? ml[slot] : make_float2(-INFINITY, 0.0f);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          v[k][i] = s < n && i * 32 + lane < quads ? po[slot * quads + i * 32 + lane]
-                                                   : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          v[k][i] = s < n && i * 32 + lane < quads &&
+                            MXFP4_IN_BOUNDS(p, kDbgPart, po + (slot * quads + i * 32 + lane), 16)
+                        ? po[slot * quads + i * 32 + lane]
+                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       }
       float x = top;
 #pragma unroll
@@ -1197,6 +1203,12 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   p.scale_bytes = static_cast<uint64_t>(c.num_pages) * c.page_size * c.num_heads * (c.head_dim / (c.nvfp4 ? 16 : 32));
   p.f16 = c.f16;
   p.softmax_scale = a.softmax_scale;
+#ifdef MXFP4_DEBUG_BOUNDS
+  debug_range(p.dbg, kDbgLens, a.seq_lens, a.num_seqs * 4);
+  debug_range(p.dbg, kDbgStatus, a.status, a.status ? 4 : 0);
+  debug_range(p.dbg, kDbgTable, a.page_table,
+              a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
+#endif
   if (a.num_q_heads == 0 || c.head_dim == 0) {  // the status word alone
     if (a.status == nullptr) return cudaSuccess;
     return launch_pdl(attention_status_kernel, 1, kThreads, 0, stream, p);
@@ -1220,8 +1232,7 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
     debug_range(p.dbg, kDbgCodes0 + i, c.codes[i], rows * (c.head_dim / 2));
     debug_range(p.dbg, kDbgScales0 + i, c.scales[i], rows * (c.head_dim / (c.nvfp4 ? 16 : 32)));
   }
-  debug_range(p.dbg, kDbgTable, a.page_table,
-              a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
+  debug_range(p.dbg, kDbgLse, a.lse, a.lse ? a.num_seqs * a.num_q_heads * 4 : 0);
   debug_range(p.dbg, kDbgOut, a.out, a.num_seqs * a.num_q_heads * c.head_dim * 2);
   debug_range(p.dbg, kDbgPart, a.workspace,
               p.workers > 0 ? ((units + p.workers) * p.columns * (c.head_dim + 2) + 4 * units + p.workers) * 4 : 0);

@@ -60,7 +60,12 @@ struct CacheParams {
 #endif
 };
 
-enum : int { kDbgX0 = 0, kDbgX1, kDbgCodes0, kDbgCodes1, kDbgScales0, kDbgScales1, kDbgSlots };
+enum : int { kDbgX0 = 0, kDbgX1, kDbgCodes0, kDbgCodes1, kDbgScales0, kDbgScales1, kDbgSlots, kDbgStatus };
+
+__device__ __forceinline__ int32_t slot_at(const CacheParams& p, int64_t t) {
+  const int32_t* at = p.slots + t;
+  return MXFP4_IN_BOUNDS(p, kDbgSlots, at, 4) ? __ldg(at) : -1;
+}
 
 // Status word: from all the slots, by CTA 0, which does nothing else (with many
 // tokens it is as long as the others' work: 16 loads in flight, and first in the
@@ -71,11 +76,11 @@ __device__ __forceinline__ bool write_status(const CacheParams& p) {
   int bad = 0;
 #pragma unroll 16
   for (int64_t t = threadIdx.x; t < p.num_tokens; t += kThreads) {
-    const int32_t s = __ldg(p.slots + t);
+    const int32_t s = slot_at(p, t);
     if (s < -1 || s >= p.num_slots) bad = 1;
   }
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) *p.status = bad ? -7 : 0;
+  if (threadIdx.x == 0 && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4)) *p.status = bad ? -7 : 0;
   return true;
 }
 
@@ -121,7 +126,7 @@ __device__ __forceinline__ void for_places(const CacheParams& p, Body body) {
         tokens[i] = live && t < p.num_tokens ? static_cast<int32_t>(t) : -1;
         slots[i] = -1;
         if (tokens[i] >= 0) {
-          const int32_t s = __ldg(p.slots + t);
+          const int32_t s = slot_at(p, t);
           slots[i] = s < p.num_slots ? s : -1;
         }
       }
@@ -287,6 +292,8 @@ CacheParams cache_params(const CacheArgs& c, const int32_t* slots, int64_t num_t
     debug_range(p.dbg, kDbgCodes0 + i, c.codes[i], p.num_slots * (row / 2));
     debug_range(p.dbg, kDbgScales0 + i, c.scales[i], p.num_slots * (row / (c.nvfp4 ? 16 : 32)));
   }
+  debug_range(p.dbg, kDbgSlots, slots, num_tokens * 4);
+  debug_range(p.dbg, kDbgStatus, status, status ? 4 : 0);
 #endif
   return p;
 }

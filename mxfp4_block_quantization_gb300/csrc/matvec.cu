@@ -98,7 +98,16 @@ struct MatvecParams {
 #endif
 };
 
-enum : int { kDbgX = 0, kDbgCodes, kDbgScales, kDbgGlobal, kDbgY, kDbgIndex, kDbgOffsets };
+enum : int { kDbgX = 0, kDbgCodes, kDbgScales, kDbgGlobal, kDbgY, kDbgIndex, kDbgOffsets, kDbgStatus };
+
+__device__ __forceinline__ int32_t offset_at(const MatvecParams& p, int e) {
+  const int32_t* at = p.offsets + e;
+  return MXFP4_IN_BOUNDS(p, kDbgOffsets, at, 4) ? __ldg(at) : 0;
+}
+__device__ __forceinline__ int32_t index_at(const MatvecParams& p, int64_t r) {
+  const int32_t* at = p.row_index + r;
+  return MXFP4_IN_BOUNDS(p, kDbgIndex, at, 4) ? __ldg(at) : -1;
+}
 
 // The rows of one unit of work: up to 8*NT consecutive rows of one segment;
 // `x`: the first of its rows of x's shared memory.
@@ -143,7 +152,7 @@ __device__ __forceinline__ UnitRows find_unit(const MatvecParams& p, const Share
   const int per = (p.E + kThreads - 1) / kThreads;
   int e = lo * per;
   for (;; ++e) {
-    const int a = __ldg(p.offsets + e), n = __ldg(p.offsets + e + 1) - a;
+    const int a = offset_at(p, e), n = offset_at(p, e + 1) - a;
     const int c = (n + R - 1) / R;
     if (base + c > u || e + 1 >= p.E) {
       r.e = e;
@@ -199,11 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     for (int i = 0; i < per; ++i) {
       const int e = threadIdx.x * per + i;
       if (e >= p.E) break;
-      const int a = __ldg(p.offsets + e), b = __ldg(p.offsets + e + 1);
+      const int a = offset_at(p, e), b = offset_at(p, e + 1);
       if (a < 0 || b < a || b > p.rows || (e == 0 && a != 0)) bad = 1;
       else sum += (b - a + R - 1) / R;
     }
-    if (p.E == 0 && threadIdx.x == 0 && __ldg(p.offsets) != 0) bad = 1;
+    if (p.E == 0 && threadIdx.x == 0 && offset_at(p, 0) != 0) bad = 1;
     bad = __syncthreads_or(bad);
     int scan = sum;
 #pragma unroll
@@ -224,14 +233,14 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
     if (blockIdx.x == 0 && p.status != nullptr) {
       int wrong = 0;
       if (!bad && p.row_index != nullptr) {
-        const int used = p.E > 0 ? __ldg(p.offsets + p.E) : 0;
+        const int used = p.E > 0 ? offset_at(p, p.E) : 0;
         for (int r = threadIdx.x; r < used; r += kThreads) {
-          const int32_t i = __ldg(p.row_index + r);
+          const int32_t i = index_at(p, r);
           if (i < 0 || i >= p.src_rows) wrong = 1;
         }
       }
       wrong = __syncthreads_or(wrong);
-      if (threadIdx.x == 0) *p.status = bad ? -6 : wrong ? -7 : 0;
+      if (threadIdx.x == 0 && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4)) *p.status = bad ? -6 : wrong ? -7 : 0;
     }
     if (bad) return;
     __syncthreads();
@@ -292,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
       int64_t src = -1;
       if (r < sh.unit[i].n) {
         src = sh.unit[i].row0 + r;
-        if (p.row_index != nullptr) src = __ldg(p.row_index + src);
+        if (p.row_index != nullptr) src = index_at(p, src);
       }
       sh.x_row[threadIdx.x] = src >= 0 && src < p.src_rows ? src : -1;
       sh.x_unit[threadIdx.x] = r < sh.unit[i].n ? i : -1;
@@ -868,6 +877,9 @@ cudaError_t launch_matvec(const MatvecArgs& a, cudaStream_t stream) {
   debug_range(p.dbg, kDbgCodes, a.codes, a.E * p.expert_codes);
   debug_range(p.dbg, kDbgScales, a.scales, a.E * p.expert_scales);
   debug_range(p.dbg, kDbgGlobal, a.global_scales, a.nvfp4 ? a.E * 4 : 0);
+  debug_range(p.dbg, kDbgIndex, a.row_index, a.row_index ? a.rows * 4 : 0);
+  debug_range(p.dbg, kDbgOffsets, a.offsets, a.offsets ? (static_cast<int64_t>(a.E) + 1) * 4 : 0);
+  debug_range(p.dbg, kDbgStatus, a.status, a.status ? 4 : 0);
   debug_range(p.dbg, kDbgY, a.y, a.rows > 0 ? ((a.rows - 1) * a.ldy + a.N) * (a.y_f32 ? 4 : 2) : 0);
 #endif
   // Tokens per unit: 8 or 16 columns of the tensor-core product (more would
