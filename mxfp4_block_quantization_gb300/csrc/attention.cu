@@ -588,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
     // scores: 64 sequences of 8192 99.4 -> 101.9 us, one of 700 6.4 -> 6.7, 32 of 4096
     // with 128 heads on 8 49.6 -> 51.5, whether a head is or not.)  With MXFP4
     // keys, which may be of any size, the largest of the unit's heads goes into the
-    // keys' scales, so that the scores' sums are of the size of q . k.
+    // keys' scales, so that the scores' sums are of the size of q . k; not above 1, so
+    // that a head of any size leaves the others' sums as they are.
     uint4 q[NB][DB];
     float qs[NB][2];  // what undoes it, with the softmax's scale, for heads 2c and 2c + 1 of a block
     float inverse[NB], common = 1.0f;
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
       uint32_t bits = 1u << 23;  // the powers' order is that of their bits
 #pragma unroll
       for (int n = 0; n < NB; ++n) bits = max(bits, __float_as_uint(inverse[n]));
-      bits = __reduce_max_sync(0xFFFFFFFFu, bits);
+      bits = min(__reduce_max_sync(0xFFFFFFFFu, bits), (127u - 15u) << 23);
       common = __uint_as_float(bits);
 #pragma unroll
       for (int n = 0; n < NB; ++n) {

@@ -175,3 +175,22 @@ def test_workspace_is_for_the_device(mx):  # noqa: F811
     units, warps = 8, 16 * torch.cuda.get_device_properties(0).multi_processor_count
     want = (units + warps) * 8 * (64 + 2) * 4 + units * 16 + warps * 4
     assert mx.mxfp4_cache_attention_workspace_bytes(1, 8, units, 64, 16, 8192) == want
+
+
+@pytest.mark.parametrize("room", [False, True])
+@pytest.mark.parametrize("power", [40, 100, 118, -120])
+@pytest.mark.parametrize("group", [4, 16])
+def test_a_head_of_any_size_leaves_the_others(mx, power, group, room):  # noqa: F811
+    """Heads of one kv head whose queries are 2^power times the others'."""
+    c = filled(mx, 20, 16, 1, 64, False, 6)
+    key_scales(c, 127 + 3, 127 + 6, 3)
+    table, n = tables(1, 19, 20, 1), torch.tensor([300], dtype=torch.int32, device="cuda")
+    table = with_room(table, 16) if room else table
+    q = rand((1, group, 64), 5)
+    mixed = q.clone()
+    mixed[:, 1::2] = (mixed[:, 1::2].float() * 2.0 ** power).to(BF16)
+    o, lse, _ = mx.cache_attention(mixed, c, table, n, 0.01)
+    k, v = contents(c, table[0].long()[:19], 300)
+    full, bound, fl, bl = R.attention(q[0], k[0], v[0], 0.01, BF16)
+    R.close(o[0, ::2], full[::2], bound[::2])
+    R.close(lse[0, ::2], fl[::2], bl[::2])
