@@ -238,7 +238,7 @@ int attention_checked(const mxfp4::AttentionArgs& a, size_t workspace_bytes, voi
   int64_t bytes[2];
   if (const int rc = cache_checked(c, work && c.num_pages > 0 && a.max_pages > 0, bytes)) return rc;
   if (c.head_dim > MXFP4_ATTENTION_MAX_HEAD_DIM || a.max_pages > INT32_MAX / c.page_size ||
-      a.table_stride < a.max_pages)
+      a.table_stride < a.max_pages || a.num_seqs > kMaxGrid)
     return MXFP4_ESHAPE;
   // the steps of all (sequence, kv head, 8 query heads) are counted in int32,
   // padded by at most a share of each; rows of the cache in uint32
@@ -250,7 +250,10 @@ int attention_checked(const mxfp4::AttentionArgs& a, size_t workspace_bytes, voi
     return MXFP4_ESHAPE;
   if (a.num_q_heads > 0 && (c.num_heads == 0 || a.num_q_heads % c.num_heads != 0))
     return MXFP4_ESHAPE;
-  if (work && (!a.q || !a.out || !a.seq_lens || (a.max_pages > 0 && !a.page_table)))
+  if (work && (!a.q || !a.out)) return MXFP4_EINVAL;
+  // without heads the status word still comes from the lengths and pages
+  if ((work || (a.status && a.num_seqs > 0)) &&
+      (!a.seq_lens || (a.max_pages > 0 && !a.page_table)))
     return MXFP4_EINVAL;
   if (a.num_q_heads > 0 && a.num_seqs > kMaxGrid / a.num_q_heads) return MXFP4_ESHAPE;
   if (a.num_seqs > 0 && a.table_stride > (INT64_MAX / 8) / a.num_seqs) return MXFP4_ESHAPE;
