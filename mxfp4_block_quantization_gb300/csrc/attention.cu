@@ -54,6 +54,7 @@
 #include "fragments.cuh"
 #include "mxfp4_device.cuh"
 #include "mxfp4_internal.h"
+#include "nvfp4_device.cuh"
 
 namespace mxfp4 {
 namespace {
@@ -333,7 +334,7 @@ template <bool kNv>
 __device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head, int d, int D, float4 acc,
                                           float sum) {
   // one after the other: their product may be past float32
-  const float by = kNv ? __ldg(p.global_scales[1]) : 1.0f;
+  const float by = kNv ? global_scale_or_one(p.global_scales[1]) : 1.0f;
   auto one = [&](float v) { return sum == 0.0f ? 0.0f : kNv ? v / sum / by : v / sum; };
   uint2 y;
   if (p.f16) {
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
         for (int i = 0; i < DB; ++i)
           q[n][i] = make_uint4(scaled(q[n][i].x), scaled(q[n][i].y), scaled(q[n][i].z), scaled(q[n][i].w));
       }
-      const float more = p.softmax_scale * kLog2e / (kNv ? __ldg(p.global_scales[0]) : 1.0f);
+      const float more = p.softmax_scale * kLog2e / (kNv ? global_scale_or_one(p.global_scales[0]) : 1.0f);
       const uint32_t sign = more < 0.0f ? 0x80008000u : 0u;  // a larger product is a larger score
 #pragma unroll
       for (int i = 0; i < DB; ++i)

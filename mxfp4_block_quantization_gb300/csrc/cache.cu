@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheParams
   if (write_status(p)) return;
   float g[2] = {1.0f, 1.0f};
   if constexpr (kNv) {
-    g[0] = __ldg(p.global_scales[0]);
-    g[1] = __ldg(p.global_scales[1]);
+    g[0] = global_scale_or_one(p.global_scales[0]);
+    g[1] = global_scale_or_one(p.global_scales[1]);
   }
   for_places(p, [&](const Place& w, const int32_t (&slots)[kAtOnce], const int32_t (&tokens)[kAtOnce]) {
     uint4 v[kAtOnce][2];
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const CacheParams 
   if (write_status(p)) return;
   float inv[2] = {1.0f, 1.0f};
   if constexpr (kNv) {
-    inv[0] = 1.0f / __ldg(p.global_scales[0]);
-    inv[1] = 1.0f / __ldg(p.global_scales[1]);
+    inv[0] = 1.0f / global_scale_or_one(p.global_scales[0]);
+    inv[1] = 1.0f / global_scale_or_one(p.global_scales[1]);
   }
   for_places(p, [&](const Place& w, const int32_t (&slots)[kAtOnce], const int32_t (&tokens)[kAtOnce]) {
     uint2 c[kAtOnce];
