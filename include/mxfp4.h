@@ -597,7 +597,8 @@ int mxfp4_dequantize_nvfp4(const uint8_t* codes, const uint8_t* scales,
  *
  * x           BF16 [num_tokens, K], row stride ldx elements (ldx >= K,
  *             ldx % 8 == 0), 16-byte aligned; num_tokens may be any size, the
- *             call is made for few (weights are read once per 16 tokens).
+ *             call is made for few (weights are read once per 16 tokens, per 8
+ *             where there are 8 or fewer).
  *             Inside a 32-element block of x, a value more than 2^32 below the
  *             block's largest may be off by up to 2^-40 of that largest.
  * codes       [N, K/2] packed E2M1 codes as mxfp4_quantize writes them,
@@ -629,7 +630,8 @@ int mxfp4_matvec_nvfp4_f16(const void* x, int64_t num_tokens, int64_t K, int64_t
  * batch (expert_offsets[e] <= r < expert_offsets[e+1], as mxfp4_moe_route
  * writes them) times expert e's weights:
  *   y[r, n] = sum_k x[row_index ? row_index[r] : r, k] * W[e][n, k].
- * Only the weights of experts that have rows are read.
+ * Only the weights of experts that have rows are read, once per 16 of an
+ * expert's rows, or per 8 where total_rows / E is 6 or less on average.
  *
  * x               [num_src_rows, K], as in mxfp4_matvec.
  * row_index       DEVICE int32 [total_rows] or NULL (then num_src_rows >=
@@ -768,6 +770,9 @@ int mxfp4_cache_read_nvfp4_f16(const uint8_t* k_codes, const uint8_t* k_scales,
  *                 current device: the parts are as many as its SMs hold.
  * out             [num_seqs, num_q_heads, head_dim], q's type, contiguous.
  *                 A sequence with no positions gives zeros.
+ *                 Softmax weights are rounded to 11 bits, and to multiples of
+ *                 2^-36 of the largest; MXFP4 values whose scale is under 2^-24 of
+ *                 the largest of the same 32 elements of head_dim may count as zero.
  * lse             DEVICE float32 [num_seqs, num_q_heads] or NULL, out: the
  *                 natural logarithm of the softmax's denominator,
  *                 log sum_j exp(softmax_scale * q . k_j) (-inf without positions).

@@ -32,11 +32,12 @@
 // formed in halves, exactly.  V: a position's scales vary along the sum, so
 // they go into the operands: NVFP4 into V; MXFP4 into P, relative to the
 // largest scale that the warp has met in that 32-value block (an integer
-// maximum, with the output rescaled when it grows).  P is formed at 2^12 times
-// its size and rounded to a half there, so it has 11 bits down to 2^-26 of the
-// warp's largest and is lost under 2^-37 (beside a position that dominates with
-// a small value, the others are the output); the denominator's sum keeps it in
-// float32.  2^12 is divided out of the sums at the end.
+// maximum, with the output rescaled when it grows; under 2^-24 of it a scale
+// is zero).  P is formed at 2^12 times its size and rounded to a half there,
+// so it has 11 bits down to 2^-26 of the warp's largest and is lost under
+// 2^-37 (beside a position that dominates with a small value, the others are
+// the output); the denominator's sum keeps it in float32.  2^12 is divided out
+// of the sums at the end.
 //
 // Measured, 64 query heads on 8: 64 sequences of up to 8192 positions (head_dim
 // 128, MXFP4, 445 MB of cache) 99 us, 4.5 TB/s.  Without the products 87, without
