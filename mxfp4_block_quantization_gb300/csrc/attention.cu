@@ -40,22 +40,22 @@
 // of the sums at the end.
 //
 // Measured, 64 query heads on 8: 64 sequences of up to 8192 positions (head_dim
-// 128, MXFP4, 445 MB of cache) 99 us, 4.5 TB/s.  Without the products 87, without
-// the second kernel 5 less: what is left to win is the copies' latency at a unit's
-// start and the parts' way through L2, not arithmetic (the vector units that decode
-// are busy for 56 % of the cycles; a decode of V without its byte permutes, half the
-// multiplications of the scores and simpler addresses each changed the time by
-// 1 % at most).  One sequence of 131072 37.9 us (head_dim 64, NVFP4: 28.1), of 700
-// 6.4 us.
+// 128, MXFP4, 445 MB of cache) 98 to 100 us, 4.5 TB/s.  A copy of the kernel without
+// the products took 87, one without the second kernel 5 less: what is left to win is
+// the copies' latency at a unit's start and the parts' way through L2, not arithmetic
+// (the vector units that decode are busy for 57 % of the cycles; a decode of V
+// without its byte permutes, half the multiplications of the scores and simpler
+// addresses each changed the time by 1 % at most).  One sequence of 131072 38.3 us
+// (head_dim 64, NVFP4: 28.4), of 700 6.4 us.
 #include <cstdint>
 
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "cache_device.cuh"
 #include "fragments.cuh"
 #include "mxfp4_device.cuh"
 #include "mxfp4_internal.h"
-#include "nvfp4_device.cuh"
 
 namespace mxfp4 {
 namespace {
@@ -116,15 +116,19 @@ struct AttentionParams {
   float softmax_scale;
 #ifdef MXFP4_DEBUG_BOUNDS
   DebugRanges dbg;
+  struct {
+    DebugRanges dbg;
+  } more;  // of the second list below
 #endif
 };
 
-enum : int { kDbgQ = 0, kDbgCodes0, kDbgCodes1, kDbgScales0, kDbgScales1, kDbgTable, kDbgOut, kDbgPart, kDbgLens, kDbgLse, kDbgStatus };
+enum : int { kDbgQ = 0, kDbgCodes0, kDbgCodes1, kDbgScales0, kDbgScales1, kDbgTable, kDbgOut, kDbgPart };
+enum : int { kDbgLens = 0, kDbgLse, kDbgStatus };
 
 // The positions [lo, hi) of sequence b; a length out of range gives none.
 __device__ __forceinline__ bool positions(const AttentionParams& p, int b, int& lo, int& hi) {
   const int32_t* at = p.seq_lens + b;
-  const int n = MXFP4_IN_BOUNDS(p, kDbgLens, at, 4) ? __ldg(at) : 0;
+  const int n = MXFP4_IN_BOUNDS(p.more, kDbgLens, at, 4) ? __ldg(at) : 0;
   const bool ok = n >= 0 && n <= p.max_len;
   hi = ok ? n : 0;
   lo = p.window > 0 && hi > p.window ? hi - p.window : 0;
@@ -299,7 +303,7 @@ __device__ __forceinline__ void write_status(const AttentionParams& p) {
     }
   }
   bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0 && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4)) *p.status = bad ? -7 : 0;
+  if (threadIdx.x == 0 && MXFP4_IN_BOUNDS(p.more, kDbgStatus, p.status, 4)) *p.status = bad ? -7 : 0;
 }
 
 // Shared memory of a stage, for head_dim = 32 * DB.
@@ -349,7 +353,7 @@ __device__ __forceinline__ void store_out(const AttentionParams& p, int64_t head
   if (MXFP4_IN_BOUNDS(p, kDbgOut, to, 8)) *reinterpret_cast<uint2*>(to) = y;
 }
 __device__ __forceinline__ void store_lse(const AttentionParams& p, int64_t head, float sum, float top) {
-  if (p.lse != nullptr && MXFP4_IN_BOUNDS(p, kDbgLse, p.lse + head, 4))
+  if (p.lse != nullptr && MXFP4_IN_BOUNDS(p.more, kDbgLse, p.lse + head, 4))
     p.lse[head] = sum == 0.0f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
@@ -642,6 +646,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(DB, kCluster, NB)) attention
       uint32_t bits = 1u << 23;  // the powers' order is that of their bits
 #pragma unroll
       for (int n = 0; n < NB; ++n) bits = max(bits, __float_as_uint(inverse[n]));
+      // (In every form tried 128 heads on 8, 32 of 4096, took 47.6 -> 49 us for this, at
+      // 255 registers; 64 sequences of 8192 100 -> 99.)
       bits = min(__reduce_max_sync(0xFFFFFFFFu, bits), (127u - 15u) << 23);
       common = __uint_as_float(bits);
 #pragma unroll
@@ -976,7 +982,7 @@ __global__ void __launch_bounds__(kPerHead == 1 ? kThreads : 32 * kPerHead)
       if (MXFP4_IN_BOUNDS(p, kDbgPart, p.bad + w, 4)) bad |= p.bad[w];
     for (int64_t b = threadIdx.x; b < p.num_seqs; b += blockDim.x) bad |= !positions(p, static_cast<int>(b), lo, hi);
     bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0 && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4)) *p.status = bad ? -7 : 0;
+    if (threadIdx.x == 0 && MXFP4_IN_BOUNDS(p.more, kDbgStatus, p.status, 4)) *p.status = bad ? -7 : 0;
     return;
   }
   const int64_t head = kPerHead == 1 ? static_cast<int64_t>(blockIdx.x - word) * kWarps + warp : blockIdx.x - word;
@@ -1152,9 +1158,9 @@ int shared_workers(int sms, int64_t units, int32_t head_dim, int columns, int64_
 
 // Query heads of a unit: two column blocks, for which the cache is decoded once,
 // where a kv head has more than 8, the registers hold them, and each warp has 2.5
-// steps or more with one.  128 heads on 8 of 128: 32 sequences of up to 4096 55.2 ->
-// 48.3 us; one of 700, with half as many warps to share it, 7.6 -> 8.7.  64 heads on
-// 4 of 64, 8 of 4096 (2.7 steps): 13.2 -> 10.7; 80 on 5 of 128, 16 of 1000 (2.1):
+// steps or more with one.  128 heads on 8 of 128: 32 sequences of up to 4096 55.3 ->
+// 48.9 us; one of 700, with half as many warps to share it, 7.6 -> 8.7.  64 heads on
+// 4 of 64, 8 of 4096 (2.7 steps): 13.0 -> 10.4; 80 on 5 of 128, 16 of 1000 (2.1):
 // 11.2 -> 11.9.
 int columns_of(int sms, int64_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                int64_t max_len) {
@@ -1207,8 +1213,8 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
   p.f16 = c.f16;
   p.softmax_scale = a.softmax_scale;
 #ifdef MXFP4_DEBUG_BOUNDS
-  debug_range(p.dbg, kDbgLens, a.seq_lens, a.num_seqs * 4);
-  debug_range(p.dbg, kDbgStatus, a.status, a.status ? 4 : 0);
+  debug_range(p.more.dbg, kDbgLens, a.seq_lens, a.num_seqs * 4);
+  debug_range(p.more.dbg, kDbgStatus, a.status, a.status ? 4 : 0);
   debug_range(p.dbg, kDbgTable, a.page_table,
               a.num_seqs > 0 ? ((a.num_seqs - 1) * a.table_stride + a.max_pages) * 4 : 0);
 #endif
@@ -1235,7 +1241,7 @@ cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) 
     debug_range(p.dbg, kDbgCodes0 + i, c.codes[i], rows * (c.head_dim / 2));
     debug_range(p.dbg, kDbgScales0 + i, c.scales[i], rows * (c.head_dim / (c.nvfp4 ? 16 : 32)));
   }
-  debug_range(p.dbg, kDbgLse, a.lse, a.lse ? a.num_seqs * a.num_q_heads * 4 : 0);
+  debug_range(p.more.dbg, kDbgLse, a.lse, a.lse ? a.num_seqs * a.num_q_heads * 4 : 0);
   debug_range(p.dbg, kDbgOut, a.out, a.num_seqs * a.num_q_heads * c.head_dim * 2);
   debug_range(p.dbg, kDbgPart, a.workspace,
               p.workers > 0 ? ((units + p.workers) * p.columns * (c.head_dim + 2) + 4 * units + p.workers) * 4 : 0);

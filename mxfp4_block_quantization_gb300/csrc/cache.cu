@@ -26,6 +26,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "cache_device.cuh"
 #include "mxfp4_device.cuh"
 #include "mxfp4_internal.h"
 #include "nvfp4_device.cuh"

@@ -31,10 +31,10 @@
 // to the 32-element partial sums; the E4M3 scale times an E2M1 value has at
 // most 6 bits and fits a half, so NVFP4 weights are scaled before the product.
 //
-// Measured (device time, weights not in L2): 64000 x 7168 MXFP4 by 1 BF16 token
-// 45 us, 5.4 TB/s of 244 MB; the copies alone take most of that, the products
-// alone 35 us.  By 16 tokens 70 us (FP16 59): 60 % of the cycles issue, with x in
-// panels.  7168 x 7168 by 1 token 11.3 us, the 128 experts'
+// Measured (device time, weights not in L2, call after call): 64000 x 7168 MXFP4 by
+// 1 BF16 token 45 us, 5.4 TB/s of 244 MB (49 alone, from flushed caches); the copies
+// alone take most of that, the products alone 35 us.  By 16 tokens 70 us (FP16 59):
+// 60 % of the cycles issue, with x in panels.  7168 x 7168 by 1 token 11.3 us, the 128 experts'
 // 1536 x 2048 NVFP4 by 64 tokens of 8 experts each 46.9 us (4.6 TB/s), 2048 x 768
 // by 1 token 5.2 us.
 #include <atomic>
@@ -412,7 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) matvec_kernel(const MatvecParams 
           }
           if (lane < kScaleBytes / 16) {
             // A piece is four rows' words of four columns.  The layout pads the columns to
-            // a multiple of four with bytes that may be anything: zeros take their place.
+            // a multiple of four with bytes that may be anything: zeros take their place
+            // (32 experts' 5760 x 2880 by 64 tokens 82.4 -> 83.6 us).
             const int kt = in.chunk * kChunkKt + (lane >> 2);
             const bool ok = kt < p.nKT && MXFP4_IN_BOUNDS(p, kDbgScales, scale, 16);
             const int cols = p.K / (kNv ? 16 : 32) - 4 * kt;

@@ -304,8 +304,8 @@ inline bool vec32_ok(const void* x, int64_t ldx_bytes) {
 }
 
 struct DebugRanges {
-  uintptr_t lo[11];
-  uintptr_t hi[11];
+  uintptr_t lo[8];
+  uintptr_t hi[8];
 };
 
 #ifdef MXFP4_DEBUG_BOUNDS

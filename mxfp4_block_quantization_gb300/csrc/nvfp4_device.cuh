@@ -56,7 +56,4 @@ __device__ __forceinline__ uint32_t nv_scale_byte(const uint4 (&v)[2], float g) 
   return cvt_e4m3_satfinite(g * nv_block_q<kF16>(v));
 }
 
-// A cache's global scale; a call that touches no cache may have none.
-__device__ __forceinline__ float global_scale_or_one(const float* g) { return g != nullptr ? __ldg(g) : 1.0f; }
-
 }  // namespace mxfp4
