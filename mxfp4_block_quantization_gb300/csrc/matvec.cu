@@ -32,7 +32,7 @@
 // most 6 bits and fits a half, so NVFP4 weights are scaled before the product.
 //
 // Measured (device time, weights not in L2, call after call): 64000 x 7168 MXFP4 by
-// 1 BF16 token 45 us, 5.4 TB/s of 244 MB (49 alone, from flushed caches); the copies
+// 1 BF16 token 45 us, 5.4 TB/s of 244 MB (48 alone, from flushed caches); the copies
 // alone take most of that, the products alone 35 us.  By 16 tokens 70 us (FP16 59):
 // 60 % of the cycles issue, with x in panels.  7168 x 7168 by 1 token 11.3 us, the 128 experts'
 // 1536 x 2048 NVFP4 by 64 tokens of 8 experts each 46.9 us (4.6 TB/s), 2048 x 768
