@@ -194,3 +194,28 @@ def test_a_head_of_any_size_leaves_the_others(mx, power, group, room):  # noqa: 
     full, bound, fl, bl = R.attention(q[0], k[0], v[0], 0.01, BF16)
     R.close(o[0, ::2], full[::2], bound[::2])
     R.close(lse[0, ::2], fl[::2], bl[::2])
+
+
+@pytest.mark.parametrize("room", [False, True])
+@pytest.mark.parametrize("gap", [6, 14, 22])
+def test_values_of_a_wide_range(mx, gap, room):  # noqa: F811
+    """Positions whose weight is 2^gap times the others' hold values 2^-gap times
+    theirs: both are half of the output.  Bound: two roundings to 11 bits, and
+    products no finer than 2^-37 of the largest weight and scale of a block."""
+    S, D, n = 16, 64, 320
+    c = make_cache(mx, n // S, S, 1, D, False)
+    k, v = torch.zeros((n, 1, D), dtype=BF16, device="cuda"), rand((n, 1, D), 8)
+    k[::2, 0, 0] = 4.0
+    v[::2] *= 2.0 ** -gap
+    mx.cache_write(k, v, torch.arange(n, dtype=torch.int32, device="cuda"), c)
+    table = torch.arange(n // S, dtype=torch.int32, device="cuda").view(1, -1)
+    q = torch.zeros((1, 2, D), dtype=BF16, device="cuda")
+    q[..., 0] = 1.0
+    scale = gap * math.log(2.0) / 4.0
+    o, _, _ = mx.cache_attention(q, c, with_room(table, S) if room else table,
+                                 torch.tensor([n], dtype=torch.int32, device="cuda"), scale)
+    kd, vd = contents(c, table[0].long(), n)
+    p = torch.softmax(scale * (q[0].double() @ kd[0].T), -1)
+    want = p @ vd[0]
+    off = (2.0 ** -10 + 2.0 ** -18) * (p @ vd[0].abs()) + n * 2.0 ** -37 * p.amax() * vd.abs().amax()
+    R.close(o[0], want, off + R.unit(BF16) * (want.abs() + off) + R.smallest(BF16))
