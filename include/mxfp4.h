@@ -824,6 +824,169 @@ int mxfp4_cache_attention_nvfp4_f16(const void* q, int64_t num_seqs, int32_t num
                                     void* workspace, size_t workspace_bytes, void* out,
                                     float* lse, int32_t* status, void* stream);
 
+/* ------------------------------------------ a layer's products, many tokens
+ * What a mixture-of-experts layer does around the calls above when there are
+ * many tokens: the router's choice (the ids that mxfp4_moe_route sorts), the
+ * products of quantized activations with quantized weights, dense and per
+ * expert, and the experts' rows back to their tokens.  No counterpart exists in
+ * the method's sources; formats and layouts are those of the calls above.
+ *
+ * mxfp4_moe_topk — the top_k experts of every token and their weights.
+ *   score[e] = softmax of the token's logits, or sigmoid(logit[e]);
+ *   pick[e]  = score[e] + bias[e];  without a bias and without group sums the
+ *              logits themselves (the same order);
+ *   groups   > 1: E / groups consecutive experts make a group, its value the
+ *              largest pick (group_sum2 == 0) or the sum of its two largest
+ *              (1; of one, where it has only one); the top_groups largest
+ *              groups stay, the other experts are out;
+ *   ids      the top_k largest picks, in falling order; equal ones in order of
+ *              their index, among the groups too.  Picks are compared as if
+ *              computed in 64 bits: where float32 cannot tell two apart, they
+ *              are computed in 64.
+ *   weights  score[id], with renormalize == 1 divided by the sum over the
+ *              chosen, times scale.
+ * A logit that is not finite takes its expert out (of the softmax's sum too);
+ * where fewer than top_k experts are left, the last ids are -1 (what
+ * mxfp4_moe_route takes as "not dispatched") and their weights 0.
+ *
+ * logits       DEVICE BF16 (_f16: binary16, _f32: float32) [num_tokens, E], row
+ *              stride ld >= E elements, aligned to the element.
+ * E            1 <= E <= MXFP4_ROUTE_MAX_EXPERTS.
+ * bias         DEVICE float32 [E] or NULL; an expert whose bias is not finite
+ *              is out as well.
+ * score        MXFP4_SCORE_SOFTMAX or MXFP4_SCORE_SIGMOID.
+ * groups       1 <= groups <= 32, E % groups == 0; 1 <= top_groups <= groups.
+ * top_k        1 <= top_k <= min(E, MXFP4_TOPK_MAX).
+ * scale        finite.
+ * ids          DEVICE int32 [num_tokens, top_k], out.
+ * weights      DEVICE float32 [num_tokens, top_k], out. */
+#define MXFP4_SCORE_SOFTMAX 0
+#define MXFP4_SCORE_SIGMOID 1
+#define MXFP4_TOPK_MAX 32
+int mxfp4_moe_topk(const void* logits, int64_t num_tokens, int32_t E, int64_t ld,
+                   const float* bias, int32_t score, int32_t groups, int32_t top_groups,
+                   int32_t group_sum2, int32_t top_k, int32_t renormalize, float scale,
+                   int32_t* ids, float* weights, void* stream);
+int mxfp4_moe_topk_f16(const void* logits, int64_t num_tokens, int32_t E, int64_t ld,
+                       const float* bias, int32_t score, int32_t groups, int32_t top_groups,
+                       int32_t group_sum2, int32_t top_k, int32_t renormalize, float scale,
+                       int32_t* ids, float* weights, void* stream);
+int mxfp4_moe_topk_f32(const void* logits, int64_t num_tokens, int32_t E, int64_t ld,
+                       const float* bias, int32_t score, int32_t groups, int32_t top_groups,
+                       int32_t group_sum2, int32_t top_k, int32_t renormalize, float scale,
+                       int32_t* ids, float* weights, void* stream);
+
+/* mxfp4_gemm — products of quantized activations with quantized weights:
+ *   z[t, n] = sum_k X[t, k] * W[n, k] + bias[n]
+ *   y[t, n] = act(z[t, n]) + residual[t, n]
+ * or, with a gate, of the two halves of W's rows (N even, y has N / 2 columns):
+ *   y[t, n] = act(z[t, n]) * z[t, N/2 + n] + residual[t, n]   MXFP4_GATE_FIRST
+ *                                                 ([w1; w3], the gate first)
+ *   y[t, n] = act(z[t, N/2 + n]) * z[t, n] + residual[t, n]   MXFP4_GATE_SECOND
+ *                                  ([w3; w1], as mxfp4_swap_w13 leaves them)
+ * X and W are MXFP4 (e2m1 * 2^(s-127); s = 255: NaN), or with _nvfp4 NVFP4
+ * (e2m1 * e4m3(s) / global scale; scale bytes with the sign bit clear, as the
+ * quantize calls write them), both as those calls leave them.  Sums are
+ * float32, the result is rounded once, to BF16 (_f16: to binary16).
+ *
+ * x_codes      [num_tokens, K/2] packed codes, 16-byte aligned; K % 32 == 0 in
+ *              both formats.
+ * x_scales     mxfp4_scale_bytes(num_tokens, K) (NVFP4:
+ *              mxfp4_nvfp4_scale_bytes) bytes, tiled, 16-byte aligned; the bytes
+ *              that pad rows and columns may hold anything.
+ * x_global_scale, global_scale  (NVFP4) DEVICE float32.
+ * codes, scales  the same of W: [N, K/2] and its tiled scales.
+ * bias         BF16 (_f16: binary16) [N] or NULL.
+ * activation   MXFP4_ACT_NONE, _SILU (z / (1 + e^-z)), _GELU (by erf) or
+ *              _GELU_TANH (0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))).
+ * residual     BF16 (_f16: binary16) [num_tokens, columns of y], row stride ldr
+ *              elements, or NULL.  It may be y itself (with ldr == ldy).
+ * y            BF16 (_f16: binary16), row stride ldy elements.
+ * K == 0 leaves the epilogue's terms.
+ *
+ * mxfp4_moe_gemm — the same per expert of a routed batch: row r of segment e
+ * (expert_offsets[e] <= r < expert_offsets[e+1]) with expert e's weights, bias
+ * and global scales.
+ * x_codes      [total_rows, K/2], rows sorted by expert; x_scales as the grouped
+ *              quantize calls write them (each segment padded to 128 rows on its
+ *              own, mxfp4_grouped_scale_bytes_bound(total_rows, E, K) bytes).
+ * expert_offsets  DEVICE int32 [E+1], 0 = o[0] <= ... <= o[E] <= total_rows
+ *              (checked on the device).  Rows of y from o[E] on are not written.
+ * x_global_scales, global_scales  (NVFP4) DEVICE float32 [E].
+ * codes, scales, bias  E consecutive ones; E <= MXFP4_ROUTE_MAX_EXPERTS.
+ * status       DEVICE int32 or NULL, out: MXFP4_OK, or MXFP4_EOFFSETS (y is then
+ *              not written). */
+#define MXFP4_ACT_NONE 0
+#define MXFP4_ACT_SILU 1
+#define MXFP4_ACT_GELU 2
+#define MXFP4_ACT_GELU_TANH 3
+#define MXFP4_GATE_NONE 0
+#define MXFP4_GATE_FIRST 1
+#define MXFP4_GATE_SECOND 2
+int mxfp4_gemm(const uint8_t* x_codes, const uint8_t* x_scales, int64_t num_tokens, int64_t K,
+               const uint8_t* codes, const uint8_t* scales, int64_t N, const void* bias,
+               int32_t activation, int32_t gate, const void* residual, int64_t ldr, void* y,
+               int64_t ldy, void* stream);
+int mxfp4_gemm_f16(const uint8_t* x_codes, const uint8_t* x_scales, int64_t num_tokens, int64_t K,
+                   const uint8_t* codes, const uint8_t* scales, int64_t N, const void* bias,
+                   int32_t activation, int32_t gate, const void* residual, int64_t ldr, void* y,
+                   int64_t ldy, void* stream);
+int mxfp4_gemm_nvfp4(const uint8_t* x_codes, const uint8_t* x_scales, const float* x_global_scale,
+                     int64_t num_tokens, int64_t K, const uint8_t* codes, const uint8_t* scales,
+                     const float* global_scale, int64_t N, const void* bias, int32_t activation,
+                     int32_t gate, const void* residual, int64_t ldr, void* y, int64_t ldy,
+                     void* stream);
+int mxfp4_gemm_nvfp4_f16(const uint8_t* x_codes, const uint8_t* x_scales,
+                         const float* x_global_scale, int64_t num_tokens, int64_t K,
+                         const uint8_t* codes, const uint8_t* scales, const float* global_scale,
+                         int64_t N, const void* bias, int32_t activation, int32_t gate,
+                         const void* residual, int64_t ldr, void* y, int64_t ldy, void* stream);
+int mxfp4_moe_gemm(const uint8_t* x_codes, const uint8_t* x_scales, int64_t total_rows, int64_t K,
+                   const int32_t* expert_offsets, int32_t E, const uint8_t* codes,
+                   const uint8_t* scales, int64_t N, const void* bias, int32_t activation,
+                   int32_t gate, void* y, int64_t ldy, int32_t* status, void* stream);
+int mxfp4_moe_gemm_f16(const uint8_t* x_codes, const uint8_t* x_scales, int64_t total_rows,
+                       int64_t K, const int32_t* expert_offsets, int32_t E, const uint8_t* codes,
+                       const uint8_t* scales, int64_t N, const void* bias, int32_t activation,
+                       int32_t gate, void* y, int64_t ldy, int32_t* status, void* stream);
+int mxfp4_moe_gemm_nvfp4(const uint8_t* x_codes, const uint8_t* x_scales,
+                         const float* x_global_scales, int64_t total_rows, int64_t K,
+                         const int32_t* expert_offsets, int32_t E, const uint8_t* codes,
+                         const uint8_t* scales, const float* global_scales, int64_t N,
+                         const void* bias, int32_t activation, int32_t gate, void* y, int64_t ldy,
+                         int32_t* status, void* stream);
+int mxfp4_moe_gemm_nvfp4_f16(const uint8_t* x_codes, const uint8_t* x_scales,
+                             const float* x_global_scales, int64_t total_rows, int64_t K,
+                             const int32_t* expert_offsets, int32_t E, const uint8_t* codes,
+                             const uint8_t* scales, const float* global_scales, int64_t N,
+                             const void* bias, int32_t activation, int32_t gate, void* y,
+                             int64_t ldy, int32_t* status, void* stream);
+
+/* mxfp4_moe_combine — the experts' rows back to their tokens:
+ *   y[t] = residual[t] + sum_j weights[t, j] * rows[dest_rows[t, j]]
+ * in order of j, in float32, rounded once.
+ *
+ * rows         BF16 (_f16: binary16), or float32 with rows_f32 == 1,
+ *              [total_rows, N], row stride ldr >= N elements, aligned to the
+ *              element.
+ * dest_rows    DEVICE int32 [num_tokens, top_k], as mxfp4_moe_route writes it;
+ *              -1: the route adds nothing (its weight and row are not read).
+ * weights      DEVICE float32 [num_tokens, top_k], as mxfp4_moe_topk writes them.
+ * top_k        >= 1; num_tokens * top_k <= INT32_MAX / 2.
+ * residual     BF16 (_f16: binary16) [num_tokens, N], row stride ld_res
+ *              elements, or NULL.  It may be y itself (with ld_res == ldy).
+ * y            BF16 (_f16: binary16) [num_tokens, N], row stride ldy elements.
+ * status       DEVICE int32 or NULL, out: MXFP4_OK, or MXFP4_EINDEX when an
+ *              entry is outside [-1, total_rows) (it adds nothing). */
+int mxfp4_moe_combine(const void* rows, int32_t rows_f32, int64_t total_rows, int64_t N,
+                      int64_t ldr, const int32_t* dest_rows, const float* weights,
+                      int64_t num_tokens, int32_t top_k, const void* residual, int64_t ld_res,
+                      void* y, int64_t ldy, int32_t* status, void* stream);
+int mxfp4_moe_combine_f16(const void* rows, int32_t rows_f32, int64_t total_rows, int64_t N,
+                          int64_t ldr, const int32_t* dest_rows, const float* weights,
+                          int64_t num_tokens, int32_t top_k, const void* residual, int64_t ld_res,
+                          void* y, int64_t ldy, int32_t* status, void* stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* mxfp4_status_string(int status);
 

@@ -8,7 +8,8 @@ CUDA kernels.  ``quantize``, ``quantize_grouped``, ``dequantize`` and
 ``swap_w13`` are conveniences that allocate the outputs with torch and call
 the matching entry point.  PyTorch supplies device memory and streams only.
 A decode step's calls (``matvec``, ``moe_matvec``, ``cache_write``,
-``cache_read``, ``cache_attention``) pick the BF16 or FP16 entry point by
+``cache_read``, ``cache_attention``) and those of a layer over many tokens
+(``moe_topk``, ``gemm``, ``moe_gemm``, ``moe_combine``) pick the entry point by
 their tensors' type.
 
 A call on ``stream`` does not wait for the current one: let it wait before its
@@ -59,7 +60,9 @@ __all__ = [
     "mxfp4_moe_matvec_nvfp4", "matvec", "matvec_nvfp4", "moe_matvec", "moe_matvec_nvfp4",
     "KVCache", "cache_alloc", "mxfp4_cache_write", "mxfp4_cache_read", "cache_write",
     "cache_read", "mxfp4_cache_attention_workspace_bytes", "mxfp4_cache_attention",
-    "cache_attention",
+    "cache_attention", "MXFP4_TOPK_MAX", "mxfp4_moe_topk", "moe_topk", "mxfp4_gemm",
+    "mxfp4_gemm_nvfp4", "gemm", "gemm_nvfp4", "mxfp4_moe_gemm", "mxfp4_moe_gemm_nvfp4",
+    "moe_gemm", "moe_gemm_nvfp4", "mxfp4_moe_combine", "moe_combine",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmxfp4_gb300.so")
@@ -71,6 +74,7 @@ MXFP4_SCATTER_MAX_TOP_K = 32
 MXFP4_ROUTE_MAX_EXPERTS = 8192
 MXFP4_NOALLOC_SCRATCH_BYTES = 4 << 20
 MXFP4_ATTENTION_MAX_HEAD_DIM = 256
+MXFP4_TOPK_MAX = 32
 MXFP4_OK = 0
 MXFP4_EINVAL = -1
 MXFP4_EALIGN = -2
@@ -188,6 +192,30 @@ def _load(path=LIB_PATH):
                 fn.restype = ctypes.c_int
                 fn.argtypes = args
                 decode[name, nv, f16] = fn, "mxfp4_" + name + tail
+    layer = L.layer = {}  # (call, type) or (call, NVFP4, FP16) -> entry point and its name
+    for tail, kind in (("", torch.bfloat16), ("_f16", torch.float16), ("_f32", torch.float32)):
+        fn = getattr(L, "mxfp4_moe_topk" + tail)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [vp, i64, i32, i64, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]
+        layer["moe_topk", kind] = fn, "mxfp4_moe_topk" + tail
+    for nv in (False, True):
+        for f16 in (False, True):
+            tail = ("_nvfp4" if nv else "") + ("_f16" if f16 else "")
+            g = [vp] if nv else []
+            for name, args in (
+                    ("gemm", [vp, vp] + g + [i64, i64, vp, vp] + g +
+                     [i64, vp, i32, i32, vp, i64, vp, i64, vp]),
+                    ("moe_gemm", [vp, vp] + g + [i64, i64, vp, i32, vp, vp] + g +
+                     [i64, vp, i32, i32, vp, i64, vp, vp])):
+                fn = getattr(L, "mxfp4_" + name + tail)
+                fn.restype = ctypes.c_int
+                fn.argtypes = args
+                layer[name, nv, f16] = fn, "mxfp4_" + name + tail
+    for f16, tail in ((False, ""), (True, "_f16")):
+        fn = getattr(L, "mxfp4_moe_combine" + tail)
+        fn.restype = ctypes.c_int
+        fn.argtypes = [vp, i32, i64, i64, i64, vp, vp, i64, i32, vp, i64, vp, i64, vp, vp]
+        layer["moe_combine", f16] = fn, "mxfp4_moe_combine" + tail
     L.mxfp4_cache_attention_workspace_bytes.restype = size
     L.mxfp4_cache_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i64]
     L.mxfp4_status_string.restype = ctypes.c_char_p
@@ -819,8 +847,12 @@ _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _decode_call(key, device, stream, args):
+    _launch(_lib.decode[key], device, stream, args)
+
+
+def _launch(entry, device, stream, args):
     """Launch an entry point on ``device`` (an index): args, then the stream."""
-    fn, name = _lib.decode[key]
+    fn, name = entry
     if stream is not None:
         stream = stream.cuda_stream
     elif _raw_current_stream is not None:
@@ -1094,6 +1126,173 @@ def mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, 
                   _address("out", out, device, q.dtype, 2 * B * Hq * D),
                   _address("lse", lse, device, torch.float32, 4 * B * Hq),
                   _address("status", status, device, torch.int32, 4)))
+
+
+# ------------------------------------------ a layer's products, many tokens
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+_GATES = {None: 0, "first": 1, "second": 2}
+_GROUP_SCORES = {"max": 0, "sum2": 1}
+
+
+def _choice(name, value, choices):
+    try:
+        return choices[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {tuple(choices)}, got {value!r}") from None
+
+
+def mxfp4_moe_topk(logits, top_k: int, ids, weights, score="softmax", bias=None, groups=1,
+                   top_groups=1, group_score="max", renormalize=True, scale=1.0,
+                   stream=None) -> None:
+    """The router's choice from ``logits`` [T, E] (BF16, FP16 or float32; row
+    stride may exceed E): ``ids`` int32 [T, top_k] and ``weights`` float32
+    [T, top_k].  ``score``: "softmax" or "sigmoid"; ``bias`` (float32 [E]) is
+    added for the choice only; ``groups`` of consecutive experts, of which the
+    ``top_groups`` best by their best expert (``group_score`` "max") or the sum
+    of their two best ("sum2") stay.  Weights are the chosen scores, divided by
+    their sum with ``renormalize``, times ``scale``.  Equal ones go to the lowest
+    index; logits that are not finite are out; -1 where no expert is left."""
+    device = _device_index("logits", logits)
+    la, T, E, ld = _matrix("logits", logits, device, (torch.bfloat16, torch.float16, torch.float32))
+    n = 4 * T * top_k
+    _launch(_lib.layer["moe_topk", logits.dtype], device, stream,
+            (la, T, E, ld, _address("bias", bias, device, torch.float32, 4 * E),
+             _choice("score", score, _SCORES), groups, top_groups,
+             _choice("group_score", group_score, _GROUP_SCORES), top_k, bool(renormalize), scale,
+             _address("ids", ids, device, torch.int32, n),
+             _address("weights", weights, device, torch.float32, n)))
+
+
+def _layer_product(x_codes, x_scales, x_globals, codes, scales, globals_, bias, activation, gate,
+                   y, rows_of_scales, E, nvfp4):
+    """The checked arguments that the dense and the experts' products share:
+    (FP16, device, x's, K, the weights', the epilogue's, y's address, rows,
+    columns and stride)."""
+    device = _device_index("x_codes", x_codes)
+    f16 = _half_type("y", y)
+    if x_codes.dim() != 2:
+        raise ValueError("x_codes must be [rows, K/2]")
+    rows, half = x_codes.shape
+    K, N = 2 * half, codes.shape[-2]
+    if codes.shape[-1] != half:
+        raise ValueError(f"codes hold {codes.shape[-1] * 2} elements per row, x_codes {K}")
+    ya = _matrix("y", y, device, (y.dtype,))
+    gate = _choice("gate", gate, _GATES)
+    cols = N // 2 if gate else N
+    if ya[1] != rows or ya[2] != cols:
+        raise ValueError(f"y must be [{rows}, {cols}], got [{ya[1]}, {ya[2]}]")
+    per = mxfp4_nvfp4_scale_bytes(N, K) if nvfp4 else mxfp4_scale_bytes(N, K)
+    u8 = torch.uint8
+    x = [_address("x_codes", x_codes, device, u8, 0),
+         _address("x_scales", x_scales, device, u8, rows_of_scales(rows, K))]
+    w = [_address("codes", codes, device, u8, E * N * half),
+         _address("scales", scales, device, u8, E * per)]
+    if nvfp4:
+        for name, g, to in (("x_global_scale", x_globals, x), ("global_scale", globals_, w)):
+            if g is None:
+                raise ValueError(f"NVFP4 operands have a {name}")
+            to.append(_address(name, g, device, torch.float32, 4 * E))
+    epilogue = (_address("bias", bias, device, y.dtype, 2 * E * N),
+                _choice("activation", activation, _ACTIVATIONS), gate)
+    return f16, device, x, K, w, N, epilogue, ya
+
+
+def _gemm(x_codes, x_scales, x_global, codes, scales, global_scale, y, bias, activation, gate,
+          residual, stream, nvfp4):
+    if codes.dim() != 2:
+        raise ValueError("codes must be [N, K/2]")
+    f16, device, x, K, w, N, epilogue, ya = _layer_product(
+        x_codes, x_scales, x_global, codes, scales, global_scale, bias, activation, gate, y,
+        mxfp4_nvfp4_scale_bytes if nvfp4 else mxfp4_scale_bytes, 1, nvfp4)
+    ra = (None, 0, 0, 0)
+    if residual is not None:
+        ra = _matrix("residual", residual, device, (y.dtype,))
+        if ra[1] != ya[1] or ra[2] != ya[2]:
+            raise ValueError(f"residual must be [{ya[1]}, {ya[2]}], got [{ra[1]}, {ra[2]}]")
+    _launch(_lib.layer["gemm", nvfp4, f16], device, stream,
+            (*x, ya[1], K, *w, N, *epilogue, ra[0], ra[3], ya[0], ya[3]))
+
+
+def mxfp4_gemm(x_codes, x_scales, codes, scales, y, bias=None, activation=None, gate=None,
+               residual=None, stream=None) -> None:
+    """``y`` [T, N] = act(X W^T + ``bias``) + ``residual`` with MXFP4 X
+    (``x_codes`` [T, K/2], tiled ``x_scales``) and W (``codes`` [N, K/2],
+    ``scales``), as the quantize calls write them.  ``activation``: None,
+    "silu", "gelu" or "gelu_tanh"; ``gate`` "first" or "second": W's rows are
+    two halves, that one is activated and multiplies the other, y is
+    [T, N/2].  ``y``, ``bias`` and ``residual`` are all BF16 or all FP16;
+    ``residual`` may be ``y``."""
+    _gemm(x_codes, x_scales, None, codes, scales, None, y, bias, activation, gate, residual,
+          stream, False)
+
+
+def mxfp4_gemm_nvfp4(x_codes, x_scales, x_global_scale, codes, scales, global_scale, y, bias=None,
+                     activation=None, gate=None, residual=None, stream=None) -> None:
+    """mxfp4_gemm with NVFP4 operands and their float32 device global scales."""
+    _gemm(x_codes, x_scales, x_global_scale, codes, scales, global_scale, y, bias, activation,
+          gate, residual, stream, True)
+
+
+def _moe_gemm(x_codes, x_scales, x_globals, expert_offsets, codes, scales, globals_, y, bias,
+              activation, gate, status, stream, nvfp4):
+    if codes.dim() != 3:
+        raise ValueError("codes must be [E, N, K/2]")
+    E = codes.shape[0]
+    bound = mxfp4_nvfp4_grouped_scale_bytes_bound if nvfp4 else mxfp4_grouped_scale_bytes_bound
+    f16, device, x, K, w, N, epilogue, ya = _layer_product(
+        x_codes, x_scales, x_globals, codes, scales, globals_, bias, activation, gate, y,
+        lambda rows, k: bound(rows, E, k), E, nvfp4)
+    offsets = _address("expert_offsets", expert_offsets, device, torch.int32, 4 * (E + 1))
+    _launch(_lib.layer["moe_gemm", nvfp4, f16], device, stream,
+            (*x, ya[1], K, offsets, E, *w, N, *epilogue, ya[0], ya[3],
+             _address("status", status, device, torch.int32, 4)))
+
+
+def mxfp4_moe_gemm(x_codes, x_scales, expert_offsets, codes, scales, y, bias=None, activation=None,
+                   gate=None, status=None, stream=None) -> None:
+    """The experts' products of a routed batch: row r of segment e
+    (``expert_offsets`` int32 [E+1]) of the MXFP4 ``x_codes`` [rows, K/2] and
+    ``x_scales`` (as the grouped quantize calls write them) with expert e's
+    weights ``codes`` [E, N, K/2] and ``bias`` [E, N], as mxfp4_gemm.  Rows of
+    ``y`` from expert_offsets[E] on are not written."""
+    _moe_gemm(x_codes, x_scales, None, expert_offsets, codes, scales, None, y, bias, activation,
+              gate, status, stream, False)
+
+
+def mxfp4_moe_gemm_nvfp4(x_codes, x_scales, x_global_scales, expert_offsets, codes, scales,
+                         global_scales, y, bias=None, activation=None, gate=None, status=None,
+                         stream=None) -> None:
+    """mxfp4_moe_gemm with NVFP4 operands (float32 global scales [E] each)."""
+    _moe_gemm(x_codes, x_scales, x_global_scales, expert_offsets, codes, scales, global_scales, y,
+              bias, activation, gate, status, stream, True)
+
+
+def mxfp4_moe_combine(rows, dest_rows, weights, y, residual=None, status=None,
+                      stream=None) -> None:
+    """``y`` [T, N] (BF16 or FP16) = ``residual`` + the sum over j of
+    ``weights[t, j] * rows[dest_rows[t, j]]``: ``rows`` [R, N] of y's type or
+    float32, ``dest_rows`` int32 [T, top_k] (-1: nothing), ``weights`` float32
+    [T, top_k].  ``residual`` may be ``y``."""
+    device = _device_index("rows", rows)
+    f16 = _half_type("y", y)
+    a = _matrix("rows", rows, device, (y.dtype, torch.float32))
+    ya = _matrix("y", y, device, (y.dtype,))
+    if dest_rows.dim() != 2:
+        raise ValueError("dest_rows must be [T, top_k]")
+    T, top_k = dest_rows.shape
+    if ya[1] != T or ya[2] != a[2]:
+        raise ValueError(f"y must be [{T}, {a[2]}], got [{ya[1]}, {ya[2]}]")
+    ra = (None, 0, 0, 0)
+    if residual is not None:
+        ra = _matrix("residual", residual, device, (y.dtype,))
+        if ra[1] != T or ra[2] != ya[2]:
+            raise ValueError(f"residual must be [{T}, {ya[2]}], got [{ra[1]}, {ra[2]}]")
+    _launch(_lib.layer["moe_combine", f16], device, stream,
+            (a[0], rows.dtype is torch.float32, a[1], a[2], a[3],
+             _address("dest_rows", dest_rows, device, torch.int32, 0),
+             _address("weights", weights, device, torch.float32, 4 * T * top_k), T, top_k, ra[0],
+             ra[3], ya[0], ya[3], _address("status", status, device, torch.int32, 4)))
 
 
 # --------------------------------------------------- allocating wrappers
@@ -1380,3 +1579,85 @@ def cache_attention(q, cache, page_table, seq_lens, softmax_scale: float, window
     mxfp4_cache_attention(q, cache, page_table, seq_lens, softmax_scale, out, window, ws, lse,
                           status, stream)
     return out, lse, status
+
+
+def moe_topk(logits, top_k: int, score="softmax", bias=None, groups=1, top_groups=1,
+             group_score="max", renormalize=True, scale=1.0, ids=None, weights=None, stream=None):
+    """Returns (ids int32 [T, top_k], weights float32 [T, top_k]) of the router's
+    ``logits`` [T, E]; see mxfp4_moe_topk."""
+    shape = (logits.shape[0], top_k)
+    if ids is None:
+        ids = _empty(shape, torch.int32, logits.device, stream)
+    if weights is None:
+        weights = _empty(shape, torch.float32, logits.device, stream)
+    mxfp4_moe_topk(logits, top_k, ids, weights, score, bias, groups, top_groups, group_score,
+                   renormalize, scale, stream)
+    return ids, weights
+
+
+def _layer_out(x_codes, codes, gate, out, out_dtype, stream):
+    if out is not None:
+        return out
+    N = codes.shape[-2]
+    return _empty((x_codes.shape[0], N if gate is None else N // 2), out_dtype, x_codes.device,
+                  stream)
+
+
+def gemm(x_codes, x_scales, codes, scales, bias=None, activation=None, gate=None, residual=None,
+         out=None, out_dtype=torch.bfloat16, stream=None):
+    """act(X W^T + bias) + residual of MXFP4 X [T, K] and W [N, K]: [T, N] (with
+    a gate [T, N/2]) of ``out_dtype`` or into ``out``; see mxfp4_gemm."""
+    out = _layer_out(x_codes, codes, gate, out, out_dtype, stream)
+    _gemm(x_codes, x_scales, None, codes, scales, None, out, bias, activation, gate, residual,
+          stream, False)
+    return out
+
+
+def gemm_nvfp4(x_codes, x_scales, x_global_scale, codes, scales, global_scale, bias=None,
+               activation=None, gate=None, residual=None, out=None, out_dtype=torch.bfloat16,
+               stream=None):
+    """gemm with NVFP4 operands and their float32 global scales."""
+    out = _layer_out(x_codes, codes, gate, out, out_dtype, stream)
+    _gemm(x_codes, x_scales, x_global_scale, codes, scales, global_scale, out, bias, activation,
+          gate, residual, stream, True)
+    return out
+
+
+def moe_gemm(x_codes, x_scales, expert_offsets, codes, scales, bias=None, activation=None,
+             gate=None, out=None, out_dtype=torch.bfloat16, status=None, stream=None):
+    """Returns (y, status) of the experts' products over a routed batch that the
+    grouped quantize calls wrote; see mxfp4_moe_gemm."""
+    out = _layer_out(x_codes, codes, gate, out, out_dtype, stream)
+    if status is None:
+        status = _empty(1, torch.int32, x_codes.device, stream)
+    _moe_gemm(x_codes, x_scales, None, expert_offsets, codes, scales, None, out, bias, activation,
+              gate, status, stream, False)
+    return out, status
+
+
+def moe_gemm_nvfp4(x_codes, x_scales, x_global_scales, expert_offsets, codes, scales,
+                   global_scales, bias=None, activation=None, gate=None, out=None,
+                   out_dtype=torch.bfloat16, status=None, stream=None):
+    """moe_gemm with NVFP4 operands and float32 global scales [E] of each."""
+    out = _layer_out(x_codes, codes, gate, out, out_dtype, stream)
+    if status is None:
+        status = _empty(1, torch.int32, x_codes.device, stream)
+    _moe_gemm(x_codes, x_scales, x_global_scales, expert_offsets, codes, scales, global_scales,
+              out, bias, activation, gate, status, stream, True)
+    return out, status
+
+
+def moe_combine(rows, dest_rows, weights, residual=None, out=None, out_dtype=None, status=None,
+                stream=None):
+    """Returns (y, status): every token's weighted sum of its experts' ``rows``,
+    added to ``residual``; y of ``out_dtype`` (of residual's or rows' type, where
+    that is not float32, else BF16) or into ``out``; see mxfp4_moe_combine."""
+    if out is None:
+        if out_dtype is None:
+            out_dtype = rows.dtype if residual is None else residual.dtype
+            out_dtype = torch.bfloat16 if out_dtype is torch.float32 else out_dtype
+        out = _empty((dest_rows.shape[0], rows.shape[1]), out_dtype, rows.device, stream)
+    if status is None:
+        status = _empty(1, torch.int32, rows.device, stream)
+    mxfp4_moe_combine(rows, dest_rows, weights, out, residual, status, stream)
+    return out, status

@@ -877,7 +877,8 @@ int64_t mxfp4_debug_bounds_violations(void) {
          mxfp4::debug_violations_dequantize() + mxfp4::debug_violations_nvfp4() +
          mxfp4::debug_violations_swap() + mxfp4::debug_violations_route() +
          mxfp4::debug_violations_matvec() + mxfp4::debug_violations_cache() +
-         mxfp4::debug_violations_attention();
+         mxfp4::debug_violations_attention() + mxfp4::debug_violations_topk() +
+         mxfp4::debug_violations_gemm() + mxfp4::debug_violations_combine();
 }
 #endif
 

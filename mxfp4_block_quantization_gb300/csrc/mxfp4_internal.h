@@ -205,6 +205,74 @@ int64_t attention_workspace_floats(int64_t num_seqs, int32_t num_q_heads, int32_
                                    int32_t head_dim, int64_t max_len);
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream);
 
+// The router's choice: the top_k picks of every token.
+enum class LogitType : int32_t { kBf16, kF16, kF32 };
+struct TopkArgs {
+  const void* logits;
+  LogitType type;
+  int64_t num_tokens;
+  int32_t E;
+  int64_t ld;
+  const float* bias;  // or NULL
+  bool sigmoid;
+  int32_t groups;
+  int32_t top_groups;
+  bool group_sum2;
+  int32_t top_k;
+  bool renormalize;
+  float scale;
+  int32_t* ids;
+  float* weights;
+};
+cudaError_t launch_moe_topk(const TopkArgs& a, cudaStream_t stream);
+
+// Products of quantized activations with quantized weights: dense (offsets ==
+// NULL) or per expert segment, with the epilogue's terms (see include/mxfp4.h).
+struct GemmArgs {
+  const uint8_t* x_codes;
+  const uint8_t* x_scales;
+  const float* x_globals;  // NVFP4 only
+  int64_t rows;
+  int64_t K;
+  const int32_t* offsets;
+  int32_t E;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  const float* globals;    // NVFP4 only
+  int64_t N;
+  const void* bias;
+  int32_t activation;
+  int32_t gate;
+  const void* residual;
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  int32_t* status;
+  bool f16;
+  bool nvfp4;
+};
+cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream);
+
+// The experts' rows back to their tokens.
+struct CombineArgs {
+  const void* rows;
+  bool rows_f32;
+  int64_t total_rows;
+  int64_t N;
+  int64_t ldr;
+  const int32_t* dest;
+  const float* weights;
+  int64_t num_tokens;
+  int32_t top_k;
+  const void* residual;
+  int64_t ld_res;
+  void* y;
+  int64_t ldy;
+  int32_t* status;
+  bool f16;
+};
+cudaError_t launch_moe_combine(const CombineArgs& a, cudaStream_t stream);
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
@@ -220,6 +288,9 @@ unsigned int debug_violations_route();
 unsigned int debug_violations_matvec();
 unsigned int debug_violations_cache();
 unsigned int debug_violations_attention();
+unsigned int debug_violations_topk();
+unsigned int debug_violations_gemm();
+unsigned int debug_violations_combine();
 #endif
 
 // Launch with programmatic dependent launch allowed: the grid may be
