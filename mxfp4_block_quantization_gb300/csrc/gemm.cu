@@ -1,141 +1,691 @@
-// gemm.cu — products of 4-bit activations with 4-bit weights for sm_103a, the
-// simple form: a CTA of 256 threads makes 64 rows by 64 columns of y, both
-// operands decoded to float32 in shared memory 32 elements of K at a time.
+// gemm.cu — products of 4-bit activations with 4-bit weights for sm_103a, dense
+// and per expert, with bias, activation, gate and residual in the epilogue
+// (formulas in include/mxfp4.h).
+//
+// The codes and tiled scales go to the tensor cores as they lie: a block-scaled
+// tcgen05.mma takes E2M1 operands packed two to a byte and, of each 512-byte
+// chunk of the 128x4-tiled scales, the copy to tensor memory that tcgen05.cp
+// makes.  Nothing is decoded.
+//
+// The 128-row operand is always the weights, tokens are the columns: their
+// number in an instruction is any multiple of 16 up to 256, so one kernel serves
+// one token and many.  A CTA's tile is 128 rows of the weights by 256 tokens, or,
+// with a gate, 128 rows of each half by 128 tokens, whose two sums meet in the
+// epilogue.  256 bytes of K at a time (a stage) are 16 KB for each 128 rows.
+//
+// Warp 0 copies stages ahead (TMA, a ring of four), one thread of warp 1 issues
+// the scales' copies and the products, warps 4 to 11 take the sums from tensor
+// memory into registers, which frees it for the next tile, and finish them.  Each
+// CTA walks every gridDim-th tile.  Where tiles are few, a cluster of up to 8 CTAs
+// shares a tile, each with a part of K, and adds the parts in rank order through
+// distributed shared memory: equal calls give equal bits.
 #include <cmath>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "fragments.cuh"
 #include "mxfp4_device.cuh"
 #include "mxfp4_internal.h"
+#include "tensor_core.cuh"
 #include "../../include/mxfp4.h"
 
 namespace mxfp4 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSide = 64;
+constexpr int kThreads = 384;
+constexpr int kFirstEpilogue = 4;              // warp
+constexpr int kEpilogueThreads = 256;
+constexpr int kStages = 4;
+constexpr int kRows = 128;                     // of an operand's tile
+constexpr int kStageBytes = 128;               // of a row's codes: 256 elements
+constexpr int kSlab = kRows * kStageBytes;     // 16 KB
+constexpr int kSlabs = 3;
+constexpr int kSteps = 4;                      // products of 64 elements to a stage
+constexpr int kBoxRows = 32;                   // tokens' rows to a copy
+constexpr int kFinished = 32;                  // tokens that a thread finishes at a time
+constexpr int kColumns = 512;                  // all of tensor memory
+// tensor memory: sums, then the scales of both weight tiles and of the tokens
+constexpr uint32_t kScalesA = 256, kScalesB = 288;
 
-struct GemmParams {
-  GemmArgs a;
-  int64_t expert_codes;
-  int64_t expert_scales;
-  int nKT;
-  int cols;
+// A stage's scales of 128 rows: two chunks of 512 bytes (four with NVFP4), for
+// three tiles and, where the second half of gated weights does not begin at a
+// tile of the scales, the tile behind it.
+template <bool kNv>
+struct Layout {
+  static constexpr int kChunks = kNv ? 4 : 2;
+  static constexpr int kScales = kChunks * 512;
+  static constexpr int kStage = kSlabs * kSlab + 4 * kScales;
+  static constexpr int kBytes = kStages * kStage;
+};
+
+struct GemmMore {
 #ifdef MXFP4_DEBUG_BOUNDS
   DebugRanges dbg;
 #endif
 };
-enum : int { kDbgXCodes = 0, kDbgXScales, kDbgCodes, kDbgScales, kDbgOffsets, kDbgResidual, kDbgY, kDbgStatus };
 
-__device__ __forceinline__ float load_half(const void* p, int64_t i, bool f16) {
-  const uint16_t v = static_cast<const uint16_t*>(p)[i];
+struct GemmParams {
+  const uint8_t* x_scales;
+  const uint8_t* scales;
+  const float* x_globals;
+  const float* globals;
+  const int32_t* offsets;   // NULL: dense
+  const uint16_t* bias;     // or NULL
+  const uint16_t* residual; // or NULL
+  uint16_t* y;
+  int32_t* status;          // or NULL
+  int64_t expert_scales;    // bytes of one expert's tiled scales
+  int64_t ldr;
+  int64_t ldy;
+  int32_t rows;
+  int32_t N;
+  int32_t cols;             // of y
+  int32_t E;
+  int32_t nKT;              // scale chunks of a row
+  int32_t steps;            // products along K
+  int32_t stages;           // stages along K
+  int32_t blocks;           // scales of a row
+  int32_t row_tiles;        // tiles of the weights' rows
+  int32_t activation;
+  bool gate_second;
+  bool f16;
+  bool paired;              // two columns of y in one store
+#ifdef MXFP4_DEBUG_BOUNDS
+  DebugRanges dbg;
+#endif
+  GemmMore more;
+};
+
+enum : int { kDbgXScales = 0, kDbgScales, kDbgOffsets, kDbgBias, kDbgResidual, kDbgY, kDbgStatus, kDbgXGlobals };
+enum : int { kDbgGlobals = 0 };
+
+__device__ __forceinline__ int32_t offset_at(const GemmParams& p, int e) {
+  const int32_t* at = p.offsets + e;
+  return MXFP4_IN_BOUNDS(p, kDbgOffsets, at, 4) ? __ldg(at) : 0;
+}
+
+// A tile: tokens [row, row + n) of expert e, whose scales begin at tiled row
+// `padded`, by weight rows from r0 on (of each half).
+struct Tile {
+  int e, row, n, padded, r0;
+};
+
+// The tiles in order of expert, weight rows, tokens.  A warp finds them
+// together, 32 experts at a time; its lanes agree.
+template <int kTokens>
+struct Walk {
+  int e0 = -32, before = 0, padded_before = 0;  // of the experts below e0
+  int lo = 0, n = 0, tiles = 0, sum = 0, padded = 0;  // the lane's expert: sum up to and with it
+  int block_tiles = 0, block_padded = 0;
+
+  __device__ bool find(const GemmParams& p, int index, Tile& t) {
+    const int lane = threadIdx.x & 31;
+    if (p.offsets == nullptr) {
+      const int token_tiles = (p.rows + kTokens - 1) / kTokens;
+      const int r = index / token_tiles, c = index - r * token_tiles;
+      if (r >= p.row_tiles) return false;
+      t = Tile{0, c * kTokens, min(kTokens, p.rows - c * kTokens), c * kTokens, r * kRows};
+      return true;
+    }
+    while (index >= before + block_tiles) {
+      before += block_tiles, padded_before += block_padded;
+      e0 += 32;
+      if (e0 >= p.E) return false;
+      const int e = e0 + lane;
+      n = 0;
+      if (e < p.E) lo = offset_at(p, e), n = offset_at(p, e + 1) - lo;
+      tiles = (n + kTokens - 1) / kTokens * p.row_tiles;
+      padded = (n + kRows - 1) / kRows * kRows;
+      sum = tiles;
+      int psum = padded;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int a = __shfl_up_sync(0xFFFFFFFFu, sum, d), b = __shfl_up_sync(0xFFFFFFFFu, psum, d);
+        if (lane >= d) sum += a, psum += b;
+      }
+      block_tiles = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      block_padded = __shfl_sync(0xFFFFFFFFu, psum, 31);
+      padded = psum - padded;
+    }
+    const int l = __ffs(__ballot_sync(0xFFFFFFFFu, index < before + sum)) - 1;
+    const int rows = __shfl_sync(0xFFFFFFFFu, n, l);
+    const int first = before + __shfl_sync(0xFFFFFFFFu, sum - tiles, l);
+    const int token_tiles = (rows + kTokens - 1) / kTokens;
+    const int r = (index - first) / token_tiles, c = index - first - r * token_tiles;
+    t = Tile{e0 + l, __shfl_sync(0xFFFFFFFFu, lo, l) + c * kTokens, min(kTokens, rows - c * kTokens),
+             padded_before + __shfl_sync(0xFFFFFFFFu, padded, l) + c * kTokens, r * kRows};
+    return true;
+  }
+};
+
+struct Barriers {
+  uint64_t full[kStages], empty[kStages], sums_full, sums_empty, drained;
+  uint32_t columns;  // tensor memory's address
+  int gave_up;
+};
+
+// --------------------------------------------------------------- epilogue
+__device__ __forceinline__ float widen(uint16_t v, bool f16) {
   return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
-
-__device__ float activate(float z, int act) {
-  if (act == MXFP4_ACT_SILU) return z / (1.0f + expf(-z));
-  if (act == MXFP4_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-  if (act == MXFP4_ACT_GELU_TANH)
-    return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-  return z;
+// Two values as halves of y's type, `lo` in the low half.
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi, bool f16) {
+  return f16 ? pack_f16x2(lo, hi) : cvt_bf16x2(lo, hi);
 }
 
-// Element k of a row whose scales begin at tiled row r.
-__device__ float element(const uint8_t* codes, const uint8_t* scales, int64_t row, int64_t r, int k,
-                         int K, int nKT, bool nvfp4) {
-  const uint32_t b = codes[row * (K / 2) + k / 2];
-  const uint32_t h2 = cvt_e2m1x2_to_f16x2(b);
-  const float v = k & 1 ? half_hi_to_f32(h2) : half_lo_to_f32(h2);
-  const int c = k / (nvfp4 ? 16 : 32);
-  const uint32_t s = scales[((r / 128) * nKT + c / 4) * 512 + chunk_offset(static_cast<int>(r % 128), c % 4)];
-  if (nvfp4) return v * e4m3_to_f32(s);
-  return s == 255u ? NAN : v * scale_from_e8m0(s);
+// By the fast exponential and division: off by 2^-21 of |z| (see pick32 in
+// topk.cu for z's sigmoid), which a later rounding to 16 bits hides.
+__device__ __forceinline__ float sigmoid_times(float z, float u) {  // z / (1 + e^-u)
+  return __fdividef(z, 1.0f + __expf(-u));
+}
+template <int kCount>
+__device__ __forceinline__ void activate(float* z, int act) {
+  if (act == MXFP4_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) z[j] = sigmoid_times(z[j], z[j]);
+  } else if (act == MXFP4_ACT_GELU) {
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) z[j] = 0.5f * z[j] * (1.0f + erff(z[j] * 0.70710678118654752f));
+  } else if (act == MXFP4_ACT_GELU_TANH) {
+    // 0.5 (1 + tanh(v)) = 1 / (1 + e^-2v)
+#pragma unroll
+    for (int j = 0; j < kCount; ++j)
+      z[j] = sigmoid_times(z[j], 1.5957691216057308f * (z[j] + 0.044715f * z[j] * z[j] * z[j]));
+  }
 }
 
-__global__ void __launch_bounds__(kThreads) gemm_kernel(const GemmParams p) {
-  __shared__ float xs[kSide][33], ws[2][kSide][33];
-  __shared__ int s_bad, s_pad;
+// What a thread's row of the weights adds and scales: z = sum * alpha + bias.
+struct RowTerms {
+  float alpha, bias, other_bias;  // `other`: of the second half
+};
+template <bool kNv, bool kGated>
+__device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t, int n) {
+  RowTerms r{1.0f, 0.0f, 0.0f};
+  if constexpr (kNv) {
+    if (p.steps > 0) {
+      const float a = MXFP4_IN_BOUNDS(p, kDbgXGlobals, p.x_globals + t.e, 4) ? __ldg(p.x_globals + t.e) : 1.0f;
+      const float b = MXFP4_IN_BOUNDS(p.more, kDbgGlobals, p.globals + t.e, 4) ? __ldg(p.globals + t.e) : 1.0f;
+      r.alpha = (1.0f / a) * (1.0f / b);
+    }
+  }
+  if (p.bias != nullptr && n < p.cols) {
+    const uint16_t* at = p.bias + static_cast<int64_t>(t.e) * p.N + n;
+    r.bias = MXFP4_IN_BOUNDS(p, kDbgBias, at, 2) ? widen(__ldg(at), p.f16) : 0.0f;
+    if (kGated) {
+      at += p.cols;
+      r.other_bias = MXFP4_IN_BOUNDS(p, kDbgBias, at, 2) ? widen(__ldg(at), p.f16) : 0.0f;
+    }
+  }
+  return r;
+}
+
+// kCount tokens from column c of the tile on (u: the second half's sums) of the
+// thread's column n of y: finished in place.
+template <bool kGated, int kCount = kFinished>
+__device__ __forceinline__ void finish(const GemmParams& p, const Tile& t, const RowTerms& r, int n,
+                                       int c, float* v, float* u) {
+#pragma unroll
+  for (int j = 0; j < kCount; ++j) v[j] = fmaf(v[j], r.alpha, r.bias);
+  if constexpr (kGated) {
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) u[j] = fmaf(u[j], r.alpha, r.other_bias);
+    if (p.gate_second) activate<kCount>(u, p.activation);
+    else activate<kCount>(v, p.activation);
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) v[j] *= u[j];
+  } else {
+    activate<kCount>(v, p.activation);
+  }
+  if (p.residual != nullptr) {
+    const uint16_t* at = p.residual + (t.row + c) * p.ldr + n;
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) {
+      // may be y: a plain load, of what this thread alone writes
+      if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) v[j] += widen(*at, p.f16);
+      at += p.ldr;
+    }
+  }
+}
+
+template <int kCount = kFinished>
+__device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n, int c,
+                                      const float* v) {
+  if (p.paired) {
+    // neighbours exchange, so that each stores two columns of every other token
+    const bool odd = n & 1;
+    uint16_t* at = p.y + (t.row + c + odd) * p.ldy + (n & ~1);
+#pragma unroll
+    for (int j = 0; j < kCount; j += 2) {
+      const uint32_t mine = narrow2(v[j], v[j + 1], p.f16);
+      const uint32_t next = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+      const uint32_t word = odd ? __byte_perm(mine, next, 0x3276) : __byte_perm(mine, next, 0x5410);
+      if (c + j + odd < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 4))
+        *reinterpret_cast<uint32_t*>(at) = word;
+      at += 2 * p.ldy;
+    }
+  } else {
+    uint16_t* at = p.y + (t.row + c) * p.ldy + n;
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) {
+      if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2))
+        *at = static_cast<uint16_t>(narrow2(v[j], 0.0f, p.f16));
+      at += p.ldy;
+    }
+  }
+}
+
+// ------------------------------------------------------------------- scales
+// A stage's scales as the products need them, where they do not lie so:
+// rows `shift` on of the two tiles that the second half spans, moved to the first;
+// bytes past the last block of a row, whatever they hold, made zero.
+template <bool kNv>
+__device__ void mend_scales(uint32_t scales, int tiles, int moved, int shift, int keep) {
+  const int lane = threadIdx.x & 31;
+  if (shift != 0) {
+    const uint32_t lo = scales + moved * Layout<kNv>::kScales, hi = scales + 3 * Layout<kNv>::kScales;
+    const int row = (shift + lane) & 31, first = (shift + lane) >> 5;  // first: 0..4
+    uint32_t w[Layout<kNv>::kChunks][4];
+#pragma unroll
+    for (int c = 0; c < Layout<kNv>::kChunks; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int q = first + j;
+        w[c][j] = lds32((q < 4 ? lo : hi) + c * 512 + row * 16 + (q & 3) * 4);
+      }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < Layout<kNv>::kChunks; ++c)
+      sts128(lo + c * 512 + lane * 16, w[c][0], w[c][1], w[c][2], w[c][3]);
+    __syncwarp();
+  }
+  if (keep >= 0) {  // bytes of the row that are scales, in this stage
+    const uint32_t mask = (1u << (8 * (keep & 3))) - 1u;  // of the chunk's word that is not full
+    for (int i = 0; i < tiles; ++i) {
+      const uint32_t at = scales + i * Layout<kNv>::kScales + (keep >> 2) * 512 + lane * 16;
+      const uint4 v = lds128(at);
+      sts128(at, v.x & mask, v.y & mask, v.z & mask, v.w & mask);
+    }
+  }
+  tc::fence_async();
+  __syncwarp();
+}
+
+// --------------------------------------------------------------- the kernel
+template <bool kNv, bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap w_map,
+                const GemmParams p) {
+  using L = Layout<kNv>;
+  constexpr int kTokens = kGated ? 128 : 256;
+  constexpr int kWeightSlabs = kGated ? 2 : 1;
+  extern __shared__ uint8_t smem[];
+  __shared__ Barriers bars;
+  __shared__ int s_bad;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t ring = (tc::shared_address(smem) + 1023u) & ~1023u;
+  const auto bar = [](const uint64_t& b) { return tc::shared_address(&b); };
+  uint32_t ranks;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
+  const uint32_t rank = ranks > 1 ? cluster_rank() : 0;
+  const int first_tile = ranks > 1 ? static_cast<int>(blockIdx.x / ranks) : static_cast<int>(blockIdx.x);
+  const int tile_step = ranks > 1 ? INT32_MAX / 2 : static_cast<int>(gridDim.x);  // clusters: one tile
+  const int k_begin = static_cast<int>(static_cast<int64_t>(p.stages) * rank / ranks);
+  const int k_end = static_cast<int>(static_cast<int64_t>(p.stages) * (rank + 1) / ranks);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) tc::barrier_init(bar(bars.full[s]), 1), tc::barrier_init(bar(bars.empty[s]), 1);
+    tc::barrier_init(bar(bars.sums_full), 1);
+    tc::barrier_init(bar(bars.sums_empty), kEpilogueThreads);
+    tc::barrier_init(bar(bars.drained), 1);
+    tc::barrier_init_fence();
+    bars.gave_up = 0;
+    s_bad = 0;
+    if (p.stages > 0) tc::prefetch_map(&x_map), tc::prefetch_map(&w_map);
+  }
+  if (warp == 1) tc::allocate(tc::shared_address(&bars.columns), kColumns);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t columns = *static_cast<volatile uint32_t*>(&bars.columns);
+  volatile int* const gave_up = &bars.gave_up;
   pdl_wait();
   pdl_release();
-  const GemmArgs& a = p.a;
-  const int e = blockIdx.z;
-  int64_t lo = 0, hi = a.rows, pad = 0;
-  if (threadIdx.x == 0) s_bad = 0, s_pad = 0;
-  __syncthreads();
-  if (a.offsets) {
-    int bad = threadIdx.x == 0 && a.offsets[0] != 0, sum = 0;
-    for (int i = threadIdx.x; i < a.E; i += kThreads) {
-      const int from = a.offsets[i], to = a.offsets[i + 1];
-      bad |= from > to || from < 0 || to > a.rows;
-      if (i < e) sum += (to - from + 127) / 128 * 128;
+
+  bool work = true;
+  if (p.offsets != nullptr) {
+    int bad = threadIdx.x == 0 && offset_at(p, 0) != 0;
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+      const int from = offset_at(p, e), to = offset_at(p, e + 1);
+      bad |= from < 0 || from > to || to > p.rows;
     }
-    if (bad) atomicOr(&s_bad, 1);
-    atomicAdd(&s_pad, sum);
-    __syncthreads();
-    if (a.status && blockIdx.x == 0 && e == 0 && threadIdx.x == 0)
-      *a.status = s_bad ? MXFP4_EOFFSETS : MXFP4_OK;
-    if (s_bad || a.E == 0 || p.cols == 0) return;
-    lo = a.offsets[e], hi = a.offsets[e + 1], pad = s_pad;
+    work = __syncthreads_or(bad) == 0;
+    if (threadIdx.x == 0 && blockIdx.x == 0 && p.status != nullptr && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4))
+      *p.status = work ? MXFP4_OK : MXFP4_EOFFSETS;
   }
-  const bool gated = a.gate != MXFP4_GATE_NONE;
-  const int n0 = blockIdx.x * kSide;
-  const int first = a.gate == MXFP4_GATE_SECOND ? p.cols : 0;   // the activated rows of W
-  const int other = a.gate == MXFP4_GATE_SECOND ? 0 : p.cols;
-  const uint8_t* const wc = a.codes + e * p.expert_codes;
-  const uint8_t* const wsc = a.scales + e * p.expert_scales;
-  const float alpha = a.nvfp4 && a.K > 0 ? (1.0f / a.x_globals[e]) * (1.0f / a.globals[e]) : 1.0f;
-  const int K = static_cast<int>(a.K);
-  for (int64_t t0 = lo; t0 < hi; t0 += kSide) {
-    float acc[2][4][4] = {};
-    for (int k0 = 0; k0 < K; k0 += 32) {
-      __syncthreads();
-      for (int i = threadIdx.x; i < kSide * 32; i += kThreads) {
-        const int r = i / 32, k = i % 32;
-        xs[r][k] = t0 + r < hi ? element(a.x_codes, a.x_scales, t0 + r, pad + t0 - lo + r, k0 + k, K, p.nKT, a.nvfp4) : 0.0f;
-        const bool in = n0 + r < p.cols;
-        ws[0][r][k] = in ? element(wc, wsc, first + n0 + r, first + n0 + r, k0 + k, K, p.nKT, a.nvfp4) : 0.0f;
-        if (gated) ws[1][r][k] = in ? element(wc, wsc, other + n0 + r, other + n0 + r, k0 + k, K, p.nKT, a.nvfp4) : 0.0f;
-      }
-      __syncthreads();
-      for (int k = 0; k < 32; ++k)
-        for (int i = 0; i < 4; ++i)
-          for (int j = 0; j < 4; ++j) {
-            const float x = xs[threadIdx.x / 16 + 16 * i][k];
-            acc[0][i][j] = fmaf(x, ws[0][threadIdx.x % 16 + 16 * j][k], acc[0][i][j]);
-            if (gated) acc[1][i][j] = fmaf(x, ws[1][threadIdx.x % 16 + 16 * j][k], acc[1][i][j]);
+  // the second half's rows begin at row `shift` of a tile of the scales
+  const int shift = kGated ? p.cols & (kRows - 1) : 0;
+
+  Walk<kTokens> walk;
+  Tile t;
+  if (!work) {
+  } else if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    uint32_t stage = 0, phase = 0;
+    bool ok = true, wrapped = false;
+    for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step) {
+      if (lane == 0) {
+        const int boxes = (t.n + kBoxRows - 1) / kBoxRows;
+        const uint8_t* const ws = p.scales + t.e * p.expert_scales;
+        const int w_row = t.e * p.N + t.r0;
+        const int upper = (p.cols + t.r0) / kRows;  // the second half's tile of scales
+        for (int k = k_begin; k < k_end; ++k) {
+          if (wrapped && !(ok = tc::barrier_wait(bar(bars.empty[stage]), phase ^ 1u, gave_up))) break;
+          const uint32_t at = ring + stage * L::kStage, sc = at + kSlabs * kSlab, full = bar(bars.full[stage]);
+          const int chunks = min(L::kChunks, p.nKT - k * L::kChunks);
+          const uint32_t bytes = chunks * 512;
+          const int64_t row_bytes = static_cast<int64_t>(p.nKT) * 512, from = static_cast<int64_t>(k) * L::kScales;
+          const uint8_t* src[4] = {ws + t.r0 / kRows * row_bytes + from, nullptr, nullptr, nullptr};
+          const uint8_t* const xs = p.x_scales + t.padded / kRows * row_bytes + from;
+          if constexpr (kGated) {
+            src[1] = ws + upper * row_bytes + from;
+            src[2] = xs;
+            // the last tile of the scales may be the weights' last
+            if (shift != 0 && (upper + 1) * kRows < (p.N + kRows - 1) / kRows * kRows) src[3] = src[1] + row_bytes;
+          } else {
+            src[1] = xs;
+            if (t.n > kRows) src[2] = xs + row_bytes;
           }
-    }
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const int64_t t = t0 + threadIdx.x / 16 + 16 * i;
-        const int n = n0 + threadIdx.x % 16 + 16 * j;
-        if (t >= hi || n >= p.cols) continue;
-        float z = acc[0][i][j] * alpha, u = acc[1][i][j] * alpha;
-        if (a.bias) z += load_half(a.bias, e * a.N + first + n, a.f16);
-        if (a.bias && gated) u += load_half(a.bias, e * a.N + other + n, a.f16);
-        float y = activate(z, a.activation);
-        if (gated) y *= u;
-        if (a.residual) y += load_half(a.residual, t * a.ldr + n, a.f16);
-        static_cast<uint16_t*>(a.y)[t * a.ldy + n] =
-            a.f16 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+          uint32_t scale_bytes = 0;
+#pragma unroll
+          for (int s = 0; s < 4; ++s) {
+            if (src[s] != nullptr &&
+                !MXFP4_IN_BOUNDS(p, (kGated ? s == 2 : s > 0) ? kDbgXScales : kDbgScales, src[s], bytes))
+              src[s] = nullptr;
+            if (src[s] != nullptr) scale_bytes += bytes;
+          }
+          tc::barrier_expect(full, kWeightSlabs * kSlab + boxes * (kBoxRows * kStageBytes) + scale_bytes);
+          const int x = k * kStageBytes;
+          tc::copy_box(at, &w_map, x, w_row, full);
+          if constexpr (kGated) tc::copy_box(at + kSlab, &w_map, x, w_row + p.cols, full);
+          for (int b = 0; b < boxes; ++b)
+            tc::copy_box(at + kWeightSlabs * kSlab + b * (kBoxRows * kStageBytes), &x_map, x, t.row + b * kBoxRows, full);
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            if (src[s] != nullptr) tc::copy_bytes(sc + s * L::kScales, src[s], bytes, full);
+          if (++stage == kStages) stage = 0, phase ^= 1u, wrapped = true;
+        }
       }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    }
+    // every copy has landed before the CTA may end: slots behind `stage` hold
+    // the phase before
+    if (lane == 0 && *gave_up) {
+      int none = 0;
+      for (uint32_t s = 0; s < kStages; ++s)
+        if (wrapped || s < stage) {
+          const uint32_t last = s < stage ? phase : phase ^ 1u;
+          for (int tries = 0; tries < 4 && !tc::barrier_wait(bar(bars.full[s]), last, &none); ++tries) none = 0;
+        }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- products
+    uint32_t stage = 0, phase = 0, sums_phase = 0;
+    bool ok = true, again = false;
+    for (int i = first_tile; ok && k_begin < k_end && walk.find(p, i, t); i += tile_step) {
+      const uint32_t inst = tc::instruction((t.n + 15) / 16 * 16, kNv);
+      if (again) {  // the sums of the tile before have been taken
+        ok = tc::barrier_wait(bar(bars.sums_empty), sums_phase, gave_up);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        sums_phase ^= 1u;
+        tc::fence_after();
+        if (!ok) break;
+      }
+      again = true;
+      for (int k = k_begin; k < k_end; ++k) {
+        ok = tc::barrier_wait(bar(bars.full[stage]), phase, gave_up);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t at = ring + stage * L::kStage, sc = at + kSlabs * kSlab;
+        const int steps = min(kSteps, p.steps - k * kSteps);
+        const int keep = k == p.stages - 1 && (p.blocks & (kNv ? 3 : 1)) ? p.blocks - k * L::kChunks * 4 : -1;
+        if (shift != 0 || keep >= 0) mend_scales<kNv>(sc, 3, 1, shift, keep);
+        if (lane == 0) {
+          const uint64_t a = tc::operand_descriptor(at), b = tc::operand_descriptor(at + kWeightSlabs * kSlab);
+          const uint64_t s0 = tc::scales_descriptor(sc);
+          constexpr uint64_t kTile = L::kScales / 16;  // a tile's scales, in descriptors' units
+          const int chunks = min(L::kChunks, p.nKT - k * L::kChunks);
+          for (int c = 0; c < chunks; ++c) {
+            tc::copy_scales(columns + kScalesA + c * 4, s0 + c * 32);
+            if constexpr (kGated) {
+              tc::copy_scales(columns + kScalesA + 16 + c * 4, s0 + kTile + c * 32);
+              tc::copy_scales(columns + kScalesB + c * 4, s0 + 2 * kTile + c * 32);
+            } else {
+              tc::copy_scales(columns + kScalesB + c * 8, s0 + kTile + c * 32);
+              if (t.n > kRows) tc::copy_scales(columns + kScalesB + c * 8 + 4, s0 + 2 * kTile + c * 32);
+            }
+          }
+          constexpr int kStride = kGated ? 4 : 8;  // the tokens' columns of a chunk
+          for (int s = 0; s < steps; ++s) {
+            const int c = kNv ? s : s >> 1;
+            const uint32_t in = kNv ? inst : tc::with_scale_byte(inst, 2u * (s & 1));
+            const bool add = k > k_begin || s > 0;
+            tc::multiply<kNv>(columns, a + 2 * s, b + 2 * s, in, columns + kScalesA + c * 4,
+                              columns + kScalesB + c * kStride, add);
+            if constexpr (kGated)
+              tc::multiply<kNv>(columns + 128, a + kSlab / 16 + 2 * s, b + 2 * s, in,
+                                columns + kScalesA + 16 + c * 4, columns + kScalesB + c * kStride, add);
+          }
+          tc::arrive_when_done(bar(bars.empty[stage]));
+          if (k == k_end - 1) tc::arrive_when_done(bar(bars.sums_full));
+        }
+        __syncwarp();
+        if (++stage == kStages) stage = 0, phase ^= 1u;
+      }
+    }
+    if (*gave_up) {  // what was issued is done before tensor memory is freed
+      int none = 0;
+      if (lane == 0) {
+        tc::arrive_when_done(bar(bars.drained));
+        tc::barrier_wait(bar(bars.drained), 0, &none);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kFirstEpilogue) {
+    // ---------------------------------------------------------- epilogue
+    const int half = (warp - kFirstEpilogue) >> 2, quarter = warp & 3;
+    const uint32_t from = columns + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int row = quarter * 32 + lane;     // of the tile
+    uint32_t sums_phase = 0;
+    bool ok = true;
+    for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step) {
+      const int n = t.r0 + row;
+      const RowTerms terms = row_terms<kNv, kGated>(p, t, n);
+      if (k_begin < k_end) {
+        ok = tc::barrier_wait(bar(bars.sums_full), sums_phase, gave_up);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        sums_phase ^= 1u;
+        tc::fence_after();
+      }
+      float v[32], u[32];
+      float* const part = reinterpret_cast<float*>(smem + (ring - tc::shared_address(smem)));
+#pragma unroll 1
+      for (int column = half * 32; column < t.n; column += 64) {
+        if (k_begin < k_end) {
+          tc::load32(from + column, v);
+          if constexpr (kGated) tc::load32(from + 128 + column, u);
+          tc::load_wait();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = u[j] = 0.0f;
+        }
+        if (!ok) {  // says that there is no result
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = NAN;
+        }
+        if (ranks > 1) {
+          // this CTA's part of the sums to its shared memory, [token][row]: the
+          // ring is free, all its products are done
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            part[(column + j) * kRows + row] = v[j];
+            if constexpr (kGated) part[(kTokens + column + j) * kRows + row] = u[j];
+          }
+        } else {
+          finish<kGated>(p, t, terms, n, column, v, u);
+          store(p, t, n, column, v);
+        }
+      }
+      tc::fence_before();
+      tc::barrier_arrive(bar(bars.sums_empty));
+    }
   }
+  if (ranks > 1) {
+    __syncwarp();
+    cluster_sync();
+    const bool mine = work && warp >= kFirstEpilogue;
+    walk = Walk<kTokens>();
+    if (mine && walk.find(p, first_tile, t)) {
+      // each rank finishes every ranks-th token, its two halves every other of those
+      const int thread = threadIdx.x - kFirstEpilogue * 32, row = thread & (kRows - 1), n = t.r0 + row;
+      const RowTerms terms = row_terms<kNv, kGated>(p, t, n);
+      for (int c = rank + ranks * (thread >> 7); c < t.n; c += 2 * ranks) {
+        float v[1] = {0.0f}, u[1] = {0.0f};
+        for (uint32_t r = 0; r < ranks; ++r) {
+          const uint32_t at = cluster_address(ring, r) + (c * kRows + row) * 4;
+          float a;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(at) : "memory");
+          v[0] += a;
+          if constexpr (kGated) {
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(at + kTokens * kRows * 4) : "memory");
+            u[0] += a;
+          }
+        }
+        finish<kGated, 1>(p, t, terms, n, c, v, u);
+        uint16_t* const at = p.y + (t.row + c) * p.ldy + n;
+        if (n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2)) *at = static_cast<uint16_t>(narrow2(v[0], 0.0f, p.f16));
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (threadIdx.x == 0 && *gave_up && p.status != nullptr && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4))
+    *p.status = MXFP4_ECUDA;
+  if (warp == 1) tc::release(columns, kColumns);
+}
+
+// ------------------------------------------------------------------- launch
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encode_tiled() {
+  static const EncodeTiled found = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult how;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &how) != cudaSuccess ||
+        how != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<EncodeTiled>(fn);
+  }();
+  return found;
+}
+
+// Rows of K/2 bytes of codes, in boxes of 128 bytes by `box` rows; zeros outside.
+cudaError_t map_codes(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t K, int box) {
+  const EncodeTiled encode = encode_tiled();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
+  const cuuint32_t boxes[2] = {kStageBytes, static_cast<cuuint32_t>(box)}, ones[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, boxes, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <bool kNv, bool kGated>
+cudaError_t launch_typed(const CUtensorMap& x_map, const CUtensorMap& w_map, const GemmParams& p, int64_t tiles,
+                         cudaStream_t stream) {
+  constexpr int kBytes = Layout<kNv>::kBytes + 1024;  // to a multiple of 1024
+  static std::atomic<uint64_t> ready{0};
+  if (const cudaError_t e = allow_smem(gemm_kernel<kNv, kGated>, kBytes, ready); e != cudaSuccess) return e;
+  // clusters that share a tile's K: as many CTAs as the SMs hold, a stage each
+  const int64_t sms = sm_count();
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks * 2 <= sms && ranks * 2 <= p.stages) ranks *= 2;
+  const int64_t grid = ranks > 1 ? tiles * ranks : tiles < sms ? tiles : sms;
+  return launch_pdl_cluster(gemm_kernel<kNv, kGated>, dim3(static_cast<unsigned>(grid)), kThreads, kBytes, stream,
+                            ranks > 1 ? ranks : 0, x_map, w_map, p);
 }
 
 }  // namespace
 
 cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
   GemmParams p{};
-  p.a = a;
-  p.nKT = static_cast<int>((a.K / (a.nvfp4 ? 16 : 32) + 3) / 4);
-  p.cols = static_cast<int>(a.gate != MXFP4_GATE_NONE ? a.N / 2 : a.N);
-  p.expert_codes = a.N * (a.K / 2);
-  p.expert_scales = (a.N + 127) / 128 * p.nKT * kChunkBytes;
-  const dim3 grid(p.cols > 0 ? (p.cols + kSide - 1) / kSide : 1, 1, a.E > 0 ? a.E : 1);
-  return launch_pdl(gemm_kernel, grid, kThreads, 0, stream, p);
+  const bool gated = a.gate != MXFP4_GATE_NONE;
+  p.x_scales = a.x_scales;
+  p.scales = a.scales;
+  p.x_globals = a.x_globals;
+  p.globals = a.globals;
+  p.offsets = a.offsets;
+  p.bias = static_cast<const uint16_t*>(a.bias);
+  p.residual = static_cast<const uint16_t*>(a.residual);
+  p.y = static_cast<uint16_t*>(a.y);
+  p.status = a.status;
+  p.ldr = a.ldr;
+  p.ldy = a.ldy;
+  p.rows = static_cast<int32_t>(a.rows);
+  p.N = static_cast<int32_t>(a.N);
+  p.cols = gated ? p.N / 2 : p.N;
+  p.E = a.E;
+  p.blocks = static_cast<int32_t>(a.K / (a.nvfp4 ? 16 : 32));
+  p.nKT = (p.blocks + 3) / 4;
+  p.steps = static_cast<int32_t>((a.K + 63) / 64);
+  p.stages = (p.steps + kSteps - 1) / kSteps;
+  p.row_tiles = (p.cols + kRows - 1) / kRows;
+  p.expert_scales = (a.N + 127) / 128 * p.nKT * static_cast<int64_t>(kChunkBytes);
+  p.activation = a.activation;
+  p.gate_second = a.gate == MXFP4_GATE_SECOND;
+  p.f16 = a.f16;
+  p.paired = p.cols % 2 == 0 && a.ldy % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0;
+#ifdef MXFP4_DEBUG_BOUNDS
+  debug_range(p.dbg, kDbgXScales, a.x_scales,
+              (a.rows + 127 * static_cast<int64_t>(a.E)) / 128 * p.nKT * kChunkBytes);
+  debug_range(p.dbg, kDbgScales, a.scales, a.E * p.expert_scales);
+  debug_range(p.dbg, kDbgOffsets, a.offsets, a.offsets ? (static_cast<int64_t>(a.E) + 1) * 4 : 0);
+  debug_range(p.dbg, kDbgBias, a.bias, a.bias ? a.E * a.N * 2 : 0);
+  debug_range(p.dbg, kDbgResidual, a.residual, a.residual ? ((a.rows - 1) * a.ldr + p.cols) * 2 : 0);
+  debug_range(p.dbg, kDbgY, a.y, a.rows > 0 ? ((a.rows - 1) * a.ldy + p.cols) * 2 : 0);
+  debug_range(p.dbg, kDbgStatus, a.status, a.status ? 4 : 0);
+  debug_range(p.dbg, kDbgXGlobals, a.x_globals, a.nvfp4 ? a.E * 4 : 0);
+  debug_range(p.more.dbg, kDbgGlobals, a.globals, a.nvfp4 ? a.E * 4 : 0);
+#endif
+  CUtensorMap x_map{}, w_map{};
+  if (a.K > 0 && a.rows > 0 && a.N > 0 && a.E > 0) {
+    if (const cudaError_t e = map_codes(&x_map, a.x_codes, a.rows, a.K, kBoxRows); e != cudaSuccess) return e;
+    if (const cudaError_t e = map_codes(&w_map, a.codes, a.E * a.N, a.K, kRows); e != cudaSuccess) return e;
+  }
+  // at most this many tiles: every expert with rows may have one that is not full
+  const int64_t tokens = gated ? 128 : 256;
+  const int64_t token_tiles = a.offsets ? a.rows / tokens + (a.rows < a.E ? a.rows : a.E)
+                                        : (a.rows + tokens - 1) / tokens;
+  int64_t tiles = token_tiles * p.row_tiles;
+  if (tiles < 1) tiles = 1;  // the status word alone
+  if (a.nvfp4)
+    return gated ? launch_typed<true, true>(x_map, w_map, p, tiles, stream)
+                 : launch_typed<true, false>(x_map, w_map, p, tiles, stream);
+  return gated ? launch_typed<false, true>(x_map, w_map, p, tiles, stream)
+               : launch_typed<false, false>(x_map, w_map, p, tiles, stream);
 }
 
 #ifdef MXFP4_DEBUG_BOUNDS

@@ -1,0 +1,168 @@
+// tensor_core.cuh — the PTX of sm_103a's fifth-generation tensor cores that the
+// products of 4-bit operands use (gemm.cu): tensor memory, block-scaled
+// tcgen05.mma, the bulk copies that feed them and the barriers between.
+#pragma once
+
+#include <cstdint>
+
+namespace mxfp4 {
+namespace tc {
+
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+// ---------------------------------------------------------------- barriers
+__device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t arrivals) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(arrivals) : "memory");
+}
+__device__ __forceinline__ void barrier_init_fence() {
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void barrier_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ uint64_t nanoseconds() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+// Waits for the phase of `parity`; gives up, and says so to the CTA by
+// `gave_up`, after two seconds or when another thread has.
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  if (barrier_try(bar, parity)) return true;
+  const uint64_t start = nanoseconds();
+  for (uint32_t i = 1;; ++i) {
+    if (barrier_try(bar, parity)) return true;
+    if ((i & 63u) == 0 && (*gave_up || nanoseconds() - start > 2000000000ull)) break;
+  }
+  *gave_up = 1;
+  return false;
+}
+
+// ------------------------------------------------------------------- copies
+// A box of a tensor map's rows to shared memory; x in elements of the map.
+__device__ __forceinline__ void copy_box(uint32_t dst, const void* map, int32_t x, int32_t y,
+                                         uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// Consecutive bytes (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32_t bytes,
+                                           uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const void* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+// What this thread wrote to shared memory is seen by copies and tensor cores.
+__device__ __forceinline__ void fence_async() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ----------------------------------------------------------- tensor memory
+// A whole warp allocates, and frees, `columns` columns of 128 lanes by 32 bits.
+__device__ __forceinline__ void allocate(uint32_t address_at, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(address_at),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void release(uint32_t address, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(address), "r"(columns) : "memory");
+}
+__device__ __forceinline__ void fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+// 32 columns of the warp's quarter of the lanes: a lane's 32 words.
+__device__ __forceinline__ void load32(uint32_t address, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(address));
+}
+__device__ __forceinline__ void load_wait() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// ------------------------------------------------------------- descriptors
+// Rows of 128 bytes (256 E2M1 codes) as a copy with the 128-byte swizzle lays
+// them: groups of 8 rows, 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand_descriptor(uint32_t address) {
+  return static_cast<uint64_t>((address >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// 512 bytes of scales, 32 rows of 16 bytes: groups of 8 rows, 128 bytes apart.
+__device__ __forceinline__ uint64_t scales_descriptor(uint32_t address) {
+  return static_cast<uint64_t>((address >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
+}
+// E2M1 by E2M1 with float32 sums, both along K; M = 128, N columns; E8M0 or
+// E4M3 scales.
+__device__ __forceinline__ uint32_t instruction(uint32_t columns, bool e4m3) {
+  return (1u << 7) | (1u << 10) | ((columns >> 3) << 17) | (e4m3 ? 0u : 1u << 23) | ((128u >> 4) << 24);
+}
+// ... with the scales that begin at byte `id` of their words.
+__device__ __forceinline__ uint32_t with_scale_byte(uint32_t instruction, uint32_t id) {
+  return instruction | (id << 4) | (id << 29);
+}
+
+// 128 rows' scales (512 bytes) to four columns of all four lane quarters.
+__device__ __forceinline__ void copy_scales(uint32_t address, uint64_t from) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(address), "l"(from) : "memory");
+}
+// 64 elements of K.  One thread issues these and copy_scales; they take effect
+// in its order.
+template <bool kE4m3>
+__device__ __forceinline__ void multiply(uint32_t sums, uint64_t a, uint64_t b, uint32_t instruction,
+                                         uint32_t a_scales, uint32_t b_scales, bool add) {
+  if constexpr (kE4m3)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(sums), "l"(a), "l"(b), "r"(instruction),
+        "r"(a_scales), "r"(b_scales), "r"(static_cast<uint32_t>(add))
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(sums), "l"(a), "l"(b), "r"(instruction),
+        "r"(a_scales), "r"(b_scales), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+// Arrives at `bar` when all that this thread issued before has been done.
+__device__ __forceinline__ void arrive_when_done(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+}  // namespace tc
+}  // namespace mxfp4
