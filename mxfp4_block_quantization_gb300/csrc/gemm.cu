@@ -14,13 +14,15 @@
 // epilogue.  256 bytes of K at a time (a stage) are 16 KB for each 128 rows.
 //
 // Warp 0 copies stages ahead (TMA, a ring of four), one thread of warp 1 issues
-// the scales' copies and the products, warps 4 to 11 take the sums from tensor
+// the scales' copies and the products, warp 2 mends scales where a half of gated
+// weights or K end inside of their tiles, warps 4 to 11 take the sums from tensor
 // memory into registers, which frees it for the next tile, and finish them.  Each
 // CTA walks every gridDim-th tile.  Where tiles are few, a cluster of up to 8 CTAs
 // shares a tile, each with a part of K, and adds the parts in rank order through
 // distributed shared memory: equal calls give equal bits.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -45,10 +47,10 @@ constexpr int kStageBytes = 128;               // of a row's codes: 256 elements
 constexpr int kSlab = kRows * kStageBytes;     // 16 KB
 constexpr int kSlabs = 3;
 constexpr int kSteps = 4;                      // products of 64 elements to a stage
-constexpr int kBoxRows = 32;                   // tokens' rows to a copy
 constexpr int kFinished = 32;                  // tokens that a thread finishes at a time
-constexpr int kColumns = 512;                  // all of tensor memory
-// tensor memory: sums, then the scales of both weight tiles and of the tokens
+constexpr int kColumns = 512;
+// tensor memory, all of which a CTA has (so that it begins at column 0): sums, then
+// the scales of both weight tiles and of the tokens
 constexpr uint32_t kScalesA = 256, kScalesB = 288;
 
 // A stage's scales of 128 rows: two chunks of 512 bytes (four with NVFP4), for
@@ -90,9 +92,9 @@ struct GemmParams {
   int32_t stages;           // stages along K
   int32_t blocks;           // scales of a row
   int32_t row_tiles;        // tiles of the weights' rows
+  int32_t box_rows;         // tokens' rows to a copy
   int32_t activation;
   bool gate_second;
-  bool f16;
   bool paired;              // two columns of y in one store
 #ifdef MXFP4_DEBUG_BOUNDS
   DebugRanges dbg;
@@ -163,18 +165,20 @@ struct Walk {
 };
 
 struct Barriers {
-  uint64_t full[kStages], empty[kStages], sums_full, sums_empty, drained;
+  uint64_t full[kStages], mended[kStages], empty[kStages], sums_full, sums_empty, drained;
   uint32_t columns;  // tensor memory's address
   int gave_up;
 };
 
 // --------------------------------------------------------------- epilogue
-__device__ __forceinline__ float widen(uint16_t v, bool f16) {
-  return f16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
+template <bool kF16>
+__device__ __forceinline__ float widen(uint16_t v) {
+  return kF16 ? __half2float(__ushort_as_half(v)) : __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
 // Two values as halves of y's type, `lo` in the low half.
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi, bool f16) {
-  return f16 ? pack_f16x2(lo, hi) : cvt_bf16x2(lo, hi);
+template <bool kF16>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+  return kF16 ? pack_f16x2(lo, hi) : cvt_bf16x2(lo, hi);
 }
 
 // By the fast exponential and division: off by 2^-21 of |z| (see pick32 in
@@ -188,8 +192,21 @@ __device__ __forceinline__ void activate(float* z, int act) {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) z[j] = sigmoid_times(z[j], z[j]);
   } else if (act == MXFP4_ACT_GELU) {
+    // erfc(x) = t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) e^(-x^2), t = 1 / (1 + p x),
+    // x >= 0, off by 1.5e-7 at most (Abramowitz and Stegun, 7.1.26): the smaller
+    // of the two halves of z is made, the larger is what is left of z
 #pragma unroll
-    for (int j = 0; j < kCount; ++j) z[j] = 0.5f * z[j] * (1.0f + erff(z[j] * 0.70710678118654752f));
+    for (int j = 0; j < kCount; ++j) {
+      const float x = fabsf(z[j]) * 0.70710678118654752f;
+      const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+      float q = fmaf(t, 1.061405429f, -1.453152027f);
+      q = fmaf(t, q, 1.421413741f);
+      q = fmaf(t, q, -0.284496736f);
+      q = fmaf(t, q, 0.254829592f);
+      q *= t * __expf(-x * x);
+      const float tail = q > 0.0f ? 0.5f * z[j] * q : 0.0f;  // of infinite z as well
+      z[j] = z[j] < 0.0f ? tail : z[j] - tail;
+    }
   } else if (act == MXFP4_ACT_GELU_TANH) {
     // 0.5 (1 + tanh(v)) = 1 / (1 + e^-2v)
 #pragma unroll
@@ -202,7 +219,7 @@ __device__ __forceinline__ void activate(float* z, int act) {
 struct RowTerms {
   float alpha, bias, other_bias;  // `other`: of the second half
 };
-template <bool kNv, bool kGated>
+template <bool kNv, bool kGated, bool kF16>
 __device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t, int n) {
   RowTerms r{1.0f, 0.0f, 0.0f};
   if constexpr (kNv) {
@@ -214,10 +231,10 @@ __device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t
   }
   if (p.bias != nullptr && n < p.cols) {
     const uint16_t* at = p.bias + static_cast<int64_t>(t.e) * p.N + n;
-    r.bias = MXFP4_IN_BOUNDS(p, kDbgBias, at, 2) ? widen(__ldg(at), p.f16) : 0.0f;
+    r.bias = MXFP4_IN_BOUNDS(p, kDbgBias, at, 2) ? widen<kF16>(__ldg(at)) : 0.0f;
     if (kGated) {
       at += p.cols;
-      r.other_bias = MXFP4_IN_BOUNDS(p, kDbgBias, at, 2) ? widen(__ldg(at), p.f16) : 0.0f;
+      r.other_bias = MXFP4_IN_BOUNDS(p, kDbgBias, at, 2) ? widen<kF16>(__ldg(at)) : 0.0f;
     }
   }
   return r;
@@ -225,7 +242,7 @@ __device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t
 
 // kCount tokens from column c of the tile on (u: the second half's sums) of the
 // thread's column n of y: finished in place.
-template <bool kGated, int kCount = kFinished>
+template <bool kGated, bool kF16, int kCount = kFinished>
 __device__ __forceinline__ void finish(const GemmParams& p, const Tile& t, const RowTerms& r, int n,
                                        int c, float* v, float* u) {
 #pragma unroll
@@ -241,17 +258,22 @@ __device__ __forceinline__ void finish(const GemmParams& p, const Tile& t, const
     activate<kCount>(v, p.activation);
   }
   if (p.residual != nullptr) {
+    // may be y: plain loads, of what this thread alone writes; all of them before
+    // the first is used
     const uint16_t* at = p.residual + (t.row + c) * p.ldr + n;
+    uint16_t r[kCount];
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
-      // may be y: a plain load, of what this thread alone writes
-      if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) v[j] += widen(*at, p.f16);
+      r[j] = 0;
+      if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) r[j] = *at;
       at += p.ldr;
     }
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) v[j] += widen<kF16>(r[j]);
   }
 }
 
-template <int kCount = kFinished>
+template <bool kF16, int kCount = kFinished>
 __device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n, int c,
                                       const float* v) {
   if (p.paired) {
@@ -260,7 +282,7 @@ __device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n,
     uint16_t* at = p.y + (t.row + c + odd) * p.ldy + (n & ~1);
 #pragma unroll
     for (int j = 0; j < kCount; j += 2) {
-      const uint32_t mine = narrow2(v[j], v[j + 1], p.f16);
+      const uint32_t mine = narrow2<kF16>(v[j], v[j + 1]);
       const uint32_t next = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
       const uint32_t word = odd ? __byte_perm(mine, next, 0x3276) : __byte_perm(mine, next, 0x5410);
       if (c + j + odd < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 4))
@@ -272,7 +294,7 @@ __device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n,
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
       if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2))
-        *at = static_cast<uint16_t>(narrow2(v[j], 0.0f, p.f16));
+        *at = static_cast<uint16_t>(narrow2<kF16>(v[j], 0.0f));
       at += p.ldy;
     }
   }
@@ -315,7 +337,7 @@ __device__ void mend_scales(uint32_t scales, int tiles, int moved, int shift, in
 }
 
 // --------------------------------------------------------------- the kernel
-template <bool kNv, bool kGated>
+template <bool kNv, bool kGated, bool kF16>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap w_map,
                 const GemmParams p) {
@@ -325,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem[];
   __shared__ Barriers bars;
   __shared__ int s_bad;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t ring = (tc::shared_address(smem) + 1023u) & ~1023u;
   const auto bar = [](const uint64_t& b) { return tc::shared_address(&b); };
   uint32_t ranks;
@@ -337,7 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k_end = static_cast<int>(static_cast<int64_t>(p.stages) * (rank + 1) / ranks);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) tc::barrier_init(bar(bars.full[s]), 1), tc::barrier_init(bar(bars.empty[s]), 1);
+    for (int s = 0; s < kStages; ++s) {
+      tc::barrier_init(bar(bars.full[s]), 1);
+      tc::barrier_init(bar(bars.mended[s]), 1);
+      tc::barrier_init(bar(bars.empty[s]), 1);
+    }
     tc::barrier_init(bar(bars.sums_full), 1);
     tc::barrier_init(bar(bars.sums_empty), kEpilogueThreads);
     tc::barrier_init(bar(bars.drained), 1);
@@ -350,7 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t columns = *static_cast<volatile uint32_t*>(&bars.columns);
   volatile int* const gave_up = &bars.gave_up;
   pdl_wait();
   pdl_release();
@@ -368,6 +393,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // the second half's rows begin at row `shift` of a tile of the scales
   const int shift = kGated ? p.cols & (kRows - 1) : 0;
+  // a product's 64 elements of K go past the last scale
+  const bool tail = (p.blocks & (kNv ? 3 : 1)) != 0;
+  const bool mended = shift != 0 || tail;
 
   Walk<kTokens> walk;
   Tile t;
@@ -378,44 +406,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, wrapped = false;
     for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step) {
       if (lane == 0) {
-        const int boxes = (t.n + kBoxRows - 1) / kBoxRows;
-        const uint8_t* const ws = p.scales + t.e * p.expert_scales;
+        const int boxes = (t.n + p.box_rows - 1) / p.box_rows;
+        const uint32_t box_bytes = p.box_rows * kStageBytes;
         const int w_row = t.e * p.N + t.r0;
-        const int upper = (p.cols + t.r0) / kRows;  // the second half's tile of scales
+        // the tiles' scales: of the weights (both halves'), of the tokens, and of the
+        // tile behind the second half's first where it does not begin at a tile and
+        // is not the last
+        const int64_t row_bytes = static_cast<int64_t>(p.nKT) * 512;
+        const uint8_t* const ws = p.scales + t.e * p.expert_scales + static_cast<int64_t>(k_begin) * L::kScales;
+        const uint8_t* const xs = p.x_scales + t.padded / kRows * row_bytes + static_cast<int64_t>(k_begin) * L::kScales;
+        const int upper = (p.cols + t.r0) / kRows;
+        const uint8_t* src[4] = {ws + t.r0 / kRows * row_bytes, kGated ? ws + upper * row_bytes : xs,
+                                 kGated ? xs : xs + row_bytes, ws + (upper + 1) * row_bytes};
+        const bool third = kGated || t.n > kRows;
+        const bool fourth = kGated && shift != 0 && (upper + 1) * kRows < p.N;
+        const uint32_t code_bytes = kWeightSlabs * kSlab + boxes * box_bytes;
+        const uint32_t scale_tiles = 2 + third + fourth;
         for (int k = k_begin; k < k_end; ++k) {
           if (wrapped && !(ok = tc::barrier_wait(bar(bars.empty[stage]), phase ^ 1u, gave_up))) break;
           const uint32_t at = ring + stage * L::kStage, sc = at + kSlabs * kSlab, full = bar(bars.full[stage]);
-          const int chunks = min(L::kChunks, p.nKT - k * L::kChunks);
-          const uint32_t bytes = chunks * 512;
-          const int64_t row_bytes = static_cast<int64_t>(p.nKT) * 512, from = static_cast<int64_t>(k) * L::kScales;
-          const uint8_t* src[4] = {ws + t.r0 / kRows * row_bytes + from, nullptr, nullptr, nullptr};
-          const uint8_t* const xs = p.x_scales + t.padded / kRows * row_bytes + from;
-          if constexpr (kGated) {
-            src[1] = ws + upper * row_bytes + from;
-            src[2] = xs;
-            // the last tile of the scales may be the weights' last
-            if (shift != 0 && (upper + 1) * kRows < (p.N + kRows - 1) / kRows * kRows) src[3] = src[1] + row_bytes;
-          } else {
-            src[1] = xs;
-            if (t.n > kRows) src[2] = xs + row_bytes;
-          }
-          uint32_t scale_bytes = 0;
+          const uint32_t bytes = min(L::kChunks, p.nKT - k * L::kChunks) * 512;
+#ifdef MXFP4_DEBUG_BOUNDS
+          uint32_t copied = 0;
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            if (src[s] != nullptr &&
-                !MXFP4_IN_BOUNDS(p, (kGated ? s == 2 : s > 0) ? kDbgXScales : kDbgScales, src[s], bytes))
-              src[s] = nullptr;
-            if (src[s] != nullptr) scale_bytes += bytes;
-          }
-          tc::barrier_expect(full, kWeightSlabs * kSlab + boxes * (kBoxRows * kStageBytes) + scale_bytes);
+          for (int s = 0; s < 4; ++s)
+            if (s < 2 || (s == 2 && third) || (s == 3 && fourth))
+              copied += MXFP4_IN_BOUNDS(p, (kGated ? s == 2 : s > 0) ? kDbgXScales : kDbgScales, src[s], bytes) ? bytes : 0;
+          tc::barrier_expect(full, code_bytes + copied);
+          const bool whole = copied == scale_tiles * bytes;
+#else
+          tc::barrier_expect(full, code_bytes + scale_tiles * bytes);
+          constexpr bool whole = true;
+#endif
           const int x = k * kStageBytes;
           tc::copy_box(at, &w_map, x, w_row, full);
           if constexpr (kGated) tc::copy_box(at + kSlab, &w_map, x, w_row + p.cols, full);
           for (int b = 0; b < boxes; ++b)
-            tc::copy_box(at + kWeightSlabs * kSlab + b * (kBoxRows * kStageBytes), &x_map, x, t.row + b * kBoxRows, full);
+            tc::copy_box(at + kWeightSlabs * kSlab + b * box_bytes, &x_map, x, t.row + b * p.box_rows, full);
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
-            if (src[s] != nullptr) tc::copy_bytes(sc + s * L::kScales, src[s], bytes, full);
+          for (int s = 0; s < 4; ++s) {
+            if ((s < 2 || (s == 2 && third) || (s == 3 && fourth)) && whole)
+              tc::copy_bytes(sc + s * L::kScales, src[s], bytes, full);
+            src[s] += L::kScales;
+          }
           if (++stage == kStages) stage = 0, phase ^= 1u, wrapped = true;
         }
       }
@@ -434,78 +467,96 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
-    uint32_t stage = 0, phase = 0, sums_phase = 0;
-    bool ok = true, again = false;
+    // One thread issues them, and its instructions are their pace: all it takes is
+    // uniform over the tile's loop.
+    uint32_t count = 0, tiles = 0;
+    bool ok = true, issued = false;
     for (int i = first_tile; ok && k_begin < k_end && walk.find(p, i, t); i += tile_step) {
-      const uint32_t inst = tc::instruction((t.n + 15) / 16 * 16, kNv);
-      if (again) {  // the sums of the tile before have been taken
-        ok = tc::barrier_wait(bar(bars.sums_empty), sums_phase, gave_up);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        sums_phase ^= 1u;
-        tc::fence_after();
-        if (!ok) break;
-      }
-      again = true;
-      for (int k = k_begin; k < k_end; ++k) {
-        ok = tc::barrier_wait(bar(bars.full[stage]), phase, gave_up);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc::fence_after();
-        const uint32_t at = ring + stage * L::kStage, sc = at + kSlabs * kSlab;
-        const int steps = min(kSteps, p.steps - k * kSteps);
-        const int keep = k == p.stages - 1 && (p.blocks & (kNv ? 3 : 1)) ? p.blocks - k * L::kChunks * 4 : -1;
-        if (shift != 0 || keep >= 0) mend_scales<kNv>(sc, 3, 1, shift, keep);
-        if (lane == 0) {
-          const uint64_t a = tc::operand_descriptor(at), b = tc::operand_descriptor(at + kWeightSlabs * kSlab);
-          const uint64_t s0 = tc::scales_descriptor(sc);
-          constexpr uint64_t kTile = L::kScales / 16;  // a tile's scales, in descriptors' units
-          const int chunks = min(L::kChunks, p.nKT - k * L::kChunks);
-          for (int c = 0; c < chunks; ++c) {
-            tc::copy_scales(columns + kScalesA + c * 4, s0 + c * 32);
+      if (tc::elected()) {
+        issued = true;
+        const uint32_t inst = tc::instruction((t.n + 15) / 16 * 16, kNv), inst_odd = tc::with_scale_byte(inst, 2);
+        const bool wide = t.n > kRows;
+        // the sums of the tile before have been taken
+        if (tiles > 0) {
+          ok = tc::barrier_wait(bar(bars.sums_empty), (tiles - 1) & 1u, gave_up);
+          tc::fence_after();
+        }
+        uint32_t stage = count % kStages, phase = count / kStages & 1u;
+        for (int k = k_begin; ok && k < k_end; ++k) {
+          ok = tc::barrier_wait(mended ? bar(bars.mended[stage]) : bar(bars.full[stage]), phase, gave_up);
+          if (!ok) break;
+          tc::fence_after();
+          const uint32_t at = ring + stage * L::kStage;
+          const uint32_t a = tc::operand_low(at), b = a + kWeightSlabs * kSlab / 16;
+          const uint32_t s0 = tc::scales_low(at + kSlabs * kSlab);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c) {  // (past the last chunk: what no product uses)
+            constexpr uint32_t kTile = L::kScales / 16;  // a tile's scales
+            const auto from = [&](int tile) { return tc::descriptor(s0 + tile * kTile + c * 32, tc::kScalesHigh); };
+            tc::copy_scales(kScalesA + c * 4, from(0));
             if constexpr (kGated) {
-              tc::copy_scales(columns + kScalesA + 16 + c * 4, s0 + kTile + c * 32);
-              tc::copy_scales(columns + kScalesB + c * 4, s0 + 2 * kTile + c * 32);
+              tc::copy_scales(kScalesA + 16 + c * 4, from(1));
+              tc::copy_scales(kScalesB + c * 4, from(2));
             } else {
-              tc::copy_scales(columns + kScalesB + c * 8, s0 + kTile + c * 32);
-              if (t.n > kRows) tc::copy_scales(columns + kScalesB + c * 8 + 4, s0 + 2 * kTile + c * 32);
+              tc::copy_scales(kScalesB + c * 8, from(1));
+              if (wide) tc::copy_scales(kScalesB + c * 8 + 4, from(2));
             }
           }
+          const int steps = p.steps - k * kSteps;
           constexpr int kStride = kGated ? 4 : 8;  // the tokens' columns of a chunk
-          for (int s = 0; s < steps; ++s) {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {
+            if (s >= steps) continue;
             const int c = kNv ? s : s >> 1;
-            const uint32_t in = kNv ? inst : tc::with_scale_byte(inst, 2u * (s & 1));
-            const bool add = k > k_begin || s > 0;
-            tc::multiply<kNv>(columns, a + 2 * s, b + 2 * s, in, columns + kScalesA + c * 4,
-                              columns + kScalesB + c * kStride, add);
+            const uint32_t in = kNv || (s & 1) == 0 ? inst : inst_odd;
+            const bool add = s > 0 || k > k_begin;
+            const uint64_t bd = tc::descriptor(b + 2 * s, tc::kOperandHigh);
+            tc::multiply<kNv>(0, tc::descriptor(a + 2 * s, tc::kOperandHigh), bd, in, kScalesA + c * 4,
+                              kScalesB + c * kStride, add);
             if constexpr (kGated)
-              tc::multiply<kNv>(columns + 128, a + kSlab / 16 + 2 * s, b + 2 * s, in,
-                                columns + kScalesA + 16 + c * 4, columns + kScalesB + c * kStride, add);
+              tc::multiply<kNv>(128, tc::descriptor(a + kSlab / 16 + 2 * s, tc::kOperandHigh), bd, in,
+                                kScalesA + 16 + c * 4, kScalesB + c * kStride, add);
           }
           tc::arrive_when_done(bar(bars.empty[stage]));
-          if (k == k_end - 1) tc::arrive_when_done(bar(bars.sums_full));
+          if (++stage == kStages) stage = 0, phase ^= 1u;
         }
-        __syncwarp();
-        if (++stage == kStages) stage = 0, phase ^= 1u;
+        if (ok) tc::arrive_when_done(bar(bars.sums_full));
       }
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      count += k_end - k_begin;
+      ++tiles;
     }
     if (*gave_up) {  // what was issued is done before tensor memory is freed
       int none = 0;
-      if (lane == 0) {
+      if (issued) {
         tc::arrive_when_done(bar(bars.drained));
         tc::barrier_wait(bar(bars.drained), 0, &none);
       }
       __syncwarp();
     }
+  } else if (warp == 2) {
+    // ------------------------------------- scales that do not lie as they should
+    uint32_t count = 0;
+    bool ok = mended;
+    for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step)
+      for (int k = k_begin; ok && k < k_end; ++k, ++count) {
+        const uint32_t stage = count % kStages;
+        ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.full[stage]), count / kStages & 1u, gave_up));
+        if (!ok) break;
+        const int keep = k == p.stages - 1 && tail ? p.blocks - k * L::kChunks * 4 : -1;
+        if (shift != 0 || keep >= 0) mend_scales<kNv>(ring + stage * L::kStage + kSlabs * kSlab, 3, 1, shift, keep);
+        if (lane == 0) tc::barrier_arrive(bar(bars.mended[stage]));
+      }
   } else if (warp >= kFirstEpilogue) {
     // ---------------------------------------------------------- epilogue
     const int half = (warp - kFirstEpilogue) >> 2, quarter = warp & 3;
-    const uint32_t from = columns + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t from = static_cast<uint32_t>(quarter * 32) << 16;
     const int row = quarter * 32 + lane;     // of the tile
     uint32_t sums_phase = 0;
     bool ok = true;
     for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step) {
       const int n = t.r0 + row;
-      const RowTerms terms = row_terms<kNv, kGated>(p, t, n);
+      const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
       if (k_begin < k_end) {
         ok = tc::barrier_wait(bar(bars.sums_full), sums_phase, gave_up);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -537,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kGated) part[(kTokens + column + j) * kRows + row] = u[j];
           }
         } else {
-          finish<kGated>(p, t, terms, n, column, v, u);
-          store(p, t, n, column, v);
+          finish<kGated, kF16>(p, t, terms, n, column, v, u);
+          store<kF16>(p, t, n, column, v);
         }
       }
       tc::fence_before();
@@ -553,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (mine && walk.find(p, first_tile, t)) {
       // each rank finishes every ranks-th token, its two halves every other of those
       const int thread = threadIdx.x - kFirstEpilogue * 32, row = thread & (kRows - 1), n = t.r0 + row;
-      const RowTerms terms = row_terms<kNv, kGated>(p, t, n);
+      const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
       for (int c = rank + ranks * (thread >> 7); c < t.n; c += 2 * ranks) {
         float v[1] = {0.0f}, u[1] = {0.0f};
         for (uint32_t r = 0; r < ranks; ++r) {
@@ -566,9 +617,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             u[0] += a;
           }
         }
-        finish<kGated, 1>(p, t, terms, n, c, v, u);
+        finish<kGated, kF16, 1>(p, t, terms, n, c, v, u);
         uint16_t* const at = p.y + (t.row + c) * p.ldy + n;
-        if (n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2)) *at = static_cast<uint16_t>(narrow2(v[0], 0.0f, p.f16));
+        if (n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2)) *at = static_cast<uint16_t>(narrow2<kF16>(v[0], 0.0f));
       }
     }
     __syncwarp();
@@ -579,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after();
   if (threadIdx.x == 0 && *gave_up && p.status != nullptr && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4))
     *p.status = MXFP4_ECUDA;
-  if (warp == 1) tc::release(columns, kColumns);
+  if (warp == 1) tc::release(bars.columns, kColumns);
 }
 
 // ------------------------------------------------------------------- launch
@@ -613,18 +664,18 @@ cudaError_t map_codes(CUtensorMap* map, const uint8_t* codes, int64_t rows, int6
              : cudaErrorInvalidValue;
 }
 
-template <bool kNv, bool kGated>
+template <bool kNv, bool kGated, bool kF16>
 cudaError_t launch_typed(const CUtensorMap& x_map, const CUtensorMap& w_map, const GemmParams& p, int64_t tiles,
                          cudaStream_t stream) {
   constexpr int kBytes = Layout<kNv>::kBytes + 1024;  // to a multiple of 1024
   static std::atomic<uint64_t> ready{0};
-  if (const cudaError_t e = allow_smem(gemm_kernel<kNv, kGated>, kBytes, ready); e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem(gemm_kernel<kNv, kGated, kF16>, kBytes, ready); e != cudaSuccess) return e;
   // clusters that share a tile's K: as many CTAs as the SMs hold, a stage each
   const int64_t sms = sm_count();
   int ranks = 1;
   while (ranks < 8 && tiles * ranks * 2 <= sms && ranks * 2 <= p.stages) ranks *= 2;
   const int64_t grid = ranks > 1 ? tiles * ranks : tiles < sms ? tiles : sms;
-  return launch_pdl_cluster(gemm_kernel<kNv, kGated>, dim3(static_cast<unsigned>(grid)), kThreads, kBytes, stream,
+  return launch_pdl_cluster(gemm_kernel<kNv, kGated, kF16>, dim3(static_cast<unsigned>(grid)), kThreads, kBytes, stream,
                             ranks > 1 ? ranks : 0, x_map, w_map, p);
 }
 
@@ -656,7 +707,6 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
   p.expert_scales = (a.N + 127) / 128 * p.nKT * static_cast<int64_t>(kChunkBytes);
   p.activation = a.activation;
   p.gate_second = a.gate == MXFP4_GATE_SECOND;
-  p.f16 = a.f16;
   p.paired = p.cols % 2 == 0 && a.ldy % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0;
 #ifdef MXFP4_DEBUG_BOUNDS
   debug_range(p.dbg, kDbgXScales, a.x_scales,
@@ -670,9 +720,13 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
   debug_range(p.dbg, kDbgXGlobals, a.x_globals, a.nvfp4 ? a.E * 4 : 0);
   debug_range(p.more.dbg, kDbgGlobals, a.globals, a.nvfp4 ? a.E * 4 : 0);
 #endif
+  // Rows to a copy of x: many in one where experts have many, few where whole
+  // boxes would be other experts' rows.
+  const int64_t average = a.offsets ? a.rows / (a.E > 0 ? a.E : 1) : a.rows;
+  p.box_rows = average > 64 ? 128 : 32;
   CUtensorMap x_map{}, w_map{};
   if (a.K > 0 && a.rows > 0 && a.N > 0 && a.E > 0) {
-    if (const cudaError_t e = map_codes(&x_map, a.x_codes, a.rows, a.K, kBoxRows); e != cudaSuccess) return e;
+    if (const cudaError_t e = map_codes(&x_map, a.x_codes, a.rows, a.K, p.box_rows); e != cudaSuccess) return e;
     if (const cudaError_t e = map_codes(&w_map, a.codes, a.E * a.N, a.K, kRows); e != cudaSuccess) return e;
   }
   // at most this many tiles: every expert with rows may have one that is not full
@@ -681,11 +735,13 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
                                         : (a.rows + tokens - 1) / tokens;
   int64_t tiles = token_tiles * p.row_tiles;
   if (tiles < 1) tiles = 1;  // the status word alone
-  if (a.nvfp4)
-    return gated ? launch_typed<true, true>(x_map, w_map, p, tiles, stream)
-                 : launch_typed<true, false>(x_map, w_map, p, tiles, stream);
-  return gated ? launch_typed<false, true>(x_map, w_map, p, tiles, stream)
-               : launch_typed<false, false>(x_map, w_map, p, tiles, stream);
+  const auto launch = [&](auto nv, auto gate) {
+    return a.f16 ? launch_typed<decltype(nv)::value, decltype(gate)::value, true>(x_map, w_map, p, tiles, stream)
+                 : launch_typed<decltype(nv)::value, decltype(gate)::value, false>(x_map, w_map, p, tiles, stream);
+  };
+  using std::false_type, std::true_type;
+  if (a.nvfp4) return gated ? launch(true_type{}, true_type{}) : launch(true_type{}, false_type{});
+  return gated ? launch(false_type{}, true_type{}) : launch(false_type{}, false_type{});
 }
 
 #ifdef MXFP4_DEBUG_BOUNDS

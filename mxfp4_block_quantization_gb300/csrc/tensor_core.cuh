@@ -12,6 +12,18 @@ __device__ __forceinline__ uint32_t shared_address(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// One thread of a converged warp; what it alone runs may use uniform registers,
+// which the instructions below take their operands from.
+__device__ __forceinline__ bool elected() {
+  uint32_t yes = 0;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 lane;\n\t"
+      "elect.sync lane|p, 0xFFFFFFFF;\n\t"
+      "@p mov.u32 %0, 1;\n\t}"
+      : "+r"(yes));
+  return yes != 0;
+}
+
 // ---------------------------------------------------------------- barriers
 __device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t arrivals) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(arrivals) : "memory");
@@ -36,19 +48,17 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-__device__ __forceinline__ uint64_t nanoseconds() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
 // Waits for the phase of `parity`; gives up, and says so to the CTA by
-// `gave_up`, after two seconds or when another thread has.
+// `gave_up`, after 2^32 cycles (about two seconds) or when another thread has.
 __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  if (barrier_try(bar, parity)) return true;
-  const uint64_t start = nanoseconds();
-  for (uint32_t i = 1;; ++i) {
+  long long start = 0;
+  for (uint32_t i = 0;; ++i) {
     if (barrier_try(bar, parity)) return true;
-    if ((i & 63u) == 0 && (*gave_up || nanoseconds() - start > 2000000000ull)) break;
+    if ((i & 63u) == 63u) {
+      const long long now = clock64();
+      if (i == 63u) start = now;
+      if (*gave_up || now - start > (1ll << 32)) break;
+    }
   }
   *gave_up = 1;
   return false;
@@ -115,15 +125,17 @@ __device__ __forceinline__ void load_wait() {
 }
 
 // ------------------------------------------------------------- descriptors
-// Rows of 128 bytes (256 E2M1 codes) as a copy with the 128-byte swizzle lays
-// them: groups of 8 rows, 1024 bytes apart.
-__device__ __forceinline__ uint64_t operand_descriptor(uint32_t address) {
-  return static_cast<uint64_t>((address >> 4) & 0x3FFFu) | (1ull << 16) | (64ull << 32) |
-         (1ull << 46) | (2ull << 61);
-}
-// 512 bytes of scales, 32 rows of 16 bytes: groups of 8 rows, 128 bytes apart.
-__device__ __forceinline__ uint64_t scales_descriptor(uint32_t address) {
-  return static_cast<uint64_t>((address >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
+// The low words of shared memory descriptors, which step with the address (in
+// units of 16 bytes), and the constant high words.
+// Operands: rows of 128 bytes (256 E2M1 codes) as a copy with the 128-byte
+// swizzle lays them, groups of 8 rows 1024 bytes apart.
+__device__ __forceinline__ uint32_t operand_low(uint32_t address) { return (address >> 4) | (1u << 16); }
+constexpr uint32_t kOperandHigh = 64u | (1u << 14) | (2u << 29);
+// Scales: 512 bytes, 32 rows of 16, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint32_t scales_low(uint32_t address) { return address >> 4; }
+constexpr uint32_t kScalesHigh = 8u | (1u << 14);
+__device__ __forceinline__ uint64_t descriptor(uint32_t low, uint32_t high) {
+  return static_cast<uint64_t>(high) << 32 | low;
 }
 // E2M1 by E2M1 with float32 sums, both along K; M = 128, N columns; E8M0 or
 // E4M3 scales.
