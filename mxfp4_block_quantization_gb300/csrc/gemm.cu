@@ -47,7 +47,6 @@ constexpr int kStageBytes = 128;               // of a row's codes: 256 elements
 constexpr int kSlab = kRows * kStageBytes;     // 16 KB
 constexpr int kSlabs = 3;
 constexpr int kSteps = 4;                      // products of 64 elements to a stage
-constexpr int kFinished = 32;                  // tokens that a thread finishes at a time
 constexpr int kColumns = 512;
 // tensor memory, all of which a CTA has (so that it begins at column 0): sums, then
 // the scales of both weight tiles and of the tokens
@@ -95,7 +94,8 @@ struct GemmParams {
   int32_t box_rows;         // tokens' rows to a copy
   int32_t activation;
   bool gate_second;
-  bool paired;              // two columns of y in one store
+  bool paired;              // rows of y lie in whole words
+  bool paired_residual;
 #ifdef MXFP4_DEBUG_BOUNDS
   DebugRanges dbg;
 #endif
@@ -187,7 +187,7 @@ __device__ __forceinline__ float sigmoid_times(float z, float u) {  // z / (1 + 
   return __fdividef(z, 1.0f + __expf(-u));
 }
 template <int kCount>
-__device__ __forceinline__ void activate(float* z, int act) {
+__device__ __forceinline__ void activate(float (&z)[kCount], int act) {
   if (act == MXFP4_ACT_SILU) {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) z[j] = sigmoid_times(z[j], z[j]);
@@ -240,61 +240,95 @@ __device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t
   return r;
 }
 
-// kCount tokens from column c of the tile on (u: the second half's sums) of the
-// thread's column n of y: finished in place.
-template <bool kGated, bool kF16, int kCount = kFinished>
-__device__ __forceinline__ void finish(const GemmParams& p, const Tile& t, const RowTerms& r, int n,
-                                       int c, float* v, float* u) {
+// kCount tokens' sums v (u: the second half's) finished in place, but for the residual.
+template <bool kGated, int kCount>
+__device__ __forceinline__ void finish(const GemmParams& p, const RowTerms& r, float (&v)[kCount],
+                                       float (&u)[kCount]) {
 #pragma unroll
   for (int j = 0; j < kCount; ++j) v[j] = fmaf(v[j], r.alpha, r.bias);
   if constexpr (kGated) {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) u[j] = fmaf(u[j], r.alpha, r.other_bias);
-    if (p.gate_second) activate<kCount>(u, p.activation);
-    else activate<kCount>(v, p.activation);
+    if (p.gate_second) activate(u, p.activation);
+    else activate(v, p.activation);
 #pragma unroll
     for (int j = 0; j < kCount; ++j) v[j] *= u[j];
   } else {
-    activate<kCount>(v, p.activation);
-  }
-  if (p.residual != nullptr) {
-    // may be y: plain loads, of what this thread alone writes; all of them before
-    // the first is used
-    const uint16_t* at = p.residual + (t.row + c) * p.ldr + n;
-    uint16_t r[kCount];
-#pragma unroll
-    for (int j = 0; j < kCount; ++j) {
-      r[j] = 0;
-      if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) r[j] = *at;
-      at += p.ldr;
-    }
-#pragma unroll
-    for (int j = 0; j < kCount; ++j) v[j] += widen<kF16>(r[j]);
+    activate(v, p.activation);
   }
 }
 
-template <bool kF16, int kCount = kFinished>
-__device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n, int c,
-                                      const float* v) {
-  if (p.paired) {
-    // neighbours exchange, so that each stores two columns of every other token
-    const bool odd = n & 1;
-    uint16_t* at = p.y + (t.row + c + odd) * p.ldy + (n & ~1);
+// A thread's 32 tokens of column n from column c of the tile on, two tokens to a
+// word.  Where rows lie in whole words, neighbours share the copies: each takes
+// both their columns of every other token, and they exchange.  `whole`: none of
+// the warp's tokens and columns is outside.
+__device__ __forceinline__ uint32_t exchange(uint32_t mine, int odd) {
+  return __byte_perm(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1), odd ? 0x3276 : 0x5410);
+}
+__device__ __forceinline__ bool whole_chunk(const GemmParams& p, const Tile& t, int c) {
+  return c + 32 <= t.n && t.r0 + kRows <= p.cols;
+}
+// The residual as loaded (plain loads: it may be y, of which these are read before
+// they are written, by this warp alone), and added.
+__device__ __forceinline__ void load_residual(const GemmParams& p, const Tile& t, int n, int c,
+                                              uint32_t (&r)[16]) {
+  if (p.paired_residual) {
+    const int odd = n & 1;
+    const uint16_t* at = p.residual + (t.row + c + odd) * p.ldr + (n & ~1);
+    const bool whole = whole_chunk(p, t, c);
 #pragma unroll
-    for (int j = 0; j < kCount; j += 2) {
-      const uint32_t mine = narrow2<kF16>(v[j], v[j + 1]);
-      const uint32_t next = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
-      const uint32_t word = odd ? __byte_perm(mine, next, 0x3276) : __byte_perm(mine, next, 0x5410);
-      if (c + j + odd < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 4))
-        *reinterpret_cast<uint32_t*>(at) = word;
-      at += 2 * p.ldy;
+    for (int j = 0; j < 16; ++j) {
+      r[j] = 0;
+      if ((whole || (c + 2 * j + odd < t.n && n < p.cols)) && MXFP4_IN_BOUNDS(p, kDbgResidual, at + 2 * j * p.ldr, 4))
+        r[j] = *reinterpret_cast<const uint32_t*>(at + 2 * j * p.ldr);
+    }
+  } else {
+    const uint16_t* at = p.residual + (t.row + c) * p.ldr + n;
+    uint16_t h[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      h[j] = 0;
+      if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) h[j] = *at;
+      at += p.ldr;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; ++j) r[j] = h[2 * j] | static_cast<uint32_t>(h[2 * j + 1]) << 16;
+  }
+}
+template <bool kF16>
+__device__ __forceinline__ void add_residual(const GemmParams& p, int n, const uint32_t (&r)[16], float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const uint32_t w = p.paired_residual ? exchange(r[j], n & 1) : r[j];
+    v[2 * j] += widen<kF16>(static_cast<uint16_t>(w));
+    v[2 * j + 1] += widen<kF16>(static_cast<uint16_t>(w >> 16));
+  }
+}
+__device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n, int c, const uint32_t (&w)[16]) {
+  if (p.paired) {
+    const int odd = n & 1;
+    uint16_t* at = p.y + (t.row + c + odd) * p.ldy + (n & ~1);
+    if (whole_chunk(p, t, c)) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t word = exchange(w[j], odd);
+        if (MXFP4_IN_BOUNDS(p, kDbgY, at + 2 * j * p.ldy, 4)) *reinterpret_cast<uint32_t*>(at + 2 * j * p.ldy) = word;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t word = exchange(w[j], odd);
+        if (c + 2 * j + odd < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 4))
+          *reinterpret_cast<uint32_t*>(at) = word;
+        at += 2 * p.ldy;
+      }
     }
   } else {
     uint16_t* at = p.y + (t.row + c) * p.ldy + n;
 #pragma unroll
-    for (int j = 0; j < kCount; ++j) {
+    for (int j = 0; j < 32; ++j) {
       if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2))
-        *at = static_cast<uint16_t>(narrow2<kF16>(v[j], 0.0f));
+        *at = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
       at += p.ldy;
     }
   }
@@ -402,10 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!work) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ copies
-    uint32_t stage = 0, phase = 0;
-    bool ok = true, wrapped = false;
+    uint32_t count = 0, copied = 0;
+    bool ok = true, copier = false;
     for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step) {
-      if (lane == 0) {
+      if (tc::elected()) {
         const int boxes = (t.n + p.box_rows - 1) / p.box_rows;
         const uint32_t box_bytes = p.box_rows * kStageBytes;
         const int w_row = t.e * p.N + t.r0;
@@ -422,22 +456,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool fourth = kGated && shift != 0 && (upper + 1) * kRows < p.N;
         const uint32_t code_bytes = kWeightSlabs * kSlab + boxes * box_bytes;
         const uint32_t scale_tiles = 2 + third + fourth;
-        for (int k = k_begin; k < k_end; ++k) {
-          if (wrapped && !(ok = tc::barrier_wait(bar(bars.empty[stage]), phase ^ 1u, gave_up))) break;
+        uint32_t stage = count % kStages, phase = count / kStages & 1u, n = count;
+        for (int k = k_begin; k < k_end; ++k, ++n) {
+          if (n >= kStages && !(ok = tc::barrier_wait(bar(bars.empty[stage]), phase ^ 1u, gave_up))) break;
           const uint32_t at = ring + stage * L::kStage, sc = at + kSlabs * kSlab, full = bar(bars.full[stage]);
           const uint32_t bytes = min(L::kChunks, p.nKT - k * L::kChunks) * 512;
-#ifdef MXFP4_DEBUG_BOUNDS
-          uint32_t copied = 0;
+          bool whole = true;  // of the buffers: false only in the bounds-checking build
 #pragma unroll
           for (int s = 0; s < 4; ++s)
             if (s < 2 || (s == 2 && third) || (s == 3 && fourth))
-              copied += MXFP4_IN_BOUNDS(p, (kGated ? s == 2 : s > 0) ? kDbgXScales : kDbgScales, src[s], bytes) ? bytes : 0;
-          tc::barrier_expect(full, code_bytes + copied);
-          const bool whole = copied == scale_tiles * bytes;
-#else
-          tc::barrier_expect(full, code_bytes + scale_tiles * bytes);
-          constexpr bool whole = true;
-#endif
+              whole &= MXFP4_IN_BOUNDS(p, (kGated ? s == 2 : s > 0) ? kDbgXScales : kDbgScales, src[s], bytes);
+          tc::barrier_expect(full, code_bytes + (whole ? scale_tiles * bytes : 0));
           const int x = k * kStageBytes;
           tc::copy_box(at, &w_map, x, w_row, full);
           if constexpr (kGated) tc::copy_box(at + kSlab, &w_map, x, w_row + p.cols, full);
@@ -449,20 +478,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::copy_bytes(sc + s * L::kScales, src[s], bytes, full);
             src[s] += L::kScales;
           }
-          if (++stage == kStages) stage = 0, phase ^= 1u, wrapped = true;
+          if (++stage == kStages) stage = 0, phase ^= 1u;
         }
+        copied = n, copier = true;
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      count += k_end - k_begin;
     }
-    // every copy has landed before the CTA may end: slots behind `stage` hold
-    // the phase before
-    if (lane == 0 && *gave_up) {
+    // every copy has landed before the CTA may end
+    if (*gave_up && copier) {
       int none = 0;
-      for (uint32_t s = 0; s < kStages; ++s)
-        if (wrapped || s < stage) {
-          const uint32_t last = s < stage ? phase : phase ^ 1u;
-          for (int tries = 0; tries < 4 && !tc::barrier_wait(bar(bars.full[s]), last, &none); ++tries) none = 0;
-        }
+      for (uint32_t n = copied > kStages ? copied - kStages : 0; n < copied; ++n)
+        for (int tries = 0; tries < 4 && !tc::barrier_wait(bar(bars.full[n % kStages]), n / kStages & 1u, &none); ++tries)
+          none = 0;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -557,16 +585,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step) {
       const int n = t.r0 + row;
       const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
+      // Finished tokens are kept as 16 bits until all sums have been taken and tensor
+      // memory is the next tile's; the stores come after that.  A chunk of 32 tokens
+      // is put into kept[0] and the others move up, so that rolled loops may put and
+      // take them.  Before, the residual is in their place, loaded while the products
+      // run: the chunk to be finished next is the last.
+      constexpr int kChunks = kTokens / 64;
+      uint32_t kept[kChunks][16] = {};
+      if (p.residual != nullptr && ranks == 1) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (half * 32 + 64 * c < t.n) load_residual(p, t, n, half * 32 + 64 * c, kept[kChunks - 1 - c]);
+      }
       if (k_begin < k_end) {
         ok = tc::barrier_wait(bar(bars.sums_full), sums_phase, gave_up);
         ok = __all_sync(0xFFFFFFFFu, ok);
         sums_phase ^= 1u;
         tc::fence_after();
       }
-      float v[32], u[32];
       float* const part = reinterpret_cast<float*>(smem + (ring - tc::shared_address(smem)));
+      int column = half * 32;
 #pragma unroll 1
-      for (int column = half * 32; column < t.n; column += 64) {
+      for (; column < t.n; column += 64) {
+        float v[32], u[32];
         if (k_begin < k_end) {
           tc::load32(from + column, v);
           if constexpr (kGated) tc::load32(from + 128 + column, u);
@@ -587,13 +628,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             part[(column + j) * kRows + row] = v[j];
             if constexpr (kGated) part[(kTokens + column + j) * kRows + row] = u[j];
           }
-        } else {
-          finish<kGated, kF16>(p, t, terms, n, column, v, u);
-          store<kF16>(p, t, n, column, v);
+          continue;
         }
+        finish<kGated>(p, terms, v, u);
+        if (p.residual != nullptr) add_residual<kF16>(p, n, kept[kChunks - 1], v);
+#pragma unroll
+        for (int d = kChunks - 1; d > 0; --d)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) kept[d][j] = kept[d - 1][j];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) kept[0][j] = narrow2<kF16>(v[2 * j], v[2 * j + 1]);
       }
       tc::fence_before();
       tc::barrier_arrive(bar(bars.sums_empty));
+      if (ranks == 1) {
+#pragma unroll 1
+        for (column -= 64; column >= 0; column -= 64) {
+          store(p, t, n, column, kept[0]);
+#pragma unroll
+          for (int d = 0; d + 1 < kChunks; ++d)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) kept[d][j] = kept[d + 1][j];
+        }
+      }
     }
   }
   if (ranks > 1) {
@@ -602,24 +659,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool mine = work && warp >= kFirstEpilogue;
     walk = Walk<kTokens>();
     if (mine && walk.find(p, first_tile, t)) {
-      // each rank finishes every ranks-th token, its two halves every other of those
+      // each rank finishes every ranks-th group of tokens, its two halves every
+      // other of those, all of a group's loads in flight
+      constexpr int kGroup = 8;
       const int thread = threadIdx.x - kFirstEpilogue * 32, row = thread & (kRows - 1), n = t.r0 + row;
       const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
-      for (int c = rank + ranks * (thread >> 7); c < t.n; c += 2 * ranks) {
-        float v[1] = {0.0f}, u[1] = {0.0f};
+      for (int c = (rank + ranks * (thread >> 7)) * kGroup; c < t.n; c += 2 * ranks * kGroup) {
+        float v[kGroup] = {}, u[kGroup] = {};
         for (uint32_t r = 0; r < ranks; ++r) {
           const uint32_t at = cluster_address(ring, r) + (c * kRows + row) * 4;
-          float a;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(at) : "memory");
-          v[0] += a;
-          if constexpr (kGated) {
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a) : "r"(at + kTokens * kRows * 4) : "memory");
-            u[0] += a;
+          float a[kGroup], b[kGroup];
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) {
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a[j]) : "r"(at + j * kRows * 4) : "memory");
+            if constexpr (kGated)
+              asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b[j]) : "r"(at + (kTokens + j) * kRows * 4) : "memory");
+          }
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) {
+            v[j] += a[j];
+            if constexpr (kGated) u[j] += b[j];
           }
         }
-        finish<kGated, kF16, 1>(p, t, terms, n, c, v, u);
-        uint16_t* const at = p.y + (t.row + c) * p.ldy + n;
-        if (n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2)) *at = static_cast<uint16_t>(narrow2<kF16>(v[0], 0.0f));
+        finish<kGated>(p, terms, v, u);
+        if (p.residual != nullptr) {
+          uint16_t r[kGroup];
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) {
+            const uint16_t* const at = p.residual + (t.row + c + j) * p.ldr + n;
+            r[j] = 0;
+            if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) r[j] = *at;
+          }
+#pragma unroll
+          for (int j = 0; j < kGroup; ++j) v[j] += widen<kF16>(r[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+          uint16_t* const at = p.y + (t.row + c + j) * p.ldy + n;
+          if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2))
+            *at = static_cast<uint16_t>(narrow2<kF16>(v[j], 0.0f));
+        }
       }
     }
     __syncwarp();
@@ -707,6 +786,7 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
   p.expert_scales = (a.N + 127) / 128 * p.nKT * static_cast<int64_t>(kChunkBytes);
   p.activation = a.activation;
   p.gate_second = a.gate == MXFP4_GATE_SECOND;
+  p.paired_residual = p.cols % 2 == 0 && a.ldr % 2 == 0 && reinterpret_cast<uintptr_t>(a.residual) % 4 == 0;
   p.paired = p.cols % 2 == 0 && a.ldy % 2 == 0 && reinterpret_cast<uintptr_t>(a.y) % 4 == 0;
 #ifdef MXFP4_DEBUG_BOUNDS
   debug_range(p.dbg, kDbgXScales, a.x_scales,
