@@ -15,7 +15,7 @@
 //
 // Warp 0 copies stages ahead (TMA, a ring of four), one thread of warp 1 issues
 // the scales' copies and the products, warp 2 mends scales where a half of gated
-// weights or K end inside of their tiles, warps 4 to 11 take the sums from tensor
+// weights or K end inside of their tiles, warps 3 to 18 take the sums from tensor
 // memory into registers, which frees it for the next tile, and finish them.  Each
 // CTA walks every gridDim-th tile.  Where tiles are few, a cluster of up to 8 CTAs
 // shares a tile, each with a part of K, and adds the parts in rank order through
@@ -38,9 +38,9 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kFirstEpilogue = 4;              // warp
-constexpr int kEpilogueThreads = 256;
+constexpr int kThreads = 608;
+constexpr int kFirstEpilogue = 3;              // warp
+constexpr int kEpilogueThreads = 512;
 constexpr int kStages = 4;
 constexpr int kRows = 128;                     // of an operand's tile
 constexpr int kStageBytes = 128;               // of a row's codes: 256 elements
@@ -165,7 +165,8 @@ struct Walk {
 };
 
 struct Barriers {
-  uint64_t full[kStages], mended[kStages], empty[kStages], sums_full, sums_empty, drained;
+  uint64_t full[kStages], mended[kStages], empty[kStages], sums_full, sums_empty, tile_full[2], drained;
+  Tile tile[2];      // of the epilogue; n < 0: there are no more
   uint32_t columns;  // tensor memory's address
   int gave_up;
 };
@@ -258,66 +259,77 @@ __device__ __forceinline__ void finish(const GemmParams& p, const RowTerms& r, f
   }
 }
 
-// A thread's 32 tokens of column n from column c of the tile on, two tokens to a
+// A thread's kSome tokens of column n from column c of the tile on, two tokens to a
 // word.  Where rows lie in whole words, neighbours share the copies: each takes
 // both their columns of every other token, and they exchange.  `whole`: none of
 // the warp's tokens and columns is outside.
 __device__ __forceinline__ uint32_t exchange(uint32_t mine, int odd) {
   return __byte_perm(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1), odd ? 0x3276 : 0x5410);
 }
+template <int kSome>
 __device__ __forceinline__ bool whole_chunk(const GemmParams& p, const Tile& t, int c) {
-  return c + 32 <= t.n && t.r0 + kRows <= p.cols;
+  return c + kSome <= t.n && t.r0 + kRows <= p.cols;
 }
-// The residual as loaded (plain loads: it may be y, of which these are read before
-// they are written, by this warp alone), and added.
-__device__ __forceinline__ void load_residual(const GemmParams& p, const Tile& t, int n, int c,
-                                              uint32_t (&r)[16]) {
+// The residual added (plain loads: it may be y, of which these are read before they
+// are written, by this warp alone).  32 tokens of it were asked into L2 before, a
+// row to a lane.
+__device__ __forceinline__ void prefetch_residual(const GemmParams& p, const Tile& t, int first, int c) {
+  const int lane = threadIdx.x & 31;
+  const uint16_t* const at = p.residual + (t.row + c + lane) * p.ldr + first;
+  if (c + lane < t.n && first < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) prefetch_l2(at);
+}
+template <bool kF16, int kSome>
+__device__ __forceinline__ void add_residual(const GemmParams& p, const Tile& t, int n, int c, float (&v)[kSome]) {
   if (p.paired_residual) {
     const int odd = n & 1;
     const uint16_t* at = p.residual + (t.row + c + odd) * p.ldr + (n & ~1);
-    const bool whole = whole_chunk(p, t, c);
+    const bool whole = whole_chunk<kSome>(p, t, c);
+    uint32_t r[kSome / 2];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < kSome / 2; ++j) {
       r[j] = 0;
-      if ((whole || (c + 2 * j + odd < t.n && n < p.cols)) && MXFP4_IN_BOUNDS(p, kDbgResidual, at + 2 * j * p.ldr, 4))
-        r[j] = *reinterpret_cast<const uint32_t*>(at + 2 * j * p.ldr);
+      if ((whole || (c + 2 * j + odd < t.n && n < p.cols)) && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 4))
+        r[j] = *reinterpret_cast<const uint32_t*>(at);
+      at += 2 * p.ldr;
+    }
+#pragma unroll
+    for (int j = 0; j < kSome / 2; ++j) {
+      const uint32_t w = exchange(r[j], odd);
+      v[2 * j] += widen<kF16>(static_cast<uint16_t>(w));
+      v[2 * j + 1] += widen<kF16>(static_cast<uint16_t>(w >> 16));
     }
   } else {
     const uint16_t* at = p.residual + (t.row + c) * p.ldr + n;
-    uint16_t h[32];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      h[j] = 0;
-      if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) h[j] = *at;
-      at += p.ldr;
+    for (int q = 0; q < kSome; q += 4) {
+      uint16_t r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[j] = 0;
+        if (c + q + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) r[j] = *at;
+        at += p.ldr;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[q + j] += widen<kF16>(r[j]);
     }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) r[j] = h[2 * j] | static_cast<uint32_t>(h[2 * j + 1]) << 16;
   }
 }
-template <bool kF16>
-__device__ __forceinline__ void add_residual(const GemmParams& p, int n, const uint32_t (&r)[16], float (&v)[32]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t w = p.paired_residual ? exchange(r[j], n & 1) : r[j];
-    v[2 * j] += widen<kF16>(static_cast<uint16_t>(w));
-    v[2 * j + 1] += widen<kF16>(static_cast<uint16_t>(w >> 16));
-  }
-}
-__device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n, int c, const uint32_t (&w)[16]) {
+template <bool kF16, int kSome>
+__device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n, int c, const float (&v)[kSome]) {
   if (p.paired) {
     const int odd = n & 1;
     uint16_t* at = p.y + (t.row + c + odd) * p.ldy + (n & ~1);
-    if (whole_chunk(p, t, c)) {
+    if (whole_chunk<kSome>(p, t, c)) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const uint32_t word = exchange(w[j], odd);
-        if (MXFP4_IN_BOUNDS(p, kDbgY, at + 2 * j * p.ldy, 4)) *reinterpret_cast<uint32_t*>(at + 2 * j * p.ldy) = word;
+      for (int j = 0; j < kSome / 2; ++j) {
+        const uint32_t word = exchange(narrow2<kF16>(v[2 * j], v[2 * j + 1]), odd);
+        if (MXFP4_IN_BOUNDS(p, kDbgY, at, 4)) *reinterpret_cast<uint32_t*>(at) = word;
+        at += 2 * p.ldy;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const uint32_t word = exchange(w[j], odd);
+      for (int j = 0; j < kSome / 2; ++j) {
+        const uint32_t word = exchange(narrow2<kF16>(v[2 * j], v[2 * j + 1]), odd);
         if (c + 2 * j + odd < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 4))
           *reinterpret_cast<uint32_t*>(at) = word;
         at += 2 * p.ldy;
@@ -326,9 +338,9 @@ __device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n,
   } else {
     uint16_t* at = p.y + (t.row + c) * p.ldy + n;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < kSome; ++j) {
       if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2))
-        *at = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+        *at = static_cast<uint16_t>(narrow2<kF16>(v[j], 0.0f));
       at += p.ldy;
     }
   }
@@ -399,6 +411,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::barrier_init(bar(bars.empty[s]), 1);
     }
     tc::barrier_init(bar(bars.sums_full), 1);
+    tc::barrier_init(bar(bars.tile_full[0]), 1);
+    tc::barrier_init(bar(bars.tile_full[1]), 1);
     tc::barrier_init(bar(bars.sums_empty), kEpilogueThreads);
     tc::barrier_init(bar(bars.drained), 1);
     tc::barrier_init_fence();
@@ -498,19 +512,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One thread issues them, and its instructions are their pace: all it takes is
     // uniform over the tile's loop.
     uint32_t count = 0, tiles = 0;
-    bool ok = true, issued = false;
-    for (int i = first_tile; ok && k_begin < k_end && walk.find(p, i, t); i += tile_step) {
+    bool ok = true, issued = false, more = true;
+    for (int i = first_tile; ok && more; i += tile_step) {
+      more = walk.find(p, i, t);
       if (tc::elected()) {
         issued = true;
-        const uint32_t inst = tc::instruction((t.n + 15) / 16 * 16, kNv), inst_odd = tc::with_scale_byte(inst, 2);
-        const bool wide = t.n > kRows;
-        // the sums of the tile before have been taken
+        // The sums of the tile before have been taken.  Then the epilogue is past
+        // the one before that, and the place of its tile is free.
         if (tiles > 0) {
           ok = tc::barrier_wait(bar(bars.sums_empty), (tiles - 1) & 1u, gave_up);
           tc::fence_after();
         }
+        if (!more) t.n = -1;
+        bars.tile[tiles & 1u] = t;
+        tc::barrier_arrive(bar(bars.tile_full[tiles & 1u]));
+        const bool products = more && k_begin < k_end;
+        const uint32_t inst = tc::instruction((t.n + 15) / 16 * 16, kNv), inst_odd = tc::with_scale_byte(inst, 2);
+        const bool wide = t.n > kRows;
         uint32_t stage = count % kStages, phase = count / kStages & 1u;
-        for (int k = k_begin; ok && k < k_end; ++k) {
+        for (int k = k_begin; ok && products && k < k_end; ++k) {
           ok = tc::barrier_wait(mended ? bar(bars.mended[stage]) : bar(bars.full[stage]), phase, gave_up);
           if (!ok) break;
           tc::fence_after();
@@ -548,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::arrive_when_done(bar(bars.empty[stage]));
           if (++stage == kStages) stage = 0, phase ^= 1u;
         }
-        if (ok) tc::arrive_when_done(bar(bars.sums_full));
+        if (ok && products) tc::arrive_when_done(bar(bars.sums_full));
       }
       ok = __all_sync(0xFFFFFFFFu, ok);
       count += k_end - k_begin;
@@ -577,79 +597,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
   } else if (warp >= kFirstEpilogue) {
     // ---------------------------------------------------------- epilogue
-    const int half = (warp - kFirstEpilogue) >> 2, quarter = warp & 3;
+    // A warp has a quarter of the rows and one or two chunks of 32 tokens, whose
+    // sums it takes at once: tensor memory is the next tile's before they are
+    // finished and stored.
+    constexpr int kChunks = kTokens / 128;
+    constexpr int kSome = kGated ? 4 : 8;    // tokens finished at a time
+    const int group = (warp - kFirstEpilogue) >> 2, quarter = warp & 3;
     const uint32_t from = static_cast<uint32_t>(quarter * 32) << 16;
-    const int row = quarter * 32 + lane;     // of the tile
-    uint32_t sums_phase = 0;
+    const bool add = p.residual != nullptr && ranks == 1;
     bool ok = true;
-    for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step) {
-      const int n = t.r0 + row;
+    for (uint32_t tiles = 0; ok; ++tiles) {
+      ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.tile_full[tiles & 1u]), tiles >> 1 & 1u, gave_up));
+      if (!ok) break;
+      t = bars.tile[tiles & 1u];
+      if (t.n < 0) break;
+      const int n = t.r0 + quarter * 32 + lane;
       const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
-      // Finished tokens are kept as 16 bits until all sums have been taken and tensor
-      // memory is the next tile's; the stores come after that.  A chunk of 32 tokens
-      // is put into kept[0] and the others move up, so that rolled loops may put and
-      // take them.  Before, the residual is in their place, loaded while the products
-      // run: the chunk to be finished next is the last.
-      constexpr int kChunks = kTokens / 64;
-      uint32_t kept[kChunks][16] = {};
-      if (p.residual != nullptr && ranks == 1) {
+      if (add) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
-          if (half * 32 + 64 * c < t.n) load_residual(p, t, n, half * 32 + 64 * c, kept[kChunks - 1 - c]);
+        for (int c = 0; c < kChunks; ++c) prefetch_residual(p, t, t.r0 + quarter * 32, group * 32 + 128 * c);
       }
-      if (k_begin < k_end) {
-        ok = tc::barrier_wait(bar(bars.sums_full), sums_phase, gave_up);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        sums_phase ^= 1u;
+      // gated: of the first half, then of the second
+      float sums[64];
+      if (p.stages > 0) {
+        ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.sums_full), tiles & 1u, gave_up));
         tc::fence_after();
+        tc::load32(from + group * 32, sums);
+        tc::load32(from + 128 + group * 32, sums + 32);
+        tc::load_wait();
+      } else {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) sums[j] = 0.0f;
       }
-      float* const part = reinterpret_cast<float*>(smem + (ring - tc::shared_address(smem)));
-      int column = half * 32;
+      tc::fence_before();
+      tc::barrier_arrive(bar(bars.sums_empty));
+      // a few tokens at a time from the front, the others moved down
 #pragma unroll 1
-      for (; column < t.n; column += 64) {
-        float v[32], u[32];
-        if (k_begin < k_end) {
-          tc::load32(from + column, v);
-          if constexpr (kGated) tc::load32(from + 128 + column, u);
-          tc::load_wait();
-        } else {
+      for (int some = 0; some < kChunks * 32; some += kSome) {
+        const int column = group * 32 + (some & 31) + (some & 32) * 4;
+        if (column >= t.n) break;
+        auto& v = *reinterpret_cast<float(*)[kSome]>(sums);
+        auto& u = *reinterpret_cast<float(*)[kSome]>(sums + 32);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = u[j] = 0.0f;
-        }
-        if (!ok) {  // says that there is no result
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = NAN;
-        }
+        for (int j = 0; j < kSome; ++j) v[j] = ok ? v[j] : NAN;  // NaN: there is no result
         if (ranks > 1) {
           // this CTA's part of the sums to its shared memory, [token][row]: the
           // ring is free, all its products are done
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            part[(column + j) * kRows + row] = v[j];
-            if constexpr (kGated) part[(kTokens + column + j) * kRows + row] = u[j];
+          for (int j = 0; j < kSome; ++j) {
+            const uint32_t at = ring + ((column + j) * kRows + quarter * 32 + lane) * 4;
+            sts32(at, __float_as_uint(v[j]));
+            if constexpr (kGated) sts32(at + kTokens * kRows * 4, __float_as_uint(u[j]));
           }
-          continue;
+        } else {
+          finish<kGated>(p, terms, v, u);
+          if (add) add_residual<kF16>(p, t, n, column, v);
+          store<kF16>(p, t, n, column, v);
         }
-        finish<kGated>(p, terms, v, u);
-        if (p.residual != nullptr) add_residual<kF16>(p, n, kept[kChunks - 1], v);
 #pragma unroll
-        for (int d = kChunks - 1; d > 0; --d)
-#pragma unroll
-          for (int j = 0; j < 16; ++j) kept[d][j] = kept[d - 1][j];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) kept[0][j] = narrow2<kF16>(v[2 * j], v[2 * j + 1]);
-      }
-      tc::fence_before();
-      tc::barrier_arrive(bar(bars.sums_empty));
-      if (ranks == 1) {
-#pragma unroll 1
-        for (column -= 64; column >= 0; column -= 64) {
-          store(p, t, n, column, kept[0]);
-#pragma unroll
-          for (int d = 0; d + 1 < kChunks; ++d)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) kept[d][j] = kept[d + 1][j];
-        }
+        for (int j = 0; j + kSome < 64; ++j)
+          if (!kGated || (j & 31) + kSome < 32) sums[j] = sums[j + kSome];
       }
     }
   }
@@ -659,12 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool mine = work && warp >= kFirstEpilogue;
     walk = Walk<kTokens>();
     if (mine && walk.find(p, first_tile, t)) {
-      // each rank finishes every ranks-th group of tokens, its two halves every
-      // other of those, all of a group's loads in flight
+      // each rank finishes every ranks-th group of tokens, its 128 threads every
+      // fourth of those, all of a group's loads in flight
       constexpr int kGroup = 8;
       const int thread = threadIdx.x - kFirstEpilogue * 32, row = thread & (kRows - 1), n = t.r0 + row;
       const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
-      for (int c = (rank + ranks * (thread >> 7)) * kGroup; c < t.n; c += 2 * ranks * kGroup) {
+      for (int c = (rank + ranks * (thread >> 7)) * kGroup; c < t.n; c += 4 * ranks * kGroup) {
         float v[kGroup] = {}, u[kGroup] = {};
         for (uint32_t r = 0; r < ranks; ++r) {
           const uint32_t at = cluster_address(ring, r) + (c * kRows + row) * 4;
