@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kThreads = 608;
 constexpr int kFirstEpilogue = 3;              // warp
-constexpr int kEpilogueThreads = 512;
+constexpr int kEpilogueWarps = 16;
 constexpr int kStages = 4;
 constexpr int kRows = 128;                     // of an operand's tile
 constexpr int kStageBytes = 128;               // of a row's codes: 256 elements
@@ -168,7 +168,7 @@ struct Barriers {
   uint64_t full[kStages], mended[kStages], empty[kStages], sums_full, sums_empty, tile_full[2], drained;
   Tile tile[2];      // of the epilogue; n < 0: there are no more
   uint32_t columns;  // tensor memory's address
-  int gave_up;
+  uint32_t gave_up;
 };
 
 // --------------------------------------------------------------- epilogue
@@ -316,24 +316,14 @@ __device__ __forceinline__ void add_residual(const GemmParams& p, const Tile& t,
 }
 template <bool kF16, int kSome>
 __device__ __forceinline__ void store(const GemmParams& p, const Tile& t, int n, int c, const float (&v)[kSome]) {
-  if (p.paired) {
+  if (p.paired && whole_chunk<kSome>(p, t, c)) {
     const int odd = n & 1;
     uint16_t* at = p.y + (t.row + c + odd) * p.ldy + (n & ~1);
-    if (whole_chunk<kSome>(p, t, c)) {
 #pragma unroll
-      for (int j = 0; j < kSome / 2; ++j) {
-        const uint32_t word = exchange(narrow2<kF16>(v[2 * j], v[2 * j + 1]), odd);
-        if (MXFP4_IN_BOUNDS(p, kDbgY, at, 4)) *reinterpret_cast<uint32_t*>(at) = word;
-        at += 2 * p.ldy;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kSome / 2; ++j) {
-        const uint32_t word = exchange(narrow2<kF16>(v[2 * j], v[2 * j + 1]), odd);
-        if (c + 2 * j + odd < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 4))
-          *reinterpret_cast<uint32_t*>(at) = word;
-        at += 2 * p.ldy;
-      }
+    for (int j = 0; j < kSome / 2; ++j) {
+      const uint32_t word = exchange(narrow2<kF16>(v[2 * j], v[2 * j + 1]), odd);
+      if (MXFP4_IN_BOUNDS(p, kDbgY, at, 4)) *reinterpret_cast<uint32_t*>(at) = word;
+      at += 2 * p.ldy;
     }
   } else {
     uint16_t* at = p.y + (t.row + c) * p.ldy + n;
@@ -383,7 +373,7 @@ __device__ void mend_scales(uint32_t scales, int tiles, int moved, int shift, in
 }
 
 // --------------------------------------------------------------- the kernel
-template <bool kNv, bool kGated, bool kF16>
+template <bool kNv, bool kGated, bool kF16, bool kAdd>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap x_map, const __grid_constant__ CUtensorMap w_map,
                 const GemmParams p) {
@@ -413,10 +403,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::barrier_init(bar(bars.sums_full), 1);
     tc::barrier_init(bar(bars.tile_full[0]), 1);
     tc::barrier_init(bar(bars.tile_full[1]), 1);
-    tc::barrier_init(bar(bars.sums_empty), kEpilogueThreads);
+    tc::barrier_init(bar(bars.sums_empty), kEpilogueWarps);
     tc::barrier_init(bar(bars.drained), 1);
     tc::barrier_init_fence();
     bars.gave_up = 0;
+    bars.tile[0].n = -1;
     s_bad = 0;
     if (p.stages > 0) tc::prefetch_map(&x_map), tc::prefetch_map(&w_map);
   }
@@ -424,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  volatile int* const gave_up = &bars.gave_up;
+  const uint32_t gave_up = tc::shared_address(&bars.gave_up);
   pdl_wait();
   pdl_release();
 
@@ -500,12 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       count += k_end - k_begin;
     }
     // every copy has landed before the CTA may end
-    if (*gave_up && copier) {
-      int none = 0;
+    if (tc::raised(gave_up) && copier)
       for (uint32_t n = copied > kStages ? copied - kStages : 0; n < copied; ++n)
-        for (int tries = 0; tries < 4 && !tc::barrier_wait(bar(bars.full[n % kStages]), n / kStages & 1u, &none); ++tries)
-          none = 0;
-    }
+        tc::barrier_wait_alone(bar(bars.full[n % kStages]), n / kStages & 1u);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
@@ -574,14 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       count += k_end - k_begin;
       ++tiles;
     }
-    if (*gave_up) {  // what was issued is done before tensor memory is freed
-      int none = 0;
-      if (issued) {
-        tc::arrive_when_done(bar(bars.drained));
-        tc::barrier_wait(bar(bars.drained), 0, &none);
-      }
-      __syncwarp();
+    if (tc::raised(gave_up) && issued) {  // what was issued is done before tensor memory is freed
+      tc::arrive_when_done(bar(bars.drained));
+      tc::barrier_wait_alone(bar(bars.drained), 0);
     }
+    __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------- scales that do not lie as they should
     uint32_t count = 0;
@@ -601,10 +586,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // sums it takes at once: tensor memory is the next tile's before they are
     // finished and stored.
     constexpr int kChunks = kTokens / 128;
-    constexpr int kSome = kGated ? 4 : 8;    // tokens finished at a time
+    // tokens finished at a time: as many as the registers hold (16 for 8: a tile's
+    // epilogue 3.0 -> 2.2 us)
+    constexpr int kSome = (kGated ? 8 : 16) / (kAdd ? 2 : 1);
     const int group = (warp - kFirstEpilogue) >> 2, quarter = warp & 3;
     const uint32_t from = static_cast<uint32_t>(quarter * 32) << 16;
-    const bool add = p.residual != nullptr && ranks == 1;
     bool ok = true;
     for (uint32_t tiles = 0; ok; ++tiles) {
       ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.tile_full[tiles & 1u]), tiles >> 1 & 1u, gave_up));
@@ -613,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t.n < 0) break;
       const int n = t.r0 + quarter * 32 + lane;
       const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
-      if (add) {
+      if (kAdd && ranks == 1) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) prefetch_residual(p, t, t.r0 + quarter * 32, group * 32 + 128 * c);
       }
@@ -625,21 +611,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::load32(from + group * 32, sums);
         tc::load32(from + 128 + group * 32, sums + 32);
         tc::load_wait();
+        if (!ok) {  // there is no result: NaN says so
+#pragma unroll
+          for (int j = 0; j < 64; ++j) sums[j] = NAN;
+        }
       } else {
 #pragma unroll
         for (int j = 0; j < 64; ++j) sums[j] = 0.0f;
       }
       tc::fence_before();
-      tc::barrier_arrive(bar(bars.sums_empty));
-      // a few tokens at a time from the front, the others moved down
-#pragma unroll 1
+      __syncwarp();
+      if (lane == 0) tc::barrier_arrive(bar(bars.sums_empty));
+#pragma unroll
       for (int some = 0; some < kChunks * 32; some += kSome) {
         const int column = group * 32 + (some & 31) + (some & 32) * 4;
         if (column >= t.n) break;
-        auto& v = *reinterpret_cast<float(*)[kSome]>(sums);
-        auto& u = *reinterpret_cast<float(*)[kSome]>(sums + 32);
-#pragma unroll
-        for (int j = 0; j < kSome; ++j) v[j] = ok ? v[j] : NAN;  // NaN: there is no result
+        auto& v = *reinterpret_cast<float(*)[kSome]>(sums + some);
+        auto& u = *reinterpret_cast<float(*)[kSome]>(sums + (kGated ? 32 + some : 0));
         if (ranks > 1) {
           // this CTA's part of the sums to its shared memory, [token][row]: the
           // ring is free, all its products are done
@@ -651,21 +639,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else {
           finish<kGated>(p, terms, v, u);
-          if (add) add_residual<kF16>(p, t, n, column, v);
+          if constexpr (kAdd) add_residual<kF16>(p, t, n, column, v);
           store<kF16>(p, t, n, column, v);
         }
-#pragma unroll
-        for (int j = 0; j + kSome < 64; ++j)
-          if (!kGated || (j & 31) + kSome < 32) sums[j] = sums[j + kSome];
       }
     }
   }
   if (ranks > 1) {
     __syncwarp();
     cluster_sync();
-    const bool mine = work && warp >= kFirstEpilogue;
-    walk = Walk<kTokens>();
-    if (mine && walk.find(p, first_tile, t)) {
+    if (warp >= kFirstEpilogue && bars.tile[0].n > 0) {  // a cluster has one tile or none
+      t = bars.tile[0];
       // each rank finishes every ranks-th group of tokens, its 128 threads every
       // fourth of those, all of a group's loads in flight
       constexpr int kGroup = 8;
@@ -689,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         finish<kGated>(p, terms, v, u);
-        if (p.residual != nullptr) {
+        if constexpr (kAdd) {
           uint16_t r[kGroup];
 #pragma unroll
           for (int j = 0; j < kGroup; ++j) {
@@ -714,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (threadIdx.x == 0 && *gave_up && p.status != nullptr && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4))
+  if (threadIdx.x == 0 && tc::raised(gave_up) && p.status != nullptr && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4))
     *p.status = MXFP4_ECUDA;
   if (warp == 1) tc::release(bars.columns, kColumns);
 }
@@ -750,18 +734,18 @@ cudaError_t map_codes(CUtensorMap* map, const uint8_t* codes, int64_t rows, int6
              : cudaErrorInvalidValue;
 }
 
-template <bool kNv, bool kGated, bool kF16>
+template <bool kNv, bool kGated, bool kF16, bool kAdd>
 cudaError_t launch_typed(const CUtensorMap& x_map, const CUtensorMap& w_map, const GemmParams& p, int64_t tiles,
                          cudaStream_t stream) {
   constexpr int kBytes = Layout<kNv>::kBytes + 1024;  // to a multiple of 1024
   static std::atomic<uint64_t> ready{0};
-  if (const cudaError_t e = allow_smem(gemm_kernel<kNv, kGated, kF16>, kBytes, ready); e != cudaSuccess) return e;
+  if (const cudaError_t e = allow_smem(gemm_kernel<kNv, kGated, kF16, kAdd>, kBytes, ready); e != cudaSuccess) return e;
   // clusters that share a tile's K: as many CTAs as the SMs hold, a stage each
   const int64_t sms = sm_count();
   int ranks = 1;
   while (ranks < 8 && tiles * ranks * 2 <= sms && ranks * 2 <= p.stages) ranks *= 2;
   const int64_t grid = ranks > 1 ? tiles * ranks : tiles < sms ? tiles : sms;
-  return launch_pdl_cluster(gemm_kernel<kNv, kGated, kF16>, dim3(static_cast<unsigned>(grid)), kThreads, kBytes, stream,
+  return launch_pdl_cluster(gemm_kernel<kNv, kGated, kF16, kAdd>, dim3(static_cast<unsigned>(grid)), kThreads, kBytes, stream,
                             ranks > 1 ? ranks : 0, x_map, w_map, p);
 }
 
@@ -822,13 +806,19 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
                                         : (a.rows + tokens - 1) / tokens;
   int64_t tiles = token_tiles * p.row_tiles;
   if (tiles < 1) tiles = 1;  // the status word alone
-  const auto launch = [&](auto nv, auto gate) {
-    return a.f16 ? launch_typed<decltype(nv)::value, decltype(gate)::value, true>(x_map, w_map, p, tiles, stream)
-                 : launch_typed<decltype(nv)::value, decltype(gate)::value, false>(x_map, w_map, p, tiles, stream);
-  };
   using std::false_type, std::true_type;
-  if (a.nvfp4) return gated ? launch(true_type{}, true_type{}) : launch(true_type{}, false_type{});
-  return gated ? launch(false_type{}, true_type{}) : launch(false_type{}, false_type{});
+  const auto launch = [&](auto nv, auto gate, auto f16, auto add) {
+    return launch_typed<decltype(nv)::value, decltype(gate)::value, decltype(f16)::value, decltype(add)::value>(
+        x_map, w_map, p, tiles, stream);
+  };
+  const auto with_add = [&](auto nv, auto gate, auto f16) {
+    return a.residual ? launch(nv, gate, f16, true_type{}) : launch(nv, gate, f16, false_type{});
+  };
+  const auto with_type = [&](auto nv, auto gate) {
+    return a.f16 ? with_add(nv, gate, true_type{}) : with_add(nv, gate, false_type{});
+  };
+  if (a.nvfp4) return gated ? with_type(true_type{}, true_type{}) : with_type(true_type{}, false_type{});
+  return gated ? with_type(false_type{}, true_type{}) : with_type(false_type{}, false_type{});
 }
 
 #ifdef MXFP4_DEBUG_BOUNDS

@@ -48,19 +48,33 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
-// Waits for the phase of `parity`; gives up, and says so to the CTA by
-// `gave_up`, after 2^32 cycles (about two seconds) or when another thread has.
-__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+// A word of shared memory that says that a wait was given up.
+__device__ __forceinline__ bool raised(uint32_t flag) {
+  uint32_t v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(flag) : "memory");
+  return v != 0;
+}
+__device__ __forceinline__ void raise(uint32_t flag) {
+  asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(flag), "r"(1) : "memory");
+}
+// Waits for the phase of `parity`; gives up after 2^32 cycles (about two seconds).
+__device__ __forceinline__ bool barrier_wait_alone(uint32_t bar, uint32_t parity) {
+  for (const long long start = clock64(); !barrier_try(bar, parity);)
+    if (clock64() - start > (1ll << 32)) return false;
+  return true;
+}
+// The same, and says so by `gave_up`; or when another thread has.
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t parity, uint32_t gave_up) {
   long long start = 0;
   for (uint32_t i = 0;; ++i) {
     if (barrier_try(bar, parity)) return true;
     if ((i & 63u) == 63u) {
       const long long now = clock64();
       if (i == 63u) start = now;
-      if (*gave_up || now - start > (1ll << 32)) break;
+      if (raised(gave_up) || now - start > (1ll << 32)) break;
     }
   }
-  *gave_up = 1;
+  raise(gave_up);
   return false;
 }
 
