@@ -1,18 +1,20 @@
 // topk.cu — the router's choice for sm_103a: the top_k experts of every token
 // and their weights (formulas in include/mxfp4.h).
 //
-// A warp to a token; lane l holds the picks of experts l, l + 32, ... as 32-bit
-// keys whose unsigned order is the picks' order (0: out), so a round of the
-// choice is one redux.max over the lanes' best keys and one redux.min over the
-// indices that have it: equal picks go to the lowest index.  Only the lane that
-// lost its best looks through its keys again.
+// A warp to a token; each lane holds the picks of some experts as 32-bit keys whose
+// unsigned order is the picks' order (0: out), so a round of the choice is one
+// redux.max over the lanes' best keys and one redux.min over the indices that have
+// it: equal picks go to the lowest index.  A lane knows its two best, and looks
+// through its keys again when both are taken.
 //
 // Without a bias and group sums the keys are the logits, and exact.  Else they
-// are float32 scores plus bias, and two closer than their error may be in the
-// wrong order.  The choice notes the gaps between neighbours in its order, one
-// beyond the last chosen; where a gap is within twice the error bound (about one
-// token in 500 with 384 experts of ordinary spread) the token is chosen again by
-// choose_exactly, which compares what is near in 64 bits.
+// are float32 scores plus bias, and two closer than their errors may be in the
+// wrong order.  The rounds go on while a pick is that near the last chosen, and
+// where any two neighbours are near each other (about one token in 500 with 384
+// experts of ordinary spread) the ones found, one to a lane, are computed in 64
+// bits and ranked again.  Groups near the last that stays are compared in 64 bits
+// as well.  Where more than 32 picks are near one another, choose_exactly finds
+// them one by one.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -30,6 +32,14 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr int kMaxPerLane = 32;  // keys in registers; more lie in shared memory
+constexpr int kNear = 32;        // picks that are ranked at once, one to a lane
+
+// A warp's words of shared memory: the picks (`held`: groups or kPer == 0), a bit for
+// each expert, and those ranked; whole 16-byte pieces, as the picks are stored.
+__host__ __device__ constexpr int warp_words(int E, bool held) {
+  const int padded = (E + 31) / 32 * 32;
+  return ((held ? padded : 0) + padded / 32 + kNear + 3) / 4 * 4;
+}
 
 struct TopkParams {
   const void* logits;
@@ -131,14 +141,40 @@ struct Exact {
   int64_t row;
   float top;        // the largest logit, and in float32 and 64 bits the softmax's
   float inv_sum;    // sum's inverse
-  double sum;
+  double inv_sum64;
   uint32_t kept;    // groups that stay
   uint32_t* gone;   // a bit for each expert that has been taken
 };
 
+// e^x in 64 bits, to about 2^-52: x = n ln 2 + r with |r| <= ln(2) / 2 and r's
+// Taylor series to r^13 (r^14 / 14! < 2^-57), without a function call and its
+// saved registers.  0 below -708, where a score no longer counts beside any other.
+__device__ __forceinline__ double exp64(double x) {
+  if (!(x > -708.0)) return 0.0;
+  x = fmin(x, 709.0);
+  const double n = rint(x * 1.4426950408889634);
+  double r = fma(n, -0.693147180369123816490, x);  // ln 2 in two parts, the first of 32 bits
+  r = fma(n, -1.90821492927058770002e-10, r);
+  double s = 1.0 / 6227020800.0;
+  constexpr double kInverse[13] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040,
+                                   1.0 / 40320, 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
+#pragma unroll
+  for (int i = 12; i >= 0; --i) s = fma(s, r, kInverse[i]);
+  return s * __hiloint2double((static_cast<int>(n) + 1023) << 20, 0);
+}
+// 1 / x for 1 <= x <= 2^1023, by Newton's steps from a power of two's inverse and
+// the float32 inverse of the rest.
+__device__ __forceinline__ double inverse64(double x) {
+  const int e = (__double2hiint(x) >> 20) - 1023;                   // x = m 2^e, 1 <= m < 2
+  const double m = x * __hiloint2double((1023 - min(e, 1022)) << 20, 0);
+  double y = __fdividef(1.0f, static_cast<float>(m));
+#pragma unroll
+  for (int i = 0; i < 3; ++i) y = fma(y, fma(-m, y, 1.0), y);
+  return y * __hiloint2double((1023 - min(e, 1022)) << 20, 0);
+}
 __device__ __forceinline__ double pick64(const TopkParams& p, const Exact& x, float l, float b) {
-  const double s = p.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(l)))
-                             : exp(static_cast<double>(l) - x.top) / x.sum;
+  const double s = p.sigmoid ? inverse64(1.0 + exp64(-static_cast<double>(l)))
+                             : exp64(static_cast<double>(l) - x.top) * x.inv_sum64;
   return s + b;
 }
 
@@ -184,82 +220,164 @@ __device__ int best_exactly(const TopkParams& p, const Exact& x, int lo, int hi,
   return at;
 }
 
-// Lane j's chosen expert (-1: none), compared in 64 bits.
 template <LogitType kType>
-__device__ __noinline__ int choose_exactly(const TopkParams& p, int64_t row, float top,
-                                           float inv_sum, uint32_t* gone) {
-  const int lane = threadIdx.x & 31;
-  Exact x{row, top, inv_sum, 1.0, kAll, gone};
-  for (int i = lane; i < (p.E + 31) / 32; i += 32) gone[i] = 0;
+__device__ __forceinline__ double softmax_inverse(const TopkParams& p, int64_t row, float top) {
+  double sum = 0.0;
+  for (int e = threadIdx.x & 31; e < p.E; e += 32) {
+    const float l = logit_at<kType>(p, row, e);
+    if (finite(l)) sum += exp64(static_cast<double>(l) - top);
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+  return inverse64(sum);
+}
+
+__device__ __forceinline__ void none_gone(const TopkParams& p, uint32_t* gone) {
   __syncwarp();
-  if (!p.sigmoid) {
-    double sum = 0.0;
-    for (int e = lane; e < p.E; e += 32) {
-      const float l = logit_at<kType>(p, row, e);
-      if (finite(l)) sum += exp(static_cast<double>(l) - top);
+  for (int i = threadIdx.x & 31; i < (p.E + 31) / 32; i += 32) gone[i] = 0;
+  __syncwarp();
+}
+__device__ __forceinline__ void take(uint32_t* gone, int e) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) gone[e >> 5] |= 1u << (e & 31);
+  __syncwarp();
+}
+
+// Of the groups in `near`, the `count` best by their values in 64 bits.
+template <LogitType kType>
+__device__ __forceinline__ uint32_t best_groups_exactly(const TopkParams& p, Exact x, uint32_t near, int count) {
+  const int lane = threadIdx.x & 31;
+  if (!p.sigmoid) x.inv_sum64 = softmax_inverse<kType>(p, x.row, x.top);
+  double mine = 0.0, value;
+  bool open = false;
+  for (uint32_t rest = near; rest != 0; rest &= rest - 1) {
+    const int g = __ffs(rest) - 1, lo = g * p.size, hi = lo + p.size;
+    none_gone(p, x.gone);
+    const int first = best_exactly<kType>(p, x, lo, hi, value);
+    double total = value;
+    if (first >= 0 && p.group_sum2) {
+      take(x.gone, first);
+      if (best_exactly<kType>(p, x, lo, hi, value) >= 0) total += value;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
-    x.sum = sum;
+    if (lane == g) mine = total, open = first >= 0;
   }
-  const auto take = [&](int e) {
-    if (lane == 0) gone[e >> 5] |= 1u << (e & 31);
-    __syncwarp();
-  };
-  double value;
-  if (p.groups > 1) {
-    double mine = 0.0;
-    bool open = false;
-    for (int g = 0; g < p.groups; ++g) {
-      const int lo = g * p.size, hi = lo + p.size;
-      const int first = best_exactly<kType>(p, x, lo, hi, value);
-      double total = value;
-      if (first >= 0 && p.group_sum2) {
-        take(first);
-        if (best_exactly<kType>(p, x, lo, hi, value) >= 0) total += value;
-      }
-      if (lane == g) mine = total, open = first >= 0;
-    }
-    __syncwarp();
-    for (int i = lane; i < (p.E + 31) / 32; i += 32) gone[i] = 0;
-    __syncwarp();
-    uint32_t kept = 0;
-    for (int j = 0; j < p.top_groups; ++j) {
-      double best = mine;
-      int at = open ? lane : INT32_MAX;
+  uint32_t kept = 0;
+  for (int j = 0; j < count; ++j) {
+    double best = mine;
+    int at = open ? lane : INT32_MAX;
 #pragma unroll
-      for (int d = 16; d > 0; d >>= 1) {
-        const double other = __shfl_xor_sync(kAll, best, d);
-        const int from = __shfl_xor_sync(kAll, at, d);
-        if (from != INT32_MAX && (at == INT32_MAX || other > best || (other == best && from < at)))
-          best = other, at = from;
-      }
-      if (at == INT32_MAX) break;
-      kept |= 1u << at;
-      if (lane == at) open = false;
+    for (int d = 16; d > 0; d >>= 1) {
+      const double other = __shfl_xor_sync(kAll, best, d);
+      const int from = __shfl_xor_sync(kAll, at, d);
+      if (from != INT32_MAX && (at == INT32_MAX || other > best || (other == best && from < at)))
+        best = other, at = from;
     }
-    x.kept = kept;
+    if (at == INT32_MAX) break;
+    kept |= 1u << at;
+    if (lane == at) open = false;
   }
+  return kept;
+}
+
+// Lane j's chosen expert (-1: none), found one by one in 64 bits.
+template <LogitType kType>
+__device__ __forceinline__ int choose_exactly(const TopkParams& p, const Exact& x) {
+  none_gone(p, x.gone);
   int id = -1;
+  double value;
   for (int j = 0; j < p.top_k; ++j) {
     const int e = best_exactly<kType>(p, x, 0, p.E, value);
     if (e < 0) break;
-    if (lane == j) id = e;
-    take(e);
+    if (static_cast<int>(threadIdx.x & 31) == j) id = e;
+    take(x.gone, e);
   }
   return id;
 }
 
+// The lanes' experts (-1: none) ranked by their picks in 64 bits: lane j gets the
+// j-th.  `order`: 32 words of the warp's.
+template <LogitType kType>
+__device__ __forceinline__ int rank_exactly(const TopkParams& p, const Exact& x, int id, int found, uint32_t* order) {
+  const int lane = threadIdx.x & 31;
+  double mine = 0.0;
+  if (id >= 0) mine = pick64(p, x, logit_at<kType>(p, x.row, id), bias_at(p, id));
+  int rank = 0;
+  for (int j = 0; j < found; ++j) {
+    const double other = __shfl_sync(kAll, mine, j);
+    const int e = __shfl_sync(kAll, id, j);
+    rank += other > mine || (other == mine && e < id);
+  }
+  __syncwarp();
+  if (id >= 0) order[rank] = id;
+  __syncwarp();
+  return lane < found ? static_cast<int>(order[lane]) : -1;
+}
+
+// What the rounds found near one another (`many`: more than kNear), in exact order.
+template <LogitType kType>
+__device__ __forceinline__ int order_exactly(const TopkParams& p, Exact x, int id, int found, bool many, uint32_t* order) {
+  if (!p.sigmoid) x.inv_sum64 = softmax_inverse<kType>(p, x.row, x.top);
+  return many ? choose_exactly<kType>(p, x) : rank_exactly<kType>(p, x, id, found, order);
+}
+
 // ------------------------------------------------------------ the kernel
-template <int kPer, LogitType kType>
-__global__ void __launch_bounds__(kThreads) moe_topk_kernel(const TopkParams p) {
-  extern __shared__ uint32_t s_words[];  // per warp: E picks (groups or kPer == 0), E bits
+// A lane's key i is that of expert expert_of(i): with kVec == 4 four consecutive
+// experts in a load, else one.
+template <int kVec>
+__device__ __forceinline__ int expert_of(int i) {
+  const int lane = threadIdx.x & 31;
+  return kVec == 4 ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane;
+}
+// The logits (infinity: no expert) or biases of keys i to i + kVec - 1.
+template <int kVec, LogitType kType>
+__device__ __forceinline__ void load_logits(const TopkParams& p, int64_t row, int i, float (&l)[kVec]) {
+  const int e = expert_of<kVec>(i);
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) l[j] = INFINITY;
+  if (e >= p.E) return;
+  if constexpr (kVec == 1) {
+    l[0] = logit_at<kType>(p, row, e);
+  } else if constexpr (kType == LogitType::kF32) {
+    const float* at = static_cast<const float*>(p.logits) + row * p.ld + e;
+    if (!MXFP4_IN_BOUNDS(p, kDbgLogits, at, 16)) return;
+    const float4 v = __ldg(reinterpret_cast<const float4*>(at));
+    l[0] = v.x, l[1] = v.y, l[2] = v.z, l[3] = v.w;
+  } else {
+    const uint16_t* at = static_cast<const uint16_t*>(p.logits) + row * p.ld + e;
+    if (!MXFP4_IN_BOUNDS(p, kDbgLogits, at, 8)) return;
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+    if constexpr (kType == LogitType::kF16) {
+      l[0] = half_lo_to_f32(v.x), l[1] = half_hi_to_f32(v.x), l[2] = half_lo_to_f32(v.y), l[3] = half_hi_to_f32(v.y);
+    } else {
+      l[0] = __uint_as_float(v.x << 16), l[1] = __uint_as_float(v.x & 0xFFFF0000u);
+      l[2] = __uint_as_float(v.y << 16), l[3] = __uint_as_float(v.y & 0xFFFF0000u);
+    }
+  }
+}
+template <int kVec>
+__device__ __forceinline__ void load_biases(const TopkParams& p, int i, float (&b)[kVec]) {
+  const int e = expert_of<kVec>(i);
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) b[j] = 0.0f;
+  if (p.bias == nullptr || e >= p.E) return;
+  if constexpr (kVec == 1) {
+    b[0] = bias_at(p, e);
+  } else if (MXFP4_IN_BOUNDS(p, kDbgBias, p.bias + e, 16)) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p.bias + e));
+    b[0] = v.x, b[1] = v.y, b[2] = v.z, b[3] = v.w;
+  }
+}
+
+template <int kPer, int kVec, LogitType kType>
+__global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams p) {
+  extern __shared__ __align__(16) uint32_t s_words[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int padded = (p.E + 31) / 32 * 32;
   const bool in_smem = kPer == 0 || p.groups > 1;
-  uint32_t* picks = s_words + static_cast<size_t>(warp) * ((in_smem ? padded : 0) + padded / 32);
+  uint32_t* picks = s_words + warp * warp_words(p.E, in_smem);
   uint32_t* gone = picks + (in_smem ? padded : 0);
+  uint32_t* order = gone + padded / 32;
   pdl_wait();
   pdl_release();
   if (row >= p.tokens) return;
@@ -268,15 +386,17 @@ __global__ void __launch_bounds__(kThreads) moe_topk_kernel(const TopkParams p) 
   Keys<kPer> keys;
   if constexpr (kPer == 0) keys.v = picks + lane, keys.n = padded / 32;
   float top = -INFINITY, inv_sum = 1.0f;
-  const bool softmax = !p.sigmoid;
 #pragma unroll
-  for (int i = 0; i < keys.count(); ++i) {
-    const int e = i * 32 + lane;
-    const float l = e < p.E ? logit_at<kType>(p, row, e) : INFINITY;
-    keys.set(i, finite(l) ? key_of(l) : 0u);
-    if (finite(l)) top = fmaxf(top, l);
+  for (int i = 0; i < keys.count(); i += kVec) {
+    float l[kVec];
+    load_logits<kVec, kType>(p, row, i, l);
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+      keys.set(i + j, finite(l[j]) ? key_of(l[j]) : 0u);
+      if (finite(l[j])) top = fmaxf(top, l[j]);
+    }
   }
-  if (softmax) {
+  if (!p.sigmoid) {
     top = warp_max(top);
     if (p.scored || !p.renormalize) {
       float sum = 0.0f;
@@ -285,25 +405,34 @@ __global__ void __launch_bounds__(kThreads) moe_topk_kernel(const TopkParams p) 
         const uint32_t k = keys.get(i);
         if (k != 0) sum += expf(value_of(k) - top);
       }
-      inv_sum = 1.0f / warp_sum(sum);
+      inv_sum = __fdividef(1.0f, warp_sum(sum));
     }
   }
   if (p.scored) {
 #pragma unroll
-    for (int i = 0; i < keys.count(); ++i) {
-      const int e = i * 32 + lane;
-      const uint32_t k = keys.get(i);
-      const float b = e < p.E ? bias_at(p, e) : 0.0f;
-      keys.set(i, k != 0 && finite(b) ? key_of(pick32(p, value_of(k), b, top, inv_sum)) : 0u);
+    for (int i = 0; i < keys.count(); i += kVec) {
+      float b[kVec];
+      load_biases<kVec>(p, i, b);
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) {
+        const uint32_t k = keys.get(i + j);
+        keys.set(i + j, k != 0 && finite(b[j]) ? key_of(pick32(p, value_of(k), b[j], top, inv_sum)) : 0u);
+      }
     }
   }
+  Exact x{row, top, inv_sum, 0.0, kAll, gone};  // the sum in 64 bits: where it is needed
 
-  bool near = false;  // two neighbours in the order closer than their errors
   if (p.groups > 1) {
     if constexpr (kPer > 0) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i * 32 < padded) picks[i * 32 + lane] = keys.get(i);
+      for (int i = 0; i < kPer; i += kVec) {
+        const int e = expert_of<kVec>(i);
+        if constexpr (kVec == 4) {
+          if (e < p.E) *reinterpret_cast<uint4*>(picks + e) = make_uint4(keys.v[i], keys.v[i + 1], keys.v[i + 2], keys.v[i + 3]);
+        } else {
+          if (e < p.E) picks[e] = keys.v[i];
+        }
+      }
     }
     __syncwarp();
     // 32 / share lanes to a group, its two best merged over them
@@ -325,57 +454,83 @@ __global__ void __launch_bounds__(kThreads) moe_topk_kernel(const TopkParams p) 
     }
     float value = a ? value_of(a) : 0.0f, size = fabsf(value);
     if (p.group_sum2 && b) size += fabsf(value_of(b)), value += value_of(b);
-    uint32_t key = a != 0 && g < p.groups && lane % lanes == 0 ? key_of(value) : 0u;
-    const float tol = 2.0f * tolerance(p, p.scored ? warp_max(size) : 0.0f);
-    uint32_t kept = 0;
-    float last = 0.0f;
-    for (int j = 0; j <= p.top_groups; ++j) {
-      const uint32_t m = __reduce_max_sync(kAll, key);
-      if (m == 0) break;
-      if (j > 0) near |= last - value_of(m) <= tol;
-      last = value_of(m);
-      if (j == p.top_groups) break;
-      const int at = __ffs(__ballot_sync(kAll, key == m)) - 1;
-      kept |= 1u << (at / lanes);
-      if (lane == at) key = 0;
+    // a group to a lane: those before it are larger, or equal and of a lower index
+    const uint32_t all = __shfl_sync(kAll, a != 0 ? key_of(value) : 0u, lane < p.groups ? lane * lanes : 0);
+    const uint32_t key = lane < p.groups ? all : 0u;
+    int before = 0;
+    for (int j = 0; j < p.groups; ++j) {
+      const uint32_t other = __shfl_sync(kAll, key, j);
+      before += other > key || (other == key && j < lane);
     }
+    uint32_t kept = __ballot_sync(kAll, key != 0 && before < p.top_groups);
+    if (p.scored && p.top_groups < p.groups) {
+      // what could be on either side of the border in exact terms
+      const float tol = 2.0f * tolerance(p, warp_max(size));
+      const uint32_t first_out = __reduce_max_sync(kAll, before >= p.top_groups ? key : 0u);
+      const uint32_t last_in = __reduce_min_sync(kAll, key != 0 && before < p.top_groups ? key : 0xFFFFFFFFu);
+      if (first_out != 0 && value_of(last_in) - value_of(first_out) <= tol) {
+        const float border = value_of(last_in);
+        const uint32_t near = __ballot_sync(kAll, key != 0 && fabsf(value_of(key) - border) <= 2.0f * tol);
+        const uint32_t sure = kept & ~near;
+        kept = sure | best_groups_exactly<kType>(p, x, near, p.top_groups - __popc(sure));
+      }
+    }
+    x.kept = kept;
+    // (read again: nothing is held over the calls above)
 #pragma unroll
     for (int i = 0; i < keys.count(); ++i) {
-      const int e = i * 32 + lane;
-      if (e < p.E && !((kept >> (e / p.size)) & 1u)) keys.set(i, 0u);
+      const int e = expert_of<kVec>(i);
+      keys.set(i, e < p.E && ((kept >> (e / p.size)) & 1u) ? picks[e] : 0u);
     }
   }
 
   // the rounds
-  int id = -1;
-  uint32_t best = 0;
-  int best_i = 0;
+  int id = -1, found = 0, best_i = 0, next_i = 0;
+  uint32_t best = 0, next = 0;
+  bool fresh = false;  // `next` is known
   const auto look = [&] {
-    best = 0;
+    best = next = 0;
 #pragma unroll
-    for (int i = 0; i < keys.count(); ++i)
-      if (keys.get(i) > best) best = keys.get(i), best_i = i;
+    for (int i = 0; i < keys.count(); ++i) {
+      const uint32_t k = keys.get(i);
+      if (k > best) next = best, next_i = best_i, best = k, best_i = i;
+      else if (k > next) next = k, next_i = i;
+    }
+    fresh = true;
   };
   look();
-  float last = 0.0f;
-  const int rounds = p.top_k + (p.scored ? 1 : 0);
-  for (int j = 0; j < rounds; ++j) {
+  bool near = false, many = false;
+  float last = 0.0f, kth = 0.0f;
+  for (;;) {
     const uint32_t m = __reduce_max_sync(kAll, best);
     if (m == 0) break;
-    if (j > 0) near |= last - value_of(m) <= tolerance(p, last);
-    last = value_of(m);
-    if (j == p.top_k) break;
-    const int mine = best == m ? best_i * 32 + lane : INT32_MAX;
+    const float value = value_of(m);
+    if (found >= p.top_k) {
+      if (!p.scored || kth - value > tolerance(p, kth)) break;
+      if (found == kNear) {
+        many = true;
+        break;
+      }
+    }
+    if (found > 0) near |= last - value <= tolerance(p, last);
+    last = value;
+    const int mine = best == m ? expert_of<kVec>(best_i) : INT32_MAX;
     const int e = __reduce_min_sync(kAll, mine);
-    if (lane == j) id = e;
+    if (lane == found) id = e;
+    if (++found == p.top_k) {
+      kth = value;
+      if (!p.scored) break;
+    }
     if (mine == e) {
 #pragma unroll
       for (int i = 0; i < keys.count(); ++i)
         if (i == best_i) keys.set(i, 0u);
-      look();
+      if (fresh) best = next, best_i = next_i, fresh = false;
+      else look();
     }
   }
-  if (p.scored && near) id = choose_exactly<kType>(p, row, top, inv_sum, gone);
+  if (p.scored && (near || many)) id = order_exactly<kType>(p, x, id, found, many, order);
+  if (lane >= p.top_k) id = -1;
 
   // the weights, from the chosen logits (a renormalised softmax is the chosen
   // ones' own; small sigmoids are raised together, so that they do not vanish)
@@ -385,11 +540,11 @@ __global__ void __launch_bounds__(kThreads) moe_topk_kernel(const TopkParams p) 
   if (p.renormalize) high = p.sigmoid ? fminf(warp_max(l), 0.0f) : warp_max(l);
   if (id >= 0) {
     const float e = expf(l - high);
-    w = !p.sigmoid ? e * inv_sum : l > 0.0f ? 1.0f / (1.0f + expf(-l)) : e / (1.0f + expf(l));
+    w = !p.sigmoid ? e * inv_sum : l > 0.0f ? __fdividef(1.0f, 1.0f + expf(-l)) : __fdividef(e, 1.0f + expf(l));
   }
   if (p.renormalize) {
     const float total = warp_sum(w);
-    if (id >= 0) w = w / total;
+    if (id >= 0) w = __fdividef(w, total);
   }
   if (lane < p.top_k) {
     const int64_t at = row * p.top_k + lane;
@@ -398,29 +553,31 @@ __global__ void __launch_bounds__(kThreads) moe_topk_kernel(const TopkParams p) 
   }
 }
 
-template <int kPer, LogitType kType>
+template <int kPer, int kVec, LogitType kType>
 cudaError_t launch_per(const TopkParams& p, cudaStream_t stream) {
   static std::atomic<uint64_t> ready{0};
-  const int padded = (p.E + 31) / 32 * 32;
-  const size_t words = (kPer == 0 || p.groups > 1 ? padded : 0) + padded / 32;
-  const size_t bytes = kWarps * words * 4;
+  const size_t words = warp_words(p.E, kPer == 0 || p.groups > 1);
   if (kPer == 0)
-    if (const cudaError_t e = allow_smem(moe_topk_kernel<kPer, kType>,
-                                         kWarps * (MXFP4_ROUTE_MAX_EXPERTS + MXFP4_ROUTE_MAX_EXPERTS / 32) * 4, ready);
+    if (const cudaError_t e = allow_smem(moe_topk_kernel<kPer, kVec, kType>,
+                                         kWarps * warp_words(MXFP4_ROUTE_MAX_EXPERTS, true) * 4, ready);
         e != cudaSuccess)
       return e;
-  return launch_pdl(moe_topk_kernel<kPer, kType>, dim3((p.tokens + kWarps - 1) / kWarps), kThreads,
-                    bytes, stream, p);
+  return launch_pdl(moe_topk_kernel<kPer, kVec, kType>, dim3((p.tokens + kWarps - 1) / kWarps), kThreads,
+                    kWarps * words * 4, stream, p);
 }
 
 template <LogitType kType>
 cudaError_t launch_type(const TopkParams& p, cudaStream_t stream) {
+  // four experts to a load where every row and the biases allow it
+  const int size = kType == LogitType::kF32 ? 4 : 2;
+  const bool wide = p.E % 4 == 0 && p.ld % 4 == 0 && reinterpret_cast<uintptr_t>(p.logits) % (4 * size) == 0 &&
+                    reinterpret_cast<uintptr_t>(p.bias) % 16 == 0;
   // the fewest registers that hold a lane's keys
-  if (p.E <= 4 * 32) return launch_per<4, kType>(p, stream);
-  if (p.E <= 8 * 32) return launch_per<8, kType>(p, stream);
-  if (p.E <= 12 * 32) return launch_per<12, kType>(p, stream);
-  if (p.E <= kMaxPerLane * 32) return launch_per<kMaxPerLane, kType>(p, stream);
-  return launch_per<0, kType>(p, stream);
+  if (p.E <= 4 * 32) return wide ? launch_per<4, 4, kType>(p, stream) : launch_per<4, 1, kType>(p, stream);
+  if (p.E <= 12 * 32) return wide ? launch_per<12, 4, kType>(p, stream) : launch_per<12, 1, kType>(p, stream);
+  if (p.E <= kMaxPerLane * 32)
+    return wide ? launch_per<kMaxPerLane, 4, kType>(p, stream) : launch_per<kMaxPerLane, 1, kType>(p, stream);
+  return launch_per<0, 1, kType>(p, stream);
 }
 
 }  // namespace

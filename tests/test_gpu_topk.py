@@ -84,6 +84,32 @@ def test_picks_that_float32_cannot_tell_apart(mx, score, groups):
               group_score=group_score)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups", [(64, 1), (384, 8), (129, 1), (2000, 4)])
+@pytest.mark.parametrize("alike", [2, 3, 9])
+def test_a_few_picks_near_each_other(mx, score, E, groups, alike):
+    """Runs of picks that differ by float32 roundings, others well apart, anywhere
+    in the order and over the border of the chosen; and groups that are near."""
+    g = gen(E + alike)
+    one = torch.randn(E, device="cuda", generator=g)
+    s = torch.sigmoid(one.double()) if score == "sigmoid" else torch.softmax(one.double(), 0)
+    level = torch.rand(-(-E // alike), device="cuda", generator=g).repeat_interleave(alike)[:E]
+    order = torch.randperm(E, device="cuda", generator=g)
+    bias = (level[order].double() - s).float()
+    logits = one.repeat(9, 1)
+    for k in (1, 5, 8, 16):
+        for group_score in ("max", "sum2"):
+            check(mx, logits, k, score=score, bias=bias, groups=groups, top_groups=max(1, groups // 2),
+                  group_score=group_score)
+    if groups > 1:      # the groups all alike, in another order each
+        size = E // groups
+        first, fs = one[:size], s[:size]
+        bias = torch.cat([(torch.rand(size, device="cuda", generator=gen(5)).double() - fs).float()] * groups)
+        shuffled = torch.cat([torch.arange(size, device="cuda").roll(3 * i) + i * size for i in range(groups)])
+        logits = first.repeat(groups)[shuffled].repeat(3, 1) if score == "sigmoid" else logits[:3]
+        check(mx, logits, 8, score=score, bias=bias[shuffled], groups=groups, top_groups=groups // 2, group_score="sum2")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_logits_that_are_not_finite_are_out(mx, dtype, score):
