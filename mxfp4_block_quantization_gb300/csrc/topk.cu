@@ -1,13 +1,12 @@
 // topk.cu — the router's choice for sm_103a: the top_k experts of every token
 // and their weights (formulas in include/mxfp4.h).
 //
-// A warp to a token; each lane holds the picks of some experts as 32-bit keys whose
-// unsigned order is the picks' order (0: out), so a round of the choice is one
-// redux.max over the lanes' best keys and one redux.min over the indices that have
-// it: equal picks go to the lowest index.  A lane knows its two best, and looks
-// through its keys again when both are taken.
+// A warp to a token; each lane holds the picks of some experts (-infinity: out), and
+// a round of the choice is one redux.max over the lanes' best picks and one redux.min
+// over the indices that have it: equal picks go to the lowest index.  A lane knows its two best, and looks
+// through its picks again when both are taken.
 //
-// Without a bias and group sums the keys are the logits, and exact.  Else they
+// Without a bias and group sums the picks are the logits, and exact.  Else they
 // are float32 scores plus bias, and two closer than their errors may be in the
 // wrong order.  The rounds go on while a pick is that near the last chosen, and
 // where any two neighbours are near each other (about one token in 500 with 384
@@ -51,6 +50,7 @@ struct TopkParams {
   int32_t E;
   int32_t groups;
   int32_t size;  // experts of a group
+  float inv_size;
   int32_t top_groups;
   int32_t top_k;
   float scale;
@@ -82,22 +82,26 @@ __device__ __forceinline__ float bias_at(const TopkParams& p, int e) {
   return MXFP4_IN_BOUNDS(p, kDbgBias, p.bias + e, 4) ? __ldg(p.bias + e) : 0.0f;
 }
 
+// e / size: (e + 1/2) / size is at least 1 / (2 size) >= 2^-14 from the next whole
+// number (sizes are up to 8192), the product off by less than 2^-16 (it is under 32).
+__device__ __forceinline__ int group_of(const TopkParams& p, int e) {
+  return static_cast<int>((e + 0.5f) * p.inv_size);
+}
+
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
-// Unsigned keys in the order of finite floats, -0 with +0; none of them is 0.
-__device__ __forceinline__ uint32_t key_of(float x) {
-  const uint32_t b = __float_as_uint(x + 0.0f);
-  return b ^ ((b & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
+__device__ __forceinline__ float warp_most(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
+  return r;
 }
-__device__ __forceinline__ float value_of(uint32_t key) {
-  return __uint_as_float(key ^ ((key & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
+__device__ __forceinline__ float warp_least(float x) {
+  float r;
+  asm("redux.sync.min.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
+  return r;
 }
+constexpr float kOut = -INFINITY;
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kAll, x, d));
-  return x;
-}
 __device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kAll, x, d);
@@ -119,20 +123,20 @@ __device__ __forceinline__ float tolerance(const TopkParams& p, float m) {
   return (p.sigmoid ? 0x1p-20f : 0x1p-18f + 0x1p-27f * p.E) + 0x1p-21f * fabsf(m);
 }
 
-// The lanes' keys, in registers or (kPer == 0) in shared memory.
+// The lanes' picks, in registers or (kPer == 0) in shared memory.
 template <int kPer>
-struct Keys {
-  uint32_t v[kPer];
-  __device__ __forceinline__ uint32_t get(int i) const { return v[i]; }
-  __device__ __forceinline__ void set(int i, uint32_t k) { v[i] = k; }
+struct Picks {
+  float v[kPer];
+  __device__ __forceinline__ float get(int i) const { return v[i]; }
+  __device__ __forceinline__ void set(int i, float k) { v[i] = k; }
   __device__ __forceinline__ int count() const { return kPer; }
 };
 template <>
-struct Keys<0> {
-  uint32_t* v;
+struct Picks<0> {
+  float* v;
   int n;
-  __device__ __forceinline__ uint32_t get(int i) const { return v[i * 32]; }
-  __device__ __forceinline__ void set(int i, uint32_t k) { v[i * 32] = k; }
+  __device__ __forceinline__ float get(int i) const { return v[i * 32]; }
+  __device__ __forceinline__ void set(int i, float k) { v[i * 32] = k; }
   __device__ __forceinline__ int count() const { return n; }
 };
 
@@ -188,16 +192,16 @@ __device__ int best_exactly(const TopkParams& p, const Exact& x, int lo, int hi,
     b = bias_at(p, e);
     v = pick32(p, l, b, x.top, x.inv_sum);
     return finite(l) && finite(b) && !((x.gone[e >> 5] >> (e & 31)) & 1u) &&
-           ((x.kept >> (e / p.size)) & 1u);
+           ((x.kept >> group_of(p, e)) & 1u);
   };
-  uint32_t most = 0;
+  float most = kOut;
   for (int e = lo + lane; e < hi; e += 32) {
     float l, b, v;
-    if (pick_at(e, l, b, v)) most = max(most, key_of(v));
+    if (pick_at(e, l, b, v)) most = fmaxf(most, v);
   }
-  most = __reduce_max_sync(kAll, most);
-  if (most == 0) return -1;
-  const float from = value_of(most) - tolerance(p, value_of(most));
+  most = warp_most(most);
+  if (most == kOut) return -1;
+  const float from = most - tolerance(p, most);
   int at = INT32_MAX;
   double best = 0.0;
   float at_l = 0.0f, at_b = 0.0f;
@@ -370,53 +374,57 @@ __device__ __forceinline__ void load_biases(const TopkParams& p, int i, float (&
 
 template <int kPer, int kVec, LogitType kType>
 __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams p) {
-  extern __shared__ __align__(16) uint32_t s_words[];
+  extern __shared__ __align__(16) float s_words[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   const int padded = (p.E + 31) / 32 * 32;
   const bool in_smem = kPer == 0 || p.groups > 1;
-  uint32_t* picks = s_words + warp * warp_words(p.E, in_smem);
-  uint32_t* gone = picks + (in_smem ? padded : 0);
+  float* held = s_words + warp * warp_words(p.E, in_smem);
+  uint32_t* gone = reinterpret_cast<uint32_t*>(held + (in_smem ? padded : 0));
   uint32_t* order = gone + padded / 32;
   pdl_wait();
   pdl_release();
   if (row >= p.tokens) return;
 
-  // the logits, and the keys
-  Keys<kPer> keys;
-  if constexpr (kPer == 0) keys.v = picks + lane, keys.n = padded / 32;
-  float top = -INFINITY, inv_sum = 1.0f;
+  Picks<kPer> picks;
+  if constexpr (kPer == 0) picks.v = held + lane, picks.n = padded / 32;
+  float top = kOut, inv_sum = 1.0f;
+  const bool direct = p.scored && p.sigmoid;  // a logit's pick needs no other's
 #pragma unroll
-  for (int i = 0; i < keys.count(); i += kVec) {
-    float l[kVec];
+  for (int i = 0; i < picks.count(); i += kVec) {
+    float l[kVec], b[kVec];
     load_logits<kVec, kType>(p, row, i, l);
+    if (direct) load_biases<kVec>(p, i, b);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-      keys.set(i + j, finite(l[j]) ? key_of(l[j]) : 0u);
-      if (finite(l[j])) top = fmaxf(top, l[j]);
+      float v = l[j];
+      if (direct) v = pick32(p, v, b[j], 0.0f, 1.0f);
+      v = finite(l[j]) && finite(v) ? v : kOut;
+      picks.set(i + j, v);
+      if (!p.sigmoid) top = fmaxf(top, v);
     }
   }
   if (!p.sigmoid) {
-    top = warp_max(top);
+    top = warp_most(top);
     if (p.scored || !p.renormalize) {
       float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < keys.count(); ++i) {
-        const uint32_t k = keys.get(i);
-        if (k != 0) sum += expf(value_of(k) - top);
+      for (int i = 0; i < picks.count(); ++i) {
+        const float l = picks.get(i);
+        if (l != kOut) sum += expf(l - top);
       }
       inv_sum = __fdividef(1.0f, warp_sum(sum));
     }
-  }
-  if (p.scored) {
+    if (p.scored) {
 #pragma unroll
-    for (int i = 0; i < keys.count(); i += kVec) {
-      float b[kVec];
-      load_biases<kVec>(p, i, b);
+      for (int i = 0; i < picks.count(); i += kVec) {
+        float b[kVec];
+        load_biases<kVec>(p, i, b);
 #pragma unroll
-      for (int j = 0; j < kVec; ++j) {
-        const uint32_t k = keys.get(i + j);
-        keys.set(i + j, k != 0 && finite(b[j]) ? key_of(pick32(p, value_of(k), b[j], top, inv_sum)) : 0u);
+        for (int j = 0; j < kVec; ++j) {
+          const float l = picks.get(i + j), v = pick32(p, l, b[j], top, inv_sum);
+          picks.set(i + j, l != kOut && finite(v) ? v : kOut);
+        }
       }
     }
   }
@@ -428,9 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
       for (int i = 0; i < kPer; i += kVec) {
         const int e = expert_of<kVec>(i);
         if constexpr (kVec == 4) {
-          if (e < p.E) *reinterpret_cast<uint4*>(picks + e) = make_uint4(keys.v[i], keys.v[i + 1], keys.v[i + 2], keys.v[i + 3]);
+          if (e < p.E) *reinterpret_cast<float4*>(held + e) = make_float4(picks.v[i], picks.v[i + 1], picks.v[i + 2], picks.v[i + 3]);
         } else {
-          if (e < p.E) picks[e] = keys.v[i];
+          if (e < p.E) held[e] = picks.v[i];
         }
       }
     }
@@ -440,37 +448,37 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
     while (share < p.groups) share <<= 1;
     const int lanes = 32 / share;
     const int g = lane / lanes;
-    uint32_t a = 0, b = 0;
+    float a = kOut, b = kOut;
     if (g < p.groups)
+#pragma unroll 4
       for (int i = lane % lanes; i < p.size; i += lanes) {
-        const uint32_t k = picks[g * p.size + i];
-        b = max(b, min(a, k));
-        a = max(a, k);
+        const float k = held[g * p.size + i];
+        b = fmaxf(b, fminf(a, k));
+        a = fmaxf(a, k);
       }
     for (int d = lanes >> 1; d > 0; d >>= 1) {
-      const uint32_t oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
-      b = max(min(a, oa), max(b, ob));
-      a = max(a, oa);
+      const float oa = __shfl_xor_sync(kAll, a, d), ob = __shfl_xor_sync(kAll, b, d);
+      b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+      a = fmaxf(a, oa);
     }
-    float value = a ? value_of(a) : 0.0f, size = fabsf(value);
-    if (p.group_sum2 && b) size += fabsf(value_of(b)), value += value_of(b);
+    float size = a != kOut ? fabsf(a) : 0.0f;
+    if (p.group_sum2 && b != kOut) size += fabsf(b), a += b;
     // a group to a lane: those before it are larger, or equal and of a lower index
-    const uint32_t all = __shfl_sync(kAll, a != 0 ? key_of(value) : 0u, lane < p.groups ? lane * lanes : 0);
-    const uint32_t key = lane < p.groups ? all : 0u;
+    const float value = __shfl_sync(kAll, a, lane < p.groups ? lane * lanes : 0);
+    const float mine = lane < p.groups ? value : kOut;
     int before = 0;
     for (int j = 0; j < p.groups; ++j) {
-      const uint32_t other = __shfl_sync(kAll, key, j);
-      before += other > key || (other == key && j < lane);
+      const float other = __shfl_sync(kAll, mine, j);
+      before += other > mine || (other == mine && j < lane);
     }
-    uint32_t kept = __ballot_sync(kAll, key != 0 && before < p.top_groups);
+    const bool open = mine != kOut, in = open && before < p.top_groups;
+    uint32_t kept = __ballot_sync(kAll, in);
     if (p.scored && p.top_groups < p.groups) {
       // what could be on either side of the border in exact terms
-      const float tol = 2.0f * tolerance(p, warp_max(size));
-      const uint32_t first_out = __reduce_max_sync(kAll, before >= p.top_groups ? key : 0u);
-      const uint32_t last_in = __reduce_min_sync(kAll, key != 0 && before < p.top_groups ? key : 0xFFFFFFFFu);
-      if (first_out != 0 && value_of(last_in) - value_of(first_out) <= tol) {
-        const float border = value_of(last_in);
-        const uint32_t near = __ballot_sync(kAll, key != 0 && fabsf(value_of(key) - border) <= 2.0f * tol);
+      const float tol = 2.0f * tolerance(p, warp_most(size));
+      const float first_out = warp_most(open && !in ? mine : kOut), border = warp_least(in ? mine : INFINITY);
+      if (first_out != kOut && border - first_out <= tol) {
+        const uint32_t near = __ballot_sync(kAll, open && fabsf(mine - border) <= 2.0f * tol);
         const uint32_t sure = kept & ~near;
         kept = sure | best_groups_exactly<kType>(p, x, near, p.top_groups - __popc(sure));
       }
@@ -478,55 +486,68 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
     x.kept = kept;
     // (read again: nothing is held over the calls above)
 #pragma unroll
-    for (int i = 0; i < keys.count(); ++i) {
+    for (int i = 0; i < picks.count(); ++i) {
       const int e = expert_of<kVec>(i);
-      keys.set(i, e < p.E && ((kept >> (e / p.size)) & 1u) ? picks[e] : 0u);
+      picks.set(i, e < p.E && ((kept >> group_of(p, e)) & 1u) ? held[e] : kOut);
     }
   }
 
   // the rounds
   int id = -1, found = 0, best_i = 0, next_i = 0;
-  uint32_t best = 0, next = 0;
-  bool fresh = false;  // `next` is known
-  const auto look = [&] {
-    best = next = 0;
+  float best = kOut, next = kOut;
+  bool fresh = true;  // `next` is known
 #pragma unroll
-    for (int i = 0; i < keys.count(); ++i) {
-      const uint32_t k = keys.get(i);
-      if (k > best) next = best, next_i = best_i, best = k, best_i = i;
-      else if (k > next) next = k, next_i = i;
-    }
-    fresh = true;
-  };
-  look();
+  for (int i = 0; i < picks.count(); ++i) {
+    const float k = picks.get(i);
+    const bool first = k > best, second = k > next;
+    next = fminf(fmaxf(k, next), best);
+    next_i = first ? best_i : second ? i : next_i;
+    best = fmaxf(k, best);
+    best_i = first ? i : best_i;
+  }
   bool near = false, many = false;
   float last = 0.0f, kth = 0.0f;
   for (;;) {
-    const uint32_t m = __reduce_max_sync(kAll, best);
-    if (m == 0) break;
-    const float value = value_of(m);
+    const float m = warp_most(best);
+    if (m == kOut) break;
     if (found >= p.top_k) {
-      if (!p.scored || kth - value > tolerance(p, kth)) break;
+      if (kth - m > tolerance(p, kth)) break;
       if (found == kNear) {
         many = true;
         break;
       }
     }
-    if (found > 0) near |= last - value <= tolerance(p, last);
-    last = value;
+    if (p.scored) {
+      if (found > 0) near |= last - m <= tolerance(p, last);
+      last = m;
+    }
     const int mine = best == m ? expert_of<kVec>(best_i) : INT32_MAX;
     const int e = __reduce_min_sync(kAll, mine);
     if (lane == found) id = e;
     if (++found == p.top_k) {
-      kth = value;
+      kth = m;
       if (!p.scored) break;
     }
     if (mine == e) {
+      if (fresh) {
+        best = next, best_i = next_i, fresh = false;
+      } else {
+        // the two best behind the last taken in their order
+        const float limit = best;
+        const int limit_i = best_i;
+        best = next = kOut;
 #pragma unroll
-      for (int i = 0; i < keys.count(); ++i)
-        if (i == best_i) keys.set(i, 0u);
-      if (fresh) best = next, best_i = next_i, fresh = false;
-      else look();
+        for (int i = 0; i < picks.count(); ++i) {
+          float k = picks.get(i);
+          k = k < limit || (k == limit && i > limit_i) ? k : kOut;
+          const bool first = k > best, second = k > next;
+          next = fminf(fmaxf(k, next), best);
+          next_i = first ? best_i : second ? i : next_i;
+          best = fmaxf(k, best);
+          best_i = first ? i : best_i;
+        }
+        fresh = true;
+      }
     }
   }
   if (p.scored && (near || many)) id = order_exactly<kType>(p, x, id, found, many, order);
@@ -537,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
   float w = 0.0f;
   const float l = id >= 0 ? logit_at<kType>(p, row, id) : -INFINITY;
   float high = p.sigmoid ? 0.0f : top;
-  if (p.renormalize) high = p.sigmoid ? fminf(warp_max(l), 0.0f) : warp_max(l);
+  if (p.renormalize) high = p.sigmoid ? fminf(warp_most(l), 0.0f) : warp_most(l);
   if (id >= 0) {
     const float e = expf(l - high);
     w = !p.sigmoid ? e * inv_sum : l > 0.0f ? __fdividef(1.0f, 1.0f + expf(-l)) : __fdividef(e, 1.0f + expf(l));
@@ -594,6 +615,7 @@ cudaError_t launch_moe_topk(const TopkArgs& a, cudaStream_t stream) {
   p.E = a.E;
   p.groups = a.groups;
   p.size = a.E / a.groups;
+  p.inv_size = 1.0f / static_cast<float>(p.size);
   p.top_groups = a.top_groups;
   p.top_k = a.top_k;
   p.scale = a.scale;
