@@ -11,15 +11,17 @@
 // number in an instruction is any multiple of 16 up to 256, so one kernel serves
 // one token and many.  A CTA's tile is 128 rows of the weights by 256 tokens, or,
 // with a gate, 128 rows of each half by 128 tokens, whose two sums meet in the
-// epilogue.  256 bytes of K at a time (a stage) are 16 KB for each 128 rows.
+// epilogue.  256 elements of K at a time (a stage) are 16 KB for each 128 rows.
 //
-// Warp 0 copies stages ahead (TMA, a ring of four), one thread of warp 1 issues
+// Warp 0 copies stages ahead (TMA, a ring of four to eight), one thread of warp 1 issues
 // the scales' copies and the products, warp 2 mends scales where a half of gated
-// weights or K end inside of their tiles, warps 3 to 18 take the sums from tensor
+// weights or K end inside of their tiles, warp 3 finds the tiles, warps 4 to 19 take
+// the sums from tensor
 // memory into registers, which frees it for the next tile, and finish them.  Each
 // CTA walks every gridDim-th tile.  Where tiles are few, a cluster of up to 8 CTAs
 // shares a tile, each with a part of K, and adds the parts in rank order through
 // distributed shared memory: equal calls give equal bits.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -38,29 +40,30 @@
 namespace mxfp4 {
 namespace {
 
-constexpr int kThreads = 608;
-constexpr int kFirstEpilogue = 3;              // warp
+constexpr int kThreads = 640;
+constexpr int kFirstEpilogue = 4;              // warp
 constexpr int kEpilogueWarps = 16;
-constexpr int kStages = 4;
+constexpr int kMaxStages = 8;
+constexpr int kRingBytes = 224 * 1024;
 constexpr int kRows = 128;                     // of an operand's tile
 constexpr int kStageBytes = 128;               // of a row's codes: 256 elements
 constexpr int kSlab = kRows * kStageBytes;     // 16 KB
-constexpr int kSlabs = 3;
 constexpr int kSteps = 4;                      // products of 64 elements to a stage
 constexpr int kColumns = 512;
+constexpr int kJobs = 4;                       // tiles found ahead
 // tensor memory, all of which a CTA has (so that it begins at column 0): sums, then
 // the scales of both weight tiles and of the tokens
+constexpr uint32_t kSecond = 128;              // sums of the other 128 tokens, or of the second half
 constexpr uint32_t kScalesA = 256, kScalesB = 288;
 
 // A stage's scales of 128 rows: two chunks of 512 bytes (four with NVFP4), for
 // three tiles and, where the second half of gated weights does not begin at a
-// tile of the scales, the tile behind it.
+// tile of the scales, the tile behind it.  Before them are the codes: one or two
+// tiles of weights, and the tokens.
 template <bool kNv>
 struct Layout {
   static constexpr int kChunks = kNv ? 4 : 2;
   static constexpr int kScales = kChunks * 512;
-  static constexpr int kStage = kSlabs * kSlab + 4 * kScales;
-  static constexpr int kBytes = kStages * kStage;
 };
 
 struct GemmMore {
@@ -92,6 +95,10 @@ struct GemmParams {
   int32_t blocks;           // scales of a row
   int32_t row_tiles;        // tiles of the weights' rows
   int32_t box_rows;         // tokens' rows to a copy
+  int32_t tile_tokens;      // tokens of a tile at most
+  uint32_t ring_stages;
+  uint32_t stage_bytes;     // of which the scales' begin at
+  uint32_t scales_at;
   int32_t activation;
   bool gate_second;
   bool paired;              // rows of y lie in whole words
@@ -116,9 +123,17 @@ struct Tile {
   int e, row, n, padded, r0;
 };
 
+// A tile as warp 3 hands it to the others (n < 0: there are no more), with the row
+// of its weights and where its scales begin: of the weights (both halves' tiles), of
+// the tokens.
+struct Job {
+  Tile t;
+  int w_row;
+  int64_t scales, upper, x_scales;
+};
+
 // The tiles in order of expert, weight rows, tokens.  A warp finds them
 // together, 32 experts at a time; its lanes agree.
-template <int kTokens>
 struct Walk {
   int e0 = -32, before = 0, padded_before = 0;  // of the experts below e0
   int lo = 0, n = 0, tiles = 0, sum = 0, padded = 0;  // the lane's expert: sum up to and with it
@@ -127,10 +142,10 @@ struct Walk {
   __device__ bool find(const GemmParams& p, int index, Tile& t) {
     const int lane = threadIdx.x & 31;
     if (p.offsets == nullptr) {
-      const int token_tiles = (p.rows + kTokens - 1) / kTokens;
+      const int token_tiles = (p.rows + p.tile_tokens - 1) / p.tile_tokens;
       const int r = index / token_tiles, c = index - r * token_tiles;
       if (r >= p.row_tiles) return false;
-      t = Tile{0, c * kTokens, min(kTokens, p.rows - c * kTokens), c * kTokens, r * kRows};
+      t = Tile{0, c * p.tile_tokens, min(p.tile_tokens, p.rows - c * p.tile_tokens), c * p.tile_tokens, r * kRows};
       return true;
     }
     while (index >= before + block_tiles) {
@@ -140,7 +155,7 @@ struct Walk {
       const int e = e0 + lane;
       n = 0;
       if (e < p.E) lo = offset_at(p, e), n = offset_at(p, e + 1) - lo;
-      tiles = (n + kTokens - 1) / kTokens * p.row_tiles;
+      tiles = (n + p.tile_tokens - 1) / p.tile_tokens * p.row_tiles;
       padded = (n + kRows - 1) / kRows * kRows;
       sum = tiles;
       int psum = padded;
@@ -156,17 +171,17 @@ struct Walk {
     const int l = __ffs(__ballot_sync(0xFFFFFFFFu, index < before + sum)) - 1;
     const int rows = __shfl_sync(0xFFFFFFFFu, n, l);
     const int first = before + __shfl_sync(0xFFFFFFFFu, sum - tiles, l);
-    const int token_tiles = (rows + kTokens - 1) / kTokens;
+    const int token_tiles = (rows + p.tile_tokens - 1) / p.tile_tokens;
     const int r = (index - first) / token_tiles, c = index - first - r * token_tiles;
-    t = Tile{e0 + l, __shfl_sync(0xFFFFFFFFu, lo, l) + c * kTokens, min(kTokens, rows - c * kTokens),
-             padded_before + __shfl_sync(0xFFFFFFFFu, padded, l) + c * kTokens, r * kRows};
+    t = Tile{e0 + l, __shfl_sync(0xFFFFFFFFu, lo, l) + c * p.tile_tokens, min(p.tile_tokens, rows - c * p.tile_tokens),
+             padded_before + __shfl_sync(0xFFFFFFFFu, padded, l) + c * p.tile_tokens, r * kRows};
     return true;
   }
 };
 
 struct Barriers {
-  uint64_t full[kStages], mended[kStages], empty[kStages], sums_full, sums_empty, tile_full[2], drained;
-  Tile tile[2];      // of the epilogue; n < 0: there are no more
+  uint64_t full[kMaxStages], mended[kMaxStages], empty[kMaxStages], sums_full, sums_empty, job_full[kJobs], job_empty[kJobs], drained;
+  Job job[kJobs];
   uint32_t columns;  // tensor memory's address
   uint32_t gave_up;
 };
@@ -382,7 +397,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kWeightSlabs = kGated ? 2 : 1;
   extern __shared__ uint8_t smem[];
   __shared__ Barriers bars;
-  __shared__ int s_bad;
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t ring = (tc::shared_address(smem) + 1023u) & ~1023u;
   const auto bar = [](const uint64_t& b) { return tc::shared_address(&b); };
@@ -394,21 +408,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int k_begin = static_cast<int>(static_cast<int64_t>(p.stages) * rank / ranks);
   const int k_end = static_cast<int>(static_cast<int64_t>(p.stages) * (rank + 1) / ranks);
 
+  // the second half's rows begin at row `shift` of a tile of the scales
+  const int shift = kGated ? p.cols & (kRows - 1) : 0;
+  // a product's 64 elements of K go past the last scale
+  const bool tail = (p.blocks & (kNv ? 3 : 1)) != 0;
+  const bool mended = shift != 0 || tail;
+
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kMaxStages; ++s) {
       tc::barrier_init(bar(bars.full[s]), 1);
       tc::barrier_init(bar(bars.mended[s]), 1);
       tc::barrier_init(bar(bars.empty[s]), 1);
     }
     tc::barrier_init(bar(bars.sums_full), 1);
-    tc::barrier_init(bar(bars.tile_full[0]), 1);
-    tc::barrier_init(bar(bars.tile_full[1]), 1);
     tc::barrier_init(bar(bars.sums_empty), kEpilogueWarps);
+    for (int i = 0; i < kJobs; ++i) {
+      tc::barrier_init(bar(bars.job_full[i]), 1);
+      tc::barrier_init(bar(bars.job_empty[i]), 2 + mended + kEpilogueWarps);
+    }
     tc::barrier_init(bar(bars.drained), 1);
     tc::barrier_init_fence();
     bars.gave_up = 0;
-    bars.tile[0].n = -1;
-    s_bad = 0;
+    bars.job[0].t.n = -1;
     if (p.stages > 0) tc::prefetch_map(&x_map), tc::prefetch_map(&w_map);
   }
   if (warp == 1) tc::allocate(tc::shared_address(&bars.columns), kColumns);
@@ -430,41 +451,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && blockIdx.x == 0 && p.status != nullptr && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4))
       *p.status = work ? MXFP4_OK : MXFP4_EOFFSETS;
   }
-  // the second half's rows begin at row `shift` of a tile of the scales
-  const int shift = kGated ? p.cols & (kRows - 1) : 0;
-  // a product's 64 elements of K go past the last scale
-  const bool tail = (p.blocks & (kNv ? 3 : 1)) != 0;
-  const bool mended = shift != 0 || tail;
-
-  Walk<kTokens> walk;
-  Tile t;
+  Tile t{};
   if (!work) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ copies
-    uint32_t count = 0, copied = 0;
-    bool ok = true, copier = false;
-    for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step) {
-      if (tc::elected()) {
-        const int boxes = (t.n + p.box_rows - 1) / p.box_rows;
+    if (tc::elected()) {
+      const int64_t row_bytes = static_cast<int64_t>(p.nKT) * 512, begin = static_cast<int64_t>(k_begin) * L::kScales;
+      uint32_t stage = 0, phase = 0, copied = 0;
+      bool ok = true;
+      for (uint32_t j = 0; ok; ++j) {
+        ok = tc::barrier_wait(bar(bars.job_full[j % kJobs]), j / kJobs & 1u, gave_up);
+        if (!ok) break;
+        const Job job = bars.job[j % kJobs];
+        tc::barrier_arrive(bar(bars.job_empty[j % kJobs]));
+        if (job.t.n < 0) break;
+        const int boxes = (job.t.n + p.box_rows - 1) / p.box_rows;
         const uint32_t box_bytes = p.box_rows * kStageBytes;
-        const int w_row = t.e * p.N + t.r0;
         // the tiles' scales: of the weights (both halves'), of the tokens, and of the
         // tile behind the second half's first where it does not begin at a tile and
         // is not the last
-        const int64_t row_bytes = static_cast<int64_t>(p.nKT) * 512;
-        const uint8_t* const ws = p.scales + t.e * p.expert_scales + static_cast<int64_t>(k_begin) * L::kScales;
-        const uint8_t* const xs = p.x_scales + t.padded / kRows * row_bytes + static_cast<int64_t>(k_begin) * L::kScales;
-        const int upper = (p.cols + t.r0) / kRows;
-        const uint8_t* src[4] = {ws + t.r0 / kRows * row_bytes, kGated ? ws + upper * row_bytes : xs,
-                                 kGated ? xs : xs + row_bytes, ws + (upper + 1) * row_bytes};
-        const bool third = kGated || t.n > kRows;
-        const bool fourth = kGated && shift != 0 && (upper + 1) * kRows < p.N;
+        const uint8_t* const ws = p.scales + begin;
+        const uint8_t* const xs = p.x_scales + job.x_scales + begin;
+        const uint8_t* src[4] = {ws + job.scales, kGated ? ws + job.upper : xs, kGated ? xs : xs + row_bytes,
+                                 ws + job.upper + row_bytes};
+        const bool third = kGated || job.t.n > kRows;
+        const bool fourth = kGated && shift != 0 && (p.cols + job.t.r0) / kRows * kRows + kRows < p.N;
         const uint32_t code_bytes = kWeightSlabs * kSlab + boxes * box_bytes;
         const uint32_t scale_tiles = 2 + third + fourth;
-        uint32_t stage = count % kStages, phase = count / kStages & 1u, n = count;
-        for (int k = k_begin; k < k_end; ++k, ++n) {
-          if (n >= kStages && !(ok = tc::barrier_wait(bar(bars.empty[stage]), phase ^ 1u, gave_up))) break;
-          const uint32_t at = ring + stage * L::kStage, sc = at + kSlabs * kSlab, full = bar(bars.full[stage]);
+        for (int k = k_begin; k < k_end; ++k, ++copied) {
+          if (copied >= p.ring_stages && !(ok = tc::barrier_wait(bar(bars.empty[stage]), phase ^ 1u, gave_up))) break;
+          const uint32_t at = ring + stage * p.stage_bytes, sc = at + p.scales_at, full = bar(bars.full[stage]);
           const uint32_t bytes = min(L::kChunks, p.nKT - k * L::kChunks) * 512;
           bool whole = true;  // of the buffers: false only in the bounds-checking build
 #pragma unroll
@@ -473,58 +489,49 @@ __global__ void __launch_bounds__(kThreads, 1)
               whole &= MXFP4_IN_BOUNDS(p, (kGated ? s == 2 : s > 0) ? kDbgXScales : kDbgScales, src[s], bytes);
           tc::barrier_expect(full, code_bytes + (whole ? scale_tiles * bytes : 0));
           const int x = k * kStageBytes;
-          tc::copy_box(at, &w_map, x, w_row, full);
-          if constexpr (kGated) tc::copy_box(at + kSlab, &w_map, x, w_row + p.cols, full);
+          tc::copy_box(at, &w_map, x, job.w_row, full);
+          if constexpr (kGated) tc::copy_box(at + kSlab, &w_map, x, job.w_row + p.cols, full);
           for (int b = 0; b < boxes; ++b)
-            tc::copy_box(at + kWeightSlabs * kSlab + b * box_bytes, &x_map, x, t.row + b * p.box_rows, full);
+            tc::copy_box(at + kWeightSlabs * kSlab + b * box_bytes, &x_map, x, job.t.row + b * p.box_rows, full);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
             if ((s < 2 || (s == 2 && third) || (s == 3 && fourth)) && whole)
               tc::copy_bytes(sc + s * L::kScales, src[s], bytes, full);
             src[s] += L::kScales;
           }
-          if (++stage == kStages) stage = 0, phase ^= 1u;
+          if (++stage == p.ring_stages) stage = 0, phase ^= 1u;
         }
-        copied = n, copier = true;
       }
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      count += k_end - k_begin;
+      // every copy has landed before the CTA may end
+      if (tc::raised(gave_up))
+        for (uint32_t n = copied > p.ring_stages ? copied - p.ring_stages : 0; n < copied; ++n)
+          tc::barrier_wait_alone(bar(bars.full[n % p.ring_stages]), n / p.ring_stages & 1u);
     }
-    // every copy has landed before the CTA may end
-    if (tc::raised(gave_up) && copier)
-      for (uint32_t n = copied > kStages ? copied - kStages : 0; n < copied; ++n)
-        tc::barrier_wait_alone(bar(bars.full[n % kStages]), n / kStages & 1u);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------- products
-    // One thread issues them, and its instructions are their pace: all it takes is
-    // uniform over the tile's loop.
-    uint32_t count = 0, tiles = 0;
-    bool ok = true, issued = false, more = true;
-    for (int i = first_tile; ok && more; i += tile_step) {
-      more = walk.find(p, i, t);
-      if (tc::elected()) {
-        issued = true;
-        // The sums of the tile before have been taken.  Then the epilogue is past
-        // the one before that, and the place of its tile is free.
-        if (tiles > 0) {
-          ok = tc::barrier_wait(bar(bars.sums_empty), (tiles - 1) & 1u, gave_up);
-          tc::fence_after();
-        }
-        if (!more) t.n = -1;
-        bars.tile[tiles & 1u] = t;
-        tc::barrier_arrive(bar(bars.tile_full[tiles & 1u]));
-        const bool products = more && k_begin < k_end;
-        const uint32_t inst = tc::instruction((t.n + 15) / 16 * 16, kNv), inst_odd = tc::with_scale_byte(inst, 2);
-        const bool wide = t.n > kRows;
-        uint32_t stage = count % kStages, phase = count / kStages & 1u;
-        for (int k = k_begin; ok && products && k < k_end; ++k) {
+    // One thread issues them, and its instructions are their pace.
+    if (tc::elected()) {
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (uint32_t j = 0; ok; ++j) {
+        ok = tc::barrier_wait(bar(bars.job_full[j % kJobs]), j / kJobs & 1u, gave_up);
+        if (!ok) break;
+        const int n = bars.job[j % kJobs].t.n;
+        tc::barrier_arrive(bar(bars.job_empty[j % kJobs]));
+        if (n < 0) break;
+        if (k_begin == k_end) continue;
+        if (j > 0) ok = tc::barrier_wait(bar(bars.sums_empty), (j - 1) & 1u, gave_up);  // the tile's before
+        tc::fence_after();
+        const uint32_t inst = tc::instruction((n + 15) / 16 * 16, kNv), inst_odd = tc::with_scale_byte(inst, 2);
+        const bool wide = n > kRows;
+        for (int k = k_begin; ok && k < k_end; ++k) {
           ok = tc::barrier_wait(mended ? bar(bars.mended[stage]) : bar(bars.full[stage]), phase, gave_up);
           if (!ok) break;
           tc::fence_after();
-          const uint32_t at = ring + stage * L::kStage;
+          const uint32_t at = ring + stage * p.stage_bytes;
           const uint32_t a = tc::operand_low(at), b = a + kWeightSlabs * kSlab / 16;
-          const uint32_t s0 = tc::scales_low(at + kSlabs * kSlab);
+          const uint32_t s0 = tc::scales_low(at + p.scales_at);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c) {  // (past the last chunk: what no product uses)
             constexpr uint32_t kTile = L::kScales / 16;  // a tile's scales
@@ -550,36 +557,60 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::multiply<kNv>(0, tc::descriptor(a + 2 * s, tc::kOperandHigh), bd, in, kScalesA + c * 4,
                               kScalesB + c * kStride, add);
             if constexpr (kGated)
-              tc::multiply<kNv>(128, tc::descriptor(a + kSlab / 16 + 2 * s, tc::kOperandHigh), bd, in,
+              tc::multiply<kNv>(kSecond, tc::descriptor(a + kSlab / 16 + 2 * s, tc::kOperandHigh), bd, in,
                                 kScalesA + 16 + c * 4, kScalesB + c * kStride, add);
           }
           tc::arrive_when_done(bar(bars.empty[stage]));
-          if (++stage == kStages) stage = 0, phase ^= 1u;
+          if (++stage == p.ring_stages) stage = 0, phase ^= 1u;
         }
-        if (ok && products) tc::arrive_when_done(bar(bars.sums_full));
+        if (ok) tc::arrive_when_done(bar(bars.sums_full));
       }
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      count += k_end - k_begin;
-      ++tiles;
-    }
-    if (tc::raised(gave_up) && issued) {  // what was issued is done before tensor memory is freed
-      tc::arrive_when_done(bar(bars.drained));
-      tc::barrier_wait_alone(bar(bars.drained), 0);
+      if (tc::raised(gave_up)) {  // what was issued is done before tensor memory is freed
+        tc::arrive_when_done(bar(bars.drained));
+        tc::barrier_wait_alone(bar(bars.drained), 0);
+      }
     }
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------- scales that do not lie as they should
     uint32_t count = 0;
     bool ok = mended;
-    for (int i = first_tile; ok && walk.find(p, i, t); i += tile_step)
+    for (uint32_t j = 0; ok; ++j) {
+      ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.job_full[j % kJobs]), j / kJobs & 1u, gave_up));
+      if (!ok) break;
+      const int n = bars.job[j % kJobs].t.n;
+      __syncwarp();
+      if (lane == 0) tc::barrier_arrive(bar(bars.job_empty[j % kJobs]));
+      if (n < 0) break;
       for (int k = k_begin; ok && k < k_end; ++k, ++count) {
-        const uint32_t stage = count % kStages;
-        ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.full[stage]), count / kStages & 1u, gave_up));
+        const uint32_t stage = count % p.ring_stages;
+        ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.full[stage]), count / p.ring_stages & 1u, gave_up));
         if (!ok) break;
         const int keep = k == p.stages - 1 && tail ? p.blocks - k * L::kChunks * 4 : -1;
-        if (shift != 0 || keep >= 0) mend_scales<kNv>(ring + stage * L::kStage + kSlabs * kSlab, 3, 1, shift, keep);
+        if (shift != 0 || keep >= 0) mend_scales<kNv>(ring + stage * p.stage_bytes + p.scales_at, 3, 1, shift, keep);
         if (lane == 0) tc::barrier_arrive(bar(bars.mended[stage]));
       }
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------- the tiles
+    Walk walk;
+    const int64_t row_bytes = static_cast<int64_t>(p.nKT) * 512;
+    bool ok = true, more = true;
+    uint32_t j = 0;
+    for (int i = first_tile; ok && more; i += tile_step, ++j) {
+      more = walk.find(p, i, t);
+      if (!more) t.n = -1;
+      if (lane == 0) {
+        if (j >= kJobs) ok = tc::barrier_wait(bar(bars.job_empty[j % kJobs]), (j / kJobs - 1) & 1u, gave_up);
+        if (ok) {
+          const int64_t scales = t.e * p.expert_scales;
+          bars.job[j % kJobs] = Job{t, t.e * p.N + t.r0, scales + t.r0 / kRows * row_bytes,
+                                    scales + (p.cols + t.r0) / kRows * row_bytes, t.padded / kRows * row_bytes};
+          tc::barrier_arrive(bar(bars.job_full[j % kJobs]));
+        }
+      }
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+    }
   } else if (warp >= kFirstEpilogue) {
     // ---------------------------------------------------------- epilogue
     // A warp has a quarter of the rows and one or two chunks of 32 tokens, whose
@@ -592,10 +623,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = (warp - kFirstEpilogue) >> 2, quarter = warp & 3;
     const uint32_t from = static_cast<uint32_t>(quarter * 32) << 16;
     bool ok = true;
-    for (uint32_t tiles = 0; ok; ++tiles) {
-      ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.tile_full[tiles & 1u]), tiles >> 1 & 1u, gave_up));
+    for (uint32_t j = 0; ok; ++j) {
+      ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.job_full[j % kJobs]), j / kJobs & 1u, gave_up));
       if (!ok) break;
-      t = bars.tile[tiles & 1u];
+      t = bars.job[j % kJobs].t;
+      __syncwarp();
+      if (lane == 0) tc::barrier_arrive(bar(bars.job_empty[j % kJobs]));
       if (t.n < 0) break;
       const int n = t.r0 + quarter * 32 + lane;
       const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
@@ -606,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // gated: of the first half, then of the second
       float sums[64];
       if (p.stages > 0) {
-        ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.sums_full), tiles & 1u, gave_up));
+        ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.sums_full), j & 1u, gave_up));
         tc::fence_after();
         tc::load32(from + group * 32, sums);
-        tc::load32(from + 128 + group * 32, sums + 32);
+        tc::load32(from + kSecond + group * 32, sums + 32);
         tc::load_wait();
         if (!ok) {  // there is no result: NaN says so
 #pragma unroll
@@ -648,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (ranks > 1) {
     __syncwarp();
     cluster_sync();
-    if (warp >= kFirstEpilogue && bars.tile[0].n > 0) {  // a cluster has one tile or none
-      t = bars.tile[0];
+    if (warp >= kFirstEpilogue && bars.job[0].t.n > 0) {  // a cluster has one tile or none
+      t = bars.job[0].t;
       // each rank finishes every ranks-th group of tokens, its 128 threads every
       // fourth of those, all of a group's loads in flight
       constexpr int kGroup = 8;
@@ -737,7 +770,7 @@ cudaError_t map_codes(CUtensorMap* map, const uint8_t* codes, int64_t rows, int6
 template <bool kNv, bool kGated, bool kF16, bool kAdd>
 cudaError_t launch_typed(const CUtensorMap& x_map, const CUtensorMap& w_map, const GemmParams& p, int64_t tiles,
                          cudaStream_t stream) {
-  constexpr int kBytes = Layout<kNv>::kBytes + 1024;  // to a multiple of 1024
+  constexpr int kBytes = kRingBytes + 1024;  // the ring begins at a multiple of 1024
   static std::atomic<uint64_t> ready{0};
   if (const cudaError_t e = allow_smem(gemm_kernel<kNv, kGated, kF16, kAdd>, kBytes, ready); e != cudaSuccess) return e;
   // clusters that share a tile's K: as many CTAs as the SMs hold, a stage each
@@ -792,18 +825,25 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
   debug_range(p.more.dbg, kDbgGlobals, a.globals, a.nvfp4 ? a.E * 4 : 0);
 #endif
   // Rows to a copy of x: many in one where experts have many, few where whole
-  // boxes would be other experts' rows.
+  // boxes would be other experts' rows.  Tiles of 128 tokens where there are no more:
+  // their stages are smaller, and more of them are under way (64 tokens by 7168 x 7168
+  // 11.0 -> 10.7 us).  Not where experts have that many on average: some have more, and
+  // twice the tiles (2000 tokens' 8 routes to 128 experts, down products 38 -> 42).
   const int64_t average = a.offsets ? a.rows / (a.E > 0 ? a.E : 1) : a.rows;
   p.box_rows = average > 64 ? 128 : 32;
+  p.tile_tokens = gated || a.rows <= 128 ? 128 : 256;
+  const int64_t slab_rows = std::min<int64_t>(p.tile_tokens, (a.rows + p.box_rows - 1) / p.box_rows * p.box_rows);
+  p.scales_at = static_cast<uint32_t>((gated ? 2 : 1) * kSlab + slab_rows * kStageBytes);
+  p.stage_bytes = p.scales_at + (gated ? 4 : 3) * (a.nvfp4 ? Layout<true>::kScales : Layout<false>::kScales);
+  p.ring_stages = std::min<uint32_t>(kMaxStages, kRingBytes / p.stage_bytes);
   CUtensorMap x_map{}, w_map{};
   if (a.K > 0 && a.rows > 0 && a.N > 0 && a.E > 0) {
     if (const cudaError_t e = map_codes(&x_map, a.x_codes, a.rows, a.K, p.box_rows); e != cudaSuccess) return e;
     if (const cudaError_t e = map_codes(&w_map, a.codes, a.E * a.N, a.K, kRows); e != cudaSuccess) return e;
   }
   // at most this many tiles: every expert with rows may have one that is not full
-  const int64_t tokens = gated ? 128 : 256;
-  const int64_t token_tiles = a.offsets ? a.rows / tokens + (a.rows < a.E ? a.rows : a.E)
-                                        : (a.rows + tokens - 1) / tokens;
+  const int64_t token_tiles = a.offsets ? a.rows / p.tile_tokens + (a.rows < a.E ? a.rows : a.E)
+                                        : (a.rows + p.tile_tokens - 1) / p.tile_tokens;
   int64_t tiles = token_tiles * p.row_tiles;
   if (tiles < 1) tiles = 1;  // the status word alone
   using std::false_type, std::true_type;
