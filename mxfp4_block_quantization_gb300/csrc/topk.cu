@@ -115,7 +115,10 @@ __device__ __forceinline__ float warp_sum(float x) {
 // adds (E / 32 + 5) 2^-24.  The addition of the bias is off by 2^-24 of the pick.
 __device__ __forceinline__ float pick32(const TopkParams& p, float l, float b, float top,
                                         float inv_sum) {
-  const float s = p.sigmoid ? __fdividef(1.0f, 1.0f + __expf(-l)) : __expf(l - top) * inv_sum;
+  if (!p.sigmoid) return fmaf(__expf(l - top), inv_sum, b);
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
   return s + b;
 }
 // Twice what two neighbours of at most `m` may be off by together.
@@ -247,23 +250,40 @@ __device__ __forceinline__ void take(uint32_t* gone, int e) {
   __syncwarp();
 }
 
-// Of the groups in `near`, the `count` best by their values in 64 bits.
+// Of the groups in `near`, the `count` best by their values in 64 bits: of those
+// of a group's `held` picks that may be its best (or two best) in exact terms.
+// Lane g: group g's best pick, or with group sums its second (kOut: it has one).
 template <LogitType kType>
-__device__ __forceinline__ uint32_t best_groups_exactly(const TopkParams& p, Exact x, uint32_t near, int count) {
+__device__ __forceinline__ uint32_t best_groups_exactly(const TopkParams& p, Exact x, const float* held, float lowest,
+                                                     uint32_t near, int count) {
   const int lane = threadIdx.x & 31;
   if (!p.sigmoid) x.inv_sum64 = softmax_inverse<kType>(p, x.row, x.top);
-  double mine = 0.0, value;
+  constexpr double kNone = -1.7976931348623157e308;
+  double mine = kNone;
   bool open = false;
   for (uint32_t rest = near; rest != 0; rest &= rest - 1) {
-    const int g = __ffs(rest) - 1, lo = g * p.size, hi = lo + p.size;
-    none_gone(p, x.gone);
-    const int first = best_exactly<kType>(p, x, lo, hi, value);
-    double total = value;
-    if (first >= 0 && p.group_sum2) {
-      take(x.gone, first);
-      if (best_exactly<kType>(p, x, lo, hi, value) >= 0) total += value;
+    const int g = __ffs(rest) - 1;
+    const float low = __shfl_sync(kAll, lowest, g);
+    const float from = low != kOut ? low - tolerance(p, low) : kOut;
+    double first = kNone, second = kNone;
+    for (int i = lane; i < p.size; i += 32) {
+      const int e = g * p.size + i;
+      const float v = held[e];
+      if (v == kOut || v < from) continue;
+      const double d = pick64(p, x, logit_at<kType>(p, x.row, e), bias_at(p, e));
+      second = fmax(second, fmin(first, d));
+      first = fmax(first, d);
     }
-    if (lane == g) mine = total, open = first >= 0;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      const double a = __shfl_xor_sync(kAll, first, d), b = __shfl_xor_sync(kAll, second, d);
+      second = fmax(fmin(first, a), fmax(second, b));
+      first = fmax(first, a);
+    }
+    if (lane == g) {
+      open = first != kNone;
+      mine = p.group_sum2 && second != kNone ? first + second : first;
+    }
   }
   uint32_t kept = 0;
   for (int j = 0; j < count; ++j) {
@@ -328,9 +348,12 @@ __device__ __forceinline__ int order_exactly(const TopkParams& p, Exact x, int i
 // A lane's key i is that of expert expert_of(i): with kVec == 4 four consecutive
 // experts in a load, else one.
 template <int kVec>
+__device__ __forceinline__ int key_part(int i) {
+  return kVec == 4 ? (i >> 2) * 128 + (i & 3) : i * 32;
+}
+template <int kVec>
 __device__ __forceinline__ int expert_of(int i) {
-  const int lane = threadIdx.x & 31;
-  return kVec == 4 ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane;
+  return key_part<kVec>(i) + static_cast<int>(threadIdx.x & 31) * kVec;
 }
 // The logits (infinity: no expert) or biases of keys i to i + kVec - 1.
 template <int kVec, LogitType kType>
@@ -461,6 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
       b = fmaxf(fminf(a, oa), fmaxf(b, ob));
       a = fmaxf(a, oa);
     }
+    const float lowest = p.group_sum2 && b != kOut ? b : a;
     float size = a != kOut ? fabsf(a) : 0.0f;
     if (p.group_sum2 && b != kOut) size += fabsf(b), a += b;
     // a group to a lane: those before it are larger, or equal and of a lower index
@@ -480,15 +504,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
       if (first_out != kOut && border - first_out <= tol) {
         const uint32_t near = __ballot_sync(kAll, open && fabsf(mine - border) <= 2.0f * tol);
         const uint32_t sure = kept & ~near;
-        kept = sure | best_groups_exactly<kType>(p, x, near, p.top_groups - __popc(sure));
+        const float low = __shfl_sync(kAll, lowest, lane < p.groups ? lane * lanes : 0);
+        kept = sure | best_groups_exactly<kType>(p, x, held, low, near, p.top_groups - __popc(sure));
       }
     }
     x.kept = kept;
     // (read again: nothing is held over the calls above)
+    if (kVec == 4 && kPer > 0 && (p.size & 3) == 0) {  // four experts of a load are of one group
 #pragma unroll
-    for (int i = 0; i < picks.count(); ++i) {
-      const int e = expert_of<kVec>(i);
-      picks.set(i, e < p.E && ((kept >> group_of(p, e)) & 1u) ? held[e] : kOut);
+      for (int i = 0; i < kPer; i += 4) {
+        const int e = expert_of<kVec>(i);
+        const bool in_kept = e < p.E && ((kept >> group_of(p, e)) & 1u);
+        const float4 v = in_kept ? *reinterpret_cast<const float4*>(held + e) : make_float4(kOut, kOut, kOut, kOut);
+        picks.set(i, v.x), picks.set(i + 1, v.y), picks.set(i + 2, v.z), picks.set(i + 3, v.w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < picks.count(); ++i) {
+        const int e = expert_of<kVec>(i);
+        picks.set(i, e < p.E && ((kept >> group_of(p, e)) & 1u) ? held[e] : kOut);
+      }
     }
   }
 
@@ -501,9 +536,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
     const float k = picks.get(i);
     const bool first = k > best, second = k > next;
     next = fminf(fmaxf(k, next), best);
-    next_i = first ? best_i : second ? i : next_i;
+    next_i = first ? best_i : second ? key_part<kVec>(i) : next_i;
     best = fmaxf(k, best);
-    best_i = first ? i : best_i;
+    best_i = first ? key_part<kVec>(i) : best_i;
   }
   bool near = false, many = false;
   float last = 0.0f, kth = 0.0f;
@@ -521,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
       if (found > 0) near |= last - m <= tolerance(p, last);
       last = m;
     }
-    const int mine = best == m ? expert_of<kVec>(best_i) : INT32_MAX;
+    const int mine = best == m ? best_i + lane * kVec : INT32_MAX;  // (best_i: key_part)
     const int e = __reduce_min_sync(kAll, mine);
     if (lane == found) id = e;
     if (++found == p.top_k) {
@@ -539,12 +574,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_topk_kernel(const TopkParams 
 #pragma unroll
         for (int i = 0; i < picks.count(); ++i) {
           float k = picks.get(i);
-          k = k < limit || (k == limit && i > limit_i) ? k : kOut;
+          k = k < limit || (k == limit && key_part<kVec>(i) > limit_i) ? k : kOut;
           const bool first = k > best, second = k > next;
           next = fminf(fmaxf(k, next), best);
-          next_i = first ? best_i : second ? i : next_i;
+          next_i = first ? best_i : second ? key_part<kVec>(i) : next_i;
           best = fmaxf(k, best);
-          best_i = first ? i : best_i;
+          best_i = first ? key_part<kVec>(i) : best_i;
         }
         fresh = true;
       }
