@@ -4,8 +4,8 @@
   q, k, v   = three products of the normalised token with MXFP4 weights
   cache     <- k, v quantized into the sequence's next slot
   attention over the paged cache, its output product added to the token
-  router    -> the top experts; mxfp4_moe_route sorts the routes
-  experts   = gate/up products, SiLU gate, down products, weighted sum
+  router    -> the top experts and their weights; mxfp4_moe_route sorts the routes
+  experts   = gate/up products, SiLU gate, down products, their weighted sum
 
 Run it on a GPU:  python examples/decode_step.py
 It prints how far the step is from the same step in plain float32 torch on the
@@ -87,15 +87,14 @@ class DecodeStep:
         x = x + mx.matvec(o.view(B, -1), *self.wo)
 
         h = torch.nn.functional.rms_norm(x, (c.hidden,))
-        weights, ids = torch.softmax(h.float() @ self.router.float().T, -1).topk(c.top_k, -1)
-        self.chosen = ids
-        offsets, dest, rows, _ = mx.moe_route(ids.to(torch.int32), c.experts)
+        ids, weights = mx.moe_topk(h.float() @ self.router.float().T, c.top_k, renormalize=False)
+        self.chosen = ids.long()
+        offsets, dest, rows, _ = mx.moe_route(ids, c.experts)
         gate_up, _ = mx.moe_matvec(h, rows, offsets, *self.w13)
         gate, up = gate_up.chunk(2, -1)
         y, _ = mx.moe_matvec((torch.nn.functional.silu(gate) * up).contiguous(), None, offsets,
                              *self.w2, out_dtype=torch.float32)
-        out = (y[dest.long()] * weights.unsqueeze(-1)).sum(1)
-        return x + out.to(x.dtype)
+        return mx.moe_combine(y, dest, weights, residual=x)[0]
 
     def plain(self, x, k_cache, v_cache):
         """The last step in float32 on the dequantized weights, with the experts
