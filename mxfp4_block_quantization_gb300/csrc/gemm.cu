@@ -231,18 +231,20 @@ __device__ __forceinline__ void activate(float (&z)[kCount], int act) {
   }
 }
 
-// What a thread's row of the weights adds and scales: z = sum * alpha + bias.
+// What a thread's row of the weights adds and scales: z = sum * alpha * beta + bias,
+// the inverses of the global scales one after another: their product may overflow
+// beside a sum of zero.
 struct RowTerms {
-  float alpha, bias, other_bias;  // `other`: of the second half
+  float alpha, beta, bias, other_bias;  // `other`: of the second half
 };
 template <bool kNv, bool kGated, bool kF16>
 __device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t, int n) {
-  RowTerms r{1.0f, 0.0f, 0.0f};
+  RowTerms r{1.0f, 1.0f, 0.0f, 0.0f};
   if constexpr (kNv) {
     if (p.steps > 0) {
       const float a = MXFP4_IN_BOUNDS(p, kDbgXGlobals, p.x_globals + t.e, 4) ? __ldg(p.x_globals + t.e) : 1.0f;
       const float b = MXFP4_IN_BOUNDS(p.more, kDbgGlobals, p.globals + t.e, 4) ? __ldg(p.globals + t.e) : 1.0f;
-      r.alpha = (1.0f / a) * (1.0f / b);
+      r.alpha = 1.0f / a, r.beta = 1.0f / b;
     }
   }
   if (p.bias != nullptr && n < p.cols) {
@@ -261,10 +263,10 @@ template <bool kGated, int kCount>
 __device__ __forceinline__ void finish(const GemmParams& p, const RowTerms& r, float (&v)[kCount],
                                        float (&u)[kCount]) {
 #pragma unroll
-  for (int j = 0; j < kCount; ++j) v[j] = fmaf(v[j], r.alpha, r.bias);
+  for (int j = 0; j < kCount; ++j) v[j] = fmaf(v[j] * r.alpha, r.beta, r.bias);
   if constexpr (kGated) {
 #pragma unroll
-    for (int j = 0; j < kCount; ++j) u[j] = fmaf(u[j], r.alpha, r.other_bias);
+    for (int j = 0; j < kCount; ++j) u[j] = fmaf(u[j] * r.alpha, r.beta, r.other_bias);
     if (p.gate_second) activate(u, p.activation);
     else activate(v, p.activation);
 #pragma unroll
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::barrier_init_fence();
     bars.gave_up = 0;
     bars.job[0].t.n = -1;
-    if (p.stages > 0) tc::prefetch_map(&x_map), tc::prefetch_map(&w_map);
+    if (p.stages > 0 && p.rows > 0 && p.E > 0 && p.N > 0) tc::prefetch_map(&x_map), tc::prefetch_map(&w_map);
   }
   if (warp == 1) tc::allocate(tc::shared_address(&bars.columns), kColumns);
   tc::fence_before();

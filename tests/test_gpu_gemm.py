@@ -137,6 +137,22 @@ def test_a_scale_of_nan_stays_in_its_row(mx, nv, T):
     assert torch.equal(torch.isnan(y), want)
 
 
+@pytest.mark.parametrize("T", [5, 140])
+def test_global_scales_far_apart(mx, T):
+    """Global scales whose product, or its inverse, no float32 holds: sums of zero
+    stay zero, and the others are what two divisions make of them."""
+    g = gen(15)
+    K, N = 128, 40
+    (xc, xs), (wc, ws) = operand(T, K, True, g), operand(N, K, True, g)
+    xc[1], wc[3] = 0, 0
+    for a, b in ((2.0 ** -100, 2.0 ** -100), (2.0 ** 100, 2.0 ** -100), (2.0 ** 70, 2.0 ** 80)):
+        ga, gb = torch.tensor([a], device="cuda"), torch.tensor([b], device="cuda")
+        y = mx.gemm_nvfp4(xc, xs, ga, wc, ws, gb)
+        want, bound = L.gemm(R.weights(xc, xs, True), R.weights(wc, ws, True), BF)
+        L.close(y, want / a / b, bound / a / b + R.smallest(BF) + 2.0 ** -126)
+        assert (y[1] == 0).all() and (y[:, 3] == 0).all()
+
+
 def test_strides_and_places(mx):
     """y and the residual at odd addresses with odd strides, and the residual in y."""
     g = gen(11)
