@@ -891,10 +891,12 @@ def _address(name, t, device, dtype, nbytes):
     on ``device`` that holds at least ``nbytes``."""
     if t is None:
         return None
-    if (isinstance(t, torch.Tensor) and t.get_device() == device >= 0 and
-            (dtype is None or t.dtype is dtype) and t.is_contiguous() and
-            t.numel() * t.element_size() >= nbytes):
-        return t.data_ptr()
+    try:
+        if (t.get_device() == device and (dtype is None or t.dtype is dtype) and
+                t.is_contiguous() and t.numel() * t.element_size() >= nbytes):
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if _device_index(name, t) != device:  # says what is wrong
         raise ValueError(f"all tensors must be on the same CUDA device, {name} is on {t.device}")
     if dtype is not None and t.dtype is not dtype:

@@ -258,6 +258,18 @@ __device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t
   return r;
 }
 
+// Activation and gate of z = v (u: the second half's), in place.
+template <bool kGated, int kCount>
+__device__ __forceinline__ void activate_gate(const GemmParams& p, float (&v)[kCount], float (&u)[kCount]) {
+  if constexpr (kGated) {
+    if (p.gate_second) activate(u, p.activation);
+    else activate(v, p.activation);
+#pragma unroll
+    for (int j = 0; j < kCount; ++j) v[j] *= u[j];
+  } else {
+    activate(v, p.activation);
+  }
+}
 // kCount tokens' sums v (u: the second half's) finished in place, but for the residual.
 template <bool kGated, int kCount>
 __device__ __forceinline__ void finish(const GemmParams& p, const RowTerms& r, float (&v)[kCount],
@@ -267,13 +279,8 @@ __device__ __forceinline__ void finish(const GemmParams& p, const RowTerms& r, f
   if constexpr (kGated) {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) u[j] = fmaf(u[j] * r.alpha, r.beta, r.other_bias);
-    if (p.gate_second) activate(u, p.activation);
-    else activate(v, p.activation);
-#pragma unroll
-    for (int j = 0; j < kCount; ++j) v[j] *= u[j];
-  } else {
-    activate(v, p.activation);
   }
+  activate_gate<kGated>(p, v, u);
 }
 
 // A thread's kSome tokens of column n from column c of the tile on, two tokens to a
@@ -621,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kChunks = kTokens / 128;
     // tokens finished at a time: as many as the registers hold (16 for 8: a tile's
     // epilogue 3.0 -> 2.2 us)
-    constexpr int kSome = (kGated ? 8 : 16) / (kAdd ? 2 : 1);
+    constexpr int kSome = (kGated ? 8 : 16) / (kAdd ? kNv && !kGated ? 4 : 2 : 1);
     const int group = (warp - kFirstEpilogue) >> 2, quarter = warp & 3;
     const uint32_t from = static_cast<uint32_t>(quarter * 32) << 16;
     bool ok = true;
@@ -685,45 +692,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync();
     if (warp >= kFirstEpilogue && bars.job[0].t.n > 0) {  // a cluster has one tile or none
       t = bars.job[0].t;
-      // each rank finishes every ranks-th group of tokens, its 128 threads every
-      // fourth of those, all of a group's loads in flight
-      constexpr int kGroup = 8;
-      const int thread = threadIdx.x - kFirstEpilogue * 32, row = thread & (kRows - 1), n = t.r0 + row;
-      const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
-      for (int c = (rank + ranks * (thread >> 7)) * kGroup; c < t.n; c += 4 * ranks * kGroup) {
-        float v[kGroup] = {}, u[kGroup] = {};
-        for (uint32_t r = 0; r < ranks; ++r) {
-          const uint32_t at = cluster_address(ring, r) + (c * kRows + row) * 4;
-          float a[kGroup], b[kGroup];
+      // Each rank finishes every ranks-th token, a warp of it every 16th of those, a
+      // thread four rows: the parts of all ranks in flight at once, added in order.
+      constexpr int kSome = 4, kMaxRanks = 8;
+      const int n = t.r0 + lane * kSome;
+      RowTerms terms[kSome];
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j) {
-            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(a[j]) : "r"(at + j * kRows * 4) : "memory");
-            if constexpr (kGated)
-              asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(b[j]) : "r"(at + (kTokens + j) * kRows * 4) : "memory");
+      for (int j = 0; j < kSome; ++j) terms[j] = row_terms<kNv, kGated, kF16>(p, t, n + j);
+      for (int c = rank + ranks * (warp - kFirstEpilogue); c < t.n; c += ranks * kEpilogueWarps) {
+        float4 a[kMaxRanks], b[kMaxRanks];
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxRanks; ++r)
+          if (r < ranks) {
+            const uint32_t at = cluster_address(ring, r) + (c * kRows + lane * kSome) * 4;
+            a[r] = ld_cluster_f4(at);
+            if constexpr (kGated) b[r] = ld_cluster_f4(at + kTokens * kRows * 4);
+          }
+        float v[kSome] = {}, u[kSome] = {};
+#pragma unroll
+        for (uint32_t r = 0; r < kMaxRanks; ++r)
+          if (r < ranks) {
+            v[0] += a[r].x, v[1] += a[r].y, v[2] += a[r].z, v[3] += a[r].w;
+            if constexpr (kGated) u[0] += b[r].x, u[1] += b[r].y, u[2] += b[r].z, u[3] += b[r].w;
           }
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j) {
-            v[j] += a[j];
-            if constexpr (kGated) u[j] += b[j];
-          }
+        for (int j = 0; j < kSome; ++j) {
+          v[j] = fmaf(v[j] * terms[j].alpha, terms[j].beta, terms[j].bias);
+          if constexpr (kGated) u[j] = fmaf(u[j] * terms[j].alpha, terms[j].beta, terms[j].other_bias);
         }
-        finish<kGated>(p, terms, v, u);
+        activate_gate<kGated>(p, v, u);
         if constexpr (kAdd) {
-          uint16_t r[kGroup];
+          const uint16_t* const at = p.residual + (t.row + c) * p.ldr + n;
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j) {
-            const uint16_t* const at = p.residual + (t.row + c + j) * p.ldr + n;
-            r[j] = 0;
-            if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at, 2)) r[j] = *at;
-          }
-#pragma unroll
-          for (int j = 0; j < kGroup; ++j) v[j] += widen<kF16>(r[j]);
+          for (int j = 0; j < kSome; ++j)
+            if (n + j < p.cols && MXFP4_IN_BOUNDS(p, kDbgResidual, at + j, 2)) v[j] += widen<kF16>(at[j]);
         }
+        uint16_t* const at = p.y + (t.row + c) * p.ldy + n;
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
-          uint16_t* const at = p.y + (t.row + c + j) * p.ldy + n;
-          if (c + j < t.n && n < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at, 2))
-            *at = static_cast<uint16_t>(narrow2<kF16>(v[j], 0.0f));
+        for (int j = 0; j < kSome; j += 2) {
+          const uint32_t word = narrow2<kF16>(v[j], v[j + 1]);
+          if (p.paired) {
+            if (n + j < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at + j, 4)) *reinterpret_cast<uint32_t*>(at + j) = word;
+          } else {
+            if (n + j < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at + j, 2)) at[j] = static_cast<uint16_t>(word);
+            if (n + j + 1 < p.cols && MXFP4_IN_BOUNDS(p, kDbgY, at + j + 1, 2)) at[j + 1] = static_cast<uint16_t>(word >> 16);
+          }
         }
       }
     }
@@ -827,13 +840,15 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
   debug_range(p.more.dbg, kDbgGlobals, a.globals, a.nvfp4 ? a.E * 4 : 0);
 #endif
   // Rows to a copy of x: many in one where experts have many, few where whole
-  // boxes would be other experts' rows.  Tiles of 128 tokens where there are no more:
-  // their stages are smaller, and more of them are under way (64 tokens by 7168 x 7168
-  // 11.0 -> 10.7 us).  Not where experts have that many on average: some have more, and
-  // twice the tiles (2000 tokens' 8 routes to 128 experts, down products 38 -> 42).
+  // boxes would be other experts' rows.  Tiles of 128 tokens where
+  // the SMs hold them all: a tile is done sooner, and its stages are smaller (512 tokens
+  // by 2881 x 2880 12.9 -> 9.5 us; 600 by 4096 x 4096, 160 of them, 13.3 -> 15.3).  Not
+  // for experts with fewer tokens on average: some have more, and twice the tiles (2000
+  // tokens' 8 routes to 128 experts, down products 38 -> 42).
   const int64_t average = a.offsets ? a.rows / (a.E > 0 ? a.E : 1) : a.rows;
   p.box_rows = average > 64 ? 128 : 32;
-  p.tile_tokens = gated || a.rows <= 128 ? 128 : 256;
+  const bool few = !a.offsets && (a.rows + 127) / 128 * p.row_tiles <= sm_count();
+  p.tile_tokens = gated || few ? 128 : 256;
   const int64_t slab_rows = std::min<int64_t>(p.tile_tokens, (a.rows + p.box_rows - 1) / p.box_rows * p.box_rows);
   p.scales_at = static_cast<uint32_t>((gated ? 2 : 1) * kSlab + slab_rows * kStageBytes);
   p.stage_bytes = p.scales_at + (gated ? 4 : 3) * (a.nvfp4 ? Layout<true>::kScales : Layout<false>::kScales);
