@@ -204,11 +204,20 @@ __device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
   return kF16 ? pack_f16x2(lo, hi) : cvt_bf16x2(lo, hi);
 }
 
-// By the fast exponential and division: off by 2^-21 of |z| (see pick32 in
-// topk.cu for z's sigmoid), which a later rounding to 16 bits hides.
-__device__ __forceinline__ float sigmoid_times(float z, float u) {  // z / (1 + e^-u)
-  return __fdividef(z, 1.0f + __expf(-u));
+// The fast exponential and inverse (2^-22 and 2^-23 off), results below 2^-126 as 0.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
 }
+__device__ __forceinline__ float fast_inverse(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// z / (1 + e^-u): off by 2^-21 of |z| (see pick32 in topk.cu), which a later rounding
+// to 16 bits hides.
+__device__ __forceinline__ float sigmoid_times(float z, float u) { return z * fast_inverse(1.0f + fast_exp(-u)); }
 template <int kCount>
 __device__ __forceinline__ void activate(float (&z)[kCount], int act) {
   if (act == MXFP4_ACT_SILU) {
@@ -221,12 +230,12 @@ __device__ __forceinline__ void activate(float (&z)[kCount], int act) {
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
       const float x = fabsf(z[j]) * 0.70710678118654752f;
-      const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+      const float t = fast_inverse(fmaf(0.3275911f, x, 1.0f));
       float q = fmaf(t, 1.061405429f, -1.453152027f);
       q = fmaf(t, q, 1.421413741f);
       q = fmaf(t, q, -0.284496736f);
       q = fmaf(t, q, 0.254829592f);
-      q *= t * __expf(-x * x);
+      q *= t * fast_exp(-x * x);
       const float tail = q > 0.0f ? 0.5f * z[j] * q : 0.0f;  // of infinite z as well
       z[j] = z[j] < 0.0f ? tail : z[j] - tail;
     }
