@@ -914,8 +914,9 @@ int mxfp4_moe_topk_f32(const void* logits, int64_t num_tokens, int32_t E, int64_
  *              (checked on the device).  Rows of y from o[E] on are not written.
  * x_global_scales, global_scales  (NVFP4) DEVICE float32 [E].
  * codes, scales, bias  E consecutive ones; E <= MXFP4_ROUTE_MAX_EXPERTS.
- * status       DEVICE int32 or NULL, out: MXFP4_OK, or MXFP4_EOFFSETS (y is then
- *              not written). */
+ * status       DEVICE int32 or NULL, out: MXFP4_OK, MXFP4_EOFFSETS (y is then not
+ *              written), or MXFP4_ECUDA where a wait inside the kernel ran out
+ *              after about two seconds (a part of y is then NaN or not written). */
 #define MXFP4_ACT_NONE 0
 #define MXFP4_ACT_SILU 1
 #define MXFP4_ACT_GELU 2
