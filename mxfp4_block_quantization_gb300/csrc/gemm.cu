@@ -247,22 +247,45 @@ __device__ __forceinline__ void activate(float (&z)[kCount], int act) {
   }
 }
 
-// What a thread's row of the weights adds and scales: z = sum * alpha * beta + bias,
-// the inverses of the global scales one after another: their product may overflow
-// beside a sum of zero.
+// 1 / (a b), the global scales' inverse, as alpha * beta for sum * alpha * beta: neither
+// overflows or vanishes where the result does not (sum * 1/a * 1/b would: a sum of 2^20
+// beside 2^-120 and 2^120).  The mantissas' part and half of the exponent are alpha, the
+// other half is beta; off by 2^-24 for the product and 2^-23 for its inverse.  A sum of E2M1 and E4M3 products
+// is 0 or 2^-20 to 2^53, so past 2^240 and 2^-240 nothing changes, and a sum of zero
+// stays zero beside any of them.
+struct Scaling {
+  float alpha, beta;
+};
+// A number's mantissa in [1, 2) with its sign, its exponent (biased by 127) taken from
+// `e`; 0, infinity and NaN are their own mantissas.
+__device__ __forceinline__ float mantissa_of(float a, int& e) {
+  if (fabsf(a) < 0x1p-126f) a *= 0x1p64f, e += 64;
+  const int bits = __float_as_int(a), field = (bits >> 23) & 255;
+  e -= field;
+  return field == 0 || field == 255 ? a : __int_as_float((bits & 0x807FFFFF) | 0x3F800000);
+}
+__device__ __forceinline__ Scaling scaling_of(float a, float b) {
+  int e = 2 * 127;
+  const float ma = mantissa_of(a, e), mb = mantissa_of(b, e), m = fast_inverse(ma * mb);
+  e = max(-240, min(240, e));
+  const int half = e >> 1;
+  const auto power = [](int n) { return __int_as_float((n + 127) << 23); };
+  return Scaling{m * power(half), power(e - half)};
+}
+
+// What a thread's row of the weights adds and scales: z = sum * alpha * beta + bias.
 struct RowTerms {
   float alpha, beta, bias, other_bias;  // `other`: of the second half
 };
-template <bool kNv, bool kGated, bool kF16>
-__device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t, int n) {
-  RowTerms r{1.0f, 1.0f, 0.0f, 0.0f};
-  if constexpr (kNv) {
-    if (p.steps > 0) {
-      const float a = MXFP4_IN_BOUNDS(p, kDbgXGlobals, p.x_globals + t.e, 4) ? __ldg(p.x_globals + t.e) : 1.0f;
-      const float b = MXFP4_IN_BOUNDS(p.more, kDbgGlobals, p.globals + t.e, 4) ? __ldg(p.globals + t.e) : 1.0f;
-      r.alpha = 1.0f / a, r.beta = 1.0f / b;
-    }
-  }
+template <bool kNv>
+__device__ __forceinline__ Scaling scaling(const GemmParams& p, int e) {
+  if (!kNv || p.steps == 0) return Scaling{1.0f, 1.0f};
+  return scaling_of(MXFP4_IN_BOUNDS(p, kDbgXGlobals, p.x_globals + e, 4) ? __ldg(p.x_globals + e) : 1.0f,
+                    MXFP4_IN_BOUNDS(p.more, kDbgGlobals, p.globals + e, 4) ? __ldg(p.globals + e) : 1.0f);
+}
+template <bool kGated, bool kF16>
+__device__ __forceinline__ RowTerms row_terms(const GemmParams& p, const Tile& t, int n, Scaling g) {
+  RowTerms r{g.alpha, g.beta, 0.0f, 0.0f};
   if (p.bias != nullptr && n < p.cols) {
     const uint16_t* at = p.bias + static_cast<int64_t>(t.e) * p.N + n;
     r.bias = MXFP4_IN_BOUNDS(p, kDbgBias, at, 2) ? widen<kF16>(__ldg(at)) : 0.0f;
@@ -656,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) tc::barrier_arrive(bar(bars.job_empty[j % kJobs]));
       if (t.n < 0) break;
       const int n = t.r0 + quarter * 32 + lane;
-      const RowTerms terms = row_terms<kNv, kGated, kF16>(p, t, n);
+      const RowTerms terms = row_terms<kGated, kF16>(p, t, n, scaling<kNv>(p, t.e));
       if (kAdd && ranks == 1) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) prefetch_residual(p, t, t.r0 + quarter * 32, group * 32 + 128 * c);
@@ -713,8 +736,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kSome = 4, kMaxRanks = 8;
       const int n = t.r0 + lane * kSome;
       RowTerms terms[kSome];
+      const Scaling g = scaling<kNv>(p, t.e);
 #pragma unroll
-      for (int j = 0; j < kSome; ++j) terms[j] = row_terms<kNv, kGated, kF16>(p, t, n + j);
+      for (int j = 0; j < kSome; ++j) terms[j] = row_terms<kGated, kF16>(p, t, n + j, g);
       for (int c = rank + ranks * (warp - kFirstEpilogue); c < t.n; c += ranks * kEpilogueWarps) {
         float4 a[kMaxRanks], b[kMaxRanks];
 #pragma unroll
