@@ -898,7 +898,9 @@ int mxfp4_moe_topk_f32(const void* logits, int64_t num_tokens, int32_t E, int64_
  * codes, scales  the same of W: [N, K/2] and its tiled scales.
  * bias         BF16 (_f16: binary16) [N] or NULL.
  * activation   MXFP4_ACT_NONE, _SILU (z / (1 + e^-z)), _GELU (by erf) or
- *              _GELU_TANH (0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))).
+ *              _GELU_TANH (0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))), in
+ *              float32, off by 2^-14 of the result at most; results below 2^-119
+ *              may be 0.
  * residual     BF16 (_f16: binary16) [num_tokens, columns of y], row stride ldr
  *              elements, or NULL.  It may be y itself (with ldr == ldy).
  * y            BF16 (_f16: binary16), row stride ldy elements.

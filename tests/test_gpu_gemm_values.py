@@ -1,11 +1,13 @@
 """Products of 4-bit operands at values where a float32 step could leave the
-formula: global scales far apart."""
+formula: global scales far apart, activations where they are small."""
+import math
+
 import pytest
 import torch
 
 import decode_reference as R
 import layer_reference as L
-from test_gpu_gemm import BF, gen, operand
+from test_gpu_gemm import BF, FP, gen, operand
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +51,49 @@ def test_global_scales_at_any_distance(mx, a, b, T, K, gate):
         assert (y[1] == 0).all() and (y[:, 3] == 0).all()
         there = torch.ones_like(y, dtype=torch.bool)
     L.close(y[there], z[there], (off + R.unit(BF) * (z.abs() + off) + R.smallest(BF))[there])
+
+
+def values(act):
+    lo = {"silu": -87.0, "gelu": -13.0, "gelu_tanh": -10.0}[act]
+    return torch.cat((torch.linspace(lo, 0, 1500), torch.linspace(0, 12, 500), -torch.logspace(-4, 0, 48)))
+
+
+def exactly(z, act):
+    """act(z) in 64 bits without cancellation: of the tails, not of 1 minus them."""
+    z = z.double()
+    if act == "silu":
+        return z / (1 + torch.exp(-z))
+    if act == "gelu":
+        return 0.5 * z * torch.special.erfc(-z * math.sqrt(0.5))
+    return z / (1 + torch.exp(-2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)))
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("gate", [None, "first", "second"])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_activations_relative_to_their_own_size(mx, act, gate, dtype):
+    """act(z) alone (no terms, z from the bias), relative to itself: a half step of
+    y's type and 2^-14.  The exponential's argument, up to 88, is off by 5.5 float32
+    roundings at most (2^-24 of it each: two of z^3, its factor, the sum, log2 e and its
+    product), 2^-15, and the rest by 2^-19.  An intermediate below 2^-126 may count as 0:
+    2^-119 of a result."""
+    z = values(act).to(dtype).cuda()
+    one = torch.ones_like(z)
+    bias = {None: z, "first": torch.cat((z, one)), "second": torch.cat((one, z))}[gate].contiguous()
+    T, N = 3, bias.numel()
+    none = torch.zeros(0, dtype=torch.uint8, device="cuda")
+    y = mx.gemm(none.new_zeros(T, 0), none, none.new_zeros(N, 0), none, bias=bias, activation=act, gate=gate,
+                out_dtype=dtype)
+    want = exactly(z, act).expand(T, -1)
+    bound = (R.unit(dtype) + 2.0 ** -14) * want.abs() + R.smallest(dtype) + 2.0 ** -119
+    R.close(y, want, bound)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_gelu_at_the_ends(mx, dtype):
+    """Infinities keep their limits, infinity and 0, and NaN stays NaN."""
+    bias = torch.tensor([math.inf, -math.inf, math.nan, 0.0, -0.0, 60000.0, -60000.0], dtype=dtype, device="cuda")
+    none = torch.zeros(0, dtype=torch.uint8, device="cuda")
+    y = mx.gemm(none.new_zeros(2, 0), none, none.new_zeros(7, 0), none, bias=bias, activation="gelu", out_dtype=dtype)
+    want = torch.tensor([math.inf, 0.0, math.nan, 0.0, 0.0, float(bias[5]), 0.0], device="cuda").expand(2, -1)
+    R.close(y, want, torch.zeros_like(want))
