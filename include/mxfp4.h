@@ -905,6 +905,9 @@ int mxfp4_moe_topk_f32(const void* logits, int64_t num_tokens, int32_t E, int64_
  *              elements, or NULL.  It may be y itself (with ldr == ldy).
  * y            BF16 (_f16: binary16), row stride ldy elements.
  * K == 0 leaves the epilogue's terms.
+ * Every wait inside the kernel ends: should one run out (after about two seconds,
+ * where the device has lost a copy or a product), the tiles of y whose CTA it was are
+ * NaN throughout.
  *
  * mxfp4_moe_gemm — the same per expert of a routed batch: row r of segment e
  * (expert_offsets[e] <= r < expert_offsets[e+1]) with expert e's weights, bias
@@ -918,7 +921,7 @@ int mxfp4_moe_topk_f32(const void* logits, int64_t num_tokens, int32_t E, int64_
  * codes, scales, bias  E consecutive ones; E <= MXFP4_ROUTE_MAX_EXPERTS.
  * status       DEVICE int32 or NULL, out: MXFP4_OK, MXFP4_EOFFSETS (y is then not
  *              written), or MXFP4_ECUDA where a wait inside the kernel ran out
- *              after about two seconds (a part of y is then NaN or not written). */
+ *              (see above: a part of y is then NaN). */
 #define MXFP4_ACT_NONE 0
 #define MXFP4_ACT_SILU 1
 #define MXFP4_ACT_GELU 2

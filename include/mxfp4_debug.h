@@ -24,6 +24,13 @@ extern "C" {
  * (and resets the count), or -1 when the synchronisation reports an error. */
 int64_t mxfp4_debug_bounds_violations(void);
 
+/* From the next call on, one role of the products' last CTA (mxfp4_gemm,
+ * mxfp4_moe_gemm) takes no step in that CTA's first tile: 1 the one that finds
+ * tiles, 2 the copies, 3 the products; 0: none.  The other roles' waits for it
+ * run out after about two seconds, as they would had the device lost a copy.
+ * Synchronises the current device, for which it is set. */
+int mxfp4_debug_stall_products(int32_t role);
+
 #ifdef __cplusplus
 }
 #endif

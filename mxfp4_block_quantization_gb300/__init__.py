@@ -225,6 +225,8 @@ def _load(path=LIB_PATH):
     if hasattr(L, "mxfp4_debug_bounds_violations"):
         L.mxfp4_debug_bounds_violations.restype = ctypes.c_int64
         L.mxfp4_debug_bounds_violations.argtypes = []
+        L.mxfp4_debug_stall_products.restype = ctypes.c_int
+        L.mxfp4_debug_stall_products.argtypes = [i32]
     return L
 
 

@@ -116,6 +116,18 @@ struct GemmParams {
   GemmMore more;
 };
 
+// Bounds build: which role of the last CTA takes no step in its first tile, so that the
+// others' waits for it run out.
+enum : int { kStallNone = 0, kStallTiles, kStallCopies, kStallProducts };
+#ifdef MXFP4_DEBUG_BOUNDS
+__device__ int g_debug_stall;
+__device__ __forceinline__ bool stalled(int role) {
+  return *const_cast<volatile int*>(&g_debug_stall) == role && blockIdx.x == gridDim.x - 1;
+}
+#else
+__device__ __forceinline__ bool stalled(int) { return false; }
+#endif
+
 enum : int { kDbgXScales = 0, kDbgScales, kDbgOffsets, kDbgBias, kDbgResidual, kDbgY, kDbgStatus, kDbgXGlobals };
 enum : int { kDbgGlobals = 0 };
 
@@ -229,7 +241,7 @@ __device__ __forceinline__ void activate(float (&z)[kCount], int act) {
     // max(z, 0) - |z| erfc(x) / 2, x = |z| / sqrt(2).  erfc(x) / 2 = e^(-x^2) t Q(t) with
     // t = 1 / (1 + p x) and Q the polynomial of degree 6 that has the least relative error
     // there for x up to 9.7, 6.1e-7 (found by Remez's exchange in 40 digits; p, 0.3725, by
-    // trial): below 0 this tail is the result.  Its error is 2^-18 of it in all, and 2^-24
+    // trial): below 0 this tail is the result.  Its error is 2^-18 of it in all, and 2^-23
     // z^2 for the exponential's argument.  Past |z| = 14 it is 0, of an infinite z as well.
 #pragma unroll
     for (int j = 0; j < kCount; ++j) {
@@ -504,19 +516,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       *p.status = work ? MXFP4_OK : MXFP4_EOFFSETS;
   }
   Tile t{};
+  uint32_t copied = 0;  // stages, by this thread
   if (!work) {
   } else if (warp == 0) {
     // ------------------------------------------------------------ copies
     if (tc::elected()) {
       const int64_t row_bytes = static_cast<int64_t>(p.nKT) * 512, begin = static_cast<int64_t>(k_begin) * L::kScales;
-      uint32_t stage = 0, phase = 0, copied = 0;
+      uint32_t stage = 0, phase = 0;
       bool ok = true;
       for (uint32_t j = 0; ok; ++j) {
         ok = tc::barrier_wait(bar(bars.job_full[j % kJobs]), j / kJobs & 1u, gave_up);
         if (!ok) break;
         const Job job = bars.job[j % kJobs];
         tc::barrier_arrive(bar(bars.job_empty[j % kJobs]));
-        if (job.t.n < 0) break;
+        if (job.t.n < 0 || stalled(kStallCopies)) break;
         const int boxes = (job.t.n + p.box_rows - 1) / p.box_rows;
         const uint32_t box_bytes = p.box_rows * kStageBytes;
         // the tiles' scales: of the weights (both halves'), of the tokens, and of the
@@ -554,10 +567,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++stage == p.ring_stages) stage = 0, phase ^= 1u;
         }
       }
-      // every copy has landed before the CTA may end
-      if (tc::raised(gave_up))
-        for (uint32_t n = copied > p.ring_stages ? copied - p.ring_stages : 0; n < copied; ++n)
-          tc::barrier_wait_alone(bar(bars.full[n % p.ring_stages]), n / p.ring_stages & 1u);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -571,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const int n = bars.job[j % kJobs].t.n;
         tc::barrier_arrive(bar(bars.job_empty[j % kJobs]));
-        if (n < 0) break;
+        if (n < 0 || stalled(kStallProducts)) break;
         if (k_begin == k_end) continue;
         if (j > 0) ok = tc::barrier_wait(bar(bars.sums_empty), (j - 1) & 1u, gave_up);  // the tile's before
         tc::fence_after();
@@ -617,10 +626,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok) tc::arrive_when_done(bar(bars.sums_full));
       }
-      if (tc::raised(gave_up)) {  // what was issued is done before tensor memory is freed
-        tc::arrive_when_done(bar(bars.drained));
-        tc::barrier_wait_alone(bar(bars.drained), 0);
-      }
     }
     __syncwarp();
   } else if (warp == 2) {
@@ -652,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = first_tile; ok && more; i += tile_step, ++j) {
       more = walk.find(p, i, t);
       if (!more) t.n = -1;
+      if (stalled(kStallTiles)) break;
       if (lane == 0) {
         if (j >= kJobs) ok = tc::barrier_wait(bar(bars.job_empty[j % kJobs]), (j / kJobs - 1) & 1u, gave_up);
         if (ok) {
@@ -692,14 +698,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sums[64];
       if (p.stages > 0) {
         ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.sums_full), j & 1u, gave_up));
+        if (!ok) break;
         tc::fence_after();
         tc::load32(from + group * 32, sums);
         tc::load32(from + kSecond + group * 32, sums + 32);
         tc::load_wait();
-        if (!ok) {  // there is no result: NaN says so
-#pragma unroll
-          for (int j = 0; j < 64; ++j) sums[j] = NAN;
-        }
       } else {
 #pragma unroll
         for (int j = 0; j < 64; ++j) sums[j] = 0.0f;
@@ -743,6 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Scaling g = scaling<kNv>(p, t.e);
 #pragma unroll
       for (int j = 0; j < kSome; ++j) terms[j] = row_terms<kGated, kF16>(p, t, n + j, g);
+      // (asked for ahead of the parts, looked at behind them)
+      const bool lost = lane < static_cast<int>(ranks) && tc::raised_there(gave_up, lane);
       for (int c = rank + ranks * (warp - kFirstEpilogue); c < t.n; c += ranks * kEpilogueWarps) {
         float4 a[kMaxRanks], b[kMaxRanks];
 #pragma unroll
@@ -753,6 +758,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (kGated) b[r] = ld_cluster_f4(at + kTokens * kRows * 4);
           }
         float v[kSome] = {}, u[kSome] = {};
+        if (__any_sync(0xFFFFFFFFu, lost)) {  // a rank has not its part
+#pragma unroll
+          for (int j = 0; j < kSome; ++j) v[j] = u[j] = NAN;
+        }
 #pragma unroll
         for (uint32_t r = 0; r < kMaxRanks; ++r)
           if (r < ranks) {
@@ -790,8 +799,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  if (threadIdx.x == 0 && tc::raised(gave_up) && p.status != nullptr && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4))
-    *p.status = MXFP4_ECUDA;
+  if (tc::raised(gave_up)) {
+    // A wait ran out.  What was issued is done before the CTA may end, all of its tiles
+    // are NaN, and the status word says so.
+    if (warp == 0)
+      for (uint32_t n = copied > p.ring_stages ? copied - p.ring_stages : 0; n < copied; ++n)
+        tc::barrier_wait_alone(bar(bars.full[n % p.ring_stages]), n / p.ring_stages & 1u);
+    if (warp == 1 && tc::elected()) {
+      tc::arrive_when_done(bar(bars.drained));
+      tc::barrier_wait_alone(bar(bars.drained), 0);
+    }
+    Walk walk;
+    for (int i = first_tile; walk.find(p, i, t); i += tile_step)
+      for (int r = warp; r < t.n; r += kThreads / 32)
+        for (int n = t.r0 + lane; n < min(t.r0 + kRows, p.cols); n += 32) {
+          uint16_t* const at = p.y + (t.row + r) * p.ldy + n;
+          if (MXFP4_IN_BOUNDS(p, kDbgY, at, 2)) *at = 0x7FFF;
+        }
+    if (threadIdx.x == 0 && p.status != nullptr && MXFP4_IN_BOUNDS(p, kDbgStatus, p.status, 4))
+      *p.status = MXFP4_ECUDA;
+    __syncthreads();
+  }
   if (warp == 1) tc::release(bars.columns, kColumns);
 }
 
@@ -953,6 +981,8 @@ cudaError_t launch_gemm(const GemmArgs& a, cudaStream_t stream) {
 }
 
 #ifdef MXFP4_DEBUG_BOUNDS
+bool debug_stall_gemm(int role) { return cudaMemcpyToSymbol(g_debug_stall, &role, sizeof role) == cudaSuccess; }
+
 unsigned int debug_violations_gemm() {
   unsigned int v = 0, zero = 0;
   cudaMemcpyFromSymbol(&v, g_debug_violations, sizeof v);

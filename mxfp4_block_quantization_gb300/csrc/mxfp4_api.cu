@@ -855,7 +855,7 @@ const char* mxfp4_status_string(int status) {
     case MXFP4_EALIGN: return "MXFP4_EALIGN: pointer or row stride breaks the 16-byte rule";
     case MXFP4_ESHAPE: return "MXFP4_ESHAPE: K % 32 != 0, ldx < K, odd two_n or size overflow";
     case MXFP4_EALIAS: return "MXFP4_EALIAS: an output overlaps an input or another output";
-    case MXFP4_ECUDA: return "MXFP4_ECUDA: kernel launch failed";
+    case MXFP4_ECUDA: return "MXFP4_ECUDA: kernel launch failed, or a wait inside a kernel ran out";
     case MXFP4_EOFFSETS: return "MXFP4_EOFFSETS: expert offsets are not 0 <= ... <= total_rows";
     case MXFP4_EINDEX:
       return "MXFP4_EINDEX: a gather row index is outside [0, num_src_rows) or a scatter entry "
@@ -879,6 +879,12 @@ int64_t mxfp4_debug_bounds_violations(void) {
          mxfp4::debug_violations_matvec() + mxfp4::debug_violations_cache() +
          mxfp4::debug_violations_attention() + mxfp4::debug_violations_topk() +
          mxfp4::debug_violations_gemm() + mxfp4::debug_violations_combine();
+}
+
+int mxfp4_debug_stall_products(int32_t role) {
+  if (role < 0 || role > 3) return MXFP4_EINVAL;
+  if (cudaDeviceSynchronize() != cudaSuccess) return MXFP4_ECUDA;
+  return mxfp4::debug_stall_gemm(role) ? MXFP4_OK : MXFP4_ECUDA;
 }
 #endif
 

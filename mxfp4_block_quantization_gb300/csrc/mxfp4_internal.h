@@ -291,6 +291,8 @@ unsigned int debug_violations_attention();
 unsigned int debug_violations_topk();
 unsigned int debug_violations_gemm();
 unsigned int debug_violations_combine();
+// ... which role of the products' last CTA takes no step (0: none).
+bool debug_stall_gemm(int role);
 #endif
 
 // Launch with programmatic dependent launch allowed: the grid may be

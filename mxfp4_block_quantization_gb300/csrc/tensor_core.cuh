@@ -57,6 +57,18 @@ __device__ __forceinline__ bool raised(uint32_t flag) {
 __device__ __forceinline__ void raise(uint32_t flag) {
   asm volatile("st.volatile.shared.u32 [%0], %1;" ::"r"(flag), "r"(1) : "memory");
 }
+// The word of another CTA of the cluster.
+__device__ __forceinline__ bool raised_there(uint32_t flag, uint32_t rank) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.u32 %0, [a];\n\t}"
+      : "=r"(v)
+      : "r"(flag), "r"(rank)
+      : "memory");
+  return v != 0;
+}
 // Waits for the phase of `parity`; gives up after 2^32 cycles (about two seconds).
 __device__ __forceinline__ bool barrier_wait_alone(uint32_t bar, uint32_t parity) {
   for (const long long start = clock64(); !barrier_try(bar, parity);)
