@@ -94,14 +94,15 @@ __device__ __forceinline__ int group_of(const TopkParams& p, int e) {
 
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
+// (volatile: all lanes take part, also where a branch behind it uses the result)
 __device__ __forceinline__ float warp_most(float x) {
   float r;
-  asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float warp_least(float x) {
   float r;
-  asm("redux.sync.min.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
+  asm volatile("redux.sync.min.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
   return r;
 }
 constexpr float kOut = -INFINITY;
