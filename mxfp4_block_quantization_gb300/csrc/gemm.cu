@@ -700,9 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, tc::barrier_wait(bar(bars.sums_full), j & 1u, gave_up));
         if (!ok) break;
         tc::fence_after();
-        tc::load32(from + group * 32, sums);
-        tc::load32(from + kSecond + group * 32, sums + 32);
-        tc::load_wait();
+        tc::load_sums(from + group * 32, from + kSecond + group * 32, sums);
       } else {
 #pragma unroll
         for (int j = 0; j < 64; ++j) sums[j] = 0.0f;

@@ -36,3 +36,12 @@ def test_what_all_lanes_take_part_in_is_volatile(name):
     """Else a result that only some lanes use may be computed by those lanes alone."""
     bad = [s[:2] for s in statements() if name in s[3] and not s[2]]
     assert not bad, bad
+
+
+def test_loads_from_tensor_memory_wait_for_their_words():
+    """tcgen05.ld names its registers at once and fills them later: only a wait in the
+    same statement keeps what uses them behind it."""
+    loads = [s for s in statements() if "tcgen05.ld" in s[3]]
+    assert loads
+    bad = [s[:2] for s in loads if "tcgen05.wait::ld" not in s[3]]
+    assert not bad, bad
