@@ -158,15 +158,16 @@ struct Exact {
   uint32_t* gone;   // a bit for each expert that has been taken
 };
 
-// e^x in 64 bits, to about 2^-52: x = n ln 2 + r with |r| <= ln(2) / 2 and r's
-// Taylor series to r^13 (r^14 / 14! < 2^-57), without a function call and its
-// saved registers.  0 below -708, where a score no longer counts beside any other.
+// e^x in 64 bits, to about 2^-52: x = n ln 2 + r with |r| <= ln(2) / 2 (Cody and Waite's
+// reduction: ln 2 in two parts, the first its leading 40 bits, so that n times it is
+// exact) and r's Taylor series to r^13 (r^14 / 14! < 2^-57), without a function call and
+// its saved registers.  0 below -708, where a score no longer counts beside any other.
 __device__ __forceinline__ double exp64(double x) {
   if (!(x > -708.0)) return 0.0;
   x = fmin(x, 709.0);
   const double n = rint(x * 1.4426950408889634);
-  double r = fma(n, -0.693147180369123816490, x);  // ln 2 in two parts, the first of 32 bits
-  r = fma(n, -1.90821492927058770002e-10, r);
+  double r = fma(n, -0x1.62e42fefa2p-1, x);    // floor(2^40 ln 2) / 2^40
+  r = fma(n, -0x1.9ef35793c7673p-41, r);       // and the rest
   double s = 1.0 / 6227020800.0;
   constexpr double kInverse[13] = {1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040,
                                    1.0 / 40320, 1.0 / 362880, 1.0 / 3628800, 1.0 / 39916800, 1.0 / 479001600};
