@@ -1,5 +1,6 @@
 """Products of 4-bit operands at values where a float32 step could leave the
-formula: global scales far apart, activations where they are small."""
+formula: global scales far apart, scales at the ends of their range,
+activations where they are small."""
 import math
 
 import pytest
@@ -51,6 +52,21 @@ def test_global_scales_at_any_distance(mx, a, b, T, K, gate):
         assert (y[1] == 0).all() and (y[:, 3] == 0).all()
         there = torch.ones_like(y, dtype=torch.bool)
     L.close(y[there], z[there], (off + R.unit(BF) * (z.abs() + off) + R.smallest(BF))[there])
+
+
+@pytest.mark.parametrize("T", [5, 140])
+@pytest.mark.parametrize("far", [60, 100, 120, 127])
+def test_scales_at_the_ends_of_their_range(mx, T, far):
+    """Scales of 2^far beside scales of 2^-far, whose products are ordinary."""
+    g = gen(22)
+    K, N = 256, 140
+    (xc, xs), (wc, ws) = operand(T, K, False, g, pad=127), operand(N, K, False, g, pad=127)
+    xs[:], ws[:] = 127 + far, 127 - far
+    y = mx.gemm(xc, xs, wc, ws)
+    want, bound = L.gemm(R.elements(xc), R.elements(wc), BF)
+    L.close(y, want, bound)
+    y = mx.gemm(wc, ws, xc, xs)
+    L.close(y, want.T, bound.T)
 
 
 def values(act):
