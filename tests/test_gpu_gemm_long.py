@@ -100,3 +100,41 @@ def test_combine_in_rows_wider_apart_than_long(mx, N, pad, f32):
     mx.mxfp4_moe_combine(rows, dest, w, y, residual=y)
     R.close(y, want, bound)
     assert int(status) == 0 and (whole[:, N:] == 7).all() and (whole[T] == 7).all()
+
+
+def test_outputs_past_32_bit_offsets(mx):
+    """More than 2^32 bytes of y (and of the residual, which is y)."""
+    g = gen(19)
+    T, N, K = 310_000, 7200, 64
+    (xc, xs), (wc, ws) = operand(T, K, False, g), operand(N, K, False, g)
+    y = torch.ones(T, N, dtype=BF, device="cuda")
+    mx.mxfp4_gemm(xc, xs, wc, ws, y, residual=y)
+    w = R.weights(wc, ws, False)
+    for lo, hi in ((0, 40), (149_100, 149_160), (298_200, 298_300), (T - 150, T)):
+        flat = R.untile(xs[lo // 128 * 512:], hi - lo // 128 * 128, 2)[lo % 128:]
+        x = R.rows_of(xc[lo:hi], flat, False)
+        L.close(y[lo:hi], *L.gemm(x, w, BF, residual=torch.ones(hi - lo, N, device="cuda")))
+    del y
+
+
+def test_weights_past_32_bit_offsets(mx):
+    """More than 2^32 bytes of the experts' codes: rows of the first and the last ones."""
+    g = gen(20)
+    E, N, K = 130, 8192, 8192
+    sizes = [0] * E
+    sizes[0], sizes[127], sizes[128], sizes[129] = 3, 2, 1, 140
+    xc, xs, off, values, _ = batch(sizes, K, False, g)
+    codes = torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda")
+    scales = torch.full((E * N * K // 32,), 127, dtype=torch.uint8, device="cuda")
+    per, used = N * K // 32, [e for e, n in enumerate(sizes) if n]
+    for e in used:
+        codes[e], scales[e * per:(e + 1) * per] = operand(N, K, False, g)
+    y, status = mx.moe_gemm(xc, xs, off, codes, scales)
+    assert int(status) == 0
+    at = 0
+    for e, x in zip(used, values):
+        part = slice(0, 200) if e == 129 else slice(0, N)
+        w = R.weights(codes[e], scales[e * per:(e + 1) * per], False)
+        want, bound = L.gemm(x, w[part], BF)
+        L.close(y[at:at + sizes[e], part], want, bound)
+        at += sizes[e]
