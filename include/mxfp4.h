@@ -844,7 +844,9 @@ int mxfp4_cache_attention_nvfp4_f16(const void* q, int64_t num_seqs, int32_t num
  *              computed in 64 bits: where float32 cannot tell two apart, they
  *              are computed in 64.
  *   weights  score[id], with renormalize == 1 divided by the sum over the
- *              chosen, times scale.
+ *              chosen, times scale; in float32, off by 2^-19 and 2^-22 of the
+ *              logits' magnitudes (a softmax that is not renormalised: and by
+ *              E 2^-28).
  * A logit that is not finite takes its expert out (of the softmax's sum too);
  * where fewer than top_k experts are left, the last ids are -1 (what
  * mxfp4_moe_route takes as "not dispatched") and their weights 0.

@@ -6,7 +6,9 @@
 // pieces) and adds the routes in order, the rows of up to kAhead of them in
 // flight; nothing is shared between threads, so equal calls give equal bits.
 // 16384 tokens of 8 rows of 7168 and a residual take 358 us: 6.3 TB/s, 93 % of the
-// measured copy rate.
+// measured copy rate.  Of 1024 columns 45 us (the copy rate), of 256 9.1, of 64 3.9; but
+// the status word's CTA takes 12 to 14 us over those 131072 entries, whatever the rows'
+// length.  Of 2047 columns, one to a thread, 290 us (floor 89).
 #include <cstdint>
 
 #include <cuda_bf16.h>

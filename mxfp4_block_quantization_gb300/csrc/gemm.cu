@@ -22,12 +22,14 @@
 // shares a tile, each with a part of K, and adds the parts in rank order through
 // distributed shared memory: equal calls give equal bits.
 //
-// Measured: 4096 tokens by 7168 x 7168 MXFP4 with bias and residual 78 us (5.4 PFLOP/s,
-// the tensor pipe busy for 54 %; without a residual 71): a stage takes 0.33 us where its
-// four products take 0.26, for the copies' latency with four stages under way.  128
-// experts' gated 1536 x 2048 by 16384 tokens' 8 routes 173 us (4.8 PFLOP/s): 4.3 us to a
-// tile, of which its 8 stages 2.7 and the rest taking the sums before the next tile's
-// products.  The same by 64 tokens' 8 routes 36 us: HBM, 5.8 TB/s.
+// Measured (calls in a graph): 4096 tokens by 7168 x 7168 MXFP4 66.5 us (6.3 PFLOP/s): to
+// each CTA's six tiles 28 stages of 0.33 us, where a stage's four products take 0.26, for
+// the copies, and 1.8 us to a tile for its turn (by the times of K = 2048 to 10240).  With
+// bias and residual 77 us (5.5 PFLOP/s): the epilogue of a tile then takes 8 us (the call
+// with K = 512 48 us, without a residual 16), which the next tile's products hide but for
+// 1.7.  128 experts' gated 1536 x 2048 by 16384 tokens' 8 routes 171 us (4.8 PFLOP/s; 187
+// between calls on other inputs): 4.3 us to a tile, of which its 8 stages 2.7 and the rest
+// its turn.  The same by 64 tokens' 8 routes 36 us: HBM, 5.8 TB/s.
 #include <algorithm>
 #include <cmath>
 #include <cstdint>

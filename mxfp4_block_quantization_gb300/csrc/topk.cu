@@ -16,7 +16,7 @@
 // them one by one.
 //
 // Instructions bound it: 16384 tokens on 384 experts take 16 us by their logits, 20 with
-// sigmoid and bias, 30 in 8 groups by their two best (1330 instructions to a token;
+// sigmoid and bias, 26 to 30 in 8 groups by their two best (1330 instructions to a token;
 // the bytes alone would be 4 us), of which the ranking in 64 bits 3 and 7.
 #include <cstdint>
 
